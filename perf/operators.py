@@ -213,7 +213,7 @@ def _prefill(s):
 def run(state):
     s = state
     if own:
-        from nvfp4_block_scaled_07_gb300 import binding as B
+        from nvfp4_block_scaled_07_gb300 import mla as B
         if s["op"] == "append":
             B.mla_append(s["latent"], s["k_rope"], s["positions"], s["slots"], s["table"], s["cache"],
                          norm_weight=s["norm_weight"], eps=EPS, interleaved=s["interleaved"], q_rope=s["q_rope"],
@@ -222,7 +222,7 @@ def run(state):
         if s["op"] == "decode":
             out, lse = B.mla_decode(s["q"], s["cache"], s["block_tables"], s["seq_lens"], SCALE)
         else:
-            out, lse = B.mla_prefill(s["q"], s["k_nope"], s["k_rope"], s["v"], s["cu_q"], s["cu_k"], s["max_q"], SCALE)
+            out, lse = B.mla_prefill(s["q"], s["k_nope"], s["k_rope"], s["v"], s["cu_q"], s["cu_k"], SCALE)
         return dict(out=out, lse=lse)
     return {"append": _append, "decode": _decode, "prefill": _prefill}[s["op"]](s)
 

@@ -3,12 +3,13 @@ expert layer as a C-ABI CUDA library with a thin Python binding.
 
 Submodules:
   binding    ctypes binding of libnvfp4moe.so (fails loudly if not built)
+  mla        the same for latent attention (cache append, decode, prefill)
   workloads  seeded synthetic layer inputs
   build      nvcc build of the shared library
 """
 import importlib
 
-__all__ = ["binding", "workloads", "build"]
+__all__ = ["binding", "mla", "workloads", "build"]
 
 
 def __getattr__(name):

@@ -8,6 +8,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "../../include/nvfp4mla.h"
 #include "../../include/nvfp4moe.h"
 #include "internal.h"
 
@@ -154,9 +155,14 @@ int nvfp4moe_sync_status(cudaStream_t stream) {
   if (st) return st;
   st = cuda_status(gemm_read_and_clear_flags(&f2), "reading device flags");
   if (st) return st;
-  const unsigned f = f1 | f2;
-  if (f & kFlagTimeout) return fail(NVFP4MOE_ERR_TIMEOUT, "a device wait (grouped GEMM pipeline or prepare grid barrier) exceeded its time limit");
-  if (f & kFlagBadData) return fail(NVFP4MOE_ERR_DEVICE_DATA, "an expert id or row index was out of range");
+  unsigned f3 = 0, f4 = 0;
+  st = cuda_status(mla_append_read_and_clear_flags(&f3), "reading device flags");
+  if (st) return st;
+  st = cuda_status(mla_decode_read_and_clear_flags(&f4), "reading device flags");
+  if (st) return st;
+  const unsigned f = f1 | f2 | f3 | f4;
+  if (f & kFlagTimeout) return fail(NVFP4MOE_ERR_TIMEOUT, "a device wait (grouped GEMM or attention pipeline, or prepare grid barrier) exceeded its time limit");
+  if (f & kFlagBadData) return fail(NVFP4MOE_ERR_DEVICE_DATA, "an expert id, row index, cache slot, page, position or sequence length was out of range");
   return NVFP4MOE_OK;
 }
 
@@ -643,6 +649,116 @@ int moe_finalize(const void* y_bf16, const int32_t* flat_to_perm, const float* t
   if (int st = current_device(&d)) return st;
   return cuda_status(launch_finalize(y_bf16, flat_to_perm, topk_w, T, k, H, rows_capacity, out_bf16, stream),
                      "finalize launch");
+}
+
+// ---- latent attention ---------------------------------------------------------
+// A strided operand of the latent-attention calls: 16-byte aligned rows.
+static bool row_aligned(const void* p, int64_t stride) { return aligned16(p) && stride >= 0 && stride % 8 == 0; }
+
+int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+               const void* norm_weight, float eps, const int32_t* positions, const int64_t* slots, int T,
+               const float* rope_table, int64_t max_positions, int interleaved, int dtype, void* cache,
+               int64_t num_slots, void* rows_out, const void* q_rope, int64_t q_token_stride, int64_t q_head_stride,
+               int H, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, cudaStream_t stream) {
+  t_detail[0] = 0;
+  NVFP4MOE_REQUIRE(T >= 0 && T <= (1 << 30), NVFP4MOE_ERR_INVALID_ARG, "T = %d outside [0, 2^30]", T);
+  NVFP4MOE_REQUIRE(H >= 0 && H <= 1024, NVFP4MOE_ERR_UNSUPPORTED, "H = %d outside [0, 1024]", H);
+  NVFP4MOE_REQUIRE(dtype == NVFP4MLA_BF16 || dtype == NVFP4MLA_FP16, NVFP4MOE_ERR_INVALID_ARG, "dtype %d", dtype);
+  NVFP4MOE_REQUIRE(interleaved == 0 || interleaved == 1, NVFP4MOE_ERR_INVALID_ARG, "interleaved %d", interleaved);
+  NVFP4MOE_REQUIRE(num_slots >= 0 && max_positions >= 1, NVFP4MOE_ERR_INVALID_ARG, "num_slots %lld max_positions %lld",
+                   (long long)num_slots, (long long)max_positions);
+  NVFP4MOE_REQUIRE(!norm_weight || (eps >= 0.0f && eps < 1e30f), NVFP4MOE_ERR_INVALID_ARG,
+                   "eps must be finite and not negative");
+  if (T == 0) return NVFP4MOE_OK;
+  NVFP4MOE_REQUIRE(latent && k_rope && positions && slots && rope_table && (cache || num_slots == 0),
+                   NVFP4MOE_ERR_INVALID_ARG, "null pointer");
+  NVFP4MOE_REQUIRE(H == 0 || (q_rope && q_out), NVFP4MOE_ERR_INVALID_ARG, "H = %d without q_rope or q_out", H);
+  NVFP4MOE_REQUIRE(row_aligned(latent, latent_stride) && row_aligned(k_rope, k_rope_stride),
+                   NVFP4MOE_ERR_INVALID_ARG, "latent and k_rope must be 16-byte aligned with strides %% 8 == 0");
+  NVFP4MOE_REQUIRE(H == 0 || (row_aligned(q_rope, q_token_stride) && row_aligned(q_rope, q_head_stride) &&
+                              row_aligned(q_out, q_out_token_stride) && row_aligned(q_out, q_out_head_stride)),
+                   NVFP4MOE_ERR_INVALID_ARG, "q_rope and q_out must be 16-byte aligned with strides %% 8 == 0");
+  NVFP4MOE_REQUIRE(aligned16(norm_weight) && aligned16(rope_table) && aligned16(cache) && aligned16(rows_out) &&
+                       (reinterpret_cast<uintptr_t>(positions) & 3) == 0 &&
+                       (reinterpret_cast<uintptr_t>(slots) & 7) == 0,
+                   NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  NVFP4MOE_REQUIRE(int64_t(T) * (1 + ceil_div(H, 8)) < (int64_t(1) << 33), NVFP4MOE_ERR_UNSUPPORTED,
+                   "T = %d with H = %d exceeds the launch's grid", T, H);
+  DeviceInfo d;
+  if (int st = current_device(&d)) return st;
+  MlaAppendArgs a;
+  a.latent = latent;
+  a.latent_stride = latent_stride;
+  a.k_rope = k_rope;
+  a.k_rope_stride = k_rope_stride;
+  a.norm_weight = norm_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.slots = slots;
+  a.T = T;
+  a.table = rope_table;
+  a.max_positions = max_positions;
+  a.interleaved = interleaved != 0;
+  a.fp16 = dtype == NVFP4MLA_FP16;
+  a.cache = cache;
+  a.num_slots = num_slots;
+  a.rows_out = rows_out;
+  a.q = q_rope;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.H = H;
+  a.q_out = q_out;
+  a.qo_token_stride = q_out_token_stride;
+  a.qo_head_stride = q_out_head_stride;
+  return cuda_status(launch_mla_append(a, stream), "mla_append launch");
+}
+
+size_t mla_decode_workspace_size(void) { return mla_decode_workspace_bytes(); }
+
+int mla_decode(const void* q, const void* cache, int num_pages, int page_size, const int32_t* block_tables,
+               int64_t table_stride, int max_pages, const int32_t* seq_lens, int B, int Sq, int H, float scale,
+               int dtype, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  t_detail[0] = 0;
+  NVFP4MOE_REQUIRE(B >= 0 && Sq >= 1 && H >= 1 && max_pages >= 0, NVFP4MOE_ERR_INVALID_ARG,
+                   "B = %d Sq = %d H = %d max_pages = %d", B, Sq, H, max_pages);
+  NVFP4MOE_REQUIRE(int64_t(Sq) * H < (int64_t(1) << 31) && int64_t(B) * Sq * H < (int64_t(1) << 31),
+                   NVFP4MOE_ERR_UNSUPPORTED, "B * Sq * H must be below 2^31");
+  NVFP4MOE_REQUIRE(dtype == NVFP4MLA_BF16 || dtype == NVFP4MLA_FP16, NVFP4MOE_ERR_INVALID_ARG, "dtype %d", dtype);
+  NVFP4MOE_REQUIRE(scale > 0.0f && scale < 1e30f, NVFP4MOE_ERR_INVALID_ARG, "scale must be positive and finite");
+  NVFP4MOE_REQUIRE(page_size >= 16 && (page_size & (page_size - 1)) == 0, NVFP4MOE_ERR_UNSUPPORTED,
+                   "page_size = %d must be a power of two >= 16", page_size);
+  NVFP4MOE_REQUIRE(num_pages >= 1 && int64_t(num_pages) * page_size < (int64_t(1) << 31), NVFP4MOE_ERR_UNSUPPORTED,
+                   "num_pages = %d with pages of %d rows: 1 .. 2^31 - 1 rows", num_pages, page_size);
+  NVFP4MOE_REQUIRE(table_stride >= max_pages, NVFP4MOE_ERR_INVALID_ARG, "table_stride %lld < max_pages %d",
+                   (long long)table_stride, max_pages);
+  if (B == 0) return NVFP4MOE_OK;
+  NVFP4MOE_REQUIRE(q && cache && (block_tables || max_pages == 0) && seq_lens && out && lse,
+                   NVFP4MOE_ERR_INVALID_ARG, "null pointer");
+  NVFP4MOE_REQUIRE(aligned16(q) && aligned16(cache) && aligned16(out) &&
+                       ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(block_tables) |
+                         reinterpret_cast<uintptr_t>(seq_lens)) & 3) == 0,
+                   NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t need = mla_decode_workspace_bytes();
+  NVFP4MOE_REQUIRE(ws && ws_bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0, NVFP4MOE_ERR_WORKSPACE,
+                   "workspace %zu < %zu or not 256-byte aligned", ws_bytes, need);
+  DeviceInfo d;
+  if (int st = current_device(&d)) return st;
+  MlaDecodeArgs a;
+  a.q = q;
+  a.cache = cache;
+  a.num_pages = num_pages;
+  a.page = page_size;
+  a.tables = block_tables;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.lens = seq_lens;
+  a.B = B, a.Sq = Sq, a.H = H;
+  a.scale = scale;
+  a.fp16 = dtype == NVFP4MLA_FP16;
+  a.out = out;
+  a.lse = lse;
+  a.ws = ws;
+  return launch_mla_decode(a, d.num_sms, stream);  // detail already set on failure
 }
 
 }  // extern "C"

@@ -146,6 +146,56 @@ cudaError_t launch_tile_weights(const uint8_t* w_packed, int64_t rows, int K, ui
                                 cudaStream_t st);
 cudaError_t gemm_read_and_clear_flags(unsigned* flags);
 
+// ---- latent attention (mla_*.cu) --------------------------------------------
+struct MlaAppendArgs {
+  const void* latent;
+  int64_t latent_stride;  // strides in elements
+  const void* k_rope;
+  int64_t k_rope_stride;
+  const void* norm_weight;
+  float eps;
+  const int32_t* positions;
+  const int64_t* slots;
+  int T;
+  const float* table;
+  int64_t max_positions;
+  bool interleaved, fp16;
+  void* cache;
+  int64_t num_slots;
+  void* rows_out;
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  int H;
+  void* q_out;
+  int64_t qo_token_stride, qo_head_stride;
+};
+cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t st);
+cudaError_t mla_append_read_and_clear_flags(unsigned* flags);
+
+// Workspace of mla_decode: what each CTA's range begins with, then two
+// partial results (64 log-sums, 64 x 512 float32) a CTA.
+constexpr int kMlaDecodeMaxGrid = 160;
+constexpr size_t kMlaDecodeHeadBytes = 4096;
+size_t mla_decode_workspace_bytes();
+struct MlaDecodeArgs {
+  const void* q;
+  const void* cache;
+  int num_pages, page;  // page: a power of two
+  const int32_t* tables;
+  int64_t table_stride;
+  int max_pages;
+  const int32_t* lens;
+  int B, Sq, H;
+  float scale;
+  bool fp16;
+  void* out;
+  float* lse;
+  void* ws;
+};
+// Returns 0 or an NVFP4MOE_ERR_* code (message via set_error_detail).
+int launch_mla_decode(const MlaDecodeArgs& a, int num_sms, cudaStream_t st);
+cudaError_t mla_decode_read_and_clear_flags(unsigned* flags);
+
 // Per-thread error message used by nvfp4moe_last_error_detail().
 void set_error_detail(const char* fmt, ...);
 

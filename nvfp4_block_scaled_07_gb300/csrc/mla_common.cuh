@@ -1,0 +1,205 @@
+// Shared pieces of the latent-attention kernels: 16-bit element types,
+// bounded waits, 16-bit tcgen05 MMAs and their descriptors, tensor maps.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <mutex>
+
+#include "internal.h"
+#include "sm103_ptx.cuh"
+
+namespace nvfp4moe {
+namespace mla {
+
+constexpr int kLatent = 512;
+constexpr int kRope = 64;
+constexpr int kRow = kLatent + kRope;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Two 16-bit values in one register, the first in the low half.
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = 1;  // tcgen05 kind::f16 operand format
+  static constexpr CUtensorMapDataType kMap = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
+};
+template <> struct Elem<__half> {
+  static constexpr uint32_t kFormat = 0;
+  static constexpr CUtensorMapDataType kMap = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  static __device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---- bounded waits ---------------------------------------------------------------
+// Shared state of one CTA's waits: a wait that exceeds the limit raises the
+// sticky flag and makes every role leave its loop.
+struct WaitCtl {
+  int abort;
+  uint32_t limit_us;
+  unsigned* flags;
+};
+
+// SPIN polls without suspending the thread (the producer and the MMA issuer).
+template <bool SPIN>
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
+  if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      if (ctl->abort) return false;
+      if (ptx::globaltimer_ns() - t0 > uint64_t(ctl->limit_us) * 1000u) {
+        ctl->abort = 1;
+        atomicOr(ctl->flags, kFlagTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+// Wait for a CTA's own copies or MMAs before it leaves, also after an abort.
+__device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (ptx::globaltimer_ns() - t0 > 2000000000ull) return;
+}
+
+// ---- tcgen05 kind::f16 -------------------------------------------------------------
+// Instruction descriptor: both operands of one 16-bit format, float32
+// accumulator, dense; *_mn: the operand is stored with M (N) contiguous
+// instead of K.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t format, int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4)                               // D format: float32
+         | (format << 7) | (format << 10)        // A and B format
+         | (uint32_t(a_mn ? 1u : 0u) << 15) | (uint32_t(b_mn ? 1u : 0u) << 16)
+         | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] B[smem]^T, K = 16.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same with A in tensor memory: lane = row of A, 16-bit pairs along K.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Operand stored with M (N) contiguous in 128-byte swizzled rows: a chunk is
+// [K rows][64 values], 8-row groups 1024 bytes apart; the next 64 values of
+// M (N) start `chunk_bytes` later.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t chunk_bytes) {
+  uint64_t d = 0;
+  d |= uint64_t((saddr & 0x3FFFFu) >> 4);
+  d |= uint64_t(chunk_bytes >> 4) << 16;         // leading offset: next 64 values of M (N)
+  d |= uint64_t(1024 >> 4) << 32;                // stride offset: next 8 of K
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;                        // swizzle mode: 128 B
+  return d;
+}
+
+// 16 lanes x 64 columns of a warp's lane quarter: thread l holds, in r[4i ..
+// 4i+3], columns 8i + 2 (l % 4) + {0, 1} of lane l / 4 and then of lane l / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void sts32(uint32_t saddr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+// Barrier among `n` threads of the CTA (ids 1..15; 0 is __syncthreads).
+__device__ __forceinline__ void bar_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+// The same, returning whether any of the threads passed a true predicate.
+__device__ __forceinline__ bool bar_any(int id, int n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(uint32_t(pred))
+      : "memory");
+  return r != 0;
+}
+
+// ---- tensor maps ------------------------------------------------------------------
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+// 16-bit tensor of `rank` dimensions (innermost first, strides in bytes of
+// dimensions 1..) with a 128-byte swizzled box; out-of-range rows read zero.
+inline bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const int64_t* dims,
+                       const int64_t* strides, const int* box) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], e[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = cuuint64_t(dims[i]);
+    b[i] = cuuint32_t(box[i]);
+    e[i] = 1;
+    if (i) s[i - 1] = cuuint64_t(strides[i - 1]);
+  }
+  return enc(m, type, cuuint32_t(rank), const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mla
+}  // namespace nvfp4moe

@@ -120,17 +120,16 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Operand stored with M (N) contiguous in 128-byte swizzled rows: a chunk is
-// [K rows][64 values], 8-row groups 1024 bytes apart; the next 64 values of
-// M (N) start `chunk_bytes` later.
-__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t chunk_bytes) {
-  uint64_t d = 0;
-  d |= uint64_t((saddr & 0x3FFFFu) >> 4);
-  d |= uint64_t(chunk_bytes >> 4) << 16;         // leading offset: next 64 values of M (N)
-  d |= uint64_t(1024 >> 4) << 32;                // stride offset: next 8 of K
-  d |= uint64_t(1) << 46;
-  d |= uint64_t(2) << 61;                        // swizzle mode: 128 B
-  return d;
+// Shared-memory operand descriptors, 128-byte swizzle.  An operand is made of
+// atoms of 8 rows x 128 bytes (1024 bytes, aligned to as much).
+//   K-major: rows are M (N), their 64 values along K; `stride` from one 8-row
+//     group to the next; 16 values of K are 32 bytes.
+//   MN-major: rows are K, their 64 values along M (N); `stride` from one
+//     8-row group of K to the next, `lead` to the next 64 values of M (N).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lead, uint32_t stride) {
+  const uint32_t lo = ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
+  const uint32_t hi = (stride >> 4) | (1u << 14) | (2u << 29);
+  return (uint64_t(hi) << 32) | lo;
 }
 
 // 16 lanes x 64 columns of a warp's lane quarter: thread l holds, in r[4i ..
@@ -149,6 +148,9 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
 
 __device__ __forceinline__ void sts32(uint32_t saddr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t saddr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(saddr), "r"(a), "r"(b) : "memory");
 }
 // Barrier among `n` threads of the CTA (ids 1..15; 0 is __syncthreads).
 __device__ __forceinline__ void bar_sync(int id, int n) {

@@ -48,7 +48,8 @@ constexpr int kRows = 64;                     // rows of a block
 constexpr int kKeys = 64;                     // keys of a tile
 constexpr int kChunk = 64 * 128;              // 64 rows x 64 values, 128-byte rows
 constexpr int kTile = 9 * kChunk;
-constexpr int kParts = 5;                     // of a tile: rotary chunk, four pairs of latent chunks
+constexpr int kGroup = 8 * 2 * kRow;          // 8 keys: nine atoms of 8 rows x 128 bytes
+constexpr int kPieces = 4;                    // of a tile: 16 keys each, freed one by one
 constexpr int kStages = 2;
 constexpr int kThreads = 192;
 constexpr int kSoftmaxThreads = 128;
@@ -64,7 +65,7 @@ constexpr int kPOff = kKvOff + kStages * kTile;
 constexpr int kSmem = kPOff + kChunk;
 
 struct Control {
-  uint64_t full[kStages][kParts], empty[kStages][kParts];
+  uint64_t full[kStages], empty[kStages][kPieces];
   uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
@@ -165,19 +166,13 @@ struct Cursor {
   __device__ __forceinline__ int rows(const DecodeParams& p) const { return min(kRows, p.rows - block * kRows); }
 };
 
-// 16-bit rows [slots, 576] in boxes of 64 values x `box_rows` rows.
+// 16-bit rows [rows, 576] in boxes of `box_rows` rows x `chunks` chunks of 64
+// values, which land chunk by chunk, each as box_rows x 128 bytes.
 template <typename T>
-bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
-  const int64_t dims[2] = {kRow, rows}, strides[1] = {2 * kRow};
-  const int box[2] = {64, box_rows};
-  return encode_map(m, Elem<T>::kMap, 2, base, dims, strides, box);
-}
-
-// A whole warp's wait: lane 0 polls, all lanes get its answer.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_phase<true>(bar, parity, ctl);
-  return __all_sync(kFull, ok);
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows, int chunks) {
+  const int64_t dims[3] = {64, rows, kRow / 64}, strides[2] = {2 * kRow, 128};
+  const int box[3] = {64, box_rows, chunks};
+  return encode_map(m, Elem<T>::kMap, 3, base, dims, strides, box);
 }
 
 template <typename T>
@@ -192,11 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s)
-      for (int i = 0; i < kParts; ++i) {
-        ptx::mbar_init(bar(ctl->full[s][i]), 1);
-        ptx::mbar_init(bar(ctl->empty[s][i]), 1);
-      }
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar(ctl->full[s]), 1);
+      for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->empty[s][i]), 1);
+    }
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
     ptx::mbar_init(bar(ctl->s_full[0]), 1);
@@ -233,136 +227,131 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0)                      // lengths that are not served as they are
       for (int b = lane; b < p.B; b += 32)
         if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
-    const uint64_t policy = ptx::policy_evict_normal();
-    const int box_rows = min(p.page, kKeys);
-    const int64_t oob = int64_t(p.num_pages) * p.page;
-    uint32_t g = 0, seg = 0, issued = 0;      // tiles, Q blocks, tile parts
-    // Slot of the first row of the lane's box-row group of the cursor's tile.
-    auto slot_of = [&](const Cursor& c) -> int64_t {
-      const int row = int(c.tile) * kKeys + lane * box_rows;
-      if (lane * box_rows >= c.keys()) return oob;
-      const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
-      if (id < 0 || id >= p.num_pages) {      // zero rows instead of a page that does not exist
-        atomicOr(&g_decode_flags, kFlagBadData);
-        return oob;
-      }
-      return int64_t(id) * p.page + (row & (p.page - 1));
-    };
-    int64_t slot = cur.valid() ? slot_of(cur) : 0;
-    bool ok = true;
-    while (ok && cur.valid()) {
-      if (cur.is_first()) {
-        if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(ctl->q_full), kTile);
-        __syncwarp();
-        if (lane < 9)
-          ptx::tma_load_2d(base + kQOff + lane * kChunk, &q_map, bar(ctl->q_full), lane * 64,
-                           cur.b * p.rows + cur.block * kRows, policy);
-        ++seg;
-      }
-      const int s = int(g & 1u);
-      const uint32_t ph = (g >> 1) & 1u;
-      const int keys = cur.keys();
-      const int groups = keys > 0 ? (keys + box_rows - 1) / box_rows : 0;
-      Cursor nxt = cur;
-      nxt.next(p);
-      const int64_t next_slot = nxt.valid() ? slot_of(nxt) : 0;
-      for (int i = 0; i < kParts; ++i) {      // the rotary chunk, then the latent pairs
-        if (!wait_warp(bar(ctl->empty[s][i]), ph ^ 1u, wctl)) {
-          ok = false;
-          break;
+    if (lane == 0) {
+      const uint64_t policy = ptx::policy_evict_normal();
+      const int oob = p.num_pages * p.page;
+      const int per = p.page < kKeys ? kKeys / p.page : 1;  // pages of a tile
+      uint32_t g = 0, seg = 0;
+      // First cache rows of the tile's four pieces of 16 keys.
+      auto look_up = [&](const Cursor& c, int (&from)[kPieces]) {
+        const int row = int(c.tile) * kKeys;
+        const int32_t* t = p.tables + c.b * p.table_stride + (row >> p.log_page);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          from[i] = oob;
+          if (i * 16 < c.keys()) {
+            const int id = __ldg(t + ((i * per) >> 2));
+            if (id >= 0 && id < p.num_pages) from[i] = id * p.page + ((row + 16 * i) & (p.page - 1));
+            else atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
+          }
         }
-        ++issued;
-        const int chunks = i ? 2 : 1;
-        const uint32_t dst = base + kKvOff + s * kTile + (i ? (i - 1) * 2 * kChunk : 8 * kChunk);
-        const uint32_t fb = bar(ctl->full[s][i]);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(fb, uint32_t(chunks * groups * box_rows * 128));
-        __syncwarp();
-        const int grp = lane % 4, ch = lane / 4;  // at most 4 groups of rows and 2 chunks
-        const int64_t from = __shfl_sync(kFull, slot, grp);
-        if (grp < groups && ch < chunks)
-          ptx::tma_load_2d(dst + ch * kChunk + grp * box_rows * 128, &kv_map, fb,
-                           i ? (i - 1) * 128 + ch * 64 : kLatent, int32_t(from), policy);
+      };
+      int from[kPieces], next[kPieces];
+      if (cur.valid()) look_up(cur, from);
+      bool ok = true;
+      while (ok && cur.valid()) {
+        if (cur.is_first()) {
+          if (!wait_phase<true>(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
+          ptx::mbar_arrive_expect_tx(bar(ctl->q_full), kTile);
+#pragma unroll
+          for (int c = 0; c < 9; c += 3)
+            ptx::tma_load_3d(base + kQOff + c * kChunk, &q_map, bar(ctl->q_full), 0,
+                             cur.b * p.rows + cur.block * kRows, c, policy);
+          ++seg;
+        }
+        const int s = int(g & 1u);
+        const uint32_t ph = (g >> 1) & 1u, fb = bar(ctl->full[s]);
+        const int groups = (max(cur.keys(), 0) + 7) / 8;
+        Cursor nxt = cur;
+        nxt.next(p);
+        if (nxt.valid()) look_up(nxt, next);
+        const uint32_t dst = base + kKvOff + s * kTile;
+        ok = wait_phase<true>(bar(ctl->empty[s][0]), ph ^ 1u, wctl);
+        if (!ok) break;
+        ptx::mbar_arrive_expect_tx(fb, uint32_t(groups * kGroup));
+        ++g;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          // After an abort the rest of the tile still comes: the copies that
+          // the barrier was told to expect have to end before the CTA does.
+          if (i && ok) ok = wait_phase<true>(bar(ctl->empty[s][i]), ph ^ 1u, wctl);
+          if (2 * i < groups) ptx::tma_load_3d(dst + 2 * i * kGroup, &kv_map, fb, 0, from[i], 0, policy);
+          if (2 * i + 1 < groups)
+            ptx::tma_load_3d(dst + (2 * i + 1) * kGroup, &kv_map, fb, 0, min(from[i], oob - 8) + 8, 0, policy);
+        }
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) from[i] = next[i];
+        cur = nxt;
       }
-      if (!ok) break;
-      slot = next_slot;
-      cur = nxt;
-      ++g;
+      // every copy that was issued has landed before the CTA leaves
+      if (seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
+      for (uint32_t s = 0; s < kStages; ++s) {
+        const uint32_t n = (g + 1 - s) / 2;   // uses of the stage
+        if (n) drain_phase(bar(ctl->full[s]), (n - 1) & 1u);
+      }
     }
-    // every copy that was issued has landed before the CTA leaves
     __syncwarp();
-    if (seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
-    for (uint32_t s = 0; s < kStages; ++s)
-      for (int i = 0; i < kParts; ++i) {
-        const uint32_t n = ((issued + kParts - 1 - i) / kParts + 1 - s) / 2;  // uses of this slot
-        if (n) drain_phase(bar(ctl->full[s][i]), (n - 1) & 1u);
-      }
   } else if (warp == 5) {
     // ---- MMA issuer ----
-    const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
-    uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;
-    Cursor cs = cur;                          // S runs one tile ahead of P V
-    bool ok = true;
-    auto issue_s = [&]() {
-      const int s = int(gs & 1u);
-      const uint32_t ph = (gs >> 1) & 1u;
-      if (cs.is_first()) {
-        if (!wait_warp(bar(ctl->q_full), seg_s & 1u, wctl)) return false;
-        ++seg_s;
-      }
-      const uint32_t d = tmem + kSCol + s * kKeys;
-      for (int i = 0; i < kParts; ++i) {
-        if (!wait_warp(bar(ctl->full[s][i]), ph, wctl)) return false;
-        ptx::tc_fence_after();
-        if (lane == 0) {
-          const int c0 = i ? (i - 1) * 2 : 8, n = i ? 2 : 1;
-          for (int c = c0; c < c0 + n; ++c) {
-            const uint64_t a = ptx::desc_kmajor_sw128(base + kQOff + c * kChunk);
-            const uint64_t b = ptx::desc_kmajor_sw128(base + kKvOff + s * kTile + c * kChunk);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16(d, a + 2 * k, b + 2 * k, idesc_s, !(i == 0 && k == 0));
-          }
-          if (i == 0) ptx::tc_commit(bar(ctl->empty[s][0]));
-        }
-        __syncwarp();
-      }
-      if (lane == 0) {
-        ptx::tc_commit(bar(ctl->s_full[s]));
-        if (cs.is_last()) ptx::tc_commit(bar(ctl->q_empty));
-      }
-      __syncwarp();
-      cs.next(p);
-      ++gs;
-      return true;
-    };
-    if (cur.valid()) ok = issue_s();
-    while (ok && cur.valid()) {
-      if (cs.valid() && !issue_s()) break;
-      const int s = int(gp & 1u);
-      if (!wait_warp(bar(ctl->p_full), gp & 1u, wctl)) break;
-      if (cur.is_first()) {                   // the previous segment's accumulator has been read
-        if (seg_p && !wait_warp(bar(ctl->o_free), (seg_p - 1) & 1u, wctl)) break;
-        ++seg_p;
-      }
-      ptx::tc_fence_after();
-      if (lane == 0) {
-        const int n = (cur.rows(p) + 15) / 16 * 16;
-        const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, n, true, false);
-        const uint64_t b = ptx::desc_kmajor_sw128(base + kPOff);
-        for (int m = 0; m < 4; ++m) {
-          const uint64_t a = desc_mnmajor_sw128(base + kKvOff + s * kTile + m * 2 * kChunk, kChunk);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)         // 16 keys: 2048 bytes of C, 32 bytes of P
-            mma_f16(tmem + m * kRows, a + 128 * k, b + 2 * k, idesc_o, !(cur.is_first() && k == 0));
-          ptx::tc_commit(bar(ctl->empty[s][1 + m]));
-        }
-        ptx::tc_commit(bar(ctl->pv_done));
-      }
-      __syncwarp();
-      cur.next(p);
-      ++gp;
-    }
     if (lane == 0) {
+      const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
+      uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
+      Cursor cs = cur;
+      uint64_t idle_since = 0;
+      uint32_t idle = 0;
+      // S of the next tile and P V of the oldest go out as their operands
+      // arrive: S first would leave a tile's buffer occupied while the next
+      // tile is still on its way.
+      while (cur.valid()) {
+        if (cs.valid() && gs <= gp + 1 && ptx::mbar_test_wait(bar(ctl->full[gs & 1u]), (gs >> 1) & 1u) &&
+            (!cs.is_first() || ptx::mbar_test_wait(bar(ctl->q_full), seg_s & 1u))) {
+          ptx::tc_fence_after();
+          const uint32_t d = tmem + kSCol + (gs & 1u) * kKeys;
+          const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
+          const uint64_t b = desc_sw128(base + kKvOff + (gs & 1u) * kTile, 16, kGroup);
+#pragma unroll
+          for (int c = 0; c < 9; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16(d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc_s, c + k > 0);
+          ptx::tc_commit(bar(ctl->s_full[gs & 1u]));
+          if (cs.is_last()) ptx::tc_commit(bar(ctl->q_empty));
+          if (cs.is_first()) ++seg_s;
+          cs.next(p);
+          ++gs;
+          idle = 0;
+        } else if (gp < gs && ptx::mbar_test_wait(bar(ctl->p_full), gp & 1u) &&
+                   // the previous segment's accumulator has been read
+                   (!cur.is_first() || seg_p == 0 || ptx::mbar_test_wait(bar(ctl->o_free), (seg_p - 1) & 1u))) {
+          ptx::tc_fence_after();
+          const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, (cur.rows(p) + 15) / 16 * 16, true, false);
+          const uint32_t more = cur.is_first() ? 0u : 1u;
+          const uint64_t a = desc_sw128(base + kKvOff + (gp & 1u) * kTile, 1024, kGroup);
+          const uint64_t b = desc_sw128(base + kPOff, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) { // 16 keys: two groups of C, 32 bytes of P
+#pragma unroll
+            for (int m = 0; m < 4; ++m)       // 128 values: two chunks
+              mma_f16(tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc_o,
+                      k ? 1u : more);
+            ptx::tc_commit(bar(ctl->empty[gp & 1u][k]));
+          }
+          ptx::tc_commit(bar(ctl->pv_done));
+          if (cur.is_first()) ++seg_p;
+          cur.next(p);
+          ++gp;
+          idle = 0;
+        } else if ((++idle & 255u) == 0u) {
+          if (wctl->abort) break;
+          const uint64_t now = ptx::globaltimer_ns();
+          if (idle == 256u) idle_since = now;
+          if (now - idle_since > uint64_t(wctl->limit_us) * 1000u) {
+            wctl->abort = 1;
+            atomicOr(&g_decode_flags, kFlagTimeout);
+            break;
+          }
+        }
+      }
       ptx::tc_commit(bar(ctl->drain));
       drain_phase(bar(ctl->drain), 0);
     }
@@ -470,8 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (keys < kKeys) {
         const int from = max(keys, 0);
         const uint32_t kv = base + kKvOff + (g & 1u) * kTile;
-        for (int i = threadIdx.x; i < (kKeys - from) * 64; i += kSoftmaxThreads)
-          ptx::sts128(kv + (i & 7) * kChunk + (from + (i >> 6)) * 128 + ((i >> 3) & 7) * 16, 0, 0, 0, 0);
+        for (int i = threadIdx.x; i < (kKeys - from) * 64; i += kSoftmaxThreads) {
+          const int k = from + (i >> 6);      // 64 pieces of 16 bytes a key: eight in each of eight chunks
+          ptx::sts128(kv + (k >> 3) * kGroup + ((i >> 3) & 7) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
+        }
       }
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
@@ -614,8 +605,8 @@ template <typename T>
 int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   CUtensorMap q_map, kv_map;
   const int rows = a.Sq * a.H;
-  if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows) ||
-      !encode_rows<T>(&kv_map, a.cache, int64_t(a.num_pages) * a.page, std::min(a.page, kKeys))) {
+  if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
+      !encode_rows<T>(&kv_map, a.cache, int64_t(a.num_pages) * a.page, 8, 9)) {
     set_error_detail("cuTensorMapEncodeTiled failed or is unavailable");
     return NVFP4MOE_ERR_CUDA;
   }

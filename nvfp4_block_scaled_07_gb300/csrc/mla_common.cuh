@@ -83,6 +83,15 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
   }
 }
 
+// The same for a whole converged warp: all lanes get one answer.
+__device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, ptx::mbar_test_wait(bar, parity) != 0);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
+  if (test_warp(bar, parity)) return true;
+  return __all_sync(0xFFFFFFFFu, wait_phase<true>(bar, parity, ctl));
+}
+
 // Wait for a CTA's own copies or MMAs before it leaves, also after an abort.
 __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer_ns();
@@ -100,26 +109,70 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t format, int M, int N, 
          | (uint32_t(a_mn ? 1u : 0u) << 15) | (uint32_t(b_mn ? 1u : 0u) << 16)
          | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
-// D[tmem] (+)= A[smem] B[smem]^T, K = 16.
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// One lane of a converged warp, chosen by the hardware (the same one each
+// time).  The MMA and TMA issuers run their loops with the whole warp and
+// predicate the issue on this: with warp-uniform operands an MMA issues in
+// about 30 cycles, from a single-lane branch (whose operands are moved to
+// uniform registers one by one) in about 50 and more.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      :
+      : "memory");
+  return r;
+}
+// D[tmem] (+)= A[smem] B[smem]^T, K = 16, issued where `elected`.
+__device__ __forceinline__ void mma_f16(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
 // The same with A in tensor memory: lane = row of A, 16-bit pairs along K.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
+// Arrive on `bar` once every MMA issued so far by the elected lane has completed.
+__device__ __forceinline__ void tc_commit(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t elected, uint32_t dst, const void* tmap, uint32_t bar, int32_t c0,
+                                            int32_t c1, int32_t c2) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_expect_tx(uint32_t elected, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(elected)
+      : "memory");
+}
+
 // Shared-memory operand descriptors, 128-byte swizzle.  An operand is made of
 // atoms of 8 rows x 128 bytes (1024 bytes, aligned to as much).
 //   K-major: rows are M (N), their 64 values along K; `stride` from one 8-row

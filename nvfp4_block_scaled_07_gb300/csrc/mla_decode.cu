@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Control* ctl = reinterpret_cast<Control*>(smem);
   volatile WaitCtl* wctl = &ctl->wait;
   const uint32_t base = ptx::smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
   if (threadIdx.x == 0) {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(kFull, ctl->tmem, 0);
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
@@ -227,134 +227,124 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0)                      // lengths that are not served as they are
       for (int b = lane; b < p.B; b += 32)
         if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
-    if (lane == 0) {
-      const uint64_t policy = ptx::policy_evict_normal();
-      const int oob = p.num_pages * p.page;
-      const int per = p.page < kKeys ? kKeys / p.page : 1;  // pages of a tile
-      uint32_t g = 0, seg = 0;
-      // First cache rows of the tile's four pieces of 16 keys.
-      auto look_up = [&](const Cursor& c, int (&from)[kPieces]) {
-        const int row = int(c.tile) * kKeys;
-        const int32_t* t = p.tables + c.b * p.table_stride + (row >> p.log_page);
+    const uint32_t el = elect_one();
+    const int oob = p.num_pages * p.page;
+    const int per = p.page < kKeys ? kKeys / p.page : 1;  // pages of a tile
+    uint32_t g = 0, seg = 0;
+    // First cache rows of the tile's four pieces of 16 keys, one a lane.
+    auto look_up = [&](const Cursor& c) {
+      const int row = int(c.tile) * kKeys, i = lane & (kPieces - 1);
+      if (i * 16 >= c.keys()) return oob;
+      const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page) + ((i * per) >> 2));
+      if (id >= 0 && id < p.num_pages) return id * p.page + ((row + 16 * i) & (p.page - 1));
+      atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
+      return oob;
+    };
+    int mine = cur.valid() ? look_up(cur) : 0;
+    bool ok = true;
+    while (ok && cur.valid()) {
+      if (cur.is_first()) {
+        if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
+        arrive_expect_tx(el, bar(ctl->q_full), kTile);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          from[i] = oob;
-          if (i * 16 < c.keys()) {
-            const int id = __ldg(t + ((i * per) >> 2));
-            if (id >= 0 && id < p.num_pages) from[i] = id * p.page + ((row + 16 * i) & (p.page - 1));
-            else atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
-          }
-        }
-      };
-      int from[kPieces], next[kPieces];
-      if (cur.valid()) look_up(cur, from);
-      bool ok = true;
-      while (ok && cur.valid()) {
-        if (cur.is_first()) {
-          if (!wait_phase<true>(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
-          ptx::mbar_arrive_expect_tx(bar(ctl->q_full), kTile);
-#pragma unroll
-          for (int c = 0; c < 9; c += 3)
-            ptx::tma_load_3d(base + kQOff + c * kChunk, &q_map, bar(ctl->q_full), 0,
-                             cur.b * p.rows + cur.block * kRows, c, policy);
-          ++seg;
-        }
-        const int s = int(g & 1u);
-        const uint32_t ph = (g >> 1) & 1u, fb = bar(ctl->full[s]);
-        const int groups = (max(cur.keys(), 0) + 7) / 8;
-        Cursor nxt = cur;
-        nxt.next(p);
-        if (nxt.valid()) look_up(nxt, next);
-        const uint32_t dst = base + kKvOff + s * kTile;
-        ok = wait_phase<true>(bar(ctl->empty[s][0]), ph ^ 1u, wctl);
-        if (!ok) break;
-        ptx::mbar_arrive_expect_tx(fb, uint32_t(groups * kGroup));
-        ++g;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          // After an abort the rest of the tile still comes: the copies that
-          // the barrier was told to expect have to end before the CTA does.
-          if (i && ok) ok = wait_phase<true>(bar(ctl->empty[s][i]), ph ^ 1u, wctl);
-          if (2 * i < groups) ptx::tma_load_3d(dst + 2 * i * kGroup, &kv_map, fb, 0, from[i], 0, policy);
-          if (2 * i + 1 < groups)
-            ptx::tma_load_3d(dst + (2 * i + 1) * kGroup, &kv_map, fb, 0, min(from[i], oob - 8) + 8, 0, policy);
-        }
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) from[i] = next[i];
-        cur = nxt;
+        for (int c = 0; c < 9; c += 3)
+          tma_load_3d(el, base + kQOff + c * kChunk, &q_map, bar(ctl->q_full), 0, cur.b * p.rows + cur.block * kRows, c);
+        ++seg;
       }
-      // every copy that was issued has landed before the CTA leaves
-      if (seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
-      for (uint32_t s = 0; s < kStages; ++s) {
-        const uint32_t n = (g + 1 - s) / 2;   // uses of the stage
-        if (n) drain_phase(bar(ctl->full[s]), (n - 1) & 1u);
+      const uint32_t s = g & 1u, ph = (g >> 1) & 1u, fb = bar(ctl->full[s]);
+      const int groups = (max(cur.keys(), 0) + 7) / 8;
+      Cursor nxt = cur;
+      nxt.next(p);
+      const int next = nxt.valid() ? look_up(nxt) : 0;
+      const uint32_t dst = base + kKvOff + s * kTile;
+      ok = wait_warp(bar(ctl->empty[s][0]), ph ^ 1u, wctl);
+      if (!ok) break;
+      arrive_expect_tx(el, fb, uint32_t(groups * kGroup));
+      ++g;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        // After an abort the rest of the tile still comes: the copies that
+        // the barrier was told to expect have to end before the CTA does.
+        if (i && ok) ok = wait_warp(bar(ctl->empty[s][i]), ph ^ 1u, wctl);
+        const int from = __shfl_sync(kFull, mine, i);
+        if (2 * i < groups) tma_load_3d(el, dst + 2 * i * kGroup, &kv_map, fb, 0, from, 0);
+        if (2 * i + 1 < groups)
+          tma_load_3d(el, dst + (2 * i + 1) * kGroup, &kv_map, fb, 0, min(from, oob - 8) + 8, 0);
       }
+      mine = next;
+      cur = nxt;
+    }
+    // every copy that was issued has landed before the CTA leaves
+    if (seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
+    for (uint32_t s = 0; s < kStages; ++s) {
+      const uint32_t n = (g + 1 - s) / 2;     // uses of the stage
+      if (n) drain_phase(bar(ctl->full[s]), (n - 1) & 1u);
     }
     __syncwarp();
   } else if (warp == 5) {
     // ---- MMA issuer ----
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
-      uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
-      Cursor cs = cur;
-      uint64_t idle_since = 0;
-      uint32_t idle = 0;
-      // S of the next tile and P V of the oldest go out as their operands
-      // arrive: S first would leave a tile's buffer occupied while the next
-      // tile is still on its way.
-      while (cur.valid()) {
-        if (cs.valid() && gs <= gp + 1 && ptx::mbar_test_wait(bar(ctl->full[gs & 1u]), (gs >> 1) & 1u) &&
-            (!cs.is_first() || ptx::mbar_test_wait(bar(ctl->q_full), seg_s & 1u))) {
-          ptx::tc_fence_after();
-          const uint32_t d = tmem + kSCol + (gs & 1u) * kKeys;
-          const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
-          const uint64_t b = desc_sw128(base + kKvOff + (gs & 1u) * kTile, 16, kGroup);
+    const uint32_t el = elect_one();
+    const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
+    uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
+    Cursor cs = cur;
+    uint64_t idle_since = 0;
+    uint32_t idle = 0;
+    // S of the next tile and P V of the oldest go out as their operands
+    // arrive: S first would leave a tile's buffer occupied while the next
+    // tile is still on its way.
+    while (cur.valid()) {
+      if (cs.valid() && gs <= gp + 1 && test_warp(bar(ctl->full[gs & 1u]), (gs >> 1) & 1u) &&
+          (!cs.is_first() || test_warp(bar(ctl->q_full), seg_s & 1u))) {
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + kSCol + (gs & 1u) * kKeys;
+        const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
+        const uint64_t b = desc_sw128(base + kKvOff + (gs & 1u) * kTile, 16, kGroup);
 #pragma unroll
-          for (int c = 0; c < 9; ++c)
+        for (int c = 0; c < 9; ++c)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16(d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc_s, c + k > 0);
-          ptx::tc_commit(bar(ctl->s_full[gs & 1u]));
-          if (cs.is_last()) ptx::tc_commit(bar(ctl->q_empty));
-          if (cs.is_first()) ++seg_s;
-          cs.next(p);
-          ++gs;
-          idle = 0;
-        } else if (gp < gs && ptx::mbar_test_wait(bar(ctl->p_full), gp & 1u) &&
-                   // the previous segment's accumulator has been read
-                   (!cur.is_first() || seg_p == 0 || ptx::mbar_test_wait(bar(ctl->o_free), (seg_p - 1) & 1u))) {
-          ptx::tc_fence_after();
-          const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, (cur.rows(p) + 15) / 16 * 16, true, false);
-          const uint32_t more = cur.is_first() ? 0u : 1u;
-          const uint64_t a = desc_sw128(base + kKvOff + (gp & 1u) * kTile, 1024, kGroup);
-          const uint64_t b = desc_sw128(base + kPOff, 16, 1024);
+          for (int k = 0; k < 4; ++k)
+            mma_f16(el, d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc_s, c + k > 0);
+        tc_commit(el, bar(ctl->s_full[gs & 1u]));
+        if (cs.is_last()) tc_commit(el, bar(ctl->q_empty));
+        if (cs.is_first()) ++seg_s;
+        cs.next(p);
+        ++gs;
+        idle = 0;
+      } else if (gp < gs && test_warp(bar(ctl->p_full), gp & 1u) &&
+                 // the previous segment's accumulator has been read
+                 (!cur.is_first() || seg_p == 0 || test_warp(bar(ctl->o_free), (seg_p - 1) & 1u))) {
+        ptx::tc_fence_after();
+        const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, (cur.rows(p) + 15) / 16 * 16, true, false);
+        const uint32_t more = cur.is_first() ? 0u : 1u;
+        const uint64_t a = desc_sw128(base + kKvOff + (gp & 1u) * kTile, 1024, kGroup);
+        const uint64_t b = desc_sw128(base + kPOff, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < kPieces; ++k) { // 16 keys: two groups of C, 32 bytes of P
+        for (int k = 0; k < kPieces; ++k) {   // 16 keys: two groups of C, 32 bytes of P
 #pragma unroll
-            for (int m = 0; m < 4; ++m)       // 128 values: two chunks
-              mma_f16(tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc_o,
-                      k ? 1u : more);
-            ptx::tc_commit(bar(ctl->empty[gp & 1u][k]));
-          }
-          ptx::tc_commit(bar(ctl->pv_done));
-          if (cur.is_first()) ++seg_p;
-          cur.next(p);
-          ++gp;
-          idle = 0;
-        } else if ((++idle & 255u) == 0u) {
-          if (wctl->abort) break;
-          const uint64_t now = ptx::globaltimer_ns();
-          if (idle == 256u) idle_since = now;
-          if (now - idle_since > uint64_t(wctl->limit_us) * 1000u) {
-            wctl->abort = 1;
-            atomicOr(&g_decode_flags, kFlagTimeout);
-            break;
-          }
+          for (int m = 0; m < 4; ++m)         // 128 values: two chunks
+            mma_f16(el, tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc_o,
+                    k ? 1u : more);
+          tc_commit(el, bar(ctl->empty[gp & 1u][k]));
         }
+        tc_commit(el, bar(ctl->pv_done));
+        if (cur.is_first()) ++seg_p;
+        cur.next(p);
+        ++gp;
+        idle = 0;
+      } else if ((++idle & 255u) == 0u) {
+        const uint64_t now = ptx::globaltimer_ns();
+        if (idle == 256u) idle_since = now;
+        bool quit = wctl->abort != 0;
+        if (now - idle_since > uint64_t(wctl->limit_us) * 1000u) {
+          wctl->abort = 1;
+          atomicOr(&g_decode_flags, kFlagTimeout);
+          quit = true;
+        }
+        if (__any_sync(kFull, quit)) break;
       }
-      ptx::tc_commit(bar(ctl->drain));
-      drain_phase(bar(ctl->drain), 0);
     }
+    tc_commit(el, bar(ctl->drain));
+    drain_phase(bar(ctl->drain), 0);
     __syncwarp();
   } else {
     // ---- softmax and epilogue ----

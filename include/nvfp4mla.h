@@ -85,7 +85,8 @@ int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, in
  * ws: device scratch of mla_decode_workspace_size() bytes, 256-byte aligned,
  * not initialised; calls that share it must not overlap on the GPU.
  * Limits: page_size a power of two >= 16; num_pages * page_size < 2^31; B, Sq,
- * H >= 1 with B * Sq * H < 2^31 (B = 0 is a no-op); scale > 0 and finite. */
+ * H >= 1 with B * Sq * H < 2^31 (B = 0 is a no-op) and B * ceil(Sq * H / 64)
+ * * ceil(max_pages * page_size / 64) < 2^31; scale > 0 and finite. */
 size_t mla_decode_workspace_size(void);
 int mla_decode(const void* q, const void* cache, int num_pages, int page_size,
                const int32_t* block_tables, int64_t table_stride, int max_pages, const int32_t* seq_lens,

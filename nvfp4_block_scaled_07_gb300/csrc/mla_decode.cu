@@ -51,8 +51,9 @@ constexpr int kTile = 9 * kChunk;
 constexpr int kGroup = 8 * 2 * kRow;          // 8 keys: nine atoms of 8 rows x 128 bytes
 constexpr int kPieces = 4;                    // of a tile: 16 keys each, freed one by one
 constexpr int kStages = 2;
-constexpr int kThreads = 192;
-constexpr int kSoftmaxThreads = 128;
+constexpr int kProducer = 8, kIssuer = 12;    // first producer warp, MMA warp
+constexpr int kThreads = 416;
+constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;               // S buffers after the 4 x 64 columns of O^T
 constexpr float kGrow = 8.0f;                 // rescale O only when a maximum grew by 2^8
@@ -69,18 +70,20 @@ struct Control {
   uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
-  float col[kRows];                           // per-row factors for the transposed accumulator
+  float half[2][kRows];                       // per row: maxima, later sums, of the two halves of a tile's keys
+  alignas(16) float col[kRows];               // per-row factors for the transposed accumulator
 };
 static_assert(sizeof(Control) <= kCtrl, "control block");
 static_assert(kSmem <= 232448, "shared memory");
 
-// What CTA c's range begins with, for the kernel that joins partial results.
+// What a CTA's range begins with, for the kernel that joins partial results.
 struct Head {
-  int64_t tile, tiles;                        // first tile within the item, and the item's tiles
+  int32_t start, tiles, share;                // the item's place in the tile list, its tiles; tiles of a range
   int32_t b, block;
 };
 
 struct DecodeParams {
+  const uint8_t* cache;
   const int32_t* tables;
   int64_t table_stride;
   const int32_t* lens;
@@ -89,7 +92,7 @@ struct DecodeParams {
   float scale_log2, scale;
   uint8_t* out;                               // [B, rows, 512]
   float* lse;                                 // [B, rows]
-  int64_t min_share;
+  int min_share;
   Head* heads;                                // [grid]
   float* part_o;                              // [grid][2][64][512]
   float* part_lse;                            // [grid][2][64], log2 domain
@@ -101,35 +104,38 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int b) {
   return n < 0 ? 0 : int(min(int64_t(n), int64_t(p.max_pages) * p.page));
 }
 // Tiles of an item; an empty sequence has one, whose keys are all masked.
-__device__ __forceinline__ int64_t item_tiles(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
+__device__ __forceinline__ int item_tiles(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
 
 // Walks the tiles [pos, end) of the flattened (sequence, row block, tile) list.
 struct Cursor {
-  int64_t pos, end;                           // in the tile list
-  int64_t tile, tiles, first;                 // within the item; where this CTA entered it
+  int pos, end;                               // in the tile list
+  int tile, tiles, first;                     // within the item; where this CTA entered it
   int b, block, len;
 
   // Executed by a whole warp: the CTA's range and its first item.  Returns the share.
-  __device__ __forceinline__ int64_t init(const DecodeParams& p) {
+  __device__ __forceinline__ int init(const DecodeParams& p) {
     const int lane = threadIdx.x & 31;
-    int64_t total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) total += b0 + lane < p.B ? item_tiles(seq_len(p, b0 + lane)) : 0;
+    int total = 0, n = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
+      total += b0 + lane < p.B ? item_tiles(n) : 0;
+    }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
     total *= p.blocks;
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    share = share > p.min_share ? share : p.min_share;
-    pos = share * blockIdx.x;
-    end = min(total, pos + share);
+    const int share = max(int((unsigned(total) + gridDim.x - 1) / gridDim.x), p.min_share);
+    const int64_t from = int64_t(share) * blockIdx.x;
+    pos = int(min(from, int64_t(total)));
+    end = int(min(from + share, int64_t(total)));
     if (pos >= end) return share;
-    int64_t before = 0;                       // tiles of the sequences before b0
+    int before = 0;                           // tiles of the sequences before b0
     for (int b0 = 0;; b0 += 32) {
-      const int n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-      const int64_t mine = b0 + lane < p.B ? item_tiles(n) * p.blocks : 0;
-      int64_t upto = mine;
+      if (p.B > 32) n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
+      const int mine = b0 + lane < p.B ? item_tiles(n) * p.blocks : 0;
+      int upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int64_t v = __shfl_up_sync(kFull, upto, d);
+        const int v = __shfl_up_sync(kFull, upto, d);
         if (lane >= d) upto += v;
       }
       const unsigned hit = __ballot_sync(kFull, before + upto > pos);
@@ -137,10 +143,10 @@ struct Cursor {
         const int src = __ffs(hit) - 1;
         b = b0 + src;
         len = __shfl_sync(kFull, n, src);
-        const int64_t in = pos - before - __shfl_sync(kFull, upto - mine, src);
+        const int in = pos - before - __shfl_sync(kFull, upto - mine, src);
         tiles = item_tiles(len);
-        block = int(in / tiles);
-        tile = first = in - int64_t(block) * tiles;
+        block = in / tiles;
+        tile = first = in - block * tiles;
         return share;
       }
       before += __shfl_sync(kFull, upto, 31);
@@ -162,9 +168,18 @@ struct Cursor {
       }
     }
   }
-  __device__ __forceinline__ int keys() const { return min(kKeys, len - int(tile) * kKeys); }  // <= 0: none
+  __device__ __forceinline__ int keys() const { return min(kKeys, len - tile * kKeys); }  // <= 0: none
   __device__ __forceinline__ int rows(const DecodeParams& p) const { return min(kRows, p.rows - block * kRows); }
 };
+
+__device__ __forceinline__ void prefetch_l2(uint32_t elected, const void* at, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q cp.async.bulk.prefetch.L2.global [%0], %1;\n\t}" ::"l"(at),
+      "r"(bytes), "r"(elected)
+      : "memory");
+}
 
 // 16-bit rows [rows, 576] in boxes of `box_rows` rows x `chunks` chunks of 64
 // values, which land chunk by chunk, each as box_rows x 128 bytes.
@@ -188,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->full[s]), 1);
+      ptx::mbar_init(bar(ctl->full[s]), kPieces);
       for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->empty[s][i]), 1);
     }
     ptx::mbar_init(bar(ctl->q_full), 1);
@@ -204,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->wait.limit_us = p.wait_us;
     ctl->wait.flags = &g_decode_flags;
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == kProducer && lane == 0) {
     ptx::prefetch_tmap(&q_map);
     ptx::prefetch_tmap(&kv_map);
   }
-  if (warp == 5) {
+  if (warp == kIssuer) {
     ptx::tmem_alloc(base + uint32_t(offsetof(Control, tmem)), kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -220,30 +235,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::grid_dep_launch();
 
   Cursor cur;
-  const int64_t share = cur.init(p);
+  const int share = cur.init(p);
 
-  if (warp == 4) {
-    // ---- producer ----
-    if (blockIdx.x == 0)                      // lengths that are not served as they are
+  if (warp >= kProducer && warp < kProducer + kPieces) {
+    // ---- producers: one warp for each piece of 16 keys, so that a tile's
+    // copies are issued in the time of two ----
+    const int piece = warp - kProducer;
+    if (piece == 0 && blockIdx.x == 0)        // lengths that are not served as they are
       for (int b = lane; b < p.B; b += 32)
         if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
     const uint32_t el = elect_one();
     const int oob = p.num_pages * p.page;
-    const int per = p.page < kKeys ? kKeys / p.page : 1;  // pages of a tile
     uint32_t g = 0, seg = 0;
-    // First cache rows of the tile's four pieces of 16 keys, one a lane.
+    // First cache row of the piece.
     auto look_up = [&](const Cursor& c) {
-      const int row = int(c.tile) * kKeys, i = lane & (kPieces - 1);
-      if (i * 16 >= c.keys()) return oob;
-      const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page) + ((i * per) >> 2));
-      if (id >= 0 && id < p.num_pages) return id * p.page + ((row + 16 * i) & (p.page - 1));
-      atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
+      const int row = c.tile * kKeys + 16 * piece;
+      if (row >= c.len) return oob;
+      const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
+      if (id >= 0 && id < p.num_pages) return id * p.page + (row & (p.page - 1));
+      if (lane == 0) atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
       return oob;
     };
     int mine = cur.valid() ? look_up(cur) : 0;
-    bool ok = true;
-    while (ok && cur.valid()) {
-      if (cur.is_first()) {
+    while (cur.valid()) {
+      if (piece == 0 && cur.is_first()) {
         if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
         arrive_expect_tx(el, bar(ctl->q_full), kTile);
 #pragma unroll
@@ -251,72 +266,76 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(el, base + kQOff + c * kChunk, &q_map, bar(ctl->q_full), 0, cur.b * p.rows + cur.block * kRows, c);
         ++seg;
       }
-      const uint32_t s = g & 1u, ph = (g >> 1) & 1u, fb = bar(ctl->full[s]);
-      const int groups = (max(cur.keys(), 0) + 7) / 8;
-      Cursor nxt = cur;
-      nxt.next(p);
-      const int next = nxt.valid() ? look_up(nxt) : 0;
-      const uint32_t dst = base + kKvOff + s * kTile;
-      ok = wait_warp(bar(ctl->empty[s][0]), ph ^ 1u, wctl);
-      if (!ok) break;
+      const uint32_t s = g & 1u, fb = bar(ctl->full[s]);
+      const uint32_t dst = base + kKvOff + s * kTile + 2 * piece * kGroup;
+      const int groups = min(2, max(0, (cur.keys() - 16 * piece + 7) / 8));
+      if (!wait_warp(bar(ctl->empty[s][piece]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
       arrive_expect_tx(el, fb, uint32_t(groups * kGroup));
+      if (groups > 0) tma_load_3d(el, dst, &kv_map, fb, 0, mine, 0);
+      if (groups > 1) tma_load_3d(el, dst + kGroup, &kv_map, fb, 0, min(mine, oob - 8) + 8, 0);
       ++g;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        // After an abort the rest of the tile still comes: the copies that
-        // the barrier was told to expect have to end before the CTA does.
-        if (i && ok) ok = wait_warp(bar(ctl->empty[s][i]), ph ^ 1u, wctl);
-        const int from = __shfl_sync(kFull, mine, i);
-        if (2 * i < groups) tma_load_3d(el, dst + 2 * i * kGroup, &kv_map, fb, 0, from, 0);
-        if (2 * i + 1 < groups)
-          tma_load_3d(el, dst + (2 * i + 1) * kGroup, &kv_map, fb, 0, min(from, oob - 8) + 8, 0);
+      cur.next(p);
+      if (cur.valid()) {
+        // Shared memory holds two tiles, too few to cover the latency of HBM:
+        // the next piece is requested into L2 while its buffer is still in
+        // use.  One tile ahead measured best (three ahead: 6 % slower).
+        mine = look_up(cur);
+        const int rows = min(16, cur.len - cur.tile * kKeys - 16 * piece);
+        if (rows > 0 && mine != oob)
+          prefetch_l2(el, p.cache + int64_t(mine) * (2 * kRow), uint32_t(rows) * (2 * kRow));
       }
-      mine = next;
-      cur = nxt;
     }
-    // every copy that was issued has landed before the CTA leaves
+    // Every copy that this warp issued has landed before the CTA leaves: the
+    // barrier's phase also needs the other pieces, which after an abort may
+    // not come, so the wait is bounded.
     if (seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
     for (uint32_t s = 0; s < kStages; ++s) {
       const uint32_t n = (g + 1 - s) / 2;     // uses of the stage
       if (n) drain_phase(bar(ctl->full[s]), (n - 1) & 1u);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == kIssuer) {
     // ---- MMA issuer ----
     const uint32_t el = elect_one();
     const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
     uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
     Cursor cs = cur;
-    uint64_t idle_since = 0;
-    uint32_t idle = 0;
-    // S of the next tile and P V of the oldest go out as their operands
-    // arrive: S first would leave a tile's buffer occupied while the next
-    // tile is still on its way.
-    while (cur.valid()) {
-      if (cs.valid() && gs <= gp + 1 && test_warp(bar(ctl->full[gs & 1u]), (gs >> 1) & 1u) &&
-          (!cs.is_first() || test_warp(bar(ctl->q_full), seg_s & 1u))) {
+    bool ok = true;
+    // The two tiles in shared memory go through together: S, S, P V, P V.
+    // The softmax of each then runs under an MMA of the other, and the copies
+    // of the next two under both P V.  Issuing whatever was ready instead put
+    // an S in front of the P V that frees a buffer in most rounds (3500
+    // cycles a tile).
+    while (ok && cur.valid()) {
+      for (int i = 0; i < kStages && ok && cs.valid(); ++i) {
+        const uint32_t s = gs & 1u;
+        ok = wait_warp(bar(ctl->full[s]), (gs >> 1) & 1u, wctl);
+        if (ok && cs.is_first()) ok = wait_warp(bar(ctl->q_full), seg_s++ & 1u, wctl);
+        if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + kSCol + (gs & 1u) * kKeys;
+        const uint32_t d = tmem + kSCol + s * kKeys;
         const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
-        const uint64_t b = desc_sw128(base + kKvOff + (gs & 1u) * kTile, 16, kGroup);
+        const uint64_t b = desc_sw128(base + kKvOff + s * kTile, 16, kGroup);
 #pragma unroll
         for (int c = 0; c < 9; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_f16(el, d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc_s, c + k > 0);
-        tc_commit(el, bar(ctl->s_full[gs & 1u]));
+        tc_commit(el, bar(ctl->s_full[s]));
         if (cs.is_last()) tc_commit(el, bar(ctl->q_empty));
-        if (cs.is_first()) ++seg_s;
         cs.next(p);
         ++gs;
-        idle = 0;
-      } else if (gp < gs && test_warp(bar(ctl->p_full), gp & 1u) &&
-                 // the previous segment's accumulator has been read
-                 (!cur.is_first() || seg_p == 0 || test_warp(bar(ctl->o_free), (seg_p - 1) & 1u))) {
+      }
+      while (ok && gp < gs) {
+        const uint32_t s = gp & 1u;
+        ok = wait_warp(bar(ctl->p_full), gp & 1u, wctl);
+        // the previous segment's accumulator has been read
+        if (ok && cur.is_first() && seg_p++) ok = wait_warp(bar(ctl->o_free), seg_p & 1u, wctl);
+        if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, (cur.rows(p) + 15) / 16 * 16, true, false);
         const uint32_t more = cur.is_first() ? 0u : 1u;
-        const uint64_t a = desc_sw128(base + kKvOff + (gp & 1u) * kTile, 1024, kGroup);
+        const uint64_t a = desc_sw128(base + kKvOff + s * kTile, 1024, kGroup);
         const uint64_t b = desc_sw128(base + kPOff, 16, 1024);
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: two groups of C, 32 bytes of P
@@ -324,23 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int m = 0; m < 4; ++m)         // 128 values: two chunks
             mma_f16(el, tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc_o,
                     k ? 1u : more);
-          tc_commit(el, bar(ctl->empty[gp & 1u][k]));
+          tc_commit(el, bar(ctl->empty[s][k]));
         }
         tc_commit(el, bar(ctl->pv_done));
-        if (cur.is_first()) ++seg_p;
         cur.next(p);
         ++gp;
-        idle = 0;
-      } else if ((++idle & 255u) == 0u) {
-        const uint64_t now = ptx::globaltimer_ns();
-        if (idle == 256u) idle_since = now;
-        bool quit = wctl->abort != 0;
-        if (now - idle_since > uint64_t(wctl->limit_us) * 1000u) {
-          wctl->abort = 1;
-          atomicOr(&g_decode_flags, kFlagTimeout);
-          quit = true;
-        }
-        if (__any_sync(kFull, quit)) break;
       }
     }
     tc_commit(el, bar(ctl->drain));
@@ -350,88 +357,101 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- softmax and epilogue ----
     if (threadIdx.x == 0) {
       Head h;
-      h.tile = cur.valid() ? cur.tile : 0;
+      h.share = share;
+      h.start = cur.valid() ? cur.pos - cur.tile : 0;
       h.tiles = cur.valid() ? cur.tiles : 0;
       h.b = cur.valid() ? cur.b : 0;
       h.block = cur.valid() ? cur.block : 0;
       p.heads[blockIdx.x] = h;
     }
-    const uint32_t quarter = uint32_t(warp) << 21;  // lane 32 * warp
-    const int r0 = 16 * warp + (lane >> 2);         // this thread's rows: r0 and r0 + 8
-    float m[2], l[2];                               // running maximum (log2 domain) and sum
+    // Two warps share a quarter of the lanes: each takes half of a tile's keys
+    // in the softmax and half of the accumulator's values.
+    const int half = warp >> 2, lanes = 32 * (warp & 3);
+    const uint32_t quarter = uint32_t(lanes) << 16;
+    const int r0 = lanes / 2 + (lane >> 2);         // this thread's rows: r0 and r0 + 8
+    float m[2], l[2];                               // running maximum (log2 domain) and half's sum
     uint32_t g = 0;
-    // A failed wait is remembered and ends the loop for all four warps at the
+    // A failed wait is remembered and ends the loop for all warps at the
     // next tile's vote, so that no thread leaves others at a barrier.
     bool dead = false;
     auto wait = [&](uint32_t b, uint32_t parity) {
       dead |= !wait_phase<false>(b, parity, wctl);
       __syncwarp();
     };
+    int behind[2] = {0, 0};                         // keys of the sequence that come after the rows' tokens
     while (cur.valid()) {
+      if (cur.is_first()) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) behind[i] = p.Sq - 1 - (cur.block * kRows + r0 + 8 * i) / p.H;
+      }
       const bool first = cur.is_first(), last = cur.is_last();
       const int keys = cur.keys(), rows = cur.rows(p);
       wait(bar(ctl->s_full[g & 1u]), (g >> 1) & 1u);
       ptx::tc_fence_after();
-      uint32_t sr[32];
-      tmem_ld_16x256b_x8(tmem + quarter + kSCol + (g & 1u) * kKeys, sr);
+      uint32_t sr[16];
+      tmem_ld_16x256b_x4(tmem + quarter + kSCol + (g & 1u) * kKeys + 32 * half, sr);
       ptx::tmem_ld_wait();
       ptx::tc_fence_before();
-      // keys that row r0 + 8 i sees in this tile: query token s of Sq sees len - Sq + s + 1
+      // keys of this half that row r0 + 8 i sees: query token s of Sq sees len - Sq + s + 1
       int sees[2];
       bool masked = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + 8 * i;
-        const int tok = (cur.block * kRows + r) / p.H;
-        sees[i] = r < rows ? cur.len - (p.Sq - 1 - tok) - int(cur.tile) * kKeys : 0;
-        masked |= sees[i] < kKeys;
+        sees[i] = r < rows ? cur.len - behind[i] - cur.tile * kKeys - 32 * half : 0;
+        masked |= sees[i] < 32;
       }
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 16; ++i)
           if (8 * (i >> 2) + 2 * (lane & 3) + (i & 1) >= sees[(i >> 1) & 1]) sr[i] = 0xFF800000u;
       }
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < 32; ++i) top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], __uint_as_float(sr[i]));
-      bool grew = false;
-      float mn[2];
+      for (int i = 0; i < 16; ++i) top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], __uint_as_float(sr[i]));
+      bool grew = first;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], 1));
         top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], 2));
         top[i] *= p.scale_log2;
-        if (first) m[i] = top[i], l[i] = 0.0f;  // a first tile grows nothing
-        mn[i] = fmaxf(m[i], top[i]);
-        grew |= mn[i] - m[i] > kGrow;         // also from -inf
+        if (first) m[i] = -INFINITY, l[i] = 0.0f;
+        grew |= top[i] - m[i] > kGrow;        // also from -inf
+        if ((lane & 3) == 0) ctl->half[half][r0 + 8 * i] = top[i];
       }
+      // The reference maximum moves only when some row's maximum grew by 2^8:
+      // until then weights of up to 2^8 are as exact as weights of up to 1.
       if (bar_any(1, kSoftmaxThreads, grew || dead)) {
         if (bar_any(2, kSoftmaxThreads, dead)) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float a = mn[i] == m[i] ? 1.0f : exp2_approx(m[i] - mn[i]);
-          m[i] = mn[i];
+          const float mn = fmaxf(m[i], fmaxf(top[i], ctl->half[half ^ 1][r0 + 8 * i]));
+          const float a = mn == m[i] ? 1.0f : exp2_approx(m[i] - mn);
+          m[i] = mn;
           l[i] *= a;
-          if ((lane & 3) == 0) ctl->col[r0 + 8 * i] = a;
+          if (half == 0 && (lane & 3) == 0) ctl->col[r0 + 8 * i] = a;
         }
         bar_sync(2, kSoftmaxThreads);
-        wait(bar(ctl->pv_done), (g - 1) & 1u);
-        ptx::tc_fence_after();
-        for (int c = 0; c < 4 * kRows; c += 32) {
-          if ((c & (kRows - 1)) >= rows) continue;
-          uint32_t o[32];
-          ptx::tmem_ld_32x32b_x32(tmem + quarter + c, o);
-          ptx::tmem_ld_wait();
+        if (!first) {
+          wait(bar(ctl->pv_done), (g - 1) & 1u);
+          ptx::tc_fence_after();
+          for (int c = 2 * half * kRows; c < 2 * (half + 1) * kRows; c += 32) {
+            if ((c & (kRows - 1)) >= rows) continue;
+            uint32_t o[32];
+            ptx::tmem_ld_32x32b_x32(tmem + quarter + c, o);
+            ptx::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ctl->col[(c & (kRows - 1)) + i]);
-          ptx::tmem_st_32x32b_x32(tmem + quarter + c, o);
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * ctl->col[(c & (kRows - 1)) + i]);
+            ptx::tmem_st_32x32b_x32(tmem + quarter + c, o);
+          }
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
         }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
       }
       // the weights, rounded to 16 bits for the second product; their sum stays float32
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < 16; ++i) {
         const int k = (i >> 1) & 1;
         const float e = exp2_approx(fmaf(__uint_as_float(sr[i]), p.scale_log2, m[k] == -INFINITY ? 0.0f : -m[k]));
         l[k] += e;
@@ -439,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (g) wait(bar(ctl->pv_done), (g - 1) & 1u);  // P is free
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
+      for (int i = 0; i < 16; i += 2) {
         const int r = r0 + 8 * ((i >> 1) & 1);
-        sts32(base + kPOff + r * 128 + (((i >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4,
+        sts32(base + kPOff + r * 128 + ((((i >> 2) + 4 * half) ^ (r & 7)) << 4) + (lane & 3) * 4,
               Elem<T>::pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
       }
       // Rows of the tile past the last key may hold anything, and 0 * NaN is
@@ -459,45 +479,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_arrive(bar(ctl->p_full));
       if (last) {
         const bool whole = cur.first == 0 && cur.tile + 1 == cur.tiles;
-        const int64_t part = 2 * int64_t(blockIdx.x) + (cur.pos - cur.tile + cur.first == share * blockIdx.x ? 0 : 1);
+        const int64_t part = 2 * blockIdx.x + (cur.pos - cur.tile + cur.first == int(share * blockIdx.x) ? 0 : 1);
+        const int64_t row0 = whole ? int64_t(cur.b) * p.rows + cur.block * kRows : part * kRows;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           l[i] += __shfl_xor_sync(kFull, l[i], 1);
           l[i] += __shfl_xor_sync(kFull, l[i], 2);
-          const int r = r0 + 8 * i;
-          const float e = l[i] == 0.0f ? -INFINITY : m[i] + log2f(l[i]);
-          if ((lane & 3) == 0) {
-            ctl->col[r] = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
-            if (r < rows) {
-              if (whole) p.lse[int64_t(cur.b) * p.rows + cur.block * kRows + r] = e * kLn2;
-              else p.part_lse[part * kRows + r] = e;
-            }
-          }
+          if ((lane & 3) == 0) ctl->half[half][r0 + 8 * i] = l[i];
         }
         bar_sync(2, kSoftmaxThreads);
+        bool empty = false;                   // some row saw no key
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + 8 * i;
+          const float sum = l[i] + ctl->half[half ^ 1][r];
+          empty |= sum == 0.0f;
+          if (half == 0 && (lane & 3) == 0) {
+            ctl->col[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float e = sum == 0.0f ? -INFINITY : m[i] + log2f(sum);
+            if (r < rows) (whole ? p.lse : p.part_lse)[row0 + r] = whole ? e * kLn2 : e;
+          }
+        }
+        empty = bar_any(2, kSoftmaxThreads, empty);
         wait(bar(ctl->pv_done), g & 1u);
         ptx::tc_fence_after();
-        for (int c = 0; c < 4 * kRows; c += 32) {
-          const int c0 = c & (kRows - 1);     // first row of the piece
-          if (c0 >= rows) continue;
-          uint32_t o[32];
-          ptx::tmem_ld_32x32b_x32(tmem + quarter + c, o);
-          ptx::tmem_ld_wait();
-          const int dim = (c / kRows) * 128 + 32 * warp + lane;
-          if (whole) {
-            T* out = reinterpret_cast<T*>(p.out) +
-                     (int64_t(cur.b) * p.rows + cur.block * kRows + c0) * kLatent + dim;
+        for (int c0 = 0; c0 < rows; c0 += 32) {
+          float f[32];                        // the factors of 32 rows, for both blocks of values
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float v = ctl->col[c0 + i] == 0.0f ? 0.0f : __uint_as_float(o[i]) * ctl->col[c0 + i];
-              if (c0 + i < rows) out[i * kLatent] = Elem<T>::from(v);
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(ctl->col + c0 + i);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t o[32];
+            ptx::tmem_ld_32x32b_x32(tmem + quarter + (2 * half + v) * kRows + c0, o);
+            ptx::tmem_ld_wait();
+            const int dim = (2 * half + v) * 128 + lanes + lane, n = min(32, rows - c0);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
+            if (empty) {                      // zeros, also where masked values were not finite
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (f[i] == 0.0f) o[i] = 0u;
             }
-          } else {
-            float* out = p.part_o + (part * kRows + c0) * kLatent + dim;
+            if (whole) {
+              T* out = reinterpret_cast<T*>(p.out) + (row0 + c0) * kLatent + dim;
+              if (n == 32) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float v = ctl->col[c0 + i] == 0.0f ? 0.0f : __uint_as_float(o[i]) * ctl->col[c0 + i];
-              if (c0 + i < rows) out[i * kLatent] = v;
+                for (int i = 0; i < 32; ++i) out[i * kLatent] = Elem<T>::from(__uint_as_float(o[i]));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i < n) out[i * kLatent] = Elem<T>::from(__uint_as_float(o[i]));
+              }
+            } else {
+              float* out = p.part_o + (row0 + c0) * kLatent + dim;
+              if (n == 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) out[i * kLatent] = __uint_as_float(o[i]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i < n) out[i * kLatent] = __uint_as_float(o[i]);
+              }
             }
           }
         }
@@ -511,79 +554,108 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 5) ptx::tmem_dealloc(tmem, kTmemCols);
+  if (warp == kIssuer) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial results of the items that a range border cut.  Block
-// (c, .) serves the item that CTA c + 1's range begins inside of, if no
-// earlier range does.  With e_i the log2-sum of piece i and o_i its
-// normalised rows, out = sum 2^(e_i - e) o_i, e = log2 sum 2^e_i.
-// A block takes `4 / groups` rows; `groups` sets of 128 threads (four values
-// each) share a row's pieces.
-template <typename T>
-__global__ void __launch_bounds__(512) join_kernel(const DecodeParams p, int grid, int groups) {
-  __shared__ float4 s_sum[3][128];
+// Joins the partial results of the items that a range border cut.  With e_i
+// the log2-sum of piece i and o_i its normalised rows, out = sum 2^(e_i - e)
+// o_i, e = log2 sum 2^e_i, the pieces always in the same order.
+// A warp takes a row (16 values a lane).  BY_ITEM (few items of many pieces):
+// block (item, .), four warps share a row's pieces.  Otherwise block (c, .)
+// serves the item that the border between ranges c and c + 1 is the first to
+// cut.
+constexpr int kJoinThreads = 256;
+template <typename T, bool BY_ITEM>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p) {
+  constexpr int kShare = BY_ITEM ? 4 : 1, kJoinRows = kJoinThreads / 32 / kShare;  // warps a row, rows a block
+  __shared__ float4 s_sum[BY_ITEM ? kJoinThreads / 32 : 1][4][32];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const int c = int(blockIdx.x) + 1;
-  const Head h = p.heads[c];
-  if (h.tile == 0 || h.tiles == 0) return;
-  // the share is the same for every CTA: recovered from this one's predecessor
-  const Head before = p.heads[c - 1];
-  const bool same = before.b == h.b && before.block == h.block && before.tiles == h.tiles && before.tile != 0;
-  if (same) return;                           // an earlier border inside the item serves it
-  // pieces: the end of range c - 1, then ranges c, c + 1, ... while they begin inside the item
-  int last = c;
-  while (last + 1 < grid) {
-    const Head n = p.heads[last + 1];
-    if (n.b != h.b || n.block != h.block || n.tile == 0 || n.tiles == 0) break;
-    ++last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, set = warp % kShare;
+  int start, tiles, share, b, block;
+  if (BY_ITEM) {
+    b = int(blockIdx.x) / p.blocks;
+    block = int(blockIdx.x) - b * p.blocks;
+    share = p.heads[0].share;
+    tiles = item_tiles(seq_len(p, b));
+    start = 0;
+    for (int i = lane; i < b; i += 32) start += item_tiles(seq_len(p, i)) * p.blocks;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) start += __shfl_xor_sync(kFull, start, d);
+    start += tiles * block;
+  } else {
+    const Head h = p.heads[blockIdx.x + 1];
+    start = h.start, tiles = h.tiles, share = h.share, b = h.b, block = h.block;
+    // no item, or one that an earlier border cuts first
+    if (tiles == 0 || start < int(blockIdx.x) * share) return;
   }
-  const int pieces = last - c + 2;
-  const int set = threadIdx.x >> 7, t = threadIdx.x & 127;
-  const int row = blockIdx.y * (4 / groups) + set / groups, grp = set % groups;
-  const int rows = min(kRows, p.rows - h.block * kRows);
-  const bool live = row < rows;
-  // piece 0 is the first segment of range c - 1 if that range begins with the item, else its last
-  const bool at_start = before.b == h.b && before.block == h.block && before.tiles != 0 && before.tile == 0;
-  auto piece_row = [&](int i) -> int64_t {
-    return (i == 0 ? 2 * int64_t(c - 1) + (at_start ? 0 : 1) : 2 * int64_t(c - 1 + i)) * kRows + row;
-  };
-  float e_top = -INFINITY, sum = 0.0f;
-  float4 acc = make_float4(0, 0, 0, 0);
+  const int first = start / share, last = (start + tiles - 1) / share;
+  if (first == last) return;                  // whole: written by its CTA (also an item that begins at the border)
+  const int pieces = last - first + 1;
+  const int row = blockIdx.y * kJoinRows + warp / kShare;
+  const bool live = row < min(kRows, p.rows - block * kRows);
+  // piece 0 is the last segment of range `first` unless the range begins with it
+  const int lead = start != first * share ? 1 : 0;
+  auto piece_row = [&](int i) { return int64_t(2 * (first + i) + (i == 0 ? lead : 0)) * kRows + row; };
+  constexpr int kPer = (kMlaDecodeMaxGrid + 31) / 32;
+  float w[kPer];                              // the weights of pieces lane, lane + 32, ...
+  float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    w[k] = live && lane + 32 * k < pieces ? p.part_lse[piece_row(lane + 32 * k)] : -INFINITY;
+    top = fmaxf(top, w[k]);
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+  const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) sum += w[k] = exp2_approx(w[k] - ref);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  float4 acc[4] = {};                         // values 128 j + 4 lane ..
   if (live) {
-    for (int i = 0; i < pieces; ++i) e_top = fmaxf(e_top, p.part_lse[piece_row(i)]);
-    const float ref = e_top == -INFINITY ? 0.0f : e_top;
-    for (int i = 0; i < pieces; ++i) sum += exp2_approx(p.part_lse[piece_row(i)] - ref);
-    const float e = sum == 0.0f ? -INFINITY : ref + log2f(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll 4
-    for (int i = grp; i < pieces; i += groups) {
-      const int64_t at = piece_row(i);
-      const float w = exp2_approx(p.part_lse[at] - ref) * inv;
-      const float4 o = *reinterpret_cast<const float4*>(p.part_o + at * kLatent + 4 * t);
-      acc.x += w * o.x, acc.y += w * o.y, acc.z += w * o.z, acc.w += w * o.w;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int n = min(32, pieces - 32 * k);
+#pragma unroll 2
+      for (int i = set; i < n; i += kShare) {
+        const float* at = p.part_o + piece_row(32 * k + i) * kLatent + 4 * lane;
+        const float a = __shfl_sync(kFull, w[k], i) * inv;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 o = *reinterpret_cast<const float4*>(at + 128 * j);
+          acc[j].x += a * o.x, acc[j].y += a * o.y, acc[j].z += a * o.z, acc[j].w += a * o.w;
+        }
+      }
     }
-    if (grp == 0 && t == 0) p.lse[int64_t(h.b) * p.rows + h.block * kRows + row] = e * kLn2;
   }
-  if (groups > 1) {
-    if (grp) s_sum[set - 1][t] = acc;
+  if (BY_ITEM) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s_sum[warp][j][lane] = acc[j];
     __syncthreads();
-    if (grp) return;
-    for (int i = 1; i < groups; ++i) {
-      const float4 o = s_sum[set + i - 1][t];
-      acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
-    }
+    if (set) return;
+#pragma unroll
+    for (int i = 1; i < kShare; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 o = s_sum[warp + i][j][lane];
+        acc[j].x += o.x, acc[j].y += o.y, acc[j].z += o.z, acc[j].w += o.w;
+      }
   }
-  if (live)
-    *reinterpret_cast<uint2*>(p.out + 2 * ((int64_t(h.b) * p.rows + h.block * kRows + row) * kLatent + 4 * t)) =
-        make_uint2(Elem<T>::pack(acc.x, acc.y), Elem<T>::pack(acc.z, acc.w));
+  if (!live) return;
+  const int64_t at = int64_t(b) * p.rows + block * kRows + row;
+  if (lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint2*>(p.out + 2 * (at * kLatent + 128 * j + 4 * lane)) =
+        make_uint2(Elem<T>::pack(acc[j].x, acc[j].y), Elem<T>::pack(acc[j].z, acc[j].w));
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles a CTA takes at least: below this, splitting a sequence costs more in partial results than it gains.
-constexpr int64_t kMinShare = 4;
+constexpr int kMinShare = 4;
 
 // Most tiles the call can have, and the grid that covers them.
 int64_t most_tiles(const MlaDecodeArgs& a) {
@@ -593,6 +665,11 @@ int64_t most_tiles(const MlaDecodeArgs& a) {
 
 template <typename T>
 int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
+  if (most_tiles(a) >= (int64_t(1) << 31)) {
+    set_error_detail("B = %d, Sq * H = %d and max_pages * page_size = %lld keys exceed 2^31 tiles of 64 rows x 64 keys",
+                     a.B, a.Sq * a.H, (long long)a.max_pages * a.page);
+    return NVFP4MOE_ERR_UNSUPPORTED;
+  }
   CUtensorMap q_map, kv_map;
   const int rows = a.Sq * a.H;
   if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
@@ -608,6 +685,7 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   p.B = a.B, p.Sq = a.Sq, p.H = a.H;
   p.rows = rows;
   p.blocks = int(ceil_div(rows, kRows));
+  p.cache = static_cast<const uint8_t*>(a.cache);
   p.num_pages = a.num_pages;
   p.page = a.page;
   p.log_page = 0;
@@ -623,13 +701,17 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   p.part_lse = reinterpret_cast<float*>(ws + kMlaDecodeHeadBytes);
   p.part_o = p.part_lse + int64_t(kMlaDecodeMaxGrid) * 2 * kRows;
   p.wait_us = wait_limit_us();
-  static_assert(sizeof(Head) * (kMlaDecodeMaxGrid + 1) <= kMlaDecodeHeadBytes, "workspace header");
+  static_assert(sizeof(Head) * kMlaDecodeMaxGrid <= kMlaDecodeHeadBytes, "workspace header");
   auto kernel = decode_kernel<T>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err == cudaSuccess) err = launch_kernel(kernel, dim3(grid), dim3(kThreads), kSmem, st, false, q_map, kv_map, p);
+  const int64_t items = int64_t(a.B) * p.blocks;
   if (err == cudaSuccess && grid > 1) {
-    const int groups = int64_t(a.B) * p.blocks * 8 <= grid ? 4 : 1;
-    err = launch_kernel(join_kernel<T>, dim3(grid - 1, kRows * groups / 4), dim3(512), 0, st, false, p, grid, groups);
+    const int most = std::min(kRows, rows);
+    if (items * 4 <= grid)
+      err = launch_kernel(join_kernel<T, true>, dim3(int(items), (most + 1) / 2), dim3(kJoinThreads), 0, st, false, p);
+    else
+      err = launch_kernel(join_kernel<T, false>, dim3(grid - 1, (most + 7) / 8), dim3(kJoinThreads), 0, st, false, p);
   }
   if (err != cudaSuccess) {
     set_error_detail("mla_decode launch: %s", cudaGetErrorString(err));

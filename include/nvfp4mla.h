@@ -93,6 +93,31 @@ int mla_decode(const void* q, const void* cache, int num_pages, int page_size,
                int B, int Sq, int H, float scale, int dtype, void* out, float* lse,
                void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* Expanded attention over a ragged batch.  Sequence b has queries cu_q[b] ..
+ * cu_q[b+1] - 1 and keys cu_k[b] .. cu_k[b+1] - 1 (nq and nk of them); its
+ * query i sees keys 0 .. nk - nq + i with causal = 1 (the queries are the
+ * last of the keys) and all nk with 0.  For head h, query t and key j:
+ *   S_j = scale * (q[t, h, :128] . k_nope[j, h] + q[t, h, 128:] . k_rope[j])
+ *   out[t, h] = sum_j softmax(S)_j v[j, h],  lse[t, h] = ln sum_j exp(S_j)
+ * A query that sees no key gets zeros and -inf.  Values of v that a query does
+ * not see must be finite where they are of its own sequence (a weight of zero
+ * is multiplied with them); those of other sequences may be anything.
+ * q [Tq, H, 192], k_nope [Tk, H, 128], k_rope [Tk, 64], v [Tk, H, 128]:
+ * innermost dimension contiguous, strides multiples of 8 and below 2^38; they may be
+ * slices of larger tensors.  out [Tq, H, 128] and lse float32 [Tq, H]
+ * contiguous.  cu_q, cu_k device int32 [B + 1], ascending, within [0, Tq] and
+ * [0, Tk]: offsets outside are clamped and raise NVFP4MOE_ERR_DEVICE_DATA.
+ * Outputs of tokens in no sequence are left untouched.  The softmax's weights
+ * are rounded to dtype for the product with the values; their sum is not.
+ * Limits: B, H >= 1, Tq, Tk >= 0, Tq * H and Tk * H < 2^31, (Tq / 256 + B) * H < 2^31
+ * (B = 0, Tq = 0 or H = 0 is a no-op); scale > 0 and finite. */
+int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                const void* k_nope, int64_t k_nope_token_stride, int64_t k_nope_head_stride,
+                const void* k_rope, int64_t k_rope_token_stride,
+                const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk, int H,
+                float scale, int causal, int dtype, void* out, float* lse, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -155,12 +155,14 @@ int nvfp4moe_sync_status(cudaStream_t stream) {
   if (st) return st;
   st = cuda_status(gemm_read_and_clear_flags(&f2), "reading device flags");
   if (st) return st;
-  unsigned f3 = 0, f4 = 0;
+  unsigned f3 = 0, f4 = 0, f5 = 0;
   st = cuda_status(mla_append_read_and_clear_flags(&f3), "reading device flags");
   if (st) return st;
   st = cuda_status(mla_decode_read_and_clear_flags(&f4), "reading device flags");
   if (st) return st;
-  const unsigned f = f1 | f2 | f3 | f4;
+  st = cuda_status(mla_prefill_read_and_clear_flags(&f5), "reading device flags");
+  if (st) return st;
+  const unsigned f = f1 | f2 | f3 | f4 | f5;
   if (f & kFlagTimeout) return fail(NVFP4MOE_ERR_TIMEOUT, "a device wait (grouped GEMM or attention pipeline, or prepare grid barrier) exceeded its time limit");
   if (f & kFlagBadData) return fail(NVFP4MOE_ERR_DEVICE_DATA, "an expert id, row index, cache slot, page, position or sequence length was out of range");
   return NVFP4MOE_OK;
@@ -759,6 +761,51 @@ int mla_decode(const void* q, const void* cache, int num_pages, int page_size, c
   a.lse = lse;
   a.ws = ws;
   return launch_mla_decode(a, d.num_sms, stream);  // detail already set on failure
+}
+
+int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,
+                int64_t k_nope_token_stride, int64_t k_nope_head_stride, const void* k_rope,
+                int64_t k_rope_token_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk, int H, float scale, int causal,
+                int dtype, void* out, float* lse, cudaStream_t stream) {
+  t_detail[0] = 0;
+  NVFP4MOE_REQUIRE(B >= 0 && Tq >= 0 && Tk >= 0 && H >= 0, NVFP4MOE_ERR_INVALID_ARG, "B = %d Tq = %d Tk = %d H = %d", B,
+                   Tq, Tk, H);
+  NVFP4MOE_REQUIRE(int64_t(Tq) * H < (int64_t(1) << 31) && int64_t(Tk) * H < (int64_t(1) << 31) &&
+                       (int64_t(Tq) / 256 + B) * H < (int64_t(1) << 31),
+                   NVFP4MOE_ERR_UNSUPPORTED, "Tq * H, Tk * H and the blocks (Tq / 256 + B) * H must be below 2^31");
+  NVFP4MOE_REQUIRE(dtype == NVFP4MLA_BF16 || dtype == NVFP4MLA_FP16, NVFP4MOE_ERR_INVALID_ARG, "dtype %d", dtype);
+  NVFP4MOE_REQUIRE(causal == 0 || causal == 1, NVFP4MOE_ERR_INVALID_ARG, "causal %d", causal);
+  NVFP4MOE_REQUIRE(scale > 0.0f && scale < 1e30f, NVFP4MOE_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (B == 0 || Tq == 0 || H == 0) return NVFP4MOE_OK;
+  NVFP4MOE_REQUIRE(q && cu_q && cu_k && out && lse && (Tk == 0 || (k_nope && k_rope && v)), NVFP4MOE_ERR_INVALID_ARG,
+                   "null pointer");
+  const int64_t strides[7] = {q_token_stride, q_head_stride, k_nope_token_stride, k_nope_head_stride,
+                              k_rope_token_stride, v_token_stride, v_head_stride};
+  for (int64_t s : strides)
+    NVFP4MOE_REQUIRE(s >= 8 && s % 8 == 0 && s < (int64_t(1) << 38), NVFP4MOE_ERR_INVALID_ARG,
+                     "stride %lld must be a positive multiple of 8 below 2^38", (long long)s);
+  NVFP4MOE_REQUIRE(aligned16(q) && aligned16(k_nope) && aligned16(k_rope) && aligned16(v) && aligned16(out) &&
+                       ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_q) |
+                         reinterpret_cast<uintptr_t>(cu_k)) & 3) == 0,
+                   NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  DeviceInfo d;
+  if (int st = current_device(&d)) return st;
+  MlaPrefillArgs a;
+  a.q = q, a.q_token_stride = q_token_stride, a.q_head_stride = q_head_stride;
+  a.k_nope = k_nope, a.kn_token_stride = k_nope_token_stride, a.kn_head_stride = k_nope_head_stride;
+  a.k_rope = k_rope, a.kr_token_stride = k_rope_token_stride;
+  a.v = v, a.v_token_stride = v_token_stride, a.v_head_stride = v_head_stride;
+  // without keys nothing is loaded, but the tensor maps still describe something
+  if (Tk == 0) a.k_nope = a.k_rope = a.v = q;
+  a.cu_q = cu_q, a.cu_k = cu_k;
+  a.B = B, a.Tq = Tq, a.Tk = Tk, a.H = H;
+  a.scale = scale;
+  a.causal = causal;
+  a.fp16 = dtype == NVFP4MLA_FP16;
+  a.out = out;
+  a.lse = lse;
+  return launch_mla_prefill(a, stream);  // detail already set on failure
 }
 
 }  // extern "C"

@@ -196,6 +196,27 @@ struct MlaDecodeArgs {
 int launch_mla_decode(const MlaDecodeArgs& a, int num_sms, cudaStream_t st);
 cudaError_t mla_decode_read_and_clear_flags(unsigned* flags);
 
+struct MlaPrefillArgs {
+  const void* q;          // [Tq, H, 192], strides in elements
+  int64_t q_token_stride, q_head_stride;
+  const void* k_nope;     // [Tk, H, 128]
+  int64_t kn_token_stride, kn_head_stride;
+  const void* k_rope;     // [Tk, 64]
+  int64_t kr_token_stride;
+  const void* v;          // [Tk, H, 128]
+  int64_t v_token_stride, v_head_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int B, Tq, Tk, H;
+  float scale;
+  int causal;
+  bool fp16;
+  void* out;
+  float* lse;
+};
+int launch_mla_prefill(const MlaPrefillArgs& a, cudaStream_t st);
+cudaError_t mla_prefill_read_and_clear_flags(unsigned* flags);
+
 // Per-thread error message used by nvfp4moe_last_error_detail().
 void set_error_detail(const char* fmt, ...);
 

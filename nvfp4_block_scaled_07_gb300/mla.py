@@ -22,6 +22,8 @@ _SIGS = {
     "mla_append": (_i, [_p, _i64, _p, _i64, _p, _f, _p, _p, _i, _p, _i64, _i, _i, _p, _i64, _p, _p, _i64, _i64, _i, _p,
                         _i64, _i64, _p]),
     "mla_decode_workspace_size": (_sz, []),
+    "mla_prefill": (_i, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i64, _p, _p, _i, _i, _i, _i, _f, _i, _i, _p,
+                         _p, _p]),
     "mla_decode": (_i, [_p, _p, _i, _i, _p, _i64, _i, _p, _i, _i, _i, _f, _i, _p, _p, _p, _sz, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -159,4 +161,42 @@ def mla_decode(q, cache, block_tables, seq_lens, scale, out=None, lse=None, work
                               max(max_pages, block_tables.stride(0) if B > 1 else 0), max_pages, _b._ptr(seq_lens), B,
                               Sq, H, float(scale), dt, _b._ptr(out), _b._ptr(lse), _b._ptr(workspace),
                               workspace.numel(), _b._stream()), "mla_decode")
+    return out, lse
+
+
+def _span(t, dim, dense):
+    """Stride of a dimension; `dense` where it has at most one entry, whose stride says nothing."""
+    return t.stride(dim) if t.shape[dim] > 1 else dense
+
+
+def mla_prefill(q, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None):
+    """Expanded attention over a ragged batch; queries are the last of their sequence's keys.
+
+    q [Tq, H, 192], k_nope [Tk, H, 128], k_rope [Tk, 64] and v [Tk, H, 128] may
+    be slices of projections' outputs; cu_q, cu_k int32 [B + 1] are the
+    sequences' offsets.  Returns (out [Tq, H, 128], lse float32 [Tq, H])."""
+    dt = _dtype(q, "q")
+    t = q.dtype
+    _strided(q, t, (None, None, NOPE + ROPE), "q")
+    Tq, H, _ = q.shape
+    _strided(k_nope, t, (None, H, NOPE), "k_nope")
+    Tk = k_nope.shape[0]
+    _strided(k_rope, t, (Tk, ROPE), "k_rope")
+    _strided(v, t, (Tk, H, VALUE), "v")
+    _dense(cu_q, torch.int32, (None,), "cu_q")
+    B = cu_q.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_q must have an entry more than there are sequences")
+    _dense(cu_k, torch.int32, (B + 1,), "cu_k")
+    out = torch.empty((Tq, H, VALUE), dtype=t, device=q.device) if out is None else out
+    lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if lse is None else lse
+    _dense(out, t, (Tq, H, VALUE), "out")
+    _dense(lse, torch.float32, (Tq, H), "lse")
+    _one_device(q=q, k_nope=k_nope, k_rope=k_rope, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+    _b._check(_lib.mla_prefill(
+        _b._ptr(q), _span(q, 0, 192 * max(H, 1)), _span(q, 1, 192),
+        _b._ptr(k_nope), _span(k_nope, 0, NOPE * max(H, 1)), _span(k_nope, 1, NOPE),
+        _b._ptr(k_rope), _span(k_rope, 0, ROPE), _b._ptr(v), _span(v, 0, VALUE * max(H, 1)), _span(v, 1, VALUE),
+        _b._ptr(cu_q), _b._ptr(cu_k), B, Tq, Tk, H, float(scale), int(bool(causal)), dt, _b._ptr(out), _b._ptr(lse),
+        _b._stream()), "mla_prefill")
     return out, lse

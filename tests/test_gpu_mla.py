@@ -1,4 +1,4 @@
-"""Latent attention against 64-bit references: cache append, absorbed decode.
+"""Latent attention against 64-bit references: cache append, absorbed decode, expanded prefill.
 
 The shapes are those where such kernels go wrong: lengths of 0, 1 and around a
 tile, pages that end inside a tile, row blocks that are not full, rows that
@@ -320,3 +320,162 @@ def test_decode_empty_batch(M):
                             torch.empty(0, 4, dtype=torch.int32, device="cuda"),
                             torch.empty(0, dtype=torch.int32, device="cuda"), SCALE)
     assert out.shape == (0, 1, 16, 512) and lse.shape == (0, 1, 16)
+
+
+# ---- prefill -------------------------------------------------------------------------------------------------
+def prefill_case(lens, H, dtype, seed, pad=5, q_std=1.0):
+    """lens: (queries, keys) of each sequence.  `pad` tokens of NaN follow the last sequence."""
+    g = gen(seed)
+    cu_q = [0]
+    cu_k = [0]
+    for n, m in lens:
+        cu_q.append(cu_q[-1] + n)
+        cu_k.append(cu_k[-1] + m)
+    Tq, Tk = cu_q[-1] + pad, cu_k[-1] + pad
+    q = normal(g, Tq, H, 192, dtype=dtype, std=q_std)
+    up, kr = normal(g, Tk, H, 256, dtype=dtype), normal(g, Tk, 576, dtype=dtype)
+    for x, n in ((q, cu_q[-1]), (up, cu_k[-1]), (kr, cu_k[-1])):
+        x[n:] = math.nan
+    return dict(q=q, up=up, kr=kr[:, 512:], lens=lens, host_q=cu_q, host_k=cu_k,
+                cu_q=torch.tensor(cu_q, dtype=torch.int32, device="cuda"),
+                cu_k=torch.tensor(cu_k, dtype=torch.int32, device="cuda"))
+
+
+def prefill_run(M, c, causal=True, **kw):
+    return M.mla_prefill(c["q"], c["up"][..., :128], c["kr"], c["up"][..., 128:], c["cu_q"], c["cu_k"], SCALE,
+                         causal=causal, **kw)
+
+
+def prefill_check(c, out, lse, causal=True, what="", only=None, heads=None):
+    H = c["q"].shape[1]
+    for b in (range(len(c["lens"])) if only is None else only):
+        n, m = c["lens"][b]
+        if n == 0:
+            continue
+        q0, k0 = c["host_q"][b], c["host_k"][b]
+        sees = (m - n + 1 + torch.arange(n, device="cuda")).clamp(0, m) if causal else torch.full((n,), m, device="cuda")
+        for h in (range(H) if heads is None else heads):
+            k = torch.cat([c["up"][k0:k0 + m, h, :128], c["kr"][k0:k0 + m]], 1).double()
+            v = c["up"][k0:k0 + m, h, 128:].double()
+            ref = R.attend(c["q"][q0:q0 + n, h].double(), k, v, SCALE, sees)
+            R.check(out[q0:q0 + n, h], lse[q0:q0 + n, h], ref[0], ref[1], ref[2], ref[3], c["q"].dtype, m,
+                    f"{what} sequence {b} ({n} of {m}) head {h}")
+
+
+@pytest.mark.parametrize("lens,H,dtype", [
+    ([(1, 1)], 1, BF16), ([(19, 19)], 2, BF16), ([(128, 128)], 1, FP16), ([(129, 129)], 1, BF16),
+    ([(256, 256)], 2, BF16), ([(257, 257)], 1, BF16), ([(1, 300)], 3, FP16), ([(130, 517)], 2, BF16),
+    ([(64, 64), (0, 0), (1, 1), (200, 333), (0, 40), (300, 300)], 3, BF16), ([(5, 0), (7, 3), (300, 129)], 2, BF16),
+    ([(1000, 1000)], 5, FP16), ([(300, 2000), (77, 1024), (513, 513)], 2, BF16),
+    ([(1 + 3 * i, 1 + 5 * i) for i in range(70)], 1, BF16)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_matches_reference(M, lens, H, dtype, causal):
+    c = prefill_case(lens, H, dtype, seed=len(lens) + H)
+    out = torch.full((c["q"].shape[0], H, 128), 7.0, dtype=dtype, device="cuda")
+    lse = torch.full((c["q"].shape[0], H), 7.0, device="cuda")
+    prefill_run(M, c, causal, out=out, lse=lse)
+    M.sync_status()
+    prefill_check(c, out, lse, causal)
+    assert bool((out[c["host_q"][-1]:] == 7.0).all()) and bool((lse[c["host_q"][-1]:] == 7.0).all())
+
+
+def test_prefill_long_and_repeatable(M):
+    c = prefill_case([(5000, 5000)], 4, BF16, seed=21)
+    out, lse = prefill_run(M, c)
+    again = prefill_run(M, c)
+    M.sync_status()
+    prefill_check(c, out, lse, heads=[0, 3])
+    n = c["host_q"][-1]
+    assert torch.equal(out[:n], again[0][:n]) and torch.equal(lse[:n], again[1][:n])
+
+
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_prefill_scores_that_grow(M, order):
+    n = 700
+    c = prefill_case([(n, n)], 2, BF16, seed=22)
+    ramp = torch.linspace(0.0, 20.0, n, device="cuda")
+    if order == "falling":
+        ramp = ramp.flip(0)
+    c["up"][:n, :, :128] = (ramp[:, None, None] / 4 + 0.1 * c["up"][:n, :, :128].float()).to(BF16)
+    c["q"][:n] = (c["q"][:n].float() * 0.2 + 1.0).to(BF16)
+    out, lse = prefill_run(M, c)
+    M.sync_status()
+    prefill_check(c, out, lse, what=order)
+
+
+def test_prefill_random_shapes(M):
+    rng = random.Random(4)
+    for i in range(16):
+        B, H, top = rng.choice([1, 2, 5, 33]), rng.choice([1, 3, 8]), rng.choice([2, 130, 700])
+        lens = [(rng.randint(0, top), rng.randint(0, top)) for _ in range(B)]
+        causal = rng.random() < 0.7
+        c = prefill_case(lens, H, rng.choice([BF16, FP16]), seed=50 + i)
+        out, lse = prefill_run(M, c, causal)
+        M.sync_status()
+        prefill_check(c, out, lse, causal, what=f"draw {i}", heads=[0, H - 1])
+
+
+def test_prefill_non_finite_stays_in_its_sequence_and_row(M):
+    c = prefill_case([(100, 100), (150, 150)], 2, BF16, seed=23)
+    clean, clean_lse = prefill_run(M, c)
+    c["up"][:100] = math.nan                               # all of sequence 0's keys and values
+    c["q"][100 + 7, 1, 3] = math.nan                       # one query of sequence 1
+    out, lse = prefill_run(M, c)
+    M.sync_status()
+    assert bool(out[:100].isnan().all()) and bool(out[107, 1].isnan().all()) and bool(lse[107, 1].isnan())
+    out[107, 1], lse[107, 1] = clean[107, 1], clean_lse[107, 1]
+    assert torch.equal(out[100:250], clean[100:250]) and torch.equal(lse[100:250], clean_lse[100:250])
+
+
+def test_prefill_bad_offsets_are_clamped_and_reported(M):
+    c = prefill_case([(100, 100), (60, 60)], 2, BF16, seed=24, pad=0)
+    want, want_lse = prefill_run(M, c)
+    M.sync_status()
+    for name, i, value in (("cu_q", 2, 1000), ("cu_k", 2, 1 << 30), ("cu_q", 0, -5), ("cu_k", 0, -1)):
+        bad = dict(c)
+        bad[name] = c[name].clone()
+        bad[name][i] = value
+        out, lse = prefill_run(M, bad)
+        with pytest.raises(M.Nvfp4MoeError) as e:
+            M.sync_status()
+        assert e.value.status == 7
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)       # clamping restores these offsets
+    bad = dict(c)
+    bad["cu_q"] = torch.tensor([100, 0, 160], dtype=torch.int32, device="cuda")   # descending: an empty sequence
+    prefill_run(M, bad)
+    with pytest.raises(M.Nvfp4MoeError):
+        M.sync_status()
+    M.sync_status()
+
+
+def test_prefill_graph_replays_on_new_offsets(M):
+    c = prefill_case([(150, 150), (300, 400)], 2, BF16, seed=25)
+    out, lse = prefill_run(M, c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        prefill_run(M, c, out=out, lse=lse)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            prefill_run(M, c, out=out, lse=lse)
+    torch.cuda.current_stream().wait_stream(side)
+    c["lens"], c["host_q"], c["host_k"] = [(430, 430), (20, 120)], [0, 430, 450], [0, 430, 550]
+    c["cu_q"].copy_(torch.tensor(c["host_q"], dtype=torch.int32))
+    c["cu_k"].copy_(torch.tensor(c["host_k"], dtype=torch.int32))
+    graph.replay()
+    M.sync_status()
+    prefill_check(c, out, lse, what="replay")
+
+
+def test_prefill_without_tokens_or_sequences(M):
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    e = torch.empty(0, 2, 192, dtype=BF16, device="cuda")
+    out, lse = M.mla_prefill(e, e[..., :128], torch.empty(0, 64, dtype=BF16, device="cuda"), e[..., :128], z, z, SCALE)
+    assert out.shape == (0, 2, 128) and lse.shape == (0, 2)
+    q = torch.ones(3, 2, 192, dtype=BF16, device="cuda")                   # queries, but no keys at all
+    cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    out, lse = M.mla_prefill(q, e[..., :128], torch.empty(0, 64, dtype=BF16, device="cuda"), e[..., :128], cu,
+                             torch.zeros(2, dtype=torch.int32, device="cuda"), SCALE)
+    M.sync_status()
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())

@@ -89,6 +89,24 @@ def test_decode_refusals(M, change, code):
     assert status(M._lib.mla_decode, DECODE, **change) == code
 
 
+PREFILL = dict(q=D, q_tok=384, q_head=192, kn=D, kn_tok=512, kn_head=256, kr=D, kr_tok=64, v=D, v_tok=512, v_head=256,
+               cu_q=D, cu_k=D, B=2, Tq=100, Tk=100, H=2, scale=0.1, causal=1, dtype=0, out=D, lse=D, stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(B=-1), 1), (dict(Tq=-1), 1), (dict(Tk=-1), 1), (dict(H=-2), 1), (dict(Tq=1 << 30, H=2), 2),
+    (dict(Tk=1 << 30, H=2), 2), (dict(B=1 << 30, H=2), 2), (dict(dtype=2), 1), (dict(causal=2), 1), (dict(scale=0.0), 1),
+    (dict(scale=float("nan")), 1), (dict(q=None), 1), (dict(kn=None), 1), (dict(kr=None), 1), (dict(v=None), 1),
+    (dict(cu_q=None), 1), (dict(cu_k=None), 1), (dict(out=None), 1), (dict(lse=None), 1), (dict(q_tok=0), 1),
+    (dict(q_head=196), 1), (dict(kn_tok=-8), 1), (dict(kn_head=4), 1), (dict(kr_tok=0), 1), (dict(v_tok=1 << 38), 1),
+    (dict(v_head=1), 1), (dict(q=P(4104)), 1), (dict(kn=P(4104)), 1), (dict(kr=P(4104)), 1), (dict(v=P(4104)), 1),
+    (dict(out=P(4104)), 1), (dict(lse=P(4098)), 1), (dict(cu_q=P(4098)), 1), (dict(B=0, q=None), 0),
+    (dict(Tq=0, out=None), 0), (dict(H=0, lse=None), 0)])
+def test_prefill_refusals(M, change, code):
+    _no_device()
+    assert status(M._lib.mla_prefill, PREFILL, **change) == code
+
+
 def test_python_checks_come_before_the_call(M):
     """Types and shapes are refused with the argument's name, and CPU tensors are not taken."""
     bf, f32, i32, i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64

@@ -31,52 +31,67 @@ for _name, (_res, _args) in _SIGS.items():
     _fn.restype = _res
     _fn.argtypes = _args
 _lib = _b._lib
+_DECODE_WORKSPACE = int(_lib.mla_decode_workspace_size())
 
 
-def _typed(t, dtype, shape, name):
-    """Checks everything but the layout; a None in `shape` is any size."""
-    if t.dtype != dtype:
+# The checks below run on every call of a decode step, whose kernels take
+# microseconds: they read each property once and build no message before it is
+# needed.
+def _typed(t, dtype, shape, name, device):
+    """Checks everything but the layout; returns the data pointer."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('*' if s is None else s for s in shape)}")
-    return t
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{device}")
+    return t.data_ptr()
 
 
-def _dense(t, dtype, shape, name):
-    _typed(t, dtype, shape, name)
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _dense(t, dtype, shape, name, device):
+    p = _typed(t, dtype, shape, name, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    return p
 
 
-def _strided(t, dtype, shape, name):
-    """A view whose innermost dimension is contiguous and whose rows start on 16-byte boundaries."""
-    _typed(t, dtype, shape, name)
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.numel() and (t.stride(-1) != 1 or t.data_ptr() % 16 or
-                      any(s % 8 for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1)):
-        raise ValueError(f"{name}: strides {t.stride()} (innermost 1, others multiples of 8, 16-byte aligned)")
-    return t
+def _strided(t, dtype, shape, name, device):
+    """A view whose innermost dimension is contiguous and whose rows start on
+    16-byte boundaries.  Returns the pointer and the other dimensions' strides,
+    which say nothing (a dense tensor's are given) where a dimension has one
+    entry."""
+    p = _typed(t, dtype, shape, name, device)
+    stride = t.stride()
+    if len(shape) == 2:
+        steps = (stride[0] if shape[0] > 1 else shape[1],)
+        bad = steps[0] % 8
+    else:
+        steps = (stride[0] if shape[0] > 1 else shape[1] * shape[2] or 8, stride[1] if shape[1] > 1 else shape[2])
+        bad = steps[0] % 8 or steps[1] % 8
+    if bad or p % 16 or stride[-1] != 1 and t.numel():
+        raise ValueError(f"{name}: strides {stride}, address {p:#x} (innermost 1, others multiples of 8, 16-byte aligned)")
+    return (p, *steps)
 
 
-def _step(t, dim):
-    """Stride of a dimension; 0 where it has one entry, whose stride says nothing."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
-
-
-def _one_device(**tensors):
-    devices = {t.device for t in tensors.values() if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(str(d) for d in devices)}")
-
-
-def _dtype(t, name):
+def _first(t, name, dims):
+    """The first tensor of a call sets its dtype and device: (dtype, its code, device index)."""
     if t.dtype not in DTYPE:
         raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
-    return DTYPE[t.dtype]
+    if t.dim() != dims:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {dims}")
+    return t.dtype, DTYPE[t.dtype], t.get_device()
+
+
+def _on_cuda(device, name):
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _stream(device):
+    """The device's current stream; calls are made with that device current."""
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def rope_table(max_positions, base=10000.0, device="cuda"):
@@ -97,40 +112,37 @@ def mla_append(latent, k_rope, positions, slots, rope_table, cache, norm_weight=
     takes a copy of the rows (what the expanded form projects).  q_out [T, H,
     64] may be a slice of the queries' buffer or q_rope itself; it is made when
     q_rope comes without it.  Returns q_out (None without queries)."""
-    dt = _dtype(latent, "latent")
-    T, t = latent.shape[0], latent.dtype
-    _strided(latent, t, (None, LATENT), "latent")
-    _strided(k_rope, t, (T, ROPE), "k_rope")
-    _dense(positions, torch.int32, (T,), "positions")
-    _dense(slots, torch.int64, (T,), "slots")
-    _dense(rope_table, torch.float32, (None, ROPE), "rope_table")
-    _dense(cache, t, (None, None, ROW), "cache")
-    if norm_weight is not None:
-        _dense(norm_weight, t, (LATENT,), "norm_weight")
-    if rows_out is not None:
-        _dense(rows_out, t, (T, ROW), "rows_out")
-    H = 0
+    t, code, dev = _first(latent, "latent", 2)
+    T = latent.shape[0]
+    latent_at = _strided(latent, t, (T, LATENT), "latent", dev)
+    _on_cuda(dev, "latent")
+    rope_at = _strided(k_rope, t, (T, ROPE), "k_rope", dev)
+    if cache.dim() != 3 or rope_table.dim() != 2 or (q_rope is not None and q_rope.dim() != 3):
+        raise ValueError("cache and q_rope have three dimensions, rope_table has two")
+    pages, page = cache.shape[0], cache.shape[1]
+    cache_at = _dense(cache, t, (pages, page, ROW), "cache", dev)
+    span = rope_table.shape[0]
+    q_at, q_out_at, H = (None, 0, 0), (None, 0, 0), 0
     if q_rope is not None:
         H = q_rope.shape[1]
-        _strided(q_rope, t, (T, None, ROPE), "q_rope")
         if q_out is None:
             q_out = torch.empty((T, H, ROPE), dtype=t, device=latent.device)
-        _strided(q_out, t, (T, H, ROPE), "q_out")
+        if H:
+            q_at = _strided(q_rope, t, (T, H, ROPE), "q_rope", dev)
+            q_out_at = _strided(q_out, t, (T, H, ROPE), "q_out", dev)
     elif q_out is not None:
         raise ValueError("q_out without q_rope")
-    _one_device(latent=latent, k_rope=k_rope, positions=positions, slots=slots, rope_table=rope_table, cache=cache,
-                norm_weight=norm_weight, rows_out=rows_out, q_rope=q_rope, q_out=q_out)
-    q = (_b._ptr(q_rope), _step(q_rope, 0), _step(q_rope, 1), H, _b._ptr(q_out), _step(q_out, 0), _step(q_out, 1)) \
-        if H else (None, 0, 0, 0, None, 0, 0)
-    _b._check(_lib.mla_append(_b._ptr(latent), _step(latent, 0), _b._ptr(k_rope), _step(k_rope, 0),
-                              _b._ptr(norm_weight), float(eps), _b._ptr(positions), _b._ptr(slots), T,
-                              _b._ptr(rope_table), rope_table.shape[0], int(bool(interleaved)), dt, _b._ptr(cache),
-                              cache.shape[0] * cache.shape[1], _b._ptr(rows_out), *q, _b._stream()), "mla_append")
+    _b._check(_lib.mla_append(
+        *latent_at, *rope_at, None if norm_weight is None else _dense(norm_weight, t, (LATENT,), "norm_weight", dev),
+        eps, _dense(positions, torch.int32, (T,), "positions", dev), _dense(slots, torch.int64, (T,), "slots", dev), T,
+        _dense(rope_table, torch.float32, (span, ROPE), "rope_table", dev), span, 1 if interleaved else 0, code,
+        cache_at, pages * page, None if rows_out is None else _dense(rows_out, t, (T, ROW), "rows_out", dev),
+        *q_at, H, *q_out_at, _stream(dev)), "mla_append")
     return q_out
 
 
 def mla_decode_workspace_size():
-    return int(_lib.mla_decode_workspace_size())
+    return _DECODE_WORKSPACE
 
 
 def mla_decode(q, cache, block_tables, seq_lens, scale, out=None, lse=None, workspace=None):
@@ -139,34 +151,31 @@ def mla_decode(q, cache, block_tables, seq_lens, scale, out=None, lse=None, work
     q [B, Sq, H, 576], cache [num_pages, page_size, 576], block_tables int32
     [B, max_pages], seq_lens int32 [B] (the new tokens counted).  Returns (out
     [B, Sq, H, 512], lse float32 [B, Sq, H])."""
-    dt = _dtype(q, "q")
-    t = q.dtype
-    _dense(q, t, (None, None, None, ROW), "q")
+    t, code, dev = _first(q, "q", 4)
     B, Sq, H, _ = q.shape
-    _dense(cache, t, (None, None, ROW), "cache")
-    _typed(block_tables, torch.int32, (B, None), "block_tables")
-    if not block_tables.is_cuda or (block_tables.numel() and block_tables.stride(1) != 1):
-        raise ValueError("block_tables must be a CUDA tensor with contiguous rows")
-    _dense(seq_lens, torch.int32, (B,), "seq_lens")
-    out = torch.empty((B, Sq, H, LATENT), dtype=t, device=q.device) if out is None else out
-    lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device) if lse is None else lse
-    _dense(out, t, (B, Sq, H, LATENT), "out")
-    _dense(lse, torch.float32, (B, Sq, H), "lse")
-    if workspace is None:
-        workspace = torch.empty((mla_decode_workspace_size(),), dtype=torch.uint8, device=q.device)
-    _dense(workspace, torch.uint8, (None,), "workspace")
-    _one_device(q=q, cache=cache, block_tables=block_tables, seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
+    q_at = _dense(q, t, (B, Sq, H, ROW), "q", dev)
+    _on_cuda(dev, "q")
+    if cache.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("cache has three dimensions, block_tables two")
+    pages, page = cache.shape[0], cache.shape[1]
     max_pages = block_tables.shape[1]
-    _b._check(_lib.mla_decode(_b._ptr(q), _b._ptr(cache), cache.shape[0], cache.shape[1], _b._ptr(block_tables),
-                              max(max_pages, block_tables.stride(0) if B > 1 else 0), max_pages, _b._ptr(seq_lens), B,
-                              Sq, H, float(scale), dt, _b._ptr(out), _b._ptr(lse), _b._ptr(workspace),
-                              workspace.numel(), _b._stream()), "mla_decode")
+    tables_at = _typed(block_tables, torch.int32, (B, max_pages), "block_tables", dev)
+    step = block_tables.stride()
+    if max_pages > 1 and step[1] != 1:
+        raise ValueError(f"block_tables: strides {step}, rows must be contiguous")
+    if out is None:
+        out = torch.empty((B, Sq, H, LATENT), dtype=t, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty((_DECODE_WORKSPACE,), dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.numel()
+    _b._check(_lib.mla_decode(
+        q_at, _dense(cache, t, (pages, page, ROW), "cache", dev), pages, page, tables_at,
+        step[0] if B > 1 else max_pages, max_pages, _dense(seq_lens, torch.int32, (B,), "seq_lens", dev), B, Sq, H,
+        scale, code, _dense(out, t, (B, Sq, H, LATENT), "out", dev), _dense(lse, torch.float32, (B, Sq, H), "lse", dev),
+        _dense(workspace, torch.uint8, (ws_bytes,), "workspace", dev), ws_bytes, _stream(dev)), "mla_decode")
     return out, lse
-
-
-def _span(t, dim, dense):
-    """Stride of a dimension; `dense` where it has at most one entry, whose stride says nothing."""
-    return t.stride(dim) if t.shape[dim] > 1 else dense
 
 
 def mla_prefill(q, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None):
@@ -175,28 +184,21 @@ def mla_prefill(q, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, 
     q [Tq, H, 192], k_nope [Tk, H, 128], k_rope [Tk, 64] and v [Tk, H, 128] may
     be slices of projections' outputs; cu_q, cu_k int32 [B + 1] are the
     sequences' offsets.  Returns (out [Tq, H, 128], lse float32 [Tq, H])."""
-    dt = _dtype(q, "q")
-    t = q.dtype
-    _strided(q, t, (None, None, NOPE + ROPE), "q")
+    t, code, dev = _first(q, "q", 3)
     Tq, H, _ = q.shape
-    _strided(k_nope, t, (None, H, NOPE), "k_nope")
-    Tk = k_nope.shape[0]
-    _strided(k_rope, t, (Tk, ROPE), "k_rope")
-    _strided(v, t, (Tk, H, VALUE), "v")
-    _dense(cu_q, torch.int32, (None,), "cu_q")
-    B = cu_q.shape[0] - 1
+    q_at = _strided(q, t, (Tq, H, NOPE + ROPE), "q", dev)
+    _on_cuda(dev, "q")
+    Tk, B = k_nope.shape[0], cu_q.numel() - 1
     if B < 0:
-        raise ValueError("cu_q must have an entry more than there are sequences")
-    _dense(cu_k, torch.int32, (B + 1,), "cu_k")
-    out = torch.empty((Tq, H, VALUE), dtype=t, device=q.device) if out is None else out
-    lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device) if lse is None else lse
-    _dense(out, t, (Tq, H, VALUE), "out")
-    _dense(lse, torch.float32, (Tq, H), "lse")
-    _one_device(q=q, k_nope=k_nope, k_rope=k_rope, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+        raise ValueError("cu_q: one entry more than there are sequences")
+    if out is None:
+        out = torch.empty((Tq, H, VALUE), dtype=t, device=q.device)
+    if lse is None:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
     _b._check(_lib.mla_prefill(
-        _b._ptr(q), _span(q, 0, 192 * max(H, 1)), _span(q, 1, 192),
-        _b._ptr(k_nope), _span(k_nope, 0, NOPE * max(H, 1)), _span(k_nope, 1, NOPE),
-        _b._ptr(k_rope), _span(k_rope, 0, ROPE), _b._ptr(v), _span(v, 0, VALUE * max(H, 1)), _span(v, 1, VALUE),
-        _b._ptr(cu_q), _b._ptr(cu_k), B, Tq, Tk, H, float(scale), int(bool(causal)), dt, _b._ptr(out), _b._ptr(lse),
-        _b._stream()), "mla_prefill")
+        *q_at, *_strided(k_nope, t, (Tk, H, NOPE), "k_nope", dev), *_strided(k_rope, t, (Tk, ROPE), "k_rope", dev),
+        *_strided(v, t, (Tk, H, VALUE), "v", dev), _dense(cu_q, torch.int32, (B + 1,), "cu_q", dev),
+        _dense(cu_k, torch.int32, (B + 1,), "cu_k", dev), B, Tq, Tk, H, scale, 1 if causal else 0, code,
+        _dense(out, t, (Tq, H, VALUE), "out", dev), _dense(lse, torch.float32, (Tq, H), "lse", dev), _stream(dev)),
+        "mla_prefill")
     return out, lse

@@ -56,6 +56,22 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// Two float32 values in one instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c) {  // (x, y) = (x, y) * a + b, c
+  asm("{\n\t.reg .b64 v, f, g;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 g, {%3, %4};\n\t"
+      "fma.rn.f32x2 v, v, f, g;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {           // (x, y) += (a, b)
+  asm("{\n\t.reg .b64 v, w;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
 // ---- bounded waits ---------------------------------------------------------------
 // Shared state of one CTA's waits: a wait that exceeds the limit raises the
 // sticky flag and makes every role leave its loop.
@@ -196,6 +212,15 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// 16 consecutive columns of each lane.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void sts32(uint32_t saddr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
 }

@@ -296,24 +296,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(kFull, wait_phase<false>(bar(ctl->s_full[t]), j & 1u, wctl));
       if (!ok) break;
       ptx::tc_fence_after();
-      // The row is read twice, 32 columns at a time: once for its maximum, once
-      // for the weights.  128 live values would spill (168 registers a thread).
-      const int sees = limit - j * kKeys;
-      const bool masked = __any_sync(kFull, sees < kKeys);
-      uint32_t s[2][32];
-      ptx::tmem_ld_32x32b_x32(s_col, s[0]);
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_col + 32 * c, s[c]);
       ptx::tmem_ld_wait();
-      float top = -INFINITY;
+      const int sees = limit - j * kKeys;
+      if (__any_sync(kFull, sees < kKeys)) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c < 3) ptx::tmem_ld_32x32b_x32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
-        if (masked) mask_from(s[c & 1], sees - 32 * c);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[c & 1][k]));
-        if (c < 3) ptx::tmem_ld_wait();
+        for (int c = 0; c < 4; ++c) mask_from(s[c], sees - 32 * c);
       }
-      ptx::tmem_ld_32x32b_x32(s_col, s[0]);
-      const float mn = fmaxf(m, top * p.scale_log2);
+      float top[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {           // four chains of three-way maxima
+        top[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int k = 1; k < 31; k += 2)
+          top[c] = fmaxf(fmaxf(top[c], __uint_as_float(s[c][k])), __uint_as_float(s[c][k + 1]));
+        top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
+      }
+      const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2);
       // The reference maximum moves only when it grew by 2^8 in some row of
       // the warp: until then weights of up to 2^8 are as exact as of up to 1.
       if (__any_sync(kFull, j == 0 || mn - m > kGrow)) {
@@ -325,36 +326,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            ptx::tmem_ld_32x32b_x32(o_col + 32 * c, o);
+          for (int c = 0; c < kValueDim; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_col + c, o);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-            ptx::tmem_st_32x32b_x32(o_col + 32 * c, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            ptx::tmem_st_32x32b_x16(o_col + c, o);
           }
         }
       }
       // the weights, rounded to 16 bits for the second product; their sum stays float32
       const float neg = m == -INFINITY ? 0.0f : -m;
-      ptx::tmem_ld_wait();
+      float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {           // weights go over columns that have been read
-        if (c < 3) ptx::tmem_ld_32x32b_x32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
-        if (masked) mask_from(s[c & 1], sees - 32 * c);
+      for (int c = 0; c < 4; ++c) {
         uint32_t w[16];
-        float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-          const float e0 = exp2_approx(fmaf(__uint_as_float(s[c & 1][k]), p.scale_log2, neg));
-          const float e1 = exp2_approx(fmaf(__uint_as_float(s[c & 1][k + 1]), p.scale_log2, neg));
-          sum += e0 + e1;
+          float e0 = __uint_as_float(s[c][k]), e1 = __uint_as_float(s[c][k + 1]);
+          fma2(e0, e1, p.scale_log2, neg, neg);
+          e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+          add2(sum0, sum1, e0, e1);
           w[k / 2] = Elem<T>::pack(e0, e1);
         }
-        l += sum;
-        if (c < 3) ptx::tmem_ld_wait();
         ptx::tmem_st_32x32b_x16(s_col + 16 * c, w);
       }
+      l += sum0 + sum1;
       ptx::tmem_st_wait();
       // Rows of V past the last key belong to another sequence or lie beyond
       // the tensor, and 0 * NaN is NaN: they are zeroed before P V reads them.

@@ -61,7 +61,7 @@ constexpr int kSmem = kVOff + kVTile;
 
 struct Control {
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];  // v: halves of 64 keys
-  uint64_t s_full[2], p_full[2], pv_done[2], drain;                  // per tile of rows
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], drain;       // per tile of rows
   uint32_t tmem, pad;
   WaitCtl wait;
 };
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(ctl->v_full[t]), 1);
       ptx::mbar_init(bar(ctl->v_empty[t]), 1);
       ptx::mbar_init(bar(ctl->s_full[t]), 1);
+      ptx::mbar_init(bar(ctl->p_half[t]), 128);
       ptx::mbar_init(bar(ctl->p_full[t]), 128);
       ptx::mbar_init(bar(ctl->pv_done[t]), 1);
     }
@@ -247,16 +248,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_commit(el, bar(ctl->s_full[t]));
     };
     // V is stored with its values contiguous: 16 keys are 2048 bytes, the second 64 values a chunk further.
+    // The first 64 keys go out as soon as their weights are there.
     auto issue_pv = [&](int t, int j, bool last_user) {
       const uint64_t v = desc_sw128(base + kVOff, kChunk, 1024);
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        mma_f16_ts(el, tmem + 256 + t * kValueDim, tmem + t * kKeys + 8 * s, v + s * (2048 >> 4), idesc_o,
-                   s ? 1u : uint32_t(j > 0));
-        if (s == 3 && last_user) tc_commit(el, bar(ctl->v_empty[0]));
+      for (int h = 0; h < 2; ++h) {
+        if (!wait_warp(bar(ctl->v_full[h]), j & 1u, wctl) ||
+            !wait_warp(bar(h ? ctl->p_full[t] : ctl->p_half[t]), j & 1u, wctl))
+          return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int s = 4 * h; s < 4 * h + 4; ++s)
+          mma_f16_ts(el, tmem + 256 + t * kValueDim, tmem + t * kKeys + 8 * s, v + s * (2048 >> 4), idesc_o,
+                     s ? 1u : uint32_t(j > 0));
+        if (last_user) tc_commit(el, bar(ctl->v_empty[h]));
       }
-      if (last_user) tc_commit(el, bar(ctl->v_empty[1]));
       tc_commit(el, bar(ctl->pv_done[t]));
+      return true;
     };
     bool ok = true;
     for (int j = -1; ok && j < tiles; ++j) {
@@ -264,11 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int t = 0; t < 2 && ok; ++t) {
         if (j >= 0 && j < n[t]) {
-          ok = wait_warp(bar(ctl->v_full[0]), j & 1u, wctl) && wait_warp(bar(ctl->v_full[1]), j & 1u, wctl) &&
-               wait_warp(bar(ctl->p_full[t]), j & 1u, wctl);
+          ok = issue_pv(t, j, t == 1 || j >= n[1]);
           if (!ok) break;
-          ptx::tc_fence_after();
-          issue_pv(t, j, t == 1 || j >= n[1]);
         }
         if (j + 1 < n[t]) {
           if (j < 0) ok = wait_warp(bar(ctl->q_full[t]), 0, wctl);
@@ -336,8 +341,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // Rows of V past the last key belong to another sequence or lie beyond
+      // the tensor, and 0 * NaN is NaN: they are zeroed before P V reads them.
+      const int keys = nk - j * kKeys;
+      if (keys < kKeys) {
+        ok = __all_sync(kFull, wait_phase<false>(bar(ctl->v_full[0]), j & 1u, wctl) &&
+                                   wait_phase<false>(bar(ctl->v_full[1]), j & 1u, wctl));
+        if (!ok) break;
+        for (int k = int(threadIdx.x & 127); k < (kKeys - keys) * 16; k += 128)
+          ptx::sts128(base + kVOff + (k & 1) * kChunk + (keys + (k >> 4)) * 128 + ((k >> 1) & 7) * 16, 0, 0, 0, 0);
+        ptx::fence_proxy_async_smem();
+      }
       // the weights, rounded to 16 bits for the second product; their sum stays float32
-      const float neg = m == -INFINITY ? 0.0f : -m;
+      float neg = m == -INFINITY ? 0.0f : -m;
       float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -351,60 +367,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[k / 2] = Elem<T>::pack(e0, e1);
         }
         ptx::tmem_st_32x32b_x16(s_col + 16 * c, w);
+        if (c & 1) {                          // 64 keys are complete
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(c == 1 ? ctl->p_half[t] : ctl->p_full[t]));
+          asm volatile("" : "+f"(neg)::"memory");  // the other half's weights stay behind the arrival
+        }
       }
       l += sum0 + sum1;
-      ptx::tmem_st_wait();
-      // Rows of V past the last key belong to another sequence or lie beyond
-      // the tensor, and 0 * NaN is NaN: they are zeroed before P V reads them.
-      const int keys = nk - j * kKeys;
-      if (keys < kKeys) {
-        ok = __all_sync(kFull, wait_phase<false>(bar(ctl->v_full[0]), j & 1u, wctl) &&
-                                   wait_phase<false>(bar(ctl->v_full[1]), j & 1u, wctl));
-        if (!ok) break;
-        for (int k = int(threadIdx.x & 127); k < (kKeys - keys) * 16; k += 128)
-          ptx::sts128(base + kVOff + (k & 1) * kChunk + (keys + (k >> 4)) * 128 + ((k >> 1) & 7) * 16, 0, 0, 0, 0);
-        ptx::fence_proxy_async_smem();
-      }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(bar(ctl->p_full[t]));
     }
     if (n[t] && ok) ok = __all_sync(kFull, wait_phase<false>(bar(ctl->pv_done[t]), (n[t] - 1) & 1u, wctl));
     ptx::tc_fence_after();
-    // Output through the tile's Q rows, which nothing reads any more: each
-    // warp turns its own 32 rows around, so that a row's 256 bytes leave in
-    // two consecutive halves of a warp's stores.
     if (ok) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const uint32_t rows = base + kQOff + t * kQTile + 32 * quarter * 256;
-      if (n[t]) {
+      uint8_t* out = p.out + 2 * (((int64_t(at_q) + index) * p.H + head) * kValueDim);
+      // a row that saw no key gets zeros, also where masked values were not finite
+      const bool zero = __any_sync(kFull, l == 0.0f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
+      for (int c = 0; c < 4; ++c) {           // a row's 256 bytes, 16 at a time
+        uint32_t o[32];
+        if (n[t]) {
           ptx::tmem_ld_32x32b_x32(o_col + 32 * c, o);
           ptx::tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {       // 16-byte pieces, spread over the banks by row
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = Elem<T>::pack(__uint_as_float(o[8 * k + 2 * e]), __uint_as_float(o[8 * k + 2 * e + 1]));
-            ptx::sts128(rows + lane * 256 + (((4 * c + k) ^ (lane & 15)) << 4), w[0], w[1], w[2], w[3]);
-          }
         }
-      } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) ptx::sts128(rows + lane * 256 + k * 16, 0, 0, 0, 0);
-      }
-      __syncwarp();
-      const int64_t first = int64_t(at_q) + q0 + t * kM + 32 * quarter;
-#pragma unroll 4
-      for (int k = 0; k < 16; ++k) {
-        const int row = 2 * k + (lane >> 4), piece = lane & 15;
-        const uint4 w = ptx::lds128(rows + row * 256 + ((piece ^ (row & 15)) << 4));
-        if (q0 + t * kM + 32 * quarter + row < nq)
-          *reinterpret_cast<uint4*>(p.out + 2 * (((first + row) * p.H + head) * kValueDim + 8 * piece)) = w;
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+        if (zero)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (l == 0.0f) o[k] = 0u;
+        if (index < nq) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(out + 64 * c + 2 * k) =
+                make_uint4(Elem<T>::pack(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
+                           Elem<T>::pack(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
+                           Elem<T>::pack(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
+                           Elem<T>::pack(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
+        }
       }
       if (index < nq) p.lse[(int64_t(at_q) + index) * p.H + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }

@@ -72,6 +72,23 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {    
       : "f"(a), "f"(b));
 }
 
+// Arrival on a barrier of any CTA of the cluster that releases this thread's
+// shared-memory writes to it, and the matching wait.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ uint32_t mbar_test_acquire_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
 // ---- bounded waits ---------------------------------------------------------------
 // Shared state of one CTA's waits: a wait that exceeds the limit raises the
 // sticky flag and makes every role leave its loop.
@@ -81,13 +98,18 @@ struct WaitCtl {
   unsigned* flags;
 };
 
-// SPIN polls without suspending the thread (the producer and the MMA issuer).
-template <bool SPIN>
+// SPIN polls without suspending the thread (the producer and the MMA
+// issuer); CLUSTER also acquires what other CTAs of the cluster released.
+template <bool SPIN, bool CLUSTER = false>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
-  if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+  auto poll = [&] {
+    if constexpr (CLUSTER) return mbar_test_acquire_cluster(bar, parity);
+    else return SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity);
+  };
+  if (poll()) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+    if (poll()) return true;
     if ((i & 255u) == 0u) {
       if (ctl->abort) return false;
       if (ptx::globaltimer_ns() - t0 > uint64_t(ctl->limit_us) * 1000u) {
@@ -103,9 +125,10 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 __device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, ptx::mbar_test_wait(bar, parity) != 0);
 }
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
-  if (test_warp(bar, parity)) return true;
-  return __all_sync(0xFFFFFFFFu, wait_phase<true>(bar, parity, ctl));
+  if (!CLUSTER && test_warp(bar, parity)) return true;
+  return __all_sync(0xFFFFFFFFu, wait_phase<true, CLUSTER>(bar, parity, ctl));
 }
 
 // Wait for a CTA's own copies or MMAs before it leaves, also after an abort.
@@ -161,6 +184,52 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d_tmem, ui
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
+// The same on a CTA pair, issued by the even CTA: M rows, half of them in
+// each CTA's shared memory at one offset; N rows of B likewise.  With M = 128
+// a CTA's tensor memory holds its 64 rows in lanes 0-63 for the first half of
+// the columns and in lanes 64-127 for the second.
+__device__ __forceinline__ void mma_f16_pair(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+// Arrive on the mbarrier at offset `bar` in both CTAs of the pair.
+__device__ __forceinline__ void tc_commit_pair(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"((unsigned short)3), "r"(elected)
+      : "memory");
+}
+// Pair form of the load: the data lands in this CTA, the completion counts
+// on `bar`, a cluster address.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t elected, uint32_t dst, const void* tmap, uint32_t bar,
+                                                 int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t elected, uint32_t dst, const void* tmap, uint32_t bar, int32_t c0,
+                                            int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(elected)
+      : "memory");
+}
+
 // Arrive on `bar` once every MMA issued so far by the elected lane has completed.
 __device__ __forceinline__ void tc_commit(uint32_t elected, uint32_t bar) {
   asm volatile(
@@ -212,6 +281,13 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// The same for 16 columns (r[4i ..] columns 8i ..).
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+}
 // 16 consecutive columns of each lane.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(

@@ -27,13 +27,15 @@
 // Warp roles: warps 0-3 softmax and epilogue, warp 4 TMA producer, warp 5
 // tensor-memory owner and MMA issuer.  Every wait is bounded.
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 #include "../../include/nvfp4mla.h"
 #include "internal.h"
 #include "launch.cuh"
-#include "mla_common.cuh"
+#include "mla_decode.cuh"
+#include "mla_decode_pair.cuh"
 #include "sm103_ptx.cuh"
 
 namespace nvfp4moe {
@@ -41,14 +43,8 @@ namespace {
 
 using namespace mla;
 
-__device__ unsigned g_decode_flags = 0;
-
-constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kRows = 64;                     // rows of a block
-constexpr int kKeys = 64;                     // keys of a tile
 constexpr int kChunk = 64 * 128;              // 64 rows x 64 values, 128-byte rows
 constexpr int kTile = 9 * kChunk;
-constexpr int kGroup = 8 * 2 * kRow;          // 8 keys: nine atoms of 8 rows x 128 bytes
 constexpr int kPieces = 4;                    // of a tile: 16 keys each, freed one by one
 constexpr int kStages = 2;
 constexpr int kProducer = 8, kIssuer = 12;    // first producer warp, MMA warp
@@ -56,7 +52,6 @@ constexpr int kThreads = 416;
 constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;               // S buffers after the 4 x 64 columns of O^T
-constexpr float kGrow = 8.0f;                 // rescale O only when a maximum grew by 2^8
 
 // Shared memory after the 1024-byte control block.
 constexpr int kCtrl = 1024;
@@ -75,120 +70,6 @@ struct Control {
 };
 static_assert(sizeof(Control) <= kCtrl, "control block");
 static_assert(kSmem <= 232448, "shared memory");
-
-// What a CTA's range begins with, for the kernel that joins partial results.
-struct Head {
-  int32_t start, tiles, share;                // the item's place in the tile list, its tiles; tiles of a range
-  int32_t b, block;
-};
-
-struct DecodeParams {
-  const uint8_t* cache;
-  const int32_t* tables;
-  int64_t table_stride;
-  const int32_t* lens;
-  int B, Sq, H, rows, blocks;                 // rows = Sq * H of a sequence, in `blocks` row blocks
-  int num_pages, page, log_page, max_pages;
-  float scale_log2, scale;
-  uint8_t* out;                               // [B, rows, 512]
-  float* lse;                                 // [B, rows]
-  int min_share;
-  Head* heads;                                // [grid]
-  float* part_o;                              // [grid][2][64][512]
-  float* part_lse;                            // [grid][2][64], log2 domain
-  uint32_t wait_us;
-};
-
-__device__ __forceinline__ int seq_len(const DecodeParams& p, int b) {
-  const int n = __ldg(p.lens + b);
-  return n < 0 ? 0 : int(min(int64_t(n), int64_t(p.max_pages) * p.page));
-}
-// Tiles of an item; an empty sequence has one, whose keys are all masked.
-__device__ __forceinline__ int item_tiles(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
-
-// Walks the tiles [pos, end) of the flattened (sequence, row block, tile) list.
-struct Cursor {
-  int pos, end;                               // in the tile list
-  int tile, tiles, first;                     // within the item; where this CTA entered it
-  int b, block, len;
-
-  // Executed by a whole warp: the CTA's range and its first item.  Returns the share.
-  __device__ __forceinline__ int init(const DecodeParams& p) {
-    const int lane = threadIdx.x & 31;
-    int total = 0, n = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-      total += b0 + lane < p.B ? item_tiles(n) : 0;
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-    total *= p.blocks;
-    const int share = max(int((unsigned(total) + gridDim.x - 1) / gridDim.x), p.min_share);
-    const int64_t from = int64_t(share) * blockIdx.x;
-    pos = int(min(from, int64_t(total)));
-    end = int(min(from + share, int64_t(total)));
-    if (pos >= end) return share;
-    int before = 0;                           // tiles of the sequences before b0
-    for (int b0 = 0;; b0 += 32) {
-      if (p.B > 32) n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-      const int mine = b0 + lane < p.B ? item_tiles(n) * p.blocks : 0;
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(kFull, upto, d);
-        if (lane >= d) upto += v;
-      }
-      const unsigned hit = __ballot_sync(kFull, before + upto > pos);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        b = b0 + src;
-        len = __shfl_sync(kFull, n, src);
-        const int in = pos - before - __shfl_sync(kFull, upto - mine, src);
-        tiles = item_tiles(len);
-        block = in / tiles;
-        tile = first = in - block * tiles;
-        return share;
-      }
-      before += __shfl_sync(kFull, upto, 31);
-    }
-  }
-  __device__ __forceinline__ bool valid() const { return pos < end; }
-  __device__ __forceinline__ bool is_first() const { return tile == first; }
-  __device__ __forceinline__ bool is_last() const { return tile + 1 == tiles || pos + 1 == end; }
-  __device__ __forceinline__ void next(const DecodeParams& p) {
-    ++pos;
-    if (++tile == tiles) {
-      tile = first = 0;
-      if (++block == p.blocks) {
-        block = 0;
-        if (++b < p.B) {
-          len = seq_len(p, b);
-          tiles = item_tiles(len);
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ int keys() const { return min(kKeys, len - tile * kKeys); }  // <= 0: none
-  __device__ __forceinline__ int rows(const DecodeParams& p) const { return min(kRows, p.rows - block * kRows); }
-};
-
-__device__ __forceinline__ void prefetch_l2(uint32_t elected, const void* at, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q cp.async.bulk.prefetch.L2.global [%0], %1;\n\t}" ::"l"(at),
-      "r"(bytes), "r"(elected)
-      : "memory");
-}
-
-// 16-bit rows [rows, 576] in boxes of `box_rows` rows x `chunks` chunks of 64
-// values, which land chunk by chunk, each as box_rows x 128 bytes.
-template <typename T>
-bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows, int chunks) {
-  const int64_t dims[3] = {64, rows, kRow / 64}, strides[2] = {2 * kRow, 128};
-  const int box[3] = {64, box_rows, chunks};
-  return encode_map(m, Elem<T>::kMap, 3, base, dims, strides, box);
-}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -235,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::grid_dep_launch();
 
   Cursor cur;
-  const int share = cur.init(p);
+  const int share = cur.init(p, blockIdx.x, gridDim.x);
 
   if (warp >= kProducer && warp < kProducer + kPieces) {
     // ---- producers: one warp for each piece of 16 keys, so that a tile's
@@ -593,10 +474,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
   if (first == last) return;                  // whole: written by its CTA (also an item that begins at the border)
   const int pieces = last - first + 1;
   const int row = blockIdx.y * kJoinRows + warp / kShare;
-  const bool live = row < min(kRows, p.rows - block * kRows);
+  const bool live = row < min(p.ctas * kRows, p.rows - block * p.ctas * kRows);
   // piece 0 is the last segment of range `first` unless the range begins with it
   const int lead = start != first * share ? 1 : 0;
-  auto piece_row = [&](int i) { return int64_t(2 * (first + i) + (i == 0 ? lead : 0)) * kRows + row; };
+  auto piece_row = [&](int i) {
+    return int64_t(2 * ((first + i) * p.ctas + row / kRows) + (i == 0 ? lead : 0)) * kRows + row % kRows;
+  };
   constexpr int kPer = (kMlaDecodeMaxGrid + 31) / 32;
   float w[kPer];                              // the weights of pieces lane, lane + 32, ...
   float top = -INFINITY, sum = 0.0f;
@@ -644,7 +527,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
       }
   }
   if (!live) return;
-  const int64_t at = int64_t(b) * p.rows + block * kRows + row;
+  const int64_t at = int64_t(b) * p.rows + block * p.ctas * kRows + row;
   if (lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -657,15 +540,32 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Tiles a CTA takes at least: below this, splitting a sequence costs more in partial results than it gains.
 constexpr int kMinShare = 4;
 
-// Most tiles the call can have, and the grid that covers them.
-int64_t most_tiles(const MlaDecodeArgs& a) {
+// Most tiles the call can have.
+int64_t most_tiles(const MlaDecodeArgs& a, int ctas) {
   const int64_t longest = std::max<int64_t>(1, ceil_div(int64_t(a.max_pages) * a.page, kKeys));
-  return int64_t(a.B) * ceil_div(int64_t(a.Sq) * a.H, kRows) * longest;
+  return int64_t(a.B) * ceil_div(int64_t(a.Sq) * a.H, kRows * ctas) * longest;
+}
+
+// CTA pairs that can be resident at once, per device, looked up once.
+template <typename K>
+int max_pairs(K kernel) {
+  static std::atomic<int> cached[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if ((n = cached[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pair::kSmem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(pair::kThreads);
+  cfg.dynamicSmemBytes = pair::kSmem;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  cached[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 template <typename T>
 int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
-  if (most_tiles(a) >= (int64_t(1) << 31)) {
+  if (most_tiles(a, 1) >= (int64_t(1) << 31)) {
     set_error_detail("B = %d, Sq * H = %d and max_pages * page_size = %lld keys exceed 2^31 tiles of 64 rows x 64 keys",
                      a.B, a.Sq * a.H, (long long)a.max_pages * a.page);
     return NVFP4MOE_ERR_UNSUPPORTED;
@@ -677,14 +577,29 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
     set_error_detail("cuTensorMapEncodeTiled failed or is unavailable");
     return NVFP4MOE_ERR_CUDA;
   }
-  const int grid = int(std::min<int64_t>(std::min(num_sms, kMlaDecodeMaxGrid), ceil_div(most_tiles(a), kMinShare)));
+  // A pair of CTAs shares each tile between 128 rows, in the time that one CTA
+  // needs for 64: from 65 rows on it halves the passes over the cache (128
+  // sequences x 128 heads: PAIRMEAS).  With at most 64 rows half of its rows would be
+  // padding, for no gain (32 x 64 heads: PAIRMEAS2).
+  const bool pair = rows > kRows;
+  const int ctas = pair ? 2 : 1;
+  int most_ranges = std::min(num_sms, kMlaDecodeMaxGrid);
+  if (pair) {
+    most_ranges = std::min(max_pairs(decode_pair_kernel<T>), most_ranges / 2);
+    if (most_ranges < 1) {
+      set_error_detail("no CTA pair of the absorbed attention fits on this device");
+      return NVFP4MOE_ERR_SMEM;
+    }
+  }
+  const int ranges = int(std::min<int64_t>(most_ranges, ceil_div(most_tiles(a, ctas), kMinShare)));
   DecodeParams p;
   p.tables = a.tables;
   p.table_stride = a.table_stride;
   p.lens = a.lens;
   p.B = a.B, p.Sq = a.Sq, p.H = a.H;
   p.rows = rows;
-  p.blocks = int(ceil_div(rows, kRows));
+  p.ctas = ctas;
+  p.blocks = int(ceil_div(rows, kRows * ctas));
   p.cache = static_cast<const uint8_t*>(a.cache);
   p.num_pages = a.num_pages;
   p.page = a.page;
@@ -702,16 +617,31 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   p.part_o = p.part_lse + int64_t(kMlaDecodeMaxGrid) * 2 * kRows;
   p.wait_us = wait_limit_us();
   static_assert(sizeof(Head) * kMlaDecodeMaxGrid <= kMlaDecodeHeadBytes, "workspace header");
-  auto kernel = decode_kernel<T>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (err == cudaSuccess) err = launch_kernel(kernel, dim3(grid), dim3(kThreads), kSmem, st, false, q_map, kv_map, p);
+  cudaError_t err;
+  if (pair) {
+    CUtensorMap v_map;
+    if (!encode_values<T>(&v_map, a.cache, int64_t(a.num_pages) * a.page)) {
+      set_error_detail("cuTensorMapEncodeTiled failed");
+      return NVFP4MOE_ERR_CUDA;
+    }
+    err = cudaFuncSetAttribute(decode_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, pair::kSmem);
+    if (err == cudaSuccess)
+      err = launch_kernel(decode_pair_kernel<T>, dim3(2 * ranges), dim3(pair::kThreads), pair::kSmem, st, false, q_map,
+                          kv_map, v_map, p);
+  } else {
+    err = cudaFuncSetAttribute(decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (err == cudaSuccess)
+      err = launch_kernel(decode_kernel<T>, dim3(ranges), dim3(kThreads), kSmem, st, false, q_map, kv_map, p);
+  }
   const int64_t items = int64_t(a.B) * p.blocks;
-  if (err == cudaSuccess && grid > 1) {
-    const int most = std::min(kRows, rows);
-    if (items * 4 <= grid)
+  if (err == cudaSuccess && ranges > 1) {
+    // Few items of many pieces are joined by item, several warps a row; more
+    // items by the borders that cut them, a warp a row.
+    const int most = std::min(kRows * ctas, rows);
+    if (items * 4 <= ranges)
       err = launch_kernel(join_kernel<T, true>, dim3(int(items), (most + 1) / 2), dim3(kJoinThreads), 0, st, false, p);
     else
-      err = launch_kernel(join_kernel<T, false>, dim3(grid - 1, (most + 7) / 8), dim3(kJoinThreads), 0, st, false, p);
+      err = launch_kernel(join_kernel<T, false>, dim3(ranges - 1, (most + 7) / 8), dim3(kJoinThreads), 0, st, false, p);
   }
   if (err != cudaSuccess) {
     set_error_detail("mla_decode launch: %s", cudaGetErrorString(err));

@@ -1,0 +1,142 @@
+// Shared by the two absorbed-attention kernels (one CTA, CTA pair): the tile
+// list and its ranges, and the workspace that joins their partial results.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "mla_common.cuh"
+
+namespace nvfp4moe {
+namespace {
+
+using namespace mla;
+
+__device__ unsigned g_decode_flags = 0;
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kRows = 64;                     // rows of a CTA
+constexpr int kKeys = 64;                     // keys of a tile
+constexpr int kGroup = 8 * 2 * kRow;          // 8 keys: nine atoms of 8 rows x 128 bytes
+constexpr float kGrow = 8.0f;                 // rescale O only when a maximum grew by 2^8
+
+// What a CTA's range begins with, for the kernel that joins partial results.
+struct Head {
+  int32_t start, tiles, share;                // the item's place in the tile list, its tiles; tiles of a range
+  int32_t b, block;
+};
+
+struct DecodeParams {
+  const uint8_t* cache;
+  const int32_t* tables;
+  int64_t table_stride;
+  const int32_t* lens;
+  int B, Sq, H, rows, blocks;                 // rows = Sq * H of a sequence, in `blocks` row blocks
+  int ctas;                                   // CTAs of a range: one with 64 rows, or a pair with 128
+  int num_pages, page, log_page, max_pages;
+  float scale_log2, scale;
+  uint8_t* out;                               // [B, rows, 512]
+  float* lse;                                 // [B, rows]
+  int min_share;
+  Head* heads;                                // [ranges]
+  float* part_o;                              // [grid][2][64][512]
+  float* part_lse;                            // [grid][2][64], log2 domain
+  uint32_t wait_us;
+};
+
+__device__ __forceinline__ int seq_len(const DecodeParams& p, int b) {
+  const int n = __ldg(p.lens + b);
+  return n < 0 ? 0 : int(min(int64_t(n), int64_t(p.max_pages) * p.page));
+}
+// Tiles of an item; an empty sequence has one, whose keys are all masked.
+__device__ __forceinline__ int item_tiles(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
+
+// Walks the tiles [pos, end) of range `index` of `ranges` of the flattened (sequence, row block, tile) list.
+struct Cursor {
+  int pos, end;                               // in the tile list
+  int tile, tiles, first;                     // within the item; where this CTA entered it
+  int b, block, len;
+
+  // Executed by a whole warp: the range and its first item.  Returns the share.
+  __device__ __forceinline__ int init(const DecodeParams& p, int index, int ranges) {
+    const int lane = threadIdx.x & 31;
+    int total = 0, n = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
+      total += b0 + lane < p.B ? item_tiles(n) : 0;
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+    total *= p.blocks;
+    const int share = max(int((unsigned(total) + ranges - 1) / ranges), p.min_share);
+    const int64_t from = int64_t(share) * index;
+    pos = int(min(from, int64_t(total)));
+    end = int(min(from + share, int64_t(total)));
+    if (pos >= end) return share;
+    int before = 0;                           // tiles of the sequences before b0
+    for (int b0 = 0;; b0 += 32) {
+      if (p.B > 32) n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
+      const int mine = b0 + lane < p.B ? item_tiles(n) * p.blocks : 0;
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(kFull, upto, d);
+        if (lane >= d) upto += v;
+      }
+      const unsigned hit = __ballot_sync(kFull, before + upto > pos);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        b = b0 + src;
+        len = __shfl_sync(kFull, n, src);
+        const int in = pos - before - __shfl_sync(kFull, upto - mine, src);
+        tiles = item_tiles(len);
+        block = in / tiles;
+        tile = first = in - block * tiles;
+        return share;
+      }
+      before += __shfl_sync(kFull, upto, 31);
+    }
+  }
+  __device__ __forceinline__ bool valid() const { return pos < end; }
+  __device__ __forceinline__ bool is_first() const { return tile == first; }
+  __device__ __forceinline__ bool is_last() const { return tile + 1 == tiles || pos + 1 == end; }
+  __device__ __forceinline__ void next(const DecodeParams& p) {
+    ++pos;
+    if (++tile == tiles) {
+      tile = first = 0;
+      if (++block == p.blocks) {
+        block = 0;
+        if (++b < p.B) {
+          len = seq_len(p, b);
+          tiles = item_tiles(len);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ int keys() const { return min(kKeys, len - tile * kKeys); }  // <= 0: none
+  // Rows of the item's 64-row part `part` (0, or 0 and 1 for a pair); <= 0: none.
+  __device__ __forceinline__ int rows(const DecodeParams& p, int part = 0) const {
+    return min(kRows, p.rows - (block * p.ctas + part) * kRows);
+  }
+};
+
+__device__ __forceinline__ void prefetch_l2(uint32_t elected, const void* at, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q cp.async.bulk.prefetch.L2.global [%0], %1;\n\t}" ::"l"(at),
+      "r"(bytes), "r"(elected)
+      : "memory");
+}
+
+// 16-bit rows [rows, 576] in boxes of `box_rows` rows x `chunks` chunks of 64
+// values, which land chunk by chunk, each as box_rows x 128 bytes.
+template <typename T>
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int box_rows, int chunks) {
+  const int64_t dims[3] = {64, rows, kRow / 64}, strides[2] = {2 * kRow, 128};
+  const int box[3] = {64, box_rows, chunks};
+  return encode_map(m, Elem<T>::kMap, 3, base, dims, strides, box);
+}
+
+}  // namespace
+}  // namespace nvfp4moe

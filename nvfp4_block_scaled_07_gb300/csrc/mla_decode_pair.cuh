@@ -1,0 +1,442 @@
+// Absorbed latent attention on CTA pairs: 128 rows (new token x head) share
+// one pass over the keys.
+//
+// The mathematics is that of the one-CTA kernel.  A pair issues cta_group::2
+// MMAs of M = 128 rows, 64 in each CTA, so that O (64 x 512 float32 a CTA)
+// leaves room for S, and each operand byte of the cache is staged by one CTA
+// for both:
+//   S [128 x 64 keys]     = Q x C^T     N = 64: each CTA stages 32 keys x 576
+//   O [128 x 512] += P x C[:, :512]     N = 256, twice: each CTA stages 256 of
+//                                       the values of all 64 keys
+// 36 MMAs of 28 cycles and 8 of 68 a tile, 1560 cycles, against the 1410 in
+// which HBM delivers a pair's tile; one CTA takes 2030 for its 64 rows alone.
+// A CTA's share of a tile is 36 KB for S and 32 KB for P V (its own keys'
+// values twice, so that both CTAs use the same descriptors), two tiles in
+// flight.  S of the next tile is issued before P V of this one and covers the
+// softmax.
+//
+// Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-11
+// TMA producers, warp 12 tensor-memory owner and, in the even CTA, MMA issuer.
+// The even CTA's barriers count both CTAs' copies of whole rows and softmax
+// arrivals; commits arrive in both.  The copies of values count in their own
+// CTA, whose softmax warps wait for them before they arrive: rows past the
+// last key are zeroed after their copy.
+#pragma once
+
+#include "../../include/nvfp4mla.h"
+#include "internal.h"
+#include "mla_decode.cuh"
+
+namespace nvfp4moe {
+namespace {
+
+namespace pair {
+constexpr int kStages = 2;
+constexpr int kPieces = 4;                    // of a tile's values: 16 keys each
+constexpr int kProducer = 8, kIssuer = 12;
+constexpr int kThreads = 416;
+constexpr int kSoftmaxThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 256, kSCols = 32;  // S buffers after the 256 columns of O
+constexpr int kQBytes = 64 * 2 * kRow;
+constexpr int kKBytes = 4 * kGroup;           // 32 keys
+constexpr int kVGroup = 4 * 1024;             // 8 keys: four atoms (two of each half of the values)
+constexpr int kVBytes = 8 * kVGroup;          // 64 keys
+constexpr int kCtrl = 2048;
+constexpr int kQOff = kCtrl;
+constexpr int kKOff = kQOff + kQBytes;
+constexpr int kVOff = kKOff + kStages * kKBytes;
+constexpr int kPOff = kVOff + kStages * kVBytes;
+constexpr int kSmem = kPOff + 64 * 128;
+
+struct Control {
+  // counted in the even CTA only: k_full, q_full, p_full, o_free
+  uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages][kPieces];
+  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_free, drain;
+  uint32_t tmem, pad;
+  WaitCtl wait;
+  float part[4][kRows];                       // per row: maxima, later sums, of the four quarters of a tile's keys
+  float col[kRows];                           // per row: factor of the epilogue
+};
+static_assert(sizeof(Control) <= kCtrl && kSmem <= 232448, "shared memory");
+}  // namespace pair
+
+// The values of the cached rows for P V: boxes of 8 rows x two chunks of 64
+// values x both halves (values 0 .. 255 and 256 .. 511), which land as four
+// atoms of 8 rows x 128 bytes, half by half.
+template <typename T>
+bool encode_values(CUtensorMap* m, const void* base, int64_t rows) {
+  const int64_t dims[4] = {64, rows, 4, 2}, strides[3] = {2 * kRow, 128, 512};
+  const int box[4] = {64, 8, 2, 2};
+  return encode_map(m, Elem<T>::kMap, 4, base, dims, strides, box);
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
+    decode_pair_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
+                       const __grid_constant__ CUtensorMap v_map, const DecodeParams p) {
+  using namespace pair;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Control* ctl = reinterpret_cast<Control*>(smem);
+  volatile WaitCtl* wctl = &ctl->wait;
+  const uint32_t base = ptx::smem_u32(smem);
+  const int warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int range = int(blockIdx.x >> 1), ranges = int(gridDim.x >> 1);
+  auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar(ctl->k_full[s]), kPieces);
+      ptx::mbar_init(bar(ctl->v_full[s]), kPieces);
+      ptx::mbar_init(bar(ctl->k_empty[s]), 1);
+      for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[s][i]), 1);
+    }
+    ptx::mbar_init(bar(ctl->q_full), 1);
+    ptx::mbar_init(bar(ctl->q_empty), 1);
+    ptx::mbar_init(bar(ctl->s_full[0]), 1);
+    ptx::mbar_init(bar(ctl->s_full[1]), 1);
+    ptx::mbar_init(bar(ctl->p_full), 2 * kSoftmaxThreads / 32);
+    ptx::mbar_init(bar(ctl->pv_done), 1);
+    ptx::mbar_init(bar(ctl->o_free), 2 * kSoftmaxThreads / 32);
+    ptx::mbar_init(bar(ctl->drain), 1);
+    ptx::fence_barrier_init();
+    ctl->wait.abort = 0;
+    ctl->wait.limit_us = p.wait_us;
+    ctl->wait.flags = &g_decode_flags;
+  }
+  if (warp == kProducer && lane == 0) {
+    ptx::prefetch_tmap(&q_map);
+    ptx::prefetch_tmap(&kv_map);
+    ptx::prefetch_tmap(&v_map);
+  }
+  if (warp == kIssuer) {
+    ptx::tmem_alloc_pair(base + uint32_t(offsetof(Control, tmem)), kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();                        // both CTAs' barriers exist before either signals one
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(kFull, ctl->tmem, 0);
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+
+  Cursor cur;
+  const int share = cur.init(p, range, ranges);
+
+  if (warp >= kProducer && warp < kProducer + kPieces) {
+    // ---- producers: warp i copies the values of keys 16 i .. 16 i + 15 and,
+    // of its CTA's 32 keys, group i of 8 whole rows ----
+    const int piece = warp - kProducer;
+    if (piece == 0 && blockIdx.x == 0)        // lengths that are not served as they are
+      for (int b = lane; b < p.B; b += 32)
+        if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
+    const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0u;  // the even CTA tells its barriers what to expect
+    const int oob = p.num_pages * p.page;
+    const int kgroup = 4 * int(rank) + piece;  // its group of whole rows, in the tile
+    uint32_t g = 0, seg = 0, gv = 0;          // tiles (K, V) and Q blocks begun
+    const uint32_t kf0 = ptx::mapa(bar(ctl->k_full[0]), 0);
+    const uint32_t qf = ptx::mapa(bar(ctl->q_full), 0);
+    // First cache row of 8 keys of the cursor's tile.
+    auto look_up = [&](const Cursor& c, int group) {
+      const int row = c.tile * kKeys + 8 * group;
+      if (row >= c.len) return oob;
+      const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
+      if (id >= 0 && id < p.num_pages) return id * p.page + (row & (p.page - 1));
+      if (lane == 0) atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
+      return oob;
+    };
+    int k_row = cur.valid() ? look_up(cur, kgroup) : 0, v_row = cur.valid() ? look_up(cur, 2 * piece) : 0;
+    while (cur.valid()) {
+      if (piece == 0 && cur.is_first()) {
+        if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
+        arrive_expect_tx(el0, bar(ctl->q_full), 2 * kQBytes);
+#pragma unroll
+        for (int c = 0; c < 9; c += 3)
+          tma_load_3d_pair(el, base + kQOff + c * 64 * 128, &q_map, qf, 0,
+                           cur.b * p.rows + (2 * cur.block + int(rank)) * kRows, c);
+        ++seg;
+      }
+      const uint32_t s = g & 1u, ph = ((g >> 1) & 1u) ^ 1u;
+      const int groups = (max(cur.keys(), 0) + 7) / 8;  // of 8 keys, in the tile
+      if (!wait_warp(bar(ctl->k_empty[s]), ph, wctl)) break;
+      arrive_expect_tx(el0, bar(ctl->k_full[s]), uint32_t((piece < groups ? kGroup : 0) + (4 + piece < groups ? kGroup : 0)));
+      if (kgroup < groups)
+        tma_load_3d_pair(el, base + kKOff + s * kKBytes + piece * kGroup, &kv_map, kf0 + 8 * s, 0, k_row, 0);
+      ++g;
+      const int vg = min(2, max(0, groups - 2 * piece));
+      if (!wait_warp(bar(ctl->v_empty[s][piece]), ph, wctl)) break;
+      const uint32_t vf = bar(ctl->v_full[s]), dst = base + kVOff + s * kVBytes + 2 * piece * kVGroup;
+      arrive_expect_tx(el, vf, uint32_t(vg * kVGroup));
+      if (vg > 0) tma_load_4d(el, dst, &v_map, vf, 0, v_row, 2 * int(rank), 0);
+      if (vg > 1) tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(v_row, oob - 8) + 8, 2 * int(rank), 0);
+      ++gv;
+      cur.next(p);
+      if (cur.valid()) {
+        k_row = look_up(cur, kgroup);
+        v_row = look_up(cur, 2 * piece);
+        // the next tile's rows are requested into L2 while their buffers are in use
+        const int rows = min(8, cur.len - cur.tile * kKeys - 8 * kgroup);
+        if (rows > 0 && k_row != oob)
+          prefetch_l2(el, p.cache + int64_t(k_row) * (2 * kRow), uint32_t(rows) * (2 * kRow));
+      }
+    }
+    // Every copy has landed before the pair leaves: the even CTA's barriers
+    // count both CTAs' (bounded, since an abort may leave a phase incomplete).
+    if (rank == 0 && seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
+    for (uint32_t s = 0; s < kStages; ++s) {
+      const uint32_t nk = (g + 1 - s) / 2, nv = (gv + 1 - s) / 2;
+      if (rank == 0 && nk) drain_phase(bar(ctl->k_full[s]), (nk - 1) & 1u);
+      if (nv) drain_phase(bar(ctl->v_full[s]), (nv - 1) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == kIssuer) {
+    // ---- MMA issuer, in the even CTA ----
+    if (rank == 0) {
+      const uint32_t el = elect_one();
+      const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 128, kKeys, false, false);
+      const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, 256, false, true);
+      uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
+      Cursor cs = cur;
+      auto issue_s = [&]() {
+        const uint32_t s = gs & 1u;
+        if (cs.is_first() && !wait_warp(bar(ctl->q_full), seg_s++ & 1u, wctl)) return false;
+        if (!wait_warp(bar(ctl->k_full[s]), (gs >> 1) & 1u, wctl)) return false;
+        ptx::tc_fence_after();
+        const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
+        const uint64_t b = desc_sw128(base + kKOff + s * kKBytes, 16, kGroup);
+#pragma unroll
+        for (int c = 0; c < 9; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
+                         idesc_s, c + k > 0);
+        tc_commit_pair(el, bar(ctl->k_empty[s]));
+        tc_commit_pair(el, bar(ctl->s_full[s]));
+        if (cs.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
+        cs.next(p);
+        ++gs;
+        return true;
+      };
+      bool ok = !cur.valid() || issue_s();
+      while (ok && cur.valid()) {
+        if (cs.valid() && !issue_s()) break;
+        const uint32_t s = gp & 1u;
+        if (!wait_warp<true>(bar(ctl->p_full), gp & 1u, wctl)) break;
+        // the previous segment's accumulator has been read
+        if (cur.is_first() && seg_p++ && !wait_warp<true>(bar(ctl->o_free), seg_p & 1u, wctl)) break;
+        ptx::tc_fence_after();
+        const uint32_t more = cur.is_first() ? 0u : 1u;
+        const uint64_t a = desc_sw128(base + kPOff, 16, 1024);
+        const uint64_t b = desc_sw128(base + kVOff + s * kVBytes, 1024, kVGroup);
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
+#pragma unroll
+          for (int h = 0; h < 2; ++h)         // 256 values
+            mma_f16_pair(el, tmem + 128 * h, a + 2 * k, b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc_o,
+                         k ? 1u : more);
+          tc_commit_pair(el, bar(ctl->v_empty[s][k]));
+        }
+        tc_commit_pair(el, bar(ctl->pv_done));
+        cur.next(p);
+        ++gp;
+      }
+      tc_commit_pair(el, bar(ctl->drain));
+    }
+    // Both CTAs stay until the pair's last MMA is done and its commits have
+    // arrived (the odd one waits here from the start).
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar(ctl->drain), 0))
+      if (ptx::globaltimer_ns() - t0 > 30000000000ull) break;
+    __syncwarp();
+  } else if (warp < kProducer) {
+    // ---- softmax and epilogue: this CTA's 64 rows ----
+    if (threadIdx.x == 0 && rank == 0) {
+      Head h;
+      h.share = share;
+      h.start = cur.valid() ? cur.pos - cur.tile : 0;
+      h.tiles = cur.valid() ? cur.tiles : 0;
+      h.b = cur.valid() ? cur.b : 0;
+      h.block = cur.valid() ? cur.block : 0;
+      p.heads[range] = h;
+    }
+    // Lane quarters 0 and 1 hold the rows' first 32 keys, 2 and 3 the others;
+    // two warps share a quarter, each takes 16 of its columns: a thread has one
+    // row and 16 keys, four threads share a row.
+    const int quarter = warp & 3, half = warp >> 2, upper = quarter >> 1;
+    const uint32_t lanes = uint32_t(32 * quarter) << 16;
+    const int r = 32 * (quarter & 1) + lane, key0 = 32 * upper + 16 * half, who = 2 * upper + half;
+    const uint32_t p_full = ptx::mapa(bar(ctl->p_full), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
+    float m = 0.0f, l = 0.0f;                 // running maximum (log2 domain) and this quarter's sum
+    uint32_t g = 0;
+    int behind = 0;                           // keys of the sequence that come after the row's token
+    // A failed wait is remembered and ends the loop for all warps at the next
+    // tile's vote, so that no thread leaves others at a barrier.
+    bool dead = false;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      dead |= !wait_phase<false>(b, parity, wctl);
+      __syncwarp();
+    };
+    while (cur.valid()) {
+      const bool first = cur.is_first(), last = cur.is_last();
+      const int keys = cur.keys(), rows = cur.rows(p, int(rank));
+      if (first) {
+        behind = p.Sq - 1 - ((2 * cur.block + int(rank)) * kRows + r) / p.H;
+        m = -INFINITY, l = 0.0f;
+      }
+      wait(bar(ctl->s_full[g & 1u]), (g >> 1) & 1u);
+      ptx::tc_fence_after();
+      uint32_t s[16];
+      tmem_ld_32x32b_x16(tmem + lanes + kSCol + (g & 1u) * kSCols + 16 * half, s);
+      ptx::tmem_ld_wait();
+      ptx::tc_fence_before();
+      const int sees = r < rows ? cur.len - behind - cur.tile * kKeys - key0 : 0;
+      if (sees < 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i >= sees) s[i] = 0xFF800000u;
+      }
+      float t0 = fmaxf(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])), __uint_as_float(s[2]));
+      float t1 = fmaxf(fmaxf(__uint_as_float(s[3]), __uint_as_float(s[4])), __uint_as_float(s[5]));
+#pragma unroll
+      for (int i = 6; i < 14; i += 4) {
+        t0 = fmaxf(fmaxf(t0, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+        t1 = fmaxf(fmaxf(t1, __uint_as_float(s[i + 2])), __uint_as_float(s[i + 3]));
+      }
+      const float top = fmaxf(fmaxf(fmaxf(t0, t1), __uint_as_float(s[14])), __uint_as_float(s[15])) * p.scale_log2;
+      ctl->part[who][r] = top;
+      // The reference maximum moves only when some row's maximum grew by 2^8:
+      // until then weights of up to 2^8 are as exact as weights of up to 1.
+      if (bar_any(1, kSoftmaxThreads, first || dead || top - m > kGrow)) {
+        if (bar_any(2, kSoftmaxThreads, dead)) break;
+        const float mn = fmaxf(m, fmaxf(fmaxf(ctl->part[0][r], ctl->part[1][r]), fmaxf(ctl->part[2][r], ctl->part[3][r])));
+        const float a = mn == m ? 1.0f : exp2_approx(m - mn);
+        m = mn;
+        l *= a;
+        bar_sync(2, kSoftmaxThreads);         // all have read the maxima
+        if (!first) {
+          wait(bar(ctl->pv_done), (g - 1) & 1u);
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t o[32];
+            ptx::tmem_ld_32x32b_x32(tmem + lanes + 128 * half + c, o);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            ptx::tmem_st_32x32b_x32(tmem + lanes + 128 * half + c, o);
+          }
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+        }
+      }
+      // the weights, rounded to 16 bits for the second product; their sum stays float32
+      const float neg = m == -INFINITY ? 0.0f : -m;
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float e0 = __uint_as_float(s[i]), e1 = __uint_as_float(s[i + 1]);
+        fma2(e0, e1, p.scale_log2, neg, neg);
+        e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+        l += e0 + e1;
+        w[i / 2] = Elem<T>::pack(e0, e1);
+      }
+      if (g) wait(bar(ctl->pv_done), (g - 1) & 1u);  // P is free
+      const uint32_t at = base + kPOff + r * 128;
+      ptx::sts128(at + (((key0 / 8) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+      ptx::sts128(at + (((key0 / 8 + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
+      // Rows of the tile past the last key may hold anything, and 0 * NaN is
+      // NaN: they are zeroed, once the tile's values have landed, before the
+      // second product reads them.
+      wait(bar(ctl->v_full[g & 1u]), (g >> 1) & 1u);
+      if (keys < kKeys) {
+        const int from = max(keys, 0);
+        const uint32_t v = base + kVOff + (g & 1u) * kVBytes;
+        for (int i = threadIdx.x; i < (kKeys - from) * 32; i += kSoftmaxThreads) {
+          const int k = from + (i >> 5);      // 32 pieces of 16 bytes a key: eight in each of four atoms
+          ptx::sts128(v + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_release_cluster(p_full);
+      if (last) {
+        const bool whole = cur.first == 0 && cur.tile + 1 == cur.tiles;
+        const int64_t part = 2 * blockIdx.x + (cur.pos - cur.tile + cur.first == share * range ? 0 : 1);
+        const int64_t row0 = whole ? int64_t(cur.b) * p.rows + (2 * cur.block + int(rank)) * kRows : part * kRows;
+        ctl->part[who][r] = l;                // the maxima have been read
+        bar_sync(2, kSoftmaxThreads);
+        const float sum = (ctl->part[0][r] + ctl->part[1][r]) + (ctl->part[2][r] + ctl->part[3][r]);
+        if (who == 0) {
+          ctl->col[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const float e = sum == 0.0f ? -INFINITY : m + log2f(sum);
+          if (r < rows) (whole ? p.lse : p.part_lse)[row0 + r] = whole ? e * kLn2 : e;
+        }
+        const bool empty = bar_any(2, kSoftmaxThreads, sum == 0.0f);  // some row saw no key
+        wait(bar(ctl->pv_done), g & 1u);
+        ptx::tc_fence_after();
+        // This warp's 32 lanes x 128 columns in pieces of 16 lanes x 16 columns:
+        // a thread gets two neighbouring values of rows q and q + 8, so that a
+        // row's stores fill whole sectors.
+#pragma unroll
+        for (int hl = 0; hl < 2; ++hl) {
+          const int q = 32 * (quarter & 1) + 16 * hl + (lane >> 2), c = lane & 3;
+          const float f0 = ctl->col[q], f1 = ctl->col[q + 8];
+          const int dim0 = 256 * half + 128 * upper;
+#pragma unroll
+          for (int v = 0; v < 128; v += 32) {
+            uint32_t o[16];
+            tmem_ld_16x256b_x4(tmem + lanes + (uint32_t(16 * hl) << 16) + 128 * half + v, o);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float f = i & 2 ? f1 : f0;
+              o[i] = empty && f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * f);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {     // row q, then q + 8
+              const int row = q + 8 * h;
+              if (whole) {
+                T* out = reinterpret_cast<T*>(p.out) + (row0 + row) * kLatent + dim0 + v;
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                  // two pieces of 8 columns: even threads take four values of the first, odd ones of the second
+                  const uint32_t w0 = Elem<T>::pack(__uint_as_float(o[4 * i + 2 * h]), __uint_as_float(o[4 * i + 2 * h + 1]));
+                  const uint32_t w1 = Elem<T>::pack(__uint_as_float(o[4 * i + 4 + 2 * h]), __uint_as_float(o[4 * i + 5 + 2 * h]));
+                  const uint32_t got = __shfl_xor_sync(kFull, c & 1 ? w0 : w1, 1);
+                  if (row < rows)
+                    *reinterpret_cast<uint2*>(out + 8 * (i + (c & 1)) + 4 * (c >> 1)) =
+                        c & 1 ? make_uint2(got, w1) : make_uint2(w0, got);
+                }
+              } else if (row < rows) {
+                float* out = p.part_o + (row0 + row) * kLatent + dim0 + v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  *reinterpret_cast<uint2*>(out + 8 * i + 2 * c) = make_uint2(o[4 * i + 2 * h], o[4 * i + 2 * h + 1]);
+              }
+            }
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release_cluster(o_free);
+      }
+      cur.next(p);
+      ++g;
+    }
+  }
+
+  // No CTA of the pair leaves, or frees its tensor memory, while the other's
+  // MMAs or copies may still use it.
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == kIssuer) ptx::tmem_dealloc_pair(tmem, kTmemCols);
+  ptx::cluster_sync();
+}
+
+}  // namespace
+}  // namespace nvfp4moe

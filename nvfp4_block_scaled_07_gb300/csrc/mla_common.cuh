@@ -72,23 +72,6 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {    
       : "f"(a), "f"(b));
 }
 
-// Arrival on a barrier of any CTA of the cluster that releases this thread's
-// shared-memory writes to it, and the matching wait.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ uint32_t mbar_test_acquire_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok;
-}
-
 // ---- bounded waits ---------------------------------------------------------------
 // Shared state of one CTA's waits: a wait that exceeds the limit raises the
 // sticky flag and makes every role leave its loop.
@@ -98,18 +81,13 @@ struct WaitCtl {
   unsigned* flags;
 };
 
-// SPIN polls without suspending the thread (the producer and the MMA
-// issuer); CLUSTER also acquires what other CTAs of the cluster released.
-template <bool SPIN, bool CLUSTER = false>
+// SPIN polls without suspending the thread (the producer and the MMA issuer).
+template <bool SPIN>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
-  auto poll = [&] {
-    if constexpr (CLUSTER) return mbar_test_acquire_cluster(bar, parity);
-    else return SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity);
-  };
-  if (poll()) return true;
+  if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (poll()) return true;
+    if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0u) {
       if (ctl->abort) return false;
       if (ptx::globaltimer_ns() - t0 > uint64_t(ctl->limit_us) * 1000u) {
@@ -125,10 +103,9 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 __device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, ptx::mbar_test_wait(bar, parity) != 0);
 }
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
-  if (!CLUSTER && test_warp(bar, parity)) return true;
-  return __all_sync(0xFFFFFFFFu, wait_phase<true, CLUSTER>(bar, parity, ctl));
+  if (test_warp(bar, parity)) return true;
+  return __all_sync(0xFFFFFFFFu, wait_phase<true>(bar, parity, ctl));
 }
 
 // Wait for a CTA's own copies or MMAs before it leaves, also after an abort.

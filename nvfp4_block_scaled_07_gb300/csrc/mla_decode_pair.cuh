@@ -81,7 +81,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   volatile WaitCtl* wctl = &ctl->wait;
   const uint32_t base = ptx::smem_u32(smem);
   const int warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const uint32_t rank = ptx::cluster_ctarank();
+  const uint32_t rank = blockIdx.x & 1u;      // of the cluster (2, 1, 1); from blockIdx, so that branches on it count as uniform
   const int range = int(blockIdx.x >> 1), ranges = int(gridDim.x >> 1);
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
@@ -223,9 +223,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       while (ok && cur.valid()) {
         if (cs.valid() && !issue_s()) break;
         const uint32_t s = gp & 1u;
-        if (!wait_warp<true>(bar(ctl->p_full), gp & 1u, wctl)) break;
+        if (!wait_warp(bar(ctl->p_full), gp & 1u, wctl)) break;
         // the previous segment's accumulator has been read
-        if (cur.is_first() && seg_p++ && !wait_warp<true>(bar(ctl->o_free), seg_p & 1u, wctl)) break;
+        if (cur.is_first() && seg_p++ && !wait_warp(bar(ctl->o_free), seg_p & 1u, wctl)) break;
         ptx::tc_fence_after();
         const uint32_t more = cur.is_first() ? 0u : 1u;
         const uint64_t a = desc_sw128(base + kPOff, 16, 1024);
@@ -358,10 +358,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           ptx::sts128(v + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
         }
       }
+      // What the arrival announces lies in this CTA: weights and zeros in its
+      // shared memory, ordered for the tensor core by the proxy fence, and
+      // tensor-memory reads, by the tcgen05 fence.  A cluster-scope release
+      // besides took 2000 cycles.
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_release_cluster(p_full);
+      if (lane == 0) ptx::mbar_arrive_cluster(p_full);
       if (last) {
         const bool whole = cur.first == 0 && cur.tile + 1 == cur.tiles;
         const int64_t part = 2 * blockIdx.x + (cur.pos - cur.tile + cur.first == share * range ? 0 : 1);
@@ -421,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(o_free);
+        if (lane == 0) ptx::mbar_arrive_cluster(o_free);
       }
       cur.next(p);
       ++g;

@@ -87,7 +87,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->k_full[s]), kPieces);
+      ptx::mbar_init(bar(ctl->k_full[s]), 2);
       ptx::mbar_init(bar(ctl->v_full[s]), kPieces);
       ptx::mbar_init(bar(ctl->k_empty[s]), 1);
       for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[s][i]), 1);
@@ -125,70 +125,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   Cursor cur;
   const int share = cur.init(p, range, ranges);
 
-  if (warp >= kProducer && warp < kProducer + kPieces) {
-    // ---- producers: warp i copies the values of keys 16 i .. 16 i + 15 and,
-    // of its CTA's 32 keys, group i of 8 whole rows ----
-    const int piece = warp - kProducer;
-    if (piece == 0 && blockIdx.x == 0)        // lengths that are not served as they are
-      for (int b = lane; b < p.B; b += 32)
-        if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
+  if (warp >= kProducer && warp < kIssuer) {
+    // ---- producers: two warps copy whole rows (16 of the CTA's 32 keys
+    // each), two copy values (32 of the tile's 64 keys each), so that rows,
+    // whose buffers S frees early, never wait behind values.  A tile's pages
+    // are looked up while the tile before it waits for its buffers. ----
+    const int sub = (warp - kProducer) & 1;
+    const bool rows_role = warp < kProducer + 2;
     const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0u;  // the even CTA tells its barriers what to expect
     const int oob = p.num_pages * p.page;
-    const int kgroup = 4 * int(rank) + piece;  // its group of whole rows, in the tile
-    uint32_t g = 0, seg = 0, gv = 0;          // tiles (K, V) and Q blocks begun
-    const uint32_t kf0 = ptx::mapa(bar(ctl->k_full[0]), 0);
-    const uint32_t qf = ptx::mapa(bar(ctl->q_full), 0);
-    // First cache row of 8 keys of the cursor's tile.
-    auto look_up = [&](const Cursor& c, int group) {
-      const int row = c.tile * kKeys + 8 * group;
+    // First cache row of 16 keys of the cursor's tile.
+    auto look_up = [&](const Cursor& c, int piece) {
+      const int row = c.tile * kKeys + 16 * piece;
       if (row >= c.len) return oob;
       const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
       if (id >= 0 && id < p.num_pages) return id * p.page + (row & (p.page - 1));
-      if (lane == 0) atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
+      atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
       return oob;
     };
-    int k_row = cur.valid() ? look_up(cur, kgroup) : 0, v_row = cur.valid() ? look_up(cur, 2 * piece) : 0;
-    while (cur.valid()) {
-      if (piece == 0 && cur.is_first()) {
-        if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
-        arrive_expect_tx(el0, bar(ctl->q_full), 2 * kQBytes);
+    uint32_t g = 0;                           // tiles begun (of values: complete ones)
+    if (rows_role) {
+      if (sub == 0 && blockIdx.x == 0)        // lengths that are not served as they are
+        for (int b = lane; b < p.B; b += 32)
+          if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
+      const int piece = 2 * int(rank) + sub;  // the warp's 16 keys within the tile
+      const uint32_t kf0 = ptx::mapa(bar(ctl->k_full[0]), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
+      uint32_t seg = 0;
+      int row = cur.valid() ? look_up(cur, piece) : 0;
+      while (cur.valid()) {
+        if (sub == 0 && cur.is_first()) {
+          if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
+          arrive_expect_tx(el0, bar(ctl->q_full), 2 * kQBytes);
 #pragma unroll
-        for (int c = 0; c < 9; c += 3)
-          tma_load_3d_pair(el, base + kQOff + c * 64 * 128, &q_map, qf, 0,
-                           cur.b * p.rows + (2 * cur.block + int(rank)) * kRows, c);
-        ++seg;
+          for (int c = 0; c < 9; c += 3)
+            tma_load_3d_pair(el, base + kQOff + c * 64 * 128, &q_map, qf, 0,
+                             cur.b * p.rows + (2 * cur.block + int(rank)) * kRows, c);
+          ++seg;
+        }
+        const int groups = (max(cur.keys(), 0) + 7) / 8;  // of 8 keys, in the tile
+        Cursor nxt = cur;
+        nxt.next(p);
+        const int next = nxt.valid() ? look_up(nxt, piece) : 0;
+        const uint32_t s = g & 1u, dst = base + kKOff + s * kKBytes + 2 * sub * kGroup;
+        if (!wait_warp(bar(ctl->k_empty[s]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
+        // both CTAs' groups 2 sub and 2 sub + 1 of their four
+        const int mine = min(2, max(0, groups - 2 * sub)), theirs = min(2, max(0, groups - 4 - 2 * sub));
+        arrive_expect_tx(el0, bar(ctl->k_full[s]), uint32_t((mine + theirs) * kGroup));
+        const int n = rank ? theirs : mine;
+        if (n > 0) tma_load_3d_pair(el, dst, &kv_map, kf0 + 8 * s, 0, row, 0);
+        if (n > 1) tma_load_3d_pair(el, dst + kGroup, &kv_map, kf0 + 8 * s, 0, min(row, oob - 8) + 8, 0);
+        ++g;
+        cur = nxt;
+        row = next;
+        if (cur.valid()) {                    // the next rows are requested into L2 while their buffers are in use
+          const int ahead = min(16, cur.len - cur.tile * kKeys - 16 * piece);
+          if (ahead > 0 && row != oob)
+            prefetch_l2(el, p.cache + int64_t(row) * (2 * kRow), uint32_t(ahead) * (2 * kRow));
+        }
       }
-      const uint32_t s = g & 1u, ph = ((g >> 1) & 1u) ^ 1u;
-      const int groups = (max(cur.keys(), 0) + 7) / 8;  // of 8 keys, in the tile
-      if (!wait_warp(bar(ctl->k_empty[s]), ph, wctl)) break;
-      arrive_expect_tx(el0, bar(ctl->k_full[s]), uint32_t((piece < groups ? kGroup : 0) + (4 + piece < groups ? kGroup : 0)));
-      if (kgroup < groups)
-        tma_load_3d_pair(el, base + kKOff + s * kKBytes + piece * kGroup, &kv_map, kf0 + 8 * s, 0, k_row, 0);
-      ++g;
-      const int vg = min(2, max(0, groups - 2 * piece));
-      if (!wait_warp(bar(ctl->v_empty[s][piece]), ph, wctl)) break;
-      const uint32_t vf = bar(ctl->v_full[s]), dst = base + kVOff + s * kVBytes + 2 * piece * kVGroup;
-      arrive_expect_tx(el, vf, uint32_t(vg * kVGroup));
-      if (vg > 0) tma_load_4d(el, dst, &v_map, vf, 0, v_row, 2 * int(rank), 0);
-      if (vg > 1) tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(v_row, oob - 8) + 8, 2 * int(rank), 0);
-      ++gv;
-      cur.next(p);
-      if (cur.valid()) {
-        k_row = look_up(cur, kgroup);
-        v_row = look_up(cur, 2 * piece);
-        // the next tile's rows are requested into L2 while their buffers are in use
-        const int rows = min(8, cur.len - cur.tile * kKeys - 8 * kgroup);
-        if (rows > 0 && k_row != oob)
-          prefetch_l2(el, p.cache + int64_t(k_row) * (2 * kRow), uint32_t(rows) * (2 * kRow));
+      // Every copy has landed before the pair leaves: the even CTA's barriers
+      // count both CTAs' (bounded, since an abort may leave a phase incomplete).
+      if (rank == 0 && seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
+      for (uint32_t s = 0; s < kStages; ++s) {
+        const uint32_t n = (g + 1 - s) / 2;
+        if (rank == 0 && n) drain_phase(bar(ctl->k_full[s]), (n - 1) & 1u);
       }
-    }
-    // Every copy has landed before the pair leaves: the even CTA's barriers
-    // count both CTAs' (bounded, since an abort may leave a phase incomplete).
-    if (rank == 0 && seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
-    for (uint32_t s = 0; s < kStages; ++s) {
-      const uint32_t nk = (g + 1 - s) / 2, nv = (gv + 1 - s) / 2;
-      if (rank == 0 && nk) drain_phase(bar(ctl->k_full[s]), (nk - 1) & 1u);
-      if (nv) drain_phase(bar(ctl->v_full[s]), (nv - 1) & 1u);
+    } else {
+      bool ok = true;
+      int row = cur.valid() ? look_up(cur, 2 * sub + (lane & 1)) : 0;  // of pieces 2 sub (even lanes) and 2 sub + 1
+      while (ok && cur.valid()) {
+        const int groups = (max(cur.keys(), 0) + 7) / 8;
+        Cursor nxt = cur;
+        nxt.next(p);
+        const int next = nxt.valid() ? look_up(nxt, 2 * sub + (lane & 1)) : 0;
+        const uint32_t s = g & 1u, vf = bar(ctl->v_full[s]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int piece = 2 * sub + i, from = __shfl_sync(kFull, row, i);
+          // after an abort the second piece still comes: a phase that was begun has to end
+          if (ok) ok = wait_warp(bar(ctl->v_empty[s][piece]), ((g >> 1) & 1u) ^ 1u, wctl);
+          if (i == 0 && !ok) break;
+          const int n = min(2, max(0, groups - 2 * piece));
+          const uint32_t dst = base + kVOff + s * kVBytes + 2 * piece * kVGroup;
+          arrive_expect_tx(el, vf, uint32_t(n * kVGroup));
+          if (n > 0) tma_load_4d(el, dst, &v_map, vf, 0, from, 2 * int(rank), 0);
+          if (n > 1) tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(from, oob - 8) + 8, 2 * int(rank), 0);
+          if (i == 1) ++g;
+        }
+        cur = nxt;
+        row = next;
+      }
+      for (uint32_t s = 0; s < kStages; ++s) {
+        const uint32_t n = (g + 1 - s) / 2;
+        if (n) drain_phase(bar(ctl->v_full[s]), (n - 1) & 1u);
+      }
     }
     __syncwarp();
   } else if (warp == kIssuer) {

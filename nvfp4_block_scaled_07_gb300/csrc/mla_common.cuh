@@ -82,15 +82,18 @@ struct WaitCtl {
 };
 
 // SPIN polls without suspending the thread (the producer and the MMA issuer).
+// The timer is read only after 256 polls: reading it takes longer than most
+// waits last.
 template <bool SPIN>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
-  if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer_ns();
+  uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0u) {
       if (ctl->abort) return false;
-      if (ptx::globaltimer_ns() - t0 > uint64_t(ctl->limit_us) * 1000u) {
+      const uint64_t now = ptx::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > uint64_t(ctl->limit_us) * 1000u) {
         ctl->abort = 1;
         atomicOr(ctl->flags, kFlagTimeout);
         return false;

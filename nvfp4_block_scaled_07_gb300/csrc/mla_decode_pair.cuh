@@ -12,11 +12,11 @@
 // which HBM delivers a pair's tile; one CTA takes 2030 for its 64 rows alone.
 // A CTA's share of a tile is 36 KB for S and 32 KB for P V (its own keys'
 // values twice, so that both CTAs use the same descriptors), two tiles in
-// flight.  S of the next tile is issued before P V of this one and covers the
-// softmax.
+// flight; S runs up to two tiles ahead of P V and covers the softmax.
 //
 // Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-11
-// TMA producers, warp 12 tensor-memory owner and, in the even CTA, MMA issuer.
+// TMA producers, warp 12 tensor-memory owner and, in the even CTA, issuer of
+// S, warp 13 issuer of P V there.
 // The even CTA's barriers count both CTAs' copies of whole rows and softmax
 // arrivals; commits arrive in both.  The copies of values count in their own
 // CTA, whose softmax warps wait for them before they arrive: rows past the
@@ -33,8 +33,8 @@ namespace {
 namespace pair {
 constexpr int kStages = 2;
 constexpr int kPieces = 4;                    // of a tile's values: 16 keys each
-constexpr int kProducer = 8, kIssuer = 12;
-constexpr int kThreads = 416;
+constexpr int kProducer = 8, kIssuer = 12;    // first producer warp; the MMA warps, S and P V
+constexpr int kThreads = 448;
 constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256, kSCols = 32;  // S buffers after the 256 columns of O
@@ -50,9 +50,9 @@ constexpr int kPOff = kVOff + kStages * kVBytes;
 constexpr int kSmem = kPOff + 64 * 128;
 
 struct Control {
-  // counted in the even CTA only: k_full, q_full, p_full, o_free
+  // counted in the even CTA only: k_full, q_full, s_free, p_full, o_free
   uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages][kPieces];
-  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_free, drain;
+  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
   float part[4][kRows];                       // per row: maxima, later sums, of the four quarters of a tile's keys
@@ -99,7 +99,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     ptx::mbar_init(bar(ctl->p_full), 2 * kSoftmaxThreads / 32);
     ptx::mbar_init(bar(ctl->pv_done), 1);
     ptx::mbar_init(bar(ctl->o_free), 2 * kSoftmaxThreads / 32);
-    ptx::mbar_init(bar(ctl->drain), 1);
+    ptx::mbar_init(bar(ctl->s_free[0]), 2 * kSoftmaxThreads / 32);
+    ptx::mbar_init(bar(ctl->s_free[1]), 2 * kSoftmaxThreads / 32);
+    ptx::mbar_init(bar(ctl->drain), 2);
     ptx::fence_barrier_init();
     ctl->wait.abort = 0;
     ctl->wait.limit_us = p.wait_us;
@@ -221,60 +223,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kIssuer) {
-    // ---- MMA issuer, in the even CTA ----
-    if (rank == 0) {
-      const uint32_t el = elect_one();
-      const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 128, kKeys, false, false);
-      const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, 256, false, true);
-      uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
-      Cursor cs = cur;
-      auto issue_s = [&]() {
-        const uint32_t s = gs & 1u;
-        if (cs.is_first() && !wait_warp(bar(ctl->q_full), seg_s++ & 1u, wctl)) return false;
-        if (!wait_warp(bar(ctl->k_full[s]), (gs >> 1) & 1u, wctl)) return false;
+  } else if (warp >= kIssuer) {
+    // ---- MMA issuers, in the even CTA: one warp for S, one for P V.  A single
+    // warp's waits, commits and list walking between the two products took as
+    // long as the MMAs themselves (2600 cycles a tile). ----
+    const uint32_t el = elect_one();
+    if (rank == 0 && warp == kIssuer) {
+      const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, kKeys, false, false);
+      const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
+      for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
+        const uint32_t s = g & 1u, ph = (g >> 1) & 1u;
+        if (cur.is_first() && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
+        if (!wait_warp(bar(ctl->s_free[s]), ph ^ 1u, wctl) || !wait_warp(bar(ctl->k_full[s]), ph, wctl)) break;
         ptx::tc_fence_after();
-        const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
         const uint64_t b = desc_sw128(base + kKOff + s * kKBytes, 16, kGroup);
 #pragma unroll
         for (int c = 0; c < 9; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
-                         idesc_s, c + k > 0);
-        tc_commit_pair(el, bar(ctl->k_empty[s]));
+                         idesc, c + k > 0);
         tc_commit_pair(el, bar(ctl->s_full[s]));
-        if (cs.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
-        cs.next(p);
-        ++gs;
-        return true;
-      };
-      bool ok = !cur.valid() || issue_s();
-      while (ok && cur.valid()) {
-        if (cs.valid() && !issue_s()) break;
-        const uint32_t s = gp & 1u;
-        if (!wait_warp(bar(ctl->p_full), gp & 1u, wctl)) break;
+        tc_commit_pair(el, bar(ctl->k_empty[s]));
+        if (cur.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
+        cur.next(p);
+      }
+    } else if (rank == 0) {
+      const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, 256, false, true);
+      const uint64_t a = desc_sw128(base + kPOff, 16, 1024);
+      for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
+        const uint32_t s = g & 1u;
+        if (!wait_warp(bar(ctl->p_full), g & 1u, wctl)) break;
         // the previous segment's accumulator has been read
-        if (cur.is_first() && seg_p++ && !wait_warp(bar(ctl->o_free), seg_p & 1u, wctl)) break;
+        if (cur.is_first() && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
         ptx::tc_fence_after();
         const uint32_t more = cur.is_first() ? 0u : 1u;
-        const uint64_t a = desc_sw128(base + kPOff, 16, 1024);
         const uint64_t b = desc_sw128(base + kVOff + s * kVBytes, 1024, kVGroup);
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
 #pragma unroll
           for (int h = 0; h < 2; ++h)         // 256 values
-            mma_f16_pair(el, tmem + 128 * h, a + 2 * k, b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc_o,
+            mma_f16_pair(el, tmem + 128 * h, a + 2 * k, b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
                          k ? 1u : more);
           tc_commit_pair(el, bar(ctl->v_empty[s][k]));
         }
         tc_commit_pair(el, bar(ctl->pv_done));
         cur.next(p);
-        ++gp;
       }
-      tc_commit_pair(el, bar(ctl->drain));
     }
-    // Both CTAs stay until the pair's last MMA is done and its commits have
+    if (rank == 0) tc_commit_pair(el, bar(ctl->drain));
+    // Both CTAs stay until the pair's last MMAs are done and their commits have
     // arrived (the odd one waits here from the start).
     const uint64_t t0 = ptx::globaltimer_ns();
     while (!ptx::mbar_try_wait(bar(ctl->drain), 0))
@@ -298,6 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
     const int r = 32 * (quarter & 1) + lane, key0 = 32 * upper + 16 * half, who = 2 * upper + half;
     const uint32_t p_full = ptx::mapa(bar(ctl->p_full), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
+    const uint32_t s_free = ptx::mapa(bar(ctl->s_free[0]), 0);
     float m = 0.0f, l = 0.0f;                 // running maximum (log2 domain) and this quarter's sum
     uint32_t g = 0;
     int behind = 0;                           // keys of the sequence that come after the row's token
@@ -321,6 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       tmem_ld_32x32b_x16(tmem + lanes + kSCol + (g & 1u) * kSCols + 16 * half, s);
       ptx::tmem_ld_wait();
       ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(s_free + 8 * (g & 1u));
       const int sees = r < rows ? cur.len - behind - cur.tile * kKeys - key0 : 0;
       if (sees < 16) {
 #pragma unroll

@@ -72,6 +72,30 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {    
       : "f"(a), "f"(b));
 }
 
+__device__ __forceinline__ float max_of(const uint32_t (&s)[32]) {
+  float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);  // two chains of three-way maxima
+#pragma unroll
+  for (int k = 2; k < 30; k += 4) {
+    a = fmaxf(fmaxf(a, __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
+    b = fmaxf(fmaxf(b, __uint_as_float(s[k + 2])), __uint_as_float(s[k + 3]));
+  }
+  return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31])));
+}
+// w = exp2(s * scale + neg) of 32 scores, rounded to 16 bits for the second
+// product; their float32 sum is added to sum0 + sum1.
+template <typename T>
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t (&w)[16], float scale, float neg, float& sum0,
+                                        float& sum1) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    float e0 = __uint_as_float(s[k]), e1 = __uint_as_float(s[k + 1]);
+    fma2(e0, e1, scale, neg, neg);
+    e0 = exp2_approx(e0), e1 = exp2_approx(e1);
+    add2(sum0, sum1, e0, e1);
+    w[k / 2] = Elem<T>::pack(e0, e1);
+  }
+}
+
 // ---- bounded waits ---------------------------------------------------------------
 // Shared state of one CTA's waits: a wait that exceeds the limit raises the
 // sticky flag and makes every role leave its loop.

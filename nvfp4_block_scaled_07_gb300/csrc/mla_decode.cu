@@ -43,6 +43,7 @@ namespace {
 
 using namespace mla;
 
+constexpr int kKeys = 64;                     // keys of a tile
 constexpr int kChunk = 64 * 128;              // 64 rows x 64 values, 128-byte rows
 constexpr int kTile = 9 * kChunk;
 constexpr int kPieces = 4;                    // of a tile: 16 keys each, freed one by one
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
-  Cursor cur;
+  Cursor<kKeys> cur;
   const int share = cur.init(p, blockIdx.x, gridDim.x);
 
   if (warp >= kProducer && warp < kProducer + kPieces) {
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int oob = p.num_pages * p.page;
     uint32_t g = 0, seg = 0;
     // First cache row of the piece.
-    auto look_up = [&](const Cursor& c) {
+    auto look_up = [&](const Cursor<kKeys>& c) {
       const int row = c.tile * kKeys + 16 * piece;
       if (row >= c.len) return oob;
       const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t el = elect_one();
     const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
     uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
-    Cursor cs = cur;
+    Cursor<kKeys> cs = cur;
     bool ok = true;
     // The two tiles in shared memory go through together: S, S, P V, P V.
     // The softmax of each then runs under an MMA of the other, and the copies
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // serves the item that the border between ranges c and c + 1 is the first to
 // cut.
 constexpr int kJoinThreads = 256;
-template <typename T, bool BY_ITEM>
+template <typename T, bool BY_ITEM, int KEYS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p) {
   constexpr int kShare = BY_ITEM ? 4 : 1, kJoinRows = kJoinThreads / 32 / kShare;  // warps a row, rows a block
   __shared__ float4 s_sum[BY_ITEM ? kJoinThreads / 32 : 1][4][32];
@@ -458,9 +459,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
     b = int(blockIdx.x) / p.blocks;
     block = int(blockIdx.x) - b * p.blocks;
     share = p.heads[0].share;
-    tiles = item_tiles(seq_len(p, b));
+    tiles = item_tiles<KEYS>(seq_len(p, b));
     start = 0;
-    for (int i = lane; i < b; i += 32) start += item_tiles(seq_len(p, i)) * p.blocks;
+    for (int i = lane; i < b; i += 32) start += item_tiles<KEYS>(seq_len(p, i)) * p.blocks;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) start += __shfl_xor_sync(kFull, start, d);
     start += tiles * block;
@@ -541,8 +542,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kMinShare = 4;
 
 // Most tiles the call can have.
-int64_t most_tiles(const MlaDecodeArgs& a, int ctas) {
-  const int64_t longest = std::max<int64_t>(1, ceil_div(int64_t(a.max_pages) * a.page, kKeys));
+int64_t most_tiles(const MlaDecodeArgs& a, int ctas, int keys) {
+  const int64_t longest = std::max<int64_t>(1, ceil_div(int64_t(a.max_pages) * a.page, keys));
   return int64_t(a.B) * ceil_div(int64_t(a.Sq) * a.H, kRows * ctas) * longest;
 }
 
@@ -565,7 +566,7 @@ int max_pairs(K kernel) {
 
 template <typename T>
 int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
-  if (most_tiles(a, 1) >= (int64_t(1) << 31)) {
+  if (most_tiles(a, 1, kKeys) >= (int64_t(1) << 31)) {
     set_error_detail("B = %d, Sq * H = %d and max_pages * page_size = %lld keys exceed 2^31 tiles of 64 rows x 64 keys",
                      a.B, a.Sq * a.H, (long long)a.max_pages * a.page);
     return NVFP4MOE_ERR_UNSUPPORTED;
@@ -591,7 +592,8 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
       return NVFP4MOE_ERR_SMEM;
     }
   }
-  const int ranges = int(std::min<int64_t>(most_ranges, ceil_div(most_tiles(a, ctas), kMinShare)));
+  const int min_share = pair ? kMinShare * kKeys / pair::kKeys : kMinShare;
+  const int ranges = int(std::min<int64_t>(most_ranges, ceil_div(most_tiles(a, ctas, pair ? pair::kKeys : kKeys), min_share)));
   DecodeParams p;
   p.tables = a.tables;
   p.table_stride = a.table_stride;
@@ -610,7 +612,7 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   p.scale_log2 = a.scale * kLog2e;
   p.out = static_cast<uint8_t*>(a.out);
   p.lse = a.lse;
-  p.min_share = kMinShare;
+  p.min_share = min_share;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.heads = reinterpret_cast<Head*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + kMlaDecodeHeadBytes);
@@ -638,10 +640,11 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
     // Few items of many pieces are joined by item, several warps a row; more
     // items by the borders that cut them, a warp a row.
     const int most = std::min(kRows * ctas, rows);
-    if (items * 4 <= ranges)
-      err = launch_kernel(join_kernel<T, true>, dim3(int(items), (most + 1) / 2), dim3(kJoinThreads), 0, st, false, p);
-    else
-      err = launch_kernel(join_kernel<T, false>, dim3(ranges - 1, (most + 7) / 8), dim3(kJoinThreads), 0, st, false, p);
+    const bool by_item = items * 4 <= ranges;
+    const dim3 blocks = by_item ? dim3(int(items), (most + 1) / 2) : dim3(ranges - 1, (most + 7) / 8);
+    auto join = by_item ? (pair ? join_kernel<T, true, pair::kKeys> : join_kernel<T, true, kKeys>)
+                        : (pair ? join_kernel<T, false, pair::kKeys> : join_kernel<T, false, kKeys>);
+    err = launch_kernel(join, blocks, dim3(kJoinThreads), 0, st, false, p);
   }
   if (err != cudaSuccess) {
     set_error_detail("mla_decode launch: %s", cudaGetErrorString(err));

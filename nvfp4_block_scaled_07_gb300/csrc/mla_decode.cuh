@@ -16,7 +16,6 @@ __device__ unsigned g_decode_flags = 0;
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kRows = 64;                     // rows of a CTA
-constexpr int kKeys = 64;                     // keys of a tile
 constexpr int kGroup = 8 * 2 * kRow;          // 8 keys: nine atoms of 8 rows x 128 bytes
 constexpr float kGrow = 8.0f;                 // rescale O only when a maximum grew by 2^8
 
@@ -49,9 +48,13 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int b) {
   return n < 0 ? 0 : int(min(int64_t(n), int64_t(p.max_pages) * p.page));
 }
 // Tiles of an item; an empty sequence has one, whose keys are all masked.
-__device__ __forceinline__ int item_tiles(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
+template <int KEYS>
+__device__ __forceinline__ int item_tiles(int len) {
+  return len > 0 ? (len + KEYS - 1) / KEYS : 1;
+}
 
 // Walks the tiles [pos, end) of range `index` of `ranges` of the flattened (sequence, row block, tile) list.
+template <int KEYS>
 struct Cursor {
   int pos, end;                               // in the tile list
   int tile, tiles, first;                     // within the item; where this CTA entered it
@@ -63,7 +66,7 @@ struct Cursor {
     int total = 0, n = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-      total += b0 + lane < p.B ? item_tiles(n) : 0;
+      total += b0 + lane < p.B ? item_tiles<KEYS>(n) : 0;
     }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
@@ -76,7 +79,7 @@ struct Cursor {
     int before = 0;                           // tiles of the sequences before b0
     for (int b0 = 0;; b0 += 32) {
       if (p.B > 32) n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-      const int mine = b0 + lane < p.B ? item_tiles(n) * p.blocks : 0;
+      const int mine = b0 + lane < p.B ? item_tiles<KEYS>(n) * p.blocks : 0;
       int upto = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -89,7 +92,7 @@ struct Cursor {
         b = b0 + src;
         len = __shfl_sync(kFull, n, src);
         const int in = pos - before - __shfl_sync(kFull, upto - mine, src);
-        tiles = item_tiles(len);
+        tiles = item_tiles<KEYS>(len);
         block = in / tiles;
         tile = first = in - block * tiles;
         return share;
@@ -108,12 +111,12 @@ struct Cursor {
         block = 0;
         if (++b < p.B) {
           len = seq_len(p, b);
-          tiles = item_tiles(len);
+          tiles = item_tiles<KEYS>(len);
         }
       }
     }
   }
-  __device__ __forceinline__ int keys() const { return min(kKeys, len - tile * kKeys); }  // <= 0: none
+  __device__ __forceinline__ int keys() const { return min(KEYS, len - tile * KEYS); }  // <= 0: none
   // Rows of the item's 64-row part `part` (0, or 0 and 1 for a pair); <= 0: none.
   __device__ __forceinline__ int rows(const DecodeParams& p, int part = 0) const {
     return min(kRows, p.rows - (block * p.ctas + part) * kRows);

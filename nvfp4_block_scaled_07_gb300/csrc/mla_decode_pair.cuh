@@ -5,14 +5,19 @@
 // MMAs of M = 128 rows, 64 in each CTA, so that O (64 x 512 float32 a CTA)
 // leaves room for S, and each operand byte of the cache is staged by one CTA
 // for both:
-//   S [128 x 64 keys]     = Q x C^T     N = 64: each CTA stages 32 keys x 576
+//   S [128 x 128 keys]    = Q x C^T     N = 128: each CTA stages 64 keys x 576
 //   O [128 x 512] += P x C[:, :512]     N = 256, twice: each CTA stages 256 of
-//                                       the values of all 64 keys
-// 36 MMAs of 28 cycles and 8 of 68 a tile, 1560 cycles, against the 1410 in
-// which HBM delivers a pair's tile; one CTA takes 2030 for its 64 rows alone.
-// A CTA's share of a tile is 36 KB for S and 32 KB for P V (its own keys'
-// values twice, so that both CTAs use the same descriptors), two tiles in
-// flight; S runs up to two tiles ahead of P V and covers the softmax.
+//                                       the values of all 128 keys
+// 36 MMAs of 36 cycles and 16 of 68 a tile of 128 keys, 2360 cycles, against
+// the 2820 in which HBM delivers it to a pair.  Shared memory moves 400 KB a
+// tile (operands of S 144, of P V 96, copies 136, weights 24): 3100 cycles at
+// 128 bytes a clock, the tightest of the three.  Tiles of 64 keys in two
+// stages would read Q twice as often (measured 187 us against PAIR128 for
+// 128 sequences x 128 heads).
+// A CTA's share of a tile is 72 KB for S and 64 KB for P V (its own keys'
+// values twice, so that both CTAs use the same descriptors).  S frees its
+// rows while the softmax and P V of the tile still run, so that S is always a
+// tile ahead.
 //
 // Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-11
 // TMA producers, warp 12 tensor-memory owner and, in the even CTA, issuer of
@@ -31,27 +36,28 @@ namespace nvfp4moe {
 namespace {
 
 namespace pair {
-constexpr int kStages = 2;
-constexpr int kPieces = 4;                    // of a tile's values: 16 keys each
+constexpr int kKeys = 128;                    // keys of a tile
+constexpr int kPieces = 8;                    // of a tile: 16 keys each
 constexpr int kProducer = 8, kIssuer = 12;    // first producer warp; the MMA warps, S and P V
 constexpr int kThreads = 448;
 constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSCol = 256, kSCols = 32;  // S buffers after the 256 columns of O
+constexpr uint32_t kSCol = 256, kSCols = 64;  // S buffers after the 256 columns of O
 constexpr int kQBytes = 64 * 2 * kRow;
-constexpr int kKBytes = 4 * kGroup;           // 32 keys
+constexpr int kKBytes = 8 * kGroup;           // 64 keys
 constexpr int kVGroup = 4 * 1024;             // 8 keys: four atoms (two of each half of the values)
-constexpr int kVBytes = 8 * kVGroup;          // 64 keys
+constexpr int kVBytes = 16 * kVGroup;         // 128 keys
+constexpr int kPBytes = 64 * 128;             // 64 rows x 64 keys
 constexpr int kCtrl = 2048;
 constexpr int kQOff = kCtrl;
 constexpr int kKOff = kQOff + kQBytes;
-constexpr int kVOff = kKOff + kStages * kKBytes;
-constexpr int kPOff = kVOff + kStages * kVBytes;
-constexpr int kSmem = kPOff + 64 * 128;
+constexpr int kVOff = kKOff + kKBytes;
+constexpr int kPOff = kVOff + kVBytes;
+constexpr int kSmem = kPOff + 2 * kPBytes;
 
 struct Control {
   // counted in the even CTA only: k_full, q_full, s_free, p_full, o_free
-  uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages][kPieces];
+  uint64_t k_full, v_full, k_empty, v_empty[kPieces];
   uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
@@ -86,12 +92,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(bar(ctl->k_full[s]), 2);
-      ptx::mbar_init(bar(ctl->v_full[s]), kPieces);
-      ptx::mbar_init(bar(ctl->k_empty[s]), 1);
-      for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[s][i]), 1);
-    }
+    ptx::mbar_init(bar(ctl->k_full), 2);
+    ptx::mbar_init(bar(ctl->v_full), 2);
+    ptx::mbar_init(bar(ctl->k_empty), 1);
+    for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[i]), 1);
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
     ptx::mbar_init(bar(ctl->s_full[0]), 1);
@@ -124,20 +128,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
-  Cursor cur;
+  Cursor<kKeys> cur;
   const int share = cur.init(p, range, ranges);
 
   if (warp >= kProducer && warp < kIssuer) {
-    // ---- producers: two warps copy whole rows (16 of the CTA's 32 keys
-    // each), two copy values (32 of the tile's 64 keys each), so that rows,
+    // ---- producers: two warps copy whole rows (32 of the CTA's 64 keys
+    // each), two copy values (64 of the tile's 128 keys each), so that rows,
     // whose buffers S frees early, never wait behind values.  A tile's pages
     // are looked up while the tile before it waits for its buffers. ----
     const int sub = (warp - kProducer) & 1;
     const bool rows_role = warp < kProducer + 2;
     const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0u;  // the even CTA tells its barriers what to expect
     const int oob = p.num_pages * p.page;
-    // First cache row of 16 keys of the cursor's tile.
-    auto look_up = [&](const Cursor& c, int piece) {
+    // First cache row of piece `piece` (16 keys) of the cursor's tile.
+    auto look_up = [&](const Cursor<kKeys>& c, int piece) {
       const int row = c.tile * kKeys + 16 * piece;
       if (row >= c.len) return oob;
       const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
@@ -145,15 +149,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
       return oob;
     };
-    uint32_t g = 0;                           // tiles begun (of values: complete ones)
+    uint32_t g = 0;                           // tiles begun
     if (rows_role) {
       if (sub == 0 && blockIdx.x == 0)        // lengths that are not served as they are
         for (int b = lane; b < p.B; b += 32)
           if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
-      const int piece = 2 * int(rank) + sub;  // the warp's 16 keys within the tile
-      const uint32_t kf0 = ptx::mapa(bar(ctl->k_full[0]), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
+      const int piece0 = 4 * int(rank) + 2 * sub;  // the warp's two pieces, one looked up by even lanes, one by odd
+      const uint32_t kf = ptx::mapa(bar(ctl->k_full), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
+      const uint32_t dst = base + kKOff + 4 * sub * kGroup;
       uint32_t seg = 0;
-      int row = cur.valid() ? look_up(cur, piece) : 0;
+      int row = cur.valid() ? look_up(cur, piece0 + (lane & 1)) : 0;
       while (cur.valid()) {
         if (sub == 0 && cur.is_first()) {
           if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
@@ -165,62 +170,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           ++seg;
         }
         const int groups = (max(cur.keys(), 0) + 7) / 8;  // of 8 keys, in the tile
-        Cursor nxt = cur;
+        Cursor<kKeys> nxt = cur;
         nxt.next(p);
-        const int next = nxt.valid() ? look_up(nxt, piece) : 0;
-        const uint32_t s = g & 1u, dst = base + kKOff + s * kKBytes + 2 * sub * kGroup;
-        if (!wait_warp(bar(ctl->k_empty[s]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
-        // both CTAs' groups 2 sub and 2 sub + 1 of their four
-        const int mine = min(2, max(0, groups - 2 * sub)), theirs = min(2, max(0, groups - 4 - 2 * sub));
-        arrive_expect_tx(el0, bar(ctl->k_full[s]), uint32_t((mine + theirs) * kGroup));
+        const int next = nxt.valid() ? look_up(nxt, piece0 + (lane & 1)) : 0;
+        if (!wait_warp(bar(ctl->k_empty), (g & 1u) ^ 1u, wctl)) break;
+        // both CTAs' groups 4 sub .. 4 sub + 3 of their eight
+        const int mine = min(4, max(0, groups - 4 * sub)), theirs = min(4, max(0, groups - 8 - 4 * sub));
+        arrive_expect_tx(el0, bar(ctl->k_full), uint32_t((mine + theirs) * kGroup));
         const int n = rank ? theirs : mine;
-        if (n > 0) tma_load_3d_pair(el, dst, &kv_map, kf0 + 8 * s, 0, row, 0);
-        if (n > 1) tma_load_3d_pair(el, dst + kGroup, &kv_map, kf0 + 8 * s, 0, min(row, oob - 8) + 8, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int from = __shfl_sync(kFull, row, i >> 1);
+          if (i < n) tma_load_3d_pair(el, dst + i * kGroup, &kv_map, kf, 0, min(from, oob - 8 * (i & 1)) + 8 * (i & 1), 0);
+        }
         ++g;
         cur = nxt;
         row = next;
         if (cur.valid()) {                    // the next rows are requested into L2 while their buffers are in use
-          const int ahead = min(16, cur.len - cur.tile * kKeys - 16 * piece);
-          if (ahead > 0 && row != oob)
-            prefetch_l2(el, p.cache + int64_t(row) * (2 * kRow), uint32_t(ahead) * (2 * kRow));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int from = __shfl_sync(kFull, row, i);
+            const int ahead = min(16, cur.len - cur.tile * kKeys - 16 * (piece0 + i));
+            if (ahead > 0 && from != oob)
+              prefetch_l2(el, p.cache + int64_t(from) * (2 * kRow), uint32_t(ahead) * (2 * kRow));
+          }
         }
       }
       // Every copy has landed before the pair leaves: the even CTA's barriers
       // count both CTAs' (bounded, since an abort may leave a phase incomplete).
       if (rank == 0 && seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
-      for (uint32_t s = 0; s < kStages; ++s) {
-        const uint32_t n = (g + 1 - s) / 2;
-        if (rank == 0 && n) drain_phase(bar(ctl->k_full[s]), (n - 1) & 1u);
-      }
+      if (rank == 0 && g) drain_phase(bar(ctl->k_full), (g - 1) & 1u);
     } else {
       bool ok = true;
-      int row = cur.valid() ? look_up(cur, 2 * sub + (lane & 1)) : 0;  // of pieces 2 sub (even lanes) and 2 sub + 1
+      int row = cur.valid() ? look_up(cur, 4 * sub + (lane & 3)) : 0;  // of the warp's four pieces
       while (ok && cur.valid()) {
         const int groups = (max(cur.keys(), 0) + 7) / 8;
-        Cursor nxt = cur;
+        Cursor<kKeys> nxt = cur;
         nxt.next(p);
-        const int next = nxt.valid() ? look_up(nxt, 2 * sub + (lane & 1)) : 0;
-        const uint32_t s = g & 1u, vf = bar(ctl->v_full[s]);
+        const int next = nxt.valid() ? look_up(nxt, 4 * sub + (lane & 3)) : 0;
+        const uint32_t vf = bar(ctl->v_full);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int piece = 2 * sub + i, from = __shfl_sync(kFull, row, i);
-          // after an abort the second piece still comes: a phase that was begun has to end
-          if (ok) ok = wait_warp(bar(ctl->v_empty[s][piece]), ((g >> 1) & 1u) ^ 1u, wctl);
-          if (i == 0 && !ok) break;
-          const int n = min(2, max(0, groups - 2 * piece));
-          const uint32_t dst = base + kVOff + s * kVBytes + 2 * piece * kVGroup;
-          arrive_expect_tx(el, vf, uint32_t(n * kVGroup));
-          if (n > 0) tma_load_4d(el, dst, &v_map, vf, 0, from, 2 * int(rank), 0);
-          if (n > 1) tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(from, oob - 8) + 8, 2 * int(rank), 0);
-          if (i == 1) ++g;
+        for (int i = 0; i < 4; ++i) {
+          const int piece = 4 * sub + i, from = __shfl_sync(kFull, row, i);
+          // after an abort the other pieces still come: a phase that was begun has to end
+          if (ok) ok = wait_warp(bar(ctl->v_empty[piece]), (g & 1u) ^ 1u, wctl);
+          if (i == 0) {
+            if (!ok) break;
+            arrive_expect_tx(el, vf, uint32_t(min(8, max(0, groups - 8 * sub)) * kVGroup));
+          }
+          const uint32_t dst = base + kVOff + 2 * piece * kVGroup;
+          if (2 * piece < groups) tma_load_4d(el, dst, &v_map, vf, 0, from, 2 * int(rank), 0);
+          if (2 * piece + 1 < groups)
+            tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(from, oob - 8) + 8, 2 * int(rank), 0);
+          if (i == 3) ++g;
         }
         cur = nxt;
         row = next;
       }
-      for (uint32_t s = 0; s < kStages; ++s) {
-        const uint32_t n = (g + 1 - s) / 2;
-        if (n) drain_phase(bar(ctl->v_full[s]), (n - 1) & 1u);
-      }
+      if (g) drain_phase(bar(ctl->v_full), (g - 1) & 1u);
     }
     __syncwarp();
   } else if (warp >= kIssuer) {
@@ -232,40 +239,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, kKeys, false, false);
       const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
-        const uint32_t s = g & 1u, ph = (g >> 1) & 1u;
+        const uint32_t s = g & 1u;
         if (cur.is_first() && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
-        if (!wait_warp(bar(ctl->s_free[s]), ph ^ 1u, wctl) || !wait_warp(bar(ctl->k_full[s]), ph, wctl)) break;
+        if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl) || !wait_warp(bar(ctl->k_full), g & 1u, wctl)) break;
         ptx::tc_fence_after();
-        const uint64_t b = desc_sw128(base + kKOff + s * kKBytes, 16, kGroup);
+        const uint64_t b = desc_sw128(base + kKOff, 16, kGroup);
 #pragma unroll
         for (int c = 0; c < 9; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
                          idesc, c + k > 0);
+        tc_commit_pair(el, bar(ctl->k_empty));
         tc_commit_pair(el, bar(ctl->s_full[s]));
-        tc_commit_pair(el, bar(ctl->k_empty[s]));
         if (cur.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
         cur.next(p);
       }
     } else if (rank == 0) {
       const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, 256, false, true);
-      const uint64_t a = desc_sw128(base + kPOff, 16, 1024);
+      const uint64_t a = desc_sw128(base + kPOff, 16, 1024), b = desc_sw128(base + kVOff, 1024, kVGroup);
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
-        const uint32_t s = g & 1u;
         if (!wait_warp(bar(ctl->p_full), g & 1u, wctl)) break;
         // the previous segment's accumulator has been read
         if (cur.is_first() && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
         ptx::tc_fence_after();
         const uint32_t more = cur.is_first() ? 0u : 1u;
-        const uint64_t b = desc_sw128(base + kVOff + s * kVBytes, 1024, kVGroup);
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
 #pragma unroll
           for (int h = 0; h < 2; ++h)         // 256 values
-            mma_f16_pair(el, tmem + 128 * h, a + 2 * k, b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
+            mma_f16_pair(el, tmem + 128 * h, a + (k >> 2) * (kPBytes >> 4) + 2 * (k & 3), b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
                          k ? 1u : more);
-          tc_commit_pair(el, bar(ctl->v_empty[s][k]));
+          tc_commit_pair(el, bar(ctl->v_empty[k]));
         }
         tc_commit_pair(el, bar(ctl->pv_done));
         cur.next(p);
@@ -289,12 +294,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       h.block = cur.valid() ? cur.block : 0;
       p.heads[range] = h;
     }
-    // Lane quarters 0 and 1 hold the rows' first 32 keys, 2 and 3 the others;
-    // two warps share a quarter, each takes 16 of its columns: a thread has one
-    // row and 16 keys, four threads share a row.
+    // Lane quarters 0 and 1 hold the rows' first 64 keys, 2 and 3 the others;
+    // two warps share a quarter, each takes 32 of its columns: a thread has one
+    // row and 32 keys, four threads share a row.
     const int quarter = warp & 3, half = warp >> 2, upper = quarter >> 1;
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
-    const int r = 32 * (quarter & 1) + lane, key0 = 32 * upper + 16 * half, who = 2 * upper + half;
+    const int r = 32 * (quarter & 1) + lane, key0 = 64 * upper + 32 * half, who = 2 * upper + half;
     const uint32_t p_full = ptx::mapa(bar(ctl->p_full), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
     const uint32_t s_free = ptx::mapa(bar(ctl->s_free[0]), 0);
     float m = 0.0f, l = 0.0f;                 // running maximum (log2 domain) and this quarter's sum
@@ -316,26 +321,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       }
       wait(bar(ctl->s_full[g & 1u]), (g >> 1) & 1u);
       ptx::tc_fence_after();
-      uint32_t s[16];
-      tmem_ld_32x32b_x16(tmem + lanes + kSCol + (g & 1u) * kSCols + 16 * half, s);
+      uint32_t s[32];
+      ptx::tmem_ld_32x32b_x32(tmem + lanes + kSCol + (g & 1u) * kSCols + 32 * half, s);
       ptx::tmem_ld_wait();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(s_free + 8 * (g & 1u));
       const int sees = r < rows ? cur.len - behind - cur.tile * kKeys - key0 : 0;
-      if (sees < 16) {
+      if (sees < 32) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 32; ++i)
           if (i >= sees) s[i] = 0xFF800000u;
       }
-      float t0 = fmaxf(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])), __uint_as_float(s[2]));
-      float t1 = fmaxf(fmaxf(__uint_as_float(s[3]), __uint_as_float(s[4])), __uint_as_float(s[5]));
-#pragma unroll
-      for (int i = 6; i < 14; i += 4) {
-        t0 = fmaxf(fmaxf(t0, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
-        t1 = fmaxf(fmaxf(t1, __uint_as_float(s[i + 2])), __uint_as_float(s[i + 3]));
-      }
-      const float top = fmaxf(fmaxf(fmaxf(t0, t1), __uint_as_float(s[14])), __uint_as_float(s[15])) * p.scale_log2;
+      const float top = max_of(s) * p.scale_log2;
       ctl->part[who][r] = top;
       // The reference maximum moves only when some row's maximum grew by 2^8:
       // until then weights of up to 2^8 are as exact as weights of up to 1.
@@ -364,26 +362,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       }
       // the weights, rounded to 16 bits for the second product; their sum stays float32
       const float neg = m == -INFINITY ? 0.0f : -m;
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        float e0 = __uint_as_float(s[i]), e1 = __uint_as_float(s[i + 1]);
-        fma2(e0, e1, p.scale_log2, neg, neg);
-        e0 = exp2_approx(e0), e1 = exp2_approx(e1);
-        l += e0 + e1;
-        w[i / 2] = Elem<T>::pack(e0, e1);
-      }
+      uint32_t w[16];
+      float l1 = 0.0f;
+      weights<T>(s, w, p.scale_log2, neg, l, l1);
+      l += l1;
       if (g) wait(bar(ctl->pv_done), (g - 1) & 1u);  // P is free
-      const uint32_t at = base + kPOff + r * 128;
-      ptx::sts128(at + (((key0 / 8) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-      ptx::sts128(at + (((key0 / 8 + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
+      const uint32_t at = base + kPOff + upper * kPBytes + r * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        ptx::sts128(at + (((4 * half + i) ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
       // Rows of the tile past the last key may hold anything, and 0 * NaN is
       // NaN: they are zeroed, once the tile's values have landed, before the
       // second product reads them.
-      wait(bar(ctl->v_full[g & 1u]), (g >> 1) & 1u);
+      wait(bar(ctl->v_full), g & 1u);
       if (keys < kKeys) {
         const int from = max(keys, 0);
-        const uint32_t v = base + kVOff + (g & 1u) * kVBytes;
+        const uint32_t v = base + kVOff;
         for (int i = threadIdx.x; i < (kKeys - from) * 32; i += kSoftmaxThreads) {
           const int k = from + (i >> 5);      // 32 pieces of 16 bytes a key: eight in each of four atoms
           ptx::sts128(v + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);

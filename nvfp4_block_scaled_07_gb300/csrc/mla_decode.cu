@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!first) {
           wait(bar(ctl->pv_done), (g - 1) & 1u);
           ptx::tc_fence_after();
+#pragma unroll 1
           for (int c = 2 * half * kRows; c < 2 * (half + 1) * kRows; c += 32) {
             if ((c & (kRows - 1)) >= rows) continue;
             uint32_t o[32];
@@ -385,12 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         empty = bar_any(2, kSoftmaxThreads, empty);
         wait(bar(ctl->pv_done), g & 1u);
         ptx::tc_fence_after();
+#pragma unroll 1
         for (int c0 = 0; c0 < rows; c0 += 32) {
           float f[32];                        // the factors of 32 rows, for both blocks of values
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(f + i) = *reinterpret_cast<const float4*>(ctl->col + c0 + i);
-#pragma unroll
+#pragma unroll 1
           for (int v = 0; v < 2; ++v) {
             uint32_t o[32];
             ptx::tmem_ld_32x32b_x32(tmem + quarter + (2 * half + v) * kRows + c0, o);
@@ -405,24 +407,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (whole) {
               T* out = reinterpret_cast<T*>(p.out) + (row0 + c0) * kLatent + dim;
-              if (n == 32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) out[i * kLatent] = Elem<T>::from(__uint_as_float(o[i]));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i < n) out[i * kLatent] = Elem<T>::from(__uint_as_float(o[i]));
-              }
+              for (int i = 0; i < 32; ++i)
+                if (i < n) out[i * kLatent] = Elem<T>::from(__uint_as_float(o[i]));
             } else {
               float* out = p.part_o + (row0 + c0) * kLatent + dim;
-              if (n == 32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) out[i * kLatent] = __uint_as_float(o[i]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i < n) out[i * kLatent] = __uint_as_float(o[i]);
-              }
+              for (int i = 0; i < 32; ++i)
+                if (i < n) out[i * kLatent] = __uint_as_float(o[i]);
             }
           }
         }
@@ -447,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // serves the item that the border between ranges c and c + 1 is the first to
 // cut.
 constexpr int kJoinThreads = 256;
-template <typename T, bool BY_ITEM, int KEYS>
+template <typename T, bool BY_ITEM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p) {
   constexpr int kShare = BY_ITEM ? 4 : 1, kJoinRows = kJoinThreads / 32 / kShare;  // warps a row, rows a block
   __shared__ float4 s_sum[BY_ITEM ? kJoinThreads / 32 : 1][4][32];
@@ -459,9 +451,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
     b = int(blockIdx.x) / p.blocks;
     block = int(blockIdx.x) - b * p.blocks;
     share = p.heads[0].share;
-    tiles = item_tiles<KEYS>(seq_len(p, b));
+    tiles = item_tiles<kKeys>(seq_len(p, b));
     start = 0;
-    for (int i = lane; i < b; i += 32) start += item_tiles<KEYS>(seq_len(p, i)) * p.blocks;
+    for (int i = lane; i < b; i += 32) start += item_tiles<kKeys>(seq_len(p, i)) * p.blocks;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) start += __shfl_xor_sync(kFull, start, d);
     start += tiles * block;
@@ -475,11 +467,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
   if (first == last) return;                  // whole: written by its CTA (also an item that begins at the border)
   const int pieces = last - first + 1;
   const int row = blockIdx.y * kJoinRows + warp / kShare;
-  const bool live = row < min(p.ctas * kRows, p.rows - block * p.ctas * kRows);
+  const bool live = row < min(kRows, p.rows - block * kRows);
   // piece 0 is the last segment of range `first` unless the range begins with it
   const int lead = start != first * share ? 1 : 0;
   auto piece_row = [&](int i) {
-    return int64_t(2 * ((first + i) * p.ctas + row / kRows) + (i == 0 ? lead : 0)) * kRows + row % kRows;
+    return int64_t(2 * (first + i) + (i == 0 ? lead : 0)) * kRows + row;
   };
   constexpr int kPer = (kMlaDecodeMaxGrid + 31) / 32;
   float w[kPer];                              // the weights of pieces lane, lane + 32, ...
@@ -528,7 +520,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
       }
   }
   if (!live) return;
-  const int64_t at = int64_t(b) * p.rows + block * p.ctas * kRows + row;
+  const int64_t at = int64_t(b) * p.rows + block * kRows + row;
   if (lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -641,10 +633,13 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
     // items by the borders that cut them, a warp a row.
     const int most = std::min(kRows * ctas, rows);
     const bool by_item = items * 4 <= ranges;
-    const dim3 blocks = by_item ? dim3(int(items), (most + 1) / 2) : dim3(ranges - 1, (most + 7) / 8);
-    auto join = by_item ? (pair ? join_kernel<T, true, pair::kKeys> : join_kernel<T, true, kKeys>)
-                        : (pair ? join_kernel<T, false, pair::kKeys> : join_kernel<T, false, kKeys>);
-    err = launch_kernel(join, blocks, dim3(kJoinThreads), 0, st, false, p);
+    const int across = by_item ? int(items) : ranges - 1;
+    if (pair)  // a task is eight rows x 128 values
+      err = launch_kernel(by_item ? join_pair_kernel<T, true> : join_pair_kernel<T, false>,
+                          dim3(across, by_item ? (most + 7) / 8 * 4 : (most + 7) / 8), dim3(kPairJoinThreads), 0, st, false, p);
+    else
+      err = launch_kernel(by_item ? join_kernel<T, true> : join_kernel<T, false>,
+                          dim3(across, by_item ? (most + 1) / 2 : (most + 7) / 8), dim3(kJoinThreads), 0, st, false, p);
   }
   if (err != cudaSuccess) {
     set_error_detail("mla_decode launch: %s", cudaGetErrorString(err));

@@ -62,7 +62,6 @@ struct Control {
   uint32_t tmem, pad;
   WaitCtl wait;
   float part[4][kRows];                       // per row: maxima, later sums, of the four quarters of a tile's keys
-  float col[kRows];                           // per row: factor of the epilogue
 };
 static_assert(sizeof(Control) <= kCtrl && kSmem <= 232448, "shared memory");
 }  // namespace pair
@@ -75,6 +74,12 @@ bool encode_values(CUtensorMap* m, const void* base, int64_t rows) {
   const int64_t dims[4] = {64, rows, 4, 2}, strides[3] = {2 * kRow, 128, 512};
   const int box[4] = {64, 8, 2, 2};
   return encode_map(m, Elem<T>::kMap, 4, base, dims, strides, box);
+}
+
+// Place of four values of a partial row (floats): row r of 64, values 256
+// half + 128 upper + 4 q .. + 3.  32 rows' pieces of 16 bytes are contiguous.
+__device__ __forceinline__ int part_offset(int r, int half, int upper, int q) {
+  return (((half * 32 + q) * 4 + 2 * upper + (r >> 5)) * 32 + (r & 31)) * 4;
 }
 
 template <typename T>
@@ -347,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         if (!first) {
           wait(bar(ctl->pv_done), (g - 1) & 1u);
           ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
             uint32_t o[32];
             ptx::tmem_ld_32x32b_x32(tmem + lanes + 128 * half + c, o);
@@ -398,54 +403,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         ctl->part[who][r] = l;                // the maxima have been read
         bar_sync(2, kSoftmaxThreads);
         const float sum = (ctl->part[0][r] + ctl->part[1][r]) + (ctl->part[2][r] + ctl->part[3][r]);
-        if (who == 0) {
-          ctl->col[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (who == 0 && r < rows) {
           const float e = sum == 0.0f ? -INFINITY : m + log2f(sum);
-          if (r < rows) (whole ? p.lse : p.part_lse)[row0 + r] = whole ? e * kLn2 : e;
+          (whole ? p.lse : p.part_lse)[row0 + r] = whole ? e * kLn2 : e;
         }
-        const bool empty = bar_any(2, kSoftmaxThreads, sum == 0.0f);  // some row saw no key
+        const bool empty = __any_sync(kFull, sum == 0.0f);  // some row saw no key
         wait(bar(ctl->pv_done), g & 1u);
         ptx::tc_fence_after();
-        // This warp's 32 lanes x 128 columns in pieces of 16 lanes x 16 columns:
-        // a thread gets two neighbouring values of rows q and q + 8, so that a
-        // row's stores fill whole sectors.
+        // Columns 32 c .. of half `half` are values 256 half + 128 upper + 32 c ...
+        // Not unrolled here and where else code runs once an item: its
+        // instructions come from L2 each time (unrolled, 5 us an item).
+        const uint32_t stage = base + kPOff + warp * 2048;  // P is free until the next tile's vote
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          ptx::tmem_ld_32x32b_x32(tmem + lanes + 128 * half + 32 * c, o);
+          ptx::tmem_ld_wait();
 #pragma unroll
-        for (int hl = 0; hl < 2; ++hl) {
-          const int q = 32 * (quarter & 1) + 16 * hl + (lane >> 2), c = lane & 3;
-          const float f0 = ctl->col[q], f1 = ctl->col[q + 8];
-          const int dim0 = 256 * half + 128 * upper;
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          if (empty) {                        // zeros, also where masked values were not finite
 #pragma unroll
-          for (int v = 0; v < 128; v += 32) {
-            uint32_t o[16];
-            tmem_ld_16x256b_x4(tmem + lanes + (uint32_t(16 * hl) << 16) + 128 * half + v, o);
-            ptx::tmem_ld_wait();
+            for (int i = 0; i < 32; ++i)
+              if (sum == 0.0f) o[i] = 0u;
+          }
+          if (whole) {
+            // a row's 64 bytes through shared memory, so that a store covers 8 rows' whole sectors
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float f = i & 2 ? f1 : f0;
-              o[i] = empty && f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * f);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = Elem<T>::pack(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+              ptx::sts128(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
             }
+            __syncwarp();
+            T* out = reinterpret_cast<T*>(p.out) + row0 * kLatent + 256 * half + 128 * upper + 32 * c + 8 * (lane & 3);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {     // row q, then q + 8
-              const int row = q + 8 * h;
-              if (whole) {
-                T* out = reinterpret_cast<T*>(p.out) + (row0 + row) * kLatent + dim0 + v;
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                  // two pieces of 8 columns: even threads take four values of the first, odd ones of the second
-                  const uint32_t w0 = Elem<T>::pack(__uint_as_float(o[4 * i + 2 * h]), __uint_as_float(o[4 * i + 2 * h + 1]));
-                  const uint32_t w1 = Elem<T>::pack(__uint_as_float(o[4 * i + 4 + 2 * h]), __uint_as_float(o[4 * i + 5 + 2 * h]));
-                  const uint32_t got = __shfl_xor_sync(kFull, c & 1 ? w0 : w1, 1);
-                  if (row < rows)
-                    *reinterpret_cast<uint2*>(out + 8 * (i + (c & 1)) + 4 * (c >> 1)) =
-                        c & 1 ? make_uint2(got, w1) : make_uint2(w0, got);
-                }
-              } else if (row < rows) {
-                float* out = p.part_o + (row0 + row) * kLatent + dim0 + v;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  *reinterpret_cast<uint2*>(out + 8 * i + 2 * c) = make_uint2(o[4 * i + 2 * h], o[4 * i + 2 * h + 1]);
-              }
+            for (int k = 0; k < 4; ++k) {
+              const int q = 8 * k + (lane >> 2), row = 32 * (quarter & 1) + q;
+              const uint4 w = ptx::lds128(stage + q * 64 + (((lane & 3) ^ ((q >> 1) & 3)) << 4));
+              if (row < rows) *reinterpret_cast<uint4*>(out + int64_t(row) * kLatent) = w;
             }
+            __syncwarp();
+          } else {
+            // partial rows stay in the order of tensor memory (part_offset), 512 bytes a store
+            float* out = p.part_o + part * kRows * kLatent;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(out + part_offset(r, half, upper, 8 * c + i)) =
+                  make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
         ptx::tc_fence_before();
@@ -465,6 +472,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   ptx::tc_fence_after();
   if (warp == kIssuer) ptx::tmem_dealloc_pair(tmem, kTmemCols);
   ptx::cluster_sync();
+}
+
+// Joins the pair kernel's partial results (see join_kernel).  A warp takes
+// eight rows and 128 values: lane l row l % 8 and every fourth piece of four
+// values, so that loads cover 128 contiguous bytes and stores whole sectors.
+// BY_ITEM: block (item, .), four warps share the pieces of the ranges.
+constexpr int kPairJoinThreads = 128;
+template <typename T, bool BY_ITEM>
+__global__ void __launch_bounds__(kPairJoinThreads) join_pair_kernel(const DecodeParams p) {
+  __shared__ float4 s_sum[BY_ITEM ? 3 : 1][8][32];
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int start, tiles, share, b, block;
+  if (BY_ITEM) {
+    b = int(blockIdx.x) / p.blocks;
+    block = int(blockIdx.x) - b * p.blocks;
+    share = p.heads[0].share;
+    tiles = item_tiles<pair::kKeys>(seq_len(p, b));
+    start = 0;
+    for (int i = lane; i < b; i += 32) start += item_tiles<pair::kKeys>(seq_len(p, i)) * p.blocks;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) start += __shfl_xor_sync(kFull, start, d);
+    start += tiles * block;
+  } else {
+    const Head h = p.heads[blockIdx.x + 1];
+    start = h.start, tiles = h.tiles, share = h.share, b = h.b, block = h.block;
+    // no item, or one that an earlier border cuts first
+    if (tiles == 0 || start < int(blockIdx.x) * share) return;
+  }
+  const int first = start / share, last = (start + tiles - 1) / share;
+  if (first == last) return;                  // whole: written by its pair
+  const int pieces = last - first + 1, lead = start != first * share ? 1 : 0;
+  // 16 groups of eight rows x four blocks of 128 values: blockIdx.y, and the warp where it has no pieces of its own
+  const int task = BY_ITEM ? blockIdx.y : blockIdx.y * 4 + warp;
+  const int row = (task >> 2) * 8 + (lane & 7), half = (task >> 1) & 1, upper = task & 1, q0 = lane >> 3;
+  const int rows = p.rows - block * 2 * kRows;  // of the item
+  if ((task >> 2) * 8 >= rows) return;        // the same for all warps that share a row
+  const int cta = row >> 6, r = row & 63;
+  auto slot = [&](int i) { return int64_t(2 * (2 * (first + i) + cta) + (i == 0 ? lead : 0)); };
+  float top = -INFINITY, sum = 0.0f;
+  const bool live = row < rows;
+  if (live) {
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.part_lse[slot(i) * kRows + r]);
+  }
+  const float ref = top == -INFINITY ? 0.0f : top;
+  if (live) {
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) sum += exp2_approx(p.part_lse[slot(i) * kRows + r] - ref);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  float4 acc[8] = {};
+  if (live) {
+#pragma unroll 2
+    for (int i = BY_ITEM ? warp : 0; i < pieces; i += BY_ITEM ? 4 : 1) {
+      const float a = exp2_approx(p.part_lse[slot(i) * kRows + r] - ref) * inv;
+      const float* at = p.part_o + slot(i) * kRows * kLatent;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 o = *reinterpret_cast<const float4*>(at + part_offset(r, half, upper, 4 * k + q0));
+        acc[k].x += a * o.x, acc[k].y += a * o.y, acc[k].z += a * o.z, acc[k].w += a * o.w;
+      }
+    }
+  }
+  if (BY_ITEM) {
+    if (warp) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s_sum[warp - 1][k][lane] = acc[k];
+    }
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 o = s_sum[i][k][lane];
+        acc[k].x += o.x, acc[k].y += o.y, acc[k].z += o.z, acc[k].w += o.w;
+      }
+  }
+  if (!live) return;
+  const int64_t at = int64_t(b) * p.rows + block * 2 * kRows + row;
+  if ((task & 3) == 0 && q0 == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<uint2*>(p.out + 2 * (at * kLatent + 256 * half + 128 * upper + 4 * (4 * k + q0))) =
+        make_uint2(Elem<T>::pack(acc[k].x, acc[k].y), Elem<T>::pack(acc[k].z, acc[k].w));
 }
 
 }  // namespace

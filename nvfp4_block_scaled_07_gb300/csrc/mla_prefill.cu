@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(kFull, wait_phase<false>(bar(ctl->pv_done[t]), (j - 1) & 1u, wctl));
           if (!ok) break;
           ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kValueDim; c += 16) {
             uint32_t o[16];
             tmem_ld_32x32b_x16(o_col + c, o);
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* out = p.out + 2 * (((int64_t(at_q) + index) * p.H + head) * kValueDim);
       // a row that saw no key gets zeros, also where masked values were not finite
       const bool zero = __any_sync(kFull, l == 0.0f);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 4; ++c) {           // a row's 256 bytes, 16 at a time
         uint32_t o[32];
         if (n[t]) {

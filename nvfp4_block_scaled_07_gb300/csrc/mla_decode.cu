@@ -563,18 +563,18 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
                      a.B, a.Sq * a.H, (long long)a.max_pages * a.page);
     return NVFP4MOE_ERR_UNSUPPORTED;
   }
-  CUtensorMap q_map, kv_map;
   const int rows = a.Sq * a.H;
-  if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
-      !encode_rows<T>(&kv_map, a.cache, int64_t(a.num_pages) * a.page, 8, 9)) {
-    set_error_detail("cuTensorMapEncodeTiled failed or is unavailable");
-    return NVFP4MOE_ERR_CUDA;
-  }
   // A pair of CTAs shares each tile between 128 rows, in the time that one CTA
   // needs for 64: from 65 rows on it halves the passes over the cache (128
   // sequences x 128 heads: PAIRMEAS).  With at most 64 rows half of its rows would be
   // padding, for no gain (32 x 64 heads: PAIRMEAS2).
   const bool pair = rows > kRows;
+  CUtensorMap q_map, kv_map;
+  if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
+      !encode_rows<T>(&kv_map, a.cache, int64_t(a.num_pages) * a.page, pair ? std::min(a.page, 32) : 8, pair ? 1 : 9)) {
+    set_error_detail("cuTensorMapEncodeTiled failed or is unavailable");
+    return NVFP4MOE_ERR_CUDA;
+  }
   const int ctas = pair ? 2 : 1;
   int most_ranges = std::min(num_sms, kMlaDecodeMaxGrid);
   if (pair) {

@@ -15,9 +15,11 @@
 // stages would read Q twice as often (measured 187 us against PAIR128 for
 // 128 sequences x 128 heads).
 // A CTA's share of a tile is 72 KB for S and 64 KB for P V (its own keys'
-// values twice, so that both CTAs use the same descriptors).  S frees its
-// rows while the softmax and P V of the tile still run, so that S is always a
-// tile ahead.
+// values twice, so that both CTAs use the same descriptors), one tile at a
+// time but in parts: S frees its rows three chunks of 64 values at a time, P V
+// its values 16 keys at a time, and both start on parts (waiting for whole
+// tiles took 4000 cycles a tile).  S is up to a tile ahead of P V and covers
+// the softmax.
 //
 // Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-11
 // TMA producers, warp 12 tensor-memory owner and, in the even CTA, issuer of
@@ -44,7 +46,9 @@ constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256, kSCols = 64;  // S buffers after the 256 columns of O
 constexpr int kQBytes = 64 * 2 * kRow;
-constexpr int kKBytes = 8 * kGroup;           // 64 keys
+constexpr int kKChunk = 64 * 128;             // 64 keys x 64 values
+constexpr int kKParts = 3;                    // of a tile's rows: three chunks each, freed one by one
+constexpr int kKBytes = 9 * kKChunk;
 constexpr int kVGroup = 4 * 1024;             // 8 keys: four atoms (two of each half of the values)
 constexpr int kVBytes = 16 * kVGroup;         // 128 keys
 constexpr int kPBytes = 64 * 128;             // 64 rows x 64 keys
@@ -57,8 +61,8 @@ constexpr int kSmem = kPOff + 2 * kPBytes;
 
 struct Control {
   // counted in the even CTA only: k_full, q_full, s_free, p_full, o_free
-  uint64_t k_full, v_full, k_empty, v_empty[kPieces];
-  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
+  uint64_t k_full[kKParts], k_empty[kKParts], v_full[2], v_empty[kPieces];  // v_full, p_full: halves of 64 keys
+  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full[2], pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
   float part[4][kRows];                       // per row: maxima, later sums, of the four quarters of a tile's keys
@@ -84,7 +88,7 @@ __device__ __forceinline__ int part_offset(int r, int half, int upper, int q) {
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
-    decode_pair_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
+    decode_pair_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, const DecodeParams p) {
   using namespace pair;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -97,15 +101,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bar(ctl->k_full), 2);
-    ptx::mbar_init(bar(ctl->v_full), 2);
-    ptx::mbar_init(bar(ctl->k_empty), 1);
+    for (int i = 0; i < kKParts; ++i) {
+      ptx::mbar_init(bar(ctl->k_full[i]), 2);
+      ptx::mbar_init(bar(ctl->k_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(ctl->v_full[i]), 1);
+      ptx::mbar_init(bar(ctl->p_full[i]), kSoftmaxThreads / 32);  // half of each CTA's warps
+    }
     for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[i]), 1);
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
     ptx::mbar_init(bar(ctl->s_full[0]), 1);
     ptx::mbar_init(bar(ctl->s_full[1]), 1);
-    ptx::mbar_init(bar(ctl->p_full), 2 * kSoftmaxThreads / 32);
     ptx::mbar_init(bar(ctl->pv_done), 1);
     ptx::mbar_init(bar(ctl->o_free), 2 * kSoftmaxThreads / 32);
     ptx::mbar_init(bar(ctl->s_free[0]), 2 * kSoftmaxThreads / 32);
@@ -118,7 +126,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   }
   if (warp == kProducer && lane == 0) {
     ptx::prefetch_tmap(&q_map);
-    ptx::prefetch_tmap(&kv_map);
+    ptx::prefetch_tmap(&k_map);
     ptx::prefetch_tmap(&v_map);
   }
   if (warp == kIssuer) {
@@ -160,8 +168,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         for (int b = lane; b < p.B; b += 32)
           if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
       const int piece0 = 4 * int(rank) + 2 * sub;  // the warp's two pieces, one looked up by even lanes, one by odd
-      const uint32_t kf = ptx::mapa(bar(ctl->k_full), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
-      const uint32_t dst = base + kKOff + 4 * sub * kGroup;
+      const uint32_t kf0 = ptx::mapa(bar(ctl->k_full[0]), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
+      const uint32_t dst = base + kKOff + sub * (kKChunk / 2);
+      const int box = min(p.page, 32);        // keys of a copy
+      uint32_t done = 0;                      // parts begun
       uint32_t seg = 0;
       int row = cur.valid() ? look_up(cur, piece0 + (lane & 1)) : 0;
       while (cur.valid()) {
@@ -174,20 +184,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                              cur.b * p.rows + (2 * cur.block + int(rank)) * kRows, c);
           ++seg;
         }
-        const int groups = (max(cur.keys(), 0) + 7) / 8;  // of 8 keys, in the tile
         Cursor<kKeys> nxt = cur;
         nxt.next(p);
         const int next = nxt.valid() ? look_up(nxt, piece0 + (lane & 1)) : 0;
-        if (!wait_warp(bar(ctl->k_empty), (g & 1u) ^ 1u, wctl)) break;
-        // both CTAs' groups 4 sub .. 4 sub + 3 of their eight
-        const int mine = min(4, max(0, groups - 4 * sub)), theirs = min(4, max(0, groups - 8 - 4 * sub));
-        arrive_expect_tx(el0, bar(ctl->k_full), uint32_t((mine + theirs) * kGroup));
+        // both CTAs' keys 32 sub .. of their 64, in whole copies of `box` keys
+        const int mine = min(32, max(0, (cur.keys() - 32 * sub + box - 1) / box * box));
+        const int theirs = min(32, max(0, (cur.keys() - 64 - 32 * sub + box - 1) / box * box));
         const int n = rank ? theirs : mine;
+        const int from0 = __shfl_sync(kFull, row, 0), from1 = __shfl_sync(kFull, row, 1);
+        bool ok = true;
+#pragma unroll 1
+        for (int part = 0; part < kKParts; ++part) {
+          if (!wait_warp(bar(ctl->k_empty[part]), (g & 1u) ^ 1u, wctl)) {
+            ok = false;
+            break;
+          }
+          ++done;
+          arrive_expect_tx(el0, bar(ctl->k_full[part]), uint32_t(3 * 128 * (mine + theirs)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int from = __shfl_sync(kFull, row, i >> 1);
-          if (i < n) tma_load_3d_pair(el, dst + i * kGroup, &kv_map, kf, 0, min(from, oob - 8 * (i & 1)) + 8 * (i & 1), 0);
+          for (int c = 0; c < 3; ++c) {
+            const int chunk = 3 * part + c;
+            if (n > 0) tma_load_3d_pair(el, dst + chunk * kKChunk, &k_map, kf0 + 8 * part, 0, from0, chunk);
+            if (box == 16 && n > 16)
+              tma_load_3d_pair(el, dst + chunk * kKChunk + 16 * 128, &k_map, kf0 + 8 * part, 0, from1, chunk);
+          }
         }
+        if (!ok) break;
         ++g;
         cur = nxt;
         row = next;
@@ -204,7 +226,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       // Every copy has landed before the pair leaves: the even CTA's barriers
       // count both CTAs' (bounded, since an abort may leave a phase incomplete).
       if (rank == 0 && seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
-      if (rank == 0 && g) drain_phase(bar(ctl->k_full), (g - 1) & 1u);
+      for (uint32_t i = 0; i < kKParts; ++i) {
+        const uint32_t n = (done + kKParts - 1 - i) / kKParts;
+        if (rank == 0 && n) drain_phase(bar(ctl->k_full[i]), (n - 1) & 1u);
+      }
     } else {
       bool ok = true;
       int row = cur.valid() ? look_up(cur, 4 * sub + (lane & 3)) : 0;  // of the warp's four pieces
@@ -213,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         Cursor<kKeys> nxt = cur;
         nxt.next(p);
         const int next = nxt.valid() ? look_up(nxt, 4 * sub + (lane & 3)) : 0;
-        const uint32_t vf = bar(ctl->v_full);
+        const uint32_t vf = bar(ctl->v_full[sub]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int piece = 4 * sub + i, from = __shfl_sync(kFull, row, i);
@@ -232,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         cur = nxt;
         row = next;
       }
-      if (g) drain_phase(bar(ctl->v_full), (g - 1) & 1u);
+      if (g) drain_phase(bar(ctl->v_full[sub]), (g - 1) & 1u);
     }
     __syncwarp();
   } else if (warp >= kIssuer) {
@@ -246,16 +271,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
         const uint32_t s = g & 1u;
         if (cur.is_first() && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
-        if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl) || !wait_warp(bar(ctl->k_full), g & 1u, wctl)) break;
-        ptx::tc_fence_after();
-        const uint64_t b = desc_sw128(base + kKOff, 16, kGroup);
+        if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
+        const uint64_t b = desc_sw128(base + kKOff, 16, 1024);
+        bool ok = true;
 #pragma unroll
-        for (int c = 0; c < 9; ++c)
+        for (int part = 0; part < kKParts; ++part) {
+          ok = ok && wait_warp(bar(ctl->k_full[part]), g & 1u, wctl);
+          if (!ok) break;
+          ptx::tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
-                         idesc, c + k > 0);
-        tc_commit_pair(el, bar(ctl->k_empty));
+          for (int c = 3 * part; c < 3 * part + 3; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (kKChunk >> 4) + 2 * k,
+                           idesc, c + k > 0);
+          tc_commit_pair(el, bar(ctl->k_empty[part]));
+        }
+        if (!ok) break;
         tc_commit_pair(el, bar(ctl->s_full[s]));
         if (cur.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
         cur.next(p);
@@ -264,19 +296,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, 256, false, true);
       const uint64_t a = desc_sw128(base + kPOff, 16, 1024), b = desc_sw128(base + kVOff, 1024, kVGroup);
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
-        if (!wait_warp(bar(ctl->p_full), g & 1u, wctl)) break;
         // the previous segment's accumulator has been read
         if (cur.is_first() && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
-        ptx::tc_fence_after();
         const uint32_t more = cur.is_first() ? 0u : 1u;
+        bool ok = true;
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
+          if ((k & 3) == 0) {
+            ok = ok && wait_warp(bar(ctl->p_full[k >> 2]), g & 1u, wctl);
+            if (!ok) break;
+            ptx::tc_fence_after();
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h)         // 256 values
             mma_f16_pair(el, tmem + 128 * h, a + (k >> 2) * (kPBytes >> 4) + 2 * (k & 3), b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
                          k ? 1u : more);
           tc_commit_pair(el, bar(ctl->v_empty[k]));
         }
+        if (!ok) break;
         tc_commit_pair(el, bar(ctl->pv_done));
         cur.next(p);
       }
@@ -305,7 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const int quarter = warp & 3, half = warp >> 2, upper = quarter >> 1;
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
     const int r = 32 * (quarter & 1) + lane, key0 = 64 * upper + 32 * half, who = 2 * upper + half;
-    const uint32_t p_full = ptx::mapa(bar(ctl->p_full), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
+    const uint32_t p_full = ptx::mapa(bar(ctl->p_full[upper]), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
     const uint32_t s_free = ptx::mapa(bar(ctl->s_free[0]), 0);
     float m = 0.0f, l = 0.0f;                 // running maximum (log2 domain) and this quarter's sum
     uint32_t g = 0;
@@ -379,13 +416,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       // Rows of the tile past the last key may hold anything, and 0 * NaN is
       // NaN: they are zeroed, once the tile's values have landed, before the
       // second product reads them.
-      wait(bar(ctl->v_full), g & 1u);
-      if (keys < kKeys) {
-        const int from = max(keys, 0);
-        const uint32_t v = base + kVOff;
-        for (int i = threadIdx.x; i < (kKeys - from) * 32; i += kSoftmaxThreads) {
+      // A half's four warps zero their own keys.
+      wait(bar(ctl->v_full[upper]), g & 1u);
+      if (keys < 64 * (upper + 1)) {
+        const int from = max(keys, 64 * upper);
+        for (int i = 64 * half + 32 * (quarter & 1) + lane; i < (64 * (upper + 1) - from) * 32; i += 128) {
           const int k = from + (i >> 5);      // 32 pieces of 16 bytes a key: eight in each of four atoms
-          ptx::sts128(v + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
+          ptx::sts128(base + kVOff + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
         }
       }
       // What the arrival announces lies in this CTA: weights and zeros in its

@@ -61,8 +61,8 @@ constexpr int kSmem = kPOff + 2 * kPBytes;
 
 struct Control {
   // counted in the even CTA only: k_full, q_full, s_free, p_full, o_free
-  uint64_t k_full[kKParts], k_empty[kKParts], v_full[2], v_empty[kPieces];  // v_full, p_full: halves of 64 keys
-  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full[2], pv_done, o_free, drain;
+  uint64_t k_full[kKParts], k_empty[kKParts], v_full[2], v_empty[kPieces];  // v_full, p_full, pv_done: halves of 64 keys
+  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full[2], pv_done[2], o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
   float part[4][kRows];                       // per row: maxima, later sums, of the four quarters of a tile's keys
@@ -107,6 +107,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(ctl->v_full[i]), 1);
+      ptx::mbar_init(bar(ctl->pv_done[i]), 1);
       ptx::mbar_init(bar(ctl->p_full[i]), kSoftmaxThreads / 32);  // half of each CTA's warps
     }
     for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[i]), 1);
@@ -114,7 +115,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     ptx::mbar_init(bar(ctl->q_empty), 1);
     ptx::mbar_init(bar(ctl->s_full[0]), 1);
     ptx::mbar_init(bar(ctl->s_full[1]), 1);
-    ptx::mbar_init(bar(ctl->pv_done), 1);
     ptx::mbar_init(bar(ctl->o_free), 2 * kSoftmaxThreads / 32);
     ptx::mbar_init(bar(ctl->s_free[0]), 2 * kSoftmaxThreads / 32);
     ptx::mbar_init(bar(ctl->s_free[1]), 2 * kSoftmaxThreads / 32);
@@ -153,11 +153,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const bool rows_role = warp < kProducer + 2;
     const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0u;  // the even CTA tells its barriers what to expect
     const int oob = p.num_pages * p.page;
-    // First cache row of piece `piece` (16 keys) of the cursor's tile.
-    auto look_up = [&](const Cursor<kKeys>& c, int piece) {
+    // First cache row of piece `piece` (16 keys) of the cursor's tile, in two
+    // steps: the page's load, and, after the copies of the tile before it,
+    // what is made of it.  A warp that uses the page at once waits 1000 cycles
+    // for it every tile.
+    auto page_of = [&](const Cursor<kKeys>& c, int piece) {
       const int row = c.tile * kKeys + 16 * piece;
-      if (row >= c.len) return oob;
-      const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
+      return c.valid() && row < c.len ? __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page)) : 0;
+    };
+    auto row_of = [&](const Cursor<kKeys>& c, int piece, int id) {
+      asm volatile("" : "+r"(id)::"memory");  // not before this point
+      const int row = c.tile * kKeys + 16 * piece;
+      if (!c.valid() || row >= c.len) return oob;
       if (id >= 0 && id < p.num_pages) return id * p.page + (row & (p.page - 1));
       atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
       return oob;
@@ -173,7 +180,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const int box = min(p.page, 32);        // keys of a copy
       uint32_t done = 0;                      // parts begun
       uint32_t seg = 0;
-      int row = cur.valid() ? look_up(cur, piece0 + (lane & 1)) : 0;
+      const int piece = piece0 + (lane & 1);
+      int row = row_of(cur, piece, page_of(cur, piece));
       while (cur.valid()) {
         if (sub == 0 && cur.is_first()) {
           if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
@@ -186,7 +194,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         }
         Cursor<kKeys> nxt = cur;
         nxt.next(p);
-        const int next = nxt.valid() ? look_up(nxt, piece0 + (lane & 1)) : 0;
+        const int next = page_of(nxt, piece);
         // both CTAs' keys 32 sub .. of their 64, in whole copies of `box` keys
         const int mine = min(32, max(0, (cur.keys() - 32 * sub + box - 1) / box * box));
         const int theirs = min(32, max(0, (cur.keys() - 64 - 32 * sub + box - 1) / box * box));
@@ -212,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         if (!ok) break;
         ++g;
         cur = nxt;
-        row = next;
+        row = row_of(cur, piece, next);
         if (cur.valid()) {                    // the next rows are requested into L2 while their buffers are in use
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -232,12 +240,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       }
     } else {
       bool ok = true;
-      int row = cur.valid() ? look_up(cur, 4 * sub + (lane & 3)) : 0;  // of the warp's four pieces
+      const int lane_piece = 4 * sub + (lane & 3);  // the warp's four pieces, one a lane
+      int row = row_of(cur, lane_piece, page_of(cur, lane_piece));
       while (ok && cur.valid()) {
         const int groups = (max(cur.keys(), 0) + 7) / 8;
         Cursor<kKeys> nxt = cur;
         nxt.next(p);
-        const int next = nxt.valid() ? look_up(nxt, 4 * sub + (lane & 3)) : 0;
+        const int next = page_of(nxt, lane_piece);
         const uint32_t vf = bar(ctl->v_full[sub]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -255,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           if (i == 3) ++g;
         }
         cur = nxt;
-        row = next;
+        row = row_of(cur, lane_piece, next);
       }
       if (g) drain_phase(bar(ctl->v_full[sub]), (g - 1) & 1u);
     }
@@ -272,22 +281,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         const uint32_t s = g & 1u;
         if (cur.is_first() && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
         if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
+        // Waits leave the loop directly: a condition carried over the parts
+        // made the compiler issue each MMA as divergent code (100 cycles).
         const uint64_t b = desc_sw128(base + kKOff, 16, 1024);
-        bool ok = true;
-#pragma unroll
-        for (int part = 0; part < kKParts; ++part) {
-          ok = ok && wait_warp(bar(ctl->k_full[part]), g & 1u, wctl);
-          if (!ok) break;
+        auto part = [&](int i) {
           ptx::tc_fence_after();
 #pragma unroll
-          for (int c = 3 * part; c < 3 * part + 3; ++c)
+          for (int c = 3 * i; c < 3 * i + 3; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (kKChunk >> 4) + 2 * k,
                            idesc, c + k > 0);
-          tc_commit_pair(el, bar(ctl->k_empty[part]));
-        }
-        if (!ok) break;
+          tc_commit_pair(el, bar(ctl->k_empty[i]));
+        };
+        static_assert(kKParts == 3, "parts of S");
+        if (!wait_warp(bar(ctl->k_full[0]), g & 1u, wctl)) break;
+        part(0);
+        if (!wait_warp(bar(ctl->k_full[1]), g & 1u, wctl)) break;
+        part(1);
+        if (!wait_warp(bar(ctl->k_full[2]), g & 1u, wctl)) break;
+        part(2);
         tc_commit_pair(el, bar(ctl->s_full[s]));
         if (cur.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
         cur.next(p);
@@ -299,22 +312,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         // the previous segment's accumulator has been read
         if (cur.is_first() && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
         const uint32_t more = cur.is_first() ? 0u : 1u;
-        bool ok = true;
+        auto keys64 = [&](int i) {            // 64 keys
+          ptx::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
-          if ((k & 3) == 0) {
-            ok = ok && wait_warp(bar(ctl->p_full[k >> 2]), g & 1u, wctl);
-            if (!ok) break;
-            ptx::tc_fence_after();
+          for (int k = 4 * i; k < 4 * i + 4; ++k) {  // 16 keys: 32 bytes of P, two groups of values
+#pragma unroll
+            for (int h = 0; h < 2; ++h)       // 256 values
+              mma_f16_pair(el, tmem + 128 * h, a + i * (kPBytes >> 4) + 2 * (k & 3),
+                           b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc, k ? 1u : more);
+            tc_commit_pair(el, bar(ctl->v_empty[k]));
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)         // 256 values
-            mma_f16_pair(el, tmem + 128 * h, a + (k >> 2) * (kPBytes >> 4) + 2 * (k & 3), b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
-                         k ? 1u : more);
-          tc_commit_pair(el, bar(ctl->v_empty[k]));
-        }
-        if (!ok) break;
-        tc_commit_pair(el, bar(ctl->pv_done));
+          tc_commit_pair(el, bar(ctl->pv_done[i]));
+        };
+        if (!wait_warp(bar(ctl->p_full[0]), g & 1u, wctl)) break;
+        keys64(0);
+        if (!wait_warp(bar(ctl->p_full[1]), g & 1u, wctl)) break;
+        keys64(1);
         cur.next(p);
       }
     }
@@ -387,7 +400,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         l *= a;
         bar_sync(2, kSoftmaxThreads);         // all have read the maxima
         if (!first) {
-          wait(bar(ctl->pv_done), (g - 1) & 1u);
+          wait(bar(ctl->pv_done[0]), (g - 1) & 1u);
+          wait(bar(ctl->pv_done[1]), (g - 1) & 1u);
           ptx::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
@@ -408,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       float l1 = 0.0f;
       weights<T>(s, w, p.scale_log2, neg, l, l1);
       l += l1;
-      if (g) wait(bar(ctl->pv_done), (g - 1) & 1u);  // P is free
+      if (g) wait(bar(ctl->pv_done[upper]), (g - 1) & 1u);  // this half of P is free
       const uint32_t at = base + kPOff + upper * kPBytes + r * 128;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -446,7 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           (whole ? p.lse : p.part_lse)[row0 + r] = whole ? e * kLn2 : e;
         }
         const bool empty = __any_sync(kFull, sum == 0.0f);  // some row saw no key
-        wait(bar(ctl->pv_done), g & 1u);
+        wait(bar(ctl->pv_done[0]), g & 1u);
+        wait(bar(ctl->pv_done[1]), g & 1u);
         ptx::tc_fence_after();
         // Columns 32 c .. of half `half` are values 256 half + 128 upper + 32 c ...
         // Not unrolled here and where else code runs once an item: its

@@ -126,14 +126,30 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
   }
 }
 
-// The same for a whole converged warp: all lanes get one answer.
+// The same for a whole converged warp, whose lanes all get one answer.  The
+// loop itself is uniform: code behind a divergent one would issue its MMAs
+// and copies through per-lane registers, several times slower.
 __device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, ptx::mbar_test_wait(bar, parity) != 0);
 }
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
-  if (test_warp(bar, parity)) return true;
-  return __all_sync(0xFFFFFFFFu, wait_phase<true>(bar, parity, ctl));
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (test_warp(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      const uint64_t now = ptx::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      const bool late = now - t0 > uint64_t(ctl->limit_us) * 1000u;
+      if (__any_sync(0xFFFFFFFFu, late)) {
+        ctl->abort = 1;
+        atomicOr(ctl->flags, kFlagTimeout);
+      }
+      if (__any_sync(0xFFFFFFFFu, late || ctl->abort)) return false;
+    }
+  }
 }
+// A value that is the same in all lanes, said so to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // Wait for a CTA's own copies or MMAs before it leaves, also after an abort.
 __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {

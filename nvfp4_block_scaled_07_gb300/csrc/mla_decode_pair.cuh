@@ -15,11 +15,9 @@
 // stages would read Q twice as often (measured 187 us against PAIR128 for
 // 128 sequences x 128 heads).
 // A CTA's share of a tile is 72 KB for S and 64 KB for P V (its own keys'
-// values twice, so that both CTAs use the same descriptors), one tile at a
-// time but in parts: S frees its rows three chunks of 64 values at a time, P V
-// its values 16 keys at a time, and both start on parts (waiting for whole
-// tiles took 4000 cycles a tile).  S is up to a tile ahead of P V and covers
-// the softmax.
+// values twice, so that both CTAs use the same descriptors).  S frees its
+// rows while the softmax and P V of the tile still run, so that S is always a
+// tile ahead.
 //
 // Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-11
 // TMA producers, warp 12 tensor-memory owner and, in the even CTA, issuer of
@@ -40,15 +38,13 @@ namespace {
 namespace pair {
 constexpr int kKeys = 128;                    // keys of a tile
 constexpr int kPieces = 8;                    // of a tile: 16 keys each
-constexpr int kProducer = 8, kIssuer = 12;    // first producer warp; the MMA warps, S and P V
-constexpr int kThreads = 448;
+constexpr int kProducer = 8, kIssuer = 14;    // first producer warp; the MMA warps, S and P V
+constexpr int kThreads = 512;
 constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256, kSCols = 64;  // S buffers after the 256 columns of O
 constexpr int kQBytes = 64 * 2 * kRow;
-constexpr int kKChunk = 64 * 128;             // 64 keys x 64 values
-constexpr int kKParts = 3;                    // of a tile's rows: three chunks each, freed one by one
-constexpr int kKBytes = 9 * kKChunk;
+constexpr int kKBytes = 8 * kGroup;           // 64 keys
 constexpr int kVGroup = 4 * 1024;             // 8 keys: four atoms (two of each half of the values)
 constexpr int kVBytes = 16 * kVGroup;         // 128 keys
 constexpr int kPBytes = 64 * 128;             // 64 rows x 64 keys
@@ -61,8 +57,8 @@ constexpr int kSmem = kPOff + 2 * kPBytes;
 
 struct Control {
   // counted in the even CTA only: k_full, q_full, s_free, p_full, o_free
-  uint64_t k_full[kKParts], k_empty[kKParts], v_full[2], v_empty[kPieces];  // v_full, p_full, pv_done: halves of 64 keys
-  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full[2], pv_done[2], o_free, drain;
+  uint64_t k_full, v_full, k_empty, v_empty[kPieces];
+  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
   float part[4][kRows];                       // per row: maxima, later sums, of the four quarters of a tile's keys
@@ -88,7 +84,7 @@ __device__ __forceinline__ int part_offset(int r, int half, int upper, int q) {
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
-    decode_pair_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+    decode_pair_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                        const __grid_constant__ CUtensorMap v_map, const DecodeParams p) {
   using namespace pair;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -101,20 +97,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kKParts; ++i) {
-      ptx::mbar_init(bar(ctl->k_full[i]), 2);
-      ptx::mbar_init(bar(ctl->k_empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(ctl->v_full[i]), 1);
-      ptx::mbar_init(bar(ctl->pv_done[i]), 1);
-      ptx::mbar_init(bar(ctl->p_full[i]), kSoftmaxThreads / 32);  // half of each CTA's warps
-    }
+    ptx::mbar_init(bar(ctl->k_full), 2);
+    ptx::mbar_init(bar(ctl->v_full), 4);
+    ptx::mbar_init(bar(ctl->k_empty), 1);
     for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[i]), 1);
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
     ptx::mbar_init(bar(ctl->s_full[0]), 1);
     ptx::mbar_init(bar(ctl->s_full[1]), 1);
+    ptx::mbar_init(bar(ctl->p_full), 2 * kSoftmaxThreads / 32);
+    ptx::mbar_init(bar(ctl->pv_done), 1);
     ptx::mbar_init(bar(ctl->o_free), 2 * kSoftmaxThreads / 32);
     ptx::mbar_init(bar(ctl->s_free[0]), 2 * kSoftmaxThreads / 32);
     ptx::mbar_init(bar(ctl->s_free[1]), 2 * kSoftmaxThreads / 32);
@@ -126,7 +118,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   }
   if (warp == kProducer && lane == 0) {
     ptx::prefetch_tmap(&q_map);
-    ptx::prefetch_tmap(&k_map);
+    ptx::prefetch_tmap(&kv_map);
     ptx::prefetch_tmap(&v_map);
   }
   if (warp == kIssuer) {
@@ -146,25 +138,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 
   if (warp >= kProducer && warp < kIssuer) {
     // ---- producers: two warps copy whole rows (32 of the CTA's 64 keys
-    // each), two copy values (64 of the tile's 128 keys each), so that rows,
+    // each), four copy values (32 of the tile's 128 keys each), so that rows,
     // whose buffers S frees early, never wait behind values.  A tile's pages
     // are looked up while the tile before it waits for its buffers. ----
-    const int sub = (warp - kProducer) & 1;
     const bool rows_role = warp < kProducer + 2;
+    const int sub = rows_role ? warp - kProducer : warp - kProducer - 2;
     const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0u;  // the even CTA tells its barriers what to expect
     const int oob = p.num_pages * p.page;
-    // First cache row of piece `piece` (16 keys) of the cursor's tile, in two
-    // steps: the page's load, and, after the copies of the tile before it,
-    // what is made of it.  A warp that uses the page at once waits 1000 cycles
-    // for it every tile.
-    auto page_of = [&](const Cursor<kKeys>& c, int piece) {
+    // First cache row of piece `piece` (16 keys) of the cursor's tile.
+    auto look_up = [&](const Cursor<kKeys>& c, int piece) {
       const int row = c.tile * kKeys + 16 * piece;
-      return c.valid() && row < c.len ? __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page)) : 0;
-    };
-    auto row_of = [&](const Cursor<kKeys>& c, int piece, int id) {
-      asm volatile("" : "+r"(id)::"memory");  // not before this point
-      const int row = c.tile * kKeys + 16 * piece;
-      if (!c.valid() || row >= c.len) return oob;
+      if (row >= c.len) return oob;
+      const int id = __ldg(p.tables + c.b * p.table_stride + (row >> p.log_page));
       if (id >= 0 && id < p.num_pages) return id * p.page + (row & (p.page - 1));
       atomicOr(&g_decode_flags, kFlagBadData);  // zero rows instead of a page that does not exist
       return oob;
@@ -175,13 +160,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         for (int b = lane; b < p.B; b += 32)
           if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
       const int piece0 = 4 * int(rank) + 2 * sub;  // the warp's two pieces, one looked up by even lanes, one by odd
-      const uint32_t kf0 = ptx::mapa(bar(ctl->k_full[0]), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
-      const uint32_t dst = base + kKOff + sub * (kKChunk / 2);
-      const int box = min(p.page, 32);        // keys of a copy
-      uint32_t done = 0;                      // parts begun
+      const uint32_t kf = ptx::mapa(bar(ctl->k_full), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
+      const uint32_t dst = base + kKOff + 4 * sub * kGroup;
       uint32_t seg = 0;
-      const int piece = piece0 + (lane & 1);
-      int row = row_of(cur, piece, page_of(cur, piece));
+      int row = cur.valid() ? look_up(cur, piece0 + (lane & 1)) : 0;
       while (cur.valid()) {
         if (sub == 0 && cur.is_first()) {
           if (!wait_warp(bar(ctl->q_empty), (seg & 1u) ^ 1u, wctl)) break;
@@ -192,35 +174,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                              cur.b * p.rows + (2 * cur.block + int(rank)) * kRows, c);
           ++seg;
         }
+        const int groups = (max(cur.keys(), 0) + 7) / 8;  // of 8 keys, in the tile
         Cursor<kKeys> nxt = cur;
         nxt.next(p);
-        const int next = page_of(nxt, piece);
-        // both CTAs' keys 32 sub .. of their 64, in whole copies of `box` keys
-        const int mine = min(32, max(0, (cur.keys() - 32 * sub + box - 1) / box * box));
-        const int theirs = min(32, max(0, (cur.keys() - 64 - 32 * sub + box - 1) / box * box));
+        const int next = nxt.valid() ? look_up(nxt, piece0 + (lane & 1)) : 0;
+        if (!wait_warp(bar(ctl->k_empty), (g & 1u) ^ 1u, wctl)) break;
+        // both CTAs' groups 4 sub .. 4 sub + 3 of their eight
+        const int mine = min(4, max(0, groups - 4 * sub)), theirs = min(4, max(0, groups - 8 - 4 * sub));
+        arrive_expect_tx(el0, bar(ctl->k_full), uint32_t((mine + theirs) * kGroup));
         const int n = rank ? theirs : mine;
-        const int from0 = __shfl_sync(kFull, row, 0), from1 = __shfl_sync(kFull, row, 1);
-        bool ok = true;
-#pragma unroll 1
-        for (int part = 0; part < kKParts; ++part) {
-          if (!wait_warp(bar(ctl->k_empty[part]), (g & 1u) ^ 1u, wctl)) {
-            ok = false;
-            break;
-          }
-          ++done;
-          arrive_expect_tx(el0, bar(ctl->k_full[part]), uint32_t(3 * 128 * (mine + theirs)));
 #pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const int chunk = 3 * part + c;
-            if (n > 0) tma_load_3d_pair(el, dst + chunk * kKChunk, &k_map, kf0 + 8 * part, 0, from0, chunk);
-            if (box == 16 && n > 16)
-              tma_load_3d_pair(el, dst + chunk * kKChunk + 16 * 128, &k_map, kf0 + 8 * part, 0, from1, chunk);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int from = __shfl_sync(kFull, row, i >> 1);
+          if (i < n) tma_load_3d_pair(el, dst + i * kGroup, &kv_map, kf, 0, min(from, oob - 8 * (i & 1)) + 8 * (i & 1), 0);
         }
-        if (!ok) break;
         ++g;
         cur = nxt;
-        row = row_of(cur, piece, next);
+        row = next;
         if (cur.valid()) {                    // the next rows are requested into L2 while their buffers are in use
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -234,39 +204,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       // Every copy has landed before the pair leaves: the even CTA's barriers
       // count both CTAs' (bounded, since an abort may leave a phase incomplete).
       if (rank == 0 && seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
-      for (uint32_t i = 0; i < kKParts; ++i) {
-        const uint32_t n = (done + kKParts - 1 - i) / kKParts;
-        if (rank == 0 && n) drain_phase(bar(ctl->k_full[i]), (n - 1) & 1u);
-      }
+      if (rank == 0 && g) drain_phase(bar(ctl->k_full), (g - 1) & 1u);
     } else {
       bool ok = true;
-      const int lane_piece = 4 * sub + (lane & 3);  // the warp's four pieces, one a lane
-      int row = row_of(cur, lane_piece, page_of(cur, lane_piece));
+      const uint32_t vf = bar(ctl->v_full), dst = base + kVOff + 4 * sub * kVGroup;
+      int row = cur.valid() ? look_up(cur, 2 * sub + (lane & 1)) : 0;  // of the warp's two pieces
       while (ok && cur.valid()) {
-        const int groups = (max(cur.keys(), 0) + 7) / 8;
+        const int n = min(4, max(0, (cur.keys() + 7) / 8 - 4 * sub));  // groups of 8 keys
         Cursor<kKeys> nxt = cur;
         nxt.next(p);
-        const int next = page_of(nxt, lane_piece);
-        const uint32_t vf = bar(ctl->v_full[sub]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int piece = 4 * sub + i, from = __shfl_sync(kFull, row, i);
-          // after an abort the other pieces still come: a phase that was begun has to end
-          if (ok) ok = wait_warp(bar(ctl->v_empty[piece]), (g & 1u) ^ 1u, wctl);
-          if (i == 0) {
-            if (!ok) break;
-            arrive_expect_tx(el, vf, uint32_t(min(8, max(0, groups - 8 * sub)) * kVGroup));
-          }
-          const uint32_t dst = base + kVOff + 2 * piece * kVGroup;
-          if (2 * piece < groups) tma_load_4d(el, dst, &v_map, vf, 0, from, 2 * int(rank), 0);
-          if (2 * piece + 1 < groups)
-            tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(from, oob - 8) + 8, 2 * int(rank), 0);
-          if (i == 3) ++g;
-        }
+        const int next = nxt.valid() ? look_up(nxt, 2 * sub + (lane & 1)) : 0;
+        const int from0 = uniform(row), from1 = __shfl_sync(kFull, row, 1);
+        ok = wait_warp(bar(ctl->v_empty[2 * sub]), (g & 1u) ^ 1u, wctl);
+        if (!ok) break;
+        arrive_expect_tx(el, vf, uint32_t(n * kVGroup));
+        ++g;
+        if (n > 0) tma_load_4d(el, dst, &v_map, vf, 0, from0, 2 * int(rank), 0);
+        if (n > 1) tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(from0, oob - 8) + 8, 2 * int(rank), 0);
+        // after an abort the second piece still comes: a phase that was begun has to end
+        ok = wait_warp(bar(ctl->v_empty[2 * sub + 1]), (g & 1u), wctl);
+        if (n > 2) tma_load_4d(el, dst + 2 * kVGroup, &v_map, vf, 0, from1, 2 * int(rank), 0);
+        if (n > 3) tma_load_4d(el, dst + 3 * kVGroup, &v_map, vf, 0, min(from1, oob - 8) + 8, 2 * int(rank), 0);
         cur = nxt;
-        row = row_of(cur, lane_piece, next);
+        row = next;
       }
-      if (g) drain_phase(bar(ctl->v_full[sub]), (g - 1) & 1u);
+      if (g) drain_phase(bar(ctl->v_full), (g - 1) & 1u);
     }
     __syncwarp();
   } else if (warp >= kIssuer) {
@@ -280,27 +242,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
         const uint32_t s = g & 1u;
         if (cur.is_first() && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
-        if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
-        // Waits leave the loop directly: a condition carried over the parts
-        // made the compiler issue each MMA as divergent code (100 cycles).
-        const uint64_t b = desc_sw128(base + kKOff, 16, 1024);
-        auto part = [&](int i) {
-          ptx::tc_fence_after();
+        if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl) || !wait_warp(bar(ctl->k_full), g & 1u, wctl)) break;
+        ptx::tc_fence_after();
+        const uint64_t b = desc_sw128(base + kKOff, 16, kGroup);
 #pragma unroll
-          for (int c = 3 * i; c < 3 * i + 3; ++c)
+        for (int c = 0; c < 9; ++c)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (kKChunk >> 4) + 2 * k,
-                           idesc, c + k > 0);
-          tc_commit_pair(el, bar(ctl->k_empty[i]));
-        };
-        static_assert(kKParts == 3, "parts of S");
-        if (!wait_warp(bar(ctl->k_full[0]), g & 1u, wctl)) break;
-        part(0);
-        if (!wait_warp(bar(ctl->k_full[1]), g & 1u, wctl)) break;
-        part(1);
-        if (!wait_warp(bar(ctl->k_full[2]), g & 1u, wctl)) break;
-        part(2);
+          for (int k = 0; k < 4; ++k)
+            mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
+                         idesc, c + k > 0);
+        tc_commit_pair(el, bar(ctl->k_empty));
         tc_commit_pair(el, bar(ctl->s_full[s]));
         if (cur.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
         cur.next(p);
@@ -309,25 +260,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, 256, false, true);
       const uint64_t a = desc_sw128(base + kPOff, 16, 1024), b = desc_sw128(base + kVOff, 1024, kVGroup);
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
+        if (!wait_warp(bar(ctl->p_full), g & 1u, wctl)) break;
         // the previous segment's accumulator has been read
         if (cur.is_first() && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
+        ptx::tc_fence_after();
         const uint32_t more = cur.is_first() ? 0u : 1u;
-        auto keys64 = [&](int i) {            // 64 keys
-          ptx::tc_fence_after();
 #pragma unroll
-          for (int k = 4 * i; k < 4 * i + 4; ++k) {  // 16 keys: 32 bytes of P, two groups of values
+        for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
 #pragma unroll
-            for (int h = 0; h < 2; ++h)       // 256 values
-              mma_f16_pair(el, tmem + 128 * h, a + i * (kPBytes >> 4) + 2 * (k & 3),
-                           b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc, k ? 1u : more);
-            tc_commit_pair(el, bar(ctl->v_empty[k]));
-          }
-          tc_commit_pair(el, bar(ctl->pv_done[i]));
-        };
-        if (!wait_warp(bar(ctl->p_full[0]), g & 1u, wctl)) break;
-        keys64(0);
-        if (!wait_warp(bar(ctl->p_full[1]), g & 1u, wctl)) break;
-        keys64(1);
+          for (int h = 0; h < 2; ++h)         // 256 values
+            mma_f16_pair(el, tmem + 128 * h, a + (k >> 2) * (kPBytes >> 4) + 2 * (k & 3), b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
+                         k ? 1u : more);
+          tc_commit_pair(el, bar(ctl->v_empty[k]));
+        }
+        tc_commit_pair(el, bar(ctl->pv_done));
         cur.next(p);
       }
     }
@@ -355,7 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const int quarter = warp & 3, half = warp >> 2, upper = quarter >> 1;
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
     const int r = 32 * (quarter & 1) + lane, key0 = 64 * upper + 32 * half, who = 2 * upper + half;
-    const uint32_t p_full = ptx::mapa(bar(ctl->p_full[upper]), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
+    const uint32_t p_full = ptx::mapa(bar(ctl->p_full), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
     const uint32_t s_free = ptx::mapa(bar(ctl->s_free[0]), 0);
     float m = 0.0f, l = 0.0f;                 // running maximum (log2 domain) and this quarter's sum
     uint32_t g = 0;
@@ -400,8 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         l *= a;
         bar_sync(2, kSoftmaxThreads);         // all have read the maxima
         if (!first) {
-          wait(bar(ctl->pv_done[0]), (g - 1) & 1u);
-          wait(bar(ctl->pv_done[1]), (g - 1) & 1u);
+          wait(bar(ctl->pv_done), (g - 1) & 1u);
           ptx::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 128; c += 32) {
@@ -422,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       float l1 = 0.0f;
       weights<T>(s, w, p.scale_log2, neg, l, l1);
       l += l1;
-      if (g) wait(bar(ctl->pv_done[upper]), (g - 1) & 1u);  // this half of P is free
+      if (g) wait(bar(ctl->pv_done), (g - 1) & 1u);  // P is free
       const uint32_t at = base + kPOff + upper * kPBytes + r * 128;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -430,13 +375,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       // Rows of the tile past the last key may hold anything, and 0 * NaN is
       // NaN: they are zeroed, once the tile's values have landed, before the
       // second product reads them.
-      // A half's four warps zero their own keys.
-      wait(bar(ctl->v_full[upper]), g & 1u);
-      if (keys < 64 * (upper + 1)) {
-        const int from = max(keys, 64 * upper);
-        for (int i = 64 * half + 32 * (quarter & 1) + lane; i < (64 * (upper + 1) - from) * 32; i += 128) {
+      wait(bar(ctl->v_full), g & 1u);
+      if (keys < kKeys) {
+        const int from = max(keys, 0);
+        const uint32_t v = base + kVOff;
+        for (int i = threadIdx.x; i < (kKeys - from) * 32; i += kSoftmaxThreads) {
           const int k = from + (i >> 5);      // 32 pieces of 16 bytes a key: eight in each of four atoms
-          ptx::sts128(base + kVOff + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
+          ptx::sts128(v + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
         }
       }
       // What the arrival announces lies in this CTA: weights and zeros in its
@@ -460,8 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           (whole ? p.lse : p.part_lse)[row0 + r] = whole ? e * kLn2 : e;
         }
         const bool empty = __any_sync(kFull, sum == 0.0f);  // some row saw no key
-        wait(bar(ctl->pv_done[0]), g & 1u);
-        wait(bar(ctl->pv_done[1]), g & 1u);
+        wait(bar(ctl->pv_done), g & 1u);
         ptx::tc_fence_after();
         // Columns 32 c .. of half `half` are values 256 half + 128 upper + 32 c ...
         // Not unrolled here and where else code runs once an item: its

@@ -24,8 +24,9 @@
 // partial results (unnormalised rows and their log-sums) in the workspace,
 // which a second kernel joins.
 //
-// Warp roles: warps 0-3 softmax and epilogue, warp 4 TMA producer, warp 5
-// tensor-memory owner and MMA issuer.  Every wait is bounded.
+// Warp roles: warps 0-7 softmax and epilogue, 8-11 TMA producers, warp 12
+// tensor-memory owner and issuer of S, warp 13 issuer of P V.  Every wait is
+// bounded.
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
@@ -48,8 +49,8 @@ constexpr int kChunk = 64 * 128;              // 64 rows x 64 values, 128-byte r
 constexpr int kTile = 9 * kChunk;
 constexpr int kPieces = 4;                    // of a tile: 16 keys each, freed one by one
 constexpr int kStages = 2;
-constexpr int kProducer = 8, kIssuer = 12;    // first producer warp, MMA warp
-constexpr int kThreads = 416;
+constexpr int kProducer = 8, kIssuer = 12;    // first producer warp; the MMA warps, S and P V
+constexpr int kThreads = 448;
 constexpr int kSoftmaxThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;               // S buffers after the 4 x 64 columns of O^T
@@ -63,7 +64,7 @@ constexpr int kSmem = kPOff + kChunk;
 
 struct Control {
   uint64_t full[kStages], empty[kStages][kPieces];
-  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_free, drain;
+  uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
   float half[2][kRows];                       // per row: maxima, later sums, of the two halves of a tile's keys
@@ -95,7 +96,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(bar(ctl->p_full), kSoftmaxThreads);
     ptx::mbar_init(bar(ctl->pv_done), 1);
     ptx::mbar_init(bar(ctl->o_free), kSoftmaxThreads);
-    ptx::mbar_init(bar(ctl->drain), 1);
+    ptx::mbar_init(bar(ctl->s_free[0]), kSoftmaxThreads);
+    ptx::mbar_init(bar(ctl->s_free[1]), kSoftmaxThreads);
+    ptx::mbar_init(bar(ctl->drain), 2);
     ptx::fence_barrier_init();
     ctl->wait.abort = 0;
     ctl->wait.limit_us = p.wait_us;
@@ -176,60 +179,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n) drain_phase(bar(ctl->full[s]), (n - 1) & 1u);
     }
     __syncwarp();
-  } else if (warp == kIssuer) {
-    // ---- MMA issuer ----
+  } else if (warp >= kIssuer) {
+    // ---- MMA issuers: one warp for S, one for P V.  A single one that took
+    // what was ready put an S in front of the P V that frees a buffer in most
+    // rounds (3500 cycles a tile). ----
     const uint32_t el = elect_one();
-    const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
-    uint32_t gs = 0, gp = 0, seg_s = 0, seg_p = 0;  // tiles and segments begun by S and by P V
-    Cursor<kKeys> cs = cur;
-    bool ok = true;
-    // The two tiles in shared memory go through together: S, S, P V, P V.
-    // The softmax of each then runs under an MMA of the other, and the copies
-    // of the next two under both P V.  Issuing whatever was ready instead put
-    // an S in front of the P V that frees a buffer in most rounds (3500
-    // cycles a tile).
-    while (ok && cur.valid()) {
-      for (int i = 0; i < kStages && ok && cs.valid(); ++i) {
-        const uint32_t s = gs & 1u;
-        ok = wait_warp(bar(ctl->full[s]), (gs >> 1) & 1u, wctl);
-        if (ok && cs.is_first()) ok = wait_warp(bar(ctl->q_full), seg_s++ & 1u, wctl);
-        if (!ok) break;
+    const int n = uniform(cur.end - cur.pos);
+    uint32_t seg = 0;
+    if (warp == kIssuer) {
+      const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
+      const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
+      for (int g = 0; g < n; ++g) {
+        const uint32_t s = g & 1u, ph = (g >> 1) & 1u, d = tmem + kSCol + s * kKeys;
+        const bool first = uniform(cur.is_first()), last = uniform(cur.is_last());
+        cur.next(p);
+        if (first && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
+        if (!wait_warp(bar(ctl->s_free[s]), ph ^ 1u, wctl)) break;
+        if (!wait_warp(bar(ctl->full[s]), ph, wctl)) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + kSCol + s * kKeys;
-        const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
         const uint64_t b = desc_sw128(base + kKvOff + s * kTile, 16, kGroup);
 #pragma unroll
         for (int c = 0; c < 9; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16(el, d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc_s, c + k > 0);
+            mma_f16(el, d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc, c + k > 0);
         tc_commit(el, bar(ctl->s_full[s]));
-        if (cs.is_last()) tc_commit(el, bar(ctl->q_empty));
-        cs.next(p);
-        ++gs;
+        if (last) tc_commit(el, bar(ctl->q_empty));
       }
-      while (ok && gp < gs) {
-        const uint32_t s = gp & 1u;
-        ok = wait_warp(bar(ctl->p_full), gp & 1u, wctl);
+    } else {
+      const uint64_t b = desc_sw128(base + kPOff, 16, 1024);
+      for (int g = 0; g < n; ++g) {
+        const uint32_t s = g & 1u;
+        const bool first = uniform(cur.is_first());
+        const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, uniform((cur.rows(p) + 15) / 16 * 16), true, false);
+        cur.next(p);
+        if (!wait_warp(bar(ctl->p_full), g & 1u, wctl)) break;
         // the previous segment's accumulator has been read
-        if (ok && cur.is_first() && seg_p++) ok = wait_warp(bar(ctl->o_free), seg_p & 1u, wctl);
-        if (!ok) break;
+        if (first && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
         ptx::tc_fence_after();
-        const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, 128, (cur.rows(p) + 15) / 16 * 16, true, false);
-        const uint32_t more = cur.is_first() ? 0u : 1u;
+        const uint32_t more = first ? 0u : 1u;
         const uint64_t a = desc_sw128(base + kKvOff + s * kTile, 1024, kGroup);
-        const uint64_t b = desc_sw128(base + kPOff, 16, 1024);
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: two groups of C, 32 bytes of P
 #pragma unroll
           for (int m = 0; m < 4; ++m)         // 128 values: two chunks
-            mma_f16(el, tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc_o,
+            mma_f16(el, tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc,
                     k ? 1u : more);
           tc_commit(el, bar(ctl->empty[s][k]));
         }
         tc_commit(el, bar(ctl->pv_done));
-        cur.next(p);
-        ++gp;
       }
     }
     tc_commit(el, bar(ctl->drain));
@@ -274,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_16x256b_x4(tmem + quarter + kSCol + (g & 1u) * kKeys + 32 * half, sr);
       ptx::tmem_ld_wait();
       ptx::tc_fence_before();
+      ptx::mbar_arrive(bar(ctl->s_free[g & 1u]));
       // keys of this half that row r0 + 8 i sees: query token s of Sq sees len - Sq + s + 1
       int sees[2];
       bool masked = false;

@@ -62,43 +62,44 @@ struct Cursor {
 
   // Executed by a whole warp: the range and its first item.  Returns the share.
   __device__ __forceinline__ int init(const DecodeParams& p, int index, int ranges) {
-    const int lane = threadIdx.x & 31;
-    int total = 0, n = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-      total += b0 + lane < p.B ? item_tiles<KEYS>(n) : 0;
-    }
+    // A lane takes `per` consecutive sequences: independent loads and one scan.
+    const int lane = threadIdx.x & 31, per = (p.B + 31) / 32, from_b = lane * per;
+    int mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i)
+      if (from_b + i < p.B) mine += item_tiles<KEYS>(seq_len(p, from_b + i));
+    mine *= p.blocks;
+    int upto = mine;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
-    total *= p.blocks;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(kFull, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const int total = __shfl_sync(kFull, upto, 31);
     const int share = max(int((unsigned(total) + ranges - 1) / ranges), p.min_share);
     const int64_t from = int64_t(share) * index;
     pos = int(min(from, int64_t(total)));
     end = int(min(from + share, int64_t(total)));
     if (pos >= end) return share;
-    int before = 0;                           // tiles of the sequences before b0
-    for (int b0 = 0;; b0 += 32) {
-      if (p.B > 32) n = b0 + lane < p.B ? seq_len(p, b0 + lane) : 0;
-      const int mine = b0 + lane < p.B ? item_tiles<KEYS>(n) * p.blocks : 0;
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(kFull, upto, d);
-        if (lane >= d) upto += v;
-      }
-      const unsigned hit = __ballot_sync(kFull, before + upto > pos);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        b = b0 + src;
-        len = __shfl_sync(kFull, n, src);
-        const int in = pos - before - __shfl_sync(kFull, upto - mine, src);
+    const int src = __ffs(__ballot_sync(kFull, upto > pos)) - 1;
+    int in = pos - (upto - mine);             // tiles into the lane's sequences, where lane == src
+    b = from_b;
+    len = tiles = 0;
+    if (lane == src) {
+      for (;; ++b) {
+        len = seq_len(p, b);
         tiles = item_tiles<KEYS>(len);
-        block = in / tiles;
-        tile = first = in - block * tiles;
-        return share;
+        if (in < tiles * p.blocks) break;
+        in -= tiles * p.blocks;
       }
-      before += __shfl_sync(kFull, upto, 31);
     }
+    b = __shfl_sync(kFull, b, src);
+    len = __shfl_sync(kFull, len, src);
+    in = __shfl_sync(kFull, in, src);
+    tiles = item_tiles<KEYS>(len);
+    block = in / tiles;
+    tile = first = in - block * tiles;
+    return share;
   }
   __device__ __forceinline__ bool valid() const { return pos < end; }
   __device__ __forceinline__ bool is_first() const { return tile == first; }

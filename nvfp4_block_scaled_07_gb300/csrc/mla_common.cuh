@@ -182,40 +182,59 @@ __device__ __forceinline__ uint32_t elect_one() {
       : "memory");
   return r;
 }
+// Shared-memory operand descriptors, 128-byte swizzle.  An operand is made of
+// atoms of 8 rows x 128 bytes (1024 bytes, aligned to as much).
+//   K-major: rows are M (N), their 64 values along K; `stride` from one 8-row
+//     group to the next; 16 values of K are 32 bytes.
+//   MN-major: rows are K, their 64 values along M (N); `stride` from one
+//     8-row group of K to the next, `lead` to the next 64 values of M (N).
+// The address and lead are the low word, which the MMAs of a tile step by
+// constants; the stride is the high word, a constant of the MMA.
+__device__ __forceinline__ uint32_t desc_sw128(uint32_t saddr, uint32_t lead) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t stride) { return (stride >> 4) | (1u << 14) | (2u << 29); }
+
 // D[tmem] (+)= A[smem] B[smem]^T, K = 16, issued where `elected`.
-__device__ __forceinline__ void mma_f16(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+template <uint32_t A_STRIDE, uint32_t B_STRIDE>
+__device__ __forceinline__ void mma_f16(uint32_t elected, uint32_t d_tmem, uint32_t a_desc, uint32_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %7};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_desc), "r"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected), "n"(desc_hi(A_STRIDE)), "n"(desc_hi(B_STRIDE))
       : "memory");
 }
 // The same with A in tensor memory: lane = row of A, 16-bit pairs along K.
-__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+template <uint32_t B_STRIDE>
+__device__ __forceinline__ void mma_f16_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected), "n"(desc_hi(B_STRIDE))
       : "memory");
 }
-// The same on a CTA pair, issued by the even CTA: M rows, half of them in
+// The first on a CTA pair, issued by the even CTA: M rows, half of them in
 // each CTA's shared memory at one offset; N rows of B likewise.  With M = 128
 // a CTA's tensor memory holds its 64 rows in lanes 0-63 for the first half of
 // the columns and in lanes 64-127 for the second.
-__device__ __forceinline__ void mma_f16_pair(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+template <uint32_t A_STRIDE, uint32_t B_STRIDE>
+__device__ __forceinline__ void mma_f16_pair(uint32_t elected, uint32_t d_tmem, uint32_t a_desc, uint32_t b_desc,
                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %7};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_desc), "r"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected), "n"(desc_hi(A_STRIDE)), "n"(desc_hi(B_STRIDE))
       : "memory");
 }
 // Arrive on the mbarrier at offset `bar` in both CTAs of the pair.
@@ -276,18 +295,6 @@ __device__ __forceinline__ void arrive_expect_tx(uint32_t elected, uint32_t bar,
       "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
       "r"(bytes), "r"(elected)
       : "memory");
-}
-
-// Shared-memory operand descriptors, 128-byte swizzle.  An operand is made of
-// atoms of 8 rows x 128 bytes (1024 bytes, aligned to as much).
-//   K-major: rows are M (N), their 64 values along K; `stride` from one 8-row
-//     group to the next; 16 values of K are 32 bytes.
-//   MN-major: rows are K, their 64 values along M (N); `stride` from one
-//     8-row group of K to the next, `lead` to the next 64 values of M (N).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lead, uint32_t stride) {
-  const uint32_t lo = ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
-  const uint32_t hi = (stride >> 4) | (1u << 14) | (2u << 29);
-  return (uint64_t(hi) << 32) | lo;
 }
 
 // 16 lanes x 32 columns of a warp's lane quarter: thread l holds, in r[4i ..

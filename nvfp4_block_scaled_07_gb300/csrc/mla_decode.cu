@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t seg = 0;
     if (warp == kIssuer) {
       const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 64, kKeys, false, false);
-      const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
+      const uint32_t a = desc_sw128(base + kQOff, 16);
       for (int g = 0; g < n; ++g) {
         const uint32_t s = g & 1u, ph = (g >> 1) & 1u, d = tmem + kSCol + s * kKeys;
         const bool first = uniform(cur.is_first()), last = uniform(cur.is_last());
@@ -197,17 +197,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(bar(ctl->s_free[s]), ph ^ 1u, wctl)) break;
         if (!wait_warp(bar(ctl->full[s]), ph, wctl)) break;
         ptx::tc_fence_after();
-        const uint64_t b = desc_sw128(base + kKvOff + s * kTile, 16, kGroup);
+        const uint32_t b = desc_sw128(base + kKvOff + s * kTile, 16);
 #pragma unroll
         for (int c = 0; c < 9; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16(el, d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc, c + k > 0);
+            mma_f16<1024, kGroup>(el, d, a + c * (kChunk >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k, idesc, c + k > 0);
         tc_commit(el, bar(ctl->s_full[s]));
         if (last) tc_commit(el, bar(ctl->q_empty));
       }
     } else {
-      const uint64_t b = desc_sw128(base + kPOff, 16, 1024);
+      const uint32_t b = desc_sw128(base + kPOff, 16);
       for (int g = 0; g < n; ++g) {
         const uint32_t s = g & 1u;
         const bool first = uniform(cur.is_first());
@@ -218,12 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (first && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
         ptx::tc_fence_after();
         const uint32_t more = first ? 0u : 1u;
-        const uint64_t a = desc_sw128(base + kKvOff + s * kTile, 1024, kGroup);
+        const uint32_t a = desc_sw128(base + kKvOff + s * kTile, 1024);
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: two groups of C, 32 bytes of P
 #pragma unroll
           for (int m = 0; m < 4; ++m)         // 128 values: two chunks
-            mma_f16(el, tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc,
+            mma_f16<kGroup, 1024>(el, tmem + m * kRows, a + k * (2 * kGroup >> 4) + m * (2 * 1024 >> 4), b + 2 * k, idesc,
                     k ? 1u : more);
           tc_commit(el, bar(ctl->empty[s][k]));
         }

@@ -238,18 +238,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const uint32_t el = elect_one();
     if (rank == 0 && warp == kIssuer) {
       const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, kKeys, false, false);
-      const uint64_t a = desc_sw128(base + kQOff, 16, 1024);
+      const uint32_t a = desc_sw128(base + kQOff, 16);
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
         const uint32_t s = g & 1u;
         if (cur.is_first() && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
         if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl) || !wait_warp(bar(ctl->k_full), g & 1u, wctl)) break;
         ptx::tc_fence_after();
-        const uint64_t b = desc_sw128(base + kKOff, 16, kGroup);
+        const uint32_t b = desc_sw128(base + kKOff, 16);
 #pragma unroll
         for (int c = 0; c < 9; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16_pair(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
+            mma_f16_pair<1024, kGroup>(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
                          idesc, c + k > 0);
         tc_commit_pair(el, bar(ctl->k_empty));
         tc_commit_pair(el, bar(ctl->s_full[s]));
@@ -258,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       }
     } else if (rank == 0) {
       const uint32_t idesc = idesc_f16(Elem<T>::kFormat, 128, 256, false, true);
-      const uint64_t a = desc_sw128(base + kPOff, 16, 1024), b = desc_sw128(base + kVOff, 1024, kVGroup);
+      const uint32_t a = desc_sw128(base + kPOff, 16), b = desc_sw128(base + kVOff, 1024);
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
         if (!wait_warp(bar(ctl->p_full), g & 1u, wctl)) break;
         // the previous segment's accumulator has been read
@@ -269,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
 #pragma unroll
           for (int h = 0; h < 2; ++h)         // 256 values
-            mma_f16_pair(el, tmem + 128 * h, a + (k >> 2) * (kPBytes >> 4) + 2 * (k & 3), b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
+            mma_f16_pair<1024, kVGroup>(el, tmem + 128 * h, a + (k >> 2) * (kPBytes >> 4) + 2 * (k & 3), b + k * (2 * kVGroup >> 4) + h * (2048 >> 4), idesc,
                          k ? 1u : more);
           tc_commit_pair(el, bar(ctl->v_empty[k]));
         }

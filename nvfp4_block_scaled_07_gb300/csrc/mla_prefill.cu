@@ -86,9 +86,10 @@ __device__ __forceinline__ int2 range_of(const int32_t* cu, int b, int total) {
 
 // Scores of columns from `sees` on become -inf.
 __device__ __forceinline__ void mask_from(uint32_t (&s)[32], int sees) {
+  const uint32_t seen = sees >= 32 ? 0xFFFFFFFFu : sees <= 0 ? 0u : (1u << sees) - 1u;
 #pragma unroll
   for (int k = 0; k < 32; ++k)
-    if (k >= sees) s[k] = 0xFF800000u;
+    if (!(seen >> k & 1u)) s[k] = 0xFF800000u;
 }
 
 template <typename T>
@@ -238,19 +239,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc_s = idesc_f16(Elem<T>::kFormat, kM, kKeys, false, false);
     const uint32_t idesc_o = idesc_f16(Elem<T>::kFormat, kM, kValueDim, false, true);
     auto issue_s = [&](int t, int j) {
-      const uint64_t a = desc_sw128(base + kQOff + t * kQTile, 16, 1024);
-      const uint64_t k = desc_sw128(base + kKOff + (j & 1) * kKTile, 16, 1024);
+      const uint32_t a = desc_sw128(base + kQOff + t * kQTile, 16);
+      const uint32_t k = desc_sw128(base + kKOff + (j & 1) * kKTile, 16);
 #pragma unroll
       for (int c = 0; c < 3; ++c)
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          mma_f16(el, tmem + t * kKeys, a + c * (kChunk >> 4) + 2 * s, k + c * (kChunk >> 4) + 2 * s, idesc_s, c + s > 0);
+          mma_f16<1024, 1024>(el, tmem + t * kKeys, a + c * (kChunk >> 4) + 2 * s, k + c * (kChunk >> 4) + 2 * s, idesc_s, c + s > 0);
       tc_commit(el, bar(ctl->s_full[t]));
     };
     // V is stored with its values contiguous: 16 keys are 2048 bytes, the second 64 values a chunk further.
     // The first 64 keys go out as soon as their weights are there.
     auto issue_pv = [&](int t, int j, bool last_user) {
-      const uint64_t v = desc_sw128(base + kVOff, kChunk, 1024);
+      const uint32_t v = desc_sw128(base + kVOff, kChunk);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!wait_warp(bar(ctl->v_full[h]), j & 1u, wctl) ||
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
 #pragma unroll
         for (int s = 4 * h; s < 4 * h + 4; ++s)
-          mma_f16_ts(el, tmem + 256 + t * kValueDim, tmem + t * kKeys + 8 * s, v + s * (2048 >> 4), idesc_o,
+          mma_f16_ts<1024>(el, tmem + 256 + t * kValueDim, tmem + t * kKeys + 8 * s, v + s * (2048 >> 4), idesc_o,
                      s ? 1u : uint32_t(j > 0));
         if (last_user) tc_commit(el, bar(ctl->v_empty[h]));
       }
@@ -306,10 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(s_col + 32 * c, s[c]);
       ptx::tmem_ld_wait();
       const int sees = limit - j * kKeys;
-      if (__any_sync(kFull, sees < kKeys)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) mask_from(s[c], sees - 32 * c);
-      }
+      for (int c = 0; c < 4; ++c)
+        if (__any_sync(kFull, sees < 32 * c + 32)) mask_from(s[c], sees - 32 * c);
       float top[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {           // four chains of three-way maxima

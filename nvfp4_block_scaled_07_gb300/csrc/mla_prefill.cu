@@ -19,13 +19,14 @@
 //
 // The parts of a key come from three tensors (k_nope and v usually slices of
 // one projection's output), so nothing is concatenated in memory.
-// Blocks are ordered by head, the longest rows of a sequence first: the CTAs
-// that run together read the same few heads' keys from L2, and short blocks
-// fill the end.
+// Blocks are ordered by the keys that they see, most first, and by head among
+// those: the hardware hands them out in this order, and short blocks fill the
+// end (by head and sequence instead: ORDERMEAS).
 //
 // Warp roles: warps 0-3 and 4-7 softmax and epilogue of the two tiles, warp 8
 // TMA producer, warp 9 tensor-memory owner and MMA issuer.  Every wait is
 // bounded.
+#include <climits>
 #include <cstddef>
 #include <cstdint>
 
@@ -105,33 +106,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
   ptx::grid_dep_wait();
-  // The block's place: sequence b, its 256 queries from q0 on.  All warps find it.
-  const int head = blockIdx.x / p.most;
-  int i = int(blockIdx.x) - head * p.most;
+  // The block's place: head, sequence b, its 256 queries from q0 on (q0 < 0:
+  // none, the grid is sized by what the lengths could need).  All warps find it.
+  const int head = int(blockIdx.x) % p.H;
   int b = 0, at_q = 0, at_k = 0, nq = 0, nk = 0, q0 = -1;
-  for (int b0 = 0; b0 < p.B && q0 < 0; b0 += 32) {
-    const bool in = b0 + lane < p.B;
-    const int2 rq = in ? range_of(p.cu_q, b0 + lane, p.Tq) : make_int2(0, 0);
-    const int mine = (rq.y + 2 * kM - 1) / (2 * kM);
-    int upto = mine;
+  {
+    // Level of a block: the keys that its last row sees, in units of 256.  The
+    // blocks of a sequence have consecutive levels from `low` on (causal), or
+    // all the same.
+    struct Levels {
+      int blocks, low;
+    };
+    auto levels = [&](int k) {
+      Levels v = {0, 0};
+      if (k < p.B) {
+        const int2 rq = range_of(p.cu_q, k, p.Tq), rk = range_of(p.cu_k, k, p.Tk);
+        v.blocks = (rq.y + 2 * kM - 1) / (2 * kM);
+        v.low = p.causal ? (rk.y - rq.y + 4 * kM - 1) >> 8 : (rk.y + 2 * kM - 1) >> 8;
+      }
+      return v;
+    };
+    const Levels mine = levels(lane);         // of the first 32 sequences
+    auto at_least = [&](const Levels& v, int level) {  // a sequence's blocks of this level or above
+      if (p.causal) return min(max(v.low + v.blocks - level, 0), v.blocks);
+      return v.low >= level ? v.blocks : 0;
+    };
+    auto count = [&](int level) {
+      int n = at_least(mine, level);
+      for (int k = 32 + lane; k < p.B; k += 32) n += at_least(levels(k), level);
+      return int(__reduce_add_sync(kFull, unsigned(n)));
+    };
+    int lo = INT_MAX, hi = INT_MIN;
+    for (int k = lane; k < p.B; k += 32) {
+      const Levels v = k == lane ? mine : levels(k);
+      if (v.blocks) lo = min(lo, v.low), hi = max(hi, v.low + (p.causal ? v.blocks - 1 : 0));
+    }
+    lo = __reduce_min_sync(kFull, lo), hi = __reduce_max_sync(kFull, hi);
+    const int i = int(blockIdx.x) / p.H;      // the i-th block from the highest level down
+    if (lo <= hi && i < count(lo)) {
+      while (lo < hi) {                       // the highest level with more than i blocks at or above it
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (count(mid) > i) lo = mid;
+        else hi = mid - 1;
+      }
+      int left = i - count(lo + 1);           // among the blocks of this level, by sequence
+      for (int b0 = 0; b0 < p.B && q0 < 0; b0 += 32) {
+        const Levels v = b0 ? levels(b0 + lane) : mine;
+        const int here = at_least(v, lo) - at_least(v, lo + 1);
+        int upto = here;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(kFull, upto, d);
-      if (lane >= d) upto += v;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int n = __shfl_up_sync(kFull, upto, d);
+          if (lane >= d) upto += n;
+        }
+        const unsigned hit = __ballot_sync(kFull, upto > left);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          b = b0 + src;
+          q0 = 2 * kM * (p.causal ? lo - __shfl_sync(kFull, v.low, src) : left - __shfl_sync(kFull, upto - here, src));
+          const int2 rq = range_of(p.cu_q, b, p.Tq), rk = range_of(p.cu_k, b, p.Tk);
+          at_q = rq.x, nq = rq.y, at_k = rk.x, nk = rk.y;
+        }
+        left -= __shfl_sync(kFull, upto, 31);
+      }
     }
-    const unsigned hit = __ballot_sync(kFull, upto > i);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      b = b0 + src;
-      at_q = __shfl_sync(kFull, rq.x, src);
-      nq = __shfl_sync(kFull, rq.y, src);
-      // the sequence's blocks from its end, where rows see the most keys
-      q0 = (__shfl_sync(kFull, upto, src) - 1 - i) * (2 * kM);
-      const int2 rk = range_of(p.cu_k, b, p.Tk);
-      at_k = rk.x;
-      nk = rk.y;
-    }
-    i -= __shfl_sync(kFull, upto, 31);
   }
   if (blockIdx.x == 0 && warp == kProducer)   // offsets that are not served as they are
     for (int k = lane; k < p.B; k += 32)

@@ -202,3 +202,58 @@ def mla_prefill(q, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, 
         _dense(out, t, (Tq, H, VALUE), "out", dev), _dense(lse, torch.float32, (Tq, H), "lse", dev), _stream(dev)),
         "mla_prefill")
     return out, lse
+
+
+# ---- the whole attention of a layer --------------------------------------------------
+class LatentAttention:
+    """Weights of one layer's latent attention and its two forms.
+
+    prefill() takes whole prompts: it appends their rows to the cache and
+    attends in the expanded form.  decode() takes the newest tokens of
+    sequences whose rows are in the cache: it appends theirs and attends in the
+    absorbed form, with the keys' and values' projections folded into the
+    queries and the outputs.  The projections are plain matrix products.
+
+    w_q [H * 192, D], w_kv [576, D], kv_norm [512], w_up [H * 256, 512] (of each
+    head first the 128 rows of its keys, then of its values), w_o [D, H * 128],
+    all of one 16-bit type; rope_table as mla_append takes it."""
+
+    def __init__(self, w_q, w_kv, kv_norm, w_up, w_o, rope_table, eps=1e-6, interleaved=True, scale=None):
+        self.H = w_up.shape[0] // (NOPE + VALUE)
+        for name, w, shape in (("w_q", w_q, (self.H * (NOPE + ROPE), w_q.shape[1])), ("w_kv", w_kv, (ROW, w_q.shape[1])),
+                               ("kv_norm", kv_norm, (LATENT,)), ("w_up", w_up, (self.H * (NOPE + VALUE), LATENT)),
+                               ("w_o", w_o, (w_q.shape[1], self.H * VALUE))):
+            _dense(w, w_q.dtype, shape, name, w_q.get_device())
+        self.w_q, self.w_kv, self.kv_norm, self.w_up, self.w_o = w_q, w_kv, kv_norm, w_up, w_o
+        up = w_up.view(self.H, NOPE + VALUE, LATENT)
+        self.w_uk, self.w_uv = up[:, :NOPE], up[:, NOPE:].transpose(1, 2)   # [H, 128, 512], [H, 512, 128]
+        self.rope_table, self.eps, self.interleaved = rope_table, eps, interleaved
+        self.scale = (NOPE + ROPE) ** -0.5 if scale is None else scale
+
+    def _project(self, x):
+        return (x @ self.w_q.T).view(x.shape[0], self.H, NOPE + ROPE), x @ self.w_kv.T
+
+    def _append(self, kv, positions, slots, cache, q_rope, q_out, rows_out=None):
+        mla_append(kv[:, :LATENT], kv[:, LATENT:], positions, slots, self.rope_table, cache, norm_weight=self.kv_norm,
+                   eps=self.eps, interleaved=self.interleaved, q_rope=q_rope, q_out=q_out, rows_out=rows_out)
+
+    def prefill(self, x, positions, slots, cache, cu_seqlens):
+        """x [T, D]: the tokens of whole prompts, sequence b from cu_seqlens[b] on.  Returns [T, D]."""
+        q, kv = self._project(x)
+        rows = torch.empty_like(kv)
+        self._append(kv, positions, slots, cache, q[..., NOPE:], q[..., NOPE:], rows)
+        up = (rows[:, :LATENT] @ self.w_up.T).view(-1, self.H, NOPE + VALUE)
+        out, _ = mla_prefill(q, up[..., :NOPE], rows[:, LATENT:], up[..., NOPE:], cu_seqlens, cu_seqlens, self.scale)
+        return out.flatten(1) @ self.w_o.T
+
+    def decode(self, x, positions, slots, cache, block_tables, seq_lens, workspace=None):
+        """x [B * Sq, D]: the Sq newest tokens of each sequence, seq_lens counting them.  Returns [B * Sq, D]."""
+        B = seq_lens.shape[0]
+        q, kv = self._project(x)
+        absorbed = torch.empty((x.shape[0], self.H, ROW), dtype=x.dtype, device=x.device)
+        absorbed[..., :LATENT] = torch.bmm(q[..., :NOPE].transpose(0, 1), self.w_uk).transpose(0, 1)
+        self._append(kv, positions, slots, cache, q[..., NOPE:], absorbed[..., LATENT:])
+        out, _ = mla_decode(absorbed.view(B, -1, self.H, ROW), cache, block_tables, seq_lens, self.scale,
+                            workspace=workspace)
+        heads = torch.bmm(out.view(-1, self.H, LATENT).transpose(0, 1), self.w_uv)
+        return heads.transpose(0, 1).reshape(x.shape[0], -1) @ self.w_o.T

@@ -37,22 +37,22 @@ _DECODE_WORKSPACE = int(_lib.mla_decode_workspace_size())
 # The checks below run on every call of a decode step, whose kernels take
 # microseconds: they read each property once and build no message before it is
 # needed.
-def _typed(t, dtype, shape, name, device):
-    """Checks everything but the layout; returns the data pointer."""
+def _refuse(t, dtype, shape, name, device):
+    """The error of a tensor that is not what a call needs."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _dense(t, dtype, shape, name, device):
-    p = _typed(t, dtype, shape, name, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return p
+    """A contiguous tensor's data pointer."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, name, device)
 
 
 def _strided(t, dtype, shape, name, device):
@@ -60,8 +60,9 @@ def _strided(t, dtype, shape, name, device):
     16-byte boundaries.  Returns the pointer and the other dimensions' strides,
     which say nothing (a dense tensor's are given) where a dimension has one
     entry."""
-    p = _typed(t, dtype, shape, name, device)
-    stride = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, dtype, shape, name, device)
+    p, stride = t.data_ptr(), t.stride()
     if len(shape) == 2:
         steps = (stride[0] if shape[0] > 1 else shape[1],)
         bad = steps[0] % 8
@@ -89,7 +90,7 @@ def _on_cuda(device, name):
 
 def _stream(device):
     """The device's current stream; calls are made with that device current."""
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on cuda:{device}, but the current device is cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(device)
 
@@ -113,20 +114,20 @@ def mla_append(latent, k_rope, positions, slots, rope_table, cache, norm_weight=
     64] may be a slice of the queries' buffer or q_rope itself; it is made when
     q_rope comes without it.  Returns q_out (None without queries)."""
     t, code, dev = _first(latent, "latent", 2)
-    T = latent.shape[0]
+    T = len(latent)
     latent_at = _strided(latent, t, (T, LATENT), "latent", dev)
     _on_cuda(dev, "latent")
     rope_at = _strided(k_rope, t, (T, ROPE), "k_rope", dev)
     if cache.dim() != 3 or rope_table.dim() != 2 or (q_rope is not None and q_rope.dim() != 3):
         raise ValueError("cache and q_rope have three dimensions, rope_table has two")
-    pages, page = cache.shape[0], cache.shape[1]
+    pages, page, _ = cache.shape
     cache_at = _dense(cache, t, (pages, page, ROW), "cache", dev)
-    span = rope_table.shape[0]
+    span = len(rope_table)
     q_at, q_out_at, H = (None, 0, 0), (None, 0, 0), 0
     if q_rope is not None:
         H = q_rope.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, H, ROPE), dtype=t, device=latent.device)
+            q_out = q_rope.new_empty((T, H, ROPE))
         if H:
             q_at = _strided(q_rope, t, (T, H, ROPE), "q_rope", dev)
             q_out_at = _strided(q_out, t, (T, H, ROPE), "q_out", dev)
@@ -157,24 +158,33 @@ def mla_decode(q, cache, block_tables, seq_lens, scale, out=None, lse=None, work
     _on_cuda(dev, "q")
     if cache.dim() != 3 or block_tables.dim() != 2:
         raise ValueError("cache has three dimensions, block_tables two")
-    pages, page = cache.shape[0], cache.shape[1]
-    max_pages = block_tables.shape[1]
-    tables_at = _typed(block_tables, torch.int32, (B, max_pages), "block_tables", dev)
+    pages, page, _ = cache.shape
+    rows, max_pages = block_tables.shape
+    if block_tables.dtype is not torch.int32 or rows != B or block_tables.get_device() != dev:
+        _refuse(block_tables, torch.int32, (B, max_pages), "block_tables", dev)
     step = block_tables.stride()
     if max_pages > 1 and step[1] != 1:
         raise ValueError(f"block_tables: strides {step}, rows must be contiguous")
-    if out is None:
-        out = torch.empty((B, Sq, H, LATENT), dtype=t, device=q.device)
+    if out is None:                           # what is made here needs no check
+        out = q.new_empty((B, Sq, H, LATENT))
+        out_at = out.data_ptr()
+    else:
+        out_at = _dense(out, t, (B, Sq, H, LATENT), "out", dev)
     if lse is None:
-        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Sq, H), dtype=torch.float32)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _dense(lse, torch.float32, (B, Sq, H), "lse", dev)
     if workspace is None:
-        workspace = torch.empty((_DECODE_WORKSPACE,), dtype=torch.uint8, device=q.device)
-    ws_bytes = workspace.numel()
+        workspace = q.new_empty((_DECODE_WORKSPACE,), dtype=torch.uint8)
+        ws_at, ws_bytes = workspace.data_ptr(), _DECODE_WORKSPACE
+    else:
+        ws_bytes = workspace.numel()
+        ws_at = _dense(workspace, torch.uint8, (ws_bytes,), "workspace", dev)
     _b._check(_lib.mla_decode(
-        q_at, _dense(cache, t, (pages, page, ROW), "cache", dev), pages, page, tables_at,
+        q_at, _dense(cache, t, (pages, page, ROW), "cache", dev), pages, page, block_tables.data_ptr(),
         step[0] if B > 1 else max_pages, max_pages, _dense(seq_lens, torch.int32, (B,), "seq_lens", dev), B, Sq, H,
-        scale, code, _dense(out, t, (B, Sq, H, LATENT), "out", dev), _dense(lse, torch.float32, (B, Sq, H), "lse", dev),
-        _dense(workspace, torch.uint8, (ws_bytes,), "workspace", dev), ws_bytes, _stream(dev)), "mla_decode")
+        scale, code, out_at, lse_at, ws_at, ws_bytes, _stream(dev)), "mla_decode")
     return out, lse
 
 
@@ -188,19 +198,24 @@ def mla_prefill(q, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, 
     Tq, H, _ = q.shape
     q_at = _strided(q, t, (Tq, H, NOPE + ROPE), "q", dev)
     _on_cuda(dev, "q")
-    Tk, B = k_nope.shape[0], cu_q.numel() - 1
+    Tk, B = len(k_nope), cu_q.numel() - 1
     if B < 0:
         raise ValueError("cu_q: one entry more than there are sequences")
     if out is None:
-        out = torch.empty((Tq, H, VALUE), dtype=t, device=q.device)
+        out = q.new_empty((Tq, H, VALUE))
+        out_at = out.data_ptr()
+    else:
+        out_at = _dense(out, t, (Tq, H, VALUE), "out", dev)
     if lse is None:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((Tq, H), dtype=torch.float32)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _dense(lse, torch.float32, (Tq, H), "lse", dev)
     _b._check(_lib.mla_prefill(
         *q_at, *_strided(k_nope, t, (Tk, H, NOPE), "k_nope", dev), *_strided(k_rope, t, (Tk, ROPE), "k_rope", dev),
         *_strided(v, t, (Tk, H, VALUE), "v", dev), _dense(cu_q, torch.int32, (B + 1,), "cu_q", dev),
         _dense(cu_k, torch.int32, (B + 1,), "cu_k", dev), B, Tq, Tk, H, scale, 1 if causal else 0, code,
-        _dense(out, t, (Tq, H, VALUE), "out", dev), _dense(lse, torch.float32, (Tq, H), "lse", dev), _stream(dev)),
-        "mla_prefill")
+        out_at, lse_at, _stream(dev)), "mla_prefill")
     return out, lse
 
 

@@ -112,15 +112,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc(base + uint32_t(offsetof(Control, tmem)), kTmemCols);
     ptx::tmem_relinquish();
   }
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  Cursor<kKeys> cur;                          // its loads run while tensor memory is allocated
+  const int share = cur.init(p, blockIdx.x, gridDim.x);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, ctl->tmem, 0);
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
-
-  Cursor<kKeys> cur;
-  const int share = cur.init(p, blockIdx.x, gridDim.x);
 
   if (warp >= kProducer && warp < kProducer + kPieces) {
     // ---- producers: one warp for each piece of 16 keys, so that a tile's
@@ -442,21 +441,14 @@ template <typename T, bool BY_ITEM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p) {
   constexpr int kShare = BY_ITEM ? 4 : 1, kJoinRows = kJoinThreads / 32 / kShare;  // warps a row, rows a block
   __shared__ float4 s_sum[BY_ITEM ? kJoinThreads / 32 : 1][4][32];
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, set = warp % kShare;
   int start, tiles, share, b, block;
-  if (BY_ITEM) {
-    b = int(blockIdx.x) / p.blocks;
-    block = int(blockIdx.x) - b * p.blocks;
-    share = p.heads[0].share;
-    tiles = item_tiles<kKeys>(seq_len(p, b));
-    start = 0;
-    for (int i = lane; i < b; i += 32) start += item_tiles<kKeys>(seq_len(p, i)) * p.blocks;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) start += __shfl_xor_sync(kFull, start, d);
-    start += tiles * block;
-  } else {
+  // The lengths are older than the kernel before this one, which waited for
+  // them before it let this one begin: they need no wait here.
+  if (BY_ITEM) find_item<kKeys>(p, blockIdx.x, b, block, start, tiles, share);
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (!BY_ITEM) {
     const Head h = p.heads[blockIdx.x + 1];
     start = h.start, tiles = h.tiles, share = h.share, b = h.b, block = h.block;
     // no item, or one that an earlier border cuts first
@@ -505,26 +497,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
       }
     }
   }
-  if (BY_ITEM) {
+  const int64_t at = int64_t(b) * p.rows + block * kRows + row;
+  auto store = [&](int j, float4 v) {
+    *reinterpret_cast<uint2*>(p.out + 2 * (at * kLatent + 128 * j + 4 * lane)) =
+        make_uint2(Elem<T>::pack(v.x, v.y), Elem<T>::pack(v.z, v.w));
+  };
+  if (live && lane == 0 && set == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  if (BY_ITEM) {                              // warp j of a row adds up the j-th quarter of the values
 #pragma unroll
     for (int j = 0; j < 4; ++j) s_sum[warp][j][lane] = acc[j];
     __syncthreads();
-    if (set) return;
+    float4 v = s_sum[warp - set][set][lane];
 #pragma unroll
-    for (int i = 1; i < kShare; ++i)
+    for (int i = 1; i < kShare; ++i) {
+      const float4 o = s_sum[warp - set + i][set][lane];
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    if (live) store(set, v);
+  } else if (live) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 o = s_sum[warp + i][j][lane];
-        acc[j].x += o.x, acc[j].y += o.y, acc[j].z += o.z, acc[j].w += o.w;
-      }
+    for (int j = 0; j < 4; ++j) store(j, acc[j]);
   }
-  if (!live) return;
-  const int64_t at = int64_t(b) * p.rows + block * kRows + row;
-  if (lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint2*>(p.out + 2 * (at * kLatent + 128 * j + 4 * lane)) =
-        make_uint2(Elem<T>::pack(acc[j].x, acc[j].y), Elem<T>::pack(acc[j].z, acc[j].w));
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -603,6 +596,7 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   p.scale_log2 = a.scale * kLog2e;
   p.out = static_cast<uint8_t*>(a.out);
   p.lse = a.lse;
+  p.ranges = ranges;
   p.min_share = min_share;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.heads = reinterpret_cast<Head*>(ws);
@@ -635,7 +629,7 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
     const int across = by_item ? int(items) : ranges - 1;
     if (pair)  // a task is eight rows x 128 values
       err = launch_kernel(by_item ? join_pair_kernel<T, true> : join_pair_kernel<T, false>,
-                          dim3(across, by_item ? (most + 7) / 8 * 4 : (most + 7) / 8), dim3(kPairJoinThreads), 0, st, false, p);
+                          dim3(across, by_item ? (most + 7) / 8 * 4 : (most + 7) / 8), dim3(by_item ? 2 * kPairJoinThreads : kPairJoinThreads), 0, st, false, p);
     else
       err = launch_kernel(by_item ? join_kernel<T, true> : join_kernel<T, false>,
                           dim3(across, by_item ? (most + 1) / 2 : (most + 7) / 8), dim3(kJoinThreads), 0, st, false, p);

@@ -36,7 +36,7 @@ struct DecodeParams {
   float scale_log2, scale;
   uint8_t* out;                               // [B, rows, 512]
   float* lse;                                 // [B, rows]
-  int min_share;
+  int ranges, min_share;
   Head* heads;                                // [ranges]
   float* part_o;                              // [grid][2][64][512]
   float* part_lse;                            // [grid][2][64], log2 domain
@@ -51,6 +51,11 @@ __device__ __forceinline__ int seq_len(const DecodeParams& p, int b) {
 template <int KEYS>
 __device__ __forceinline__ int item_tiles(int len) {
   return len > 0 ? (len + KEYS - 1) / KEYS : 1;
+}
+
+// Tiles of a range, of `total` in the list.
+__device__ __forceinline__ int range_tiles(const DecodeParams& p, int total, int ranges) {
+  return max(int((unsigned(total) + ranges - 1) / ranges), p.min_share);
 }
 
 // Walks the tiles [pos, end) of range `index` of `ranges` of the flattened (sequence, row block, tile) list.
@@ -76,7 +81,7 @@ struct Cursor {
       if (lane >= d) upto += v;
     }
     const int total = __shfl_sync(kFull, upto, 31);
-    const int share = max(int((unsigned(total) + ranges - 1) / ranges), p.min_share);
+    const int share = range_tiles(p, total, ranges);
     const int64_t from = int64_t(share) * index;
     pos = int(min(from, int64_t(total)));
     end = int(min(from + share, int64_t(total)));
@@ -123,6 +128,29 @@ struct Cursor {
     return min(kRows, p.rows - (block * p.ctas + part) * kRows);
   }
 };
+
+// Place of an item in the tile list and the tiles of a range, from the lengths
+// alone: a whole warp of a joining kernel finds them while the ranges still run.
+template <int KEYS>
+__device__ __forceinline__ void find_item(const DecodeParams& p, int item, int& b, int& block, int& start, int& tiles,
+                                          int& share) {
+  b = item / p.blocks;
+  block = item - b * p.blocks;
+  int before = 0, total = 0;
+  for (int i = threadIdx.x & 31; i < p.B; i += 32) {
+    const int t = item_tiles<KEYS>(seq_len(p, i));
+    total += t;
+    if (i < b) before += t;
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) {
+    before += __shfl_xor_sync(kFull, before, d);
+    total += __shfl_xor_sync(kFull, total, d);
+  }
+  tiles = item_tiles<KEYS>(seq_len(p, b));
+  start = before * p.blocks + tiles * block;
+  share = range_tiles(p, total * p.blocks, p.ranges);
+}
 
 __device__ __forceinline__ void prefetch_l2(uint32_t elected, const void* at, uint32_t bytes) {
   asm volatile(

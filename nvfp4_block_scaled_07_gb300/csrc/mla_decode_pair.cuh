@@ -125,16 +125,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     ptx::tmem_alloc_pair(base + uint32_t(offsetof(Control, tmem)), kTmemCols);
     ptx::tmem_relinquish_pair();
   }
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  Cursor<kKeys> cur;                          // its loads run while tensor memory is allocated
+  const int share = cur.init(p, range, ranges);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();                        // both CTAs' barriers exist before either signals one
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, ctl->tmem, 0);
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
-
-  Cursor<kKeys> cur;
-  const int share = cur.init(p, range, ranges);
 
   if (warp >= kProducer && warp < kIssuer) {
     // ---- producers: two warps copy whole rows (32 of the CTA's 64 keys
@@ -473,26 +472,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 // Joins the pair kernel's partial results (see join_kernel).  A warp takes
 // eight rows and 128 values: lane l row l % 8 and every fourth piece of four
 // values, so that loads cover 128 contiguous bytes and stores whole sectors.
-// BY_ITEM: block (item, .), four warps share the pieces of the ranges.
+// BY_ITEM: block (item, .), eight warps share the pieces of the ranges.
 constexpr int kPairJoinThreads = 128;
 template <typename T, bool BY_ITEM>
-__global__ void __launch_bounds__(kPairJoinThreads) join_pair_kernel(const DecodeParams p) {
-  __shared__ float4 s_sum[BY_ITEM ? 3 : 1][8][32];
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
+__global__ void __launch_bounds__((BY_ITEM ? 2 : 1) * kPairJoinThreads) join_pair_kernel(const DecodeParams p) {
+  constexpr int kShare = BY_ITEM ? 8 : 1;
+  __shared__ float4 s_sum[kShare][8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int start, tiles, share, b, block;
-  if (BY_ITEM) {
-    b = int(blockIdx.x) / p.blocks;
-    block = int(blockIdx.x) - b * p.blocks;
-    share = p.heads[0].share;
-    tiles = item_tiles<pair::kKeys>(seq_len(p, b));
-    start = 0;
-    for (int i = lane; i < b; i += 32) start += item_tiles<pair::kKeys>(seq_len(p, i)) * p.blocks;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) start += __shfl_xor_sync(kFull, start, d);
-    start += tiles * block;
-  } else {
+  if (BY_ITEM) find_item<pair::kKeys>(p, blockIdx.x, b, block, start, tiles, share);  // as in join_kernel
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (!BY_ITEM) {
     const Head h = p.heads[blockIdx.x + 1];
     start = h.start, tiles = h.tiles, share = h.share, b = h.b, block = h.block;
     // no item, or one that an earlier border cuts first
@@ -522,39 +513,52 @@ __global__ void __launch_bounds__(kPairJoinThreads) join_pair_kernel(const Decod
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   float4 acc[8] = {};
   if (live) {
-#pragma unroll 2
-    for (int i = BY_ITEM ? warp : 0; i < pieces; i += BY_ITEM ? 4 : 1) {
-      const float a = exp2_approx(p.part_lse[slot(i) * kRows + r] - ref) * inv;
-      const float* at = p.part_o + slot(i) * kRows * kLatent;
+    constexpr int kAhead = BY_ITEM ? 3 : 2;   // pieces whose loads are in flight together
+#pragma unroll 1
+    for (int i = BY_ITEM ? warp : 0; i < pieces; i += kAhead * kShare) {
+      float4 o[kAhead][8];
+      float a[kAhead];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 o = *reinterpret_cast<const float4*>(at + part_offset(r, half, upper, 4 * k + q0));
-        acc[k].x += a * o.x, acc[k].y += a * o.y, acc[k].z += a * o.z, acc[k].w += a * o.w;
+      for (int j = 0; j < kAhead; ++j) {
+        const bool more = i + j * kShare < pieces;
+        const int64_t from = slot(more ? i + j * kShare : i);
+        const float* at = p.part_o + from * kRows * kLatent;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          o[j][k] = more ? *reinterpret_cast<const float4*>(at + part_offset(r, half, upper, 4 * k + q0)) : float4{};
+        a[j] = more ? p.part_lse[from * kRows + r] : -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const float w = exp2_approx(a[j] - ref) * inv;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          acc[k].x += w * o[j][k].x, acc[k].y += w * o[j][k].y, acc[k].z += w * o[j][k].z, acc[k].w += w * o[j][k].w;
       }
     }
   }
-  if (BY_ITEM) {
-    if (warp) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s_sum[warp - 1][k][lane] = acc[k];
-    }
-    __syncthreads();
-    if (warp) return;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 o = s_sum[i][k][lane];
-        acc[k].x += o.x, acc[k].y += o.y, acc[k].z += o.z, acc[k].w += o.w;
-      }
-  }
-  if (!live) return;
   const int64_t at = int64_t(b) * p.rows + block * 2 * kRows + row;
-  if ((task & 3) == 0 && q0 == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
+  auto store = [&](int k, float4 v) {
     *reinterpret_cast<uint2*>(p.out + 2 * (at * kLatent + 256 * half + 128 * upper + 4 * (4 * k + q0))) =
-        make_uint2(Elem<T>::pack(acc[k].x, acc[k].y), Elem<T>::pack(acc[k].z, acc[k].w));
+        make_uint2(Elem<T>::pack(v.x, v.y), Elem<T>::pack(v.z, v.w));
+  };
+  if (live && (task & 3) == 0 && q0 == 0 && (!BY_ITEM || warp == 0))
+    p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  if (BY_ITEM) {                              // warp k adds up the k-th part of the values
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s_sum[warp][k][lane] = acc[k];
+    __syncthreads();
+    float4 v = s_sum[0][warp][lane];
+#pragma unroll
+    for (int i = 1; i < kShare; ++i) {
+      const float4 o = s_sum[i][warp][lane];
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    if (live) store(warp, v);
+  } else if (live) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) store(k, acc[k]);
+  }
 }
 
 }  // namespace

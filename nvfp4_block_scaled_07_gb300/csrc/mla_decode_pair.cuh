@@ -501,15 +501,20 @@ __global__ void __launch_bounds__((BY_ITEM ? 2 : 1) * kPairJoinThreads) join_pai
   auto slot = [&](int i) { return int64_t(2 * (2 * (first + i) + cta) + (i == 0 ? lead : 0)); };
   float top = -INFINITY, sum = 0.0f;
   const bool live = row < rows;
+  // the four lanes of a row share its log-sums
   if (live) {
 #pragma unroll 4
-    for (int i = 0; i < pieces; ++i) top = fmaxf(top, p.part_lse[slot(i) * kRows + r]);
+    for (int i = q0; i < pieces; i += 4) top = fmaxf(top, p.part_lse[slot(i) * kRows + r]);
   }
+  top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+  top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
   const float ref = top == -INFINITY ? 0.0f : top;
   if (live) {
 #pragma unroll 4
-    for (int i = 0; i < pieces; ++i) sum += exp2_approx(p.part_lse[slot(i) * kRows + r] - ref);
+    for (int i = q0; i < pieces; i += 4) sum += exp2_approx(p.part_lse[slot(i) * kRows + r] - ref);
   }
+  sum += __shfl_xor_sync(kFull, sum, 8);
+  sum += __shfl_xor_sync(kFull, sum, 16);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   float4 acc[8] = {};
   if (live) {

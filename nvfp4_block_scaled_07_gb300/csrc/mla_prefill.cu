@@ -21,7 +21,9 @@
 // one projection's output), so nothing is concatenated in memory.
 // Blocks are ordered by the keys that they see, most first, and by head among
 // those: the hardware hands them out in this order, and short blocks fill the
-// end (by head and sequence instead: ORDERMEAS).
+// end (by head and sequence instead: 16384 tokens
+// of one sequence 883 us instead of 834, seven ragged sequences 150 instead of
+// 144).
 //
 // Warp roles: warps 0-3 and 4-7 softmax and epilogue of the two tiles, warp 8
 // TMA producer, warp 9 tensor-memory owner and MMA issuer.  Every wait is
@@ -51,6 +53,7 @@ constexpr int kNopeDim = 128, kValueDim = 128;
 constexpr int kQTile = 3 * kChunk, kKTile = 3 * kChunk, kVTile = 2 * kChunk;
 constexpr int kProducer = 8, kIssuer = 9;
 constexpr int kThreads = 320;
+constexpr int kStageRow = 2 * kValueDim + 16; // bytes of an output row on its way out; 16 more against bank conflicts
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrow = 8.0f;                 // rescale O only when a maximum grew by 2^8
 
@@ -418,11 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     if (ok) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      uint8_t* out = p.out + 2 * (((int64_t(at_q) + index) * p.H + head) * kValueDim);
+      // Rows go through the tile's Q, which no product reads any more, so that
+      // a store covers two whole rows and not 16 bytes of 32 (this part of a
+      // block 4500 -> 2600 cycles, a ragged batch 136.6 -> 133.1 us).
+      uint8_t* stage = smem + kQOff + t * kQTile + 32 * quarter * kStageRow;
       // a row that saw no key gets zeros, also where masked values were not finite
       const bool zero = __any_sync(kFull, l == 0.0f);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {           // a row's 256 bytes, 16 at a time
+      for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         if (n[t]) {
           ptx::tmem_ld_32x32b_x32(o_col + 32 * c, o);
@@ -434,15 +440,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (l == 0.0f) o[k] = 0u;
-        if (index < nq) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(out + 64 * c + 2 * k) =
-                make_uint4(Elem<T>::pack(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
-                           Elem<T>::pack(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
-                           Elem<T>::pack(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
-                           Elem<T>::pack(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
-        }
+        for (int k = 0; k < 32; k += 8)
+          *reinterpret_cast<uint4*>(stage + lane * kStageRow + 64 * c + 2 * k) =
+              make_uint4(Elem<T>::pack(__uint_as_float(o[k]), __uint_as_float(o[k + 1])),
+                         Elem<T>::pack(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])),
+                         Elem<T>::pack(__uint_as_float(o[k + 4]), __uint_as_float(o[k + 5])),
+                         Elem<T>::pack(__uint_as_float(o[k + 6]), __uint_as_float(o[k + 7])));
+      }
+      __syncwarp();
+      const int first = q0 + t * kM + 32 * quarter;  // the warp's first row
+      uint8_t* out = p.out + 2 * (((int64_t(at_q) + first) * p.H + head) * kValueDim) + 16 * (lane & 15);
+#pragma unroll
+      for (int k = lane >> 4; k < 32; k += 2) {
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + k * kStageRow + 16 * (lane & 15));
+        if (first + k < nq) *reinterpret_cast<uint4*>(out + int64_t(k) * p.H * (2 * kValueDim)) = v;
       }
       if (index < nq) p.lse[(int64_t(at_q) + index) * p.H + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     }

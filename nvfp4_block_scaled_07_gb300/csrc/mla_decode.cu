@@ -432,23 +432,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partial results of the items that a range border cut.  With e_i
 // the log2-sum of piece i and o_i its normalised rows, out = sum 2^(e_i - e)
 // o_i, e = log2 sum 2^e_i, the pieces always in the same order.
-// A warp takes a row (16 values a lane).  BY_ITEM (few items of many pieces):
-// block (item, .), four warps share a row's pieces.  Otherwise block (c, .)
-// serves the item that the border between ranges c and c + 1 is the first to
-// cut.
+// SHARE warps share the pieces of a row.  With one, a warp takes a whole row
+// and block (c, .) serves the item that the border between ranges c and c + 1
+// is the first to cut.  With more (few items of many pieces), block (item, .)
+// serves an item; eight take 128 of a row's values, one block for each.
 constexpr int kJoinThreads = 256;
-template <typename T, bool BY_ITEM>
+template <typename T, int SHARE>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p) {
-  constexpr int kShare = BY_ITEM ? 4 : 1, kJoinRows = kJoinThreads / 32 / kShare;  // warps a row, rows a block
-  __shared__ float4 s_sum[BY_ITEM ? kJoinThreads / 32 : 1][4][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, set = warp % kShare;
+  constexpr bool kByItem = SHARE > 1;
+  constexpr int kWarps = kJoinThreads / 32, kParts = SHARE == 8 ? 4 : 1, kVecs = 4 / kParts;
+  __shared__ float4 s_sum[kByItem ? kWarps : 1][kVecs][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, set = warp % SHARE;
   int start, tiles, share, b, block;
   // The lengths are older than the kernel before this one, which waited for
   // them before it let this one begin: they need no wait here.
-  if (BY_ITEM) find_item<kKeys>(p, blockIdx.x, b, block, start, tiles, share);
+  if (kByItem) find_item<kKeys>(p, blockIdx.x, b, block, start, tiles, share);
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  if (!BY_ITEM) {
+  if (!kByItem) {
     const Head h = p.heads[blockIdx.x + 1];
     start = h.start, tiles = h.tiles, share = h.share, b = h.b, block = h.block;
     // no item, or one that an earlier border cuts first
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
   const int first = start / share, last = (start + tiles - 1) / share;
   if (first == last) return;                  // whole: written by its CTA (also an item that begins at the border)
   const int pieces = last - first + 1;
-  const int row = blockIdx.y * kJoinRows + warp / kShare;
+  const int row = int(blockIdx.y) / kParts * (kWarps / SHARE) + warp / SHARE, part = int(blockIdx.y) % kParts;
   const bool live = row < min(kRows, p.rows - block * kRows);
   // piece 0 is the last segment of range `first` unless the range begins with it
   const int lead = start != first * share ? 1 : 0;
@@ -480,17 +481,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  float4 acc[4] = {};                         // values 128 j + 4 lane ..
+  float4 acc[kVecs] = {};                     // values 128 (part * kVecs + j) + 4 lane ..
   if (live) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int n = min(32, pieces - 32 * k);
-#pragma unroll 2
-      for (int i = set; i < n; i += kShare) {
-        const float* at = p.part_o + piece_row(32 * k + i) * kLatent + 4 * lane;
+#pragma unroll 4 / kVecs * 2
+      for (int i = set; i < n; i += SHARE) {
+        const float* at = p.part_o + piece_row(32 * k + i) * kLatent + 128 * kVecs * part + 4 * lane;
         const float a = __shfl_sync(kFull, w[k], i) * inv;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kVecs; ++j) {
           const float4 o = *reinterpret_cast<const float4*>(at + 128 * j);
           acc[j].x += a * o.x, acc[j].y += a * o.y, acc[j].z += a * o.z, acc[j].w += a * o.w;
         }
@@ -499,31 +500,36 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
   }
   const int64_t at = int64_t(b) * p.rows + block * kRows + row;
   auto store = [&](int j, float4 v) {
-    *reinterpret_cast<uint2*>(p.out + 2 * (at * kLatent + 128 * j + 4 * lane)) =
+    *reinterpret_cast<uint2*>(p.out + 2 * (at * kLatent + 128 * (part * kVecs + j) + 4 * lane)) =
         make_uint2(Elem<T>::pack(v.x, v.y), Elem<T>::pack(v.z, v.w));
   };
-  if (live && lane == 0 && set == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
-  if (BY_ITEM) {                              // warp j of a row adds up the j-th quarter of the values
+  if (live && lane == 0 && set == 0 && part == 0) p.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  if (kByItem) {                              // warp j of a row adds up the j-th of its vectors
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s_sum[warp][j][lane] = acc[j];
+    for (int j = 0; j < kVecs; ++j) s_sum[warp][j][lane] = acc[j];
     __syncthreads();
+    if (set >= kVecs) return;
     float4 v = s_sum[warp - set][set][lane];
 #pragma unroll
-    for (int i = 1; i < kShare; ++i) {
+    for (int i = 1; i < SHARE; ++i) {
       const float4 o = s_sum[warp - set + i][set][lane];
       v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
     }
     if (live) store(set, v);
   } else if (live) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) store(j, acc[j]);
+    for (int j = 0; j < kVecs; ++j) store(j, acc[j]);
   }
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles a CTA takes at least: below this, splitting a sequence costs more in partial results than it gains.
-constexpr int kMinShare = 4;
+// Tiles of a range at least, of 64 keys with one CTA and of 128 with a pair:
+// below this, splitting a sequence costs more than it gains.  A sequence of
+// 1024 keys with 16 heads takes 9.9 us (9.8 with 1, 11.6 with 3, 12.4 with 4),
+// of 4096 keys 12.0 (13.8 with 1); with 128 heads 13.0 (12.3 with 1), of 8192
+// keys 15.4 (18.6 with 1, 16.7 with 4).
+constexpr int kMinShare = 2;
 
 // Most tiles the call can have.
 int64_t most_tiles(const MlaDecodeArgs& a, int ctas, int keys) {
@@ -558,8 +564,9 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   const int rows = a.Sq * a.H;
   // A pair of CTAs shares each tile between 128 rows, in the time that one CTA
   // needs for 64: from 65 rows on it halves the passes over the cache (128
-  // sequences x 128 heads: PAIRMEAS).  With at most 64 rows half of its rows would be
-  // padding, for no gain (32 x 64 heads: PAIRMEAS2).
+  // sequences x 128 heads: 181 us, with single CTAs 265).  With at most 64 rows
+  // half of its rows would be padding, and single CTAs are faster (32 x 64 heads:
+  // 58 us, with pairs 65; 128 x 16 heads 83 and 95).
   const bool pair = rows > kRows;
   CUtensorMap q_map, kv_map;
   if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
@@ -576,8 +583,7 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
       return NVFP4MOE_ERR_SMEM;
     }
   }
-  const int min_share = pair ? kMinShare * kKeys / pair::kKeys : kMinShare;
-  const int ranges = int(std::min<int64_t>(most_ranges, ceil_div(most_tiles(a, ctas, pair ? pair::kKeys : kKeys), min_share)));
+  const int ranges = int(std::min<int64_t>(most_ranges, ceil_div(most_tiles(a, ctas, pair ? pair::kKeys : kKeys), kMinShare)));
   DecodeParams p;
   p.tables = a.tables;
   p.table_stride = a.table_stride;
@@ -597,7 +603,7 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   p.out = static_cast<uint8_t*>(a.out);
   p.lse = a.lse;
   p.ranges = ranges;
-  p.min_share = min_share;
+  p.min_share = kMinShare;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.heads = reinterpret_cast<Head*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + kMlaDecodeHeadBytes);
@@ -622,16 +628,26 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   }
   const int64_t items = int64_t(a.B) * p.blocks;
   if (err == cudaSuccess && ranges > 1) {
-    // Few items of many pieces are joined by item, several warps a row; more
-    // items by the borders that cut them, a warp a row.
+    // Few items of many pieces are joined by item, several warps a row (two
+    // sequences of 116000 keys: 84 us, by the borders 126); more items by the
+    // borders that cut them, a warp a row (128 sequences of 5000 keys: 181 us,
+    // by item 206).
     const int most = std::min(kRows * ctas, rows);
     const bool by_item = items * 4 <= ranges;
+    // From 16 pieces on, and while the blocks are resident at once, eight warps
+    // share a quarter of a row: one sequence of 32768 keys with 16 heads takes
+    // 21.2 us, 33.8 with four warps a row, eight with 16 heads 46.9 and 48.7; but
+    // eight with 64 heads (2048 blocks) 56.7 and 52.6, eight of 1024 keys (eight
+    // pieces each) 11.8 and 10.6.
+    const bool wide = items * 16 <= ranges && items * most * 4 <= num_sms * 8;
     const int across = by_item ? int(items) : ranges - 1;
     if (pair)  // a task is eight rows x 128 values
       err = launch_kernel(by_item ? join_pair_kernel<T, true> : join_pair_kernel<T, false>,
                           dim3(across, by_item ? (most + 7) / 8 * 4 : (most + 7) / 8), dim3(by_item ? 2 * kPairJoinThreads : kPairJoinThreads), 0, st, false, p);
+    else if (wide)
+      err = launch_kernel(join_kernel<T, 8>, dim3(across, most * 4), dim3(kJoinThreads), 0, st, false, p);
     else
-      err = launch_kernel(by_item ? join_kernel<T, true> : join_kernel<T, false>,
+      err = launch_kernel(by_item ? join_kernel<T, 4> : join_kernel<T, 1>,
                           dim3(across, by_item ? (most + 1) / 2 : (most + 7) / 8), dim3(kJoinThreads), 0, st, false, p);
   }
   if (err != cudaSuccess) {

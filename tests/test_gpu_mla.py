@@ -219,6 +219,19 @@ def test_decode_ranges_that_cut_sequences(M, B, Sq, H, lens, page):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])       # the same sums in the same order
 
 
+@pytest.mark.parametrize("B,Sq,H,lens,page", [
+    (8, 1, 64, [3000 - 211 * i for i in range(8)], 64), (20, 1, 16, [(397 * i) % 2100 for i in range(20)], 32),
+    (1, 1, 5, [9001], 16), (9, 1, 33, [4000 if i % 4 == 0 else 64 * i for i in range(9)], 64),
+    (1, 2, 60, [7003], 64), (3, 3, 50, [0, 6000, 129], 128)])
+def test_decode_joins_of_few_sequences(M, B, Sq, H, lens, page):
+    """Every way in which partial results are joined: by item with several warps a row, eight warps a quarter row."""
+    c = decode_case(B, Sq, H, lens, page, FP16, seed=B + 7 * H)
+    ws = torch.full((M.mla_decode_workspace_size(),), 255, dtype=torch.uint8, device="cuda")   # NaN everywhere
+    out, lse = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE, workspace=ws)
+    M.sync_status()
+    decode_check(c, out, lse)
+
+
 def test_decode_random_shapes(M):
     rng = random.Random(3)
     for i in range(24):

@@ -75,9 +75,10 @@ int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, in
  * A row that sees no key gets zeros and -inf.  Key j of sequence b is row j %
  * page_size of page block_tables[b * table_stride + j / page_size]; entries
  * past a sequence's last page and cache rows past its last key are never used,
- * whatever they hold.  A page id outside [0, num_pages) reads as zero rows, a
- * length is clamped to [0, max_pages * page_size]; both raise
- * NVFP4MOE_ERR_DEVICE_DATA.
+ * whatever they hold; with Sq > 1 the rows of all Sq new tokens must be finite
+ * (a weight of zero is multiplied with those that a row does not see).  A page
+ * id outside [0, num_pages) reads as zero rows, a length is clamped to [0,
+ * max_pages * page_size]; both raise NVFP4MOE_ERR_DEVICE_DATA.
  * q [B, Sq, H, 576], out [B, Sq, H, 512], lse float32 [B, Sq, H], cache
  * [num_pages, page_size, 576], all contiguous; block_tables device int32;
  * seq_lens device int32 [B].  The softmax's weights are rounded to dtype for

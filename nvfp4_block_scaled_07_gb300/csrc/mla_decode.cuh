@@ -33,7 +33,7 @@ struct DecodeParams {
   int B, Sq, H, rows, blocks;                 // rows = Sq * H of a sequence, in `blocks` row blocks
   int ctas;                                   // CTAs of a range: one with 64 rows, or a pair with 128
   int num_pages, page, log_page, max_pages;
-  float scale_log2, scale;
+  float scale_log2;
   uint8_t* out;                               // [B, rows, 512]
   float* lse;                                 // [B, rows]
   int ranges, min_share;

@@ -9,19 +9,20 @@
 //   O [128 x 512] += P x C[:, :512]     N = 256, twice: each CTA stages 256 of
 //                                       the values of all 128 keys
 // 36 MMAs of 36 cycles and 16 of 68 a tile of 128 keys, 2360 cycles, against
-// the 2820 in which HBM delivers it to a pair.  Shared memory moves 400 KB a
-// tile (operands of S 144, of P V 96, copies 136, weights 24): 3100 cycles at
-// 128 bytes a clock, the tightest of the three.  Tiles of 64 keys in two
-// stages would read Q twice as often (measured 187 us against PAIR128 for
-// 128 sequences x 128 heads).
+// the 2820 in which HBM delivers it to a pair.  Measured: about 4000.  128
+// sequences x 128 heads of 2048 to 8192 keys (803 MB) take 168 us, 4.8 TB/s, with the
+// tensor pipe active for 48 % of the time, DRAM for 59 % and shared memory's
+// banks for a third: no unit is full, the way of a tile through one buffer of
+// each operand (copy, S, softmax, P V, free) is what bounds.  Two stages of 64
+// keys fit as well, but read Q twice as often: 187 us where 128 keys took 182.
 // A CTA's share of a tile is 72 KB for S and 64 KB for P V (its own keys'
 // values twice, so that both CTAs use the same descriptors).  S frees its
 // rows while the softmax and P V of the tile still run, so that S is always a
 // tile ahead.
 //
-// Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-11
-// TMA producers, warp 12 tensor-memory owner and, in the even CTA, issuer of
-// S, warp 13 issuer of P V there.
+// Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-9
+// TMA producers of whole rows, 10-13 of values, warp 14 tensor-memory owner
+// and, in the even CTA, issuer of S, warp 15 issuer of P V there.
 // The even CTA's barriers count both CTAs' copies of whole rows and softmax
 // arrivals; commits arrive in both.  The copies of values count in their own
 // CTA, whose softmax warps wait for them before they arrive: rows past the

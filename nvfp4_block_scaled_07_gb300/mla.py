@@ -127,7 +127,7 @@ def mla_append(latent, k_rope, positions, slots, rope_table, cache, norm_weight=
     if q_rope is not None:
         H = q_rope.shape[1]
         if q_out is None:
-            q_out = q_rope.new_empty((T, H, ROPE))
+            q_out = torch.empty((T, H, ROPE), dtype=t, device=latent.device)
         if H:
             q_at = _strided(q_rope, t, (T, H, ROPE), "q_rope", dev)
             q_out_at = _strided(q_out, t, (T, H, ROPE), "q_out", dev)
@@ -166,17 +166,17 @@ def mla_decode(q, cache, block_tables, seq_lens, scale, out=None, lse=None, work
     if max_pages > 1 and step[1] != 1:
         raise ValueError(f"block_tables: strides {step}, rows must be contiguous")
     if out is None:                           # what is made here needs no check
-        out = q.new_empty((B, Sq, H, LATENT))
+        out = torch.empty((B, Sq, H, LATENT), dtype=t, device=q.device)
         out_at = out.data_ptr()
     else:
         out_at = _dense(out, t, (B, Sq, H, LATENT), "out", dev)
     if lse is None:
-        lse = q.new_empty((B, Sq, H), dtype=torch.float32)
+        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
         lse_at = lse.data_ptr()
     else:
         lse_at = _dense(lse, torch.float32, (B, Sq, H), "lse", dev)
     if workspace is None:
-        workspace = q.new_empty((_DECODE_WORKSPACE,), dtype=torch.uint8)
+        workspace = torch.empty((_DECODE_WORKSPACE,), dtype=torch.uint8, device=q.device)
         ws_at, ws_bytes = workspace.data_ptr(), _DECODE_WORKSPACE
     else:
         ws_bytes = workspace.numel()
@@ -202,12 +202,12 @@ def mla_prefill(q, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, 
     if B < 0:
         raise ValueError("cu_q: one entry more than there are sequences")
     if out is None:
-        out = q.new_empty((Tq, H, VALUE))
+        out = torch.empty((Tq, H, VALUE), dtype=t, device=q.device)
         out_at = out.data_ptr()
     else:
         out_at = _dense(out, t, (Tq, H, VALUE), "out", dev)
     if lse is None:
-        lse = q.new_empty((Tq, H), dtype=torch.float32)
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
         lse_at = lse.data_ptr()
     else:
         lse_at = _dense(lse, torch.float32, (Tq, H), "lse", dev)

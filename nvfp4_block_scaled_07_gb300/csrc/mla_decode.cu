@@ -577,7 +577,7 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   const bool pair = rows > kRows;
   CUtensorMap q_map, kv_map;
   if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
-      !encode_rows<T>(&kv_map, a.cache, int64_t(a.num_pages) * a.page, 8, 9)) {
+      !encode_rows<T>(&kv_map, a.cache, int64_t(a.num_pages) * a.page, 8, pair ? 9 / pair::kParts : 9)) {
     set_error_detail("cuTensorMapEncodeTiled failed or is unavailable");
     return NVFP4MOE_ERR_CUDA;
   }

@@ -39,6 +39,7 @@ namespace {
 namespace pair {
 constexpr int kKeys = 128;                    // keys of a tile
 constexpr int kPieces = 8;                    // of a tile: 16 keys each
+constexpr int kParts = 3;                     // of a row: 192 values each
 constexpr int kProducer = 8, kIssuer = 14;    // first producer warp; the MMA warps, S and P V
 constexpr int kThreads = 512;
 constexpr int kSoftmaxThreads = 256;
@@ -58,7 +59,7 @@ constexpr int kSmem = kPOff + 2 * kPBytes;
 
 struct Control {
   // counted in the even CTA only: k_full, q_full, s_free, p_full, o_free
-  uint64_t k_full, v_full, k_empty, v_empty[kPieces];
+  uint64_t k_full[kParts], v_full, k_empty[kParts], v_empty[kPieces];
   uint64_t q_full, q_empty, s_full[2], s_free[2], p_full, pv_done, o_free, drain;
   uint32_t tmem, pad;
   WaitCtl wait;
@@ -98,9 +99,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
   auto bar = [&](const uint64_t& b) { return base + uint32_t(reinterpret_cast<const uint8_t*>(&b) - smem); };
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bar(ctl->k_full), 2);
+    for (int i = 0; i < kParts; ++i) {
+      ptx::mbar_init(bar(ctl->k_full[i]), 2);
+      ptx::mbar_init(bar(ctl->k_empty[i]), 1);
+    }
     ptx::mbar_init(bar(ctl->v_full), 4);
-    ptx::mbar_init(bar(ctl->k_empty), 1);
     for (int i = 0; i < kPieces; ++i) ptx::mbar_init(bar(ctl->v_empty[i]), 1);
     ptx::mbar_init(bar(ctl->q_full), 1);
     ptx::mbar_init(bar(ctl->q_empty), 1);
@@ -160,9 +163,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         for (int b = lane; b < p.B; b += 32)
           if (__ldg(p.lens + b) != seq_len(p, b)) atomicOr(&g_decode_flags, kFlagBadData);
       const int piece0 = 4 * int(rank) + 2 * sub;  // the warp's two pieces, one looked up by even lanes, one by odd
-      const uint32_t kf = ptx::mapa(bar(ctl->k_full), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
+      const uint32_t kf = ptx::mapa(bar(ctl->k_full[0]), 0), qf = ptx::mapa(bar(ctl->q_full), 0);
       const uint32_t dst = base + kKOff + 4 * sub * kGroup;
-      uint32_t seg = 0;
+      uint32_t seg = 0, begun = 0;            // parts begun
       int row = cur.valid() ? look_up(cur, piece0 + (lane & 1)) : 0;
       while (cur.valid()) {
         if (sub == 0 && cur.is_first()) {
@@ -178,16 +181,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         Cursor<kKeys> nxt = cur;
         nxt.next(p);
         const int next = nxt.valid() ? look_up(nxt, piece0 + (lane & 1)) : 0;
-        if (!wait_warp(bar(ctl->k_empty), (g & 1u) ^ 1u, wctl)) break;
         // both CTAs' groups 4 sub .. 4 sub + 3 of their eight
         const int mine = min(4, max(0, groups - 4 * sub)), theirs = min(4, max(0, groups - 8 - 4 * sub));
-        arrive_expect_tx(el0, bar(ctl->k_full), uint32_t((mine + theirs) * kGroup));
         const int n = rank ? theirs : mine;
+        const int from0 = uniform(row), from1 = __shfl_sync(kFull, row, 1);
+        bool ok = true;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int from = __shfl_sync(kFull, row, i >> 1);
-          if (i < n) tma_load_3d_pair(el, dst + i * kGroup, &kv_map, kf, 0, min(from, oob - 8 * (i & 1)) + 8 * (i & 1), 0);
+        for (int part = 0; part < kParts; ++part) {
+          ok = ok && wait_warp(bar(ctl->k_empty[part]), (g & 1u) ^ 1u, wctl);
+          if (!ok) break;
+          ++begun;
+          arrive_expect_tx(el0, bar(ctl->k_full[part]), uint32_t((mine + theirs) * (kGroup / kParts)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int from = i < 2 ? from0 : from1;
+            if (i < n)
+              tma_load_3d_pair(el, dst + i * kGroup + part * (kGroup / kParts), &kv_map, kf + 8 * part, 0,
+                               min(from, oob - 8 * (i & 1)) + 8 * (i & 1), part * (9 / kParts));
+          }
         }
+        if (!ok) break;
         ++g;
         cur = nxt;
         row = next;
@@ -204,7 +217,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       // Every copy has landed before the pair leaves: the even CTA's barriers
       // count both CTAs' (bounded, since an abort may leave a phase incomplete).
       if (rank == 0 && seg) drain_phase(bar(ctl->q_full), (seg - 1) & 1u);
-      if (rank == 0 && g) drain_phase(bar(ctl->k_full), (g - 1) & 1u);
+#pragma unroll
+      for (uint32_t part = 0; part < kParts; ++part) {
+        const uint32_t n = (begun + kParts - 1 - part) / kParts;
+        if (rank == 0 && n) drain_phase(bar(ctl->k_full[part]), (n - 1) & 1u);
+      }
     } else {
       bool ok = true;
       const uint32_t vf = bar(ctl->v_full), dst = base + kVOff + 4 * sub * kVGroup;
@@ -242,16 +259,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
         const uint32_t s = g & 1u;
         if (cur.is_first() && !wait_warp(bar(ctl->q_full), seg++ & 1u, wctl)) break;
-        if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl) || !wait_warp(bar(ctl->k_full), g & 1u, wctl)) break;
-        ptx::tc_fence_after();
+        if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
         const uint32_t b = desc_sw128(base + kKOff, 16);
+        bool ok = true;
 #pragma unroll
-        for (int c = 0; c < 9; ++c)
+        for (int part = 0; part < kParts; ++part) {
+          ok = ok && wait_warp(bar(ctl->k_full[part]), g & 1u, wctl);
+          if (!ok) break;
+          ptx::tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_pair<1024, kGroup>(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k, b + c * (1024 >> 4) + 2 * k,
-                         idesc, c + k > 0);
-        tc_commit_pair(el, bar(ctl->k_empty));
+          for (int c = part * (9 / kParts); c < (part + 1) * (9 / kParts); ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_pair<1024, kGroup>(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k,
+                                         b + c * (1024 >> 4) + 2 * k, idesc, c + k > 0);
+          tc_commit_pair(el, bar(ctl->k_empty[part]));
+        }
+        if (!ok) break;
         tc_commit_pair(el, bar(ctl->s_full[s]));
         if (cur.is_last()) tc_commit_pair(el, bar(ctl->q_empty));
         cur.next(p);

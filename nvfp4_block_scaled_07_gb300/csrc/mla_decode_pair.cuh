@@ -186,7 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         const int n = rank ? theirs : mine;
         const int from0 = uniform(row), from1 = __shfl_sync(kFull, row, 1);
         bool ok = true;
-#pragma unroll
+#pragma unroll 1
         for (int part = 0; part < kParts; ++part) {
           ok = ok && wait_warp(bar(ctl->k_empty[part]), (g & 1u) ^ 1u, wctl);
           if (!ok) break;
@@ -262,17 +262,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         if (!wait_warp(bar(ctl->s_free[s]), ((g >> 1) & 1u) ^ 1u, wctl)) break;
         const uint32_t b = desc_sw128(base + kKOff, 16);
         bool ok = true;
-#pragma unroll
+#pragma unroll 1
         for (int part = 0; part < kParts; ++part) {
           ok = ok && wait_warp(bar(ctl->k_full[part]), g & 1u, wctl);
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll
-          for (int c = part * (9 / kParts); c < (part + 1) * (9 / kParts); ++c)
+          for (int c = 0; c < 9 / kParts; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16_pair<1024, kGroup>(el, tmem + kSCol + s * kSCols, a + c * (64 * 128 >> 4) + 2 * k,
-                                         b + c * (1024 >> 4) + 2 * k, idesc, c + k > 0);
+              mma_f16_pair<1024, kGroup>(el, tmem + kSCol + s * kSCols,
+                                         a + part * (9 / kParts * 64 * 128 >> 4) + c * (64 * 128 >> 4) + 2 * k,
+                                         b + part * (9 / kParts * 1024 >> 4) + c * (1024 >> 4) + 2 * k, idesc,
+                                         c + k ? 1u : uint32_t(part));
           tc_commit_pair(el, bar(ctl->k_empty[part]));
         }
         if (!ok) break;

@@ -291,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         if (cur.is_first() && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
         ptx::tc_fence_after();
         const uint32_t more = cur.is_first() ? 0u : 1u;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kPieces; ++k) {   // 16 keys: 32 bytes of P, two groups of values
 #pragma unroll
           for (int h = 0; h < 2; ++h)         // 256 values
@@ -405,6 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       if (keys < kKeys) {
         const int from = max(keys, 0);
         const uint32_t v = base + kVOff;
+#pragma unroll 1
         for (int i = threadIdx.x; i < (kKeys - from) * 32; i += kSoftmaxThreads) {
           const int k = from + (i >> 5);      // 32 pieces of 16 bytes a key: eight in each of four atoms
           ptx::sts128(v + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);

@@ -571,9 +571,9 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   const int rows = a.Sq * a.H;
   // A pair of CTAs shares each tile between 128 rows, in the time that one CTA
   // needs for 64: from 65 rows on it halves the passes over the cache (128
-  // sequences x 128 heads: 181 us, with single CTAs 265).  With at most 64 rows
+  // sequences x 128 heads: 155 us, with single CTAs 252).  With at most 64 rows
   // half of its rows would be padding, and single CTAs are faster (32 x 64 heads:
-  // 58 us, with pairs 65; 128 x 16 heads 83 and 95).
+  // 47.8 us, with pairs 50.8; 128 x 16 heads 66 and 79).
   const bool pair = rows > kRows;
   CUtensorMap q_map, kv_map;
   if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
@@ -636,8 +636,8 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   if (err == cudaSuccess && ranges > 1) {
     // Few items of many pieces are joined by item, several warps a row (two
     // sequences of 116000 keys: 84 us, by the borders 126); more items by the
-    // borders that cut them, a warp a row (128 sequences of 5000 keys: 181 us,
-    // by item 206).
+    // borders that cut them, a warp a row (128 sequences of 5000 keys: 181 us, by
+    // item 206; all from cold caches).
     const int most = std::min(kRows * ctas, rows);
     const bool by_item = items * 4 <= ranges;
     // From 16 pieces on, and while the blocks are resident at once, eight warps

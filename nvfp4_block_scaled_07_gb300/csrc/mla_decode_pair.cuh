@@ -9,16 +9,19 @@
 //   O [128 x 512] += P x C[:, :512]     N = 256, twice: each CTA stages 256 of
 //                                       the values of all 128 keys
 // 36 MMAs of 36 cycles and 16 of 68 a tile of 128 keys, 2360 cycles, against
-// the 2820 in which HBM delivers it to a pair.  Measured: about 4000.  128
-// sequences x 128 heads of 2048 to 8192 keys (803 MB) take 168 us, 4.8 TB/s, with the
-// tensor pipe active for 48 % of the time, DRAM for 59 % and shared memory's
-// banks for a third: no unit is full, the way of a tile through one buffer of
-// each operand (copy, S, softmax, P V, free) is what bounds.  Two stages of 64
-// keys fit as well, but read Q twice as often: 187 us where 128 keys took 182.
+// the 2820 in which HBM delivers it to a pair.  Measured: about 3400.  128
+// sequences x 128 heads of 2048 to 8192 keys (803 MB) take 155 us, 5.2 TB/s, with the
+// tensor pipe active for 54 % of the time, DRAM for 70 % and shared memory's
+// banks for 40 %: what bounds is the way of the rows through one buffer, MMAs
+// of a part 430 cycles, its release 850, its copy 2000.  Two stages of 64 keys
+// fit as well, but read Q twice as often: 187 us where 128 keys took 182.
 // A CTA's share of a tile is 72 KB for S and 64 KB for P V (its own keys'
-// values twice, so that both CTAs use the same descriptors).  S frees its
-// rows while the softmax and P V of the tile still run, so that S is always a
-// tile ahead.
+// values twice, so that both CTAs use the same descriptors).  S frees its rows
+// in three parts of 192 values, so that the next tile's are copied while it
+// still reads the others and while softmax and P V of the tile run (whole rows:
+// 168 us where parts took 159; nine parts, boxes of 1 KB: 339).
+// All roles share the instruction cache: loops whose bodies are not unrolled
+// gave another 4 us.
 //
 // Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-9
 // TMA producers of whole rows, 10-13 of values, warp 14 tensor-memory owner

@@ -429,6 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         ctl->part[who][r] = l;                // the maxima have been read
         bar_sync(2, kSoftmaxThreads);
         const float sum = (ctl->part[0][r] + ctl->part[1][r]) + (ctl->part[2][r] + ctl->part[3][r]);
+        bar_sync(2, kSoftmaxThreads);         // all have read the sums: the next tile's maxima take their place
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         if (who == 0 && r < rows) {
           const float e = sum == 0.0f ? -INFINITY : m + log2f(sum);

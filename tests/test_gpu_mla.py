@@ -232,6 +232,22 @@ def test_decode_joins_of_few_sequences(M, B, Sq, H, lens, page):
     decode_check(c, out, lse)
 
 
+@pytest.mark.parametrize("Sq,H,dtype,top", [(1, 128, BF16, 128), (1, 96, FP16, 128), (2, 64, BF16, 128), (1, 128, BF16, 300)])
+def test_decode_many_short_sequences_on_pairs(M, Sq, H, dtype, top):
+    """Ranges of many items back to back, most of one tile: an item's sums are read before the next item's maxima
+    take their place.  The same bits each time."""
+    B = 1000
+    c = decode_case(B, Sq, H, [(37 * i) % top + 1 for i in range(B)], 16, dtype, seed=H + top)
+    # scores of very different sizes from one item to the next, so that a maximum taken for a sum would show
+    c["q"] *= torch.linspace(0.1, 6.0, 7, device="cuda")[torch.arange(B, device="cuda") % 7].to(dtype)[:, None, None, None]
+    out, lse = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE)
+    decode_check(c, out, lse, only=range(0, B, 13))
+    for _ in range(20):
+        again = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    M.sync_status()
+
+
 def test_decode_random_shapes(M):
     rng = random.Random(3)
     for i in range(24):

@@ -290,6 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const uint32_t a = desc_sw128(base + kPOff, 16), b = desc_sw128(base + kVOff, 1024);
       for (uint32_t g = 0, seg = 0; cur.valid(); ++g) {
         if (!wait_warp(bar(ctl->p_full), g & 1u, wctl)) break;
+        ptx::mbar_acquire_smem(bar(ctl->p_full), g & 1u);
         // the previous segment's accumulator has been read
         if (cur.is_first() && seg++ && !wait_warp(bar(ctl->o_free), seg & 1u, wctl)) break;
         ptx::tc_fence_after();
@@ -414,14 +415,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           ptx::sts128(v + (k >> 3) * kVGroup + ((i >> 3) & 3) * 1024 + (k & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
         }
       }
-      // What the arrival announces lies in this CTA: weights and zeros in its
-      // shared memory, ordered for the tensor core by the proxy fence, and
-      // tensor-memory reads, by the tcgen05 fence.  A cluster-scope release
-      // besides took 2000 cycles.
+      // What the arrival announces lies in this CTA, and the even CTA's issuer
+      // has both CTAs' tensor cores use it: weights and zeros in shared memory,
+      // ordered for the tensor core by the proxy fence and across the pair by
+      // the arrival's release, which is restricted to shared memory (a full
+      // cluster-scope release waits for global memory too, some 2000 cycles:
+      // 128 sequences x 128 heads 202 us, even with one warp alone releasing;
+      // like this 154); a rescaled O in tensor memory, by the tcgen05 fence.
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(p_full);
+      if (lane == 0) ptx::mbar_arrive_release_smem(p_full);
       if (last) {
         const bool whole = cur.first == 0 && cur.tile + 1 == cur.tiles;
         const int64_t part = 2 * blockIdx.x + (cur.pos - cur.tile + cur.first == share * range ? 0 : 1);

@@ -122,6 +122,26 @@ __device__ __forceinline__ uint32_t mapa(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same where the waiting CTA goes on to use what this thread, or one that it
+// has synchronised with, wrote to ordinary shared memory before: a release to
+// the cluster, restricted to shared memory, so that it waits for no global
+// store.  The waiter acquires with mbar_acquire_smem.
+__device__ __forceinline__ void mbar_arrive_release_smem(uint32_t cluster_addr) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+      : "memory");
+}
+// After a wait has seen a phase of this CTA's mbarrier complete: the same
+// observation at cluster scope, and the acquire that matches the release above.
+__device__ __forceinline__ void mbar_acquire_smem(uint32_t bar, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%0], %1;\n\t"
+      "fence.acquire.sync_restrict::shared::cluster.cluster;\n\t}" ::"r"(bar),
+      "r"(parity)
+      : "memory");
+}
 // All threads of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -225,6 +225,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         const uint32_t n = (begun + kParts - 1 - part) / kParts;
         if (rank == 0 && n) drain_phase(bar(ctl->k_full[part]), (n - 1) & 1u);
       }
+      // After an abort the odd CTA may have begun a part that the even one did
+      // not, and it cannot wait on the other's barriers: 10 ms cover the copy.
+      if (rank == 1 && cur.valid()) {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - t0 < 10000000ull) {
+        }
+      }
     } else {
       bool ok = true;
       const uint32_t vf = bar(ctl->v_full), dst = base + kVOff + 4 * sub * kVGroup;

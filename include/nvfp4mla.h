@@ -82,7 +82,8 @@ int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, in
  * q [B, Sq, H, 576], out [B, Sq, H, 512], lse float32 [B, Sq, H], cache
  * [num_pages, page_size, 576], all contiguous; block_tables device int32;
  * seq_lens device int32 [B].  The softmax's weights are rounded to dtype for
- * the product with the values; their sum is not.
+ * the product with the values (fp16: to half a step, or 2^-32 of the row's
+ * largest weight if that is more); their sum is not.
  * ws: device scratch of mla_decode_workspace_size() bytes, 256-byte aligned,
  * not initialised; calls that share it must not overlap on the GPU.
  * Limits: page_size a power of two >= 16; num_pages * page_size < 2^31; B, Sq,
@@ -109,7 +110,7 @@ int mla_decode(const void* q, const void* cache, int num_pages, int page_size,
  * contiguous.  cu_q, cu_k device int32 [B + 1], ascending, within [0, Tq] and
  * [0, Tk]: offsets outside are clamped and raise NVFP4MOE_ERR_DEVICE_DATA.
  * Outputs of tokens in no sequence are left untouched.  The softmax's weights
- * are rounded to dtype for the product with the values; their sum is not.
+ * are rounded as in mla_decode.
  * Limits: B, H >= 1, Tq, Tk >= 0, Tq * H and Tk * H < 2^31, (Tq / 256 + B) * H < 2^31
  * (B = 0, Tq = 0 or H = 0 is a no-op); scale > 0 and finite. */
 int mla_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -24,9 +24,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Two 16-bit values in one register, the first in the low half.
+// kLift: log2 of a softmax weight at its row's maximum.  float16 ends at 2^-24,
+// and many small weights beside a large one would vanish in the product with
+// the values but not in their sum: its weights begin at 2^7, so that with a
+// maximum that grew by 2^8 (kGrow) they stay below 2^16.  bfloat16 has the
+// exponents of float32.
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
   static constexpr uint32_t kFormat = 1;  // tcgen05 kind::f16 operand format
+  static constexpr float kLift = 0.0f;
   static constexpr CUtensorMapDataType kMap = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
@@ -39,6 +45,7 @@ template <> struct Elem<__nv_bfloat16> {
 };
 template <> struct Elem<__half> {
   static constexpr uint32_t kFormat = 0;
+  static constexpr float kLift = 7.0f;
   static constexpr CUtensorMapDataType kMap = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   static __device__ __forceinline__ float2 unpack(uint32_t v) {
     return __half22float2(*reinterpret_cast<const __half2*>(&v));

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, lanes = 32 * (warp & 3);
     const uint32_t quarter = uint32_t(lanes) << 16;
     const int r0 = lanes / 2 + (lane >> 2);         // this thread's rows: r0 and r0 + 8
-    float m[2], l[2];                               // running maximum (log2 domain) and half's sum
+    float m[2], l[2];                               // running maximum (log2 domain) less kLift, and half's sum
     uint32_t g = 0;
     // A failed wait is remembered and ends the loop for all warps at the
     // next tile's vote, so that no thread leaves others at a barrier.
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], 2));
         top[i] *= p.scale_log2;
         if (first) m[i] = -INFINITY, l[i] = 0.0f;
-        grew |= top[i] - m[i] > kGrow;        // also from -inf
+        grew |= top[i] - m[i] > kGrow + Elem<T>::kLift;  // also from -inf
         if ((lane & 3) == 0) ctl->half[half][r0 + 8 * i] = top[i];
       }
       // The reference maximum moves only when some row's maximum grew by 2^8:
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bar_any(2, kSoftmaxThreads, dead)) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float mn = fmaxf(m[i], fmaxf(top[i], ctl->half[half ^ 1][r0 + 8 * i]));
+          const float mn = fmaxf(m[i], fmaxf(top[i], ctl->half[half ^ 1][r0 + 8 * i]) - Elem<T>::kLift);
           const float a = mn == m[i] ? 1.0f : exp2_approx(m[i] - mn);
           m[i] = mn;
           l[i] *= a;

@@ -340,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     const int r = 32 * (quarter & 1) + lane, key0 = 64 * upper + 32 * half, who = 2 * upper + half;
     const uint32_t p_full = ptx::mapa(bar(ctl->p_full), 0), o_free = ptx::mapa(bar(ctl->o_free), 0);
     const uint32_t s_free = ptx::mapa(bar(ctl->s_free[0]), 0);
-    float m = 0.0f, l = 0.0f;                 // running maximum (log2 domain) and this quarter's sum
+    float m = 0.0f, l = 0.0f;                 // running maximum (log2 domain) less kLift, and this quarter's sum
     uint32_t g = 0;
     int behind = 0;                           // keys of the sequence that come after the row's token
     // A failed wait is remembered and ends the loop for all warps at the next
@@ -375,9 +375,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       ctl->part[who][r] = top;
       // The reference maximum moves only when some row's maximum grew by 2^8:
       // until then weights of up to 2^8 are as exact as weights of up to 1.
-      if (bar_any(1, kSoftmaxThreads, first || dead || top - m > kGrow)) {
+      if (bar_any(1, kSoftmaxThreads, first || dead || top - m > kGrow + Elem<T>::kLift)) {
         if (bar_any(2, kSoftmaxThreads, dead)) break;
-        const float mn = fmaxf(m, fmaxf(fmaxf(ctl->part[0][r], ctl->part[1][r]), fmaxf(ctl->part[2][r], ctl->part[3][r])));
+        const float tops = fmaxf(fmaxf(ctl->part[0][r], ctl->part[1][r]), fmaxf(ctl->part[2][r], ctl->part[3][r]));
+        const float mn = fmaxf(m, tops - Elem<T>::kLift);
         const float a = mn == m ? 1.0f : exp2_approx(m - mn);
         m = mn;
         l *= a;

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
     const uint32_t s_col = tmem + lanes + t * kKeys, o_col = tmem + lanes + 256 + t * kValueDim;
     const int limit = index < nq ? min(nk, p.causal ? shift + index + 1 : nk) : 0;
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY, l = 0.0f;            // running maximum (log2 domain) less kLift, and sum
     bool ok = true;                           // the same for all lanes of a warp
     for (int j = 0; j < n[t]; ++j) {
       ok = __all_sync(kFull, wait_phase<false>(bar(ctl->s_full[t]), j & 1u, wctl));
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           top[c] = fmaxf(fmaxf(top[c], __uint_as_float(s[c][k])), __uint_as_float(s[c][k + 1]));
         top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
       }
-      const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2);
+      const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2 - Elem<T>::kLift);
       // The reference maximum moves only when it grew by 2^8 in some row of
       // the warp: until then weights of up to 2^8 are as exact as of up to 1.
       if (__any_sync(kFull, j == 0 || mn - m > kGrow)) {

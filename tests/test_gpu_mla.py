@@ -280,6 +280,57 @@ def test_decode_scores_that_grow(M, order):
     decode_check(c, out, lse, what=order)
 
 
+# Softmax weights far below a row's largest.  float16 ends at 2^-24 (steps of 2^-24, so off by 2^-25 at most); a row's
+# weights are held against a reference that leaves the largest between 2^7 and 2^15, so that a weight is off by its half
+# step or by 2^-25 / 2^7 of the largest one, whichever is more: keys * 2^-32 * max |v| of a result.  In units of
+# R.check's spread, which it multiplies with half a step:
+def small_weights(spread, keys, v, dtype):
+    return spread + (keys * 2.0 ** -32 * v.abs().amax() / R.half_step(dtype) if dtype == FP16 else 0.0)
+
+
+def sink_rows(n, gap, g, dtype):
+    """Cached rows: key 0 is `gap` above the others, which are alike, and its values are zero; queries of (0, 1)."""
+    rows = torch.zeros(n, 576, device="cuda")
+    rows[1:, :512] = 40.0 + normal(g, n - 1, 512, dtype=torch.float32)
+    rows[0, 512:] = gap / (64 * SCALE)
+    return rows.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("gap", [12.0, 15.0, 17.5, 19.0])
+@pytest.mark.parametrize("H", [16, 128])
+def test_decode_weights_far_below_the_largest(M, H, gap, dtype):
+    n = 120
+    c = decode_case(1, 1, H, [n], 64, dtype, seed=15)
+    rows = sink_rows(n, gap, gen(16), dtype)
+    ids = c["table"][0, :2].long()
+    c["cache"][ids] = torch.cat([rows, rows[:8]]).view(2, 64, 576)
+    c["q"] = torch.cat([torch.zeros(512), torch.ones(64)]).to("cuda", dtype).expand(1, 1, H, 576).contiguous()
+    out, lse = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE)
+    M.sync_status()
+    kv = rows.double()
+    ref = R.attend(c["q"].double().reshape(H, 576), kv, kv[:, :512], SCALE, torch.full((H,), n, device="cuda"))
+    R.check(out.view(H, 512), lse.view(H), ref[0], ref[1], small_weights(ref[2], n, kv[:, :512], dtype), ref[3], dtype, n)
+
+
+@pytest.mark.parametrize("H,tile", [(16, 64), (128, 128)])
+def test_decode_maxima_that_grow_by_just_less_than_a_rescaling(M, H, tile):
+    """The largest weights that float16 has to hold: every tile's maximum is 2^7.9 times the one before."""
+    n = 4 * tile
+    c = decode_case(1, 1, H, [n], 64, FP16, seed=17)
+    g = gen(18)
+    rows = normal(g, n, 576, dtype=torch.float32)
+    rows[:, 512:] = (5.47 * (torch.arange(n, device="cuda") // tile) / (64 * SCALE))[:, None]
+    rows = rows.to(FP16)
+    c["cache"][c["table"][0, :n // 64].long()] = rows.view(-1, 64, 576)
+    c["q"] = torch.cat([torch.zeros(512), torch.ones(64)]).to("cuda", FP16).expand(1, 1, H, 576).contiguous()
+    out, lse = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE)
+    M.sync_status()
+    kv = rows.double()
+    ref = R.attend(c["q"].double().reshape(H, 576), kv, kv[:, :512], SCALE, torch.full((H,), n, device="cuda"))
+    R.check(out.view(H, 512), lse.view(H), ref[0], ref[1], small_weights(ref[2], n, kv[:, :512], FP16), ref[3], FP16, n)
+
+
 def test_decode_non_finite_scores_stay_in_their_rows(M):
     """A NaN query spoils its own row and no other."""
     c = decode_case(2, 1, 16, [200, 90], 16, BF16, seed=12)
@@ -430,6 +481,39 @@ def test_prefill_scores_that_grow(M, order):
     out, lse = prefill_run(M, c)
     M.sync_status()
     prefill_check(c, out, lse, what=order)
+
+
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("gap", [12.0, 15.0, 17.5, 19.0])
+def test_prefill_weights_far_below_the_largest(M, gap, dtype):
+    n = 300
+    c = prefill_case([(n, n)], 2, dtype, seed=26, pad=0)
+    rows = sink_rows(n, gap, gen(27), dtype)
+    c["up"][..., :128] = 0.0
+    c["up"][..., 128:] = rows[:, None, :128]
+    c["kr"] = rows[:, 512:]
+    c["q"][...] = 0.0
+    c["q"][..., 128:] = 1.0
+    out, lse = prefill_run(M, c)
+    M.sync_status()
+    v, k = rows[:, :128].double(), torch.cat([torch.zeros(n, 128, device="cuda"), rows[:, 512:]], 1).double()
+    ref = R.attend(c["q"][:, 0].double(), k, v, SCALE, torch.arange(1, n + 1, device="cuda"))
+    for h in range(2):
+        R.check(out[:, h], lse[:, h], ref[0], ref[1], small_weights(ref[2], n, v, dtype), ref[3], dtype, n)
+
+
+def test_prefill_maxima_that_grow_by_just_less_than_a_rescaling(M):
+    n = 512
+    c = prefill_case([(n, n)], 1, FP16, seed=28, pad=0)
+    c["up"][..., :128] = 0.0
+    c["kr"] = (5.47 * (torch.arange(n, device="cuda") // 128) / (64 * SCALE))[:, None].expand(n, 64).to(FP16).contiguous()
+    c["q"][..., :128] = 0.0
+    c["q"][..., 128:] = 1.0
+    out, lse = prefill_run(M, c)
+    M.sync_status()
+    v, k = c["up"][:, 0, 128:].double(), torch.cat([c["up"][:, 0, :128], c["kr"]], 1).double()
+    ref = R.attend(c["q"][:, 0].double(), k, v, SCALE, torch.arange(1, n + 1, device="cuda"))
+    R.check(out[:, 0], lse[:, 0], ref[0], ref[1], small_weights(ref[2], n, v, FP16), ref[3], FP16, n)
 
 
 def test_prefill_random_shapes(M):

@@ -263,12 +263,15 @@ class LatentAttention:
 
     def decode(self, x, positions, slots, cache, block_tables, seq_lens, workspace=None):
         """x [B * Sq, D]: the Sq newest tokens of each sequence, seq_lens counting them.  Returns [B * Sq, D]."""
-        B = seq_lens.shape[0]
+        B, tokens = seq_lens.shape[0], x.shape[0]
+        Sq = tokens // B if B else 1
+        if Sq == 0 or tokens != B * Sq:       # before the cache is written
+            raise ValueError(f"x: {tokens} tokens are not as many for each of {B} sequences")
         q, kv = self._project(x)
         absorbed = torch.empty((x.shape[0], self.H, ROW), dtype=x.dtype, device=x.device)
         absorbed[..., :LATENT] = torch.bmm(q[..., :NOPE].transpose(0, 1), self.w_uk).transpose(0, 1)
         self._append(kv, positions, slots, cache, q[..., NOPE:], absorbed[..., LATENT:])
-        out, _ = mla_decode(absorbed.view(B, -1, self.H, ROW), cache, block_tables, seq_lens, self.scale,
+        out, _ = mla_decode(absorbed.view(B, Sq, self.H, ROW), cache, block_tables, seq_lens, self.scale,
                             workspace=workspace)
         heads = torch.bmm(out.view(-1, self.H, LATENT).transpose(0, 1), self.w_uv)
-        return heads.transpose(0, 1).reshape(x.shape[0], -1) @ self.w_o.T
+        return heads.transpose(0, 1).flatten(1) @ self.w_o.T

@@ -89,6 +89,35 @@ def test_prefill_and_decode_follow_the_definition(M, lens):
     assert rel(z, torch.stack([w[-1] for w in want])) < TOL
 
 
+def no_tokens(x):
+    return torch.empty(x, dtype=torch.int32, device="cuda"), torch.empty(x, dtype=torch.int64, device="cuda")
+
+
+def test_empty_batches_give_empty_results(M):
+    """A batch that has drained: no prompts, or no sequences to decode."""
+    a = layer(M)
+    cache = torch.zeros((2, 16, 576), dtype=torch.bfloat16, device="cuda")
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    pos, slots = no_tokens(0)
+    y = a.prefill(x, pos, slots, cache, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    z = a.decode(x, pos, slots, cache, torch.empty((0, 2), dtype=torch.int32, device="cuda"), no_tokens(0)[0])
+    M.sync_status()
+    assert y.shape == z.shape == (0, 256) and y.dtype == z.dtype == torch.bfloat16
+
+
+@pytest.mark.parametrize("tokens,sequences", [(3, 2), (0, 2), (1, 0)])
+def test_decode_refuses_unequal_tokens_before_the_cache_is_written(M, tokens, sequences):
+    a = layer(M)
+    cache = torch.zeros((2, 16, 576), dtype=torch.bfloat16, device="cuda")
+    x = torch.ones((tokens, 256), dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(tokens, device="cuda")
+    with pytest.raises(ValueError, match="tokens"):
+        a.decode(x, at.to(torch.int32), at, cache, torch.zeros((sequences, 2), dtype=torch.int32, device="cuda"),
+                 torch.full((sequences,), 3, dtype=torch.int32, device="cuda"))
+    M.sync_status()
+    assert bool((cache == 0).all())
+
+
 def test_example_block_decodes_what_it_prefills(M):
     from examples import decoder_block as E
     decoded, whole = E.serve(lengths=(37, 130, 5), steps=3)

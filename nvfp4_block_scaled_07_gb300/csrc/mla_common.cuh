@@ -304,6 +304,16 @@ __device__ __forceinline__ void arrive_expect_tx(uint32_t elected, uint32_t bar,
       : "memory");
 }
 
+// Arrive on an mbarrier of the other CTA of a pair; it announces nothing but itself.
+__device__ __forceinline__ void arrive_peer(uint32_t elected, uint32_t cluster_addr) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+      "r"(elected)
+      : "memory");
+}
+
 // 16 lanes x 32 columns of a warp's lane quarter: thread l holds, in r[4i ..
 // 4i+3], columns 8i + 2 (l % 4) + {0, 1} of lane l / 4 and then of lane l / 4 + 8.
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {

@@ -103,7 +103,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kParts; ++i) {
-      ptx::mbar_init(bar(ctl->k_full[i]), 2);
+      ptx::mbar_init(bar(ctl->k_full[i]), 4);
       ptx::mbar_init(bar(ctl->k_empty[i]), 1);
     }
     ptx::mbar_init(bar(ctl->v_full), 4);
@@ -149,7 +149,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     // are looked up while the tile before it waits for its buffers. ----
     const bool rows_role = warp < kProducer + 2;
     const int sub = rows_role ? warp - kProducer : warp - kProducer - 2;
-    const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0u;  // the even CTA tells its barriers what to expect
+    const uint32_t el = elect_one(), el0 = rank == 0 ? el : 0u, el1 = rank ? el : 0u;  // the even CTA tells its barriers what to expect
     const int oob = p.num_pages * p.page;
     // First cache row of piece `piece` (16 keys) of the cursor's tile.
     auto look_up = [&](const Cursor<kKeys>& c, int piece) {
@@ -202,6 +202,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
               tma_load_3d_pair(el, dst + i * kGroup + part * (kGroup / kParts), &kv_map, kf + 8 * part, 0,
                                min(from, oob - 8 * (i & 1)) + 8 * (i & 1), part * (9 / kParts));
           }
+          // The odd CTA's warps arrive too, also where they have no keys to copy:
+          // otherwise a slow one could miss a phase of k_empty, whose parity then
+          // repeats, and the pair would wait until the limit.  (Behind the copies:
+          // ahead of them 128 x 128 took 157 us and not 155.)
+          arrive_peer(el1, kf + 8 * part);
         }
         if (!ok) break;
         ++g;

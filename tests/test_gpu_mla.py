@@ -248,6 +248,24 @@ def test_decode_many_short_sequences_on_pairs(M, Sq, H, dtype, top):
     M.sync_status()
 
 
+@pytest.mark.parametrize("top", [30, 64, 100, 300])
+def test_decode_pairs_whose_odd_cta_has_no_keys_to_copy(M, top):
+    """Tiles of at most 64 (or 96) keys of 128: the odd CTA's warps copy nothing and still keep step with the even one's.
+    Every call writes outputs that hold NaN, and is looked at on its own."""
+    B, H = 3000, 80
+    c = decode_case(B, 1, H, [(53 * i) % top + 1 for i in range(B)], 64, BF16, seed=top)
+    out, lse = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE)
+    M.sync_status()
+    decode_check(c, out, lse, only=range(0, B, 101))
+    got, got_lse = torch.empty_like(out), torch.empty_like(lse)
+    for i in range(30):
+        got.fill_(math.nan)
+        got_lse.fill_(math.nan)
+        M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE, out=got, lse=got_lse)
+        M.sync_status()
+        assert torch.equal(got, out) and torch.equal(got_lse, lse), f"call {i}"
+
+
 def test_decode_random_shapes(M):
     rng = random.Random(3)
     for i in range(24):

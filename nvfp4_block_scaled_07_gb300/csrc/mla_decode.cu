@@ -459,11 +459,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
   if (!kByItem) {
     const Head h = p.heads[blockIdx.x + 1];
     start = h.start, tiles = h.tiles, share = h.share, b = h.b, block = h.block;
-    // no item, or one that an earlier border cuts first
-    if (tiles == 0 || start < int(blockIdx.x) * share) return;
+    if (!border_joins(int(blockIdx.x), start, tiles, share)) return;
   }
   const int first = start / share, last = (start + tiles - 1) / share;
-  if (first == last) return;                  // whole: written by its CTA (also an item that begins at the border)
+  if (first == last) return;                  // whole: written by its CTA
   const int pieces = last - first + 1;
   const int row = int(blockIdx.y) / kParts * (kWarps / SHARE) + warp / SHARE, part = int(blockIdx.y) % kParts;
   const bool live = row < min(kRows, p.rows - block * kRows);

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "mla_common.cuh"
+#include "mla_join.h"
 
 namespace nvfp4moe {
 namespace {

@@ -535,8 +535,7 @@ __global__ void __launch_bounds__((BY_ITEM ? 2 : 1) * kPairJoinThreads) join_pai
   if (!BY_ITEM) {
     const Head h = p.heads[blockIdx.x + 1];
     start = h.start, tiles = h.tiles, share = h.share, b = h.b, block = h.block;
-    // no item, or one that an earlier border cuts first
-    if (tiles == 0 || start < int(blockIdx.x) * share) return;
+    if (!border_joins(int(blockIdx.x), start, tiles, share)) return;
   }
   const int first = start / share, last = (start + tiles - 1) / share;
   if (first == last) return;                  // whole: written by its pair

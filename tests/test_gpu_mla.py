@@ -266,6 +266,16 @@ def test_decode_pairs_whose_odd_cta_has_no_keys_to_copy(M, top):
         assert torch.equal(got, out) and torch.equal(got_lse, lse), f"call {i}"
 
 
+@pytest.mark.parametrize("B,H,n", [(76, 64, 256), (38, 128, 512), (76, 16, 250), (50, 48, 1200)])
+def test_decode_items_that_begin_at_a_border(M, B, H, n):
+    """Sequences of equal length whose tiles are a multiple of a range's (152 SMs), and others near it."""
+    c = decode_case(B, 1, H, [n] * B, 64, BF16, seed=n + H)
+    ws = torch.full((M.mla_decode_workspace_size(),), 255, dtype=torch.uint8, device="cuda")   # NaN everywhere
+    out, lse = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE, workspace=ws)
+    M.sync_status()
+    decode_check(c, out, lse)
+
+
 def test_decode_random_shapes(M):
     rng = random.Random(3)
     for i in range(24):

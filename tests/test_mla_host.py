@@ -1,7 +1,10 @@
 """Host side of the latent-attention calls: the ABI of include/nvfp4mla.h and every refusal, without a GPU."""
 import ctypes
 import os
+import random
 import re
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -133,3 +136,60 @@ def test_rope_table_is_the_rounded_64_bit_angle(M):
         for i in (0, 1, 17, 31):
             a = p * 10000.0 ** (-i / 32)
             assert abs(float(t[p, i]) - math.cos(a)) < 2e-7 and abs(float(t[p, 32 + i]) - math.sin(a)) < 2e-7
+
+
+JOIN = r"""
+#include <cstdio>
+#include <vector>
+#include "mla_join.h"
+// stdin: cases of "ranges min_share items tiles...": prints how often each item is joined
+int main() {
+  int ranges, least, n;
+  while (std::scanf("%d %d %d", &ranges, &least, &n) == 3) {
+    std::vector<int> tiles(n), start(n), joined(n, 0);
+    int total = 0;
+    for (int i = 0; i < n; ++i) {
+      if (std::scanf("%d", &tiles[i]) != 1) return 1;
+      start[i] = total;
+      total += tiles[i];
+    }
+    int share = (total + ranges - 1) / ranges;
+    if (share < least) share = least;
+    for (int c = 0; c + 1 < ranges; ++c) {      // block c looks at the item that range c + 1 begins with
+      const long long pos = (long long)share * (c + 1);
+      int at = 0, k = 0, i = 0;
+      if (pos < total) {
+        while (start[i] + tiles[i] <= pos) ++i;
+        at = start[i], k = tiles[i];
+      }
+      if (nvfp4moe::border_joins(c, at, k, share)) ++joined[i];
+    }
+    for (int i = 0; i < n; ++i) std::printf("%d ", joined[i]);
+    std::printf("\n");
+  }
+}
+"""
+
+
+def test_every_cut_item_is_joined_once(tmp_path):
+    """Items of random sizes, and of sizes that begin and end at the borders of ranges."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    (tmp_path / "join.cpp").write_text(JOIN)
+    csrc = os.path.join(ROOT, "nvfp4_block_scaled_07_gb300", "csrc")
+    subprocess.run([cxx, "-O1", "-I", csrc, str(tmp_path / "join.cpp"), "-o", str(tmp_path / "join")], check=True)
+    rng = random.Random(1)
+    cases = [(152, 2, [4] * 76), (76, 2, [4] * 38), (10, 2, [6] * 4), (10, 2, [20]), (3, 2, [1]), (152, 2, [1] * 1000)]
+    for _ in range(400):
+        top = rng.choice([1, 2, 5, 40, 300])
+        cases.append((rng.randint(1, 160), 2, [rng.randint(1, top) for _ in range(rng.randint(1, 60))]))
+    text = "".join(f"{r} {m} {len(t)} {' '.join(map(str, t))}\n" for r, m, t in cases)
+    got = subprocess.run([str(tmp_path / "join")], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
+    assert len(got) == len(cases)
+    for (ranges, least, tiles), line in zip(cases, got):
+        share, at, want = max(-(-sum(tiles) // ranges), least), 0, []
+        for t in tiles:
+            want.append(int(at // share != (at + t - 1) // share))
+            at += t
+        assert [int(v) for v in line.split()] == want, (ranges, tiles)

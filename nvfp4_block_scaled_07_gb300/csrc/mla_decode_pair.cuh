@@ -253,8 +253,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         ++g;
         if (n > 0) tma_load_4d(el, dst, &v_map, vf, 0, from0, 2 * int(rank), 0);
         if (n > 1) tma_load_4d(el, dst + kVGroup, &v_map, vf, 0, min(from0, oob - 8) + 8, 2 * int(rank), 0);
-        // after an abort the second piece still comes: a phase that was begun has to end
-        ok = wait_warp(bar(ctl->v_empty[2 * sub + 1]), (g & 1u), wctl);
+        // The second piece's buffer is waited for only where it is copied: without
+        // bytes of it the tile does not wait for this warp any more, which could
+        // then miss a phase, whose parity repeats.  After an abort the piece still
+        // comes: a phase that was begun has to end.
+        if (n > 2) ok = wait_warp(bar(ctl->v_empty[2 * sub + 1]), (g & 1u), wctl);
         if (n > 2) tma_load_4d(el, dst + 2 * kVGroup, &v_map, vf, 0, from1, 2 * int(rank), 0);
         if (n > 3) tma_load_4d(el, dst + 3 * kVGroup, &v_map, vf, 0, min(from1, oob - 8) + 8, 2 * int(rank), 0);
         cur = nxt;

@@ -59,7 +59,7 @@ extern "C" {
  * Two tokens of a call must not share a slot.  A position outside [0,
  * max_positions) leaves the token's outputs untouched; a slot >= num_slots
  * leaves the cache untouched; both raise NVFP4MOE_ERR_DEVICE_DATA.
- * Limits: 0 <= T <= 2^30, 0 <= H <= 1024. */
+ * Limits: 0 <= T <= 2^30, 0 <= H <= 1024, T * (1 + ceil(H / 16)) <= 8 * (2^31 - 1). */
 int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
                const void* norm_weight, float eps, const int32_t* positions, const int64_t* slots, int T,
                const float* rope_table, int64_t max_positions, int interleaved, int dtype,

@@ -684,8 +684,9 @@ int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, in
                        (reinterpret_cast<uintptr_t>(positions) & 3) == 0 &&
                        (reinterpret_cast<uintptr_t>(slots) & 7) == 0,
                    NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
-  NVFP4MOE_REQUIRE(int64_t(T) * (1 + ceil_div(H, 8)) < (int64_t(1) << 33), NVFP4MOE_ERR_UNSUPPORTED,
-                   "T = %d with H = %d exceeds the launch's grid", T, H);
+  NVFP4MOE_REQUIRE(mla_append_blocks(T, H) < (int64_t(1) << 31), NVFP4MOE_ERR_UNSUPPORTED,
+                   "T * (1 + ceil(H / 16)) = %lld units are more than a grid of 2^31 - 1 blocks takes",
+                   (long long)T * (1 + ceil_div(H, 16)));
   DeviceInfo d;
   if (int st = current_device(&d)) return st;
   MlaAppendArgs a;

@@ -169,6 +169,7 @@ struct MlaAppendArgs {
   void* q_out;
   int64_t qo_token_stride, qo_head_stride;
 };
+int64_t mla_append_blocks(int T, int H);  // of the launch
 cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t st);
 cudaError_t mla_append_read_and_clear_flags(unsigned* flags);
 

@@ -55,7 +55,7 @@ struct AppendParams {
   int H;
   uint8_t* q_out;
   int64_t qo_token_stride, qo_head_stride;
-  int units;               // units a token: its row and ceil(H / 8) groups of heads
+  int units;               // units a token: its row and ceil(H / 16) groups of heads
 };
 
 // Rotates the eight pairs 8j .. 8j+7 of one head (j = 0..3).  In the
@@ -180,7 +180,11 @@ __global__ void __launch_bounds__(32 * kWarps, 5) append_kernel(const AppendPara
   }
 }
 
+int units_of(int H) { return 1 + (H + kHeadsPerWarp - 1) / kHeadsPerWarp; }
+
 }  // namespace
+
+int64_t mla_append_blocks(int T, int H) { return (int64_t(T) * units_of(H) + kWarps - 1) / kWarps; }
 
 cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t st) {
   AppendParams p;
@@ -205,11 +209,10 @@ cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t st) {
   p.q_out = static_cast<uint8_t*>(a.q_out);
   p.qo_token_stride = 2 * a.qo_token_stride;
   p.qo_head_stride = 2 * a.qo_head_stride;
-  p.units = 1 + (a.H + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  const int64_t blocks = (int64_t(a.T) * p.units + kWarps - 1) / kWarps;
+  p.units = units_of(a.H);
   auto kernel = a.fp16 ? (a.interleaved ? append_kernel<__half, true> : append_kernel<__half, false>)
                        : (a.interleaved ? append_kernel<__nv_bfloat16, true> : append_kernel<__nv_bfloat16, false>);
-  return launch_kernel(kernel, dim3(unsigned(blocks)), dim3(32 * kWarps), 0, st, false, p);
+  return launch_kernel(kernel, dim3(unsigned(mla_append_blocks(a.T, a.H))), dim3(32 * kWarps), 0, st, false, p);
 }
 
 cudaError_t mla_append_read_and_clear_flags(unsigned* flags) {

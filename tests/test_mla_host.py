@@ -75,6 +75,16 @@ def test_append_refusals(M, change, code):
     assert status(M._lib.mla_append, APPEND, **change) == code
 
 
+@pytest.mark.parametrize("T,H,fits", [(1 << 27, 1024, True), (1 << 30, 16, True), (1 << 30, 224, True),
+                                      (264305000, 1024, True), (264306000, 1024, False), (1 << 30, 240, False)])
+def test_append_takes_what_its_grid_takes(M, T, H, fits):
+    """8 units a block, a unit is a token's row or 16 of its heads, 2^31 - 1 blocks: what fits is not refused for its size
+    (and then ends here for want of a device)."""
+    _no_device()
+    assert fits == (T * (1 + -(-H // 16)) <= 8 * (2 ** 31 - 1))
+    assert (status(M._lib.mla_append, APPEND, T=T, H=H) != 2) == fits
+
+
 DECODE = dict(q=D, cache=D, num_pages=8, page=64, tables=D, stride=4, max_pages=4, lens=D, B=2, Sq=1, H=16, scale=0.1,
               dtype=0, out=D, lse=D, ws=D, ws_bytes=1 << 30, stream=None)
 

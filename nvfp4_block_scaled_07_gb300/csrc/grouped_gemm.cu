@@ -1928,11 +1928,8 @@ cudaError_t launch_wait_selftest(uint32_t expected, uint32_t arrivals, cudaStrea
   return cudaGetLastError();
 }
 
-cudaError_t gemm_read_and_clear_flags(unsigned* flags) {
-  unsigned zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbol(flags, g_gemm_flags, sizeof(unsigned));
-  if (err != cudaSuccess) return err;
-  return cudaMemcpyToSymbol(g_gemm_flags, &zero, sizeof(unsigned));
+cudaError_t gemm_flags_address(unsigned** at) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_gemm_flags);
 }
 
 }  // namespace nvfp4moe

@@ -94,7 +94,7 @@ cudaError_t launch_finalize(const void* y, const int32_t* flat_to_perm, const fl
 cudaError_t launch_finalize_f32(float* acc, int64_t n, void* out, int num_sms, cudaStream_t st);
 
 // Reads and clears the sticky device flags of the kernels in kernels_prep.cu.
-cudaError_t prep_read_and_clear_flags(unsigned* flags);
+cudaError_t prep_flags_address(unsigned** at);
 
 struct GemmArgs {
   const uint8_t* a_packed;
@@ -144,7 +144,7 @@ int launch_grouped_gemm(const GemmArgs& a, int num_sms, int smem_optin, cudaStre
 constexpr int64_t kWeightBoxBytes = 128 * 128;
 cudaError_t launch_tile_weights(const uint8_t* w_packed, int64_t rows, int K, uint8_t* w_tiled, int num_sms,
                                 cudaStream_t st);
-cudaError_t gemm_read_and_clear_flags(unsigned* flags);
+cudaError_t gemm_flags_address(unsigned** at);
 
 // ---- latent attention (mla_*.cu) --------------------------------------------
 struct MlaAppendArgs {
@@ -171,7 +171,7 @@ struct MlaAppendArgs {
 };
 int64_t mla_append_blocks(int T, int H);  // of the launch
 cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t st);
-cudaError_t mla_append_read_and_clear_flags(unsigned* flags);
+cudaError_t mla_append_flags_address(unsigned** at);
 
 // Workspace of mla_decode: what each CTA's range begins with, then two
 // partial results (64 log-sums, 64 x 512 float32) a CTA.
@@ -195,7 +195,7 @@ struct MlaDecodeArgs {
 };
 // Returns 0 or an NVFP4MOE_ERR_* code (message via set_error_detail).
 int launch_mla_decode(const MlaDecodeArgs& a, int num_sms, cudaStream_t st);
-cudaError_t mla_decode_read_and_clear_flags(unsigned* flags);
+cudaError_t mla_decode_flags_address(unsigned** at);
 
 struct MlaPrefillArgs {
   const void* q;          // [Tq, H, 192], strides in elements
@@ -216,7 +216,7 @@ struct MlaPrefillArgs {
   float* lse;
 };
 int launch_mla_prefill(const MlaPrefillArgs& a, cudaStream_t st);
-cudaError_t mla_prefill_read_and_clear_flags(unsigned* flags);
+cudaError_t mla_prefill_flags_address(unsigned** at);
 
 // Per-thread error message used by nvfp4moe_last_error_detail().
 void set_error_detail(const char* fmt, ...);

@@ -1348,11 +1348,8 @@ cudaError_t launch_permute_static_scratch(int32_t* base, const int32_t* topk_idx
                         flat_to_perm, a_packed, a_scales, rows_capacity, rank, seg_count, seg_base, num_sms, st);
 }
 
-cudaError_t prep_read_and_clear_flags(unsigned* flags) {
-  unsigned zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbol(flags, g_prep_flags, sizeof(unsigned));
-  if (err != cudaSuccess) return err;
-  return cudaMemcpyToSymbol(g_prep_flags, &zero, sizeof(unsigned));
+cudaError_t prep_flags_address(unsigned** at) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_prep_flags);
 }
 
 }  // namespace nvfp4moe

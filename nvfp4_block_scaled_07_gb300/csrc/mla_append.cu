@@ -215,11 +215,8 @@ cudaError_t launch_mla_append(const MlaAppendArgs& a, cudaStream_t st) {
   return launch_kernel(kernel, dim3(unsigned(mla_append_blocks(a.T, a.H))), dim3(32 * kWarps), 0, st, false, p);
 }
 
-cudaError_t mla_append_read_and_clear_flags(unsigned* flags) {
-  unsigned zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbol(flags, g_append_flags, sizeof(unsigned));
-  if (err != cudaSuccess) return err;
-  return cudaMemcpyToSymbol(g_append_flags, &zero, sizeof(unsigned));
+cudaError_t mla_append_flags_address(unsigned** at) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_append_flags);
 }
 
 }  // namespace nvfp4moe

@@ -672,11 +672,8 @@ int launch_mla_decode(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   return a.fp16 ? launch<__half>(a, num_sms, st) : launch<__nv_bfloat16>(a, num_sms, st);
 }
 
-cudaError_t mla_decode_read_and_clear_flags(unsigned* flags) {
-  unsigned zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbol(flags, g_decode_flags, sizeof(unsigned));
-  if (err != cudaSuccess) return err;
-  return cudaMemcpyToSymbol(g_decode_flags, &zero, sizeof(unsigned));
+cudaError_t mla_decode_flags_address(unsigned** at) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_decode_flags);
 }
 
 }  // namespace nvfp4moe

@@ -520,11 +520,8 @@ int launch_mla_prefill(const MlaPrefillArgs& a, cudaStream_t st) {
   return a.fp16 ? launch<__half>(a, st) : launch<__nv_bfloat16>(a, st);
 }
 
-cudaError_t mla_prefill_read_and_clear_flags(unsigned* flags) {
-  unsigned zero = 0;
-  cudaError_t err = cudaMemcpyFromSymbol(flags, g_prefill_flags, sizeof(unsigned));
-  if (err != cudaSuccess) return err;
-  return cudaMemcpyToSymbol(g_prefill_flags, &zero, sizeof(unsigned));
+cudaError_t mla_prefill_flags_address(unsigned** at) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_prefill_flags);
 }
 
 }  // namespace nvfp4moe

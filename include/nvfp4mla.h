@@ -51,8 +51,9 @@ extern "C" {
  * with interleaved = 1 and (i, i + 32) with 0.  The caller makes the table
  * (any base or scaling of the angles).
  * latent [T, 512], k_rope [T, 64], q_rope and q_out [T, H, 64]: innermost
- * dimension contiguous, the given strides multiples of 8.  q_out may be
- * q_rope itself (same strides) and must not overlap it otherwise.
+ * dimension contiguous, the given strides multiples of 8 (0 in an input: the
+ * same row again).  q_out's rows must not overlap; it may be q_rope itself (same
+ * strides) and must not overlap it otherwise.
  * norm_weight [512]; positions device int32 [T]; slots device int64 [T];
  * rope_table device float32 [max_positions, 64]; cache [num_slots, 576];
  * rows_out [T, 576].

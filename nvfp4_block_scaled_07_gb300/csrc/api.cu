@@ -684,6 +684,12 @@ int moe_finalize(const void* y_bf16, const int32_t* flat_to_perm, const float* t
 // ---- latent attention ---------------------------------------------------------
 // A strided operand of the latent-attention calls: 16-byte aligned rows.
 static bool row_aligned(const void* p, int64_t stride) { return aligned16(p) && stride >= 0 && stride % 8 == 0; }
+// Rows of 64 values of T tokens x H heads that do not overlap: one dimension's rows lie within a step of the other.
+static bool rows_apart(int64_t T, int64_t token_stride, int64_t H, int64_t head_stride) {
+  const int64_t heads = H > 1 ? (H - 1) * head_stride + 64 : 64, tokens = T > 1 ? (T - 1) * token_stride + 64 : 64;
+  return (H == 1 || head_stride >= 64) && (T == 1 || token_stride >= 64) &&
+         (T == 1 || H == 1 || token_stride >= heads || head_stride >= tokens);
+}
 
 int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
                const void* norm_weight, float eps, const int32_t* positions, const int64_t* slots, int T,
@@ -715,6 +721,9 @@ int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, in
   NVFP4MOE_REQUIRE(mla_append_blocks(T, H) < (int64_t(1) << 31), NVFP4MOE_ERR_UNSUPPORTED,
                    "T * (1 + ceil(H / 16)) = %lld units are more than a grid of 2^31 - 1 blocks takes",
                    (long long)T * (1 + ceil_div(H, 16)));
+  NVFP4MOE_REQUIRE(H == 0 || rows_apart(T, q_out_token_stride, H, q_out_head_stride), NVFP4MOE_ERR_INVALID_ARG,
+                   "rows of q_out overlap: strides %lld (tokens) and %lld (heads)", (long long)q_out_token_stride,
+                   (long long)q_out_head_stride);
   DeviceInfo d;
   if (int st = current_device(&d)) return st;
   MlaAppendArgs a;

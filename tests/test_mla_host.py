@@ -85,6 +85,18 @@ def test_append_takes_what_its_grid_takes(M, T, H, fits):
     assert (status(M._lib.mla_append, APPEND, T=T, H=H) != 2) == fits
 
 
+@pytest.mark.parametrize("change,code", [
+    (dict(qo_head=0), 1), (dict(qo_tok=0), 1), (dict(qo_head=56), 1), (dict(qo_tok=120), 1), (dict(qo_tok=64), 1),
+    (dict(qo_tok=64, qo_head=248), 1), (dict(qo_tok=0, qo_head=0, T=1), 1), (dict(qo_tok=0, qo_head=64, T=1), 0),
+    (dict(qo_tok=64, qo_head=0, H=1), 0), (dict(qo_tok=64, qo_head=256), 0), (dict(q_tok=0), 0), (dict(q_head=0), 0)])
+def test_append_refuses_query_rows_that_overlap(M, change, code):
+    """Outputs that overlap would be written by several threads at once; inputs may be broadcast (and then the call ends
+    here for want of a device)."""
+    _no_device()
+    got = status(M._lib.mla_append, APPEND, **change)
+    assert got == 1 if code else got not in (0, 1, 2)
+
+
 DECODE = dict(q=D, cache=D, num_pages=8, page=64, tables=D, stride=4, max_pages=4, lens=D, B=2, Sq=1, H=16, scale=0.1,
               dtype=0, out=D, lse=D, ws=D, ws_bytes=1 << 30, stream=None)
 

@@ -112,14 +112,12 @@ struct WaitCtl {
   unsigned* flags;
 };
 
-// SPIN polls without suspending the thread (the producer and the MMA issuer).
 // The timer is read only after 256 polls: reading it takes longer than most
 // waits last.
-template <bool SPIN>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile WaitCtl* ctl) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (SPIN ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) return true;
+    if (ptx::mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0u) {
       if (ctl->abort) return false;
       const uint64_t now = ptx::globaltimer_ns();
@@ -133,7 +131,8 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
   }
 }
 
-// The same for a whole converged warp, whose lanes all get one answer.  The
+// The same for a whole converged warp (producers and MMA issuers), polled
+// without suspending the threads; its lanes all get one answer.  The
 // loop itself is uniform: code behind a divergent one would issue its MMAs
 // and copies through per-lane registers, several times slower.
 __device__ __forceinline__ bool test_warp(uint32_t bar, uint32_t parity) {

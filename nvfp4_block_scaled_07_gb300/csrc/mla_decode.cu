@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // next tile's vote, so that no thread leaves others at a barrier.
     bool dead = false;
     auto wait = [&](uint32_t b, uint32_t parity) {
-      dead |= !wait_phase<false>(b, parity, wctl);
+      dead |= !wait_phase(b, parity, wctl);
       __syncwarp();
     };
     int behind[2] = {0, 0};                         // keys of the sequence that come after the rows' tokens

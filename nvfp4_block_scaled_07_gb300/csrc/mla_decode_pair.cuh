@@ -355,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     // tile's vote, so that no thread leaves others at a barrier.
     bool dead = false;
     auto wait = [&](uint32_t b, uint32_t parity) {
-      dead |= !wait_phase<false>(b, parity, wctl);
+      dead |= !wait_phase(b, parity, wctl);
       __syncwarp();
     };
     while (cur.valid()) {

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.0f;            // running maximum (log2 domain) less kLift, and sum
     bool ok = true;                           // the same for all lanes of a warp
     for (int j = 0; j < n[t]; ++j) {
-      ok = __all_sync(kFull, wait_phase<false>(bar(ctl->s_full[t]), j & 1u, wctl));
+      ok = __all_sync(kFull, wait_phase(bar(ctl->s_full[t]), j & 1u, wctl));
       if (!ok) break;
       ptx::tc_fence_after();
       uint32_t s[4][32];
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mn;
         l *= a;
         if (j) {
-          ok = __all_sync(kFull, wait_phase<false>(bar(ctl->pv_done[t]), (j - 1) & 1u, wctl));
+          ok = __all_sync(kFull, wait_phase(bar(ctl->pv_done[t]), (j - 1) & 1u, wctl));
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll 1
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the tensor, and 0 * NaN is NaN: they are zeroed before P V reads them.
       const int keys = nk - j * kKeys;
       if (keys < kKeys) {
-        ok = __all_sync(kFull, wait_phase<false>(bar(ctl->v_full[0]), j & 1u, wctl) &&
-                                   wait_phase<false>(bar(ctl->v_full[1]), j & 1u, wctl));
+        ok = __all_sync(kFull, wait_phase(bar(ctl->v_full[0]), j & 1u, wctl) &&
+                                   wait_phase(bar(ctl->v_full[1]), j & 1u, wctl));
         if (!ok) break;
         for (int k = int(threadIdx.x & 127); k < (kKeys - keys) * 16; k += 128)
           ptx::sts128(base + kVOff + (k & 1) * kChunk + (keys + (k >> 4)) * 128 + ((k >> 1) & 7) * 16, 0, 0, 0, 0);
@@ -406,14 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float e0 = __uint_as_float(s[c][k]), e1 = __uint_as_float(s[c][k + 1]);
-          fma2(e0, e1, p.scale_log2, neg, neg);
-          e0 = exp2_approx(e0), e1 = exp2_approx(e1);
-          add2(sum0, sum1, e0, e1);
-          w[k / 2] = Elem<T>::pack(e0, e1);
-        }
+        weights<T>(s[c], w, p.scale_log2, neg, sum0, sum1);
         ptx::tmem_st_32x32b_x16(s_col + 16 * c, w);
         if (c & 1) {                          // 64 keys are complete
           ptx::tmem_st_wait();
@@ -424,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       l += sum0 + sum1;
     }
-    if (n[t] && ok) ok = __all_sync(kFull, wait_phase<false>(bar(ctl->pv_done[t]), (n[t] - 1) & 1u, wctl));
+    if (n[t] && ok) ok = __all_sync(kFull, wait_phase(bar(ctl->pv_done[t]), (n[t] - 1) & 1u, wctl));
     ptx::tc_fence_after();
     if (ok) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;

@@ -569,10 +569,12 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   }
   const int rows = a.Sq * a.H;
   // A pair of CTAs shares each tile between 128 rows, in the time that one CTA
-  // needs for 64: from 65 rows on it halves the passes over the cache (128
-  // sequences x 128 heads: 155 us, with single CTAs 252).  With at most 64 rows
-  // half of its rows would be padding, and single CTAs are faster (32 x 64 heads:
-  // 47.8 us, with pairs 50.8; 128 x 16 heads 66 and 79).
+  // needs for 64: from 65 rows on it halves the passes over the cache (sequences
+  // of some 3500 keys, with pairs and with single CTAs: 32 x 66 heads 43.3 and 51.7
+  // us, 32 x 96 43.7 and 52.9, 128 x 66 108 and 172, 128 x 128 113 and 178; 2 of
+  // 28000 x 72 28.2 and 32.5).  With at most 64 rows half of its rows would be
+  // padding, and single CTAs are faster (32 x 64 heads: 47.8 us, with pairs 50.8;
+  // 128 x 16 heads 66 and 79).
   const bool pair = rows > kRows;
   CUtensorMap q_map, kv_map;
   if (!encode_rows<T>(&q_map, a.q, int64_t(a.B) * rows, kRows, 3) ||
@@ -633,12 +635,16 @@ int launch(const MlaDecodeArgs& a, int num_sms, cudaStream_t st) {
   }
   const int64_t items = int64_t(a.B) * p.blocks;
   if (err == cudaSuccess && ranges > 1) {
-    // Few items of many pieces are joined by item, several warps a row (two
-    // sequences of 116000 keys: 84 us, by the borders 126); more items by the
-    // borders that cut them, a warp a row (128 sequences of 5000 keys: 181 us, by
-    // item 206; all from cold caches).
+    // Few items of many pieces are joined by item, several warps a row; more items
+    // by the borders that cut them, a warp a row.  Single CTAs (152 ranges), calls
+    // in a graph, by item and by borders: 8 sequences of 8192 keys x 64 heads 25.6
+    // and 29.1 us, 20 45.1 and 46.4, 36 of 4096 x 16 heads 36.3 and 37.2, 38 x 64
+    // heads 45.9 and 44.7, 76 75.6 and 68.2: a quarter of the ranges.  Pairs (76
+    // ranges), whose items have half as many pieces of twice the rows, x 128 heads:
+    // 2 of 32768 keys 28.3 and 43.1, 5 of 16384 38.3 and 40.5, 6 43.4 and 42.9, 8
+    // 50.2 and 48.0, 12 of 4096 36.7 and 29.2, 19 of 8192 63.7 and 49.9: a twelfth.
     const int most = std::min(kRows * ctas, rows);
-    const bool by_item = items * 4 <= ranges;
+    const bool by_item = items * (pair ? 12 : 4) <= ranges;
     // From 16 pieces on, and while the blocks are resident at once, eight warps
     // share a quarter of a row: one sequence of 32768 keys with 16 heads takes
     // 21.2 us, 33.8 with four warps a row, eight with 16 heads 46.9 and 48.7; but

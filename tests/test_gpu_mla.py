@@ -276,6 +276,16 @@ def test_decode_items_that_begin_at_a_border(M, B, H, n):
     decode_check(c, out, lse)
 
 
+@pytest.mark.parametrize("B,Sq,H,top", [(6, 1, 128, 5000), (7, 1, 128, 5000), (12, 1, 80, 3000), (19, 2, 40, 2100), (3, 2, 128, 4000)])
+def test_decode_joins_of_pairs(M, B, Sq, H, top):
+    """Both ways in which the pairs' partial results are joined, on both sides of the rule between them."""
+    c = decode_case(B, Sq, H, [max(0, top - 317 * i) for i in range(B)], 64, BF16, seed=B + H)
+    ws = torch.full((M.mla_decode_workspace_size(),), 255, dtype=torch.uint8, device="cuda")   # NaN everywhere
+    out, lse = M.mla_decode(c["q"], c["cache"], c["table"], c["lens"], SCALE, workspace=ws)
+    M.sync_status()
+    decode_check(c, out, lse)
+
+
 def test_decode_random_shapes(M):
     rng = random.Random(3)
     for i in range(24):

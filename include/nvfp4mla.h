@@ -13,6 +13,10 @@
  *   mla_prefill  expanded form: per-head keys of 128 + 64 values (the 64 are
  *                shared by the heads) and values of 128
  *
+ * The sizes are fixed.  A layer that caches 512 + 64 values a token but expands
+ * them to other keys or values (192 + 64 and 256, say) is served by mla_append
+ * and mla_decode and not by mla_prefill.
+ *
  * Conventions are those of nvfp4moe.h: C ABI, status codes and messages,
  * caller-owned 16-byte aligned device buffers, work enqueued on `stream`
  * without synchronising, programmatic dependent launch, compute capability

@@ -26,8 +26,8 @@
 //
 // Bound by the cache's bytes: a tile takes 2800 cycles in the middle of a range,
 // the rate at which HBM feeds an SM (S takes 1400 of them, P V 650 to 1000, the
-// softmax 1000).  128 sequences x 16 heads of 300 to 4100 keys (340 MB): 66 us, 5.1
-// TB/s; 32 x 64 heads of 1000 to 8191 (172 MB): 47.7 us, where a range is only
+// softmax 1000).  Ten calls in a graph (a loop of calls takes 1 us more), 128
+// sequences x 16 heads of 300 to 4100 keys (340 MB): 66 us, 5.1 TB/s; 32 x 64 heads of 1000 to 8191 (172 MB): 47.7 us, where a range is only
 // 16 tiles and pays 5000 cycles to its first copy (lengths, pages), 4000 for its
 // last tile, 5800 to store its rows, and the join 8 us.
 //
@@ -532,9 +532,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles of a range at least, of 64 keys with one CTA and of 128 with a pair:
 // below this, splitting a sequence costs more than it gains.  A sequence of
-// 1024 keys with 16 heads takes 9.9 us (9.8 with 1, 11.6 with 3, 12.4 with 4),
-// of 4096 keys 12.0 (13.8 with 1); with 128 heads 13.0 (12.3 with 1), of 8192
-// keys 15.4 (18.6 with 1, 16.7 with 4).
+// 1024 keys with 16 heads takes 10.5 us (9.6 with 1, 12.6 with 4), of 4096 keys
+// 11.4 (12.1 with 1, 13.2 with 4); with 128 heads 14.5 (15.0 and 16.5), of 8192
+// keys 15.7 (18.7 and 16.7); eight of 1024 keys with 16 heads 10.9 (11.9 and 13.2).
 constexpr int kMinShare = 2;
 
 // Most tiles the call can have.

@@ -10,10 +10,12 @@
 //                                       the values of all 128 keys
 // 36 MMAs of 36 cycles and 16 of 68 a tile of 128 keys, 2360 cycles, against
 // the 2820 in which HBM delivers it to a pair.  Measured: about 3400.  128
-// sequences x 128 heads of 2048 to 8192 keys (803 MB) take 155 us, 5.2 TB/s, with the
-// tensor pipe active for 54 % of the time, DRAM for 70 % and shared memory's
-// banks for 40 %: what bounds is the way of the rows through one buffer, MMAs
-// of a part 430 cycles, its release 850, its copy 2000.  Two stages of 64 keys
+// sequences x 128 heads of 2048 to 8192 keys (803 MB) take 155 us, 5.2 TB/s, as ten
+// calls in a graph, and 160 to 173 us in a loop of calls, where the power limit
+// lowers the clock; the tensor pipe is active for 57 % of the time, DRAM for 71 %
+// and shared memory's banks for 43 %: what bounds is the way of the rows through
+// one buffer, MMAs of a part 430 cycles, its release 850, its copy 2000.  (Times
+// below are of ten calls in a graph.)  Two stages of 64 keys
 // fit as well, but read Q twice as often: 187 us where 128 keys took 182.
 // A CTA's share of a tile is 72 KB for S and 64 KB for P V (its own keys'
 // values twice, so that both CTAs use the same descriptors).  S frees its rows
@@ -26,8 +28,9 @@
 // Warp roles in each CTA: warps 0-7 softmax and epilogue of its 64 rows, 8-9
 // TMA producers of whole rows, 10-13 of values, warp 14 tensor-memory owner
 // and, in the even CTA, issuer of S, warp 15 issuer of P V there.
-// The even CTA's barriers count both CTAs' copies of whole rows and softmax
-// arrivals; commits arrive in both.  The copies of values count in their own
+// The even CTA's barriers count both CTAs' copies of whole rows, the arrivals of
+// both CTAs' row warps (with and without rows to copy) and of their softmax
+// warps; commits arrive in both.  The copies of values count in their own
 // CTA, whose softmax warps wait for them before they arrive: rows past the
 // last key are zeroed after their copy.
 #pragma once

@@ -7,8 +7,9 @@
 // absorbed kernel (p = exp2(S * scale * log2 e - m)).
 //
 // Bound by the tensor core: 2 * (192 + 128) operations a score.  One sequence
-// of 16384 tokens x 16 heads takes 826 us, 1.66 PFLOP/s, at about 1.55 GHz under
-// the power limit; a tile of keys with two tiles of rows takes 3400 cycles, of
+// of 16384 tokens x 16 heads takes 826 to 871 us as ten calls in a graph, 1.58 to
+// 1.66 PFLOP/s, at about 1.55 GHz under the power limit, and 874 to 890 us in a
+// loop of calls; a tile of keys with two tiles of rows takes 3400 cycles, of
 // which the MMAs need 2700.  Short sequences pay for the ends of a block, 16000
 // cycles (place 3000, first copies 2700, softmax and output of the last tile
 // 8000, the next block's start 2000): seven of 101 to 2500 tokens take 133 us,

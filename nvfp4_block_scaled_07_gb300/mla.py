@@ -112,7 +112,8 @@ def mla_append(latent, k_rope, positions, slots, rope_table, cache, norm_weight=
     projection's output; cache [num_pages, page_size, 576].  rows_out [T, 576]
     takes a copy of the rows (what the expanded form projects).  q_out [T, H,
     64] may be a slice of the queries' buffer or q_rope itself; it is made when
-    q_rope comes without it.  Returns q_out (None without queries)."""
+    q_rope comes without it.  A token whose position is outside the table is
+    not written anywhere (sync_status reports it).  Returns q_out (None without queries)."""
     t, code, dev = _first(latent, "latent", 2)
     T = len(latent)
     latent_at = _strided(latent, t, (T, LATENT), "latent", dev)
@@ -193,7 +194,8 @@ def mla_prefill(q, k_nope, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, 
 
     q [Tq, H, 192], k_nope [Tk, H, 128], k_rope [Tk, 64] and v [Tk, H, 128] may
     be slices of projections' outputs; cu_q, cu_k int32 [B + 1] are the
-    sequences' offsets.  Returns (out [Tq, H, 128], lse float32 [Tq, H])."""
+    sequences' offsets.  Returns (out [Tq, H, 128], lse float32 [Tq, H]), whose
+    rows of tokens in no sequence are not written."""
     t, code, dev = _first(q, "q", 3)
     Tq, H, _ = q.shape
     q_at = _strided(q, t, (Tq, H, NOPE + ROPE), "q", dev)

@@ -7,6 +7,7 @@
  * position).  The cache is paged: [num_pages, page_size, 576], row-major;
  * slot s is row s % page_size of page s / page_size.
  *
+ *   mla_plan     block tables, slots and positions of a step's new tokens
  *   mla_append   writes new tokens into the cache and rotates their queries
  *   mla_decode   absorbed form: queries of 576 values against the cached rows,
  *                whose first 512 values are also the values
@@ -43,6 +44,41 @@ extern "C" {
 #define NVFP4MLA_ROW    576
 #define NVFP4MLA_NOPE   128 /* expanded form: unrotated values of a key or query */
 #define NVFP4MLA_VALUE  128 /* expanded form: values of a head */
+
+/* The pages and slots of a step's new tokens, from the lengths of B requests
+ * and the free pages, without the host.  Request b has past = past_lens[b]
+ * tokens in the cache and brings n = new_lens[b] (0: none).  In the order of
+ * the requests, one that misses m = ceil((past + n) / page_size) - ceil(past /
+ * page_size) pages pops them from the end of free_pages[0 .. free_count[0]) and
+ * gets them as entries ceil(past / page_size) .. of its row of block_tables.
+ * A request is refused as a whole (no page, no slot) when the pages that it
+ * and the requests before it miss are more than free_count, its tokens more
+ * than max_pages hold, or its last token past row T; the first leaves the
+ * later requests that miss no page as they are, the second and third miss
+ * nothing.
+ *   granted[b]     n, or 0 of a refused request
+ *   seq_lens[b]    past + granted[b], as mla_decode takes it
+ *   cu_seqlens     [B + 1] offsets of the requests' tokens, min(sum of n, T)
+ *   positions[t]   past + i for token i of its request
+ *   slots[t]       page * page_size + position % page_size, as mla_append takes
+ *                  it; -1 of a refused request or a table entry below 0
+ *   free_count_out free pages left; may be free_count itself
+ * Rows of positions and slots past the last token become 0 and -1, so a
+ * captured step may have more rows than tokens.  Nothing else of block_tables
+ * is written, nor anything of free_pages: what lies from free_count_out on is
+ * in use, and pages return by being written there and counted.
+ * A negative length counts as 0, a count outside [0, num_free] as the nearer
+ * end; these and tokens past row T raise NVFP4MOE_ERR_DEVICE_DATA.
+ * past_lens, new_lens, seq_lens, granted device int32 [B]; block_tables device
+ * int32 [B, max_pages], rows table_stride apart; free_pages device int32
+ * [num_free]; positions device int32 [T], slots device int64 [T]; outputs must
+ * not overlap anything else.  Limits: B, T, max_pages, num_free >= 0, page_size
+ * a power of two >= 16. */
+int mla_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size,
+             int32_t* block_tables, int64_t table_stride, int max_pages,
+             const int32_t* free_pages, int num_free, const int32_t* free_count, int T,
+             int32_t* positions, int64_t* slots, int32_t* cu_seqlens, int32_t* seq_lens, int32_t* granted,
+             int32_t* free_count_out, cudaStream_t stream);
 
 /* Appends T tokens to the cache.  For token t with position p = positions[t]:
  *   n      = latent[t] / sqrt(mean(latent[t]^2) + eps) * norm_weight  (norm_weight NULL: n = latent[t])

@@ -81,7 +81,17 @@ _SIGS = {
                                              _p, _i, _i, ctypes.c_int32, ctypes.c_int32, _p, _sz, _p]),
     "moe_finalize_f32": (_i, [_p, _i, _i, _p, _p]),
 }
-for _name, (_res, _args) in _SIGS.items():
+# include/nvfp4few.h
+_FEW_SIGS = {
+    "moe_route_grouped": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]),
+    "moe_matvec_workspace_size": (_sz, [_i, _i]),
+    "moe_matvec_nvfp4": (_i, [_p, _i64, _i, _i, _p, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
+    "moe_matvec_mxfp4": (_i, [_p, _i64, _i, _i, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
+    "moe_experts_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_experts_nvfp4": (_i, [_p, _i64, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _i, _p, _p, _sz, _p]),
+    "moe_experts_mxfp4": (_i, [_p, _i64, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _i, _p, _p, _sz, _p]),
+}
+for _name, (_res, _args) in [*_SIGS.items(), *_FEW_SIGS.items()]:
     _fn = getattr(_lib, _name)
     _fn.restype = _res
     _fn.argtypes = _args
@@ -106,6 +116,18 @@ def _ptr(t):
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _stream_of(t):
+    """The current stream; calls are made with the tensors' device current."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return _stream()
+
+
+def _same_device(first, t, name):
+    if t.get_device() != first.get_device():
+        raise ValueError(f"{name} is on {t.device}, the first tensor on {first.device}")
 
 
 def _need(t, dtype, shape=None, name="tensor"):
@@ -196,6 +218,30 @@ def moe_route_batch_aware(logits, k, k_primary, score_fn="sigmoid", renormalize=
     _check(_lib.moe_route_batch_aware(_ptr(logits), _ptr(bias), T, E, k, int(k_primary), SCORE[score_fn],
                                       int(bool(renormalize)), _ptr(topk_idx), _ptr(topk_w), _ptr(workspace),
                                       workspace.numel(), _stream()), "moe_route_batch_aware")
+    return topk_idx, topk_w
+
+
+def moe_route_grouped(logits, k, score_fn="sigmoid", renormalize=True, select_bias=None, n_group=1, topk_group=1,
+                      group_best=2, scale=1.0, topk_idx=None, topk_w=None):
+    """Routing with groups of experts (the topk_group best of n_group are kept,
+    by their largest or their two largest biased scores), a bias that selects
+    but is not in the weights, and a factor on the weights."""
+    T, E = logits.shape
+    _need(logits, torch.float32, name="logits")
+    if select_bias is not None:
+        _need(select_bias, torch.float32, (E,), "select_bias")
+        _same_device(logits, select_bias, "select_bias")
+    if topk_idx is None:
+        topk_idx = _empty((T, k), torch.int32, logits.device)
+    if topk_w is None:
+        topk_w = _empty((T, k), torch.float32, logits.device)
+    _need(topk_idx, torch.int32, (T, k), "topk_idx")
+    _need(topk_w, torch.float32, (T, k), "topk_w")
+    _same_device(logits, topk_idx, "topk_idx")
+    _same_device(logits, topk_w, "topk_w")
+    _check(_lib.moe_route_grouped(_ptr(logits), _ptr(select_bias), T, E, k, n_group, topk_group, group_best,
+                                  SCORE[score_fn], int(bool(renormalize)), scale, _ptr(topk_idx), _ptr(topk_w),
+                                  _stream_of(logits)), "moe_route_grouped")
     return topk_idx, topk_w
 
 
@@ -665,6 +711,135 @@ def moe_finalize(y, flat_to_perm, topk_w, out=None):
     _check(_lib.moe_finalize(_ptr(y), _ptr(flat_to_perm), _ptr(topk_w), T, k, H, cap, _ptr(out), _stream()),
            "moe_finalize")
     return out
+
+
+# ---- few tokens: 4-bit weights, 16-bit activations ---------------------------------
+FEW_MAX_TOKENS = 32
+X_DTYPE = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _rows(x, dtypes, name):
+    """[T, K] whose rows are contiguous and start on 16-byte boundaries: (T, K, stride)."""
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {x.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name}: {x.dim()} dimensions, expected 2")
+    T, K = x.shape
+    step = x.stride(0) if T > 1 else K
+    if (x.stride(1) != 1 and K > 1) or step % 8 or x.data_ptr() % 16:
+        raise ValueError(f"{name}: strides {x.stride()}, address {x.data_ptr():#x} (innermost 1, the other a multiple of 8, "
+                         "16-byte aligned)")
+    return T, K, step
+
+
+def _few_weights(x, w_packed, w_scales, w_gscale, fmt, name):
+    """(E, N, K, arguments without the layout, layout) of one call's weights."""
+    data = w_packed.data if isinstance(w_packed, TiledWeights) else w_packed
+    if not isinstance(w_packed, TiledWeights) and w_packed.dim() == 2:
+        w_packed = w_packed[None]
+    E, N, K, ptr, layout = _weights_args(w_packed)
+    if isinstance(w_packed, TiledWeights):
+        _need(data, torch.uint8, name=name)
+        if data.numel() < int(_lib.nvfp4moe_tiled_weights_bytes(E * N, K)):
+            raise ValueError(f"{name}: smaller than the tiled layout needs")
+    _need(w_scales, torch.uint8, name=f"{name} scales")
+    need = E * blocked_scales_bytes(N, K, fmt)
+    if w_scales.numel() < need:
+        raise ValueError(f"{name}: scale buffer smaller than the blocked layout needs")
+    _same_device(x, data, name)
+    _same_device(x, w_scales, f"{name} scales")
+    args = [ptr, _ptr(w_scales)]
+    if fmt == "nvfp4":
+        _need(w_gscale, torch.float32, (E,), f"{name} gscale")
+        _same_device(x, w_gscale, f"{name} gscale")
+        args.append(_ptr(w_gscale))
+    return E, N, K, args, layout
+
+
+def _few_workspace(x, need, workspace):
+    if workspace is None:
+        return _empty((need,), torch.uint8, x.device) if need else None
+    _need(workspace, torch.uint8, name="workspace")
+    _same_device(x, workspace, "workspace")
+    return workspace
+
+
+def moe_matvec_workspace_size(T, K):
+    return int(_lib.moe_matvec_workspace_size(T, K))
+
+
+def _matvec(fmt, x, w_packed, w_scales, w_gscale, out, workspace):
+    T, K, step = _rows(x, X_DTYPE, "x")
+    E, N, Kw, w_args, layout = _few_weights(x, w_packed, w_scales, w_gscale, fmt, "w_packed")
+    if E != 1 or Kw != K:
+        raise ValueError(f"w_packed: {E} matrices of {Kw} columns, expected one of {K}")
+    if out is None:
+        out = _empty((T, N), x.dtype, x.device)
+    else:
+        _need(out, x.dtype, (T, N), "out")
+        _same_device(x, out, "out")
+    ws = _few_workspace(x, moe_matvec_workspace_size(T, K), workspace)
+    call = _lib.moe_matvec_nvfp4 if fmt == "nvfp4" else _lib.moe_matvec_mxfp4
+    _check(call(_ptr(x), step, T, X_DTYPE[x.dtype], *w_args, N, K, layout, _ptr(out), _ptr(ws),
+                0 if ws is None else ws.numel(), _stream_of(x)), f"moe_matvec_{fmt}")
+    return out
+
+
+def moe_matvec_nvfp4(x, w_packed, w_scales, w_gscale, out=None, workspace=None):
+    """out [T, N] = x W^T for up to 32 rows x [T, K] (bf16 or fp16, rows may be
+    strided) and one NVFP4 matrix: w_packed [N, K/2] or TiledWeights, w_scales
+    blocked, w_gscale [1]."""
+    return _matvec("nvfp4", x, w_packed, w_scales, w_gscale, out, workspace)
+
+
+def moe_matvec_mxfp4(x, w_packed, w_scales, out=None, workspace=None):
+    """moe_matvec_nvfp4 for an MXFP4 matrix (no per-tensor scale)."""
+    return _matvec("mxfp4", x, w_packed, w_scales, None, out, workspace)
+
+
+def moe_experts_workspace_size(T, k, H, I):
+    return int(_lib.moe_experts_workspace_size(T, k, H, I))
+
+
+def _experts(fmt, x, topk_idx, topk_w, gu, d, out, workspace):
+    T, H, step = _rows(x, (torch.bfloat16,), "x")
+    E, N, K, gu_args, layout = _few_weights(x, *gu, fmt, "w_gu_packed")
+    Ed, Nd, I, d_args, layout_d = _few_weights(x, *d, fmt, "w_d_packed")
+    if (Ed, Nd, 2 * I, K) != (E, H, N, H) or layout != layout_d:
+        raise ValueError(f"w_gu {E} x [{N}, {K}] and w_d {Ed} x [{Nd}, {I}] (one layout for both) do not fit x [{T}, {H}]")
+    k = topk_idx.shape[-1]
+    _need(topk_idx, torch.int32, (T, k), "topk_idx")
+    _need(topk_w, torch.float32, (T, k), "topk_w")
+    _same_device(x, topk_idx, "topk_idx")
+    _same_device(x, topk_w, "topk_w")
+    if out is None:
+        out = _empty((T, H), x.dtype, x.device)
+    else:
+        _need(out, x.dtype, (T, H), "out")
+        _same_device(x, out, "out")
+    ws = _few_workspace(x, moe_experts_workspace_size(T, k, H, I), workspace)
+    call = _lib.moe_experts_nvfp4 if fmt == "nvfp4" else _lib.moe_experts_mxfp4
+    _check(call(_ptr(x), step, _ptr(topk_idx), _ptr(topk_w), T, k, E, H, I, *gu_args, *d_args, layout, _ptr(out), _ptr(ws),
+                0 if ws is None else ws.numel(), _stream_of(x)), f"moe_experts_{fmt}")
+    return out
+
+
+def moe_experts_nvfp4(x, topk_idx, topk_w, w_gu_packed, w_gu_scales, w_gu_gscale, w_d_packed, w_d_scales, w_d_gscale,
+                      out=None, workspace=None):
+    """The chosen experts' gated products of up to 32 tokens, weighted and summed:
+    x bf16 [T, H] (rows may be strided), topk_idx and topk_w [T, k] as the
+    routers return them, w_gu [E, 2I, H] and w_d [E, H, I] as the grouped GEMM
+    takes them.  The activations are not quantised.  Returns bf16 [T, H]."""
+    return _experts("nvfp4", x, topk_idx, topk_w, (w_gu_packed, w_gu_scales, w_gu_gscale),
+                    (w_d_packed, w_d_scales, w_d_gscale), out, workspace)
+
+
+def moe_experts_mxfp4(x, topk_idx, topk_w, w_gu_packed, w_gu_scales, w_d_packed, w_d_scales, out=None, workspace=None):
+    """moe_experts_nvfp4 for MXFP4 weights (no per-tensor scales)."""
+    return _experts("mxfp4", x, topk_idx, topk_w, (w_gu_packed, w_gu_scales, None), (w_d_packed, w_d_scales, None), out,
+                    workspace)
 
 
 # ---- the whole layer -------------------------------------------------------------

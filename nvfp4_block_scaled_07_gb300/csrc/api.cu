@@ -8,6 +8,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "../../include/nvfp4few.h"
 #include "../../include/nvfp4mla.h"
 #include "../../include/nvfp4moe.h"
 #include "internal.h"
@@ -97,8 +98,8 @@ uint32_t wait_limit_us() { return g_wait_limit_us.load(std::memory_order_relaxed
 
 namespace nvfp4moe {
 namespace {
-// The sticky flags of the five kernel files on the current device.
-constexpr int kFlagWords = 5;
+// The sticky flags of the kernel files that raise any, on the current device.
+constexpr int kFlagWords = 7;
 struct FlagWords {
   unsigned* at[kFlagWords];
 };
@@ -120,7 +121,8 @@ cudaError_t read_and_clear_flags(unsigned* flags, cudaStream_t st) {
   cudaError_t err;
   if ((err = prep_flags_address(&w.at[0])) != cudaSuccess || (err = gemm_flags_address(&w.at[1])) != cudaSuccess ||
       (err = mla_append_flags_address(&w.at[2])) != cudaSuccess || (err = mla_decode_flags_address(&w.at[3])) != cudaSuccess ||
-      (err = mla_prefill_flags_address(&w.at[4])) != cudaSuccess)
+      (err = mla_prefill_flags_address(&w.at[4])) != cudaSuccess || (err = few_flags_address(&w.at[5])) != cudaSuccess ||
+      (err = mla_plan_flags_address(&w.at[6])) != cudaSuccess)
     return err;
   std::lock_guard<std::mutex> lock(g_status_mutex);
   collect_flags<<<1, 32, 0, st>>>(w);
@@ -681,6 +683,146 @@ int moe_finalize(const void* y_bf16, const int32_t* flat_to_perm, const float* t
                      "finalize launch");
 }
 
+// ---- grouped routing ----------------------------------------------------------
+int moe_route_grouped(const float* logits, const float* select_bias, int T, int E, int k, int n_group, int topk_group,
+                      int group_best, int score_fn, int renormalize, float scale, int32_t* topk_idx, float* topk_w,
+                      cudaStream_t stream) {
+  t_detail[0] = 0;
+  NVFP4MOE_REQUIRE(T >= 0, NVFP4MOE_ERR_INVALID_ARG, "T = %d must be >= 0", T);
+  NVFP4MOE_REQUIRE(E >= 1 && E <= 1024, NVFP4MOE_ERR_UNSUPPORTED, "E = %d outside [1, 1024]", E);
+  NVFP4MOE_REQUIRE(k >= 1 && k <= E && k <= 32, NVFP4MOE_ERR_UNSUPPORTED, "k = %d outside [1, min(E, 32)]", k);
+  NVFP4MOE_REQUIRE(n_group >= 1 && n_group <= 32 && E % n_group == 0, NVFP4MOE_ERR_UNSUPPORTED,
+                   "n_group = %d outside [1, 32] or no divisor of E = %d", n_group, E);
+  NVFP4MOE_REQUIRE(topk_group >= 1 && topk_group <= n_group, NVFP4MOE_ERR_INVALID_ARG,
+                   "topk_group = %d outside [1, n_group = %d]", topk_group, n_group);
+  NVFP4MOE_REQUIRE(k <= topk_group * (E / n_group), NVFP4MOE_ERR_INVALID_ARG, "k = %d experts of %d groups of %d", k,
+                   topk_group, E / n_group);
+  NVFP4MOE_REQUIRE((group_best == 1 || group_best == 2) && (n_group == 1 || group_best <= E / n_group),
+                   NVFP4MOE_ERR_INVALID_ARG, "group_best = %d with groups of %d", group_best, E / n_group);
+  NVFP4MOE_REQUIRE(score_fn == NVFP4MOE_SCORE_SOFTMAX || score_fn == NVFP4MOE_SCORE_SIGMOID,
+                   NVFP4MOE_ERR_INVALID_ARG, "score_fn %d", score_fn);
+  NVFP4MOE_REQUIRE(scale > -1e30f && scale < 1e30f, NVFP4MOE_ERR_INVALID_ARG, "scale must be finite");
+  if (T == 0) return NVFP4MOE_OK;
+  NVFP4MOE_REQUIRE(logits && topk_idx && topk_w, NVFP4MOE_ERR_INVALID_ARG, "null pointer");
+  NVFP4MOE_REQUIRE(((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(select_bias) |
+                     reinterpret_cast<uintptr_t>(topk_idx) | reinterpret_cast<uintptr_t>(topk_w)) & 3) == 0,
+                   NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  DeviceInfo d;
+  if (int st = current_device(&d)) return st;
+  return cuda_status(launch_route_grouped(logits, select_bias, T, E, k, n_group, topk_group, group_best,
+                                          score_fn == NVFP4MOE_SCORE_SOFTMAX, renormalize != 0, scale, topk_idx, topk_w,
+                                          stream),
+                     "route_grouped launch");
+}
+
+// ---- few tokens -----------------------------------------------------------------
+// One 4-bit matrix (or one of each expert) of the few-token calls.
+static int check_matrix(const FewMatrix& w, int n_of, const char* name) {
+  const int kq = w.mx ? 128 : 64;
+  NVFP4MOE_REQUIRE(w.K > 0 && w.K % kq == 0, NVFP4MOE_ERR_UNSUPPORTED, "%s: %d columns, not a positive multiple of %d", name,
+                   w.K, kq);
+  NVFP4MOE_REQUIRE(w.N > 0 && w.N % n_of == 0, NVFP4MOE_ERR_UNSUPPORTED, "%s: %d rows, not a positive multiple of %d", name,
+                   w.N, n_of);
+  NVFP4MOE_REQUIRE(w.packed && w.scales && (w.mx || w.gscale), NVFP4MOE_ERR_INVALID_ARG, "%s: null pointer", name);
+  NVFP4MOE_REQUIRE(aligned16(w.packed) && aligned16(w.scales) && (reinterpret_cast<uintptr_t>(w.gscale) & 3) == 0,
+                   NVFP4MOE_ERR_INVALID_ARG, "%s: misaligned pointer", name);
+  return NVFP4MOE_OK;
+}
+
+size_t moe_matvec_workspace_size(int T, int K) {
+  if (T < 1 || T > kFewMaxTokens || K < 1) return 0;
+  return few_matvec_workspace_bytes(T, K);
+}
+
+static int matvec_common(const void* x, int64_t x_stride, int T, int x_dtype, const FewMatrix& w, int w_layout, void* out,
+                         void* ws, size_t ws_bytes, cudaStream_t stream) {
+  t_detail[0] = 0;
+  NVFP4MOE_REQUIRE(T >= 0, NVFP4MOE_ERR_INVALID_ARG, "T = %d must be >= 0", T);
+  NVFP4MOE_REQUIRE(T <= kFewMaxTokens, NVFP4MOE_ERR_UNSUPPORTED, "T = %d above %d", T, kFewMaxTokens);
+  NVFP4MOE_REQUIRE(x_dtype == NVFP4MOE_X_BF16 || x_dtype == NVFP4MOE_X_FP16, NVFP4MOE_ERR_INVALID_ARG, "x_dtype %d", x_dtype);
+  NVFP4MOE_REQUIRE(w_layout == NVFP4MOE_W_ROWMAJOR || w_layout == NVFP4MOE_W_TILED, NVFP4MOE_ERR_INVALID_ARG,
+                   "w_layout %d", w_layout);
+  if (int st = check_matrix(w, 128, "w")) return st;
+  if (T == 0) return NVFP4MOE_OK;
+  NVFP4MOE_REQUIRE(x && out && aligned16(x) && aligned16(out), NVFP4MOE_ERR_INVALID_ARG, "null or misaligned pointer");
+  NVFP4MOE_REQUIRE(T == 1 || (x_stride >= 0 && x_stride % 8 == 0), NVFP4MOE_ERR_INVALID_ARG,
+                   "x_stride %lld must be a multiple of 8", (long long)x_stride);
+  const size_t need = moe_matvec_workspace_size(T, w.K);
+  NVFP4MOE_REQUIRE(need == 0 || (ws && ws_bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0),
+                   NVFP4MOE_ERR_WORKSPACE, "workspace %zu < %zu or not 256-byte aligned", ws_bytes, need);
+  DeviceInfo d;
+  if (int st = current_device(&d)) return st;
+  return cuda_status(launch_few_matvec(x, T == 1 ? 0 : x_stride, T, x_dtype == NVFP4MOE_X_FP16, w, out, ws, stream),
+                     "matvec launch");
+}
+
+int moe_matvec_nvfp4(const void* x, int64_t x_stride, int T, int x_dtype, const uint8_t* w_packed, const uint8_t* w_scales,
+                     const float* w_gscale, int N, int K, int w_layout, void* out, void* ws, size_t ws_bytes,
+                     cudaStream_t stream) {
+  const FewMatrix w = {w_packed, w_scales, w_gscale, N, K, false, w_layout == NVFP4MOE_W_TILED};
+  return matvec_common(x, x_stride, T, x_dtype, w, w_layout, out, ws, ws_bytes, stream);
+}
+
+int moe_matvec_mxfp4(const void* x, int64_t x_stride, int T, int x_dtype, const uint8_t* w_packed, const uint8_t* w_scales,
+                     int N, int K, int w_layout, void* out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const FewMatrix w = {w_packed, w_scales, nullptr, N, K, true, w_layout == NVFP4MOE_W_TILED};
+  return matvec_common(x, x_stride, T, x_dtype, w, w_layout, out, ws, ws_bytes, stream);
+}
+
+size_t moe_experts_workspace_size(int T, int k, int H, int I) {
+  if (T < 1 || T > kFewMaxTokens || k < 1 || k > 32 || H < 1 || I < 1) return 0;
+  return few_experts_workspace_bytes(T, k, H, I);
+}
+
+static int experts_common(const void* x, int64_t x_stride, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,
+                          int I, const FewMatrix& gu, const FewMatrix& dn, int w_layout, void* out, void* ws,
+                          size_t ws_bytes, cudaStream_t stream) {
+  t_detail[0] = 0;
+  NVFP4MOE_REQUIRE(T >= 0, NVFP4MOE_ERR_INVALID_ARG, "T = %d must be >= 0", T);
+  NVFP4MOE_REQUIRE(T <= kFewMaxTokens, NVFP4MOE_ERR_UNSUPPORTED, "T = %d above %d", T, kFewMaxTokens);
+  NVFP4MOE_REQUIRE(E >= 1 && E <= 1024, NVFP4MOE_ERR_UNSUPPORTED, "E = %d outside [1, 1024]", E);
+  NVFP4MOE_REQUIRE(k >= 1 && k <= 32, NVFP4MOE_ERR_UNSUPPORTED, "k = %d outside [1, 32]", k);
+  NVFP4MOE_REQUIRE(I > 0 && I % 128 == 0 && I < (1 << 30), NVFP4MOE_ERR_UNSUPPORTED, "I = %d must be a positive multiple of 128", I);
+  NVFP4MOE_REQUIRE(w_layout == NVFP4MOE_W_ROWMAJOR || w_layout == NVFP4MOE_W_TILED, NVFP4MOE_ERR_INVALID_ARG,
+                   "w_layout %d", w_layout);
+  if (int st = check_matrix(gu, 256, "w_gu")) return st;
+  if (int st = check_matrix(dn, 128, "w_d")) return st;
+  if (T == 0) return NVFP4MOE_OK;
+  NVFP4MOE_REQUIRE(x && topk_idx && topk_w && out, NVFP4MOE_ERR_INVALID_ARG, "null pointer");
+  NVFP4MOE_REQUIRE(aligned16(x) && aligned16(out) &&
+                       ((reinterpret_cast<uintptr_t>(topk_idx) | reinterpret_cast<uintptr_t>(topk_w)) & 3) == 0,
+                   NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  NVFP4MOE_REQUIRE(T == 1 || (x_stride >= 0 && x_stride % 8 == 0), NVFP4MOE_ERR_INVALID_ARG,
+                   "x_stride %lld must be a multiple of 8", (long long)x_stride);
+  const size_t need = moe_experts_workspace_size(T, k, gu.K, dn.K);
+  NVFP4MOE_REQUIRE(ws && ws_bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0, NVFP4MOE_ERR_WORKSPACE,
+                   "workspace %zu < %zu or not 256-byte aligned", ws_bytes, need);
+  DeviceInfo d;
+  if (int st = current_device(&d)) return st;
+  return cuda_status(launch_few_experts(x, T == 1 ? 0 : x_stride, topk_idx, topk_w, T, k, E, gu, dn, out, ws, stream),
+                     "experts launch");
+}
+
+int moe_experts_nvfp4(const void* x_bf16, int64_t x_stride, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,
+                      int H, int I, const uint8_t* w_gu_packed, const uint8_t* w_gu_scales, const float* w_gu_gscale,
+                      const uint8_t* w_d_packed, const uint8_t* w_d_scales, const float* w_d_gscale, int w_layout,
+                      void* out_bf16, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const bool tiled = w_layout == NVFP4MOE_W_TILED;
+  const FewMatrix gu = {w_gu_packed, w_gu_scales, w_gu_gscale, I < (1 << 30) ? 2 * I : 0, H, false, tiled};
+  const FewMatrix dn = {w_d_packed, w_d_scales, w_d_gscale, H, I, false, tiled};
+  return experts_common(x_bf16, x_stride, topk_idx, topk_w, T, k, E, I, gu, dn, w_layout, out_bf16, ws, ws_bytes, stream);
+}
+
+int moe_experts_mxfp4(const void* x_bf16, int64_t x_stride, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,
+                      int H, int I, const uint8_t* w_gu_packed, const uint8_t* w_gu_scales, const uint8_t* w_d_packed,
+                      const uint8_t* w_d_scales, int w_layout, void* out_bf16, void* ws, size_t ws_bytes,
+                      cudaStream_t stream) {
+  const bool tiled = w_layout == NVFP4MOE_W_TILED;
+  const FewMatrix gu = {w_gu_packed, w_gu_scales, nullptr, I < (1 << 30) ? 2 * I : 0, H, true, tiled};
+  const FewMatrix dn = {w_d_packed, w_d_scales, nullptr, H, I, true, tiled};
+  return experts_common(x_bf16, x_stride, topk_idx, topk_w, T, k, E, I, gu, dn, w_layout, out_bf16, ws, ws_bytes, stream);
+}
+
 // ---- latent attention ---------------------------------------------------------
 // A strided operand of the latent-attention calls: 16-byte aligned rows.
 static bool row_aligned(const void* p, int64_t stride) { return aligned16(p) && stride >= 0 && stride % 8 == 0; }
@@ -751,6 +893,38 @@ int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, in
   a.qo_token_stride = q_out_token_stride;
   a.qo_head_stride = q_out_head_stride;
   return cuda_status(launch_mla_append(a, stream), "mla_append launch");
+}
+
+int mla_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_tables,
+             int64_t table_stride, int max_pages, const int32_t* free_pages, int num_free, const int32_t* free_count, int T,
+             int32_t* positions, int64_t* slots, int32_t* cu_seqlens, int32_t* seq_lens, int32_t* granted,
+             int32_t* free_count_out, cudaStream_t stream) {
+  t_detail[0] = 0;
+  NVFP4MOE_REQUIRE(B >= 0 && T >= 0 && max_pages >= 0 && num_free >= 0, NVFP4MOE_ERR_INVALID_ARG,
+                   "B = %d T = %d max_pages = %d num_free = %d", B, T, max_pages, num_free);
+  NVFP4MOE_REQUIRE(page_size >= 16 && (page_size & (page_size - 1)) == 0, NVFP4MOE_ERR_UNSUPPORTED,
+                   "page_size = %d must be a power of two >= 16", page_size);
+  NVFP4MOE_REQUIRE(table_stride >= max_pages, NVFP4MOE_ERR_INVALID_ARG, "table_stride %lld < max_pages %d",
+                   (long long)table_stride, max_pages);
+  NVFP4MOE_REQUIRE(free_count && free_count_out && cu_seqlens && (free_pages || num_free == 0) &&
+                       (T == 0 || (positions && slots)) &&
+                       (B == 0 || (past_lens && new_lens && seq_lens && granted && (block_tables || max_pages == 0))),
+                   NVFP4MOE_ERR_INVALID_ARG, "null pointer");
+  const void* words[] = {past_lens, new_lens, block_tables, free_pages, free_count, positions, cu_seqlens, seq_lens, granted,
+                         free_count_out};
+  for (const void* w : words)
+    NVFP4MOE_REQUIRE((reinterpret_cast<uintptr_t>(w) & 3) == 0, NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  NVFP4MOE_REQUIRE((reinterpret_cast<uintptr_t>(slots) & 7) == 0, NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  DeviceInfo d;
+  if (int st = current_device(&d)) return st;
+  MlaPlanArgs a;
+  a.past = past_lens, a.fresh = new_lens;
+  a.B = B, a.shift = __builtin_ctz(unsigned(page_size));
+  a.tables = block_tables, a.table_stride = table_stride, a.max_pages = max_pages;
+  a.free_pages = free_pages, a.num_free = num_free, a.free_count = free_count;
+  a.T = T, a.positions = positions, a.slots = slots;
+  a.cu_seqlens = cu_seqlens, a.seq_lens = seq_lens, a.granted = granted, a.free_count_out = free_count_out;
+  return cuda_status(launch_mla_plan(a, stream), "mla_plan launch");
 }
 
 size_t mla_decode_workspace_size(void) { return mla_decode_workspace_bytes(); }

@@ -1,0 +1,664 @@
+// Products of a few tokens with 4-bit matrices (moe_matvec_*, moe_experts_*):
+// 16-bit activations against NVFP4 or MXFP4 weights in the layouts of the
+// grouped GEMM.
+//
+//   y[t, n] = s sum_k x[t, k] code[n, k] scale[n, k / B]          B = 16 or 32
+//   experts:  h = silu(x Wg^T) * (x Wu^T) for each routed token, then
+//   out[t] = sum over its experts of weight * h Wd^T
+//
+// Bound by the weights' bytes: with at most 32 tokens every matrix is read
+// once and each byte of it serves 4 T flops.  The tensor core takes the codes
+// as float16: a code times its ue4m3 scale has at most 6 significant bits and
+// lies in 2^-10 .. 2688, so the product is exact.  E8M0 scales do not fit that
+// range: of the 256 values of a row that a step takes, the largest scale is
+// the reference 2^X, codes are multiplied by 2^(scale - X + 13), and the sum
+// by 2^(X - 13); what is smaller than 2^-27 of that reference counts as zero.
+// Activations become float16 too, in blocks of 256 values of a token that are
+// multiplied by the power of two which brings the largest into 2^14 .. 2^15:
+// exact for every bf16 or fp16 value above 2^-28 of its block's largest, and
+// smaller ones are off by at most 2^-40 of it.  The gated products h (float32)
+// are rounded to 11 bits by it, an eighth of what the bf16 result is rounded
+// by.  Sums are float32.
+//
+// A warp takes 32 rows of a matrix as two 16-row tiles (of gate and of up in
+// the gated product) and steps of 256 of its columns, a lane 32 bytes of four
+// rows a step.  The rows of a tile are four of each 32, because the blocked
+// scale layout keeps the scales of rows r, r + 32, r + 64 and r + 96 together:
+// so a tile's scales are whole sectors.  Eight columns of a tile's product are
+// tokens.  The warps of a block share rows or columns (WK warps along the
+// columns, their sums joined in shared memory in a fixed order).
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/nvfp4few.h"
+#include "internal.h"
+#include "launch.cuh"
+#include "sm103_ptx.cuh"
+
+namespace nvfp4moe {
+namespace {
+
+__device__ unsigned g_few_flags = 0;
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kStep = 256;                // columns of a matrix in one step of a warp
+constexpr int kUnitBytes = 2 * kStep;     // float16 activations of one token and step
+constexpr int kMaxSegs = 1024;
+
+enum Source { kBf16 = 0, kFp16 = 1, kF32 = 2 };
+enum Mode { kDense = 0, kGateUp = 1, kDown = 2 };
+
+// The experts that a batch hits, in their order: what the down product walks
+// through.  Written by the gate/up kernel.
+struct Plan {
+  int nseg;
+  int pad[63];
+  int expert[kMaxSegs];
+  uint32_t tokens[kMaxSegs];  // bit t: token t is routed to it
+  int base[kMaxSegs];         // first row of h; token t's is base + number of lower tokens
+};
+
+struct FewParams {
+  const void* x;             // [T, K] of Source, or h [T * k, K] float32
+  int64_t x_stride;
+  const uint8_t* frag;       // activations converted beforehand (not SELF): [row][step][kUnitBytes]
+  const float* factor;       // [row][step]
+  int T, k, E;
+  const int32_t* idx;        // [T, k]
+  const float* topk_w;
+  const uint8_t* packed;
+  const uint8_t* scales;
+  const float* gscale;       // null: 1
+  const float* next_gscale;  // gate/up: the down matrices' scales, null: 1
+  int N, K;                  // rows (gate and up together) and columns of one matrix
+  int tiled, wide;           // wide: rows start on 32-byte boundaries
+  int wk;                    // warps of a block along the columns
+  int out_fp16;
+  void* out;
+  Plan* plan;
+};
+
+// 32 bytes of each of a lane's four rows, and their scale words.
+struct Rows {
+  uint32_t w[4][8];
+  uint32_t s[4];
+};
+
+__device__ __forceinline__ void load32(uint32_t (&r)[8], const uint8_t* p, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+  }
+}
+
+// The eight codes of a word as float16 pairs (in order).
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t ue4m3x2_to_half(uint32_t two) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
+  return h;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Where a lane's weights lie: rows g and g + 8 of two tiles, its 32 bytes of a step.
+struct Lane {
+  int64_t w0, w_tile, w_half, w_step, w_matrix;  // byte offsets
+  int64_t s0, s_tile, s_step, s_matrix;
+  int tg;
+};
+
+template <bool MX>
+__device__ __forceinline__ Lane lane_of(const FewParams& p, int rb, int st, int64_t tile_rows, int lane) {
+  Lane l;
+  const int g = lane >> 2;
+  l.tg = lane & 3;
+  const int64_t half = p.K / 2, kc = (p.K + 255) / 256, kb = p.K / (MX ? 128 : 64);
+  const int r = 4 * st + (g & 3) + 32 * (g >> 2);
+  // tile_rows: rows between the two tiles, a multiple of 128 (gate and up) or 4
+  if (p.tiled) {
+    l.w0 = int64_t(rb) * kc * 16384 + r * 128 + l.tg * 32;
+    l.w_tile = (tile_rows / 128) * kc * 16384 + (tile_rows % 128) * 128;
+    l.w_half = 64 * 128;
+    l.w_step = 16384;
+    l.w_matrix = int64_t(p.N / 128) * kc * 16384;
+  } else {
+    l.w0 = (int64_t(rb) * 128 + r) * half + l.tg * 32;
+    l.w_tile = tile_rows * half;
+    l.w_half = 64 * half;
+    l.w_step = 128;
+    l.w_matrix = int64_t(p.N) * half;
+  }
+  l.s0 = int64_t(rb) * kb * 512 + (4 * st + (g & 3)) * 16 + (g >> 2) * 4 + (MX ? (l.tg >> 1) * 512 + (l.tg & 1) * 2 : l.tg * 512);
+  l.s_tile = (tile_rows / 128) * kb * 512 + (tile_rows % 128) * 16;
+  l.s_step = MX ? 1024 : 2048;
+  l.s_matrix = int64_t(p.N / 128) * kb * 512;
+  return l;
+}
+
+template <bool MX>
+__device__ __forceinline__ void load_rows(Rows& r, const FewParams& p, const Lane& l, int e, int step) {
+  if (step * kStep + l.tg * 64 < p.K) {
+    const uint8_t* w = p.packed + e * l.w_matrix + l.w0 + step * l.w_step;
+    const uint8_t* s = p.scales + e * l.s_matrix + l.s0 + step * l.s_step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (tile i / 2, rows g or g + 8)
+      load32(r.w[i], w + (i >> 1) * l.w_tile + (i & 1) * l.w_half, p.wide);
+      const uint8_t* sp = s + (i >> 1) * l.s_tile + (i & 1) * 8;
+      r.s[i] = MX ? uint32_t(__ldg(reinterpret_cast<const uint16_t*>(sp))) : __ldg(reinterpret_cast<const uint32_t*>(sp));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.s[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r.w[i][j] = 0;
+    }
+  }
+}
+
+// Converts 8 values that the lane holds of a block of 256 to float16 as the
+// header says; returns the factor that undoes it.
+__device__ __forceinline__ float block_to_half(const float (&v)[8], uint4* out) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(kFull, top) >> 23;
+  const int e = top == 255 ? 127 : max(int(top) - 127, -112);
+  const float m = exp2i(14 - e);
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 t = __floats2half2_rn(v[2 * i] * m, v[2 * i + 1] * m);
+    h[i] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  *out = make_uint4(h[0], h[1], h[2], h[3]);
+  return exp2i(e - 14);
+}
+
+// Values 8 lane .. 8 lane + 7 of step `step` of a row of K values (zeros past its end).
+template <int SRC>
+__device__ __forceinline__ void load_block(float (&v)[8], const void* row, int step, int K, int lane) {
+  const int k = step * kStep + 8 * lane;
+  if (k >= K) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    return;
+  }
+  if (SRC == kF32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(row) + k);
+    const float4 a = q[0], b = q[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    return;
+  }
+  const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (SRC == kBf16) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// Activations of all rows beforehand: a warp each row and step.
+template <int SRC>
+__global__ void __launch_bounds__(kThreads) convert_kernel(const void* x, int64_t x_stride, int rows, int K,
+                                                           uint8_t* frag, float* factor) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int steps = (K + kStep - 1) / kStep, lane = threadIdx.x & 31;
+  const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int row = int(item / steps), step = int(item % steps);
+  if (row >= rows) return;
+  float v[8];
+  load_block<SRC>(v, static_cast<const uint8_t*>(x) + row * x_stride * (SRC == kF32 ? 4 : 2), step, K, lane);
+  uint4 h;
+  const float f = block_to_half(v, &h);
+  // piece j of lane group tg of the product at 64 j + 16 tg
+  *reinterpret_cast<uint4*>(frag + item * kUnitBytes + (lane & 7) * 64 + (lane >> 3) * 16) = h;
+  if (lane == 0) factor[item] = f;
+}
+
+// The experts that the batch hits, written by one block.  mask, count: E words
+// of shared memory each.
+__device__ void write_plan(const FewParams& p, uint32_t* mask, int* count) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.T * p.k;
+  __shared__ int sum_warp[2][kWarps];
+  for (int e = tid; e < p.E; e += kThreads) mask[e] = 0, count[e] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int e = p.idx[i];
+    if (e >= 0 && e < p.E) {
+      atomicOr(mask + e, 1u << (i / p.k));
+      atomicAdd(count + e, 1);
+    } else {
+      atomicOr(&g_few_flags, kFlagBadData);
+    }
+  }
+  __syncthreads();
+  const int per = (p.E + kThreads - 1) / kThreads, e0 = tid * per;
+  int segs = 0, rows = 0;
+  for (int e = e0; e < min(e0 + per, p.E); ++e) segs += mask[e] != 0, rows += count[e];
+  int a = segs, b = rows;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int ua = __shfl_up_sync(kFull, a, d), ub = __shfl_up_sync(kFull, b, d);
+    if (lane >= d) a += ua, b += ub;
+  }
+  if (lane == 31) sum_warp[0][warp] = a, sum_warp[1][warp] = b;
+  __syncthreads();
+  int seg = a - segs, row = b - rows;
+  for (int w = 0; w < warp; ++w) seg += sum_warp[0][w], row += sum_warp[1][w];
+  for (int e = e0; e < min(e0 + per, p.E); ++e) {
+    if (mask[e]) {
+      p.plan->expert[seg] = e;
+      p.plan->tokens[seg] = mask[e];
+      p.plan->base[seg] = row;
+      ++seg;
+    }
+    row += count[e];
+  }
+  if (tid == kThreads - 1) p.plan->nseg = seg;
+  __syncthreads();
+}
+
+template <bool MX, int SRC, int MODE, int NB, bool SELF>
+__global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const FewParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t s_or[kWarps];
+  __shared__ int s_sum[kWarps], s_first[kWarps];
+  __shared__ float s_weight[32];
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wk = warp % p.wk, wr = warp / p.wk, wrs = kWarps / p.wk;
+  const int steps = (p.K + kStep - 1) / kStep;
+
+  // The experts of this block, the tokens of each and their rows of activations.
+  int e = 0, base = 0, nseg = 1;
+  uint32_t tokens = p.T == 32 ? kFull : (1u << p.T) - 1;
+  if (MODE == kGateUp) {
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+      write_plan(p, reinterpret_cast<uint32_t*>(smem), reinterpret_cast<int*>(smem) + p.E);
+    const int f = blockIdx.y, n = p.T * p.k;
+    e = p.idx[f];
+    if (e < 0 || e >= p.E) return;             // write_plan raises the flag
+    uint32_t bits = 0;
+    int below = 0, first = n;
+    for (int i = tid; i < n; i += kThreads) {
+      const int v = p.idx[i];
+      if (v == e) {
+        bits |= 1u << (i / p.k);
+        first = min(first, i);
+      }
+      below += v >= 0 && v < e;
+    }
+    bits = __reduce_or_sync(kFull, bits);
+    below = __reduce_add_sync(kFull, below);
+    first = __reduce_min_sync(kFull, first);
+    if (lane == 0) s_or[warp] = bits, s_sum[warp] = below, s_first[warp] = first;
+    __syncthreads();
+    tokens = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      tokens |= s_or[w];
+      base += s_sum[w];
+      first = min(first, s_first[w]);
+    }
+    if (first != f) return;                    // the block of the expert's first token has it
+    for (int t = warp; t < p.T; t += kWarps) { // a token's weight of this expert
+      const bool mine = lane < p.k && p.idx[t * p.k + lane] == e;
+      float w = mine ? p.topk_w[t * p.k + lane] : 0.0f;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(kFull, w, d);
+      if (lane == 0) s_weight[t] = w;
+    }
+  } else if (MODE == kDown) {
+    nseg = p.plan->nseg;
+  }
+  const int units = nseg * steps;
+
+  // This warp's tiles.
+  const int sub = blockIdx.x * wrs + wr;
+  const int rb = MODE == kGateUp ? sub >> 3 : sub >> 2, st = MODE == kGateUp ? sub & 7 : 2 * (sub & 3);
+  const Lane l = lane_of<MX>(p, rb, st, MODE == kGateUp ? p.N / 2 : 4, lane);
+
+  int step = wk, seg = 0;
+  while (step >= steps) step -= steps, ++seg;
+  Rows cur;
+  if (wk < units) load_rows<MX>(cur, p, l, MODE == kDown ? p.plan->expert[seg] : e, step);
+
+  // Activations as float16: [step][piece j][token of the expert][16 bytes of 4 lane groups].
+  float* factor = nullptr;
+  if (SELF) {
+    const int rows = MODE == kDown ? p.T * p.k : p.T;   // an upper bound, also of a gate/up block's tokens
+    factor = reinterpret_cast<float*>(smem + int64_t(rows) * steps * kUnitBytes);
+    for (int s = 0; s < nseg; ++s) {
+      const uint32_t who = MODE == kDown ? p.plan->tokens[s] : tokens;
+      const int first = MODE == kDown ? p.plan->base[s] : 0, m = __popc(who);
+      for (int i = warp; i < m * steps; i += kWarps) {
+        const int slot = i / steps, at = i - slot * steps;
+        const int row = MODE == kDown ? first + slot : int(__fns(who, 0, slot + 1));
+        float v[8];
+        load_block<SRC>(v, static_cast<const uint8_t*>(p.x) + row * p.x_stride * (SRC == kF32 ? 4 : 2), at, p.K, lane);
+        uint4 h;
+        const float f = block_to_half(v, &h);
+        uint8_t* dst = smem + (int64_t(first) * steps + int64_t(at) * m) * kUnitBytes;
+        *reinterpret_cast<uint4*>(dst + ((lane & 7) * m + slot) * 64 + (lane >> 3) * 16) = h;
+        if (lane == 0) factor[(first + slot) * steps + at] = f;
+      }
+    }
+    __syncthreads();
+  }
+
+  float total[2][NB][4];
+#pragma unroll
+  for (int i = 0; i < 2 * NB * 4; ++i) (&total[0][0][0])[i] = 0.0f;
+  const int g = lane >> 2;
+
+  for (int u = wk; u < units; u += p.wk) {
+    // the next step's weights on their way
+    int nstep = step + p.wk, next = seg;
+    while (nstep >= steps) nstep -= steps, ++next;
+    Rows nxt;
+    if (u + p.wk < units) load_rows<MX>(nxt, p, l, MODE == kDown ? p.plan->expert[next] : e, nstep);
+
+    if (MODE == kDown) tokens = p.plan->tokens[seg], base = p.plan->base[seg];
+    const int m = __popc(tokens);
+    // this lane's column of each eight tokens
+    const uint8_t* from[NB];
+    bool has[NB];
+    int stride_j;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int t = 8 * b + g;
+      has[b] = (tokens >> t) & 1;
+      const int slot = __popc(tokens & ((1u << t) - 1));
+      if (SELF) {
+        from[b] = smem + (int64_t(MODE == kDown ? base : 0) * steps + int64_t(step) * m) * kUnitBytes + slot * 64 + l.tg * 16;
+      } else {
+        const int64_t row = MODE == kDown ? base + slot : t;
+        from[b] = p.frag + (row * steps + step) * kUnitBytes + l.tg * 16;
+      }
+    }
+    stride_j = SELF ? m * 64 : 64;
+
+    uint32_t ref[4];                    // MX: a row's largest scale of this step
+    if (MX) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t top = max(cur.s[i] & 255u, cur.s[i] >> 8);
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
+        ref[i] = max(top, __shfl_xor_sync(kFull, top, 2));
+      }
+    }
+    float acc[2][NB][4];
+#pragma unroll
+    for (int i = 0; i < 2 * NB * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
+    uint32_t sc[4];                     // the rows' scales of this word as float16 pairs
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!MX && (j & 1) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t two = ue4m3x2_to_half(j < 4 ? cur.s[i] : cur.s[i] >> 16);
+          sc[i] = __byte_perm(two, two, (j & 2) ? 0x3232 : 0x1010);
+        }
+      }
+      if (MX && (j & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = int(j < 4 ? cur.s[i] & 255u : cur.s[i] >> 8) - int(ref[i]) + 28;
+          sc[i] = uint32_t(max(x, 0)) * 0x04000400u;   // exponent fields of 2^(scale - reference + 13), or 0
+        }
+      }
+      uint32_t a[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        codes_to_half(cur.w[i][j], a[i]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) a[i][q] = hmul2(a[i][q], sc[i]);
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (NB > 1 && ((tokens >> (8 * b)) & 255u) == 0) continue;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (has[b]) x = *reinterpret_cast<const uint4*>(from[b] + j * stride_j);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma(acc[i][b], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
+          mma(acc[i][b], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
+        }
+      }
+    }
+    // into the totals, tokens of this expert only
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int t = 8 * b + 2 * l.tg + c;
+        if ((tokens >> t) & 1) {
+          const int slot = __popc(tokens & ((1u << t) - 1));
+          const float f = SELF ? factor[(MODE == kDown ? base + slot : slot) * steps + step]
+                               : p.factor[int64_t(MODE == kDown ? base + slot : t) * steps + step];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = acc[i >> 1][b][(i & 1) * 2 + c];
+            if (MX) {
+              // 2^(ref - 127 - 13) as two factors of float32's normal range
+              const int x = int(ref[i]) - 140;
+              v = ref[i] == 255 ? __int_as_float(0x7FFFFFFF) : v * exp2i(x >> 1);
+              total[i >> 1][b][(i & 1) * 2 + c] += v * f * exp2i(x - (x >> 1));
+            } else {
+              total[i >> 1][b][(i & 1) * 2 + c] += v * f;
+            }
+          }
+        }
+      }
+    }
+    cur = nxt;
+    step = nstep;
+    seg = next;
+  }
+
+  // Joins the warps along the columns: [warp][tile][token group][row 0..15][8 tokens].
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float* at = red + ((warp * 2 + i) * NB + b) * 128 + 2 * l.tg;
+      *reinterpret_cast<float2*>(at + g * 8) = make_float2(total[i][b][0], total[i][b][1]);
+      *reinterpret_cast<float2*>(at + (g + 8) * 8) = make_float2(total[i][b][2], total[i][b][3]);
+    }
+  __syncthreads();
+  auto joined = [&](int w, int tile, int row, int t) {  // of the warps with rows group w
+    float v = 0.0f;
+    for (int c = 0; c < p.wk; ++c) v += red[(((w * p.wk + c) * 2 + tile) * NB + (t >> 3)) * 128 + row * 8 + (t & 7)];
+    return v;
+  };
+  if (MODE == kGateUp) {
+    const int m = __popc(tokens), I = p.N / 2;
+    const float s = p.gscale ? p.gscale[e] : 1.0f, s_next = p.next_gscale ? p.next_gscale[e] : 1.0f;
+    float* h = static_cast<float*>(p.out);
+    for (int i = tid; i < 16 * wrs * m; i += kThreads) {
+      const int row = i & 15, w = (i >> 4) % wrs, slot = (i >> 4) / wrs;
+      const int t = int(__fns(tokens, 0, slot + 1)), at = blockIdx.x * wrs + w;
+      const float gate = joined(w, 0, row, t) * s, up = joined(w, 1, row, t) * s;
+      const int col = (at >> 3) * 128 + (at & 7) * 4 + (row & 3) + 32 * (row >> 2);
+      h[int64_t(base + slot) * I + col] = gate / (1.0f + expf(-gate)) * up * s_weight[t] * s_next;
+    }
+  } else {
+    const float s = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
+    for (int i = tid; i < 32 * wrs * p.T; i += kThreads) {
+      const int r = i & 31, w = (i >> 5) % wrs, t = (i >> 5) / wrs;
+      const int at = blockIdx.x * wrs + w;
+      // rows 8 (at % 4) + 0..7 of each 32 of the 128: the first four of tile 0, the others of tile 1
+      const float v = joined(w, (r >> 2) & 1, (r & 3) + 4 * (r >> 3), t) * s;
+      const int64_t o = int64_t(t) * p.N + (at >> 2) * 128 + (at & 3) * 8 + (r & 7) + 32 * (r >> 3);
+      if (MODE == kDense && p.out_fp16)
+        static_cast<__half*>(p.out)[o] = __float2half_rn(v);
+      else
+        static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
+int64_t steps_of(int K) { return (K + kStep - 1) / kStep; }
+int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
+int64_t frag_bytes(int64_t rows, int K) { return round256(rows * steps_of(K) * kUnitBytes) + round256(rows * steps_of(K) * 4); }
+
+// Blocks convert the activations that they need themselves up to this many
+// bytes; above, one kernel does it for all.
+constexpr int64_t kSelfBytes = 64 * 1024;
+bool self_converts(int64_t rows, int K) { return rows * steps_of(K) * (kUnitBytes + 4) <= kSelfBytes; }
+
+template <bool MX, int SRC, int MODE, int NB, bool SELF>
+cudaError_t launch_one(const FewParams& p, dim3 grid, size_t smem, cudaStream_t st) {
+  auto kernel = few_kernel<MX, SRC, MODE, NB, SELF>;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (err != cudaSuccess) return err;
+  }
+  return launch_kernel(kernel, grid, dim3(kThreads), smem, st, false, p);
+}
+
+template <bool MX, int SRC, int MODE>
+cudaError_t launch_few(const FewParams& p, int64_t rows, bool self, dim3 grid, cudaStream_t st) {
+  const int nb = p.T <= 8 ? 1 : (p.T <= 16 ? 2 : 4);
+  size_t smem = size_t(kWarps) * nb * 1024;
+  if (self) smem = max(smem, size_t(rows * steps_of(p.K) * (kUnitBytes + 4)));
+  if (MODE == kGateUp) smem = max(smem, size_t(p.E) * 8);
+  if (self)
+    return nb == 1   ? launch_one<MX, SRC, MODE, 1, true>(p, grid, smem, st)
+           : nb == 2 ? launch_one<MX, SRC, MODE, 2, true>(p, grid, smem, st)
+                     : launch_one<MX, SRC, MODE, 4, true>(p, grid, smem, st);
+  return nb == 1   ? launch_one<MX, kF32, MODE, 1, false>(p, grid, smem, st)
+         : nb == 2 ? launch_one<MX, kF32, MODE, 2, false>(p, grid, smem, st)
+                   : launch_one<MX, kF32, MODE, 4, false>(p, grid, smem, st);
+}
+
+template <int SRC>
+cudaError_t launch_convert(const void* x, int64_t stride, int64_t rows, int K, uint8_t* frag, FewParams* p, cudaStream_t st) {
+  float* factor = reinterpret_cast<float*>(frag + round256(rows * steps_of(K) * kUnitBytes));
+  p->frag = frag;
+  p->factor = factor;
+  const int64_t blocks = (rows * steps_of(K) + kWarps - 1) / kWarps;
+  return launch_kernel(convert_kernel<SRC>, dim3(unsigned(blocks)), dim3(kThreads), 0, st, false, x, stride, int(rows), K,
+                       frag, factor);
+}
+
+// Warps of a block along the columns.
+int column_warps(int T) { return T <= 2 ? 8 : (T <= 4 ? 4 : 2); }
+
+void set_matrix(FewParams* p, const FewMatrix& w) {
+  p->packed = w.packed;
+  p->scales = w.scales;
+  p->gscale = w.gscale;
+  p->N = w.N;
+  p->K = w.K;
+  p->tiled = w.tiled;
+  p->wide = (reinterpret_cast<uintptr_t>(w.packed) & 31) == 0;
+}
+
+}  // namespace
+
+size_t few_matvec_workspace_bytes(int T, int K) { return self_converts(T, K) ? 0 : size_t(frag_bytes(T, K)); }
+
+size_t few_experts_workspace_bytes(int T, int k, int H, int I) {
+  int64_t b = round256(sizeof(Plan)) + round256(int64_t(T) * k * I * 4);
+  if (!self_converts(T, H)) b += frag_bytes(T, H);
+  if (!self_converts(int64_t(T) * k, I)) b += frag_bytes(int64_t(T) * k, I);
+  return size_t(b);
+}
+
+cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
+                              cudaStream_t st) {
+  FewParams p = {};
+  p.x = x, p.x_stride = x_stride;
+  p.T = T, p.k = 1, p.E = 1;
+  set_matrix(&p, w);
+  p.wk = column_warps(T);
+  p.out_fp16 = fp16;
+  p.out = out;
+  const bool self = self_converts(T, w.K);
+  if (!self) {
+    const cudaError_t err = fp16 ? launch_convert<kFp16>(x, x_stride, T, w.K, static_cast<uint8_t*>(ws), &p, st)
+                                 : launch_convert<kBf16>(x, x_stride, T, w.K, static_cast<uint8_t*>(ws), &p, st);
+    if (err != cudaSuccess) return err;
+  }
+  const dim3 grid(unsigned(w.N / (32 * (kWarps / p.wk))));
+  if (w.mx)
+    return fp16 ? launch_few<true, kFp16, kDense>(p, T, self, grid, st) : launch_few<true, kBf16, kDense>(p, T, self, grid, st);
+  return fp16 ? launch_few<false, kFp16, kDense>(p, T, self, grid, st) : launch_few<false, kBf16, kDense>(p, T, self, grid, st);
+}
+
+cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* idx, const float* topk_w, int T, int k,
+                               int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, cudaStream_t st) {
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  FewParams p = {};
+  p.plan = reinterpret_cast<Plan*>(at);
+  at += round256(sizeof(Plan));
+  float* h = reinterpret_cast<float*>(at);
+  at += round256(int64_t(T) * k * d.K * 4);
+  p.x = x, p.x_stride = x_stride;
+  p.T = T, p.k = k, p.E = E;
+  p.idx = idx, p.topk_w = topk_w;
+  set_matrix(&p, gu);
+  p.next_gscale = d.gscale;
+  p.out = h;
+  p.wk = 8;
+  bool self = self_converts(T, gu.K);
+  cudaError_t err;
+  if (!self) {
+    if ((err = launch_convert<kBf16>(x, x_stride, T, gu.K, at, &p, st)) != cudaSuccess) return err;
+    at += frag_bytes(T, gu.K);
+  }
+  dim3 grid(unsigned(d.K / (16 * (kWarps / p.wk))), unsigned(T * k));
+  err = gu.mx ? launch_few<true, kBf16, kGateUp>(p, T, self, grid, st) : launch_few<false, kBf16, kGateUp>(p, T, self, grid, st);
+  if (err != cudaSuccess) return err;
+
+  const int64_t rows = int64_t(T) * k;
+  set_matrix(&p, d);
+  p.gscale = p.next_gscale = nullptr;     // in h already
+  p.x = h, p.x_stride = d.K;
+  p.out = out;
+  self = self_converts(rows, d.K);
+  if (!self && (err = launch_convert<kF32>(h, d.K, rows, d.K, at, &p, st)) != cudaSuccess) return err;
+  grid = dim3(unsigned(d.N / (32 * (kWarps / p.wk))));
+  return d.mx ? launch_few<true, kF32, kDown>(p, rows, self, grid, st) : launch_few<false, kF32, kDown>(p, rows, self, grid, st);
+}
+
+cudaError_t few_flags_address(unsigned** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_few_flags); }
+
+}  // namespace nvfp4moe

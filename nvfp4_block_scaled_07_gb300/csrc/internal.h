@@ -146,6 +146,28 @@ cudaError_t launch_tile_weights(const uint8_t* w_packed, int64_t rows, int K, ui
                                 cudaStream_t st);
 cudaError_t gemm_flags_address(unsigned** at);
 
+cudaError_t launch_route_grouped(const float* logits, const float* bias, int T, int E, int k, int groups, int keep, int best,
+                                 int softmax, int renorm, float factor, int32_t* idx, float* w, cudaStream_t st);
+
+// ---- few tokens (few_tokens.cu) ------------------------------------------------
+constexpr int kFewMaxTokens = 32;
+struct FewMatrix {
+  const uint8_t* packed;
+  const uint8_t* scales;
+  const float* gscale;  // null: 1
+  int N, K;
+  bool mx, tiled;
+};
+size_t few_matvec_workspace_bytes(int T, int K);
+size_t few_experts_workspace_bytes(int T, int k, int H, int I);
+// x [T, K] 16-bit, rows x_stride elements apart; out [T, N]; 1 <= T <= 32.
+cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
+                              cudaStream_t st);
+// gu: [E, 2I, H], d: [E, H, I].
+cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* idx, const float* topk_w, int T, int k,
+                               int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, cudaStream_t st);
+cudaError_t few_flags_address(unsigned** at);
+
 // ---- latent attention (mla_*.cu) --------------------------------------------
 struct MlaAppendArgs {
   const void* latent;
@@ -217,6 +239,27 @@ struct MlaPrefillArgs {
 };
 int launch_mla_prefill(const MlaPrefillArgs& a, cudaStream_t st);
 cudaError_t mla_prefill_flags_address(unsigned** at);
+
+struct MlaPlanArgs {
+  const int32_t* past;
+  const int32_t* fresh;
+  int B, shift;           // log2 of the page size
+  int32_t* tables;
+  int64_t table_stride;
+  int max_pages;
+  const int32_t* free_pages;
+  int num_free;
+  const int32_t* free_count;
+  int T;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* cu_seqlens;
+  int32_t* seq_lens;
+  int32_t* granted;
+  int32_t* free_count_out;
+};
+cudaError_t launch_mla_plan(const MlaPlanArgs& a, cudaStream_t st);
+cudaError_t mla_plan_flags_address(unsigned** at);
 
 // Per-thread error message used by nvfp4moe_last_error_detail().
 void set_error_detail(const char* fmt, ...);

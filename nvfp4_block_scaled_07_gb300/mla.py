@@ -7,6 +7,7 @@ calls the C entry point of the same name on the current CUDA stream.
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 
 import torch
 
@@ -19,6 +20,7 @@ DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 
 _i, _i64, _sz, _p, _f = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
 _SIGS = {
+    "mla_plan": (_i, [_p, _p, _i, _i, _p, _i64, _i, _p, _i, _p, _i, _p, _p, _p, _p, _p, _p, _p]),
     "mla_append": (_i, [_p, _i64, _p, _i64, _p, _f, _p, _p, _i, _p, _i64, _i, _i, _p, _i64, _p, _p, _i64, _i64, _i, _p,
                         _i64, _i64, _p]),
     "mla_decode_workspace_size": (_sz, []),
@@ -101,6 +103,58 @@ def rope_table(max_positions, base=10000.0, device="cuda"):
     inv = float(base) ** (-torch.arange(0, ROPE, 2, dtype=torch.float64, device=device) / ROPE)
     ang = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * inv
     return torch.cat([ang.cos(), ang.sin()], dim=1).to(torch.float32)
+
+
+@dataclass
+class TokenPlan:
+    """Where a step's new tokens go: what the other calls take (see mla_plan)."""
+    positions: torch.Tensor     # int32 [T]
+    slots: torch.Tensor         # int64 [T]
+    cu_seqlens: torch.Tensor    # int32 [B + 1]
+    seq_lens: torch.Tensor      # int32 [B]
+    granted: torch.Tensor       # int32 [B]
+    free_count: torch.Tensor    # int32 [1]
+
+
+def alloc_token_plan(B, T, device, free_count=None):
+    """Buffers for mla_plan(out=...); free_count: the caller's, updated in place."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return TokenPlan(torch.empty(T, **i32), torch.empty(T, dtype=torch.int64, device=device), torch.empty(B + 1, **i32),
+                     torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32) if free_count is None else free_count)
+
+
+def mla_plan(past_lens, new_lens, block_tables, free_pages, free_count, page_size, tokens, out=None):
+    """Pages and slots of a step's new tokens, on the GPU.
+
+    past_lens, new_lens int32 [B]: tokens that each request has in the cache and
+    brings; block_tables int32 [B, max_pages], whose new entries are written;
+    free_pages int32 [n] with free_count int32 [1] of them free, popped from the
+    end; tokens: rows of the step's buffers (those past the last token get slot
+    -1).  A request whose pages are not there is refused: granted 0, slots -1.
+    Returns a TokenPlan (`out`, if given)."""
+    dev = past_lens.get_device()
+    _on_cuda(dev, "past_lens")
+    B = past_lens.shape[0]
+    i32 = torch.int32
+    past_at = _dense(past_lens, i32, (B,), "past_lens", dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables has two dimensions")
+    max_pages = block_tables.shape[1]
+    if block_tables.dtype is not i32 or block_tables.shape[0] != B or block_tables.get_device() != dev:
+        _refuse(block_tables, i32, (B, max_pages), "block_tables", dev)
+    step = block_tables.stride()
+    if (max_pages > 1 and step[1] != 1) or (B > 1 and step[0] < max_pages):
+        raise ValueError(f"block_tables: strides {step}, rows must be contiguous and apart")
+    free = free_pages.numel()
+    p = alloc_token_plan(B, tokens, past_lens.device) if out is None else out
+    _b._check(_lib.mla_plan(
+        past_at, _dense(new_lens, i32, (B,), "new_lens", dev), B, page_size, block_tables.data_ptr(),
+        step[0] if B > 1 else max_pages, max_pages, _dense(free_pages, i32, (free,), "free_pages", dev), free,
+        _dense(free_count, i32, (1,), "free_count", dev), tokens, _dense(p.positions, i32, (tokens,), "positions", dev),
+        _dense(p.slots, torch.int64, (tokens,), "slots", dev), _dense(p.cu_seqlens, i32, (B + 1,), "cu_seqlens", dev),
+        _dense(p.seq_lens, i32, (B,), "seq_lens", dev), _dense(p.granted, i32, (B,), "granted", dev),
+        _dense(p.free_count, i32, (1,), "free_count_out", dev), _stream(dev)), "mla_plan")
+    return p
 
 
 def mla_append(latent, k_rope, positions, slots, rope_table, cache, norm_weight=None, eps=1e-6, interleaved=True,

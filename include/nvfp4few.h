@@ -54,7 +54,7 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *   x device [T, K] of x_dtype, rows x_stride elements apart (a multiple of 8;
  *   0: the same row again; not read with T = 1); w_packed device uint8 [N, K/2]
  *   or its tiled copy, w_scales blocked; out device [T, N] contiguous.
- *   ws: moe_matvec_workspace_size(T, K) bytes (may be 0), 256-byte aligned.
+ *   ws: moe_matvec_workspace_size(T, N, K) bytes (may be 0), 256-byte aligned.
  *
  * moe_experts_nvfp4: the expert layer after the router.  For the tokens routed
  *   to expert e: h = silu(x Wg^T) * (x Wu^T), Wg and Wu rows [0, I) and
@@ -83,7 +83,7 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  * 128 (MXFP4), N, H and I multiples of 128, 1 <= E <= 1024, 1 <= k <= 32. */
 #define NVFP4MOE_X_BF16 0
 #define NVFP4MOE_X_FP16 1
-size_t moe_matvec_workspace_size(int T, int K);
+size_t moe_matvec_workspace_size(int T, int N, int K);
 int moe_matvec_nvfp4(const void* x, int64_t x_stride, int T, int x_dtype,
                      const uint8_t* w_packed, const uint8_t* w_scales, const float* w_gscale,
                      int N, int K, int w_layout, void* out, void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -84,7 +84,7 @@ _SIGS = {
 # include/nvfp4few.h
 _FEW_SIGS = {
     "moe_route_grouped": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]),
-    "moe_matvec_workspace_size": (_sz, [_i, _i]),
+    "moe_matvec_workspace_size": (_sz, [_i, _i, _i]),
     "moe_matvec_nvfp4": (_i, [_p, _i64, _i, _i, _p, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
     "moe_matvec_mxfp4": (_i, [_p, _i64, _i, _i, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
     "moe_experts_workspace_size": (_sz, [_i, _i, _i, _i]),
@@ -766,8 +766,8 @@ def _few_workspace(x, need, workspace):
     return workspace
 
 
-def moe_matvec_workspace_size(T, K):
-    return int(_lib.moe_matvec_workspace_size(T, K))
+def moe_matvec_workspace_size(T, N, K):
+    return int(_lib.moe_matvec_workspace_size(T, N, K))
 
 
 def _matvec(fmt, x, w_packed, w_scales, w_gscale, out, workspace):
@@ -780,7 +780,7 @@ def _matvec(fmt, x, w_packed, w_scales, w_gscale, out, workspace):
     else:
         _need(out, x.dtype, (T, N), "out")
         _same_device(x, out, "out")
-    ws = _few_workspace(x, moe_matvec_workspace_size(T, K), workspace)
+    ws = _few_workspace(x, moe_matvec_workspace_size(T, N, K), workspace)
     call = _lib.moe_matvec_nvfp4 if fmt == "nvfp4" else _lib.moe_matvec_mxfp4
     _check(call(_ptr(x), step, T, X_DTYPE[x.dtype], *w_args, N, K, layout, _ptr(out), _ptr(ws),
                 0 if ws is None else ws.numel(), _stream_of(x)), f"moe_matvec_{fmt}")

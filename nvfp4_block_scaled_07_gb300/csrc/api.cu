@@ -99,7 +99,7 @@ uint32_t wait_limit_us() { return g_wait_limit_us.load(std::memory_order_relaxed
 namespace nvfp4moe {
 namespace {
 // The sticky flags of the kernel files that raise any, on the current device.
-constexpr int kFlagWords = 7;
+constexpr int kFlagWords = 8;
 struct FlagWords {
   unsigned* at[kFlagWords];
 };
@@ -122,7 +122,7 @@ cudaError_t read_and_clear_flags(unsigned* flags, cudaStream_t st) {
   if ((err = prep_flags_address(&w.at[0])) != cudaSuccess || (err = gemm_flags_address(&w.at[1])) != cudaSuccess ||
       (err = mla_append_flags_address(&w.at[2])) != cudaSuccess || (err = mla_decode_flags_address(&w.at[3])) != cudaSuccess ||
       (err = mla_prefill_flags_address(&w.at[4])) != cudaSuccess || (err = few_flags_address(&w.at[5])) != cudaSuccess ||
-      (err = mla_plan_flags_address(&w.at[6])) != cudaSuccess)
+      (err = mla_plan_flags_address(&w.at[6])) != cudaSuccess || (err = stream_flags_address(&w.at[7])) != cudaSuccess)
     return err;
   std::lock_guard<std::mutex> lock(g_status_mutex);
   collect_flags<<<1, 32, 0, st>>>(w);
@@ -729,9 +729,9 @@ static int check_matrix(const FewMatrix& w, int n_of, const char* name) {
   return NVFP4MOE_OK;
 }
 
-size_t moe_matvec_workspace_size(int T, int K) {
-  if (T < 1 || T > kFewMaxTokens || K < 1) return 0;
-  return few_matvec_workspace_bytes(T, K);
+size_t moe_matvec_workspace_size(int T, int N, int K) {
+  if (T < 1 || T > kFewMaxTokens || N < 1 || K < 1) return 0;
+  return few_matvec_workspace_bytes(T, N, K);
 }
 
 static int matvec_common(const void* x, int64_t x_stride, int T, int x_dtype, const FewMatrix& w, int w_layout, void* out,
@@ -747,12 +747,12 @@ static int matvec_common(const void* x, int64_t x_stride, int T, int x_dtype, co
   NVFP4MOE_REQUIRE(x && out && aligned16(x) && aligned16(out), NVFP4MOE_ERR_INVALID_ARG, "null or misaligned pointer");
   NVFP4MOE_REQUIRE(T == 1 || (x_stride >= 0 && x_stride % 8 == 0), NVFP4MOE_ERR_INVALID_ARG,
                    "x_stride %lld must be a multiple of 8", (long long)x_stride);
-  const size_t need = moe_matvec_workspace_size(T, w.K);
+  const size_t need = moe_matvec_workspace_size(T, w.N, w.K);
   NVFP4MOE_REQUIRE(need == 0 || (ws && ws_bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255) == 0),
                    NVFP4MOE_ERR_WORKSPACE, "workspace %zu < %zu or not 256-byte aligned", ws_bytes, need);
   DeviceInfo d;
   if (int st = current_device(&d)) return st;
-  return cuda_status(launch_few_matvec(x, T == 1 ? 0 : x_stride, T, x_dtype == NVFP4MOE_X_FP16, w, out, ws, stream),
+  return cuda_status(launch_few_matvec(x, T == 1 ? 0 : x_stride, T, x_dtype == NVFP4MOE_X_FP16, w, out, ws, d.num_sms, stream),
                      "matvec launch");
 }
 
@@ -799,7 +799,8 @@ static int experts_common(const void* x, int64_t x_stride, const int32_t* topk_i
                    "workspace %zu < %zu or not 256-byte aligned", ws_bytes, need);
   DeviceInfo d;
   if (int st = current_device(&d)) return st;
-  return cuda_status(launch_few_experts(x, T == 1 ? 0 : x_stride, topk_idx, topk_w, T, k, E, gu, dn, out, ws, stream),
+  return cuda_status(launch_few_experts(x, T == 1 ? 0 : x_stride, topk_idx, topk_w, T, k, E, gu, dn, out, ws,
+                                        d.num_sms, stream),
                      "experts launch");
 }
 

@@ -1,0 +1,589 @@
+// The products of a few tokens as one stream of weights over all SMs
+// (moe_matvec_*, moe_experts_* from few_stream_takes() on).
+//
+// The work is a list of stages in order: of a tile (128 rows of a matrix, or
+// 64 of gate and the same 64 of up) the steps of 256 columns, of the down
+// product all steps of all experts.  Every SM takes an equal range of it,
+// whatever tiles that cuts.  A block's producer warp keeps a ring of stages in
+// flight (weights by tensor copies, 18 KB, with the activations of the
+// tokens that the step needs); its other warps form groups of four, which take
+// the stages in turn, 32 rows a warp.  A tile's sums are joined over the
+// groups in shared memory.  Where ranges cut a tile, each block leaves its sums
+// in the workspace, and the one that is last adds them in the order of the
+// ranges: a repeated call gives the same bits.
+//
+// The activations become float16 beforehand, and h when the blocks of its 256
+// columns are complete: by the block that completed them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstdint>
+
+#include "../../include/nvfp4few.h"
+#include "few_common.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "mla_common.cuh"
+#include "sm103_ptx.cuh"
+
+namespace nvfp4moe {
+using namespace few;
+namespace {
+
+__device__ unsigned g_stream_flags = 0;
+
+constexpr int kWeightBytes = 128 * 128;         // of a stage
+constexpr int kScaleBytes = 2048;
+constexpr int kTileRows = 128;
+constexpr int kRedStride = kTileRows + 4;       // floats; of one token's sums, without bank conflicts
+constexpr int kMinShare = 4;                    // stages
+
+template <int NB>
+struct Shape {
+  static constexpr int kWarps = NB == 1 ? 16 : 12;              // consumers; three groups leave 150 registers
+  static constexpr int kGroups = kWarps / 4;
+  static constexpr int kStages = NB == 1 ? 7 : (NB == 2 ? 6 : 4);
+  static constexpr int kStageBytes = kWeightBytes + kScaleBytes + 8 * NB * kUnitBytes;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kSmem = kStages * kStageBytes + kGroups * 8 * NB * kRedStride * 4 + 1024;
+};
+
+struct StreamParams {
+  const uint8_t* scales;
+  const float* gscale;       // null: 1
+  const float* next_gscale;  // gate/up: of the down matrices
+  const uint8_t* frag;       // activations as float16: [step][row][kUnitBytes]
+  const float* factor;       // [step][row]
+  int rows;                  // of frag
+  int T, k, N, K, tiled, out_fp16;
+  const int32_t* idx;
+  const float* topk_w;
+  void* out;                 // [T, N], or h [T * k, N / 2] float32
+  uint8_t* h_frag;
+  float* h_factor;
+  const Plan* plan;
+  float* partial;            // [2 * grid][T][128]
+  uint32_t* done;            // blocks that are through with a cut tile
+  uint32_t* done_block;      // tiles of 256 columns of h that are complete
+  uint32_t wait_us;
+};
+
+// Where piece j of a row's step lies in its kUnitBytes: odd rows swap pairs,
+// so that two rows are read without bank conflicts.
+__device__ __forceinline__ int piece_at(int j, int row) { return (j ^ (row & 1)) * 64; }
+
+// ---- activations, counters and plan beforehand ---------------------------------------
+constexpr int kPrepThreads = 256;
+
+template <int SRC>
+__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const void* x, int64_t x_stride, int T, int K, uint8_t* frag,
+                                                               float* factor, uint32_t* counters, int n_counters,
+                                                               const int32_t* idx, int k, int E, Plan* plan) {
+  extern __shared__ uint32_t words[];
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (plan && blockIdx.x == 0) {
+    write_plan<kPrepThreads>(idx, T, k, E, plan, &g_stream_flags, words, reinterpret_cast<int*>(words + E));
+    return;
+  }
+  const int first = plan ? 1 : 0, lane = threadIdx.x & 31;
+  const int block = blockIdx.x - first, blocks = gridDim.x - first;
+  for (int i = block * kPrepThreads + threadIdx.x; i < n_counters; i += blocks * kPrepThreads) counters[i] = 0;
+  const int items = T * ((K + kStep - 1) / kStep);
+  for (int item = block * (kPrepThreads / 32) + (threadIdx.x >> 5); item < items; item += blocks * (kPrepThreads / 32)) {
+    const int step = item / T, t = item - step * T;
+    float v[8];
+    load_block<SRC>(v, static_cast<const uint8_t*>(x) + t * x_stride * 2, step, K, lane);
+    uint4 h;
+    const float f = block_to_half(v, &h);
+    *reinterpret_cast<uint4*>(frag + int64_t(item) * kUnitBytes + piece_at(lane & 7, t) + (lane >> 3) * 16) = h;
+    if (lane == 0) factor[item] = f;
+  }
+}
+
+// ---- the stream ---------------------------------------------------------------------
+template <bool MX, int MODE, int NB>
+__global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __grid_constant__ CUtensorMap map,
+                                                                        const StreamParams p) {
+  using S = Shape<NB>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t s_full[S::kStages], s_empty[S::kStages];
+  __shared__ mla::WaitCtl s_ctl;
+  __shared__ int s_last, s_token[32];
+  __shared__ float s_weight[32];
+  uint8_t* smem = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = mla::uniform(tid >> 5);
+  const uint32_t full = ptx::smem_u32(s_full), empty = ptx::smem_u32(s_empty);
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      ptx::mbar_init(full + 8 * i, 1);
+      ptx::mbar_init(empty + 8 * i, 4);        // the warps of a group
+    }
+    ptx::fence_barrier_init();
+    s_ctl.abort = 0;
+    s_ctl.limit_us = p.wait_us;
+    s_ctl.flags = &g_stream_flags;
+    ptx::prefetch_tmap(&map);
+  }
+  __syncthreads();
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+
+  const int nseg = MODE == kDense ? 1 : p.plan->nseg;
+  if (MODE == kDown && nseg == 0) {            // no token has an expert
+    for (int64_t i = int64_t(blockIdx.x) * S::kThreads + tid; i < int64_t(p.T) * p.N; i += int64_t(gridDim.x) * S::kThreads)
+      static_cast<uint16_t*>(p.out)[i] = 0;
+    return;
+  }
+  const int steps = (p.K + kStep - 1) / kStep, seg_tiles = MODE == kGateUp ? p.N / kTileRows : 1;
+  const int tiles = MODE == kGateUp ? nseg * seg_tiles : p.N / kTileRows;
+  const int length = MODE == kDown ? nseg * steps : steps;             // stages of a tile
+  const int64_t all = int64_t(tiles) * length;
+  const int per = int(max(int64_t(kMinShare), (all + gridDim.x - 1) / gridDim.x));
+  const int64_t start = int64_t(blockIdx.x) * per, end = min(all, start + per);
+  if (start >= end) return;
+
+  if (warp == S::kWarps) {
+    // ---- producer
+    const uint64_t policy = ptx::policy_evict_first(), keep = ptx::policy_evict_normal();
+    const int kc = (p.K + kStep - 1) / kStep, blocks = p.N / 128, kb_all = p.K / (MX ? 128 : 64);
+    constexpr int kPerStep = MX ? 2 : 4;       // scale blocks of a step
+    int tile = int(start / length), at = int(start - int64_t(tile) * length);
+    int issued = 0, st = 0, parity = 1;
+    bool ok = true;
+    for (int64_t s = start; s < end && ok; ++s) {
+      const int seg = MODE == kGateUp ? tile / seg_tiles : (MODE == kDown ? at / steps : 0);
+      const int step = MODE == kDown ? at - seg * steps : at;
+      const int in = MODE == kGateUp ? tile - seg * seg_tiles : tile;  // tile of the matrix
+      const int e = MODE == kDense ? 0 : p.plan->expert[seg];
+      const uint32_t tokens = MODE == kDense ? 0 : p.plan->tokens[seg];
+      const int m = MODE == kDense ? p.T : __popc(tokens);
+      const int nkb = min(kPerStep, kb_all - step * kPerStep);
+      ok = mla::wait_warp(empty + 8 * st, parity, &s_ctl);
+      if (!ok) break;
+      const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem + st * S::kStageBytes);
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, kWeightBytes + nkb * 512 + m * kUnitBytes);
+      __syncwarp();
+      const uint32_t act = dst + kWeightBytes + kScaleBytes;
+      if (MODE == kGateUp) {
+        // gate and up: 16 rows of each 32 of a block of 128
+        const int rb = in >> 1, half = in & 1;
+        if (lane < 8) {
+          const int blk = e * blocks + rb + (lane >> 2) * (blocks / 2), r = 32 * (lane & 3) + 16 * half;
+          ptx::tma_load_2d(dst + lane * 2048, &map, bar, p.tiled ? 0 : step * 128, (p.tiled ? blk * kc + step : blk) * 128 + r,
+                           policy);
+        } else if (lane >= 16 && lane - 16 < 2 * nkb) {
+          const int up = (lane - 16) / nkb, kb = (lane - 16) % nkb;
+          const int64_t blk = int64_t(e) * blocks + rb + up * (blocks / 2);
+          ptx::bulk_load(dst + kWeightBytes + up * 1024 + kb * 256, p.scales + (blk * kb_all + step * kPerStep + kb) * 512 + half * 256,
+                         256, bar, policy);
+        }
+        if ((tokens >> lane) & 1)
+          ptx::bulk_load(act + __popc(tokens & ((1u << lane) - 1)) * kUnitBytes,
+                         p.frag + (int64_t(step) * p.rows + lane) * kUnitBytes, kUnitBytes, bar, keep);
+      } else if (lane == 0) {
+        const int blk = e * blocks + in;
+        ptx::tma_load_2d(dst, &map, bar, p.tiled ? 0 : step * 128, (p.tiled ? blk * kc + step : blk) * 128, policy);
+        ptx::bulk_load(dst + kWeightBytes, p.scales + (int64_t(blk) * kb_all + step * kPerStep) * 512, nkb * 512, bar, policy);
+        ptx::bulk_load(act, p.frag + (int64_t(step) * p.rows + (MODE == kDown ? p.plan->base[seg] : 0)) * kUnitBytes,
+                       m * kUnitBytes, bar, keep);
+      }
+      ++issued;
+      if (++st == S::kStages) st = 0, parity ^= 1;
+      if (++at == length) at = 0, ++tile;
+    }
+    if (!ok)                                   // the block's copies land before it leaves
+      for (int i = max(0, issued - S::kStages); i < issued; ++i)
+        mla::drain_phase(full + 8 * (i % S::kStages), (i / S::kStages) & 1);
+    return;
+  }
+
+  // ---- consumers: warp q of group `group`
+  constexpr int kConsumers = 32 * S::kWarps;
+  const int q = warp & 3, group = warp >> 2, g = lane >> 2, tg = lane & 3;
+  float* red = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
+  // byte offsets within a stage: the lane's rows (g of tile 0) and 16-byte pieces (swizzled), its scales
+  const int row0 = (MODE == kGateUp ? 16 : 32) * q, tile_rows = MODE == kGateUp ? 64 : 16;
+  const int w_at = (row0 + g) * 128, w_lo = ((2 * tg) ^ g) * 16, w_hi = ((2 * tg + 1) ^ g) * 16;
+  const int kb = MX ? tg >> 1 : tg;
+  const int s_at = kWeightBytes + kb * (MODE == kGateUp ? 256 : 512) + g * 16 + q * 4 + (MX ? (tg & 1) * 2 : 0);
+  const int s_tile = MODE == kGateUp ? 1024 : 256;
+
+  int tile = int(start / length), at = int(start - int64_t(tile) * length);
+  int turn = 0, st = 0, parity = 0;
+  float total[2][NB][4];
+
+  for (int64_t s = start; s < end;) {
+    const int64_t tile_start = int64_t(tile) * length;
+    const int stop = int(min(int64_t(length), end - tile_start));     // of this tile
+    uint32_t tokens = p.T == 32 ? kFull : (1u << p.T) - 1;
+    int seg = 0, step = at, base = 0;
+    if (MODE == kGateUp) {
+      seg = tile / seg_tiles;
+      tokens = p.plan->tokens[seg];
+    } else if (MODE == kDown) {
+      seg = at / steps;
+      step = at - seg * steps;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NB * 4; ++i) (&total[0][0][0])[i] = 0.0f;
+
+    for (; at < stop; ++at, ++s) {
+      if (turn == group) {
+        if (MODE == kDown) tokens = p.plan->tokens[seg], base = p.plan->base[seg];
+        // the factors of this lane's columns, for the end
+        float f[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int t = 8 * b + 2 * tg + c;
+            const int row = MODE == kDown ? base + __popc(tokens & ((1u << t) - 1)) : t;
+            f[b][c] = (tokens >> t) & 1 ? p.factor[int64_t(step) * p.rows + row] : 0.0f;
+          }
+        mla::wait_phase(full + 8 * st, parity, &s_ctl);
+        const uint8_t* stage = smem + st * S::kStageBytes;
+        const uint8_t* from[NB];
+        bool has[NB];
+        int swap[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int t = 8 * b + g, slot = __popc(tokens & ((1u << t) - 1));
+          has[b] = (tokens >> t) & 1;
+          swap[b] = (MODE == kDown ? base + slot : t) & 1;
+          from[b] = stage + kWeightBytes + kScaleBytes + slot * kUnitBytes + tg * 16;
+        }
+        const bool inside = step * kStep + tg * 64 < p.K;
+        uint32_t sw[4], ref[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {          // (tile i / 2, rows g or g + 8)
+          const uint8_t* sp = stage + s_at + (i >> 1) * s_tile + (i & 1) * 128;
+          sw[i] = MX ? uint32_t(*reinterpret_cast<const uint16_t*>(sp)) : *reinterpret_cast<const uint32_t*>(sp);
+          if (!inside) sw[i] = 0;
+          if (MX) {
+            uint32_t top = max(sw[i] & 255u, sw[i] >> 8);
+            top = max(top, __shfl_xor_sync(kFull, top, 1));
+            ref[i] = max(top, __shfl_xor_sync(kFull, top, 2));
+          }
+        }
+        float acc[2][NB][4];
+#pragma unroll
+        for (int i = 0; i < 2 * NB * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {          // the lane's two 16-byte pieces of each row
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(stage + w_at + ((i >> 1) * tile_rows + (i & 1) * 8) * 128 + (h ? w_hi : w_lo));
+          uint32_t sc[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (!MX && (j & 1) == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t two = ue4m3x2_to_half(h ? sw[i] >> 16 : sw[i]);
+                sc[i] = __byte_perm(two, two, j ? 0x3232 : 0x1010);
+              }
+            }
+            if (MX && j == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int x = int(h ? sw[i] >> 8 : sw[i] & 255u) - int(ref[i]) + 28;
+                sc[i] = uint32_t(max(x, 0)) * 0x04000400u;   // exponent fields of 2^(scale - reference + 13), or 0
+              }
+            }
+            uint32_t a[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              codes_to_half(j == 0 ? w[i].x : (j == 1 ? w[i].y : (j == 2 ? w[i].z : w[i].w)), a[i]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) a[i][c] = hmul2(a[i][c], sc[i]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              if (NB > 1 && ((tokens >> (8 * b)) & 255u) == 0) continue;
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (has[b]) x = *reinterpret_cast<const uint4*>(from[b] + ((4 * h + j) ^ swap[b]) * 64);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                mma(acc[i][b], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
+                mma(acc[i][b], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty + 8 * st);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if ((tokens >> (8 * b + 2 * tg + c)) & 1) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float v = acc[i >> 1][b][(i & 1) * 2 + c];
+                if (MX) {
+                  const int x = int(ref[i]) - 140;   // 2^(ref - 127 - 13) as two factors of float32's normal range
+                  v = ref[i] == 255 ? __int_as_float(0x7FFFFFFF) : v * exp2i(x >> 1);
+                  total[i >> 1][b][(i & 1) * 2 + c] += v * f[b][c] * exp2i(x - (x >> 1));
+                } else {
+                  total[i >> 1][b][(i & 1) * 2 + c] += v * f[b][c];
+                }
+              }
+            }
+      }
+      if (++turn == S::kGroups) turn = 0;
+      if (++st == S::kStages) st = 0, parity ^= 1;
+      if (++step == steps) step = 0, ++seg;
+    }
+
+    // ---- the tile's sums over the groups
+    if (MODE == kGateUp) {
+      seg = tile / seg_tiles;
+      base = p.plan->base[seg];
+    } else if (MODE == kDown) {
+      tokens = p.T == 32 ? kFull : (1u << p.T) - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = row0 + (i >> 1) * tile_rows + (i & 1) * 8 + g;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          red[(group * 8 * NB + 8 * b + 2 * tg + c) * kRedStride + row] = total[i >> 1][b][(i & 1) * 2 + c];
+    }
+    if (MODE == kGateUp && warp == 0 && ((tokens >> lane) & 1)) s_token[__popc(tokens & ((1u << lane) - 1))] = lane;
+    mla::bar_sync(1, kConsumers);
+    auto joined = [&](int row, int t) {
+      float v = red[t * kRedStride + row];
+#pragma unroll
+      for (int c = 1; c < S::kGroups; ++c) v += red[(c * 8 * NB + t) * kRedStride + row];
+      return v;
+    };
+    const int first = int(tile_start / per), last = int((tile_start + length - 1) / per);
+    const int m = MODE == kGateUp ? __popc(tokens) : p.T;
+    auto slot_of = [&](int block) {            // a block's first range of a cut tile, or its last
+      return p.partial + int64_t(2 * block + (int64_t(block) * per > tile_start ? 0 : 1)) * p.T * kTileRows;
+    };
+    bool mine = first == last;
+    if (!mine) {
+      float* to = slot_of(blockIdx.x);
+      for (int i = tid; i < m * kTileRows; i += kConsumers) {
+        const int row = i % kTileRows, t = MODE == kGateUp ? s_token[i / kTileRows] : i / kTileRows;
+        to[t * kTileRows + row] = joined(row, t);
+      }
+      __threadfence();
+      mla::bar_sync(1, kConsumers);
+      if (tid == 0) {
+        s_last = atomicAdd(p.done + tile, 1u) == uint32_t(last - first);
+        __threadfence();
+      }
+      mla::bar_sync(1, kConsumers);
+      mine = s_last != 0;
+    }
+    if (mine) {
+      auto value = [&](int row, int t) {
+        if (first == last) return joined(row, t);
+        float v = 0.0f;
+        for (int b = first; b <= last; ++b) v += __ldcg(slot_of(b) + t * kTileRows + row);
+        return v;
+      };
+      if (MODE == kGateUp) {
+        const int I = p.N / 2, in = tile - seg * seg_tiles, e = p.plan->expert[seg];
+        for (int i = warp; i < m; i += S::kWarps) {          // the tokens' weights of this expert
+          const int t = s_token[i];
+          float w = lane < p.k && p.idx[t * p.k + lane] == e ? p.topk_w[t * p.k + lane] : 0.0f;
+#pragma unroll
+          for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(kFull, w, d);
+          if (lane == 0) s_weight[i] = w;
+        }
+        mla::bar_sync(1, kConsumers);
+        const float scale = p.gscale ? p.gscale[e] : 1.0f, next = p.next_gscale ? p.next_gscale[e] : 1.0f;
+        float* h = static_cast<float*>(p.out);
+        for (int i = tid; i < 64 * m; i += kConsumers) {
+          const int r = i & 63, slot = i >> 6, t = s_token[slot];
+          const float gate = value(r, t) * scale, up = value(64 + r, t) * scale;
+          const int col = (in >> 1) * 128 + 32 * (r >> 4) + 16 * (in & 1) + (r & 15);
+          h[int64_t(base + slot) * I + col] = gate / (1.0f + expf(-gate)) * up * s_weight[slot] * next;
+        }
+        // the block that completes 256 columns converts them
+        const int block = in >> 2, in_block = min(4, seg_tiles - 4 * block);
+        __threadfence();
+        mla::bar_sync(1, kConsumers);
+        if (tid == 0) {
+          s_last = atomicAdd(p.done_block + seg * ((seg_tiles + 3) / 4) + block, 1u) == uint32_t(in_block - 1);
+          __threadfence();
+        }
+        mla::bar_sync(1, kConsumers);
+        if (s_last) {
+          const int64_t rows = int64_t(p.T) * p.k;
+          for (int i = warp; i < m; i += S::kWarps) {
+            const int row = base + i, c = block * kStep + 8 * lane;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const float4 a = c < I ? __ldcg(reinterpret_cast<const float4*>(h + int64_t(row) * I + c + j))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
+            }
+            uint4 x;
+            const float fac = block_to_half(v, &x);
+            *reinterpret_cast<uint4*>(p.h_frag + (block * rows + row) * kUnitBytes + piece_at(lane & 7, row) + (lane >> 3) * 16) = x;
+            if (lane == 0) p.h_factor[block * rows + row] = fac;
+          }
+        }
+      } else {
+        const float scale = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
+        for (int i = tid; i < p.T * kTileRows; i += kConsumers) {
+          const int row = i % kTileRows, t = i / kTileRows;
+          const float v = value(row, t) * scale;
+          const int64_t o = int64_t(t) * p.N + tile * kTileRows + row;
+          if (MODE == kDense && p.out_fp16)
+            static_cast<__half*>(p.out)[o] = __float2half_rn(v);
+          else
+            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+    mla::bar_sync(1, kConsumers);              // red and the shared words are free again
+    at = 0;
+    ++tile;
+  }
+}
+
+int64_t steps_of(int K) { return (K + kStep - 1) / kStep; }
+int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
+
+// The parts of a workspace.
+struct Layout {
+  int64_t plan, counters, frag, factor, h, h_frag, h_factor, partial, bytes;
+  int n_counters, n_done;
+};
+Layout layout_of(int T, int k, int E, int N, int K, int I) {  // I = 0: one matrix
+  Layout l = {};
+  const int64_t rows = int64_t(T) * k, segs = rows < E ? rows : E;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t a = at;
+    at += round256(bytes);
+    return a;
+  };
+  l.plan = take(I ? sizeof(Plan) : 0);
+  l.n_done = int(I ? segs * (I / 64) : N / kTileRows);
+  l.n_counters = l.n_done + int(I ? segs * ((I / 64 + 3) / 4) + N / kTileRows : 0);
+  l.counters = take(int64_t(l.n_counters) * 4);
+  l.frag = take(T * steps_of(K) * kUnitBytes);
+  l.factor = take(T * steps_of(K) * 4);
+  if (I) {
+    l.h = take(rows * I * 4);
+    l.h_frag = take(rows * steps_of(I) * kUnitBytes);
+    l.h_factor = take(rows * steps_of(I) * 4);
+  }
+  l.partial = take(int64_t(2) * kFewMaxGrid * T * kTileRows * 4);
+  l.bytes = at;
+  return l;
+}
+
+bool weight_map(CUtensorMap* m, const FewMatrix& w, int E, int box_rows) {
+  auto enc = mla::tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t row_bytes = w.tiled ? 128 : w.K / 2;
+  const cuuint64_t dims[2] = {row_bytes, cuuint64_t(E) * w.N * (w.tiled ? steps_of(w.K) : 1)};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, cuuint32_t(box_rows)}, unit[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w.packed), dims, strides, box, unit,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool MX, int MODE, int NB>
+cudaError_t launch_one(const FewMatrix& w, int E, const StreamParams& p, int num_sms, cudaStream_t st) {
+  auto kernel = stream_kernel<MX, MODE, NB>;
+  CUtensorMap map;
+  if (!weight_map(&map, w, E, MODE == kGateUp ? 16 : 128)) return cudaErrorInvalidValue;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NB>::kSmem);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(kernel, dim3(unsigned(num_sms < kFewMaxGrid ? num_sms : kFewMaxGrid)), dim3(Shape<NB>::kThreads),
+                       Shape<NB>::kSmem, st, false, map, p);
+}
+
+template <int MODE>
+cudaError_t launch_stream(const FewMatrix& w, int E, StreamParams p, int num_sms, cudaStream_t st) {
+  p.scales = w.scales, p.gscale = MODE == kDown ? nullptr : w.gscale;
+  p.N = w.N, p.K = w.K, p.tiled = w.tiled;
+  p.wait_us = wait_limit_us();
+  if (p.T <= 8) return w.mx ? launch_one<true, MODE, 1>(w, E, p, num_sms, st) : launch_one<false, MODE, 1>(w, E, p, num_sms, st);
+  if (p.T <= 16) return w.mx ? launch_one<true, MODE, 2>(w, E, p, num_sms, st) : launch_one<false, MODE, 2>(w, E, p, num_sms, st);
+  return w.mx ? launch_one<true, MODE, 4>(w, E, p, num_sms, st) : launch_one<false, MODE, 4>(w, E, p, num_sms, st);
+}
+
+template <int SRC>
+cudaError_t launch_prepare_few(const void* x, int64_t x_stride, int T, int K, uint8_t* ws, const Layout& l, const int32_t* idx,
+                               int k, int E, cudaStream_t st) {
+  const int64_t items = T * steps_of(K);
+  const int64_t warps = kPrepThreads / 32;
+  int64_t blocks = (items + warps - 1) / warps;
+  if (blocks > 304) blocks = 304;
+  return launch_kernel(prepare_kernel<SRC>, dim3(unsigned(blocks + (idx ? 1 : 0))), dim3(kPrepThreads), idx ? size_t(E) * 8 : 0, st,
+                       false, x, x_stride, T, K, ws + l.frag, reinterpret_cast<float*>(ws + l.factor),
+                       reinterpret_cast<uint32_t*>(ws + l.counters), l.n_counters, idx, k, E,
+                       idx ? reinterpret_cast<Plan*>(ws + l.plan) : nullptr);
+}
+
+StreamParams params_of(uint8_t* ws, const Layout& l, int T) {
+  StreamParams p = {};
+  p.T = T, p.rows = T;
+  p.frag = ws + l.frag;
+  p.factor = reinterpret_cast<float*>(ws + l.factor);
+  p.partial = reinterpret_cast<float*>(ws + l.partial);
+  p.done = reinterpret_cast<uint32_t*>(ws + l.counters);
+  return p;
+}
+
+}  // namespace
+
+size_t few_stream_matvec_bytes(int T, int N, int K) { return size_t(layout_of(T, 1, 1, N, K, 0).bytes); }
+size_t few_stream_experts_bytes(int T, int k, int H, int I) { return size_t(layout_of(T, k, kMaxSegs, H, H, I).bytes); }
+
+cudaError_t launch_stream_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
+                                 int num_sms, cudaStream_t st) {
+  const Layout l = layout_of(T, 1, 1, w.N, w.K, 0);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  const cudaError_t err = fp16 ? launch_prepare_few<kFp16>(x, x_stride, T, w.K, at, l, nullptr, 1, 0, st)
+                               : launch_prepare_few<kBf16>(x, x_stride, T, w.K, at, l, nullptr, 1, 0, st);
+  if (err != cudaSuccess) return err;
+  StreamParams p = params_of(at, l, T);
+  p.out = out, p.out_fp16 = fp16;
+  return launch_stream<kDense>(w, 1, p, num_sms, st);
+}
+
+cudaError_t launch_stream_experts(const void* x, int64_t x_stride, const int32_t* idx, const float* topk_w, int T, int k,
+                                  int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, int num_sms,
+                                  cudaStream_t st) {
+  const Layout l = layout_of(T, k, kMaxSegs, d.N, gu.K, d.K);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  cudaError_t err = launch_prepare_few<kBf16>(x, x_stride, T, gu.K, at, l, idx, k, E, st);
+  if (err != cudaSuccess) return err;
+  StreamParams p = params_of(at, l, T);
+  p.k = k, p.idx = idx, p.topk_w = topk_w;
+  p.plan = reinterpret_cast<const Plan*>(at + l.plan);
+  p.next_gscale = d.gscale;
+  p.out = at + l.h;
+  p.h_frag = at + l.h_frag;
+  p.h_factor = reinterpret_cast<float*>(at + l.h_factor);
+  const int blocks = d.K / 64;                // tiles of an expert's h
+  p.done_block = p.done + l.n_done;
+  if ((err = launch_stream<kGateUp>(gu, E, p, num_sms, st)) != cudaSuccess) return err;
+  p.rows = T * k;
+  p.frag = p.h_frag;
+  p.factor = p.h_factor;
+  p.out = out;
+  const int64_t segs = int64_t(T) * k < kMaxSegs ? int64_t(T) * k : kMaxSegs;
+  p.done = p.done_block + segs * ((blocks + 3) / 4);
+  return launch_stream<kDown>(d, E, p, num_sms, st);
+}
+
+cudaError_t stream_flags_address(unsigned** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_stream_flags); }
+
+}  // namespace nvfp4moe

@@ -32,39 +32,22 @@
 #include <cuda_fp16.h>
 
 #include "../../include/nvfp4few.h"
+#include "few_common.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "sm103_ptx.cuh"
 
 namespace nvfp4moe {
+using namespace few;
 namespace {
 
 __device__ unsigned g_few_flags = 0;
 
-constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 256, kWarps = 8;
-constexpr int kStep = 256;                // columns of a matrix in one step of a warp
-constexpr int kUnitBytes = 2 * kStep;     // float16 activations of one token and step
-constexpr int kMaxSegs = 1024;
-
-enum Source { kBf16 = 0, kFp16 = 1, kF32 = 2 };
-enum Mode { kDense = 0, kGateUp = 1, kDown = 2 };
-
-// The experts that a batch hits, in their order: what the down product walks
-// through.  Written by the gate/up kernel.
-struct Plan {
-  int nseg;
-  int pad[63];
-  int expert[kMaxSegs];
-  uint32_t tokens[kMaxSegs];  // bit t: token t is routed to it
-  int base[kMaxSegs];         // first row of h; token t's is base + number of lower tokens
-};
 
 struct FewParams {
   const void* x;             // [T, K] of Source, or h [T * k, K] float32
   int64_t x_stride;
-  const uint8_t* frag;       // activations converted beforehand (not SELF): [row][step][kUnitBytes]
-  const float* factor;       // [row][step]
   int T, k, E;
   const int32_t* idx;        // [T, k]
   const float* topk_w;
@@ -95,34 +78,6 @@ __device__ __forceinline__ void load32(uint32_t (&r)[8], const uint8_t* p, bool 
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
     r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
   }
-}
-
-// The eight codes of a word as float16 pairs (in order).
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t ue4m3x2_to_half(uint32_t two) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
-  return h;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
-
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Where a lane's weights lie: rows g and g + 8 of two tiles, its 32 bytes of a step.
@@ -181,119 +136,8 @@ __device__ __forceinline__ void load_rows(Rows& r, const FewParams& p, const Lan
   }
 }
 
-// Converts 8 values that the lane holds of a block of 256 to float16 as the
-// header says; returns the factor that undoes it.
-__device__ __forceinline__ float block_to_half(const float (&v)[8], uint4* out) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(kFull, top) >> 23;
-  const int e = top == 255 ? 127 : max(int(top) - 127, -112);
-  const float m = exp2i(14 - e);
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 t = __floats2half2_rn(v[2 * i] * m, v[2 * i + 1] * m);
-    h[i] = *reinterpret_cast<const uint32_t*>(&t);
-  }
-  *out = make_uint4(h[0], h[1], h[2], h[3]);
-  return exp2i(e - 14);
-}
-
-// Values 8 lane .. 8 lane + 7 of step `step` of a row of K values (zeros past its end).
-template <int SRC>
-__device__ __forceinline__ void load_block(float (&v)[8], const void* row, int step, int K, int lane) {
-  const int k = step * kStep + 8 * lane;
-  if (k >= K) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    return;
-  }
-  if (SRC == kF32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(row) + k);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    return;
-  }
-  const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (SRC == kBf16) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
-
-// Activations of all rows beforehand: a warp each row and step.
-template <int SRC>
-__global__ void __launch_bounds__(kThreads) convert_kernel(const void* x, int64_t x_stride, int rows, int K,
-                                                           uint8_t* frag, float* factor) {
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
-  const int steps = (K + kStep - 1) / kStep, lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int row = int(item / steps), step = int(item % steps);
-  if (row >= rows) return;
-  float v[8];
-  load_block<SRC>(v, static_cast<const uint8_t*>(x) + row * x_stride * (SRC == kF32 ? 4 : 2), step, K, lane);
-  uint4 h;
-  const float f = block_to_half(v, &h);
-  // piece j of lane group tg of the product at 64 j + 16 tg
-  *reinterpret_cast<uint4*>(frag + item * kUnitBytes + (lane & 7) * 64 + (lane >> 3) * 16) = h;
-  if (lane == 0) factor[item] = f;
-}
-
-// The experts that the batch hits, written by one block.  mask, count: E words
-// of shared memory each.
-__device__ void write_plan(const FewParams& p, uint32_t* mask, int* count) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.T * p.k;
-  __shared__ int sum_warp[2][kWarps];
-  for (int e = tid; e < p.E; e += kThreads) mask[e] = 0, count[e] = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const int e = p.idx[i];
-    if (e >= 0 && e < p.E) {
-      atomicOr(mask + e, 1u << (i / p.k));
-      atomicAdd(count + e, 1);
-    } else {
-      atomicOr(&g_few_flags, kFlagBadData);
-    }
-  }
-  __syncthreads();
-  const int per = (p.E + kThreads - 1) / kThreads, e0 = tid * per;
-  int segs = 0, rows = 0;
-  for (int e = e0; e < min(e0 + per, p.E); ++e) segs += mask[e] != 0, rows += count[e];
-  int a = segs, b = rows;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int ua = __shfl_up_sync(kFull, a, d), ub = __shfl_up_sync(kFull, b, d);
-    if (lane >= d) a += ua, b += ub;
-  }
-  if (lane == 31) sum_warp[0][warp] = a, sum_warp[1][warp] = b;
-  __syncthreads();
-  int seg = a - segs, row = b - rows;
-  for (int w = 0; w < warp; ++w) seg += sum_warp[0][w], row += sum_warp[1][w];
-  for (int e = e0; e < min(e0 + per, p.E); ++e) {
-    if (mask[e]) {
-      p.plan->expert[seg] = e;
-      p.plan->tokens[seg] = mask[e];
-      p.plan->base[seg] = row;
-      ++seg;
-    }
-    row += count[e];
-  }
-  if (tid == kThreads - 1) p.plan->nseg = seg;
-  __syncthreads();
-}
-
-template <bool MX, int SRC, int MODE, int NB, bool SELF>
-__global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const FewParams p) {
+template <bool MX, int SRC, int MODE>
+__global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_or[kWarps];
   __shared__ int s_sum[kWarps], s_first[kWarps];
@@ -309,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const Fe
   uint32_t tokens = p.T == 32 ? kFull : (1u << p.T) - 1;
   if (MODE == kGateUp) {
     if (blockIdx.x == 0 && blockIdx.y == 0)
-      write_plan(p, reinterpret_cast<uint32_t*>(smem), reinterpret_cast<int*>(smem) + p.E);
+      write_plan<kThreads>(p.idx, p.T, p.k, p.E, p.plan, &g_few_flags, reinterpret_cast<uint32_t*>(smem),
+                           reinterpret_cast<int*>(smem) + p.E);
     const int f = blockIdx.y, n = p.T * p.k;
     e = p.idx[f];
     if (e < 0 || e >= p.E) return;             // write_plan raises the flag
@@ -358,31 +203,26 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const Fe
   if (wk < units) load_rows<MX>(cur, p, l, MODE == kDown ? p.plan->expert[seg] : e, step);
 
   // Activations as float16: [step][piece j][token of the expert][16 bytes of 4 lane groups].
-  float* factor = nullptr;
-  if (SELF) {
-    const int rows = MODE == kDown ? p.T * p.k : p.T;   // an upper bound, also of a gate/up block's tokens
-    factor = reinterpret_cast<float*>(smem + int64_t(rows) * steps * kUnitBytes);
-    for (int s = 0; s < nseg; ++s) {
-      const uint32_t who = MODE == kDown ? p.plan->tokens[s] : tokens;
-      const int first = MODE == kDown ? p.plan->base[s] : 0, m = __popc(who);
-      for (int i = warp; i < m * steps; i += kWarps) {
-        const int slot = i / steps, at = i - slot * steps;
-        const int row = MODE == kDown ? first + slot : int(__fns(who, 0, slot + 1));
-        float v[8];
-        load_block<SRC>(v, static_cast<const uint8_t*>(p.x) + row * p.x_stride * (SRC == kF32 ? 4 : 2), at, p.K, lane);
-        uint4 h;
-        const float f = block_to_half(v, &h);
-        uint8_t* dst = smem + (int64_t(first) * steps + int64_t(at) * m) * kUnitBytes;
-        *reinterpret_cast<uint4*>(dst + ((lane & 7) * m + slot) * 64 + (lane >> 3) * 16) = h;
-        if (lane == 0) factor[(first + slot) * steps + at] = f;
-      }
+  const int rows = MODE == kDown ? p.T * p.k : p.T;   // an upper bound, also of a gate/up block's tokens
+  float* factor = reinterpret_cast<float*>(smem + int64_t(rows) * steps * kUnitBytes);
+  for (int s = 0; s < nseg; ++s) {
+    const uint32_t who = MODE == kDown ? p.plan->tokens[s] : tokens;
+    const int first = MODE == kDown ? p.plan->base[s] : 0, m = __popc(who);
+    for (int i = warp; i < m * steps; i += kWarps) {
+      const int slot = i / steps, at = i - slot * steps;
+      const int row = MODE == kDown ? first + slot : int(__fns(who, 0, slot + 1));
+      float v[8];
+      load_block<SRC>(v, static_cast<const uint8_t*>(p.x) + row * p.x_stride * (SRC == kF32 ? 4 : 2), at, p.K, lane);
+      uint4 h;
+      const float f = block_to_half(v, &h);
+      uint8_t* dst = smem + (int64_t(first) * steps + int64_t(at) * m) * kUnitBytes;
+      *reinterpret_cast<uint4*>(dst + ((lane & 7) * m + slot) * 64 + (lane >> 3) * 16) = h;
+      if (lane == 0) factor[(first + slot) * steps + at] = f;
     }
-    __syncthreads();
   }
+  __syncthreads();
 
-  float total[2][NB][4];
-#pragma unroll
-  for (int i = 0; i < 2 * NB * 4; ++i) (&total[0][0][0])[i] = 0.0f;
+  float total[2][4] = {};
   const int g = lane >> 2;
 
   for (int u = wk; u < units; u += p.wk) {
@@ -394,23 +234,10 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const Fe
 
     if (MODE == kDown) tokens = p.plan->tokens[seg], base = p.plan->base[seg];
     const int m = __popc(tokens);
-    // this lane's column of each eight tokens
-    const uint8_t* from[NB];
-    bool has[NB];
-    int stride_j;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int t = 8 * b + g;
-      has[b] = (tokens >> t) & 1;
-      const int slot = __popc(tokens & ((1u << t) - 1));
-      if (SELF) {
-        from[b] = smem + (int64_t(MODE == kDown ? base : 0) * steps + int64_t(step) * m) * kUnitBytes + slot * 64 + l.tg * 16;
-      } else {
-        const int64_t row = MODE == kDown ? base + slot : t;
-        from[b] = p.frag + (row * steps + step) * kUnitBytes + l.tg * 16;
-      }
-    }
-    stride_j = SELF ? m * 64 : 64;
+    // this lane's column: token g
+    const bool has = (tokens >> g) & 1;
+    const uint8_t* from = smem + ((MODE == kDown ? base : 0) * steps + step * m) * kUnitBytes +
+                          __popc(tokens & ((1u << g) - 1)) * 64 + l.tg * 16;
 
     uint32_t ref[4];                    // MX: a row's largest scale of this step
     if (MX) {
@@ -421,9 +248,7 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const Fe
         ref[i] = max(top, __shfl_xor_sync(kFull, top, 2));
       }
     }
-    float acc[2][NB][4];
-#pragma unroll
-    for (int i = 0; i < 2 * NB * 4; ++i) (&acc[0][0][0])[i] = 0.0f;
+    float acc[2][4] = {};
     uint32_t sc[4];                     // the rows' scales of this word as float16 pairs
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -448,39 +273,31 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const Fe
 #pragma unroll
         for (int q = 0; q < 4; ++q) a[i][q] = hmul2(a[i][q], sc[i]);
       }
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (has) x = *reinterpret_cast<const uint4*>(from + j * m * 64);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (NB > 1 && ((tokens >> (8 * b)) & 255u) == 0) continue;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (has[b]) x = *reinterpret_cast<const uint4*>(from[b] + j * stride_j);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mma(acc[i][b], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
-          mma(acc[i][b], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
-        }
+      for (int i = 0; i < 2; ++i) {
+        mma(acc[i], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
+        mma(acc[i], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
       }
     }
     // into the totals, tokens of this expert only
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int c = 0; c < 2; ++c) {
+      const int t = 2 * l.tg + c;
+      if ((tokens >> t) & 1) {
+        const int slot = __popc(tokens & ((1u << t) - 1));
+        const float f = factor[(MODE == kDown ? base + slot : slot) * steps + step];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int t = 8 * b + 2 * l.tg + c;
-        if ((tokens >> t) & 1) {
-          const int slot = __popc(tokens & ((1u << t) - 1));
-          const float f = SELF ? factor[(MODE == kDown ? base + slot : slot) * steps + step]
-                               : p.factor[int64_t(MODE == kDown ? base + slot : t) * steps + step];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = acc[i >> 1][b][(i & 1) * 2 + c];
-            if (MX) {
-              // 2^(ref - 127 - 13) as two factors of float32's normal range
-              const int x = int(ref[i]) - 140;
-              v = ref[i] == 255 ? __int_as_float(0x7FFFFFFF) : v * exp2i(x >> 1);
-              total[i >> 1][b][(i & 1) * 2 + c] += v * f * exp2i(x - (x >> 1));
-            } else {
-              total[i >> 1][b][(i & 1) * 2 + c] += v * f;
-            }
+        for (int i = 0; i < 4; ++i) {
+          float v = acc[i >> 1][(i & 1) * 2 + c];
+          if (MX) {
+            // 2^(ref - 127 - 13) as two factors of float32's normal range
+            const int x = int(ref[i]) - 140;
+            v = ref[i] == 255 ? __int_as_float(0x7FFFFFFF) : v * exp2i(x >> 1);
+            total[i >> 1][(i & 1) * 2 + c] += v * f * exp2i(x - (x >> 1));
+          } else {
+            total[i >> 1][(i & 1) * 2 + c] += v * f;
           }
         }
       }
@@ -490,21 +307,19 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const Fe
     seg = next;
   }
 
-  // Joins the warps along the columns: [warp][tile][token group][row 0..15][8 tokens].
+  // Joins the warps along the columns: [warp][tile][row 0..15][8 tokens].
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float* at = red + ((warp * 2 + i) * NB + b) * 128 + 2 * l.tg;
-      *reinterpret_cast<float2*>(at + g * 8) = make_float2(total[i][b][0], total[i][b][1]);
-      *reinterpret_cast<float2*>(at + (g + 8) * 8) = make_float2(total[i][b][2], total[i][b][3]);
-    }
+  for (int i = 0; i < 2; ++i) {
+    float* at = red + (warp * 2 + i) * 128 + 2 * l.tg;
+    *reinterpret_cast<float2*>(at + g * 8) = make_float2(total[i][0], total[i][1]);
+    *reinterpret_cast<float2*>(at + (g + 8) * 8) = make_float2(total[i][2], total[i][3]);
+  }
   __syncthreads();
   auto joined = [&](int w, int tile, int row, int t) {  // of the warps with rows group w
     float v = 0.0f;
-    for (int c = 0; c < p.wk; ++c) v += red[(((w * p.wk + c) * 2 + tile) * NB + (t >> 3)) * 128 + row * 8 + (t & 7)];
+    for (int c = 0; c < p.wk; ++c) v += red[((w * p.wk + c) * 2 + tile) * 128 + row * 8 + t];
     return v;
   };
   if (MODE == kGateUp) {
@@ -536,46 +351,30 @@ __global__ void __launch_bounds__(kThreads, NB == 1 ? 2 : 1) few_kernel(const Fe
 
 int64_t steps_of(int K) { return (K + kStep - 1) / kStep; }
 int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
-int64_t frag_bytes(int64_t rows, int K) { return round256(rows * steps_of(K) * kUnitBytes) + round256(rows * steps_of(K) * 4); }
+int64_t self_bytes(int64_t rows, int K) { return rows * steps_of(K) * (kUnitBytes + 4); }
 
-// Blocks convert the activations that they need themselves up to this many
-// bytes; above, one kernel does it for all.
+// What this file takes; the rest streams.  Every block holds the activations
+// that it needs, and converts them itself.
 constexpr int64_t kSelfBytes = 64 * 1024;
-bool self_converts(int64_t rows, int K) { return rows * steps_of(K) * (kUnitBytes + 4) <= kSelfBytes; }
+constexpr int kSmallTokens = 8;
+constexpr int64_t kSmallWeights = int64_t(1) << 23;
+bool takes_matvec(int T, int N, int K) { return T <= kSmallTokens && self_bytes(T, K) <= kSelfBytes && int64_t(N) * K <= kSmallWeights; }
+bool takes_experts(int T, int k, int H, int I) {
+  return T <= kSmallTokens && self_bytes(T, H) <= kSelfBytes && self_bytes(int64_t(T) * k, I) <= kSelfBytes &&
+         int64_t(T) * k * 2 * I * H <= kSmallWeights;
+}
 
-template <bool MX, int SRC, int MODE, int NB, bool SELF>
-cudaError_t launch_one(const FewParams& p, dim3 grid, size_t smem, cudaStream_t st) {
-  auto kernel = few_kernel<MX, SRC, MODE, NB, SELF>;
+template <bool MX, int SRC, int MODE>
+cudaError_t launch_few(const FewParams& p, int64_t rows, dim3 grid, cudaStream_t st) {
+  auto kernel = few_kernel<MX, SRC, MODE>;
+  size_t smem = size_t(self_bytes(rows, p.K));
+  if (smem < size_t(kWarps) * 1024) smem = size_t(kWarps) * 1024;
+  if (MODE == kGateUp && smem < size_t(p.E) * 8) smem = size_t(p.E) * 8;
   if (smem > 48 * 1024) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (err != cudaSuccess) return err;
   }
   return launch_kernel(kernel, grid, dim3(kThreads), smem, st, false, p);
-}
-
-template <bool MX, int SRC, int MODE>
-cudaError_t launch_few(const FewParams& p, int64_t rows, bool self, dim3 grid, cudaStream_t st) {
-  const int nb = p.T <= 8 ? 1 : (p.T <= 16 ? 2 : 4);
-  size_t smem = size_t(kWarps) * nb * 1024;
-  if (self) smem = max(smem, size_t(rows * steps_of(p.K) * (kUnitBytes + 4)));
-  if (MODE == kGateUp) smem = max(smem, size_t(p.E) * 8);
-  if (self)
-    return nb == 1   ? launch_one<MX, SRC, MODE, 1, true>(p, grid, smem, st)
-           : nb == 2 ? launch_one<MX, SRC, MODE, 2, true>(p, grid, smem, st)
-                     : launch_one<MX, SRC, MODE, 4, true>(p, grid, smem, st);
-  return nb == 1   ? launch_one<MX, kF32, MODE, 1, false>(p, grid, smem, st)
-         : nb == 2 ? launch_one<MX, kF32, MODE, 2, false>(p, grid, smem, st)
-                   : launch_one<MX, kF32, MODE, 4, false>(p, grid, smem, st);
-}
-
-template <int SRC>
-cudaError_t launch_convert(const void* x, int64_t stride, int64_t rows, int K, uint8_t* frag, FewParams* p, cudaStream_t st) {
-  float* factor = reinterpret_cast<float*>(frag + round256(rows * steps_of(K) * kUnitBytes));
-  p->frag = frag;
-  p->factor = factor;
-  const int64_t blocks = (rows * steps_of(K) + kWarps - 1) / kWarps;
-  return launch_kernel(convert_kernel<SRC>, dim3(unsigned(blocks)), dim3(kThreads), 0, st, false, x, stride, int(rows), K,
-                       frag, factor);
 }
 
 // Warps of a block along the columns.
@@ -593,17 +392,16 @@ void set_matrix(FewParams* p, const FewMatrix& w) {
 
 }  // namespace
 
-size_t few_matvec_workspace_bytes(int T, int K) { return self_converts(T, K) ? 0 : size_t(frag_bytes(T, K)); }
+size_t few_matvec_workspace_bytes(int T, int N, int K) { return takes_matvec(T, N, K) ? 0 : few_stream_matvec_bytes(T, N, K); }
 
 size_t few_experts_workspace_bytes(int T, int k, int H, int I) {
-  int64_t b = round256(sizeof(Plan)) + round256(int64_t(T) * k * I * 4);
-  if (!self_converts(T, H)) b += frag_bytes(T, H);
-  if (!self_converts(int64_t(T) * k, I)) b += frag_bytes(int64_t(T) * k, I);
-  return size_t(b);
+  if (!takes_experts(T, k, H, I)) return few_stream_experts_bytes(T, k, H, I);
+  return size_t(round256(sizeof(Plan)) + int64_t(T) * k * I * 4);
 }
 
 cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
-                              cudaStream_t st) {
+                              int num_sms, cudaStream_t st) {
+  if (!takes_matvec(T, w.N, w.K)) return launch_stream_matvec(x, x_stride, T, fp16, w, out, ws, num_sms, st);
   FewParams p = {};
   p.x = x, p.x_stride = x_stride;
   p.T = T, p.k = 1, p.E = 1;
@@ -611,26 +409,19 @@ cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16,
   p.wk = column_warps(T);
   p.out_fp16 = fp16;
   p.out = out;
-  const bool self = self_converts(T, w.K);
-  if (!self) {
-    const cudaError_t err = fp16 ? launch_convert<kFp16>(x, x_stride, T, w.K, static_cast<uint8_t*>(ws), &p, st)
-                                 : launch_convert<kBf16>(x, x_stride, T, w.K, static_cast<uint8_t*>(ws), &p, st);
-    if (err != cudaSuccess) return err;
-  }
   const dim3 grid(unsigned(w.N / (32 * (kWarps / p.wk))));
-  if (w.mx)
-    return fp16 ? launch_few<true, kFp16, kDense>(p, T, self, grid, st) : launch_few<true, kBf16, kDense>(p, T, self, grid, st);
-  return fp16 ? launch_few<false, kFp16, kDense>(p, T, self, grid, st) : launch_few<false, kBf16, kDense>(p, T, self, grid, st);
+  if (w.mx) return fp16 ? launch_few<true, kFp16, kDense>(p, T, grid, st) : launch_few<true, kBf16, kDense>(p, T, grid, st);
+  return fp16 ? launch_few<false, kFp16, kDense>(p, T, grid, st) : launch_few<false, kBf16, kDense>(p, T, grid, st);
 }
 
 cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* idx, const float* topk_w, int T, int k,
-                               int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, cudaStream_t st) {
-  uint8_t* at = static_cast<uint8_t*>(ws);
+                               int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, int num_sms,
+                               cudaStream_t st) {
+  if (!takes_experts(T, k, gu.K, d.K))
+    return launch_stream_experts(x, x_stride, idx, topk_w, T, k, E, gu, d, out, ws, num_sms, st);
   FewParams p = {};
-  p.plan = reinterpret_cast<Plan*>(at);
-  at += round256(sizeof(Plan));
-  float* h = reinterpret_cast<float*>(at);
-  at += round256(int64_t(T) * k * d.K * 4);
+  p.plan = static_cast<Plan*>(ws);
+  float* h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(sizeof(Plan)));
   p.x = x, p.x_stride = x_stride;
   p.T = T, p.k = k, p.E = E;
   p.idx = idx, p.topk_w = topk_w;
@@ -638,25 +429,17 @@ cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* i
   p.next_gscale = d.gscale;
   p.out = h;
   p.wk = 8;
-  bool self = self_converts(T, gu.K);
-  cudaError_t err;
-  if (!self) {
-    if ((err = launch_convert<kBf16>(x, x_stride, T, gu.K, at, &p, st)) != cudaSuccess) return err;
-    at += frag_bytes(T, gu.K);
-  }
   dim3 grid(unsigned(d.K / (16 * (kWarps / p.wk))), unsigned(T * k));
-  err = gu.mx ? launch_few<true, kBf16, kGateUp>(p, T, self, grid, st) : launch_few<false, kBf16, kGateUp>(p, T, self, grid, st);
+  const cudaError_t err = gu.mx ? launch_few<true, kBf16, kGateUp>(p, T, grid, st) : launch_few<false, kBf16, kGateUp>(p, T, grid, st);
   if (err != cudaSuccess) return err;
 
-  const int64_t rows = int64_t(T) * k;
   set_matrix(&p, d);
   p.gscale = p.next_gscale = nullptr;     // in h already
   p.x = h, p.x_stride = d.K;
   p.out = out;
-  self = self_converts(rows, d.K);
-  if (!self && (err = launch_convert<kF32>(h, d.K, rows, d.K, at, &p, st)) != cudaSuccess) return err;
   grid = dim3(unsigned(d.N / (32 * (kWarps / p.wk))));
-  return d.mx ? launch_few<true, kF32, kDown>(p, rows, self, grid, st) : launch_few<false, kF32, kDown>(p, rows, self, grid, st);
+  return d.mx ? launch_few<true, kF32, kDown>(p, int64_t(T) * k, grid, st)
+              : launch_few<false, kF32, kDown>(p, int64_t(T) * k, grid, st);
 }
 
 cudaError_t few_flags_address(unsigned** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_few_flags); }

@@ -158,15 +158,26 @@ struct FewMatrix {
   int N, K;
   bool mx, tiled;
 };
-size_t few_matvec_workspace_bytes(int T, int K);
+constexpr int kFewMaxGrid = 160;
+size_t few_matvec_workspace_bytes(int T, int N, int K);
 size_t few_experts_workspace_bytes(int T, int k, int H, int I);
 // x [T, K] 16-bit, rows x_stride elements apart; out [T, N]; 1 <= T <= 32.
 cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
-                              cudaStream_t st);
+                              int num_sms, cudaStream_t st);
 // gu: [E, 2I, H], d: [E, H, I].
 cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* idx, const float* topk_w, int T, int k,
-                               int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, cudaStream_t st);
+                               int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, int num_sms,
+                               cudaStream_t st);
 cudaError_t few_flags_address(unsigned** at);
+// The same as one stream over all SMs (few_stream.cu), for what few_tokens.cu does not take itself.
+size_t few_stream_matvec_bytes(int T, int N, int K);
+size_t few_stream_experts_bytes(int T, int k, int H, int I);
+cudaError_t launch_stream_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
+                                 int num_sms, cudaStream_t st);
+cudaError_t launch_stream_experts(const void* x, int64_t x_stride, const int32_t* idx, const float* topk_w, int T, int k,
+                                  int E, const FewMatrix& gu, const FewMatrix& d, void* out, void* ws, int num_sms,
+                                  cudaStream_t st);
+cudaError_t stream_flags_address(unsigned** at);
 
 // ---- latent attention (mla_*.cu) --------------------------------------------
 struct MlaAppendArgs {

@@ -145,8 +145,8 @@ def test_python_checks_come_before_the_call(B, M):
 
 
 def test_workspace_sizes(B):
-    assert B.moe_matvec_workspace_size(1, 1024) == 0 and B.moe_matvec_workspace_size(33, 1024) == 0
-    assert B.moe_matvec_workspace_size(32, 8192) >= 32 * 8192 * 2
+    assert B.moe_matvec_workspace_size(1, 128, 1024) == 0 and B.moe_matvec_workspace_size(33, 128, 1024) == 0
+    assert B.moe_matvec_workspace_size(32, 128, 8192) >= 32 * 8192 * 2
     assert B.moe_experts_workspace_size(1, 8, 6144, 2048) >= 8 * 2048 * 4
     assert B.moe_experts_workspace_size(32, 33, 6144, 2048) == 0
 

@@ -72,7 +72,7 @@ def test_matvec_views(B, T):
     want = matvec(B, "nvfp4", x.contiguous(), w)
     assert torch.equal(matvec(B, "nvfp4", x, w), want)
     out = torch.full_like(want, float("nan"))
-    ws = torch.empty(max(256, B.moe_matvec_workspace_size(T, K)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(256, B.moe_matvec_workspace_size(T, N, K)), dtype=torch.uint8, device="cuda")
     assert matvec(B, "nvfp4", x, w, out=out, workspace=ws) is out and torch.equal(out, want)
     same = x[:1].expand(T, K)
     assert torch.equal(matvec(B, "nvfp4", same, w), matvec(B, "nvfp4", same.contiguous(), w))

@@ -45,17 +45,16 @@ struct Shape {
   static constexpr int kStages = NB == 1 ? 7 : (NB == 2 ? 6 : 4);
   static constexpr int kStageBytes = kWeightBytes + kScaleBytes + 8 * NB * kUnitBytes;
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kSmem = kStages * kStageBytes + kGroups * 8 * NB * kRedStride * 4 + 1024;
+  static constexpr int kSmem = kStages * kStageBytes + kUnitBytes + kGroups * 8 * NB * kRedStride * 4 + 1024;
 };
 
 struct StreamParams {
-  const uint8_t* scales;
   const float* gscale;       // null: 1
   const float* next_gscale;  // gate/up: of the down matrices
   const uint8_t* frag;       // activations as float16: [step][row][kUnitBytes]
   const float* factor;       // [step][row]
   int rows;                  // of frag
-  int T, k, N, K, tiled, out_fp16;
+  int T, k, E, N, K, tiled, out_fp16;
   const int32_t* idx;
   const float* topk_w;
   void* out;                 // [T, N], or h [T * k, N / 2] float32
@@ -102,18 +101,44 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const void* x, in
 }
 
 // ---- the stream ---------------------------------------------------------------------
+// The experts of at most 32 ids, in ascending order, by one warp: their number,
+// and (unless null) the list.  What the plan says, without waiting for it.
+__device__ __forceinline__ int experts_of_warp(const int32_t* idx, int n, int E, int lane, int* list) {
+  const int e = lane < n ? __ldcg(idx + lane) : -1;
+  const uint32_t same = __match_any_sync(kFull, e);
+  const bool first = e >= 0 && e < E && __ffs(same) - 1 == lane;
+  const uint32_t leaders = __ballot_sync(kFull, first);
+  if (list) {
+    int at = 0;
+    for (int i = 0; i < n; ++i) {
+      const int other = __shfl_sync(kFull, e, i);
+      at += ((leaders >> i) & 1) && other < e;
+    }
+    if (first) list[at] = e;
+    __syncwarp();
+  }
+  return __popc(leaders);
+}
+
+// Adds bytes that the current phase of a barrier waits for.
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 template <bool MX, int MODE, int NB>
-__global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __grid_constant__ CUtensorMap map,
+__global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __grid_constant__ CUtensorMap weights,
+                                                                        const __grid_constant__ CUtensorMap scales,
                                                                         const StreamParams p) {
   using S = Shape<NB>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t s_full[S::kStages], s_empty[S::kStages];
   __shared__ mla::WaitCtl s_ctl;
-  __shared__ int s_last, s_token[32];
+  __shared__ int s_last, s_token[32], s_expert[32];
   __shared__ float s_weight[32];
   uint8_t* smem = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = mla::uniform(tid >> 5);
   const uint32_t full = ptx::smem_u32(s_full), empty = ptx::smem_u32(s_empty);
+  uint8_t* zeros = smem + S::kStages * S::kStageBytes;   // a step of a token that is not there
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
@@ -123,14 +148,27 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
     s_ctl.abort = 0;
     s_ctl.limit_us = p.wait_us;
     s_ctl.flags = &g_stream_flags;
-    ptx::prefetch_tmap(&map);
+    ptx::prefetch_tmap(&weights);
+    ptx::prefetch_tmap(&scales);
   }
+  if (tid < kUnitBytes / 4) reinterpret_cast<uint32_t*>(zeros)[tid] = 0;
   __syncthreads();
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
 
-  const int nseg = MODE == kDense ? 1 : p.plan->nseg;
+  // The kernel before is one of the same call: prepare_kernel, or before the
+  // down product the gate/up one.  Both let the next be launched after their own wait, so what
+  // was there before the call (weights, ids), and for the down product the
+  // plan, can be read before this kernel's wait (from L2).
+  const bool producer = warp == S::kWarps;
+  const bool early = MODE != kGateUp || p.T * p.k <= 32;   // the experts are known before the wait
+  if (!producer || !early) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+  }
+  const int nseg = MODE == kDense ? 1
+                   : MODE == kGateUp && early ? experts_of_warp(p.idx, p.T * p.k, p.E, lane, producer ? s_expert : nullptr)
+                                              : __ldcg(&p.plan->nseg);
   if (MODE == kDown && nseg == 0) {            // no token has an expert
+    ptx::grid_dep_wait();
     for (int64_t i = int64_t(blockIdx.x) * S::kThreads + tid; i < int64_t(p.T) * p.N; i += int64_t(gridDim.x) * S::kThreads)
       static_cast<uint16_t*>(p.out)[i] = 0;
     return;
@@ -143,65 +181,93 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
   const int64_t start = int64_t(blockIdx.x) * per, end = min(all, start + per);
   if (start >= end) return;
 
-  if (warp == S::kWarps) {
-    // ---- producer
+  if (producer) {
+    if (lane != 0) return;
     const uint64_t policy = ptx::policy_evict_first(), keep = ptx::policy_evict_normal();
-    const int kc = (p.K + kStep - 1) / kStep, blocks = p.N / 128, kb_all = p.K / (MX ? 128 : 64);
+    const int blocks = p.N / 128, kb_all = p.K / (MX ? 128 : 64);
     constexpr int kPerStep = MX ? 2 : 4;       // scale blocks of a step
-    int tile = int(start / length), at = int(start - int64_t(tile) * length);
-    int issued = 0, st = 0, parity = 1;
-    bool ok = true;
-    for (int64_t s = start; s < end && ok; ++s) {
-      const int seg = MODE == kGateUp ? tile / seg_tiles : (MODE == kDown ? at / steps : 0);
-      const int step = MODE == kDown ? at - seg * steps : at;
-      const int in = MODE == kGateUp ? tile - seg * seg_tiles : tile;  // tile of the matrix
-      const int e = MODE == kDense ? 0 : p.plan->expert[seg];
-      const uint32_t tokens = MODE == kDense ? 0 : p.plan->tokens[seg];
-      const int m = MODE == kDense ? p.T : __popc(tokens);
-      const int nkb = min(kPerStep, kb_all - step * kPerStep);
-      ok = mla::wait_warp(empty + 8 * st, parity, &s_ctl);
-      if (!ok) break;
+    struct Place {                             // of a stage: its tile, of an expert's matrix, and step
+      int tile, seg, in, step;
+    };
+    auto place_of = [&](int64_t s) {
+      Place w;
+      w.tile = int(s / length);
+      const int at = int(s - int64_t(w.tile) * length);
+      w.seg = MODE == kGateUp ? w.tile / seg_tiles : (MODE == kDown ? at / steps : 0);
+      w.in = MODE == kGateUp ? w.tile - w.seg * seg_tiles : w.tile;
+      w.step = MODE == kDown ? at - w.seg * steps : at;
+      return w;
+    };
+    auto advance = [&](Place& w) {
+      if (++w.step < steps) return;
+      w.step = 0;
+      if (MODE == kDown && ++w.seg < nseg) return;
+      if (MODE == kDown) w.seg = 0;
+      ++w.tile, ++w.in;
+      if (MODE == kGateUp && w.in == seg_tiles) w.in = 0, ++w.seg;
+    };
+    auto load_weights = [&](const Place& w, int st) {
+      const int e = MODE == kDense ? 0 : MODE == kGateUp && early ? s_expert[w.seg] : __ldcg(p.plan->expert + w.seg);
       const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem + st * S::kStageBytes);
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, kWeightBytes + nkb * 512 + m * kUnitBytes);
-      __syncwarp();
-      const uint32_t act = dst + kWeightBytes + kScaleBytes;
-      if (MODE == kGateUp) {
-        // gate and up: 16 rows of each 32 of a block of 128
-        const int rb = in >> 1, half = in & 1;
-        if (lane < 8) {
-          const int blk = e * blocks + rb + (lane >> 2) * (blocks / 2), r = 32 * (lane & 3) + 16 * half;
-          ptx::tma_load_2d(dst + lane * 2048, &map, bar, p.tiled ? 0 : step * 128, (p.tiled ? blk * kc + step : blk) * 128 + r,
-                           policy);
-        } else if (lane >= 16 && lane - 16 < 2 * nkb) {
-          const int up = (lane - 16) / nkb, kb = (lane - 16) % nkb;
-          const int64_t blk = int64_t(e) * blocks + rb + up * (blocks / 2);
-          ptx::bulk_load(dst + kWeightBytes + up * 1024 + kb * 256, p.scales + (blk * kb_all + step * kPerStep + kb) * 512 + half * 256,
-                         256, bar, policy);
+      expect_tx(bar, kWeightBytes + kPerStep * 512);
+      if (MODE == kGateUp) {                   // 16 rows of each 32 of a block of 128, of gate and of up
+        const int half = w.in & 1;
+#pragma unroll
+        for (int up = 0; up < 2; ++up) {
+          const int blk = e * blocks + (w.in >> 1) + up * (blocks / 2);
+          ptx::tma_load_3d(dst + up * (kWeightBytes / 2), &weights, bar, p.tiled ? 0 : w.step * 128, 16 * half,
+                           (p.tiled ? blk * steps + w.step : blk) * 4, policy);
+          ptx::tma_load_2d(dst + kWeightBytes + up * 1024, &scales, bar, 64 * half, blk * kb_all + w.step * kPerStep, policy);
         }
-        if ((tokens >> lane) & 1)
-          ptx::bulk_load(act + __popc(tokens & ((1u << lane) - 1)) * kUnitBytes,
-                         p.frag + (int64_t(step) * p.rows + lane) * kUnitBytes, kUnitBytes, bar, keep);
-      } else if (lane == 0) {
-        const int blk = e * blocks + in;
-        ptx::tma_load_2d(dst, &map, bar, p.tiled ? 0 : step * 128, (p.tiled ? blk * kc + step : blk) * 128, policy);
-        ptx::bulk_load(dst + kWeightBytes, p.scales + (int64_t(blk) * kb_all + step * kPerStep) * 512, nkb * 512, bar, policy);
-        ptx::bulk_load(act, p.frag + (int64_t(step) * p.rows + (MODE == kDown ? p.plan->base[seg] : 0)) * kUnitBytes,
-                       m * kUnitBytes, bar, keep);
+      } else {
+        const int blk = e * blocks + w.in;
+        ptx::tma_load_2d(dst, &weights, bar, p.tiled ? 0 : w.step * 128, (p.tiled ? blk * steps + w.step : blk) * 128, policy);
+        ptx::tma_load_2d(dst + kWeightBytes, &scales, bar, 0, blk * kb_all + w.step * kPerStep, policy);
       }
-      ++issued;
-      if (++st == S::kStages) st = 0, parity ^= 1;
-      if (++at == length) at = 0, ++tile;
+    };
+    auto load_activations = [&](const Place& w, int st) {
+      const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem + st * S::kStageBytes) + kWeightBytes + kScaleBytes;
+      const uint8_t* from = p.frag + int64_t(w.step) * p.rows * kUnitBytes;
+      uint32_t tokens = MODE == kDense ? 0 : p.plan->tokens[w.seg];
+      const int m = MODE == kDense ? p.T : __popc(tokens);
+      ptx::mbar_arrive_expect_tx(bar, m * kUnitBytes);
+      if (MODE == kGateUp && m < p.T) {
+        for (int slot = 0; slot < m; ++slot) {
+          ptx::bulk_load(dst + slot * kUnitBytes, from + (__ffs(tokens) - 1) * kUnitBytes, kUnitBytes, bar, keep);
+          tokens &= tokens - 1;
+        }
+      } else {
+        ptx::bulk_load(dst, from + (MODE == kDown ? p.plan->base[w.seg] : 0) * kUnitBytes, m * kUnitBytes, bar, keep);
+      }
+    };
+    Place w = place_of(start), b = w;
+    const int n = int(end - start), ahead = n < S::kStages ? n : S::kStages;
+    for (int i = 0; i < ahead; ++i) {
+      load_weights(w, i);
+      advance(w);
     }
-    if (!ok)                                   // the block's copies land before it leaves
-      for (int i = max(0, issued - S::kStages); i < issued; ++i)
-        mla::drain_phase(full + 8 * (i % S::kStages), (i / S::kStages) & 1);
+    ptx::grid_dep_wait();
+    for (int i = 0; i < ahead; ++i) {
+      load_activations(b, i);
+      advance(b);
+    }
+    int i = ahead, st = 0, parity = 0;
+    for (; i < n; ++i) {
+      if (!mla::wait_phase(empty + 8 * st, parity, &s_ctl)) break;
+      load_weights(w, st);
+      load_activations(w, st);
+      advance(w);
+      if (++st == S::kStages) st = 0, parity ^= 1;
+    }
+    if (i < n)                                 // given up: the block's copies land before it leaves
+      for (int j = max(0, i - S::kStages); j < i; ++j) mla::drain_phase(full + 8 * (j % S::kStages), (j / S::kStages) & 1);
     return;
   }
 
   // ---- consumers: warp q of group `group`
   constexpr int kConsumers = 32 * S::kWarps;
   const int q = warp & 3, group = warp >> 2, g = lane >> 2, tg = lane & 3;
-  float* red = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
+  float* red = reinterpret_cast<float*>(zeros + kUnitBytes);
   // byte offsets within a stage: the lane's rows (g of tile 0) and 16-byte pieces (swizzled), its scales
   const int row0 = (MODE == kGateUp ? 16 : 32) * q, tile_rows = MODE == kGateUp ? 64 : 16;
   const int w_at = (row0 + g) * 128, w_lo = ((2 * tg) ^ g) * 16, w_hi = ((2 * tg + 1) ^ g) * 16;
@@ -243,15 +309,15 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
           }
         mla::wait_phase(full + 8 * st, parity, &s_ctl);
         const uint8_t* stage = smem + st * S::kStageBytes;
-        const uint8_t* from[NB];
-        bool has[NB];
-        int swap[NB];
+        // where the lane's token of each eight lies: pieces 2i and 2i + 1 (piece_at)
+        const uint8_t *even[NB], *odd[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const int t = 8 * b + g, slot = __popc(tokens & ((1u << t) - 1));
-          has[b] = (tokens >> t) & 1;
-          swap[b] = (MODE == kDown ? base + slot : t) & 1;
-          from[b] = stage + kWeightBytes + kScaleBytes + slot * kUnitBytes + tg * 16;
+          const int swap = ((MODE == kDown ? base + slot : t) & 1) * 64;
+          const uint8_t* from = ((tokens >> t) & 1 ? stage + kWeightBytes + kScaleBytes + slot * kUnitBytes : zeros) + tg * 16;
+          even[b] = from + swap;
+          odd[b] = from + (64 - swap);
         }
         const bool inside = step * kStep + tg * 64 < p.K;
         uint32_t sw[4], ref[4];
@@ -302,8 +368,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               if (NB > 1 && ((tokens >> (8 * b)) & 255u) == 0) continue;
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (has[b]) x = *reinterpret_cast<const uint4*>(from[b] + ((4 * h + j) ^ swap[b]) * 64);
+              const uint4 x = *reinterpret_cast<const uint4*>((j & 1 ? odd[b] : even[b]) + (4 * h + (j & 2)) * 64);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 mma(acc[i][b], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
@@ -485,37 +550,46 @@ Layout layout_of(int T, int k, int E, int N, int K, int I) {  // I = 0: one matr
   return l;
 }
 
-bool weight_map(CUtensorMap* m, const FewMatrix& w, int E, int box_rows) {
+// The weights of all experts: boxes of 128 rows x 128 bytes (zeros past K/2)
+// or, for the gated product, of 16 rows of each 32 of them; and the scales'
+// blocks of 512 bytes, or their halves.
+bool weight_maps(CUtensorMap* weights, CUtensorMap* scales, const FewMatrix& w, int E, bool gate_up) {
   auto enc = mla::tensor_map_encoder();
   if (!enc) return false;
-  const cuuint64_t row_bytes = w.tiled ? 128 : w.K / 2;
-  const cuuint64_t dims[2] = {row_bytes, cuuint64_t(E) * w.N * (w.tiled ? steps_of(w.K) : 1)};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {128, cuuint32_t(box_rows)}, unit[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w.packed), dims, strides, box, unit,
+  const cuuint64_t row = w.tiled ? 128 : w.K / 2, rows = cuuint64_t(E) * w.N * (w.tiled ? steps_of(w.K) : 1);
+  const cuuint64_t dims[3] = {row, gate_up ? 32 : rows, rows / 32}, strides[2] = {row, 32 * row};
+  const cuuint32_t box[3] = {128, cuuint32_t(gate_up ? 16 : 128), 4}, unit[3] = {1, 1, 1};
+  const int per_step = w.mx ? 2 : 4;
+  const cuuint64_t s_dims[2] = {128, cuuint64_t(E) * (w.N / 128) * (w.K / (w.mx ? 128 : 64))}, s_strides[1] = {512};
+  const cuuint32_t s_box[2] = {cuuint32_t(gate_up ? 64 : 128), cuuint32_t(per_step)};
+  return enc(weights, CU_TENSOR_MAP_DATA_TYPE_UINT8, gate_up ? 3 : 2, const_cast<uint8_t*>(w.packed), dims, strides, box, unit,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         enc(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(w.scales), s_dims, s_strides, s_box, unit,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool MX, int MODE, int NB>
-cudaError_t launch_one(const FewMatrix& w, int E, const StreamParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_one(const FewMatrix& w, const StreamParams& p, int num_sms, cudaStream_t st) {
   auto kernel = stream_kernel<MX, MODE, NB>;
-  CUtensorMap map;
-  if (!weight_map(&map, w, E, MODE == kGateUp ? 16 : 128)) return cudaErrorInvalidValue;
+  CUtensorMap weights, scales;
+  if (!weight_maps(&weights, &scales, w, p.E, MODE == kGateUp)) return cudaErrorInvalidValue;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NB>::kSmem);
   if (err != cudaSuccess) return err;
   return launch_kernel(kernel, dim3(unsigned(num_sms < kFewMaxGrid ? num_sms : kFewMaxGrid)), dim3(Shape<NB>::kThreads),
-                       Shape<NB>::kSmem, st, false, map, p);
+                       Shape<NB>::kSmem, st, false, weights, scales, p);
 }
 
 template <int MODE>
 cudaError_t launch_stream(const FewMatrix& w, int E, StreamParams p, int num_sms, cudaStream_t st) {
-  p.scales = w.scales, p.gscale = MODE == kDown ? nullptr : w.gscale;
+  p.E = E;
+  p.gscale = MODE == kDown ? nullptr : w.gscale;
   p.N = w.N, p.K = w.K, p.tiled = w.tiled;
   p.wait_us = wait_limit_us();
-  if (p.T <= 8) return w.mx ? launch_one<true, MODE, 1>(w, E, p, num_sms, st) : launch_one<false, MODE, 1>(w, E, p, num_sms, st);
-  if (p.T <= 16) return w.mx ? launch_one<true, MODE, 2>(w, E, p, num_sms, st) : launch_one<false, MODE, 2>(w, E, p, num_sms, st);
-  return w.mx ? launch_one<true, MODE, 4>(w, E, p, num_sms, st) : launch_one<false, MODE, 4>(w, E, p, num_sms, st);
+  if (p.T <= 8) return w.mx ? launch_one<true, MODE, 1>(w, p, num_sms, st) : launch_one<false, MODE, 1>(w, p, num_sms, st);
+  if (p.T <= 16) return w.mx ? launch_one<true, MODE, 2>(w, p, num_sms, st) : launch_one<false, MODE, 2>(w, p, num_sms, st);
+  return w.mx ? launch_one<true, MODE, 4>(w, p, num_sms, st) : launch_one<false, MODE, 4>(w, p, num_sms, st);
 }
 
 template <int SRC>

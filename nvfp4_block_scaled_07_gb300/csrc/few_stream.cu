@@ -37,15 +37,21 @@ constexpr int kScaleBytes = 2048;
 constexpr int kTileRows = 128;
 constexpr int kRedStride = kTileRows + 4;       // floats; of one token's sums, without bank conflicts
 constexpr int kMinShare = 4;                    // stages
+constexpr int kJoinWarps = 3;
 
 template <int NB>
 struct Shape {
-  static constexpr int kWarps = NB == 1 ? 16 : 12;              // consumers; three groups leave 150 registers
+  static constexpr int kWarps = NB == 1 ? 16 : 12;              // consumers; with 16 warps in all, 128 registers each
   static constexpr int kGroups = kWarps / 4;
-  static constexpr int kStages = NB == 1 ? 7 : (NB == 2 ? 6 : 4);
+  // A multiple of the groups, so that a slot of the ring is always the same
+  // group's: with another number a group could come to a slot whose previous
+  // stage, another group's, has not landed yet, and take that phase of its barrier for its own.
+  static constexpr int kStages = NB == 1 ? 8 : 6;
+  static constexpr int kProducer = kWarps, kJoiner = kWarps + 1;  // first warps of the other roles
   static constexpr int kStageBytes = kWeightBytes + kScaleBytes + 8 * NB * kUnitBytes;
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kSmem = kStages * kStageBytes + kUnitBytes + kGroups * 8 * NB * kRedStride * 4 + 1024;
+  static constexpr int kThreads = 32 * (kWarps + 1 + kJoinWarps);
+  static constexpr int kSmem = kStages * kStageBytes + kUnitBytes + 8 * NB * kRedStride * 4 + 1024;
+  static_assert(kStages % kGroups == 0 && kSmem <= 227 * 1024);
 };
 
 struct StreamParams {
@@ -132,18 +138,23 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
   using S = Shape<NB>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t s_full[S::kStages], s_empty[S::kStages];
+  __shared__ __align__(8) uint64_t s_red[S::kGroups + 1];
   __shared__ mla::WaitCtl s_ctl;
   __shared__ int s_last, s_token[32], s_expert[32];
   __shared__ float s_weight[32];
   uint8_t* smem = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = mla::uniform(tid >> 5);
   const uint32_t full = ptx::smem_u32(s_full), empty = ptx::smem_u32(s_empty);
+  // a tile's sums: barrier 0 opens them to the first group, each group opens them to the next, the last to the joiners
+  const uint32_t red_bar = ptx::smem_u32(s_red);
   uint8_t* zeros = smem + S::kStages * S::kStageBytes;   // a step of a token that is not there
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
       ptx::mbar_init(empty + 8 * i, 4);        // the warps of a group
     }
+    ptx::mbar_init(red_bar, kJoinWarps);
+    for (int i = 1; i <= S::kGroups; ++i) ptx::mbar_init(red_bar + 8 * i, 4);
     ptx::fence_barrier_init();
     s_ctl.abort = 0;
     s_ctl.limit_us = p.wait_us;
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
   // down product the gate/up one.  Both let the next be launched after their own wait, so what
   // was there before the call (weights, ids), and for the down product the
   // plan, can be read before this kernel's wait (from L2).
-  const bool producer = warp == S::kWarps;
+  const bool producer = warp == S::kProducer;
   const bool early = MODE != kGateUp || p.T * p.k <= 32;   // the experts are known before the wait
   if (!producer || !early) {
     ptx::grid_dep_wait();
@@ -264,10 +275,121 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
     return;
   }
 
+  float* red = reinterpret_cast<float*>(zeros + kUnitBytes);   // a tile's sums: [token][row]
+
+  if (warp >= S::kJoiner) {
+    // ---- joiners: sums over the groups and the blocks, results
+    constexpr int kThreads = 32 * kJoinWarps;
+    const int id = tid - 32 * S::kJoiner, my_warp = warp - S::kJoiner;
+    int parity = 0;
+    for (int tile = int(start / length); int64_t(tile) * length < end; ++tile, parity ^= 1) {
+      const int64_t tile_start = int64_t(tile) * length;
+      const int seg = MODE == kGateUp ? tile / seg_tiles : 0;
+      const uint32_t tokens = MODE == kGateUp ? p.plan->tokens[seg] : 0;
+      const int m = MODE == kGateUp ? __popc(tokens) : p.T;
+      auto token_of = [&](int slot) { return MODE == kGateUp ? s_token[slot] : slot; };
+      if (MODE == kGateUp) {
+        const int e = p.plan->expert[seg];
+        if (my_warp == 0 && ((tokens >> lane) & 1)) s_token[__popc(tokens & ((1u << lane) - 1))] = lane;
+        mla::bar_sync(1, kThreads);
+        for (int i = my_warp; i < m; i += kJoinWarps) {      // the tokens' weights of this expert
+          const int t = s_token[i];
+          float w = lane < p.k && p.idx[t * p.k + lane] == e ? p.topk_w[t * p.k + lane] : 0.0f;
+#pragma unroll
+          for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(kFull, w, d);
+          if (lane == 0) s_weight[i] = w;
+        }
+        mla::bar_sync(1, kThreads);
+      }
+      mla::wait_phase(red_bar + 8 * S::kGroups, parity, &s_ctl);
+      auto joined = [&](int row, int t) { return red[t * kRedStride + row]; };
+      auto release = [&] {                     // the consumers may write the next tile's sums
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(red_bar);
+      };
+      const int first = int(tile_start / per), last = int((tile_start + length - 1) / per);
+      const bool whole = first == last;
+      auto slot_of = [&](int block) {          // a block's first range of a cut tile, or its last
+        return p.partial + int64_t(2 * block + (int64_t(block) * per > tile_start ? 0 : 1)) * p.T * kTileRows;
+      };
+      if (!whole) {
+        float* to = slot_of(blockIdx.x);
+        for (int i = id; i < m * kTileRows; i += kThreads) {
+          const int row = i % kTileRows, t = token_of(i / kTileRows);
+          to[t * kTileRows + row] = joined(row, t);
+        }
+        release();
+        __threadfence();
+        mla::bar_sync(1, kThreads);
+        if (id == 0) {
+          s_last = atomicAdd(p.done + tile, 1u) == uint32_t(last - first);
+          __threadfence();
+        }
+        mla::bar_sync(1, kThreads);
+        if (!s_last) continue;
+      }
+      auto value = [&](int row, int t) {
+        if (whole) return joined(row, t);
+        float v = 0.0f;
+        for (int b = first; b <= last; ++b) v += __ldcg(slot_of(b) + t * kTileRows + row);
+        return v;
+      };
+      if (MODE == kGateUp) {
+        const int I = p.N / 2, in = tile - seg * seg_tiles, e = p.plan->expert[seg], base = p.plan->base[seg];
+        const float scale = p.gscale ? p.gscale[e] : 1.0f, next = p.next_gscale ? p.next_gscale[e] : 1.0f;
+        float* h = static_cast<float*>(p.out);
+        for (int i = id; i < 64 * m; i += kThreads) {
+          const int r = i & 63, slot = i >> 6, t = s_token[slot];
+          const float gate = value(r, t) * scale, up = value(64 + r, t) * scale;
+          const int col = (in >> 1) * 128 + 32 * (r >> 4) + 16 * (in & 1) + (r & 15);
+          h[int64_t(base + slot) * I + col] = gate / (1.0f + expf(-gate)) * up * s_weight[slot] * next;
+        }
+        if (whole) release();
+        // the block that completes 256 columns converts them
+        const int block = in >> 2, in_block = min(4, seg_tiles - 4 * block);
+        __threadfence();
+        mla::bar_sync(1, kThreads);
+        if (id == 0) {
+          s_last = atomicAdd(p.done_block + seg * ((seg_tiles + 3) / 4) + block, 1u) == uint32_t(in_block - 1);
+          __threadfence();
+        }
+        mla::bar_sync(1, kThreads);
+        if (s_last) {
+          const int64_t rows = int64_t(p.T) * p.k;
+          for (int i = my_warp; i < m; i += kJoinWarps) {
+            const int row = base + i, c = block * kStep + 8 * lane;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const float4 a = c < I ? __ldcg(reinterpret_cast<const float4*>(h + int64_t(row) * I + c + j))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
+            }
+            uint4 x;
+            const float fac = block_to_half(v, &x);
+            *reinterpret_cast<uint4*>(p.h_frag + (block * rows + row) * kUnitBytes + piece_at(lane & 7, row) + (lane >> 3) * 16) = x;
+            if (lane == 0) p.h_factor[block * rows + row] = fac;
+          }
+        }
+      } else {
+        const float scale = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
+        for (int i = id; i < p.T * kTileRows; i += kThreads) {
+          const int row = i % kTileRows, t = i / kTileRows;
+          const float v = value(row, t) * scale;
+          const int64_t o = int64_t(t) * p.N + tile * kTileRows + row;
+          if (MODE == kDense && p.out_fp16)
+            static_cast<__half*>(p.out)[o] = __float2half_rn(v);
+          else
+            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+        }
+        if (whole) release();
+      }
+    }
+    return;
+  }
+
   // ---- consumers: warp q of group `group`
-  constexpr int kConsumers = 32 * S::kWarps;
   const int q = warp & 3, group = warp >> 2, g = lane >> 2, tg = lane & 3;
-  float* red = reinterpret_cast<float*>(zeros + kUnitBytes);
   // byte offsets within a stage: the lane's rows (g of tile 0) and 16-byte pieces (swizzled), its scales
   const int row0 = (MODE == kGateUp ? 16 : 32) * q, tile_rows = MODE == kGateUp ? 64 : 16;
   const int w_at = (row0 + g) * 128, w_lo = ((2 * tg) ^ g) * 16, w_hi = ((2 * tg + 1) ^ g) * 16;
@@ -276,7 +398,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
   const int s_tile = MODE == kGateUp ? 1024 : 256;
 
   int tile = int(start / length), at = int(start - int64_t(tile) * length);
-  int turn = 0, st = 0, parity = 0;
+  int turn = 0, st = 0, parity = 0, red_parity = 1;
   float total[2][NB][4];
 
   for (int64_t s = start; s < end;) {
@@ -308,6 +430,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
             f[b][c] = (tokens >> t) & 1 ? p.factor[int64_t(step) * p.rows + row] : 0.0f;
           }
         mla::wait_phase(full + 8 * st, parity, &s_ctl);
+        __syncwarp();
         const uint8_t* stage = smem + st * S::kStageBytes;
         // where the lane's token of each eight lies: pieces 2i and 2i + 1 (piece_at)
         const uint8_t *even[NB], *odd[NB];
@@ -402,116 +525,23 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
       if (++step == steps) step = 0, ++seg;
     }
 
-    // ---- the tile's sums over the groups
-    if (MODE == kGateUp) {
-      seg = tile / seg_tiles;
-      base = p.plan->base[seg];
-    } else if (MODE == kDown) {
-      tokens = p.T == 32 ? kFull : (1u << p.T) - 1;
-    }
+    // ---- the tile's sums: a group after the other, so in a fixed order
+    mla::wait_phase(red_bar + 8 * group, red_parity ^ (group ? 1 : 0), &s_ctl);
+    red_parity ^= 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = row0 + (i >> 1) * tile_rows + (i & 1) * 8 + g;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          red[(group * 8 * NB + 8 * b + 2 * tg + c) * kRedStride + row] = total[i >> 1][b][(i & 1) * 2 + c];
+        for (int c = 0; c < 2; ++c) {
+          float* to = red + (8 * b + 2 * tg + c) * kRedStride + row;
+          const float v = total[i >> 1][b][(i & 1) * 2 + c];
+          *to = group ? *to + v : v;
+        }
     }
-    if (MODE == kGateUp && warp == 0 && ((tokens >> lane) & 1)) s_token[__popc(tokens & ((1u << lane) - 1))] = lane;
-    mla::bar_sync(1, kConsumers);
-    auto joined = [&](int row, int t) {
-      float v = red[t * kRedStride + row];
-#pragma unroll
-      for (int c = 1; c < S::kGroups; ++c) v += red[(c * 8 * NB + t) * kRedStride + row];
-      return v;
-    };
-    const int first = int(tile_start / per), last = int((tile_start + length - 1) / per);
-    const int m = MODE == kGateUp ? __popc(tokens) : p.T;
-    auto slot_of = [&](int block) {            // a block's first range of a cut tile, or its last
-      return p.partial + int64_t(2 * block + (int64_t(block) * per > tile_start ? 0 : 1)) * p.T * kTileRows;
-    };
-    bool mine = first == last;
-    if (!mine) {
-      float* to = slot_of(blockIdx.x);
-      for (int i = tid; i < m * kTileRows; i += kConsumers) {
-        const int row = i % kTileRows, t = MODE == kGateUp ? s_token[i / kTileRows] : i / kTileRows;
-        to[t * kTileRows + row] = joined(row, t);
-      }
-      __threadfence();
-      mla::bar_sync(1, kConsumers);
-      if (tid == 0) {
-        s_last = atomicAdd(p.done + tile, 1u) == uint32_t(last - first);
-        __threadfence();
-      }
-      mla::bar_sync(1, kConsumers);
-      mine = s_last != 0;
-    }
-    if (mine) {
-      auto value = [&](int row, int t) {
-        if (first == last) return joined(row, t);
-        float v = 0.0f;
-        for (int b = first; b <= last; ++b) v += __ldcg(slot_of(b) + t * kTileRows + row);
-        return v;
-      };
-      if (MODE == kGateUp) {
-        const int I = p.N / 2, in = tile - seg * seg_tiles, e = p.plan->expert[seg];
-        for (int i = warp; i < m; i += S::kWarps) {          // the tokens' weights of this expert
-          const int t = s_token[i];
-          float w = lane < p.k && p.idx[t * p.k + lane] == e ? p.topk_w[t * p.k + lane] : 0.0f;
-#pragma unroll
-          for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(kFull, w, d);
-          if (lane == 0) s_weight[i] = w;
-        }
-        mla::bar_sync(1, kConsumers);
-        const float scale = p.gscale ? p.gscale[e] : 1.0f, next = p.next_gscale ? p.next_gscale[e] : 1.0f;
-        float* h = static_cast<float*>(p.out);
-        for (int i = tid; i < 64 * m; i += kConsumers) {
-          const int r = i & 63, slot = i >> 6, t = s_token[slot];
-          const float gate = value(r, t) * scale, up = value(64 + r, t) * scale;
-          const int col = (in >> 1) * 128 + 32 * (r >> 4) + 16 * (in & 1) + (r & 15);
-          h[int64_t(base + slot) * I + col] = gate / (1.0f + expf(-gate)) * up * s_weight[slot] * next;
-        }
-        // the block that completes 256 columns converts them
-        const int block = in >> 2, in_block = min(4, seg_tiles - 4 * block);
-        __threadfence();
-        mla::bar_sync(1, kConsumers);
-        if (tid == 0) {
-          s_last = atomicAdd(p.done_block + seg * ((seg_tiles + 3) / 4) + block, 1u) == uint32_t(in_block - 1);
-          __threadfence();
-        }
-        mla::bar_sync(1, kConsumers);
-        if (s_last) {
-          const int64_t rows = int64_t(p.T) * p.k;
-          for (int i = warp; i < m; i += S::kWarps) {
-            const int row = base + i, c = block * kStep + 8 * lane;
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const float4 a = c < I ? __ldcg(reinterpret_cast<const float4*>(h + int64_t(row) * I + c + j))
-                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
-            }
-            uint4 x;
-            const float fac = block_to_half(v, &x);
-            *reinterpret_cast<uint4*>(p.h_frag + (block * rows + row) * kUnitBytes + piece_at(lane & 7, row) + (lane >> 3) * 16) = x;
-            if (lane == 0) p.h_factor[block * rows + row] = fac;
-          }
-        }
-      } else {
-        const float scale = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
-        for (int i = tid; i < p.T * kTileRows; i += kConsumers) {
-          const int row = i % kTileRows, t = i / kTileRows;
-          const float v = value(row, t) * scale;
-          const int64_t o = int64_t(t) * p.N + tile * kTileRows + row;
-          if (MODE == kDense && p.out_fp16)
-            static_cast<__half*>(p.out)[o] = __float2half_rn(v);
-          else
-            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
-        }
-      }
-    }
-    mla::bar_sync(1, kConsumers);              // red and the shared words are free again
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(red_bar + 8 * (group + 1));
     at = 0;
     ++tile;
   }

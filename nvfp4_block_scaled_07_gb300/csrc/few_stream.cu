@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
         mla::bar_sync(1, kThreads);
       }
       mla::wait_phase(red_bar + 8 * S::kGroups, parity, &s_ctl);
-      auto joined = [&](int row, int t) { return red[t * kRedStride + row]; };
+      auto joined = [&](int row, int t) { return *reinterpret_cast<const float4*>(red + t * kRedStride + row); };
       auto release = [&] {                     // the consumers may write the next tile's sums
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(red_bar);
@@ -314,9 +314,9 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
       };
       if (!whole) {
         float* to = slot_of(blockIdx.x);
-        for (int i = id; i < m * kTileRows; i += kThreads) {
-          const int row = i % kTileRows, t = token_of(i / kTileRows);
-          to[t * kTileRows + row] = joined(row, t);
+        for (int i = id; i < m * (kTileRows / 4); i += kThreads) {
+          const int row = 4 * (i % (kTileRows / 4)), t = token_of(i / (kTileRows / 4));
+          *reinterpret_cast<float4*>(to + t * kTileRows + row) = joined(row, t);
         }
         release();
         __threadfence();
@@ -328,21 +328,31 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
         mla::bar_sync(1, kThreads);
         if (!s_last) continue;
       }
-      auto value = [&](int row, int t) {
+      auto value = [&](int row, int t) {       // four rows
         if (whole) return joined(row, t);
-        float v = 0.0f;
-        for (int b = first; b <= last; ++b) v += __ldcg(slot_of(b) + t * kTileRows + row);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int b = first; b <= last; ++b) {
+          const float4 a = __ldcg(reinterpret_cast<const float4*>(slot_of(b) + t * kTileRows + row));
+          v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+        }
         return v;
       };
       if (MODE == kGateUp) {
         const int I = p.N / 2, in = tile - seg * seg_tiles, e = p.plan->expert[seg], base = p.plan->base[seg];
         const float scale = p.gscale ? p.gscale[e] : 1.0f, next = p.next_gscale ? p.next_gscale[e] : 1.0f;
         float* h = static_cast<float*>(p.out);
-        for (int i = id; i < 64 * m; i += kThreads) {
-          const int r = i & 63, slot = i >> 6, t = s_token[slot];
-          const float gate = value(r, t) * scale, up = value(64 + r, t) * scale;
+        for (int i = id; i < 16 * m; i += kThreads) {
+          const int r = 4 * (i & 15), slot = i >> 4, t = s_token[slot];
+          const float4 gate = value(r, t), up = value(64 + r, t);
+          const float w = s_weight[slot] * next;
+          auto gated = [&](float a, float b) {
+            a *= scale;
+            return a / (1.0f + expf(-a)) * (b * scale) * w;
+          };
           const int col = (in >> 1) * 128 + 32 * (r >> 4) + 16 * (in & 1) + (r & 15);
-          h[int64_t(base + slot) * I + col] = gate / (1.0f + expf(-gate)) * up * s_weight[slot] * next;
+          *reinterpret_cast<float4*>(h + int64_t(base + slot) * I + col) =
+              make_float4(gated(gate.x, up.x), gated(gate.y, up.y), gated(gate.z, up.z), gated(gate.w, up.w));
         }
         if (whole) release();
         // the block that completes 256 columns converts them
@@ -373,14 +383,19 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
         }
       } else {
         const float scale = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
-        for (int i = id; i < p.T * kTileRows; i += kThreads) {
-          const int row = i % kTileRows, t = i / kTileRows;
-          const float v = value(row, t) * scale;
-          const int64_t o = int64_t(t) * p.N + tile * kTileRows + row;
-          if (MODE == kDense && p.out_fp16)
-            static_cast<__half*>(p.out)[o] = __float2half_rn(v);
-          else
-            static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
+        for (int i = id; i < p.T * (kTileRows / 4); i += kThreads) {
+          const int row = 4 * (i % (kTileRows / 4)), t = i / (kTileRows / 4);
+          const float4 v = value(row, t);
+          uint2 r;
+          if (MODE == kDense && p.out_fp16) {
+            const __half2 lo = __floats2half2_rn(v.x * scale, v.y * scale), hi = __floats2half2_rn(v.z * scale, v.w * scale);
+            r = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * scale, v.y * scale),
+                                 hi = __floats2bfloat162_rn(v.z * scale, v.w * scale);
+            r = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + int64_t(t) * p.N + tile * kTileRows + row) = r;
         }
         if (whole) release();
       }

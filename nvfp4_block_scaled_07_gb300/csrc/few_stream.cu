@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
     constexpr int kPerStep = MX ? 2 : 4;       // scale blocks of a step
     struct Place {                             // of a stage: its tile, of an expert's matrix, and step
       int tile, seg, in, step;
+      int known, expert, base;                 // the expert's entries in the plan, read when it changes
+      uint32_t tokens;
     };
     auto place_of = [&](int64_t s) {
       Place w;
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
       w.seg = MODE == kGateUp ? w.tile / seg_tiles : (MODE == kDown ? at / steps : 0);
       w.in = MODE == kGateUp ? w.tile - w.seg * seg_tiles : w.tile;
       w.step = MODE == kDown ? at - w.seg * steps : at;
+      w.known = -1;
       return w;
     };
     auto advance = [&](Place& w) {
@@ -217,8 +220,14 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
       ++w.tile, ++w.in;
       if (MODE == kGateUp && w.in == seg_tiles) w.in = 0, ++w.seg;
     };
-    auto load_weights = [&](const Place& w, int st) {
-      const int e = MODE == kDense ? 0 : MODE == kGateUp && early ? s_expert[w.seg] : __ldcg(p.plan->expert + w.seg);
+    auto load_weights = [&](Place& w, int st) {
+      if (MODE != kDense && w.seg != w.known) {
+        w.known = w.seg;
+        w.expert = MODE == kGateUp && early ? s_expert[w.seg] : __ldcg(p.plan->expert + w.seg);
+        w.tokens = MODE == kGateUp && early ? 0 : __ldcg(p.plan->tokens + w.seg);
+        w.base = MODE == kGateUp && early ? 0 : __ldcg(p.plan->base + w.seg);
+      }
+      const int e = MODE == kDense ? 0 : w.expert;
       const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem + st * S::kStageBytes);
       expect_tx(bar, kWeightBytes + kPerStep * 512);
       if (MODE == kGateUp) {                   // 16 rows of each 32 of a block of 128, of gate and of up
@@ -236,10 +245,19 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
         ptx::tma_load_2d(dst + kWeightBytes, &scales, bar, 0, blk * kb_all + w.step * kPerStep, policy);
       }
     };
+    int seen = -1;                             // the expert whose tokens these are
+    uint32_t who = 0;
+    int base = 0;
     auto load_activations = [&](const Place& w, int st) {
+      if (MODE != kDense && w.seg != seen) {
+        seen = w.seg;
+        const bool have = w.known == w.seg && !(MODE == kGateUp && early);
+        who = have ? w.tokens : p.plan->tokens[w.seg];
+        base = have ? w.base : p.plan->base[w.seg];
+      }
       const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem + st * S::kStageBytes) + kWeightBytes + kScaleBytes;
       const uint8_t* from = p.frag + int64_t(w.step) * p.rows * kUnitBytes;
-      uint32_t tokens = MODE == kDense ? 0 : p.plan->tokens[w.seg];
+      uint32_t tokens = who;
       const int m = MODE == kDense ? p.T : __popc(tokens);
       ptx::mbar_arrive_expect_tx(bar, m * kUnitBytes);
       if (MODE == kGateUp && m < p.T) {
@@ -248,7 +266,7 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
           tokens &= tokens - 1;
         }
       } else {
-        ptx::bulk_load(dst, from + (MODE == kDown ? p.plan->base[w.seg] : 0) * kUnitBytes, m * kUnitBytes, bar, keep);
+        ptx::bulk_load(dst, from + (MODE == kDown ? base : 0) * kUnitBytes, m * kUnitBytes, bar, keep);
       }
     };
     Place w = place_of(start), b = w;
@@ -415,12 +433,14 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
   int tile = int(start / length), at = int(start - int64_t(tile) * length);
   int turn = 0, st = 0, parity = 0, red_parity = 1;
   float total[2][NB][4];
+  int seen = -1, base = 0;                     // down: the expert whose plan entries these are
+  uint32_t mine = 0;
 
   for (int64_t s = start; s < end;) {
     const int64_t tile_start = int64_t(tile) * length;
     const int stop = int(min(int64_t(length), end - tile_start));     // of this tile
     uint32_t tokens = p.T == 32 ? kFull : (1u << p.T) - 1;
-    int seg = 0, step = at, base = 0;
+    int seg = 0, step = at;
     if (MODE == kGateUp) {
       seg = tile / seg_tiles;
       tokens = p.plan->tokens[seg];
@@ -433,7 +453,8 @@ __global__ void __launch_bounds__(Shape<NB>::kThreads, 1) stream_kernel(const __
 
     for (; at < stop; ++at, ++s) {
       if (turn == group) {
-        if (MODE == kDown) tokens = p.plan->tokens[seg], base = p.plan->base[seg];
+        if (MODE == kDown && seg != seen) seen = seg, mine = p.plan->tokens[seg], base = p.plan->base[seg];
+        if (MODE == kDown) tokens = mine;
         // the factors of this lane's columns, for the end
         float f[NB][2];
 #pragma unroll

@@ -2,8 +2,9 @@
 
 Bounds, element by element, with u = eps / 2 of the 16-bit result type:
   sums     float32 sums of n products: n 2^-23 sum |x w| (2^-23 and not 2^-24: the tensor core may truncate);
-  x, MX    what the exponents shared by 256 values lose: 2^-38 of the block's largest |x| times sum |w| (each value of
-           256 is off by at most 2^-40 of that), and of MX scales 2^-27 of the row's largest, times 6 sum |x|;
+  x        the stream kernel's eight 4-bit terms: each leaves at most 0.1875 (0.2 with E8M0 scales) of the largest value
+           of its 16 (32), 0.2^8 < 2^-18 of it; and 2^-34 of the row's largest where a block's scale leaves ue4m3's
+           normal numbers.  The other kernel's float16 with an exponent for 256 values: 2^-40 of their largest;
   result   one rounding, u |y|.
 The experts' h carries the errors of gate and up (a silu's slope is below 1.1), the exponential's 2^-21 and its own
 rounding to 11 bits, 2^-11 |h|; each goes through |W_d| and the token's weight.
@@ -46,13 +47,14 @@ class Matrices:
         return self.scales.view(E, N // 128, 4, 32, S // 4, 4).permute(0, 1, 4, 3, 2, 5).reshape(E, -1).contiguous()
 
 
-def product(x, w, block=256):
+def product(x, w, block=32):
     """x [T, K] and w [N, K] float64: (y, the kernel's error before its rounding)."""
     K = x.shape[1]
     size = x.abs() @ w.abs().T
     pad = torch.nn.functional.pad(x.abs(), (0, -K % block)).view(x.shape[0], -1, block).amax(2)
     wsum = torch.nn.functional.pad(w.abs(), (0, -K % block)).view(w.shape[0], -1, block).sum(2)
-    return x @ w.T, K * 2.0 ** -23 * size + 2.0 ** -38 * pad @ wsum.T
+    rows = x.abs().amax(1, keepdim=True) * 2.0 ** -34
+    return x @ w.T, K * 2.0 ** -23 * size + (2.0 ** -18 * pad + rows) @ wsum.T
 
 
 def experts(x, idx, topk_w, gu, d, dtype=torch.bfloat16):

@@ -109,6 +109,23 @@ def test_matvec_keeps_infinities_and_nan_in_their_rows(B):
     assert torch.equal(z[1].cpu() == float("inf"), column > 0) and torch.equal(z[1].cpu() == -float("inf"), column < 0)
 
 
+@pytest.mark.parametrize("T", [9, 20])
+def test_matvec_stream_of_special_rows(B, T):
+    """An infinity, a NaN, zeros, tiny and huge rows among others: each row's results are its own."""
+    m = R.Matrices(1, 256, 1536, "nvfp4", seed=6)
+    w = on_gpu(B, m, False)
+    x = normal(T, 1536, seed=5).cuda()
+    y = matvec(B, "nvfp4", x, w)
+    x[1, 300], x[3, 7] = float("inf"), float("nan")
+    x[4] = 0.0
+    x[5] *= 2.0 ** -60
+    x[6] *= 2.0 ** 90
+    z = matvec(B, "nvfp4", x, w)
+    same = [t for t in range(T) if t not in (1, 3, 4, 5, 6)]
+    assert torch.equal(z[same], y[same]) and not z[[1, 3]].isfinite().any() and (z[4] == 0).all()
+    assert torch.equal(z[5].double(), y[5].double() * 2.0 ** -60) and torch.equal(z[6].double(), y[6].double() * 2.0 ** 90)
+
+
 def test_matvec_of_zeros(B):
     m = R.Matrices(1, 128, 512, "nvfp4", seed=6)
     assert (matvec(B, "nvfp4", torch.zeros(4, 512, dtype=torch.bfloat16, device="cuda"), on_gpu(B, m, False)) == 0).all()
@@ -119,15 +136,16 @@ def test_matvec_of_zeros(B):
 
 @pytest.mark.parametrize("fmt,lo,hi", [("nvfp4", 0, 0x10), ("nvfp4", 0, 0x7F), ("nvfp4", 0x78, 0x7F), ("mxfp4", 1, 20),
                                        ("mxfp4", 220, 240), ("mxfp4", 100, 127), ("mxfp4", 127, 150)])
-def test_matvec_takes_the_scales_range(B, fmt, lo, hi):
+@pytest.mark.parametrize("T", [6, 11, 20])
+def test_matvec_takes_the_scales_range(B, fmt, lo, hi, T):
     """Subnormal and the largest ue4m3 scales, small and large E8M0 ones, up to 2^26 apart in a row."""
     m = R.Matrices(1, 128, 1280, fmt, seed=lo, lo=lo, hi=hi)
     if fmt == "mxfp4" and hi > 200:
-        x = normal(6, 1280, seed=9).float() * 2.0 ** -110
+        x = normal(T, 1280, seed=9).float() * 2.0 ** -110
     elif fmt == "mxfp4" and hi < 50:
-        x = normal(6, 1280, seed=9).float() * 2.0 ** 110
+        x = normal(T, 1280, seed=9).float() * 2.0 ** 110
     else:
-        x = normal(6, 1280, seed=9).float()
+        x = normal(T, 1280, seed=9).float()
     x = x.to(torch.bfloat16)
     y = matvec(B, fmt, x.cuda(), on_gpu(B, m, True))
     ref, tol = R.product(x.double(), m.values(0))
@@ -234,7 +252,7 @@ def test_experts_do_not_reach_tokens_that_are_not_theirs(B):
     """A NaN scale of an expert, an infinite token: only what is routed to them sees them."""
     gu, d = layer(6, 256, 128, "nvfp4", seed=3)
     x = normal(12, 256, seed=3)
-    idx, w = routing(12, 6, 2, seed=9)
+    idx, w = routing(12, 6, 2, seed=9)           # more than eight tokens: the stream kernel
     want = experts(B, "nvfp4", x.cuda(), idx.cuda(), w.cuda(), on_gpu(B, gu, False), on_gpu(B, d, False))
     gu.scales[2, 5, 3] = 0x7F
     d.scales[4, 7, 2] = 0x7F

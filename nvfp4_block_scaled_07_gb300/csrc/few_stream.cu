@@ -50,15 +50,15 @@ __device__ unsigned g_stream_flags = 0;
 
 constexpr int kTerms = 8;
 constexpr int kCodeBytes = kTerms * kStep / 2;  // of a token and step: 8 rows of 128 bytes, swizzled as TMA would
-constexpr int kTermScales = 128;                // their scales: [64 columns][term][4 bytes]
+constexpr int kTermScales = 128;                // their scales: [term][64 columns][4 bytes]
 constexpr int kWeightBytes = 128 * 128;         // of a stage
 constexpr int kScaleBytes = 2048;
 constexpr int kTileRows = 128;
 constexpr int kMinShare = 4;                    // stages
 constexpr int kMaxStages = 8;
 constexpr int kJoinWarps = 4;
-// warps: producer, MMA, four that move scales, joiners
-constexpr int kMmaWarp = 1, kScaleWarp = 2, kJoiner = 6, kThreads = 32 * (kJoiner + kJoinWarps);
+// warps: producers of weights and of terms, MMA, four that move scales, joiners
+constexpr int kTermWarp = 1, kMmaWarp = 2, kScaleWarp = 3, kJoiner = 7, kThreads = 32 * (kJoiner + kJoinWarps);
 // tensor memory: accumulators in columns 0 .. 255, then the stages' scales
 constexpr int kTmemCols = 512, kScaleCol = 256;
 constexpr int kSmemLimit = 227 * 1024;
@@ -107,7 +107,7 @@ __device__ __forceinline__ void write_terms(float (&v)[8], float s0, int lane, u
       step = exp2i(x);
       inv = exp2i(-x);
       const uint32_t next = __shfl_down_sync(kFull, sb, 4);
-      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + (lane >> 3) * 32 + r * 4) = sb | next << 8;
+      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + r * 16 + (lane >> 3) * 4) = sb | next << 8;
     } else {
       const float s = s0 * (1.0f / float(1 << shift_of(r)));
       const float t = top * (1.0f / 6.0f) / s; // s a power of two: exact
@@ -115,7 +115,7 @@ __device__ __forceinline__ void write_terms(float (&v)[8], float s0, int lane, u
       if (ue4m3_to_f32(sb) < t && sb < 0x7E) ++sb;
       step = ue4m3_to_f32(sb) * s;
       inv = sb ? 1.0f / step : 0.0f;
-      if ((lane & 1) == 0) scales[(lane >> 3) * 32 + r * 4 + ((lane >> 1) & 3)] = uint8_t(sb);
+      if ((lane & 1) == 0) scales[r * 16 + (lane >> 1)] = uint8_t(sb);
     }
     uint32_t word = 0;
 #pragma unroll
@@ -202,19 +202,59 @@ __device__ __forceinline__ int experts_of_warp(const int32_t* idx, int n, int E,
   return __popc(leaders);
 }
 
-// Adds bytes that the current phase of a barrier waits for.
-__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-// 4-D tensor copy (strips of gate and up rows).
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1, int32_t c2,
-                                            int32_t c3, uint64_t policy) {
+// Copies and MMAs issued by the elected lane of a converged warp (mla::elect_one).
+__device__ __forceinline__ void tma_2d(uint32_t elected, uint32_t dst, const void* map, uint32_t bar, int c0, int c1,
+                                       uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy), "r"(elected)
       : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t elected, uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2,
+                                       uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t elected, uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2,
+                                       int c3, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %8, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t elected, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "r"(elected)
+      : "memory");
+}
+// a, b: low words of the operands' descriptors (mla::desc_sw128)
+template <bool MX>
+__device__ __forceinline__ void mma_fp4(uint32_t elected, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+  if (MX)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %8};\n\tmov.b64 y, {%2, %8};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], x, y, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected), "n"(mla::desc_hi(1024))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %8};\n\tmov.b64 y, {%2, %8};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], x, y, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected), "n"(mla::desc_hi(1024))
+        : "memory");
 }
 
 // A run of stages that share an accumulator: a tile's, of the down product one
@@ -241,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   const uint32_t acc_full = ptx::smem_u32(s_acc), acc_empty = acc_full + 8 * kBuffers, drained = acc_empty + 8 * kBuffers;
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      ptx::mbar_init(full + 8 * i, 1);
+      ptx::mbar_init(full + 8 * i, 2);         // weights, terms
       ptx::mbar_init(ready + 8 * i, 4);        // the scale warps
       ptx::mbar_init(empty + 8 * i, 1);
     }
@@ -285,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   const int per = int(max(int64_t(kMinShare), (all + gridDim.x - 1) / gridDim.x));
   const int64_t start = int64_t(blockIdx.x) * per, end = min(all, start + per);
   const int blocks = p.N / 128, k_blocks = p.K / 64;
+  const int terms_at = (p.stage_bytes - kWeightBytes - kScaleBytes) / (kCodeBytes + kTermScales) * kCodeBytes;  // their scales
   // the units of this block's range, in order
   auto unit_at = [&](int64_t s) {
     Unit u;
@@ -303,117 +344,112 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       for (int64_t i = int64_t(blockIdx.x) * kOthers + tid - 32; i < int64_t(p.T) * p.N; i += int64_t(gridDim.x) * kOthers)
         static_cast<uint16_t*>(p.out)[i] = 0;
   } else if (warp == 0) {
-    // ---- producer
-    if (lane == 0 && start < end) {
-      const uint64_t policy = ptx::policy_evict_first(), keep = ptx::policy_evict_normal();
-      const int kb_all = p.K / (MX ? 128 : 64);
-      constexpr int kPerStep = MX ? 2 : 4;     // scale blocks of a step
-      auto load_weights = [&](const Unit& u, int step, int e, int st) {
-        const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem + st * p.stage_bytes);
-        const int in = MODE == kGateUp ? u.tile - u.seg * seg_tiles : u.tile;
-        expect_tx(bar, kWeightBytes + kPerStep * 512);
+    // ---- weights and their scales, the first stages before the wait
+    const uint32_t el = mla::elect_one();
+    const uint64_t policy = ptx::policy_evict_first();
+    const int kb_all = p.K / (MX ? 128 : 64);
+    constexpr int kPerStep = MX ? 2 : 4;       // scale blocks of a step
+    int st = 0, parity = 1;
+    int64_t count = 0;
+    bool ok = true;
+    for (int64_t s = start; s < end && ok;) {
+      const Unit u = unit_at(s);
+      const int e = mla::uniform(MODE == kDense ? 0 : MODE == kGateUp && early ? s_expert[u.seg] : __ldcg(p.plan->expert + u.seg));
+      const int in = MODE == kGateUp ? u.tile - u.seg * seg_tiles : u.tile;
+      const int blk = mla::uniform(e * blocks + (MODE == kGateUp ? in >> 1 : in)), half = mla::uniform(in & 1);
+      for (int i = 0; i < u.n; ++i, ++count) {
+        ok = mla::wait_warp(empty + 8 * st, parity, &s_ctl);
+        if (!ok) break;
+        const int step = u.step + i;
+        const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem) + st * p.stage_bytes;
+        mla::arrive_expect_tx(el, bar, kWeightBytes + kPerStep * 512);
+        const int w0 = p.tiled ? 0 : step * 128, w1 = p.tiled ? blk * steps + step : blk, s1 = blk * kb_all + step * kPerStep;
         if (MODE == kGateUp) {                 // 16 rows of each 32 of a block of 128: gate's, then up's
-          const int half = in & 1, blk = e * blocks + (in >> 1);
-          ptx::tma_load_3d(dst + kWeightBytes, &scales, bar, 64 * half, 0, blk * kb_all + step * kPerStep, policy);
-          tma_load_4d(dst, &weights, bar, p.tiled ? 0 : step * 128, 16 * half, 0, (p.tiled ? blk * steps + step : blk) * 4, policy);
+          tma_3d(el, dst + kWeightBytes, &scales, bar, 64 * half, 0, s1, policy);
+          tma_4d(el, dst, &weights, bar, w0, 16 * half, 0, w1 * 4, policy);
         } else {
-          const int blk = e * blocks + in;
-          ptx::tma_load_2d(dst + kWeightBytes, &scales, bar, 0, blk * kb_all + step * kPerStep, policy);
-          ptx::tma_load_2d(dst, &weights, bar, p.tiled ? 0 : step * 128, (p.tiled ? blk * steps + step : blk) * 128, policy);
+          tma_2d(el, dst + kWeightBytes, &scales, bar, 0, s1, policy);
+          tma_2d(el, dst, &weights, bar, w0, w1 * 128, policy);
         }
-      };
-      auto load_terms = [&](int step, uint32_t tokens, int base, int m, int st) {
-        const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem + st * p.stage_bytes) + kWeightBytes + kScaleBytes;
-        const uint32_t dst_scales = dst + (p.stage_bytes - kWeightBytes - kScaleBytes) / (kCodeBytes + kTermScales) * kCodeBytes;
-        const uint8_t* codes = p.codes + int64_t(step) * p.rows * kCodeBytes;
-        const uint8_t* sf = p.scales + int64_t(step) * p.rows * kTermScales;
-        ptx::mbar_arrive_expect_tx(bar, m * (kCodeBytes + kTermScales));
-        if (MODE == kGateUp && m < p.T) {
-          for (int slot = 0; slot < m; ++slot) {
-            const int t = __ffs(tokens) - 1;
-            ptx::bulk_load(dst + slot * kCodeBytes, codes + t * kCodeBytes, kCodeBytes, bar, keep);
-            ptx::bulk_load(dst_scales + slot * kTermScales, sf + t * kTermScales, kTermScales, bar, keep);
-            tokens &= tokens - 1;
-          }
-        } else {
-          ptx::bulk_load(dst, codes + int64_t(base) * kCodeBytes, m * kCodeBytes, bar, keep);
-          ptx::bulk_load(dst_scales, sf + int64_t(base) * kTermScales, m * kTermScales, bar, keep);
-        }
-      };
-      auto expert_of = [&](const Unit& u) {
-        return MODE == kDense ? 0 : MODE == kGateUp && early ? s_expert[u.seg] : __ldcg(p.plan->expert + u.seg);
-      };
-      // weights of the first stages, before the terms are there
-      const int ahead = int(min(int64_t(p.stages), end - start));
-      int filled = 0;
-      for (int64_t s = start; filled < ahead;) {
-        const Unit u = unit_at(s);
-        const int e = expert_of(u);
-        for (int i = 0; i < u.n && filled < ahead; ++i, ++s) load_weights(u, u.step + i, e, filled++);
+        if (++st == p.stages) st = 0, parity ^= 1;
       }
-      ptx::grid_dep_wait();
-      int st = 0, parity = 1;
-      int64_t count = 0;
-      bool ok = true;
-      for (int64_t s = start; s < end && ok;) {
-        const Unit u = unit_at(s);
-        const int e = expert_of(u);
-        const uint32_t tokens = MODE == kDense ? 0 : __ldcg(p.plan->tokens + u.seg);
-        const int base = MODE == kDown ? __ldcg(p.plan->base + u.seg) : 0, m = MODE == kDense ? p.T : __popc(tokens);
-        for (int i = 0; i < u.n; ++i, ++s, ++count) {
-          if (count >= ahead) {
-            ok = mla::wait_phase(empty + 8 * st, parity, &s_ctl);
-            if (!ok) break;
-            load_weights(u, u.step + i, e, st);
-          }
-          load_terms(u.step + i, tokens, base, m, st);
-          if (++st == p.stages) st = 0, parity ^= 1;
-        }
-      }
-      if (!ok)                                 // given up: the block's copies land before it leaves
-        for (int64_t j = max(int64_t(0), count - p.stages); j < count; ++j)
-          mla::drain_phase(full + 8 * int(j % p.stages), int(j / p.stages) & 1);
+      s += u.n;
     }
+    if (!ok)                                   // given up: the block's copies land before it leaves
+      for (int64_t j = max(int64_t(0), count - p.stages); j < count; ++j)
+        mla::drain_phase(full + 8 * int(j % p.stages), int(j / p.stages) & 1);
+    __syncwarp();
+  } else if (warp == kTermWarp) {
+    // ---- the tokens' terms
+    const uint32_t el = mla::elect_one();
+    int st = 0, parity = 1;
+    int64_t count = 0;
+    bool ok = true;
+    for (int64_t s = start; s < end && ok;) {
+      const Unit u = unit_at(s);
+      const uint32_t tokens = mla::uniform(MODE == kDense ? 0 : p.plan->tokens[u.seg]);
+      const int base = mla::uniform(MODE == kDown ? p.plan->base[u.seg] : 0), m = MODE == kDense ? p.T : __popc(tokens);
+      for (int i = 0; i < u.n; ++i, ++count) {
+        ok = mla::wait_warp(empty + 8 * st, parity, &s_ctl);
+        if (!ok) break;
+        const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem) + st * p.stage_bytes + kWeightBytes + kScaleBytes;
+        const uint8_t* codes = p.codes + int64_t(u.step + i) * p.rows * kCodeBytes;
+        const uint8_t* sf = p.scales + int64_t(u.step + i) * p.rows * kTermScales;
+        mla::arrive_expect_tx(el, bar, m * (kCodeBytes + kTermScales));
+        if (MODE == kGateUp && m < p.T) {
+          uint32_t left = tokens;
+          for (int slot = 0; slot < m; ++slot, left &= left - 1) {
+            const int t = __ffs(left) - 1;
+            bulk_copy(el, dst + slot * kCodeBytes, codes + t * kCodeBytes, kCodeBytes, bar);
+            bulk_copy(el, dst + terms_at + slot * kTermScales, sf + t * kTermScales, kTermScales, bar);
+          }
+        } else {
+          bulk_copy(el, dst, codes + int64_t(base) * kCodeBytes, m * kCodeBytes, bar);
+          bulk_copy(el, dst + terms_at, sf + int64_t(base) * kTermScales, m * kTermScales, bar);
+        }
+        if (++st == p.stages) st = 0, parity ^= 1;
+      }
+      s += u.n;
+    }
+    if (!ok)
+      for (int64_t j = max(int64_t(0), count - p.stages); j < count; ++j)
+        mla::drain_phase(full + 8 * int(j % p.stages), int(j / p.stages) & 1);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---- MMAs: 128 rows x (8 columns a token), 64 columns of K each
-    if (lane == 0) {
-      int st = 0, parity = 0;
-      uint32_t n = 0;
-      bool ok = true;
-      for (int64_t s = start; s < end && ok; ++n) {
-        const Unit u = unit_at(s);
-        const int m = MODE == kDense ? p.T : __popc(__ldcg(p.plan->tokens + u.seg));
-        const uint32_t idesc = ptx::idesc_nvfp4(128, (m * kTerms + 15) / 16 * 16, MX);
-        const uint32_t buffer = n % kBuffers, d = tmem + buffer * 128;
-        ok = mla::wait_phase(acc_empty + 8 * buffer, ((n / kBuffers) & 1) ^ 1, &s_ctl);
-        for (int i = 0; i < u.n && ok; ++i) {
-          ok = mla::wait_phase(ready + 8 * st, parity, &s_ctl);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint32_t at = ptx::smem_u32(smem + st * p.stage_bytes);
-          const uint64_t a = ptx::desc_kmajor_sw128(at), b = ptx::desc_kmajor_sw128(at + kWeightBytes + kScaleBytes);
-          const uint32_t sf = tmem + kScaleCol + st * kScaleCols;
-          const int nk = min(4, k_blocks - 4 * (u.step + i));
-          for (int kb = 0; kb < nk; ++kb) {
-            const uint32_t sfa = sf + 4 * kb, sfb = sf + 16 + (WIDE ? 8 : 4) * kb, on = i > 0 || kb > 0;
-            if (MX) ptx::tc_mma_mxfp4(d, a + 2 * kb, b + 2 * kb, idesc, sfa, sfb, on);
-            else ptx::tc_mma_nvfp4(d, a + 2 * kb, b + 2 * kb, idesc, sfa, sfb, on);
-          }
-          ptx::tc_commit(empty + 8 * st);
-          if (++st == p.stages) st = 0, parity ^= 1;
-        }
-        if (ok) ptx::tc_commit(acc_full + 8 * buffer);
-        s += u.n;
+    const uint32_t el = mla::elect_one();
+    int st = 0, parity = 0;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t s = start; s < end && ok; ++n) {
+      const Unit u = unit_at(s);
+      const int m = MODE == kDense ? p.T : __popc(p.plan->tokens[u.seg]);
+      const uint32_t idesc = mla::uniform(ptx::idesc_nvfp4(128, (m * kTerms + 15) / 16 * 16, MX));
+      const uint32_t buffer = n % kBuffers, d = tmem + buffer * 128;
+      ok = mla::wait_warp(acc_empty + 8 * buffer, ((n / kBuffers) & 1) ^ 1, &s_ctl);
+      for (int i = 0; i < u.n && ok; ++i) {
+        ok = mla::wait_warp(ready + 8 * st, parity, &s_ctl);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t a = mla::desc_sw128(ptx::smem_u32(smem) + st * p.stage_bytes, 16);
+        const uint32_t b = a + (kWeightBytes + kScaleBytes) / 16, sf = tmem + kScaleCol + st * kScaleCols;
+        const int nk = min(4, k_blocks - 4 * (u.step + i));
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+          if (kb < nk)
+            mma_fp4<MX>(el, d, a + 2 * kb, b + 2 * kb, idesc, sf + 4 * kb, sf + 16 + (WIDE ? 8 : 4) * kb, i > 0 || kb > 0);
+        mla::tc_commit(el, empty + 8 * st);
+        if (++st == p.stages) st = 0, parity ^= 1;
       }
-      ptx::tc_commit(drained);                 // before the tensor memory is freed
-      mla::drain_phase(drained, 0);
+      if (ok) mla::tc_commit(el, acc_full + 8 * buffer);
+      s += u.n;
     }
+    mla::tc_commit(el, drained);               // before the tensor memory is freed
+    mla::drain_phase(drained, 0);
     __syncwarp();
   } else if (warp < kJoiner) {
     // ---- scales to tensor memory: lane i of each quarter holds rows i, 32 + i, 64 + i and 96 + i
     const uint32_t quarter = uint32_t(warp & 3) * 32 << 16;
-    const int terms_at = (p.stage_bytes - kWeightBytes - kScaleBytes) / (kCodeBytes + kTermScales) * kCodeBytes;
     int st = 0, parity = 0;
     bool ok = true;
     for (int64_t s = start; s < end && ok;) {
@@ -424,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         if (!ok) break;
         const uint32_t at = ptx::smem_u32(smem + st * p.stage_bytes) + kWeightBytes;
         const uint32_t sf = tmem + quarter + kScaleCol + st * kScaleCols;
-        ptx::tc_fence_after();
+        uint32_t c[16], t[WIDE ? 32 : 16];       // columns: [64 columns of K][32 rows]
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) {
           uint4 w = ptx::lds128(at + (MX ? kb >> 1 : kb) * 512 + lane * 16);
@@ -432,23 +468,22 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
             const int by = (kb & 1) * 16;
             w = make_uint4((w.x >> by) & 0xFFFFu, (w.y >> by) & 0xFFFFu, (w.z >> by) & 0xFFFFu, (w.w >> by) & 0xFFFFu);
           }
-          ptx::tmem_st_32x32b_x4(sf + 4 * kb, w.x, w.y, w.z, w.w);
-          // columns 32 c + lane: term lane % 8 of token 4 c + lane / 8
-#pragma unroll
-          for (int half = 0; half < (WIDE ? 2 : 1); ++half) {
-            uint32_t c[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int token = 16 * half + 4 * j + (lane >> 3);
-              c[j] = 0;
-              if (token < m)
-                asm volatile("ld.shared.u32 %0, [%1];"
-                             : "=r"(c[j])
-                             : "r"(at + kScaleBytes + terms_at + token * kTermScales + kb * 32 + (lane & 7) * 4));
-            }
-            ptx::tmem_st_32x32b_x4(sf + 16 + (WIDE ? 8 : 4) * kb + 4 * half, c[0], c[1], c[2], c[3]);
-          }
+          c[4 * kb] = w.x, c[4 * kb + 1] = w.y, c[4 * kb + 2] = w.z, c[4 * kb + 3] = w.w;
         }
+        // row 32 j + lane of the terms: term lane % 8 of token 4 j + lane / 8
+#pragma unroll
+        for (int j = 0; j < (WIDE ? 8 : 4); ++j) {
+          const int token = 4 * j + (lane >> 3);
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (token < m) w = ptx::lds128(at + kScaleBytes + terms_at + token * kTermScales + (lane & 7) * 16);
+          constexpr int kRows = WIDE ? 8 : 4;
+          t[j] = w.x, t[kRows + j] = w.y, t[2 * kRows + j] = w.z, t[3 * kRows + j] = w.w;
+        }
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_st_32x32b_x16(sf, c);
+        if constexpr (WIDE) ptx::tmem_st_32x32b_x32(sf + 16, t);
+        else ptx::tmem_st_32x32b_x16(sf + 16, t);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::fence_proxy_async_smem();         // these reads before the copies that take the slot next

@@ -88,9 +88,11 @@ struct StreamParams {
 // ---- activations, counters and plan beforehand ---------------------------------------
 constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
 
+__device__ __forceinline__ float half_at(uint32_t low) { return __half2float(__ushort_as_half(uint16_t(low))); }
+
 // Eight terms of a step's 256 values, of which the lane holds 8 lane .. 8 lane + 7.
 template <bool MX>
-__device__ __forceinline__ void write_terms(float (&v)[8], float s0, int lane, uint8_t* codes, uint8_t* scales) {
+__device__ __forceinline__ void write_terms(float (&v)[8], float s0, float inv_s0, int lane, uint8_t* codes, uint8_t* scales) {
 #pragma unroll
   for (int r = 0; r < kTerms; ++r) {
     float top = 0.0f;
@@ -109,12 +111,14 @@ __device__ __forceinline__ void write_terms(float (&v)[8], float s0, int lane, u
       const uint32_t next = __shfl_down_sync(kFull, sb, 4);
       if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + r * 16 + (lane >> 3) * 4) = sb | next << 8;
     } else {
-      const float s = s0 * (1.0f / float(1 << shift_of(r)));
-      const float t = top * (1.0f / 6.0f) / s; // s a power of two: exact
-      sb = f32_to_ue4m3(t);
-      if (ue4m3_to_f32(sb) < t && sb < 0x7E) ++sb;
-      step = ue4m3_to_f32(sb) * s;
-      inv = sb ? 1.0f / step : 0.0f;
+      const float s = s0 * (1.0f / float(1 << shift_of(r))), t = top * (inv_s0 * (float(1 << shift_of(r)) / 6.0f));
+      uint16_t near;                           // the nearest scale, and the next where that is below t
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(near) : "f"(t));
+      sb = near & 0xFFu;
+      const float below = half_at(ue4m3x2_to_half(sb));
+      if (below < t && sb < 0x7E) ++sb;
+      step = half_at(ue4m3x2_to_half(sb)) * s;
+      inv = sb ? ptx::rcp_approx(step) : 0.0f; // a code off by this is made good by the next term
       if ((lane & 1) == 0) scales[r * 16 + (lane >> 1)] = uint8_t(sb);
     }
     uint32_t word = 0;
@@ -139,12 +143,16 @@ __device__ __forceinline__ void convert_row(const void* x, int row, int rows, in
                                             uint8_t* scales, float* row_scale) {
   __shared__ uint32_t s_top[kPrepWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, steps = (K + kStep - 1) / kStep;
+  const int step = group * kPrepWarps + warp;  // this warp's
+  float v[8];
+  load_block<SRC>(v, x, step, K, lane);
   uint32_t top = 0;
-  for (int step = warp; step < steps; step += kPrepWarps) {
-    float v[8];
-    load_block<SRC>(v, x, step, K, lane);
+#pragma unroll 4
+  for (int s = warp; s < steps; s += kPrepWarps) {
+    float u[8];
+    load_block<SRC>(u, x, s, K, lane);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(u[i]) & 0x7FFFFFFFu);
   }
   top = __reduce_max_sync(kFull, top);
   if (lane == 0) s_top[warp] = top;
@@ -152,18 +160,16 @@ __device__ __forceinline__ void convert_row(const void* x, int row, int rows, in
 #pragma unroll
   for (int w = 0; w < kPrepWarps; ++w) top = max(top, s_top[w]);
   const bool finite = top < 0x7F800000u;
-  const float s0 = exp2i(max(int(top >> 23) - 127, -80) - 10);   // the largest is 170 .. 342 times 6 of it
+  const int e0 = max(int(top >> 23) - 127, -80) - 10;
+  const float s0 = exp2i(e0);                  // the largest is 170 .. 342 times 6 of it
   if (group == 0 && threadIdx.x == 0) row_scale[row] = !finite ? __int_as_float(0x7FFFFFFF) : (MX ? 1.0f : s0);
-  const int step = group * kPrepWarps + warp;
   if (step >= steps) return;
-  float v[8];
-  load_block<SRC>(v, x, step, K, lane);
   if (!finite) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
   }
   const int64_t at = int64_t(step) * rows + row;
-  write_terms<MX>(v, finite ? s0 : 1.0f, lane, codes + at * kCodeBytes, scales + at * kTermScales);
+  write_terms<MX>(v, finite ? s0 : 1.0f, finite ? exp2i(-e0) : 1.0f, lane, codes + at * kCodeBytes, scales + at * kTermScales);
 }
 
 // Grid: (groups of eight steps, rows and, with a plan, one more).  Zeroes the counters as well.
@@ -552,22 +558,34 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       if (!whole) {
         float* to = slot_of(blockIdx.x);
         for (int i = 0; i < width; ++i) to[i * kTileRows] = total[i * kTileRows];
-        __threadfence();
         mla::bar_sync(1, 32 * kJoinWarps);
-        if (id == 0) {
-          s_last = atomicAdd(p.done + u.tile, 1u) == uint32_t(last - first);
-          __threadfence();
+        if (id == 0) {                         // releases what the barrier ordered before it, acquires the others'
+          uint32_t before;
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.done + u.tile) : "memory");
+          s_last = before == uint32_t(last - first);
         }
         mla::bar_sync(1, 32 * kJoinWarps);
         if (!s_last) continue;
+        // the ranges' sums in their order; eight tokens of four ranges on their way together
+        for (int i = 0; i < width; i += 8) {
+          float v[8] = {};
+          for (int b = first; b <= last; b += 4) {
+            float a[4][8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                a[c][j] = b + c <= last && i + j < width ? __ldcg(slot_of(b + c) + (i + j) * kTileRows) : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] += a[c][j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (i + j < width) total[(i + j) * kTileRows] = v[j];
+        }
       }
-      auto value = [&](int i) {
-        if (whole) return total[i * kTileRows];
-        float v = 0.0f;
-#pragma unroll 4
-        for (int b = first; b <= last; ++b) v += __ldcg(slot_of(b) + i * kTileRows);
-        return v;
-      };
       if (MODE == kGateUp) {
         const int I = p.N / 2, in = u.tile - u.seg * seg_tiles, e = p.plan->expert[u.seg];
         const float ws = p.gscale ? p.gscale[e] : 1.0f;
@@ -579,13 +597,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         // rows 32 q + j are gate's, 32 q + 16 + j up's
         const int col = (in >> 1) * 128 + 32 * quarter + 16 * (in & 1) + lane;
         for (int i = 0; i < m; ++i) {
-          const float gate = value(i) * ws, up = __shfl_xor_sync(kFull, gate, 16), wi = __shfl_sync(kFull, w, i);
+          const float gate = total[i * kTileRows] * ws, up = __shfl_xor_sync(kFull, gate, 16), wi = __shfl_sync(kFull, w, i);
           if (lane < 16) static_cast<float*>(p.out)[int64_t(base + i) * I + col] = gate / (1.0f + expf(-gate)) * up * wi;
         }
       } else {
         const float ws = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
         for (int t = 0; t < p.T; ++t) {
-          const float v = value(t) * ws;
+          const float v = total[t * kTileRows] * ws;
           const int64_t o = int64_t(t) * p.N + u.tile * kTileRows + row;
           if (MODE == kDense && p.out_fp16)
             static_cast<__half*>(p.out)[o] = __float2half_rn(v);

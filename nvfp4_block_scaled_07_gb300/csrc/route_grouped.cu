@@ -37,6 +37,7 @@ struct RouteParams {
   const float* bias;
   int T, E, k, groups, keep, best, softmax, renorm;
   float factor;
+  int wide;                                   // rows of logits, and the bias, start on 16-byte boundaries
   int32_t* idx;
   float* w;
 };
@@ -53,6 +54,21 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // NaN counts as -inf (score 0), +inf as the largest number.
 __device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
 
+// VPL values from e0 on, -inf past the E-th.
+template <int VPL>
+__device__ __forceinline__ void load(float (&v)[VPL], const float* from, int e0, int E, bool wide) {
+  if (VPL >= 4 && wide && e0 + VPL <= E) {
+#pragma unroll
+    for (int i = 0; i + 3 < VPL; i += 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(from + e0 + i));
+      v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? __ldg(from + e0 + i) : -INFINITY;
+  }
+}
+
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -61,81 +77,120 @@ __device__ __forceinline__ F warp_sum(F v) {
 }
 
 // ---- the choice in float64 ------------------------------------------------------
+// Keys that order like doubles, compared as integers.
+__device__ __forceinline__ uint64_t key_of(double d) {
+  const uint64_t u = uint64_t(__double_as_longlong(d));
+  return u ^ (uint64_t(int64_t(u) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double value_of(uint64_t key) {
+  return __longlong_as_double(int64_t(key & 0x8000000000000000ull ? key ^ 0x8000000000000000ull : ~key));
+}
+// The sum of a token's softmax relative to its largest logit `top` (a warp).
 template <int VPL>
-__device__ __noinline__ int choose_exactly(const RouteParams& p, int t, int lane) {
-  const float* row = p.logits + int64_t(t) * p.E;
-  const int per = p.E / p.groups;
-  double c[VPL];
-  float top = -INFINITY;
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    if (e < p.E) top = fmaxf(top, clean(row[e]));
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+__device__ __noinline__ double softmax_sum(const float* row, int E, float top, int lane) {
   double sum = 0.0;
   for (int i = 0; i < VPL; ++i) {
     const int e = lane * VPL + i;
-    c[i] = -INFINITY;
-    if (e >= p.E) continue;
-    const double v = clean(row[e]);
-    c[i] = p.softmax ? (v == -INFINITY ? 0.0 : exp(v - double(top))) : 1.0 / (1.0 + exp(-v));
-    sum += c[i];
+    const float v = e < E ? clean(row[e]) : -INFINITY;
+    if (v > -INFINITY) sum += exp(double(v) - double(top));
   }
-  if (p.softmax) {
-    sum = warp_sum(sum);
-    if (sum == 0.0) sum = 1.0;
-  }
+  return warp_sum(sum);
+}
+__device__ __noinline__ double exact_score(const RouteParams& p, const float* row, int e, float top, double sum) {
+  const double v = clean(row[e]);
+  double c;
+  if (p.softmax) c = v == -INFINITY ? 0.0 : exp(v - double(top)) / sum;
+  else c = 1.0 / (1.0 + exp(-v));
+  return p.bias ? c + double(clean(p.bias[e])) : c;
+}
+
+// All of it: the groups' values, the groups, the experts.  Lane j < k returns the j-th.
+template <int VPL>
+__device__ __noinline__ int choose_exactly(const RouteParams& p, int t, float top, int lane) {
+  const float* row = p.logits + int64_t(t) * p.E;
+  const int per = p.E / p.groups;
+  const double sum = p.softmax ? softmax_sum<VPL>(row, p.E, top, lane) : 0.0;
+  uint64_t key[VPL];                          // 0: no candidate
   for (int i = 0; i < VPL; ++i) {
     const int e = lane * VPL + i;
-    if (e >= p.E) continue;
-    if (p.softmax) c[i] /= sum;
-    if (p.bias) c[i] += double(clean(p.bias[e]));
+    key[i] = e < p.E ? key_of(exact_score(p, row, e, top, sum)) : 0;
   }
-  // the groups' values (lane g holds group g's) and ranks
-  double mine = -INFINITY;
-  for (int g = 0; g < p.groups && p.groups > 1; ++g) {
-    double a = -INFINITY, b = -INFINITY;
+  auto better = [](uint64_t& x, int& e, uint64_t y, int f) {  // of two candidates, the lower index first
+    if (y > x || (y == x && f < e)) x = y, e = f;
+  };
+  if (p.groups > 1) {
+    double mine = -INFINITY;                  // lane g: group g's value
+    for (int g = 0; g < p.groups; ++g) {
+      uint64_t best = 0, second = 0;
+      int e1 = INT_MAX, e2 = INT_MAX;
+      for (int i = 0; i < VPL; ++i)
+        if (key[i] && (lane * VPL + i) / per == g) better(best, e1, key[i], lane * VPL + i);
+      for (int d = 16; d; d >>= 1) better(best, e1, __shfl_xor_sync(kFull, best, d), __shfl_xor_sync(kFull, e1, d));
+      if (p.best == 2) {
+        for (int i = 0; i < VPL; ++i)
+          if (key[i] && (lane * VPL + i) / per == g && lane * VPL + i != e1) better(second, e2, key[i], lane * VPL + i);
+        for (int d = 16; d; d >>= 1) better(second, e2, __shfl_xor_sync(kFull, second, d), __shfl_xor_sync(kFull, e2, d));
+      }
+      if (lane == g) mine = p.best == 2 ? value_of(best) + value_of(second) : value_of(best);
+    }
+    const uint64_t value = lane < p.groups ? key_of(mine) : 0;
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const uint64_t other = __shfl_sync(kFull, value, g);
+      rank += other > value || (other == value && g < lane);
+    }
+    const uint32_t kept = __ballot_sync(kFull, lane < p.groups && rank < p.keep);
     for (int i = 0; i < VPL; ++i) {
       const int e = lane * VPL + i;
-      if (e < p.E && e / per == g) {
-        if (c[i] > a) b = a, a = c[i];
-        else if (c[i] > b) b = c[i];
-      }
+      if (e < p.E && !((kept >> (e / per)) & 1)) key[i] = 0;
     }
-    for (int d = 16; d; d >>= 1) {
-      const double oa = __shfl_xor_sync(kFull, a, d), ob = __shfl_xor_sync(kFull, b, d);
-      b = fmax(fmin(a, oa), fmax(b, ob));
-      a = fmax(a, oa);
-    }
-    if (lane == g) mine = p.best == 2 ? a + b : a;
-  }
-  int rank = 0;
-  for (int g = 0; g < p.groups; ++g) {
-    const double other = __shfl_sync(kFull, mine, g);
-    rank += other > mine || (other == mine && g < lane);
-  }
-  const uint32_t kept = __ballot_sync(kFull, lane < p.groups && rank < p.keep);
-  uint32_t open = 0;                          // bit i: expert i of the lane can be chosen
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    if (e < p.E && ((kept >> (e / per)) & 1)) open |= 1u << i;
   }
   int my_e = 0;
   for (int j = 0; j < p.k; ++j) {
-    double v = -INFINITY;
+    uint64_t best = 0;
     int e = INT_MAX;
     for (int i = 0; i < VPL; ++i)
-      if (((open >> i) & 1) && (e == INT_MAX || c[i] > v)) v = c[i], e = lane * VPL + i;
-    for (int d = 16; d; d >>= 1) {
-      const double ov = __shfl_xor_sync(kFull, v, d);
-      const int oe = __shfl_xor_sync(kFull, e, d);
-      if (oe != INT_MAX && (e == INT_MAX || ov > v || (ov == v && oe < e))) v = ov, e = oe;
-    }
-    if (e / VPL == lane) open &= ~(1u << (e % VPL));
+      if (key[i]) better(best, e, key[i], lane * VPL + i);
+    for (int d = 16; d; d >>= 1) better(best, e, __shfl_xor_sync(kFull, best, d), __shfl_xor_sync(kFull, e, d));
+    for (int i = 0; i < VPL; ++i)
+      if (lane * VPL + i == e) key[i] = 0;
     if (lane == j) my_e = e;
   }
   return my_e;
+}
+
+// Whether group `lane`, whose value is that of experts e1 and e2, is one of the best.
+template <int VPL>
+__device__ __noinline__ bool keeps_exactly(const RouteParams& p, int t, float top, int lane, int e1, int e2) {
+  const float* row = p.logits + int64_t(t) * p.E;
+  const double sum = p.softmax ? softmax_sum<VPL>(row, p.E, top, lane) : 0.0;
+  double v = exact_score(p, row, e1, top, sum);
+  if (p.best == 2) v += exact_score(p, row, e2, top, sum);
+  const uint64_t value = lane < p.groups ? key_of(v) : 0;
+  int rank = 0;
+  for (int g = 0; g < p.groups; ++g) {
+    const uint64_t other = __shfl_sync(kFull, value, g);
+    rank += other > value || (other == value && g < lane);
+  }
+  return lane < p.groups && rank < p.keep;
+}
+
+// Among at most 32 candidates, in ascending order in `from`: the k best.
+template <int VPL>
+__device__ __noinline__ int choose_among(const RouteParams& p, int t, float top, int lane, int n, int* from) {
+  const float* row = p.logits + int64_t(t) * p.E;
+  const double sum = p.softmax ? softmax_sum<VPL>(row, p.E, top, lane) : 0.0;
+  const int e = lane < n ? from[lane] : 0;
+  const uint64_t key = lane < n ? key_of(exact_score(p, row, e, top, sum)) : 0;
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const uint64_t other = __shfl_sync(kFull, key, i);
+    rank += other > key || (other == key && i < lane);
+  }
+  __syncwarp();
+  if (lane < n && rank < p.k) from[rank] = e;
+  __syncwarp();
+  return lane < p.k ? from[lane] : 0;
 }
 
 // ---- the choice in float32 --------------------------------------------------------
@@ -144,6 +199,7 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, int t, int lane
 template <int VPL, bool WHOLE>
 __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteParams p) {
   __shared__ float s_group[WHOLE ? 1 : kWarps][WHOLE ? 1 : 32 * VPL];
+  __shared__ int s_among[kWarps][32];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -152,8 +208,9 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
   const float* row = p.logits + int64_t(t) * p.E;
   const int e0 = lane * VPL, per = p.E / p.groups;
   float v[VPL], c[VPL];
+  load<VPL>(v, row, e0, p.E, p.wide);
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) v[i] = e0 + i < p.E ? clean(row[e0 + i]) : -INFINITY;
+  for (int i = 0; i < VPL; ++i) v[i] = clean(v[i]);
 
   // scores
   float top = 0.0f, sum = 0.0f;               // softmax
@@ -191,9 +248,14 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
       for (int i = 0; i < VPL; ++i) c[i] = ptx::rcp_approx(1.0f + __expf(-v[i]));
       error = 0x1p-21f;
     }
+    if (p.bias) {
+      float b[VPL];
+      load<VPL>(b, p.bias, e0, p.E, p.wide);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] += clean(b[i]);
+    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      if (p.bias) c[i] += e0 + i < p.E ? clean(__ldg(p.bias + e0 + i)) : -INFINITY;
       if (c[i] > -INFINITY) most = fmaxf(most, fabsf(c[i]));
     }
     error += __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most))) * 0x1p-23f;
@@ -239,14 +301,43 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
       const float other = __shfl_sync(kFull, mine, g);
       rank += other > mine || (other == mine && g < lane);
     }
-    const bool is_kept = lane < p.groups && rank < p.keep;
-    const uint32_t kept = __ballot_sync(kFull, is_kept);
+    bool is_kept = lane < p.groups && rank < p.keep;
     if (!plain && p.keep < p.groups) {
       const float low = value_of(__reduce_min_sync(kFull, is_kept ? key_of(mine) : kFull));
       const float high = value_of(__reduce_max_sync(kFull, lane < p.groups && !is_kept ? key_of(mine) : 0u));
       // a sum of two rounds once more
-      sure = low - high > 2.0f * (p.best * error + 0x1p-23f * fmaxf(fabsf(low), fabsf(high)));
+      const float span = 2.0f * (p.best * error + 0x1p-23f * fmaxf(fabsf(low), fabsf(high)));
+      if (!(low - high > span)) {
+        int e1 = 0, e2 = 0;                   // of group `lane`: the experts of its value
+        bool clear = true;                    // and whether float32 tells which they are
+        for (int g = 0; g < p.groups; ++g) {
+          uint32_t m[3];
+          int e[3];
+          uint32_t used = 0;
+#pragma unroll
+          for (int n = 0; n < 3; ++n) {
+            uint32_t local = 0;
+            int at = 0;
+#pragma unroll
+            for (int i = VPL - 1; i >= 0; --i)
+              if (key[i] != 0u && key[i] >= local && !((used >> i) & 1) && (e0 + i) / per == g) local = key[i], at = i;
+            m[n] = __reduce_max_sync(kFull, local);
+            const int from = __ffs(__ballot_sync(kFull, local == m[n])) - 1;
+            e[n] = __shfl_sync(kFull, e0 + at, from);
+            if (lane == from) used |= 1u << at;
+          }
+          if (lane == g) {
+            e1 = e[0], e2 = e[1];
+            const uint32_t next = p.best == 2 ? m[2] : m[1];
+            clear = next == 0u || value_of(p.best == 2 ? m[1] : m[0]) - value_of(next) > 2.0f * error;
+          }
+        }
+        const bool near = lane < p.groups && mine <= low + span && mine >= high - span;
+        sure = __ballot_sync(kFull, near && !clear) == 0u;
+        is_kept = keeps_exactly<VPL>(p, t, top, lane, e1, e2);
+      }
     }
+    const uint32_t kept = __ballot_sync(kFull, is_kept);
     if (WHOLE) {
       const bool in = (kept >> (lane / lanes)) & 1;
 #pragma unroll
@@ -257,6 +348,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
         if (!((kept >> min((e0 + i) / per, 31)) & 1)) key[i] = 0u;
     }
   }
+
+  bool groups_sure = sure;
+  uint32_t open = 0;                          // the lane's experts in kept groups
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) open |= uint32_t(key[i] != 0u) << i;
 
   // k rounds; the margin of the last is that to the best candidate left
   uint32_t local = key[0];
@@ -289,8 +385,29 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
     e = __shfl_sync(kFull, e, from);
     if (lane == j) my_e = e;
   }
+  const float last = before;                  // the k-th best
   if (!plain) margin(__reduce_max_sync(kFull, local));
-  if (!sure) my_e = choose_exactly<VPL>(p, t, lane);
+  if (!sure) {
+    // the exact k best are within 2 d of the k-th here
+    const float least = last - 2.0f * error - 0x1p-22f * fabsf(last);
+    int n = 0, at = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool in = ((open >> i) & 1) && c[i] >= least;
+      const uint32_t with = __ballot_sync(kFull, in);
+      n += __popc(with);
+      at += __popc(with & ((1u << lane) - 1));
+    }
+    if (groups_sure && n <= 32) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (((open >> i) & 1) && c[i] >= least) s_among[warp][at++] = e0 + i;
+      __syncwarp();
+      my_e = choose_among<VPL>(p, t, top, lane, n, s_among[warp]);
+    } else {
+      my_e = choose_exactly<VPL>(p, t, top, lane);
+    }
+  }
 
   // weights of the chosen
   const bool mine = lane < p.k;
@@ -330,7 +447,8 @@ cudaError_t launch_vpl(const RouteParams& p, cudaStream_t st) {
 
 cudaError_t launch_route_grouped(const float* logits, const float* bias, int T, int E, int k, int groups, int keep, int best,
                                  int softmax, int renorm, float factor, int32_t* idx, float* w, cudaStream_t st) {
-  const RouteParams p = {logits, bias, T, E, k, groups, keep, best, softmax, renorm, factor, idx, w};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(bias);
+  const RouteParams p = {logits, bias, T, E, k, groups, keep, best, softmax, renorm, factor, E % 4 == 0 && at % 16 == 0, idx, w};
   if (E <= 32) return launch_vpl<1>(p, st);
   if (E <= 64) return launch_vpl<2>(p, st);
   if (E <= 128) return launch_vpl<4>(p, st);

@@ -199,7 +199,9 @@ __device__ __noinline__ int choose_among(const RouteParams& p, int t, float top,
 template <int VPL, bool WHOLE>
 __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteParams p) {
   __shared__ float s_group[WHOLE ? 1 : kWarps][WHOLE ? 1 : 32 * VPL];
-  __shared__ int s_among[kWarps][32];
+  __shared__ __align__(16) uint32_t s_key[kWarps][32];
+  __shared__ uint32_t s_sorted[kWarps][36];
+  __shared__ int s_expert[kWarps][32];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -349,61 +351,118 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
     }
   }
 
-  bool groups_sure = sure;
-  uint32_t open = 0;                          // the lane's experts in kept groups
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) open |= uint32_t(key[i] != 0u) << i;
+  const bool groups_sure = sure;
 
-  // k rounds; the margin of the last is that to the best candidate left
+  // Candidates: keys not below the (k + 1)-th largest of the lanes' largest, the
+  // k + 1 best among them, a dozen or so.  Each goes to a lane of its own, in the order
+  // of experts, and counts those before it.
   uint32_t local = key[0];
 #pragma unroll
   for (int i = 1; i < VPL; ++i) local = max(local, key[i]);
-  int my_e = 0;
-  float before = INFINITY;
-  auto margin = [&](uint32_t m) {             // to the candidate before
-    const float now = value_of(m);
-    sure = sure && (m == 0u || before - now > 2.0f * error);
-    before = now;
-  };
-  for (int j = 0; j < p.k; ++j) {
-    const uint32_t m = __reduce_max_sync(kFull, local);
-    if (!plain) margin(m);
-    const int from = __ffs(__ballot_sync(kFull, local == m)) - 1;
-    int e = 0;
-    if (lane == from) {
-#pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == m) e = i;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == e) key[i] = 0u;
-      local = key[0];
-#pragma unroll
-      for (int i = 1; i < VPL; ++i) local = max(local, key[i]);
-      e += e0;
-    }
-    e = __shfl_sync(kFull, e, from);
-    if (lane == j) my_e = e;
+  uint32_t bound = 0;
+  for (uint32_t j = 0, rest = local; j <= uint32_t(p.k); ++j) {
+    bound = __reduce_max_sync(kFull, rest);
+    if (rest == bound) rest = 0u;             // of equal lanes all: only lowers the bound
   }
-  const float last = before;                  // the k-th best
-  if (!plain) margin(__reduce_max_sync(kFull, local));
+  bound = max(bound, 1u);
+  uint32_t in = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) in |= uint32_t(key[i] >= bound) << i;
+  int n = __popc(in), at = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(kFull, at, d);
+    if (lane >= d) at += u;
+  }
+  const int candidates = __shfl_sync(kFull, at, 31);
+  int my_e = 0;
+  float last;                                 // the k-th best
+  if (candidates <= 32) {
+    s_key[warp][lane] = 0u;
+    if (lane < 4) s_sorted[warp][32 + lane] = 0u;
+    s_sorted[warp][lane] = 0u;
+    __syncwarp();
+    at -= n;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if ((in >> i) & 1) {
+        s_key[warp][at] = key[i];
+        s_expert[warp][at++] = e0 + i;
+      }
+    __syncwarp();
+    const uint32_t mine = s_key[warp][lane];
+    const int e = s_expert[warp][lane];
+    int rank = 0;                             // equal ones: the lower index, which is the lower lane
+    for (int i = 0; i < candidates; i += 4) {
+      const uint4 q = *reinterpret_cast<const uint4*>(&s_key[warp][i]);
+      rank += (q.x + (i < lane) > mine) + (q.y + (i + 1 < lane) > mine) + (q.z + (i + 2 < lane) > mine) +
+              (q.w + (i + 3 < lane) > mine);
+    }
+    __syncwarp();
+    if (lane < candidates) {
+      s_sorted[warp][rank] = mine;
+      s_expert[warp][rank] = e;
+    }
+    __syncwarp();
+    my_e = s_expert[warp][lane];
+    const uint32_t here = s_sorted[warp][lane], next = s_sorted[warp][lane + 1];
+    last = value_of(__shfl_sync(kFull, here, p.k - 1));
+    if (!plain)
+      sure = sure && __all_sync(kFull, lane >= p.k || next == 0u || value_of(here) - value_of(next) > 2.0f * error);
+  } else {
+    // many equal or hardly any lanes: k rounds of the warp's maximum
+    uint32_t left[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) left[i] = key[i];
+    last = INFINITY;
+    auto margin = [&](uint32_t m) {           // to the one before
+      const float now = value_of(m);
+      sure = sure && (m == 0u || last - now > 2.0f * error);
+    };
+    for (int j = 0; j < p.k; ++j) {
+      const uint32_t m = __reduce_max_sync(kFull, local);
+      if (!plain) margin(m);
+      last = value_of(m);
+      const int from = __ffs(__ballot_sync(kFull, local == m)) - 1;
+      int e = 0;
+      if (lane == from) {
+#pragma unroll
+        for (int i = VPL - 1; i >= 0; --i)
+          if (left[i] == m) e = i;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (i == e) left[i] = 0u;
+        local = left[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) local = max(local, left[i]);
+        e += e0;
+      }
+      e = __shfl_sync(kFull, e, from);
+      if (lane == j) my_e = e;
+    }
+    if (!plain) margin(__reduce_max_sync(kFull, local));
+  }
   if (!sure) {
     // the exact k best are within 2 d of the k-th here
     const float least = last - 2.0f * error - 0x1p-22f * fabsf(last);
-    int n = 0, at = 0;
+    in = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool in = ((open >> i) & 1) && c[i] >= least;
-      const uint32_t with = __ballot_sync(kFull, in);
-      n += __popc(with);
-      at += __popc(with & ((1u << lane) - 1));
+    for (int i = 0; i < VPL; ++i) in |= uint32_t(key[i] != 0u && c[i] >= least) << i;
+    n = at = __popc(in);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(kFull, at, d);
+      if (lane >= d) at += u;
     }
-    if (groups_sure && n <= 32) {
+    const int near = __shfl_sync(kFull, at, 31);
+    if (groups_sure && near <= 32) {
+      at -= n;
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (((open >> i) & 1) && c[i] >= least) s_among[warp][at++] = e0 + i;
+        if ((in >> i) & 1) s_expert[warp][at++] = e0 + i;
       __syncwarp();
-      my_e = choose_among<VPL>(p, t, top, lane, n, s_among[warp]);
+      my_e = choose_among<VPL>(p, t, top, lane, near, s_expert[warp]);
     } else {
       my_e = choose_exactly<VPL>(p, t, top, lane);
     }

@@ -211,13 +211,16 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
   const int e0 = lane * VPL, per = p.E / p.groups;
   float v[VPL], c[VPL];
   load<VPL>(v, row, e0, p.E, p.wide);
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) v[i] = clean(v[i]);
 
   // scores
   float top = 0.0f, sum = 0.0f;               // softmax
-  float error = 0.0f;                         // |c - exact c| of any expert
+  // |c - exact c| is at most error + 2^-24 |c|, the rounding of a sum with the bias
+  float error = 0.0f;
   const bool plain = !p.bias && (p.groups == 1 || p.best == 1);   // c orders like v
+  if (plain || p.softmax) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = clean(v[i]);
+  }
   if (p.softmax && !(plain && p.renorm)) {
     top = v[0];
 #pragma unroll
@@ -235,7 +238,6 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
 #pragma unroll
     for (int i = 0; i < VPL; ++i) c[i] = v[i];
   } else {
-    float most = 0.0f;                        // largest |c|, for its rounding
     if (p.softmax) {
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
@@ -247,28 +249,26 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
       // __expf is within 2 + 1.2 |v| ulp, which moves s by at most 0.7 of an ulp of 1 as
       // s (1 - s) falls faster; the sum and the reciprocal take 2 ulp
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] = ptx::rcp_approx(1.0f + __expf(-v[i]));
+      for (int i = 0; i < VPL; ++i) c[i] = fmaxf(ptx::rcp_approx(1.0f + __expf(-v[i])), 0.0f);  // NaN: 0
       error = 0x1p-21f;
     }
     if (p.bias) {
       float b[VPL];
       load<VPL>(b, p.bias, e0, p.E, p.wide);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] += clean(b[i]);
+      for (int i = 0; i < VPL; ++i) c[i] = fmaxf(c[i] + b[i], -INFINITY);      // NaN: -inf
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (c[i] > -INFINITY) most = fmaxf(most, fabsf(c[i]));
-    }
-    error += __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most))) * 0x1p-23f;
   }
   uint32_t key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) key[i] = e0 + i < p.E ? key_of(c[i]) : 0u;
+  uint32_t local = key[0];                    // the lane's largest
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) local = max(local, key[i]);
 
-  bool sure = true;
+  bool sure = true, open = true;              // open (WHOLE): the lane's group is kept
   if (p.groups > 1) {
-    float value;                              // of group g, in lane g (not WHOLE) or the group's lanes
+    float value, size;                        // of group g, in lane g (not WHOLE) or the group's lanes; |c| of its parts
     const int lanes = WHOLE ? per / VPL : 1;
     if (WHOLE) {
       float a = c[0], b = -INFINITY;
@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
         a = fmaxf(a, oa);
       }
       value = p.best == 2 ? a + b : a;
+      size = p.best == 2 ? fabsf(a) + fabsf(b) : fabsf(a);
     } else {
       float* sh = s_group[warp];
 #pragma unroll
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
         a = fmaxf(a, x);
       }
       value = p.best == 2 ? a + b : a;
+      size = p.best == 2 ? fabsf(a) + fabsf(b) : fabsf(a);
     }
     // lane g: group g's value and rank
     const float mine = __shfl_sync(kFull, value, (lane * lanes) & 31);
@@ -307,8 +309,9 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
     if (!plain && p.keep < p.groups) {
       const float low = value_of(__reduce_min_sync(kFull, is_kept ? key_of(mine) : kFull));
       const float high = value_of(__reduce_max_sync(kFull, lane < p.groups && !is_kept ? key_of(mine) : 0u));
-      // a sum of two rounds once more
-      const float span = 2.0f * (p.best * error + 0x1p-23f * fmaxf(fabsf(low), fabsf(high)));
+      size = __shfl_sync(kFull, size, (lane * lanes) & 31);
+      size = __uint_as_float(__reduce_max_sync(kFull, lane < p.groups ? __float_as_uint(size) : 0u));
+      const float span = 2.0f * (p.best * error + 0x1p-23f * size);       // the parts' rounding and the sum's
       if (!(low - high > span)) {
         int e1 = 0, e2 = 0;                   // of group `lane`: the experts of its value
         bool clear = true;                    // and whether float32 tells which they are
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
           if (lane == g) {
             e1 = e[0], e2 = e[1];
             const uint32_t next = p.best == 2 ? m[2] : m[1];
-            clear = next == 0u || value_of(p.best == 2 ? m[1] : m[0]) - value_of(next) > 2.0f * error;
+            clear = next == 0u || value_of(p.best == 2 ? m[1] : m[0]) - value_of(next) > span;
           }
         }
         const bool near = lane < p.groups && mine <= low + span && mine >= high - span;
@@ -341,13 +344,15 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
     }
     const uint32_t kept = __ballot_sync(kFull, is_kept);
     if (WHOLE) {
-      const bool in = (kept >> (lane / lanes)) & 1;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = in ? key[i] : 0u;
+      open = (kept >> (lane / lanes)) & 1;
+      if (!open) local = 0u;
     } else {
+      local = 0u;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
+      for (int i = 0; i < VPL; ++i) {
         if (!((kept >> min((e0 + i) / per, 31)) & 1)) key[i] = 0u;
+        local = max(local, key[i]);
+      }
     }
   }
 
@@ -356,9 +361,6 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
   // Candidates: keys not below the (k + 1)-th largest of the lanes' largest, the
   // k + 1 best among them, a dozen or so.  Each goes to a lane of its own, in the order
   // of experts, and counts those before it.
-  uint32_t local = key[0];
-#pragma unroll
-  for (int i = 1; i < VPL; ++i) local = max(local, key[i]);
   uint32_t bound = 0;
   for (uint32_t j = 0, rest = local; j <= uint32_t(p.k); ++j) {
     bound = __reduce_max_sync(kFull, rest);
@@ -368,6 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
   uint32_t in = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) in |= uint32_t(key[i] >= bound) << i;
+  if (!open) in = 0;
   int n = __popc(in), at = n;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -408,16 +411,17 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
     const uint32_t here = s_sorted[warp][lane], next = s_sorted[warp][lane + 1];
     last = value_of(__shfl_sync(kFull, here, p.k - 1));
     if (!plain)
-      sure = sure && __all_sync(kFull, lane >= p.k || next == 0u || value_of(here) - value_of(next) > 2.0f * error);
+      sure = sure && __all_sync(kFull, lane >= p.k || next == 0u || value_of(here) - value_of(next) >
+                                                                           2.0f * error + 0x1p-22f * fmaxf(fabsf(value_of(here)), fabsf(value_of(next))));
   } else {
     // many equal or hardly any lanes: k rounds of the warp's maximum
     uint32_t left[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) left[i] = key[i];
+    for (int i = 0; i < VPL; ++i) left[i] = open ? key[i] : 0u;
     last = INFINITY;
     auto margin = [&](uint32_t m) {           // to the one before
       const float now = value_of(m);
-      sure = sure && (m == 0u || last - now > 2.0f * error);
+      sure = sure && (m == 0u || last - now > 2.0f * error + 0x1p-22f * fmaxf(fabsf(last), fabsf(now)) || last == INFINITY);
     };
     for (int j = 0; j < p.k; ++j) {
       const uint32_t m = __reduce_max_sync(kFull, local);
@@ -444,10 +448,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteP
   }
   if (!sure) {
     // the exact k best are within 2 d of the k-th here
-    const float least = last - 2.0f * error - 0x1p-22f * fabsf(last);
+    const float least = last - 2.0f * error - 0x1p-21f * fabsf(last);
     in = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) in |= uint32_t(key[i] != 0u && c[i] >= least) << i;
+    for (int i = 0; i < VPL; ++i) in |= uint32_t(open && key[i] != 0u && c[i] >= least) << i;
     n = at = __popc(in);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {

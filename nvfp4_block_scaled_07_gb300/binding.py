@@ -10,6 +10,7 @@ shared library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -118,16 +119,42 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _stream_of(t):
-    """The current stream; calls are made with the tensors' device current."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return _stream()
+# The checks of the calls of a decode step, whose kernels take microseconds: each
+# property is read once, and no message is built before it is needed.
+def _refuse(t, dtype, shape, name, device):
+    """The error of a tensor that is not what a call needs."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _same_device(first, t, name):
-    if t.get_device() != first.get_device():
-        raise ValueError(f"{name} is on {t.device}, the first tensor on {first.device}")
+def _dense(t, dtype, shape, name, device):
+    """A contiguous tensor's data pointer."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and device >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, name, device)
+
+
+def _at_least(t, numel, name, device):
+    """The data pointer of a contiguous uint8 buffer of at least so many bytes."""
+    if t.dtype is torch.uint8 and t.numel() >= numel and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is torch.uint8 and t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} bytes, needs {numel}")
+    _refuse(t, torch.uint8, t.shape, name, device)
+
+
+def _device_stream(device):
+    """The device's current stream; calls are made with that device current."""
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _need(t, dtype, shape=None, name="tensor"):
@@ -227,21 +254,17 @@ def moe_route_grouped(logits, k, score_fn="sigmoid", renormalize=True, select_bi
     by their largest or their two largest biased scores), a bias that selects
     but is not in the weights, and a factor on the weights."""
     T, E = logits.shape
-    _need(logits, torch.float32, name="logits")
-    if select_bias is not None:
-        _need(select_bias, torch.float32, (E,), "select_bias")
-        _same_device(logits, select_bias, "select_bias")
+    dev = logits.get_device()
+    logits_at = _dense(logits, torch.float32, (T, E), "logits", dev)
+    bias_at = None if select_bias is None else _dense(select_bias, torch.float32, (E,), "select_bias", dev)
     if topk_idx is None:
-        topk_idx = _empty((T, k), torch.int32, logits.device)
+        topk_idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     if topk_w is None:
-        topk_w = _empty((T, k), torch.float32, logits.device)
-    _need(topk_idx, torch.int32, (T, k), "topk_idx")
-    _need(topk_w, torch.float32, (T, k), "topk_w")
-    _same_device(logits, topk_idx, "topk_idx")
-    _same_device(logits, topk_w, "topk_w")
-    _check(_lib.moe_route_grouped(_ptr(logits), _ptr(select_bias), T, E, k, n_group, topk_group, group_best,
-                                  SCORE[score_fn], int(bool(renormalize)), scale, _ptr(topk_idx), _ptr(topk_w),
-                                  _stream_of(logits)), "moe_route_grouped")
+        topk_w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _check(_lib.moe_route_grouped(logits_at, bias_at, T, E, k, n_group, topk_group, group_best, SCORE[score_fn],
+                                  1 if renormalize else 0, scale, _dense(topk_idx, torch.int32, (T, k), "topk_idx", dev),
+                                  _dense(topk_w, torch.float32, (T, k), "topk_w", dev), _device_stream(dev)),
+           "moe_route_grouped")
     return topk_idx, topk_w
 
 
@@ -719,71 +742,66 @@ X_DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 
 
 def _rows(x, dtypes, name):
-    """[T, K] whose rows are contiguous and start on 16-byte boundaries: (T, K, stride)."""
+    """[T, K] whose rows are contiguous and start on 16-byte boundaries: (T, K, address, stride, device)."""
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {x.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.dim() != 2:
         raise ValueError(f"{name}: {x.dim()} dimensions, expected 2")
     T, K = x.shape
-    step = x.stride(0) if T > 1 else K
-    if (x.stride(1) != 1 and K > 1) or step % 8 or x.data_ptr() % 16:
-        raise ValueError(f"{name}: strides {x.stride()}, address {x.data_ptr():#x} (innermost 1, the other a multiple of 8, "
-                         "16-byte aligned)")
-    return T, K, step
+    stride = x.stride()
+    step = stride[0] if T > 1 else K
+    at = x.data_ptr()
+    if (stride[1] != 1 and K > 1) or step % 8 or at % 16:
+        raise ValueError(f"{name}: strides {stride}, address {at:#x} (innermost 1, the other a multiple of 8, 16-byte aligned)")
+    return T, K, at, step, dev
 
 
-def _few_weights(x, w_packed, w_scales, w_gscale, fmt, name):
-    """(E, N, K, arguments without the layout, layout) of one call's weights."""
-    data = w_packed.data if isinstance(w_packed, TiledWeights) else w_packed
-    if not isinstance(w_packed, TiledWeights) and w_packed.dim() == 2:
-        w_packed = w_packed[None]
-    E, N, K, ptr, layout = _weights_args(w_packed)
+def _few_weights(w_packed, w_scales, w_gscale, fmt, name, dev):
+    """(E, N, K, layout, [codes, scales, per-matrix scales]) of a call's weights, addresses."""
     if isinstance(w_packed, TiledWeights):
-        _need(data, torch.uint8, name=name)
-        if data.numel() < int(_lib.nvfp4moe_tiled_weights_bytes(E * N, K)):
-            raise ValueError(f"{name}: smaller than the tiled layout needs")
-    _need(w_scales, torch.uint8, name=f"{name} scales")
-    need = E * blocked_scales_bytes(N, K, fmt)
-    if w_scales.numel() < need:
-        raise ValueError(f"{name}: scale buffer smaller than the blocked layout needs")
-    _same_device(x, data, name)
-    _same_device(x, w_scales, f"{name} scales")
-    args = [ptr, _ptr(w_scales)]
+        E, N, K, layout = w_packed.E, w_packed.N, w_packed.K, W_TILED
+        at = _at_least(w_packed.data, E * N * (-(-K // 256) * 128), name, dev)
+    else:
+        if w_packed.dim() == 2:
+            w_packed = w_packed[None]
+        E, N, half = w_packed.shape
+        K, layout = 2 * half, W_ROWMAJOR
+        at = _dense(w_packed, torch.uint8, (E, N, half), name, dev)
+    block = 16 if fmt == "nvfp4" else 32
+    args = [at, _at_least(w_scales, E * -(-N // 128) * 128 * (K // block), f"{name} scales", dev)]
     if fmt == "nvfp4":
-        _need(w_gscale, torch.float32, (E,), f"{name} gscale")
-        _same_device(x, w_gscale, f"{name} gscale")
-        args.append(_ptr(w_gscale))
-    return E, N, K, args, layout
+        args.append(_dense(w_gscale, torch.float32, (E,), f"{name} gscale", dev))
+    return E, N, K, layout, args
 
 
-def _few_workspace(x, need, workspace):
+def _few_workspace(need, workspace, x, dev):
+    """(address, bytes, what keeps it alive) of a call's workspace."""
     if workspace is None:
-        return _empty((need,), torch.uint8, x.device) if need else None
-    _need(workspace, torch.uint8, name="workspace")
-    _same_device(x, workspace, "workspace")
-    return workspace
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    return _at_least(workspace, need, "workspace", dev), workspace.numel(), workspace
 
 
+@functools.lru_cache(maxsize=None)
 def moe_matvec_workspace_size(T, N, K):
     return int(_lib.moe_matvec_workspace_size(T, N, K))
 
 
 def _matvec(fmt, x, w_packed, w_scales, w_gscale, out, workspace):
-    T, K, step = _rows(x, X_DTYPE, "x")
-    E, N, Kw, w_args, layout = _few_weights(x, w_packed, w_scales, w_gscale, fmt, "w_packed")
+    T, K, x_at, step, dev = _rows(x, X_DTYPE, "x")
+    E, N, Kw, layout, w_args = _few_weights(w_packed, w_scales, w_gscale, fmt, "w_packed", dev)
     if E != 1 or Kw != K:
         raise ValueError(f"w_packed: {E} matrices of {Kw} columns, expected one of {K}")
     if out is None:
-        out = _empty((T, N), x.dtype, x.device)
-    else:
-        _need(out, x.dtype, (T, N), "out")
-        _same_device(x, out, "out")
-    ws = _few_workspace(x, moe_matvec_workspace_size(T, N, K), workspace)
+        out = torch.empty((T, N), dtype=x.dtype, device=x.device)
+    ws_at, ws_bytes, workspace = _few_workspace(moe_matvec_workspace_size(T, N, K), workspace, x, dev)
     call = _lib.moe_matvec_nvfp4 if fmt == "nvfp4" else _lib.moe_matvec_mxfp4
-    _check(call(_ptr(x), step, T, X_DTYPE[x.dtype], *w_args, N, K, layout, _ptr(out), _ptr(ws),
-                0 if ws is None else ws.numel(), _stream_of(x)), f"moe_matvec_{fmt}")
+    _check(call(x_at, step, T, X_DTYPE[x.dtype], *w_args, N, K, layout, _dense(out, x.dtype, (T, N), "out", dev), ws_at,
+                ws_bytes, _device_stream(dev)), f"moe_matvec_{fmt}")
     return out
 
 
@@ -799,30 +817,25 @@ def moe_matvec_mxfp4(x, w_packed, w_scales, out=None, workspace=None):
     return _matvec("mxfp4", x, w_packed, w_scales, None, out, workspace)
 
 
+@functools.lru_cache(maxsize=None)
 def moe_experts_workspace_size(T, k, H, I):
     return int(_lib.moe_experts_workspace_size(T, k, H, I))
 
 
 def _experts(fmt, x, topk_idx, topk_w, gu, d, out, workspace):
-    T, H, step = _rows(x, (torch.bfloat16,), "x")
-    E, N, K, gu_args, layout = _few_weights(x, *gu, fmt, "w_gu_packed")
-    Ed, Nd, I, d_args, layout_d = _few_weights(x, *d, fmt, "w_d_packed")
-    if (Ed, Nd, 2 * I, K) != (E, H, N, H) or layout != layout_d:
+    T, H, x_at, step, dev = _rows(x, (torch.bfloat16,), "x")
+    E, N, K, layout, gu_args = _few_weights(*gu, fmt, "w_gu_packed", dev)
+    Ed, Nd, I, layout_d, d_args = _few_weights(*d, fmt, "w_d_packed", dev)
+    if Ed != E or Nd != H or 2 * I != N or K != H or layout != layout_d:
         raise ValueError(f"w_gu {E} x [{N}, {K}] and w_d {Ed} x [{Nd}, {I}] (one layout for both) do not fit x [{T}, {H}]")
     k = topk_idx.shape[-1]
-    _need(topk_idx, torch.int32, (T, k), "topk_idx")
-    _need(topk_w, torch.float32, (T, k), "topk_w")
-    _same_device(x, topk_idx, "topk_idx")
-    _same_device(x, topk_w, "topk_w")
     if out is None:
-        out = _empty((T, H), x.dtype, x.device)
-    else:
-        _need(out, x.dtype, (T, H), "out")
-        _same_device(x, out, "out")
-    ws = _few_workspace(x, moe_experts_workspace_size(T, k, H, I), workspace)
+        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    ws_at, ws_bytes, workspace = _few_workspace(moe_experts_workspace_size(T, k, H, I), workspace, x, dev)
     call = _lib.moe_experts_nvfp4 if fmt == "nvfp4" else _lib.moe_experts_mxfp4
-    _check(call(_ptr(x), step, _ptr(topk_idx), _ptr(topk_w), T, k, E, H, I, *gu_args, *d_args, layout, _ptr(out), _ptr(ws),
-                0 if ws is None else ws.numel(), _stream_of(x)), f"moe_experts_{fmt}")
+    _check(call(x_at, step, _dense(topk_idx, torch.int32, (T, k), "topk_idx", dev),
+                _dense(topk_w, torch.float32, (T, k), "topk_w", dev), T, k, E, H, I, *gu_args, *d_args, layout,
+                _dense(out, x.dtype, (T, H), "out", dev), ws_at, ws_bytes, _device_stream(dev)), f"moe_experts_{fmt}")
     return out
 
 

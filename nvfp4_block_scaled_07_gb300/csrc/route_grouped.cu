@@ -197,7 +197,7 @@ __device__ __noinline__ int choose_among(const RouteParams& p, int t, float top,
 // A lane's experts are VPL consecutive ones.  WHOLE: a lane's are all of one
 // group, and a group is a power of two of lanes.
 template <int VPL, bool WHOLE>
-__global__ void __launch_bounds__(32 * kWarps) route_grouped_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_kernel(const RouteParams p) {
   __shared__ float s_group[WHOLE ? 1 : kWarps][WHOLE ? 1 : 32 * VPL];
   __shared__ __align__(16) uint32_t s_key[kWarps][32];
   __shared__ uint32_t s_sorted[kWarps][36];

@@ -118,9 +118,10 @@ class TokenPlan:
 
 def alloc_token_plan(B, T, device, free_count=None):
     """Buffers for mla_plan(out=...); free_count: the caller's, updated in place."""
-    i32 = dict(dtype=torch.int32, device=device)
-    return TokenPlan(torch.empty(T, **i32), torch.empty(T, dtype=torch.int64, device=device), torch.empty(B + 1, **i32),
-                     torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32) if free_count is None else free_count)
+    empty, i32 = torch.empty, torch.int32
+    return TokenPlan(empty(T, dtype=i32, device=device), empty(T, dtype=torch.int64, device=device),
+                     empty(B + 1, dtype=i32, device=device), empty(B, dtype=i32, device=device),
+                     empty(B, dtype=i32, device=device), empty(1, dtype=i32, device=device) if free_count is None else free_count)
 
 
 def mla_plan(past_lens, new_lens, block_tables, free_pages, free_count, page_size, tokens, out=None):
@@ -146,15 +147,18 @@ def mla_plan(past_lens, new_lens, block_tables, free_pages, free_count, page_siz
     if (max_pages > 1 and step[1] != 1) or (B > 1 and step[0] < max_pages):
         raise ValueError(f"block_tables: strides {step}, rows must be contiguous and apart")
     free = free_pages.numel()
-    p = alloc_token_plan(B, tokens, past_lens.device) if out is None else out
+    if out is None:                           # what is made here needs no check
+        out = alloc_token_plan(B, tokens, past_lens.device)
+        at = [t.data_ptr() for t in (out.positions, out.slots, out.cu_seqlens, out.seq_lens, out.granted, out.free_count)]
+    else:
+        at = [_dense(out.positions, i32, (tokens,), "positions", dev), _dense(out.slots, torch.int64, (tokens,), "slots", dev),
+              _dense(out.cu_seqlens, i32, (B + 1,), "cu_seqlens", dev), _dense(out.seq_lens, i32, (B,), "seq_lens", dev),
+              _dense(out.granted, i32, (B,), "granted", dev), _dense(out.free_count, i32, (1,), "free_count_out", dev)]
     _b._check(_lib.mla_plan(
         past_at, _dense(new_lens, i32, (B,), "new_lens", dev), B, page_size, block_tables.data_ptr(),
         step[0] if B > 1 else max_pages, max_pages, _dense(free_pages, i32, (free,), "free_pages", dev), free,
-        _dense(free_count, i32, (1,), "free_count", dev), tokens, _dense(p.positions, i32, (tokens,), "positions", dev),
-        _dense(p.slots, torch.int64, (tokens,), "slots", dev), _dense(p.cu_seqlens, i32, (B + 1,), "cu_seqlens", dev),
-        _dense(p.seq_lens, i32, (B,), "seq_lens", dev), _dense(p.granted, i32, (B,), "granted", dev),
-        _dense(p.free_count, i32, (1,), "free_count_out", dev), _stream(dev)), "mla_plan")
-    return p
+        _dense(free_count, i32, (1,), "free_count", dev), tokens, *at, _stream(dev)), "mla_plan")
+    return out
 
 
 def mla_append(latent, k_rope, positions, slots, rope_table, cache, norm_weight=None, eps=1e-6, interleaved=True,

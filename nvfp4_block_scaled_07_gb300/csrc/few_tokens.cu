@@ -44,6 +44,7 @@ namespace {
 __device__ unsigned g_few_flags = 0;
 
 constexpr int kThreads = 256, kWarps = 8;
+constexpr int kMaxRows = 256;             // routed rows, T * k
 
 struct FewParams {
   const void* x;             // [T, K] of Source, or h [T * k, K] float32
@@ -142,6 +143,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   __shared__ uint32_t s_or[kWarps];
   __shared__ int s_sum[kWarps], s_first[kWarps];
   __shared__ float s_weight[32];
+  __shared__ int s_expert[MODE == kDown ? kMaxRows : 1], s_base[MODE == kDown ? kMaxRows : 1];  // the plan
+  __shared__ uint32_t s_tokens[MODE == kDown ? kMaxRows : 1];
+  __shared__ int s_of_row[MODE == kDown ? kMaxRows : 1];   // the plan's entry of a row of h, or -1
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -152,10 +156,13 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   int e = 0, base = 0, nseg = 1;
   uint32_t tokens = p.T == 32 ? kFull : (1u << p.T) - 1;
   if (MODE == kGateUp) {
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-      write_plan<kThreads>(p.idx, p.T, p.k, p.E, p.plan, &g_few_flags, reinterpret_cast<uint32_t*>(smem),
-                           reinterpret_cast<int*>(smem) + p.E);
     const int f = blockIdx.y, n = p.T * p.k;
+    if (f == n) {                              // blocks of their own for the down product's plan: one works
+      if (blockIdx.x == 0)
+        write_plan<kThreads>(p.idx, p.T, p.k, p.E, p.plan, &g_few_flags, reinterpret_cast<uint32_t*>(smem),
+                             reinterpret_cast<int*>(smem) + p.E);
+      return;
+    }
     e = p.idx[f];
     if (e < 0 || e >= p.E) return;             // write_plan raises the flag
     uint32_t bits = 0;
@@ -189,6 +196,12 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
     }
   } else if (MODE == kDown) {
     nseg = p.plan->nseg;
+    s_of_row[tid] = -1;
+    if (tid < nseg) s_expert[tid] = p.plan->expert[tid], s_base[tid] = p.plan->base[tid], s_tokens[tid] = p.plan->tokens[tid];
+    __syncthreads();
+    if (tid < nseg)
+      for (int i = 0; i < __popc(s_tokens[tid]); ++i) s_of_row[s_base[tid] + i] = tid;
+    __syncthreads();
   }
   const int units = nseg * steps;
 
@@ -200,25 +213,29 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   int step = wk, seg = 0;
   while (step >= steps) step -= steps, ++seg;
   Rows cur;
-  if (wk < units) load_rows<MX>(cur, p, l, MODE == kDown ? p.plan->expert[seg] : e, step);
+  if (wk < units) load_rows<MX>(cur, p, l, MODE == kDown ? s_expert[seg] : e, step);
 
   // Activations as float16: [step][piece j][token of the expert][16 bytes of 4 lane groups].
   const int rows = MODE == kDown ? p.T * p.k : p.T;   // an upper bound, also of a gate/up block's tokens
   float* factor = reinterpret_cast<float*>(smem + int64_t(rows) * steps * kUnitBytes);
-  for (int s = 0; s < nseg; ++s) {
-    const uint32_t who = MODE == kDown ? p.plan->tokens[s] : tokens;
-    const int first = MODE == kDown ? p.plan->base[s] : 0, m = __popc(who);
-    for (int i = warp; i < m * steps; i += kWarps) {
-      const int slot = i / steps, at = i - slot * steps;
-      const int row = MODE == kDown ? first + slot : int(__fns(who, 0, slot + 1));
-      float v[8];
-      load_block<SRC>(v, static_cast<const uint8_t*>(p.x) + row * p.x_stride * (SRC == kF32 ? 4 : 2), at, p.K, lane);
-      uint4 h;
-      const float f = block_to_half(v, &h);
-      uint8_t* dst = smem + (int64_t(first) * steps + int64_t(at) * m) * kUnitBytes;
-      *reinterpret_cast<uint4*>(dst + ((lane & 7) * m + slot) * 64 + (lane >> 3) * 16) = h;
-      if (lane == 0) factor[(first + slot) * steps + at] = f;
+  const int held = MODE == kDown ? rows : __popc(tokens);
+  for (int i = warp; i < held * steps; i += kWarps) {
+    const int r = i / steps, at = i - r * steps;
+    int row = r, slot = r, first = 0, m = held;
+    if (MODE == kDown) {
+      const int s = s_of_row[r];
+      if (s < 0) continue;
+      first = s_base[s], slot = r - first, m = __popc(s_tokens[s]);
+    } else if (MODE == kGateUp) {
+      row = int(__fns(tokens, 0, slot + 1));
     }
+    float v[8];
+    load_block<SRC>(v, static_cast<const uint8_t*>(p.x) + row * p.x_stride * (SRC == kF32 ? 4 : 2), at, p.K, lane);
+    uint4 h;
+    const float f = block_to_half(v, &h);
+    uint8_t* dst = smem + (first * steps + at * m) * kUnitBytes;
+    *reinterpret_cast<uint4*>(dst + ((lane & 7) * m + slot) * 64 + (lane >> 3) * 16) = h;
+    if (lane == 0) factor[r * steps + at] = f;
   }
   __syncthreads();
 
@@ -230,9 +247,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
     int nstep = step + p.wk, next = seg;
     while (nstep >= steps) nstep -= steps, ++next;
     Rows nxt;
-    if (u + p.wk < units) load_rows<MX>(nxt, p, l, MODE == kDown ? p.plan->expert[next] : e, nstep);
+    if (u + p.wk < units) load_rows<MX>(nxt, p, l, MODE == kDown ? s_expert[next] : e, nstep);
 
-    if (MODE == kDown) tokens = p.plan->tokens[seg], base = p.plan->base[seg];
+    if (MODE == kDown) tokens = s_tokens[seg], base = s_base[seg];
     const int m = __popc(tokens);
     // this lane's column: token g
     const bool has = (tokens >> g) & 1;
@@ -353,15 +370,21 @@ int64_t steps_of(int K) { return (K + kStep - 1) / kStep; }
 int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
 int64_t self_bytes(int64_t rows, int K) { return rows * steps_of(K) * (kUnitBytes + 4); }
 
-// What this file takes; the rest streams.  Every block holds the activations
-// that it needs, and converts them itself.
+// What this file takes; few_stream.cu takes the rest.  Every block converts
+// all activations that it needs, so its work grows with the tokens twice.
+// Measured (us here, us there): one token x [512, 2048] 3.6, 7.5, x [4096,
+// 4096] 6.0, 8.2, x [6144, 8192] 13.8, 11.7; four tokens x [512, 2048] 6.1,
+// 7.8, x [1024, 4096] 10.4, 8.0; one token through 8 experts of [1024, 2048]
+// 17, 19, of [2048, 2048] 27, 22.
 constexpr int64_t kSelfBytes = 64 * 1024;
 constexpr int kSmallTokens = 8;
-constexpr int64_t kSmallWeights = int64_t(1) << 23;
-bool takes_matvec(int T, int N, int K) { return T <= kSmallTokens && self_bytes(T, K) <= kSelfBytes && int64_t(N) * K <= kSmallWeights; }
+constexpr int64_t kMatvecWork = int64_t(1) << 25, kExpertsWork = int64_t(1) << 24;
+bool takes_matvec(int T, int N, int K) {
+  return T <= kSmallTokens && self_bytes(T, K) <= kSelfBytes && int64_t(T) * T * N * K <= kMatvecWork;
+}
 bool takes_experts(int T, int k, int H, int I) {
-  return T <= kSmallTokens && self_bytes(T, H) <= kSelfBytes && self_bytes(int64_t(T) * k, I) <= kSelfBytes &&
-         int64_t(T) * k * 2 * I * H <= kSmallWeights;
+  return T <= kSmallTokens && T * k <= kMaxRows && self_bytes(T, H) <= kSelfBytes && self_bytes(int64_t(T) * k, I) <= kSelfBytes &&
+         int64_t(T) * T * k * 2 * I * H <= kExpertsWork;
 }
 
 template <bool MX, int SRC, int MODE>
@@ -429,7 +452,7 @@ cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* i
   p.next_gscale = d.gscale;
   p.out = h;
   p.wk = 8;
-  dim3 grid(unsigned(d.K / (16 * (kWarps / p.wk))), unsigned(T * k));
+  dim3 grid(unsigned(d.K / (16 * (kWarps / p.wk))), unsigned(T * k + 1));
   const cudaError_t err = gu.mx ? launch_few<true, kBf16, kGateUp>(p, T, grid, st) : launch_few<false, kBf16, kGateUp>(p, T, grid, st);
   if (err != cudaSuccess) return err;
 

@@ -190,8 +190,9 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const uint8_t* x,
 }
 
 // The experts of at most 32 ids, in ascending order, by one warp: their number,
-// and (unless null) the list.  What the plan says, without waiting for it.
-__device__ __forceinline__ int experts_of_warp(const int32_t* idx, int n, int E, int lane, int* list) {
+// and (unless null) the list and their tokens.  What the plan says, without waiting for it.
+__device__ __forceinline__ int experts_of_warp(const int32_t* idx, int T, int k, int E, int lane, int* list, uint32_t* tokens) {
+  const int n = T * k;
   const int e = lane < n ? __ldcg(idx + lane) : -1;
   const uint32_t same = __match_any_sync(kFull, e);
   const bool first = e >= 0 && e < E && __ffs(same) - 1 == lane;
@@ -202,7 +203,9 @@ __device__ __forceinline__ int experts_of_warp(const int32_t* idx, int n, int E,
       const int other = __shfl_sync(kFull, e, i);
       at += ((leaders >> i) & 1) && other < e;
     }
-    if (first) list[at] = e;
+    uint32_t mine = 0;
+    for (int t = 0; t < T; ++t) mine |= uint32_t((same & (((k < 32 ? 1u << k : 0u) - 1) << (t * k))) != 0) << t;
+    if (first) list[at] = e, tokens[at] = mine;
     __syncwarp();
   }
   return __popc(leaders);
@@ -280,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   __shared__ __align__(8) uint64_t s_full[kMaxStages], s_ready[kMaxStages], s_empty[kMaxStages], s_acc[2 * kBuffers + 1];
   __shared__ mla::WaitCtl s_ctl;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_last, s_expert[32];
+  __shared__ int s_last, s_expert[2][32];      // of each producer
+  __shared__ uint32_t s_tokens[32];
   uint8_t* smem = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = mla::uniform(tid >> 5);
   const uint32_t full = ptx::smem_u32(s_full), ready = ptx::smem_u32(s_ready), empty = ptx::smem_u32(s_empty);
@@ -315,14 +319,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   // The kernel before is one of the same call, a prepare_kernel, which lets the
   // next be launched after its own wait: what was there before it (weights,
   // ids, for the down product the plan) can be read before this kernel's wait (from L2).
-  const bool producer = warp == 0;
+  const bool producer = warp <= kTermWarp;
   const bool early = MODE != kGateUp || p.T * p.k <= 32;   // the experts are known before the wait
   if (!producer || !early) {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
   }
   const int nseg = MODE == kDense ? 1
-                   : MODE == kGateUp && early ? experts_of_warp(p.idx, p.T * p.k, p.E, lane, producer ? s_expert : nullptr)
+                   : MODE == kGateUp && early ? experts_of_warp(p.idx, p.T, p.k, p.E, lane, producer ? s_expert[warp] : nullptr, s_tokens)
                                               : __ldcg(&p.plan->nseg);
   const int steps = (p.K + kStep - 1) / kStep, seg_tiles = MODE == kGateUp ? p.N / kTileRows : 1;
   const int tiles = MODE == kGateUp ? nseg * seg_tiles : p.N / kTileRows;
@@ -345,9 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   };
 
   if (MODE == kDown && nseg == 0) {            // no token has an expert
-    constexpr int kOthers = kThreads - 32;     // the producer has not waited
+    constexpr int kOthers = kThreads - 64;     // the producers have not waited
     if (!producer)
-      for (int64_t i = int64_t(blockIdx.x) * kOthers + tid - 32; i < int64_t(p.T) * p.N; i += int64_t(gridDim.x) * kOthers)
+      for (int64_t i = int64_t(blockIdx.x) * kOthers + tid - 64; i < int64_t(p.T) * p.N; i += int64_t(gridDim.x) * kOthers)
         static_cast<uint16_t*>(p.out)[i] = 0;
   } else if (warp == 0) {
     // ---- weights and their scales, the first stages before the wait
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     bool ok = true;
     for (int64_t s = start; s < end && ok;) {
       const Unit u = unit_at(s);
-      const int e = mla::uniform(MODE == kDense ? 0 : MODE == kGateUp && early ? s_expert[u.seg] : __ldcg(p.plan->expert + u.seg));
+      const int e = mla::uniform(MODE == kDense ? 0 : MODE == kGateUp && early ? s_expert[0][u.seg] : __ldcg(p.plan->expert + u.seg));
       const int in = MODE == kGateUp ? u.tile - u.seg * seg_tiles : u.tile;
       const int blk = mla::uniform(e * blocks + (MODE == kGateUp ? in >> 1 : in)), half = mla::uniform(in & 1);
       for (int i = 0; i < u.n; ++i, ++count) {
@@ -393,8 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     bool ok = true;
     for (int64_t s = start; s < end && ok;) {
       const Unit u = unit_at(s);
-      const uint32_t tokens = mla::uniform(MODE == kDense ? 0 : p.plan->tokens[u.seg]);
-      const int base = mla::uniform(MODE == kDown ? p.plan->base[u.seg] : 0), m = MODE == kDense ? p.T : __popc(tokens);
+      const uint32_t tokens = mla::uniform(MODE == kDense ? 0 : MODE == kGateUp && early ? s_tokens[u.seg]
+                                                                                         : __ldcg(p.plan->tokens + u.seg));
+      const int base = mla::uniform(MODE == kDown ? __ldcg(p.plan->base + u.seg) : 0), m = MODE == kDense ? p.T : __popc(tokens);
+      if (s == start) ptx::grid_dep_wait();    // the terms are the kernel before's
       for (int i = 0; i < u.n; ++i, ++count) {
         ok = mla::wait_warp(empty + 8 * st, parity, &s_ctl);
         if (!ok) break;
@@ -513,6 +519,21 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       // lane i: slot i's token and the scale of its row of activations
       const int token = MODE == kDense || lane >= m ? lane : int(__fns(tokens, 0, lane + 1));
       const float scale = lane < m ? p.row_scale[MODE == kDown ? base + lane : token] : 0.0f;
+      float w = 0.0f, ws = 1.0f;               // lane i: slot i's weight of this expert, with the next matrix's scale
+      if (MODE == kGateUp) {
+        const int e = p.plan->expert[u.seg];
+        if (p.gscale) ws = p.gscale[e];
+        const float next = p.next_gscale ? p.next_gscale[e] : 1.0f;
+        if (lane < m)
+          for (int j = 0; j < p.k; ++j) {
+            const int is = p.idx[token * p.k + j];
+            const float x = p.topk_w[token * p.k + j];
+            w += is == e ? x : 0.0f;
+          }
+        w *= next;
+      } else if (MODE == kDense && p.gscale) {
+        ws = p.gscale[0];
+      }
       if (MODE == kDown && s == tile_first)
         for (int t = 0; t < p.T; ++t) total[t * kTileRows] = 0.0f;
       const uint32_t buffer = n % kBuffers;
@@ -587,13 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         }
       }
       if (MODE == kGateUp) {
-        const int I = p.N / 2, in = u.tile - u.seg * seg_tiles, e = p.plan->expert[u.seg];
-        const float ws = p.gscale ? p.gscale[e] : 1.0f;
-        float w = 0.0f;                        // lane i: slot i's weight of this expert, and the next matrix's scale
-        if (lane < m)
-          for (int j = 0; j < p.k; ++j)
-            if (p.idx[token * p.k + j] == e) w += p.topk_w[token * p.k + j];
-        w *= p.next_gscale ? p.next_gscale[e] : 1.0f;
+        const int I = p.N / 2, in = u.tile - u.seg * seg_tiles;
         // rows 32 q + j are gate's, 32 q + 16 + j up's
         const int col = (in >> 1) * 128 + 32 * quarter + 16 * (in & 1) + lane;
         for (int i = 0; i < m; ++i) {
@@ -601,7 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
           if (lane < 16) static_cast<float*>(p.out)[int64_t(base + i) * I + col] = gate / (1.0f + expf(-gate)) * up * wi;
         }
       } else {
-        const float ws = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
         for (int t = 0; t < p.T; ++t) {
           const float v = total[t * kTileRows] * ws;
           const int64_t o = int64_t(t) * p.N + u.tile * kTileRows + row;

@@ -91,6 +91,8 @@ int moe_matvec_mxfp4(const void* x, int64_t x_stride, int T, int x_dtype,
                      const uint8_t* w_packed, const uint8_t* w_scales,
                      int N, int K, int w_layout, void* out, void* ws, size_t ws_bytes, cudaStream_t stream);
 size_t moe_experts_workspace_size(int T, int k, int H, int I);
+/* Kernels that a call launches: 0 (T = 0), 2 or 4. */
+int moe_experts_launches(int T, int k, int H, int I);
 int moe_experts_nvfp4(const void* x_bf16, int64_t x_stride, const int32_t* topk_idx, const float* topk_w,
                       int T, int k, int E, int H, int I,
                       const uint8_t* w_gu_packed, const uint8_t* w_gu_scales, const float* w_gu_gscale,

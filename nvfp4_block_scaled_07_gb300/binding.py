@@ -89,6 +89,7 @@ _FEW_SIGS = {
     "moe_matvec_nvfp4": (_i, [_p, _i64, _i, _i, _p, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
     "moe_matvec_mxfp4": (_i, [_p, _i64, _i, _i, _p, _p, _i, _i, _i, _p, _p, _sz, _p]),
     "moe_experts_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_experts_launches": (_i, [_i, _i, _i, _i]),
     "moe_experts_nvfp4": (_i, [_p, _i64, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _i, _p, _p, _sz, _p]),
     "moe_experts_mxfp4": (_i, [_p, _i64, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _i, _p, _p, _sz, _p]),
 }
@@ -874,17 +875,32 @@ class MoELayer:
     times the candidate plans (autotune()) on that batch and keeps the
     fastest for the batch size: it synchronises the stream, so make that
     first call outside stream capture.  Otherwise each GEMM is one launch
-    with the given tile_n."""
+    with the given tile_n.
+
+    n_group, topk_group, group_best, select_bias and routed_scale route with
+    moe_route_grouped (the six separate calls then, not the fused prepare);
+    they exclude `bias` and k_primary.  Batches of up to few_tokens tokens (at
+    most FEW_MAX_TOKENS; 0: none) run as route and moe_experts_*: the same
+    weights with 16-bit activations, so closer to the unquantised layer than
+    the larger batches' results, and without the steps below."""
 
     def __init__(self, w_gu, w_d, k, score_fn="sigmoid", renormalize=True, h_scale=2.0 ** -4, bias=None,
                  T=None, tile_n=(0, 0), fused_prepare=True, k_primary=None, fmt="nvfp4", dynamic_schedule=True,
-                 tiled_weights=True, autotune=True, fused_finalize=False):
+                 tiled_weights=True, autotune=True, fused_finalize=False, select_bias=None, n_group=1, topk_group=1,
+                 group_best=2, routed_scale=1.0, few_tokens=0):
         if fmt not in ("nvfp4", "mxfp4"):
             raise ValueError(f"fmt {fmt}")
         self.fmt = fmt
+        self.grouped = n_group != 1 or select_bias is not None or routed_scale != 1.0
+        if self.grouped and (bias is not None or (k_primary is not None and k_primary < k)):
+            raise ValueError("groups, select_bias and routed_scale exclude bias and k_primary")
+        if not 0 <= few_tokens <= FEW_MAX_TOKENS:
+            raise ValueError(f"few_tokens {few_tokens} outside [0, {FEW_MAX_TOKENS}]")
+        self.select_bias, self.n_group, self.topk_group, self.group_best = select_bias, n_group, topk_group, group_best
+        self.routed_scale, self.few_tokens = float(routed_scale), int(few_tokens)
         # one zeroed tile-scheduler workspace for both GEMMs (they run in sequence)
         self.g_ws = alloc_gemm_workspace(w_gu.device) if dynamic_schedule else None
-        self.fused_prepare = bool(fused_prepare)
+        self.fused_prepare = bool(fused_prepare) and not self.grouped
         # batch-aware routing when k_primary < k (moe_route_batch_aware)
         self.k_primary = k if k_primary is None else int(k_primary)
         self.E, two_i, self.H = w_gu.shape
@@ -924,12 +940,17 @@ class MoELayer:
         self.T = T
         self.topk_idx = _empty((T, k), torch.int32, dev)
         self.topk_w = _empty((T, k), torch.float32, dev)
+        self.r_ws = _empty((int(_lib.moe_route_batch_aware_workspace_size(E)),), torch.uint8, dev)
+        self.out = _empty((T, H), torch.bfloat16, dev)
+        self.few = T <= self.few_tokens
+        self.few_ws = _empty((moe_experts_workspace_size(T, k, H, I),), torch.uint8, dev) if self.few and T else None
+        if self.few:
+            return
         self.x_gscale = _empty((1,), torch.float32, dev)
         self.xq = _empty((T, H // 2), torch.uint8, dev)
         self.xs = _empty((T, H // (32 if self.fmt == "mxfp4" else 16)), torch.uint8, dev)
         self.q_ws = _empty((max(1, int(_lib.moe_quantize_nvfp4_workspace_size(T, H, QUANT_COMPUTE_GLOBAL))),),
                            torch.uint8, dev)
-        self.r_ws = _empty((int(_lib.moe_route_batch_aware_workspace_size(E)),), torch.uint8, dev)
         self.perm = alloc_permutation(T, E, k, H, dev, self.fmt)
         self.p_ws = _empty((moe_permute_workspace_size(T, E, k),), torch.uint8, dev)
         self.prep_ws = alloc_prepare_workspace(T, E, k, dev)
@@ -938,11 +959,12 @@ class MoELayer:
         self.hs = _empty((blocked_scales_bytes(cap, I, self.fmt),), torch.uint8, dev)
         self.y = None if self.fused_finalize else _empty((cap, H), torch.bfloat16, dev)
         self.acc = torch.zeros((T, H), dtype=torch.float32, device=dev) if self.fused_finalize else None
-        self.out = _empty((T, H), torch.bfloat16, dev)
 
     # ---- the steps of forward() (bench.py times them one by one) ----
     def prepare(self, x, logits):
         """a1-a3: routing, quantisation of x and the permutation."""
+        if self.few:
+            raise ValueError(f"a batch of {self.T} tokens (few_tokens {self.few_tokens}) has no separate steps")
         p = self.perm
         if self.fmt == "mxfp4":
             if self.fused_prepare:
@@ -1015,6 +1037,8 @@ class MoELayer:
         T = x.shape[0]
         if self.T != T:
             self._alloc(T)
+        if self.few:
+            return self._forward_few(x, logits, out)
         if self.autotune_enabled and T not in self.plans:
             self.autotune(x, logits)
         self.prepare(x, logits)
@@ -1023,6 +1047,15 @@ class MoELayer:
         return self.finalize(out)
 
     __call__ = forward
+
+    def _forward_few(self, x, logits, out=None):
+        out = self.out if out is None else out
+        self._route(logits)
+        if self.fmt == "mxfp4":
+            return moe_experts_mxfp4(x, self.topk_idx, self.topk_w, self.w_gu_packed, self.w_gu_scales, self.w_d_packed,
+                                     self.w_d_scales, out=out, workspace=self.few_ws)
+        return moe_experts_nvfp4(x, self.topk_idx, self.topk_w, self.w_gu_packed, self.w_gu_scales, self.w_gu_gscale,
+                                 self.w_d_packed, self.w_d_scales, self.w_d_gscale, out=out, workspace=self.few_ws)
 
     def capture(self, x, logits, stream=None):
         """Captures one forward() on the tensors x and logits into a CUDA
@@ -1036,7 +1069,7 @@ class MoELayer:
         T = x.shape[0]
         if self.T != T:
             self._alloc(T)
-        if self.autotune_enabled and T not in self.plans:
+        if self.autotune_enabled and T not in self.plans and not self.few:
             self.autotune(x, logits)
         side = torch.cuda.Stream(device=self.device) if stream is None else stream
         side.wait_stream(torch.cuda.current_stream(self.device))
@@ -1104,16 +1137,21 @@ class MoELayer:
         return report
 
     def _route(self, logits):
-        if self.k_primary < self.k:
+        if self.grouped:
+            moe_route_grouped(logits, self.k, self.score_fn, self.renormalize, self.select_bias, self.n_group,
+                              self.topk_group, self.group_best, self.routed_scale, self.topk_idx, self.topk_w)
+        elif self.k_primary < self.k:
             moe_route_batch_aware(logits, self.k, self.k_primary, self.score_fn, self.renormalize, self.bias,
                                   self.topk_idx, self.topk_w, workspace=self.r_ws)
         else:
             moe_route_topk(logits, self.k, self.score_fn, self.renormalize, self.bias, self.topk_idx, self.topk_w)
 
     # kernels launched by one forward(): fused prepare 1 (else route 1-2, quantise 1-2, permute 3),
-    # one per launch of each GEMM plan, finalize 1
+    # one per launch of each GEMM plan, finalize 1; few tokens: route 1-2, experts 2-4
     @property
     def launches_per_forward(self):
+        if self.few:
+            return (2 if self.k_primary < self.k else 1) + int(_lib.moe_experts_launches(self.T, self.k, self.H, self.I))
         gu, down = self.plan()
         if self.fused_prepare:
             head = 1

@@ -774,6 +774,11 @@ size_t moe_experts_workspace_size(int T, int k, int H, int I) {
   return few_experts_workspace_bytes(T, k, H, I);
 }
 
+int moe_experts_launches(int T, int k, int H, int I) {
+  if (T < 1 || T > kFewMaxTokens || k < 1 || k > 32 || H < 1 || I < 1) return 0;
+  return few_experts_launches(T, k, H, I);
+}
+
 static int experts_common(const void* x, int64_t x_stride, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,
                           int I, const FewMatrix& gu, const FewMatrix& dn, int w_layout, void* out, void* ws,
                           size_t ws_bytes, cudaStream_t stream) {

@@ -422,6 +422,8 @@ size_t few_experts_workspace_bytes(int T, int k, int H, int I) {
   return size_t(round256(sizeof(Plan)) + int64_t(T) * k * I * 4);
 }
 
+int few_experts_launches(int T, int k, int H, int I) { return takes_experts(T, k, H, I) ? 2 : 4; }
+
 cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
                               int num_sms, cudaStream_t st) {
   if (!takes_matvec(T, w.N, w.K)) return launch_stream_matvec(x, x_stride, T, fp16, w, out, ws, num_sms, st);

@@ -161,6 +161,7 @@ struct FewMatrix {
 constexpr int kFewMaxGrid = 160;
 size_t few_matvec_workspace_bytes(int T, int N, int K);
 size_t few_experts_workspace_bytes(int T, int k, int H, int I);
+int few_experts_launches(int T, int k, int H, int I);
 // x [T, K] 16-bit, rows x_stride elements apart; out [T, N]; 1 <= T <= 32.
 cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16, const FewMatrix& w, void* out, void* ws,
                               int num_sms, cudaStream_t st);

@@ -76,6 +76,14 @@ __device__ __forceinline__ F warp_sum(F v) {
   return v;
 }
 
+// Whether all of a token's logits are equal, and the biases too (a padded token's, often): then the order is that of indexes.
+__device__ __noinline__ bool all_alike(const RouteParams& p, const float* row, int lane) {
+  bool same = true;
+  for (int e = lane; e < p.E; e += 32)
+    same = same && clean(row[e]) == clean(row[0]) && (!p.bias || clean(p.bias[e]) == clean(p.bias[0]));
+  return __all_sync(kFull, same);
+}
+
 // ---- the choice in float64 ------------------------------------------------------
 // Keys that order like doubles, compared as integers.
 __device__ __forceinline__ uint64_t key_of(double d) {
@@ -119,16 +127,18 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, int t, float to
     if (y > x || (y == x && f < e)) x = y, e = f;
   };
   if (p.groups > 1) {
+    int of[VPL];
+    for (int i = 0; i < VPL; ++i) of[i] = (lane * VPL + i) / per;
     double mine = -INFINITY;                  // lane g: group g's value
     for (int g = 0; g < p.groups; ++g) {
       uint64_t best = 0, second = 0;
       int e1 = INT_MAX, e2 = INT_MAX;
       for (int i = 0; i < VPL; ++i)
-        if (key[i] && (lane * VPL + i) / per == g) better(best, e1, key[i], lane * VPL + i);
+        if (key[i] && of[i] == g) better(best, e1, key[i], lane * VPL + i);
       for (int d = 16; d; d >>= 1) better(best, e1, __shfl_xor_sync(kFull, best, d), __shfl_xor_sync(kFull, e1, d));
       if (p.best == 2) {
         for (int i = 0; i < VPL; ++i)
-          if (key[i] && (lane * VPL + i) / per == g && lane * VPL + i != e1) better(second, e2, key[i], lane * VPL + i);
+          if (key[i] && of[i] == g && lane * VPL + i != e1) better(second, e2, key[i], lane * VPL + i);
         for (int d = 16; d; d >>= 1) better(second, e2, __shfl_xor_sync(kFull, second, d), __shfl_xor_sync(kFull, e2, d));
       }
       if (lane == g) mine = p.best == 2 ? value_of(best) + value_of(second) : value_of(best);
@@ -142,7 +152,7 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, int t, float to
     const uint32_t kept = __ballot_sync(kFull, lane < p.groups && rank < p.keep);
     for (int i = 0; i < VPL; ++i) {
       const int e = lane * VPL + i;
-      if (e < p.E && !((kept >> (e / per)) & 1)) key[i] = 0;
+      if (e < p.E && !((kept >> of[i]) & 1)) key[i] = 0;
     }
   }
   int my_e = 0;
@@ -159,20 +169,20 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, int t, float to
   return my_e;
 }
 
-// Whether group `lane`, whose value is that of experts e1 and e2, is one of the best.
+// Of `count` groups, the j-th's value that of experts e of lanes 2 j and 2 j + 1: bit 2 j, whether it is among the `places` best.
 template <int VPL>
-__device__ __noinline__ bool keeps_exactly(const RouteParams& p, int t, float top, int lane, int e1, int e2) {
+__device__ __noinline__ uint32_t among_near(const RouteParams& p, int t, float top, int lane, int e, int count, int places) {
   const float* row = p.logits + int64_t(t) * p.E;
   const double sum = p.softmax ? softmax_sum<VPL>(row, p.E, top, lane) : 0.0;
-  double v = exact_score(p, row, e1, top, sum);
-  if (p.best == 2) v += exact_score(p, row, e2, top, sum);
-  const uint64_t value = lane < p.groups ? key_of(v) : 0;
+  double v = exact_score(p, row, e, top, sum);
+  if (p.best == 2) v += __shfl_xor_sync(kFull, v, 1);
+  const uint64_t value = key_of(v);
   int rank = 0;
-  for (int g = 0; g < p.groups; ++g) {
-    const uint64_t other = __shfl_sync(kFull, value, g);
-    rank += other > value || (other == value && g < lane);
+  for (int j = 0; j < count; ++j) {
+    const uint64_t other = __shfl_sync(kFull, value, 2 * j);
+    rank += other > value || (other == value && 2 * j < lane);
   }
-  return lane < p.groups && rank < p.keep;
+  return __ballot_sync(kFull, rank < places);
 }
 
 // Among at most 32 candidates, in ascending order in `from`: the k best.
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
 #pragma unroll
   for (int i = 1; i < VPL; ++i) local = max(local, key[i]);
 
-  bool sure = true, open = true;              // open (WHOLE): the lane's group is kept
+  bool alike = false, sure = true, open = true;              // open (WHOLE): the lane's group is kept
   if (p.groups > 1) {
     float value, size;                        // of group g, in lane g (not WHOLE) or the group's lanes; |c| of its parts
     const int lanes = WHOLE ? per / VPL : 1;
@@ -312,34 +322,43 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
       size = __shfl_sync(kFull, size, (lane * lanes) & 31);
       size = __uint_as_float(__reduce_max_sync(kFull, lane < p.groups ? __float_as_uint(size) : 0u));
       const float span = 2.0f * (p.best * error + 0x1p-23f * size);       // the parts' rounding and the sum's
-      if (!(low - high > span)) {
-        int e1 = 0, e2 = 0;                   // of group `lane`: the experts of its value
-        bool clear = true;                    // and whether float32 tells which they are
-        for (int g = 0; g < p.groups; ++g) {
-          uint32_t m[3];
-          int e[3];
-          uint32_t used = 0;
+      if (!(low - high > span) && !(alike = all_alike(p, row, lane))) {
+        // Exact values of those that the order of float32 values leaves open, for the places
+        // that the others do not take: lanes 2 j and 2 j + 1 take the j-th one's two experts.
+        const uint32_t near = __ballot_sync(kFull, lane < p.groups && (is_kept ? mine <= high + span : mine >= low - span));
+        const int places = __popc(__ballot_sync(kFull, is_kept) & near), count = __popc(near);
+        sure = count <= 16;
+        int e = 0;
+        if (sure) {
+          int j = 0;
+#pragma unroll 1
+          for (uint32_t rest = near; rest; rest &= rest - 1, ++j) {
+            const int g = __ffs(rest) - 1;
+            uint32_t used = 0, last = 0, m = 0;
+#pragma unroll 1
+            for (int n = 0; n <= p.best; ++n) {
+              uint32_t largest = 0;
+              int at = 0;
 #pragma unroll
-          for (int n = 0; n < 3; ++n) {
-            uint32_t local = 0;
-            int at = 0;
-#pragma unroll
-            for (int i = VPL - 1; i >= 0; --i)
-              if (key[i] != 0u && key[i] >= local && !((used >> i) & 1) && (e0 + i) / per == g) local = key[i], at = i;
-            m[n] = __reduce_max_sync(kFull, local);
-            const int from = __ffs(__ballot_sync(kFull, local == m[n])) - 1;
-            e[n] = __shfl_sync(kFull, e0 + at, from);
-            if (lane == from) used |= 1u << at;
-          }
-          if (lane == g) {
-            e1 = e[0], e2 = e[1];
-            const uint32_t next = p.best == 2 ? m[2] : m[1];
-            clear = next == 0u || value_of(p.best == 2 ? m[1] : m[0]) - value_of(next) > span;
+              for (int i = VPL - 1; i >= 0; --i)
+                if (key[i] >= max(largest, 1u) && !((used >> i) & 1) && (WHOLE ? lane / lanes : (e0 + i) / per) == g)
+                  largest = key[i], at = i;
+              last = m;
+              m = __reduce_max_sync(kFull, largest);
+              const int from = __ffs(__ballot_sync(kFull, largest == m)) - 1;
+              const int expert = __shfl_sync(kFull, e0 + at, from);
+              if (lane == from) used |= 1u << at;
+              if (n < p.best && lane == 2 * j + n) e = expert;
+            }
+            // and whether float32 tells which experts they are
+            sure = sure && (m == 0u || value_of(last) - value_of(m) > span);
           }
         }
-        const bool near = lane < p.groups && mine <= low + span && mine >= high - span;
-        sure = __ballot_sync(kFull, near && !clear) == 0u;
-        is_kept = keeps_exactly<VPL>(p, t, top, lane, e1, e2);
+        if (sure) {
+          const uint32_t in = among_near<VPL>(p, t, top, lane, e, count, places);
+          const int j = __popc(near & ((1u << lane) - 1));
+          if ((near >> lane) & 1) is_kept = (in >> (2 * j)) & 1;
+        }
       }
     }
     const uint32_t kept = __ballot_sync(kFull, is_kept);
@@ -379,8 +398,11 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
   }
   const int candidates = __shfl_sync(kFull, at, 31);
   int my_e = 0;
-  float last;                                 // the k-th best
-  if (candidates <= 32) {
+  float last = 0.0f;                          // the k-th best
+  if (candidates > 32 && !alike) alike = all_alike(p, row, lane);
+  if (alike) {
+    my_e = lane;
+  } else if (candidates <= 32) {
     s_key[warp][lane] = 0u;
     if (lane < 4) s_sorted[warp][32 + lane] = 0u;
     s_sorted[warp][lane] = 0u;

@@ -9,6 +9,8 @@ Bounds, element by element, with u = eps / 2 of the 16-bit result type:
 The experts' h carries the errors of gate and up (a silu's slope is below 1.1), the exponential's 2^-21 and its own
 rounding to 11 bits, 2^-11 |h|; each goes through |W_d| and the token's weight.
 """
+import itertools
+
 import torch
 
 E2M1 = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
@@ -87,8 +89,9 @@ def check(got, ref, tol, what=""):
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((err / tol).nan_to_num(1e9).max()):.2f} x its bound"
 
 
-def route(logits, bias, k, score_fn, renorm, n_group, topk_group, group_best, scale):
-    """One token: (indices, weights, value of each choice) in float64 by repeated search."""
+def route(logits, bias, k, score_fn, renorm, n_group, topk_group, group_best, scale, kept=None):
+    """One token: (indices, weights) in float64 by repeated search.  `kept` takes other groups than the best: of those that
+    float64 cannot tell apart (groups_that_tie)."""
     v = [(-float("inf") if x != x else min(x, 3.4028234663852886e38)) for x in logits.double().tolist()]
     t = torch.tensor(v, dtype=torch.float64)
     if score_fn == "sigmoid":
@@ -108,12 +111,29 @@ def route(logits, bias, k, score_fn, renorm, n_group, topk_group, group_best, sc
     for g in range(n_group):
         part = sorted(c[g * per:(g + 1) * per], reverse=True)
         value.append(part[0] + (part[1] if group_best == 2 and n_group > 1 else 0.0))
-    kept = sorted(range(n_group), key=lambda g: (-value[g], g))[:topk_group]
+    if kept is None:
+        kept = sorted(range(n_group), key=lambda g: (-value[g], g))[:topk_group]
+    elif kept == "values":
+        return value, s.tolist(), c
     cand = sorted((e for e in range(E) if e // per in kept), key=lambda e: (-c[e], e))[:k]
     w = s[cand]
     if renorm:
         w = w / w.sum() if float(w.sum()) > 0 else torch.zeros_like(w)
     return cand, (w * scale).tolist()
+
+
+def groups_that_tie(logits, bias, k, score_fn, renorm, n_group, topk_group, group_best, scale):
+    """Every choice of groups that float64 allows.  A group's value is the sum of two c = s + b: three roundings of 2^-53 of
+    the parts, and s is itself off, a sigmoid by 4 such steps (exp, sum, quotient), a softmax by that and the E - 1 additions
+    of its sum in whatever order.  Values that differ by less than both sides' errors (1 and 2: sums such as (s + 3) + (z - 2)
+    and (s + 1) + z are equal but round apart) may go either way."""
+    value, s, c = route(logits, bias, k, score_fn, renorm, n_group, topk_group, group_best, scale, kept="values")
+    E, size = len(c), 2.0 * max(abs(x) for x in c if abs(x) < float("inf")) if any(abs(x) < float("inf") for x in c) else 0.0
+    off = 2.0 ** -53 * (2.0 * (4 + (E if score_fn == "softmax" else 0)) * max(s) + 3.0 * size)
+    edge = sorted(value, reverse=True)[topk_group - 1]
+    inside = [g for g in range(n_group) if value[g] > edge + 2 * off]
+    near = [g for g in range(n_group) if abs(value[g] - edge) <= 2 * off]
+    return [inside + list(some) for some in itertools.combinations(near, topk_group - len(inside))] if len(near) <= 12 else []
 
 
 def plan(past, new, tables, free_pages, count, page, T):

@@ -325,9 +325,14 @@ def check_route(B, logits, bias, k, **kw):
     idx, w = B.moe_route_grouped(logits.cuda(), k, select_bias=None if bias is None else bias.cuda(), **kw)
     B.sync_status()
     args = dict(score_fn="sigmoid", renormalize=True, n_group=1, topk_group=1, group_best=2, scale=1.0) | kw
+    args["renorm"] = args.pop("renormalize")
     for t in range(logits.shape[0]):
-        ri, rw = R.route(logits[t], bias, k, args["score_fn"], args["renormalize"], args["n_group"], args["topk_group"],
-                         args["group_best"], args["scale"])
+        ri, rw = R.route(logits[t], bias, k, **args)
+        if idx[t].tolist() != ri and args["n_group"] > 1:       # another of the choices that float64 leaves open?
+            for kept in R.groups_that_tie(logits[t], bias, k, **args):
+                oi, ow = R.route(logits[t], bias, k, **args, kept=kept)
+                if oi == idx[t].tolist():
+                    ri, rw = oi, ow
         assert idx[t].tolist() == ri, (t, idx[t].tolist(), ri)
         ref = torch.tensor(rw, dtype=torch.float64)
         assert ((w[t].double().cpu() - ref).abs() <= 1e-6 * ref.abs() + 1e-37).all(), (t, w[t].tolist(), rw)
@@ -360,6 +365,20 @@ def test_route_of_near_and_exact_ties(B, score_fn):
     for bias in (None, torch.zeros(64), torch.full((64,), 0.125), (torch.arange(64) % 4) * 0.25):
         for groups, keep, best in ((1, 1, 1), (8, 3, 2), (8, 3, 1)):
             check_route(B, logits, bias, 8, score_fn=score_fn, n_group=groups, topk_group=keep, group_best=best)
+
+
+@pytest.mark.parametrize("E,k,n_group,topk_group,group_best", [(256, 8, 8, 4, 2), (256, 6, 8, 3, 1), (60, 4, 6, 3, 2), (96, 9, 32, 20, 2),
+                                                              (128, 8, 32, 3, 2), (1024, 20, 16, 5, 2), (40, 8, 20, 7, 2)])
+@pytest.mark.parametrize("spread", [1.0, 2.0 ** -13, 2.0 ** -20])
+def test_route_of_many_close_scores(B, E, k, n_group, topk_group, group_best, spread):
+    """Scores a few float32 steps apart: of the groups, of the experts of a group's value, of the chosen; among them rows
+    with many that are equal."""
+    g = torch.Generator().manual_seed(E + k)
+    logits = 0.5 + spread * torch.randn(1500, E, generator=g)
+    logits[::5] = 0.5 + spread * torch.randint(0, 4, (300, E), generator=g).float()
+    bias = spread * torch.randint(-3, 4, (E,), generator=g).float()
+    for b, score_fn in ((bias, "sigmoid"), (bias, "softmax"), (None, "sigmoid")):
+        check_route(B, logits, b, k, score_fn=score_fn, n_group=n_group, topk_group=topk_group, group_best=group_best)
 
 
 def test_route_of_group_values_that_almost_tie(B):

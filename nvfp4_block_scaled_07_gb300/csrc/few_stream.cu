@@ -53,6 +53,7 @@ constexpr int kCodeBytes = kTerms * kStep / 2;  // of a token and step: 8 rows o
 constexpr int kTermScales = 128;                // their scales: [term][64 columns][4 bytes]
 constexpr int kWeightBytes = 128 * 128;         // of a stage
 constexpr int kScaleBytes = 2048;
+constexpr int kStageBytes = kWeightBytes + kScaleBytes;
 constexpr int kTileRows = 128;
 constexpr int kMinShare = 4;                    // stages
 constexpr int kMaxStages = 8;
@@ -75,7 +76,7 @@ struct StreamParams {
   const float* row_scale;    // s_0 of each row
   int rows;
   int T, k, E, N, K, tiled, out_fp16;
-  int stages, stage_bytes;
+  int stages, term_stages, term_bytes;         // of the weights' ring and the terms'; of a stage of terms
   const int32_t* idx;
   const float* topk_w;
   void* out;                 // [T, N], or h [T * k, N / 2] float32
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   // WIDE: up to 256 columns, one accumulator; else up to 128 and two
   constexpr int kBuffers = WIDE ? 1 : 2, kScaleCols = WIDE ? 48 : 32;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_ready[kMaxStages], s_empty[kMaxStages], s_acc[2 * kBuffers + 1];
+  __shared__ __align__(8) uint64_t s_full[2 * kMaxStages], s_ready[kMaxStages], s_empty[2 * kMaxStages], s_acc[2 * kBuffers + 1];
   __shared__ mla::WaitCtl s_ctl;
   __shared__ uint32_t s_tmem;
   __shared__ int s_last, s_expert[2][32];      // of each producer
@@ -288,12 +289,18 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   uint8_t* smem = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = mla::uniform(tid >> 5);
   const uint32_t full = ptx::smem_u32(s_full), ready = ptx::smem_u32(s_ready), empty = ptx::smem_u32(s_empty);
+  const uint32_t t_full = full + 8 * kMaxStages, t_empty = empty + 8 * kMaxStages;          // of the terms
+  const uint32_t terms = ptx::smem_u32(smem) + p.stages * kStageBytes;
   const uint32_t acc_full = ptx::smem_u32(s_acc), acc_empty = acc_full + 8 * kBuffers, drained = acc_empty + 8 * kBuffers;
   if (tid == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      ptx::mbar_init(full + 8 * i, 2);         // weights, terms
+      ptx::mbar_init(full + 8 * i, 1);
       ptx::mbar_init(ready + 8 * i, 4);        // the scale warps
       ptx::mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < p.term_stages; ++i) {
+      ptx::mbar_init(t_full + 8 * i, 1);
+      ptx::mbar_init(t_empty + 8 * i, 1);
     }
     for (int i = 0; i < kBuffers; ++i) {
       ptx::mbar_init(acc_full + 8 * i, 1);
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   const int per = int(max(int64_t(kMinShare), (all + gridDim.x - 1) / gridDim.x));
   const int64_t start = int64_t(blockIdx.x) * per, end = min(all, start + per);
   const int blocks = p.N / 128, k_blocks = p.K / 64;
-  const int terms_at = (p.stage_bytes - kWeightBytes - kScaleBytes) / (kCodeBytes + kTermScales) * kCodeBytes;  // their scales
+  const int sf_at = p.term_bytes / (kCodeBytes + kTermScales) * kCodeBytes;   // the terms' scales in their stage
   // the units of this block's range, in order
   auto unit_at = [&](int64_t s) {
     Unit u;
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         ok = mla::wait_warp(empty + 8 * st, parity, &s_ctl);
         if (!ok) break;
         const int step = u.step + i;
-        const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem) + st * p.stage_bytes;
+        const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem) + st * kStageBytes;
         mla::arrive_expect_tx(el, bar, kWeightBytes + kPerStep * 512);
         const int w0 = p.tiled ? 0 : step * 128, w1 = p.tiled ? blk * steps + step : blk, s1 = blk * kb_all + step * kPerStep;
         if (MODE == kGateUp) {                 // 16 rows of each 32 of a block of 128: gate's, then up's
@@ -402,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
       const int base = mla::uniform(MODE == kDown ? __ldcg(p.plan->base + u.seg) : 0), m = MODE == kDense ? p.T : __popc(tokens);
       if (s == start) ptx::grid_dep_wait();    // the terms are the kernel before's
       for (int i = 0; i < u.n; ++i, ++count) {
-        ok = mla::wait_warp(empty + 8 * st, parity, &s_ctl);
+        ok = mla::wait_warp(t_empty + 8 * st, parity, &s_ctl);
         if (!ok) break;
-        const uint32_t bar = full + 8 * st, dst = ptx::smem_u32(smem) + st * p.stage_bytes + kWeightBytes + kScaleBytes;
+        const uint32_t bar = t_full + 8 * st, dst = terms + st * p.term_bytes;
         const uint8_t* codes = p.codes + int64_t(u.step + i) * p.rows * kCodeBytes;
         const uint8_t* sf = p.scales + int64_t(u.step + i) * p.rows * kTermScales;
         mla::arrive_expect_tx(el, bar, m * (kCodeBytes + kTermScales));
@@ -413,24 +420,24 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
           for (int slot = 0; slot < m; ++slot, left &= left - 1) {
             const int t = __ffs(left) - 1;
             bulk_copy(el, dst + slot * kCodeBytes, codes + t * kCodeBytes, kCodeBytes, bar);
-            bulk_copy(el, dst + terms_at + slot * kTermScales, sf + t * kTermScales, kTermScales, bar);
+            bulk_copy(el, dst + sf_at + slot * kTermScales, sf + t * kTermScales, kTermScales, bar);
           }
         } else {
           bulk_copy(el, dst, codes + int64_t(base) * kCodeBytes, m * kCodeBytes, bar);
-          bulk_copy(el, dst + terms_at, sf + int64_t(base) * kTermScales, m * kTermScales, bar);
+          bulk_copy(el, dst + sf_at, sf + int64_t(base) * kTermScales, m * kTermScales, bar);
         }
-        if (++st == p.stages) st = 0, parity ^= 1;
+        if (++st == p.term_stages) st = 0, parity ^= 1;
       }
       s += u.n;
     }
     if (!ok)
-      for (int64_t j = max(int64_t(0), count - p.stages); j < count; ++j)
-        mla::drain_phase(full + 8 * int(j % p.stages), int(j / p.stages) & 1);
+      for (int64_t j = max(int64_t(0), count - p.term_stages); j < count; ++j)
+        mla::drain_phase(t_full + 8 * int(j % p.term_stages), int(j / p.term_stages) & 1);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---- MMAs: 128 rows x (8 columns a token), 64 columns of K each
     const uint32_t el = mla::elect_one();
-    int st = 0, parity = 0;
+    int st = 0, parity = 0, ts = 0;
     uint32_t n = 0;
     bool ok = true;
     for (int64_t s = start; s < end && ok; ++n) {
@@ -443,15 +450,17 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         ok = mla::wait_warp(ready + 8 * st, parity, &s_ctl);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t a = mla::desc_sw128(ptx::smem_u32(smem) + st * p.stage_bytes, 16);
-        const uint32_t b = a + (kWeightBytes + kScaleBytes) / 16, sf = tmem + kScaleCol + st * kScaleCols;
+        const uint32_t a = mla::desc_sw128(ptx::smem_u32(smem) + st * kStageBytes, 16);
+        const uint32_t b = mla::desc_sw128(terms + ts * p.term_bytes, 16), sf = tmem + kScaleCol + st * kScaleCols;
         const int nk = min(4, k_blocks - 4 * (u.step + i));
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
           if (kb < nk)
             mma_fp4<MX>(el, d, a + 2 * kb, b + 2 * kb, idesc, sf + 4 * kb, sf + 16 + (WIDE ? 8 : 4) * kb, i > 0 || kb > 0);
         mla::tc_commit(el, empty + 8 * st);
+        mla::tc_commit(el, t_empty + 8 * ts);
         if (++st == p.stages) st = 0, parity ^= 1;
+        if (++ts == p.term_stages) ts = 0;
       }
       if (ok) mla::tc_commit(el, acc_full + 8 * buffer);
       s += u.n;
@@ -462,15 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
   } else if (warp < kJoiner) {
     // ---- scales to tensor memory: lane i of each quarter holds rows i, 32 + i, 64 + i and 96 + i
     const uint32_t quarter = uint32_t(warp & 3) * 32 << 16;
-    int st = 0, parity = 0;
+    int st = 0, parity = 0, ts = 0, t_parity = 0;
     bool ok = true;
     for (int64_t s = start; s < end && ok;) {
       const Unit u = unit_at(s);
       const int m = MODE == kDense ? p.T : __popc(p.plan->tokens[u.seg]);
       for (int i = 0; i < u.n; ++i) {
-        ok = __all_sync(kFull, mla::wait_phase(full + 8 * st, parity, &s_ctl));
+        ok = __all_sync(kFull, mla::wait_phase(full + 8 * st, parity, &s_ctl) && mla::wait_phase(t_full + 8 * ts, t_parity, &s_ctl));
         if (!ok) break;
-        const uint32_t at = ptx::smem_u32(smem + st * p.stage_bytes) + kWeightBytes;
+        const uint32_t at = ptx::smem_u32(smem) + st * kStageBytes + kWeightBytes, t_at = terms + ts * p.term_bytes + sf_at;
         const uint32_t sf = tmem + quarter + kScaleCol + st * kScaleCols;
         uint32_t c[16], t[WIDE ? 32 : 16];       // columns: [64 columns of K][32 rows]
 #pragma unroll
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         for (int j = 0; j < (WIDE ? 8 : 4); ++j) {
           const int token = 4 * j + (lane >> 3);
           uint4 w = make_uint4(0, 0, 0, 0);
-          if (token < m) w = ptx::lds128(at + kScaleBytes + terms_at + token * kTermScales + (lane & 7) * 16);
+          if (token < m) w = ptx::lds128(t_at + token * kTermScales + (lane & 7) * 16);
           constexpr int kRows = WIDE ? 8 : 4;
           t[j] = w.x, t[kRows + j] = w.y, t[2 * kRows + j] = w.z, t[3 * kRows + j] = w.w;
         }
@@ -502,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ready + 8 * st);
         if (++st == p.stages) st = 0, parity ^= 1;
+        if (++ts == p.term_stages) ts = 0, t_parity ^= 1;
       }
       s += u.n;
     }
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     // ---- joiners: a thread a row; sums over the terms, the experts (down) and the blocks
     const int quarter = warp & 3, row = 32 * quarter + lane, id = tid - 32 * kJoiner;
     const uint32_t lanes = tmem + (uint32_t(32 * quarter) << 16);
-    float* total = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes) + row;   // [token or slot][128]
+    float* total = reinterpret_cast<float*>(smem + p.stages * kStageBytes + p.term_stages * p.term_bytes) + row;   // [token or slot][128]
     uint32_t n = 0;
     int64_t tile_first = start;                // the block's first stage of the tile
     for (int64_t s = start; s < end; ++n) {
@@ -702,13 +712,14 @@ cudaError_t launch_one(const FewMatrix& w, StreamParams p, int num_sms, cudaStre
   auto kernel = stream_kernel<MX, MODE, WIDE>;
   CUtensorMap weights, scales;
   if (!weight_maps(&weights, &scales, w, p.E, MODE == kGateUp)) return cudaErrorInvalidValue;
-  // as many stages as fit beside the tile's sums, and as their scales have columns of tensor memory
-  // (the terms' scales of T tokens in whole kilobytes, so that every stage starts on one)
-  const int slots = (p.T + 7) / 8 * 8;
-  p.stage_bytes = kWeightBytes + kScaleBytes + slots * (kCodeBytes + kTermScales);
-  const int rest = kSmemLimit - 2048 - p.T * kTileRows * 4, most = WIDE ? 5 : kMaxStages;
-  p.stages = rest / p.stage_bytes < most ? rest / p.stage_bytes : most;
-  const int smem = 1024 + p.stages * p.stage_bytes + p.T * kTileRows * 4;
+  // Stages of weights as their scales have columns of tensor memory, of terms as fit beside them and the tile's
+  // sums: the weights come from memory and wait longer.  (The terms' scales of T tokens in whole kilobytes, so
+  // that every stage starts on one.)
+  p.term_bytes = (p.T + 7) / 8 * 8 * (kCodeBytes + kTermScales);
+  p.stages = WIDE ? 5 : kMaxStages;
+  const int sums = p.T * kTileRows * 4, rest = kSmemLimit - 2048 - sums - p.stages * kStageBytes;
+  p.term_stages = rest / p.term_bytes < p.stages ? rest / p.term_bytes : p.stages;
+  const int smem = 1024 + p.stages * kStageBytes + p.term_stages * p.term_bytes + sums;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   return launch_kernel(kernel, dim3(unsigned(num_sms < kFewMaxGrid ? num_sms : kFewMaxGrid)), dim3(kThreads), smem, st, false,

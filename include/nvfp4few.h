@@ -45,8 +45,8 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
 
 /* Products of at most 32 tokens with the weights of the grouped GEMM (packed
  * row-major or tiled, blocked scales), which then are read once and bound the
- * time; the activations are not quantised.  No counterpart on the source
- * pages, whose paths quantise activations at every batch size.
+ * time; the activations keep their 16 bits (see below).  No counterpart on the
+ * source pages, whose paths quantise activations at every batch size.
  *
  * moe_matvec_nvfp4: out[t, n] = w_gscale[0] * sum_k x[t, k] * W[n, k]
  *   (dequantised, float32 sums), rounded once to the type of x.
@@ -60,8 +60,9 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *   to expert e: h = silu(x Wg^T) * (x Wu^T), Wg and Wu rows [0, I) and
  *   [I, 2I) of w_gu[e] (with w_gu_gscale[e]); out[t] = sum_j topk_w[t, j] *
  *   (h W_d[e]^T) over its k experts e = topk_idx[t, j] in ascending order,
- *   rounded to bf16 once.  h is held in float32 and multiplied as 11-bit
- *   values (2^-11 relative; the result's rounding is 2^-8).
+ *   rounded to bf16 once.  h is held in float32 and multiplied as described
+ *   below, in small calls as 11-bit values (2^-11 relative; the result's
+ *   rounding is 2^-8).
  * moe_experts_mxfp4: the same without the gscales.
  *   x_bf16 device [T, H], rows x_stride elements apart as above; topk_idx
  *   device int32 [T, k], topk_w device float32 [T, k]; w_gu [E, 2I, H], w_d
@@ -71,14 +72,17 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *   ws: moe_experts_workspace_size(T, k, H, I) bytes, 256-byte aligned, not
  *   initialised; calls that share one must not overlap on the GPU.
  *
- * The values reach the tensor core as float16 with exponents of their own: 256
- * consecutive activations of a token share a power of two, and so do, with
- * MXFP4, the scales of 256 consecutive weights of a row.  An activation below
- * 2^-28 of the largest of its 256 is off by up to 2^-40 of that, and an MXFP4
- * scale below 2^-27 of the largest of its eight counts as zero; all others are
- * exact.  Infinities and NaN stay in their token's results.  The results do
- * not depend on the other tokens of the call beyond float32 summation order,
- * and a repeated call gives the same bits.
+ * How exact the operands are on the tensor core goes by the size of the call:
+ *   small (T <= 8, T^2 N K <= 2^25 or T^2 k 2 I H <= 2^24): float16 with a power
+ *   of two for 256 consecutive activations of a token: exact down to 2^-28 of
+ *   their largest, below off by at most 2^-40 of it.  MXFP4 scales below 2^-27 of
+ *   the largest of eight neighbours in a row of weights count as zero.
+ *   Infinities and NaN go through the sums.
+ *   else: activations are sums of eight 4-bit terms with a scale for 16 (MXFP4:
+ *   32) of them: off by at most 2^-18 of their largest, with NVFP4 also by 2^-34
+ *   of the row's.  An infinity or NaN makes all of its token's results NaN.
+ * Either way a token's results do not depend on the others of the call beyond
+ * float32 summation order, and a repeated call gives the same bits.
  * Limits: 0 <= T <= 32 (0 is a no-op), K, H and I multiples of 64 (NVFP4) or
  * 128 (MXFP4), N, H and I multiples of 128, 1 <= E <= 1024, 1 <= k <= 32. */
 #define NVFP4MOE_X_BF16 0

@@ -6,9 +6,11 @@
 //   experts:  h = silu(x Wg^T) * (x Wu^T) for each routed token, then
 //   out[t] = sum over its experts of weight * h Wd^T
 //
-// Bound by the weights' bytes: with at most 32 tokens every matrix is read
-// once and each byte of it serves 4 T flops.  The tensor core takes the codes
-// as float16: a code times its ue4m3 scale has at most 6 significant bits and
+// This is the kernel of small products; few_stream.cu takes the rest (the rule
+// stands at takes_matvec).  What bounds these is latency: a launch (two for the
+// experts), one read of the activations and a few steps of weights.  One token x
+// [512, 2048] takes 3.0 us, three tokens through two of 8 experts each (H 256, I
+// 128) 7.7 us with the plan.  mma.sync takes the codes as float16: a code times its ue4m3 scale has at most 6 significant bits and
 // lies in 2^-10 .. 2688, so the product is exact.  E8M0 scales do not fit that
 // range: of the 256 values of a row that a step takes, the largest scale is
 // the reference 2^X, codes are multiplied by 2^(scale - X + 13), and the sum

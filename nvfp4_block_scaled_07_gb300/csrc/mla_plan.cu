@@ -8,9 +8,9 @@
 // request.
 //
 // One block scans the requests (tokens, then pages) in pieces of its threads,
-// and writes the new table entries and, up to kOneBlock tokens, the tokens.
-// More tokens are written by a second kernel over all SMs, which reads the
-// tables.  Bound by latency: a decode step is one launch and two scans.
+// and writes the new table entries and a few tokens.  More tokens are written by a second kernel over all SMs, which reads the
+// tables.  Bound by latency: a decode step is one launch and two scans.  One
+// request of one token takes 2.6 us, 700 of three 4.9 us, 37 of 7000 8.6 us.
 #include <climits>
 #include <cstdint>
 
@@ -26,7 +26,11 @@ __device__ unsigned g_plan_flags = 0;
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kMaxThreads = 1024;
-constexpr int kOneBlock = 8192;   // tokens
+// The one block writes up to kOneBlock tokens, and up to kFew a request on average, which the scanning threads write as
+// they go.  Measured (us with one kernel, with two): 8 requests of 1024 tokens together 6.4, 6.3, of 8192 9.8, 6.4, of
+// 65536 41, 6.8; 300 requests of 4096 9.8, 8.7; 700 requests of three each 4.4, 11.1; 10000 of one 24, 59.
+constexpr int kOneBlock = 1024;
+constexpr int kFew = 8;           // new tokens of a request: at most two pages
 constexpr int kSmall = 1 << 20;   // up to so many rows and free pages, a piece's two sums fit one 64-bit scan
 constexpr int kTokensPerBlock = 1024;
 
@@ -78,7 +82,6 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const MlaPlanArgs p, 
   __shared__ bool s_ok[kMaxThreads];
   __shared__ int s_given;
   constexpr int kAtOnce = 4;                  // tokens or pages of a thread
-  constexpr int kFew = 8;                     // new tokens of a request: at most two pages
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int tid = threadIdx.x, threads = blockDim.x;
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(256) plan_tokens_kernel(const MlaPlanArgs p) {
 }  // namespace
 
 cudaError_t launch_mla_plan(const MlaPlanArgs& a, cudaStream_t st) {
-  const bool one = a.T <= kOneBlock;
+  const bool one = a.T <= kOneBlock || a.T <= int64_t(kFew) * a.B;
   const int64_t most = one && a.T < kMaxThreads ? (a.T > a.B ? a.T : a.B) : kMaxThreads;   // pages of many tokens as well
   const int threads = most >= kMaxThreads ? kMaxThreads : most < 32 ? 32 : int(most + 31) / 32 * 32;
   const cudaError_t err = launch_kernel(plan_kernel, dim3(1), dim3(threads), 0, st, false, a, one);

@@ -10,13 +10,18 @@
 // one value, or change places.  A warp takes a token: it chooses by float32
 // scores and their error bound d, and where two candidates that the choice
 // depends on differ by no more than 2 d it chooses again in float64 (one token
-// in a thousand for random logits).  Without a bias c orders like v, which
+// in a thousand for random logits), of the candidates at the border only.  Without a bias c orders like v, which
 // needs no bound (unless groups are valued by sums).
 //
 // A lane holds consecutive experts, so that a group is whole lanes in the
 // usual shapes and its value takes two shuffles.  The k rounds are warp maxima
 // of integer keys that order like the floats; the lowest lane with the maximum
 // has the lowest index.
+//
+// Bound by instructions (issue slots 74 % busy, DRAM 10 %): 16384 tokens of 256
+// experts take 20 us in 8 groups of which 4 are kept, 15 us without groups, one
+// token 3.1 us.  Choosing all groups again in float64 where two were close took
+// 31 us for the 16384.
 #include <cfloat>
 #include <climits>
 #include <cstdint>

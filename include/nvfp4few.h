@@ -80,7 +80,7 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *   Infinities and NaN go through the sums.
  *   else: activations are sums of eight 4-bit terms with a scale for 16 (MXFP4:
  *   32) of them: off by at most 2^-18 of their largest, with NVFP4 also by 2^-34
- *   of the row's.  An infinity or NaN makes all of its token's results NaN.
+ *   of the row's (of 2^-80 if that is larger).  An infinity or NaN makes all of its token's results NaN.
  * Either way a token's results do not depend on the others of the call beyond
  * float32 summation order, and a repeated call gives the same bits.
  * Limits: 0 <= T <= 32 (0 is a no-op), K, H and I multiples of 64 (NVFP4) or

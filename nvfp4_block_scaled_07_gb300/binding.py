@@ -961,10 +961,13 @@ class MoELayer:
         self.acc = torch.zeros((T, H), dtype=torch.float32, device=dev) if self.fused_finalize else None
 
     # ---- the steps of forward() (bench.py times them one by one) ----
-    def prepare(self, x, logits):
-        """a1-a3: routing, quantisation of x and the permutation."""
+    def _has_steps(self):
         if self.few:
             raise ValueError(f"a batch of {self.T} tokens (few_tokens {self.few_tokens}) has no separate steps")
+
+    def prepare(self, x, logits):
+        """a1-a3: routing, quantisation of x and the permutation."""
+        self._has_steps()
         p = self.perm
         if self.fmt == "mxfp4":
             if self.fused_prepare:
@@ -1018,17 +1021,20 @@ class MoELayer:
 
     def gemm_gate_up(self, plan=None):
         """a4: gate/up GEMM with the fused SwiGLU + requantisation, by launch plan."""
+        self._has_steps()
         for tile_n, rows in (self.plan()[0] if plan is None else plan):
             self._gemm("gate_up", tile_n, rows)
 
     def gemm_down(self, plan=None):
         """a5: down GEMM to bf16, by launch plan."""
+        self._has_steps()
         for tile_n, rows in (self.plan()[1] if plan is None else plan):
             self._gemm("down", tile_n, rows)
 
     def finalize(self, out=None):
         """a6: the router-weighted sum back to token order (fused finalize:
         the conversion of the float32 accumulator, which it zeroes)."""
+        self._has_steps()
         if self.fused_finalize:
             return moe_finalize_f32(self.acc, out=self.out if out is None else out)
         return moe_finalize(self.y, self.perm.flat_to_perm, self.topk_w, out=self.out if out is None else out)

@@ -225,15 +225,6 @@ __device__ __forceinline__ void tma_2d(uint32_t elected, uint32_t dst, const voi
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void tma_3d(uint32_t elected, uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2,
-                                       uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
-      "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy), "r"(elected)
-      : "memory");
-}
 __device__ __forceinline__ void tma_4d(uint32_t elected, uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2,
                                        int c3, uint64_t policy) {
   asm volatile(
@@ -385,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         mla::arrive_expect_tx(el, bar, kWeightBytes + kPerStep * 512);
         const int w0 = p.tiled ? 0 : step * 128, w1 = p.tiled ? blk * steps + step : blk, s1 = blk * kb_all + step * kPerStep;
         if (MODE == kGateUp) {                 // 16 rows of each 32 of a block of 128: gate's, then up's
-          tma_3d(el, dst + kWeightBytes, &scales, bar, 64 * half, 0, s1, policy);
+          tma_4d(el, dst + kWeightBytes, &scales, bar, 64 * half, 0, step * kPerStep, blk, policy);
           tma_4d(el, dst, &weights, bar, w0, 16 * half, 0, w1 * 4, policy);
         } else {
           tma_2d(el, dst + kWeightBytes, &scales, bar, 0, s1, policy);
@@ -695,15 +686,17 @@ bool weight_maps(CUtensorMap* weights, CUtensorMap* scales, const FewMatrix& w, 
   const cuuint32_t per_step = w.mx ? 2 : 4;
   const cuuint64_t kb = w.K / (w.mx ? 128 : 64), s_rows = cuuint64_t(E) * (w.N / 128) * kb;
   const cuuint64_t s_dims[2] = {128, s_rows}, s_strides[1] = {512};
-  const cuuint64_t gs_dims[3] = {128, 2, s_rows}, gs_strides[2] = {cuuint64_t(w.N / 256) * kb * 512, 512};
-  const cuuint32_t s_box[2] = {128, per_step}, gs_box[3] = {64, 2, per_step};
+  // gate's blocks of 128 rows and, as many further, up's; a step's blocks past the columns are not read
+  const cuuint64_t gs_dims[4] = {128, 2, kb, cuuint64_t(E) * (w.N / 128)};
+  const cuuint64_t gs_strides[3] = {cuuint64_t(w.N / 256) * kb * 512, 512, kb * 512};
+  const cuuint32_t s_box[2] = {128, per_step}, gs_box[4] = {64, 2, per_step, 1};
   auto encode = [&](CUtensorMap* m, CUtensorMapDataType type, int rank, const uint8_t* base, const cuuint64_t* d,
                     const cuuint64_t* s, const cuuint32_t* b, CUtensorMapSwizzle swizzle) {
     return enc(m, type, cuuint32_t(rank), const_cast<uint8_t*>(base), d, s, b, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   return (gate_up ? encode(weights, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, w.packed, g_dims, g_strides, g_box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-                        encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, w.scales, gs_dims, gs_strides, gs_box,
+                        encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, w.scales, gs_dims, gs_strides, gs_box,
                                CU_TENSOR_MAP_SWIZZLE_NONE)
                   : encode(weights, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w.packed, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
                         encode(scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, w.scales, s_dims, s_strides, s_box,

@@ -220,8 +220,9 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kWarps + warp;
-  if (t >= p.T) return;
+  const unsigned row_of = blockIdx.x * kWarps + warp;   // up to 2^31 + 6
+  if (row_of >= unsigned(p.T)) return;
+  const int t = int(row_of);
   const float* row = p.logits + int64_t(t) * p.E;
   const int e0 = lane * VPL, per = p.E / p.groups;
   float v[VPL], c[VPL];
@@ -530,7 +531,7 @@ cudaError_t launch_vpl(const RouteParams& p, cudaStream_t st) {
   const int per = p.E / p.groups, lanes = per / VPL;
   const bool whole = p.E == 32 * VPL && per % VPL == 0 && (lanes & (lanes - 1)) == 0;
   return launch_kernel(whole ? route_grouped_kernel<VPL, true> : route_grouped_kernel<VPL, false>,
-                       dim3(unsigned((p.T + kWarps - 1) / kWarps)), dim3(32 * kWarps), 0, st, false, p);
+                       dim3((unsigned(p.T) + kWarps - 1) / kWarps), dim3(32 * kWarps), 0, st, false, p);
 }
 
 }  // namespace

@@ -203,7 +203,7 @@ def routing(T, E, k, seed):
 @pytest.mark.parametrize("fmt,tiled", list(itertools.product(["nvfp4", "mxfp4"], [False, True])))
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 4, 2, 256, 128), (1, 1, 1, 128, 128), (3, 8, 2, 256, 128), (8, 8, 8, 384, 256),
                                        (9, 16, 4, 256, 384), (16, 5, 3, 128, 256), (23, 40, 8, 256, 128),
-                                       (32, 3, 1, 256, 256), (32, 64, 6, 128, 128), (2, 6, 3, 4096, 640), (1, 12, 8, 640, 2304)])
+                                       (32, 3, 1, 256, 256), (32, 64, 6, 128, 128), (32, 128, 32, 128, 128), (8, 1024, 32, 128, 128), (2, 6, 3, 4096, 640), (1, 12, 8, 640, 2304)])
 def test_experts(B, T, E, k, H, I, fmt, tiled):
     gu, d = layer(E, H, I, fmt, seed=T + E)
     x = normal(T, H, seed=I)

@@ -50,10 +50,28 @@ def test_layer_of_few_tokens_is_its_two_calls(B, fmt, tiled, T):
     else:
         want = B.moe_experts_mxfp4(x, idx, w, *args)
     assert torch.equal(y, want)
-    with pytest.raises(ValueError, match="steps"):
-        layer.prepare(x, logits)
+    for step in (lambda: layer.prepare(x, logits), layer.gemm_gate_up, layer.gemm_down, layer.finalize,
+                 lambda: layer.autotune(x, logits)):
+        with pytest.raises(ValueError, match="steps"):
+            step()
     out = torch.empty_like(y)
     assert layer(x, logits, out=out) is out and torch.equal(out, y)
+    B.sync_status()
+
+
+@pytest.mark.parametrize("k_primary", [None, 2])
+def test_layer_of_few_tokens_with_the_other_routers(B, k_primary):
+    gu, d = weights(16, 256, 128)
+    bias = torch.linspace(-0.3, 0.3, 16, device="cuda")
+    few = B.MoELayer(gu, d, 4, bias=bias, k_primary=k_primary, few_tokens=16, score_fn="softmax")
+    many = B.MoELayer(gu, d, 4, bias=bias, k_primary=k_primary, score_fn="softmax", autotune=False, fused_prepare=False)
+    x, logits = batch(11, 256, 16, seed=9)
+    y = few(x, logits)
+    many(x, logits)
+    assert torch.equal(few.topk_idx, many.topk_idx) and torch.equal(few.topk_w, many.topk_w)
+    assert torch.equal(y, B.moe_experts_nvfp4(x, many.topk_idx, many.topk_w, few.w_gu_packed, few.w_gu_scales, few.w_gu_gscale,
+                                              few.w_d_packed, few.w_d_scales, few.w_d_gscale))
+    assert few.launches_per_forward == (1 if k_primary is None else 2) + B._lib.moe_experts_launches(11, 4, 256, 128)
     B.sync_status()
 
 
@@ -142,6 +160,32 @@ def test_prefill_between_steps_of_a_graph(B):
 
     plain, mixed = steps(False), steps(True)
     assert all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(plain, mixed))
+    B.sync_status()
+
+
+def test_calls_at_once_on_two_streams(B):
+    """Calls with workspaces of their own, on two streams at the same time, each give what they give alone."""
+    gu, d = R.Matrices(8, 1024, 512, "nvfp4", 1), R.Matrices(8, 512, 512, "nvfp4", 2)
+    args = [t for m in (gu, d) for t in (m.packed.cuda(), m.blocked().cuda(), m.gscale.cuda())]
+    m = R.Matrices(1, 2048, 2048, "mxfp4", 3)
+    dense = (m.packed.cuda()[0], m.blocked().cuda())
+    calls = []
+    for T in (2, 20):
+        x, logits = batch(T, 512, 8, seed=T)
+        idx, w = B.moe_route_grouped(logits, 2)
+        z = batch(T, 2048, 1, seed=T + 1)[0]
+        calls.append(lambda x=x, idx=idx, w=w: B.moe_experts_nvfp4(x, idx, w, *args))
+        calls.append(lambda z=z: B.moe_matvec_mxfp4(z, *dense))
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(20):
+        for side, call, outs in zip(sides, calls, got):
+            with torch.cuda.stream(side):
+                outs.append(call())
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, y) for y, outs in zip(want, got) for o in outs)
     B.sync_status()
 
 

@@ -766,11 +766,10 @@ def _few_weights(w_packed, w_scales, w_gscale, fmt, name, dev):
         E, N, K, layout = w_packed.E, w_packed.N, w_packed.K, W_TILED
         at = _at_least(w_packed.data, E * N * (-(-K // 256) * 128), name, dev)
     else:
-        if w_packed.dim() == 2:
-            w_packed = w_packed[None]
-        E, N, half = w_packed.shape
+        shape = w_packed.shape
+        E, N, half = shape if len(shape) == 3 else (1, *shape)
         K, layout = 2 * half, W_ROWMAJOR
-        at = _dense(w_packed, torch.uint8, (E, N, half), name, dev)
+        at = _dense(w_packed, torch.uint8, shape, name, dev)
     block = 16 if fmt == "nvfp4" else 32
     args = [at, _at_least(w_scales, E * -(-N // 128) * 128 * (K // block), f"{name} scales", dev)]
     if fmt == "nvfp4":

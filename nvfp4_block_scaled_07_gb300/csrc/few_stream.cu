@@ -28,7 +28,7 @@
 //
 // Bound by the weights' bytes up to 16 tokens, of which 132 MB take 25.6 us (one
 // token) to 27.8 us (16) with about 6 us of start and joins, 5.2 TB/s; at 32
-// tokens, 35.8 us, by the way of the terms through a ring of three stages.  The
+// tokens, 35.8 us, by one accumulator and three stages of terms.  The
 // same stream on mma.sync, with the codes widened to float16 in registers, was
 // bound by those instructions: 31 us at 8 tokens, 79 us at 32, and 1390 us for 23
 // tokens through a layer that takes 451 us here.

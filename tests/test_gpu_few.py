@@ -39,7 +39,7 @@ def normal(*shape, seed=0, dtype=torch.bfloat16):
 @pytest.mark.parametrize("fmt,tiled,dtype", list(itertools.product(["nvfp4", "mxfp4"], [False, True], ["bf16", "fp16"])))
 @pytest.mark.parametrize("T,N,K", [(1, 128, 128), (2, 256, 384), (3, 128, 640), (5, 384, 1024), (8, 128, 2048), (9, 256, 256),
                                    (16, 128, 1152), (17, 128, 384), (25, 256, 896), (32, 384, 512), (1, 640, 14336),
-                                   (7, 128, 9088), (32, 128, 4224), (4, 1152, 4096), (8, 640, 2048), (1, 4096, 9088)])
+                                   (7, 128, 9088), (32, 128, 4224), (32, 1024, 4224), (17, 512, 2304), (31, 8192, 640), (9, 4096, 1152), (20, 256, 128), (4, 1152, 4096), (8, 640, 2048), (1, 4096, 9088)])
 def test_matvec(B, T, N, K, fmt, tiled, dtype):
     m = R.Matrices(1, N, K, fmt, seed=T + N)
     x = normal(T, K, seed=K, dtype=DT[dtype])

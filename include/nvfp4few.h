@@ -10,7 +10,7 @@
  * Conventions are those of nvfp4moe.h: C ABI, status codes and messages,
  * caller-owned device buffers, work enqueued on `stream` without
  * synchronising, programmatic dependent launch, compute capability 10.3.
- * Strides count elements.
+ * Strides count elements.  Outputs and workspaces overlap nothing else.
  */
 #ifndef NVFP4FEW_H
 #define NVFP4FEW_H
@@ -73,14 +73,16 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *   initialised; calls that share one must not overlap on the GPU.
  *
  * How exact the operands are on the tensor core goes by the size of the call:
- *   small (T <= 8, T^2 N K <= 2^25 or T^2 k 2 I H <= 2^24): float16 with a power
- *   of two for 256 consecutive activations of a token: exact down to 2^-28 of
- *   their largest, below off by at most 2^-40 of it.  MXFP4 scales below 2^-27 of
- *   the largest of eight neighbours in a row of weights count as zero.
+ *   small (T <= 8, and K <= 6144, T K <= 2^14, T K^2 N <= 2^37; for experts H <=
+ *   6144, T H <= 2^14, T k 2 I H <= 2^24, (T k I)^2 2 H <= 2^36): float16 with a
+ *   power of two for 256 consecutive activations of a token: exact down to 2^-28
+ *   of their largest, below off by at most 2^-40 of it.  MXFP4 scales below 2^-27
+ *   of the largest of eight neighbours in a row of weights count as zero.
  *   Infinities and NaN go through the sums.
  *   else: activations are sums of eight 4-bit terms with a scale for 16 (MXFP4:
  *   32) of them: off by at most 2^-18 of their largest, with NVFP4 also by 2^-34
- *   of the row's (of 2^-80 if that is larger).  An infinity or NaN makes all of its token's results NaN.
+ *   of the row's (of 2^-80 if that is larger).  An infinity or NaN makes all of
+ *   its token's results NaN.
  * Either way a token's results do not depend on the others of the call beyond
  * float32 summation order, and a repeated call gives the same bits.
  * Limits: 0 <= T <= 32 (0 is a no-op), K, H and I multiples of 64 (NVFP4) or

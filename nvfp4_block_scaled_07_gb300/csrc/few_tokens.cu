@@ -9,7 +9,7 @@
 // This is the kernel of small products; few_stream.cu takes the rest (the rule
 // stands at takes_matvec).  What bounds these is latency: a launch (two for the
 // experts), one read of the activations and a few steps of weights.  One token x
-// [512, 2048] takes 3.0 us, three tokens through two of 8 experts each (H 256, I
+// [512, 2048] takes 2.7 us, three tokens through two of 8 experts each (H 256, I
 // 128) 7.7 us with the plan.  mma.sync takes the codes as float16: a code times its ue4m3 scale has at most 6 significant bits and
 // lies in 2^-10 .. 2688, so the product is exact.  E8M0 scales do not fit that
 // range: of the 256 values of a row that a step takes, the largest scale is
@@ -27,8 +27,9 @@
 // rows a step.  The rows of a tile are four of each 32, because the blocked
 // scale layout keeps the scales of rows r, r + 32, r + 64 and r + 96 together:
 // so a tile's scales are whole sectors.  Eight columns of a tile's product are
-// tokens.  The warps of a block share rows or columns (WK warps along the
-// columns, their sums joined in shared memory in a fixed order).
+// tokens.  The warps of a block take the steps of the same rows in turn, their
+// sums are joined in shared memory in a fixed order (with warps on rows of
+// their own 8 tokens x [512, 1024] took 6.1 us instead of 3.9).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -60,7 +61,6 @@ struct FewParams {
   const float* next_gscale;  // gate/up: the down matrices' scales, null: 1
   int N, K;                  // rows (gate and up together) and columns of one matrix
   int tiled, wide;           // wide: rows start on 32-byte boundaries
-  int wk;                    // warps of a block along the columns
   int out_fp16;
   void* out;
   Plan* plan;
@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wk = warp % p.wk, wr = warp / p.wk, wrs = kWarps / p.wk;
   const int steps = (p.K + kStep - 1) / kStep;
 
   // The experts of this block, the tokens of each and their rows of activations.
@@ -208,14 +207,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   const int units = nseg * steps;
 
   // This warp's tiles.
-  const int sub = blockIdx.x * wrs + wr;
+  const int sub = blockIdx.x;
   const int rb = MODE == kGateUp ? sub >> 3 : sub >> 2, st = MODE == kGateUp ? sub & 7 : 2 * (sub & 3);
   const Lane l = lane_of<MX>(p, rb, st, MODE == kGateUp ? p.N / 2 : 4, lane);
 
-  int step = wk, seg = 0;
+  int step = warp, seg = 0;                    // the warps take the columns' steps in turn
   while (step >= steps) step -= steps, ++seg;
   Rows cur;
-  if (wk < units) load_rows<MX>(cur, p, l, MODE == kDown ? s_expert[seg] : e, step);
+  if (warp < units) load_rows<MX>(cur, p, l, MODE == kDown ? s_expert[seg] : e, step);
 
   // Activations as float16: [step][piece j][token of the expert][16 bytes of 4 lane groups].
   const int rows = MODE == kDown ? p.T * p.k : p.T;   // an upper bound, also of a gate/up block's tokens
@@ -244,12 +243,12 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   float total[2][4] = {};
   const int g = lane >> 2;
 
-  for (int u = wk; u < units; u += p.wk) {
+  for (int u = warp; u < units; u += kWarps) {
     // the next step's weights on their way
-    int nstep = step + p.wk, next = seg;
+    int nstep = step + kWarps, next = seg;
     while (nstep >= steps) nstep -= steps, ++next;
     Rows nxt;
-    if (u + p.wk < units) load_rows<MX>(nxt, p, l, MODE == kDown ? s_expert[next] : e, nstep);
+    if (u + kWarps < units) load_rows<MX>(nxt, p, l, MODE == kDown ? s_expert[next] : e, nstep);
 
     if (MODE == kDown) tokens = s_tokens[seg], base = s_base[seg];
     const int m = __popc(tokens);
@@ -336,30 +335,29 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
     *reinterpret_cast<float2*>(at + (g + 8) * 8) = make_float2(total[i][2], total[i][3]);
   }
   __syncthreads();
-  auto joined = [&](int w, int tile, int row, int t) {  // of the warps with rows group w
+  auto joined = [&](int tile, int row, int t) {
     float v = 0.0f;
-    for (int c = 0; c < p.wk; ++c) v += red[((w * p.wk + c) * 2 + tile) * 128 + row * 8 + t];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += red[(w * 2 + tile) * 128 + row * 8 + t];
     return v;
   };
   if (MODE == kGateUp) {
     const int m = __popc(tokens), I = p.N / 2;
     const float s = p.gscale ? p.gscale[e] : 1.0f, s_next = p.next_gscale ? p.next_gscale[e] : 1.0f;
     float* h = static_cast<float*>(p.out);
-    for (int i = tid; i < 16 * wrs * m; i += kThreads) {
-      const int row = i & 15, w = (i >> 4) % wrs, slot = (i >> 4) / wrs;
-      const int t = int(__fns(tokens, 0, slot + 1)), at = blockIdx.x * wrs + w;
-      const float gate = joined(w, 0, row, t) * s, up = joined(w, 1, row, t) * s;
-      const int col = (at >> 3) * 128 + (at & 7) * 4 + (row & 3) + 32 * (row >> 2);
+    for (int i = tid; i < 16 * m; i += kThreads) {
+      const int row = i & 15, slot = i >> 4, t = int(__fns(tokens, 0, slot + 1));
+      const float gate = joined(0, row, t) * s, up = joined(1, row, t) * s;
+      const int col = (sub >> 3) * 128 + (sub & 7) * 4 + (row & 3) + 32 * (row >> 2);
       h[int64_t(base + slot) * I + col] = gate / (1.0f + expf(-gate)) * up * s_weight[t] * s_next;
     }
   } else {
     const float s = MODE == kDense && p.gscale ? p.gscale[0] : 1.0f;
-    for (int i = tid; i < 32 * wrs * p.T; i += kThreads) {
-      const int r = i & 31, w = (i >> 5) % wrs, t = (i >> 5) / wrs;
-      const int at = blockIdx.x * wrs + w;
-      // rows 8 (at % 4) + 0..7 of each 32 of the 128: the first four of tile 0, the others of tile 1
-      const float v = joined(w, (r >> 2) & 1, (r & 3) + 4 * (r >> 3), t) * s;
-      const int64_t o = int64_t(t) * p.N + (at >> 2) * 128 + (at & 3) * 8 + (r & 7) + 32 * (r >> 3);
+    for (int i = tid; i < 32 * p.T; i += kThreads) {
+      const int r = i & 31, t = i >> 5;
+      // rows 8 (sub % 4) + 0..7 of each 32 of the 128: the first four of tile 0, the others of tile 1
+      const float v = joined((r >> 2) & 1, (r & 3) + 4 * (r >> 3), t) * s;
+      const int64_t o = int64_t(t) * p.N + (sub >> 2) * 128 + (sub & 3) * 8 + (r & 7) + 32 * (r >> 3);
       if (MODE == kDense && p.out_fp16)
         static_cast<__half*>(p.out)[o] = __float2half_rn(v);
       else
@@ -373,20 +371,25 @@ int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
 int64_t self_bytes(int64_t rows, int K) { return rows * steps_of(K) * (kUnitBytes + 4); }
 
 // What this file takes; few_stream.cu takes the rest.  Every block converts
-// all activations that it needs, so its work grows with the tokens twice.
-// Measured (us here, us there): one token x [512, 2048] 3.6, 7.5, x [4096,
-// 4096] 6.0, 8.2, x [6144, 8192] 13.8, 11.7; four tokens x [512, 2048] 6.1,
-// 7.8, x [1024, 4096] 10.4, 8.0; one token through 8 experts of [1024, 2048]
-// 17, 19, of [2048, 2048] 27, 22.
-constexpr int64_t kSelfBytes = 64 * 1024;
-constexpr int kSmallTokens = 8;
-constexpr int64_t kMatvecWork = int64_t(1) << 25, kExpertsWork = int64_t(1) << 24;
+// all activations that it needs, so the work grows with them twice: with the
+// steps of a block and with the blocks.  Measured (us here, us there): one
+// token x [512, 2048] 2.7, 6.5, x [8192, 4096] 8.5, 10.3, x [2048, 7168] 8.8,
+// 8.0; three x [4096, 4096] 8.2, 7.8; eight x [2048, 2048] 5.6, 7.4, x [8192,
+// 2048] 9.2, 8.0.  Experts (tokens, of them, H, I): 1, 2, 2048, 2048 13.6,
+// 16.6; 1, 8, 1024, 1024 19.7, 15.6; 8, 4, 512, 256 12.4, 18.3; 4, 4, 1024,
+// 512 15.9, 16.3.
+constexpr int64_t kSelfBytes = 64 * 1024;       // of shared memory
+constexpr int kSmallTokens = 8, kSmallK = 6144;
+constexpr int64_t kValues = int64_t(1) << 14;   // activations that a block converts
 bool takes_matvec(int T, int N, int K) {
-  return T <= kSmallTokens && self_bytes(T, K) <= kSelfBytes && int64_t(T) * T * N * K <= kMatvecWork;
+  return T <= kSmallTokens && K <= kSmallK && int64_t(T) * K <= kValues && int64_t(T) * K * K * N <= int64_t(1) << 37;
 }
 bool takes_experts(int T, int k, int H, int I) {
-  return T <= kSmallTokens && T * k <= kMaxRows && self_bytes(T, H) <= kSelfBytes && self_bytes(int64_t(T) * k, I) <= kSelfBytes &&
-         int64_t(T) * T * k * 2 * I * H <= kExpertsWork;
+  if (T > kSmallTokens || T * k > kMaxRows || H > kSmallK || int64_t(T) * H > kValues ||
+      self_bytes(int64_t(T) * k, I) > kSelfBytes)
+    return false;
+  const int64_t h = int64_t(T) * k * I, work = h * 2 * H;
+  return work <= int64_t(1) << 24 && h * work <= int64_t(1) << 36;
 }
 
 template <bool MX, int SRC, int MODE>
@@ -401,9 +404,6 @@ cudaError_t launch_few(const FewParams& p, int64_t rows, dim3 grid, cudaStream_t
   }
   return launch_kernel(kernel, grid, dim3(kThreads), smem, st, false, p);
 }
-
-// Warps of a block along the columns.
-int column_warps(int T) { return T <= 2 ? 8 : (T <= 4 ? 4 : 2); }
 
 void set_matrix(FewParams* p, const FewMatrix& w) {
   p->packed = w.packed;
@@ -433,10 +433,9 @@ cudaError_t launch_few_matvec(const void* x, int64_t x_stride, int T, bool fp16,
   p.x = x, p.x_stride = x_stride;
   p.T = T, p.k = 1, p.E = 1;
   set_matrix(&p, w);
-  p.wk = column_warps(T);
   p.out_fp16 = fp16;
   p.out = out;
-  const dim3 grid(unsigned(w.N / (32 * (kWarps / p.wk))));
+  const dim3 grid(unsigned(w.N / 32));
   if (w.mx) return fp16 ? launch_few<true, kFp16, kDense>(p, T, grid, st) : launch_few<true, kBf16, kDense>(p, T, grid, st);
   return fp16 ? launch_few<false, kFp16, kDense>(p, T, grid, st) : launch_few<false, kBf16, kDense>(p, T, grid, st);
 }
@@ -455,8 +454,7 @@ cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* i
   set_matrix(&p, gu);
   p.next_gscale = d.gscale;
   p.out = h;
-  p.wk = 8;
-  dim3 grid(unsigned(d.K / (16 * (kWarps / p.wk))), unsigned(T * k + 1));
+  dim3 grid(unsigned(d.K / 16), unsigned(T * k + 1));
   const cudaError_t err = gu.mx ? launch_few<true, kBf16, kGateUp>(p, T, grid, st) : launch_few<false, kBf16, kGateUp>(p, T, grid, st);
   if (err != cudaSuccess) return err;
 
@@ -464,7 +462,7 @@ cudaError_t launch_few_experts(const void* x, int64_t x_stride, const int32_t* i
   p.gscale = p.next_gscale = nullptr;     // in h already
   p.x = h, p.x_stride = d.K;
   p.out = out;
-  grid = dim3(unsigned(d.N / (32 * (kWarps / p.wk))));
+  grid = dim3(unsigned(d.N / 32));
   return d.mx ? launch_few<true, kF32, kDown>(p, int64_t(T) * k, grid, st)
               : launch_few<false, kF32, kDown>(p, int64_t(T) * k, grid, st);
 }

@@ -193,8 +193,8 @@ int nvfp4moe_sync_status(cudaStream_t stream) {
   unsigned f = 0;
   st = cuda_status(read_and_clear_flags(&f, stream), "reading device flags");
   if (st) return st;
-  if (f & kFlagTimeout) return fail(NVFP4MOE_ERR_TIMEOUT, "a device wait (grouped GEMM or attention pipeline, or prepare grid barrier) exceeded its time limit");
-  if (f & kFlagBadData) return fail(NVFP4MOE_ERR_DEVICE_DATA, "an expert id, row index, cache slot, page, position or sequence length was out of range");
+  if (f & kFlagTimeout) return fail(NVFP4MOE_ERR_TIMEOUT, "a device wait (grouped GEMM, attention or few-token pipeline, or prepare grid barrier) exceeded its time limit");
+  if (f & kFlagBadData) return fail(NVFP4MOE_ERR_DEVICE_DATA, "an expert id, row index, cache slot, page, position, sequence length or page count was out of range");
   return NVFP4MOE_OK;
 }
 

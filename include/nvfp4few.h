@@ -61,8 +61,7 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *   [I, 2I) of w_gu[e] (with w_gu_gscale[e]); out[t] = sum_j topk_w[t, j] *
  *   (h W_d[e]^T) over its k experts e = topk_idx[t, j] in ascending order,
  *   rounded to bf16 once.  h is held in float32 and multiplied as described
- *   below, in small calls as 11-bit values (2^-11 relative; the result's
- *   rounding is 2^-8).
+ *   below, in small calls as the sum of two float16 (22 bits: 2^-22 relative).
  * moe_experts_mxfp4: the same without the gscales.
  *   x_bf16 device [T, H], rows x_stride elements apart as above; topk_idx
  *   device int32 [T, k], topk_w device float32 [T, k]; w_gu [E, 2I, H], w_d
@@ -76,7 +75,7 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *   small (T <= 8, and K <= 6144, T K <= 2^14, T K^2 N <= 2^37; for experts H <=
  *   6144, T H <= 2^14, T k 2 I H <= 2^24, (T k I)^2 2 H <= 2^36): float16 with a
  *   power of two for 256 consecutive activations of a token: exact down to 2^-28
- *   of their largest, below off by at most 2^-40 of it.  MXFP4 scales below 2^-27
+ *   of their largest, below off by at most 2^-39 of it.  MXFP4 scales below 2^-27
  *   of the largest of eight neighbours in a row of weights count as zero.
  *   Infinities and NaN go through the sums.
  *   else: activations are sums of eight 4-bit terms with a scale for 16 (MXFP4:

@@ -59,21 +59,31 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 
 // Converts 8 values that the lane holds of a block of 256 to float16 as the
-// header says; returns the factor that undoes it.
-__device__ __forceinline__ float block_to_half(const float (&v)[8], uint4* out) {
+// header says; returns the factor that undoes it.  TWO: what the rounding
+// leaves, as float16 of the same factor, to `rest` (none of an infinity or NaN).
+template <bool TWO>
+__device__ __forceinline__ float block_to_half(const float (&v)[8], uint4* out, uint4* rest) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   top = __reduce_max_sync(kFull, top) >> 23;
   const int e = top == 255 ? 127 : max(int(top) - 127, -112);
   const float m = exp2i(14 - e);
-  uint32_t h[4];
+  uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 t = __floats2half2_rn(v[2 * i] * m, v[2 * i + 1] * m);
+    const float x = v[2 * i] * m, y = v[2 * i + 1] * m;
+    const __half2 t = __floats2half2_rn(x, y);
     h[i] = *reinterpret_cast<const uint32_t*>(&t);
+    if (TWO) {
+      const float2 q = __half22float2(t);
+      const float dx = x - q.x, dy = y - q.y;  // at most 8
+      const __half2 u = __floats2half2_rn(fabsf(dx) <= 8.0f ? dx : 0.0f, fabsf(dy) <= 8.0f ? dy : 0.0f);
+      l[i] = *reinterpret_cast<const uint32_t*>(&u);
+    }
   }
   *out = make_uint4(h[0], h[1], h[2], h[3]);
+  if (TWO) *rest = make_uint4(l[0], l[1], l[2], l[3]);
   return exp2i(e - 14);
 }
 

@@ -18,9 +18,12 @@
 // Activations become float16 too, in blocks of 256 values of a token that are
 // multiplied by the power of two which brings the largest into 2^14 .. 2^15:
 // exact for every bf16 or fp16 value above 2^-28 of its block's largest, and
-// smaller ones are off by at most 2^-40 of it.  The gated products h (float32)
-// are rounded to 11 bits by it, an eighth of what the bf16 result is rounded
-// by.  Sums are float32.
+// smaller ones are off by at most 2^-39 of it.  The gated products h (float32)
+// become two such numbers, the second what the rounding to the first leaves:
+// 22 bits, off by 2^-22 of themselves, as four float32 roundings.  (One number,
+// 11 bits, was lost in differences of nearly equal products and moved one bf16
+// result in 30; it took 7.4 us instead of 7.7 for the three tokens.)  Sums are
+// float32.
 //
 // A warp takes 32 rows of a matrix as two 16-row tiles (of gate and of up in
 // the gated product) and steps of 256 of its columns, a lane 32 bytes of four
@@ -216,9 +219,12 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   Rows cur;
   if (warp < units) load_rows<MX>(cur, p, l, MODE == kDown ? s_expert[seg] : e, step);
 
-  // Activations as float16: [step][piece j][token of the expert][16 bytes of 4 lane groups].
+  // Activations as float16: [step][piece j][token of the expert][16 bytes of 4 lane groups]; the
+  // second parts of h lie `second` bytes further.
+  constexpr bool kTwo = SRC == kF32;
   const int rows = MODE == kDown ? p.T * p.k : p.T;   // an upper bound, also of a gate/up block's tokens
-  float* factor = reinterpret_cast<float*>(smem + int64_t(rows) * steps * kUnitBytes);
+  const int second = rows * steps * kUnitBytes;
+  float* factor = reinterpret_cast<float*>(smem + (kTwo ? 2 : 1) * second);
   const int held = MODE == kDown ? rows : __popc(tokens);
   for (int i = warp; i < held * steps; i += kWarps) {
     const int r = i / steps, at = i - r * steps;
@@ -232,10 +238,11 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
     }
     float v[8];
     load_block<SRC>(v, static_cast<const uint8_t*>(p.x) + row * p.x_stride * (SRC == kF32 ? 4 : 2), at, p.K, lane);
-    uint4 h;
-    const float f = block_to_half(v, &h);
-    uint8_t* dst = smem + (first * steps + at * m) * kUnitBytes;
-    *reinterpret_cast<uint4*>(dst + ((lane & 7) * m + slot) * 64 + (lane >> 3) * 16) = h;
+    uint4 h, rest;
+    const float f = block_to_half<kTwo>(v, &h, &rest);
+    uint8_t* dst = smem + (first * steps + at * m) * kUnitBytes + ((lane & 7) * m + slot) * 64 + (lane >> 3) * 16;
+    *reinterpret_cast<uint4*>(dst) = h;
+    if (kTwo) *reinterpret_cast<uint4*>(dst + second) = rest;
     if (lane == 0) factor[r * steps + at] = f;
   }
   __syncthreads();
@@ -291,12 +298,15 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) a[i][q] = hmul2(a[i][q], sc[i]);
       }
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (has) x = *reinterpret_cast<const uint4*>(from + j * m * 64);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mma(acc[i], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
-        mma(acc[i], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
+      for (int part = 0; part < (kTwo ? 2 : 1); ++part) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (has) x = *reinterpret_cast<const uint4*>(from + part * second + j * m * 64);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma(acc[i], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
+          mma(acc[i], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
+        }
       }
     }
     // into the totals, tokens of this expert only
@@ -368,17 +378,17 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
 
 int64_t steps_of(int K) { return (K + kStep - 1) / kStep; }
 int64_t round256(int64_t b) { return (b + 255) & ~int64_t(255); }
-int64_t self_bytes(int64_t rows, int K) { return rows * steps_of(K) * (kUnitBytes + 4); }
+int64_t self_bytes(int64_t rows, int K, bool two) { return rows * steps_of(K) * ((two ? 2 : 1) * kUnitBytes + 4); }
 
 // What this file takes; few_stream.cu takes the rest.  Every block converts
 // all activations that it needs, so the work grows with them twice: with the
 // steps of a block and with the blocks.  Measured (us here, us there): one
 // token x [512, 2048] 2.7, 6.5, x [8192, 4096] 8.5, 10.3, x [2048, 7168] 8.8,
 // 8.0; three x [4096, 4096] 8.2, 7.8; eight x [2048, 2048] 5.6, 7.4, x [8192,
-// 2048] 9.2, 8.0.  Experts (tokens, of them, H, I): 1, 2, 2048, 2048 13.6,
+// 2048] 9.2, 8.0.  Experts (tokens, of them, H, I): 1, 2, 2048, 2048 15.4,
 // 16.6; 1, 8, 1024, 1024 19.7, 15.6; 8, 4, 512, 256 12.4, 18.3; 4, 4, 1024,
 // 512 15.9, 16.3.
-constexpr int64_t kSelfBytes = 64 * 1024;       // of shared memory
+constexpr int64_t kSelfBytes = 128 * 1024;      // of shared memory
 constexpr int kSmallTokens = 8, kSmallK = 6144;
 constexpr int64_t kValues = int64_t(1) << 14;   // activations that a block converts
 bool takes_matvec(int T, int N, int K) {
@@ -386,7 +396,7 @@ bool takes_matvec(int T, int N, int K) {
 }
 bool takes_experts(int T, int k, int H, int I) {
   if (T > kSmallTokens || T * k > kMaxRows || H > kSmallK || int64_t(T) * H > kValues ||
-      self_bytes(int64_t(T) * k, I) > kSelfBytes)
+      self_bytes(int64_t(T) * k, I, true) > kSelfBytes)
     return false;
   const int64_t h = int64_t(T) * k * I, work = h * 2 * H;
   return work <= int64_t(1) << 24 && h * work <= int64_t(1) << 36;
@@ -395,7 +405,7 @@ bool takes_experts(int T, int k, int H, int I) {
 template <bool MX, int SRC, int MODE>
 cudaError_t launch_few(const FewParams& p, int64_t rows, dim3 grid, cudaStream_t st) {
   auto kernel = few_kernel<MX, SRC, MODE>;
-  size_t smem = size_t(self_bytes(rows, p.K));
+  size_t smem = size_t(self_bytes(rows, p.K, SRC == kF32));
   if (smem < size_t(kWarps) * 1024) smem = size_t(kWarps) * 1024;
   if (MODE == kGateUp && smem < size_t(p.E) * 8) smem = size_t(p.E) * 8;
   if (smem > 48 * 1024) {

@@ -56,8 +56,9 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// NaN counts as -inf (score 0), +inf as the largest number.
-__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX); }
+// NaN counts as -inf (score 0), +inf as the largest number; the sum makes +0 of -0,
+// which are equal as values but not as keys.
+__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : fminf(v, FLT_MAX) + 0.0f; }
 
 // VPL values from e0 on, -inf past the E-th.
 template <int VPL>

@@ -1,9 +1,11 @@
 """Few-token operators where their definitions are easily missed."""
+import itertools
+
 import pytest
 import torch
 
 from . import few_reference as R
-from .test_gpu_few import experts, normal, on_gpu, routing
+from .test_gpu_few import check_route, experts, normal, on_gpu, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +66,29 @@ def test_experts_of_many_rows_of_few_tokens(B, T, k, fmt):
     out = experts(B, fmt, x.cuda(), idx.cuda(), w.cuda(), on_gpu(B, gu, True), on_gpu(B, d, True))
     ref, tol = R.experts(x, idx, w, gu, d)
     R.check(out, ref, tol)
+
+
+# ---- routing ----------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("score_fn,renormalize", list(itertools.product(["sigmoid", "softmax"], [True, False])))
+@pytest.mark.parametrize("E,k,n_group,topk_group", [(4, 1, 1, 1), (8, 3, 1, 1), (32, 8, 4, 2), (40, 6, 8, 3), (64, 8, 1, 1),
+                                                    (256, 8, 8, 4), (1024, 20, 16, 5)])
+def test_route_of_zeros_of_both_signs(B, E, k, n_group, topk_group, score_fn, renormalize):
+    """-0 and +0 are equal: the lower index first, with few zeros and with many."""
+    g = torch.Generator().manual_seed(E)
+    zeros = torch.where(torch.rand(24, E, generator=g) < 0.5, -0.0, 0.0)
+    negative = -1.0 - torch.rand(24, E, generator=g)
+    logits = torch.where(torch.rand(24, E, generator=g) < torch.linspace(0.02, 1.0, 24)[:, None], zeros, negative)
+    logits[0] = negative[0]
+    logits[0, 0], logits[0, 1] = -0.0, 0.0
+    logits[1] = logits[0].flip(0)
+    logits[2, ::3] = 1.0
+    for bias in (None, torch.zeros(E), torch.full((E,), -0.0)):
+        check_route(B, logits, bias, k, score_fn=score_fn, renormalize=renormalize, n_group=n_group, topk_group=topk_group,
+                    group_best=1)
+
+
+def test_route_of_zeros_agrees_with_the_plain_router(B):
+    logits = torch.where(torch.rand(40, 96, generator=torch.Generator().manual_seed(1)) < 0.5, -0.0, 0.0).cuda()
+    logits[:20] -= (torch.arange(96, device="cuda") % 7 > 1).float()
+    for score_fn, renorm in itertools.product(["sigmoid", "softmax"], [True, False]):
+        assert torch.equal(B.moe_route_topk(logits, 8, score_fn, renorm)[0], B.moe_route_grouped(logits, 8, score_fn, renorm)[0])

@@ -32,8 +32,10 @@ extern "C" {
  *      the k chosen s (0 if that sum is 0).  The bias is not in the weights.
  * The choice is that of c computed in float64, also where float32 scores
  * coincide; without a bias (and group_best = 1 or one group) it is that of v.
- * Weights are float32, within 1e-6 relative.  A NaN logit or bias counts as
- * -inf (as a score: 0), +inf as the largest float32.
+ * Weights are float32, within 1e-6 relative, also where the scores themselves
+ * are too small for float32.  A NaN logit or bias counts as -inf (as a score:
+ * 0), +inf as the largest float32; sigma(v) below v = -709.78, where e^-v
+ * leaves float64, counts as 0.
  * logits device float32 [T, E]; select_bias device float32 [E] or NULL;
  * topk_idx device int32 [T, k]; topk_w device float32 [T, k].
  * Limits: those of moe_route_topk; 1 <= n_group <= 32 divides E, 1 <=

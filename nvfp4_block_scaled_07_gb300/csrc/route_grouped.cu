@@ -209,6 +209,50 @@ __device__ __noinline__ int choose_among(const RouteParams& p, int t, float top,
   return lane < p.k ? from[lane] : 0;
 }
 
+// ---- the weights ------------------------------------------------------------------
+// x - top exactly, as its rounding and what that lost.
+struct Shifted {
+  float v, lost;
+};
+__device__ __forceinline__ Shifted shifted(float x, float top) {
+  const float d = x - top, back = d - x;
+  return {d, d > -INFINITY ? (x - (d - back)) + (-top - back) : 0.0f};
+}
+
+constexpr float kFar = -80.0f;                // below, exp(x) nears the end of float32's normal numbers
+// The factor is below e^70: e^-200 of anything is no float32 with it.
+constexpr float kFarthest = 200.0f;
+constexpr float kNoSigmoid = -709.78f;        // below, exp(-x) is no float64: a score of 0
+
+// A token's weights where scores leave float32's normal numbers, of a warp whose lane j holds the j-th chosen logit x
+// (-inf: none).  Scores are taken relative to e^ref, and one below e^-80 of that as a number with the factor e^-72, so
+// that neither the sum nor what a large factor brings back is lost.
+__device__ __noinline__ float far_weight(const RouteParams& p, float x, float top, float sum) {
+  float ref = top;
+  if (!p.softmax) {
+    if (x < kNoSigmoid) x = -INFINITY;
+    ref = 0.0f;
+    if (p.renorm) {                           // e^x / (1 + e^x): e^ref cancels
+      ref = fminf(value_of(__reduce_max_sync(kFull, key_of(x))), 0.0f);
+      if (ref == -INFINITY) ref = 0.0f;
+    }
+  }
+  const Shifted d = shifted(x, ref);
+  const float v = fminf(d.v, 0.0f);
+  const bool small = v < kFar;
+  float s = v > -kFarthest ? expf(small ? v + 72.0f : v) * (1.0f + d.lost) : 0.0f;   // v + 72 is exact
+  const float unit = small ? 5.3801861e-32f : 1.0f;                                  // e^-72
+  if (!p.softmax) s /= 1.0f + expf(-fabsf(x));
+  float f = p.factor;
+  if (p.renorm) {
+    const float all = warp_sum(s * unit);     // at least 1/2 if there is any
+    f = all > 0.0f ? f / all : 0.0f;
+  } else if (p.softmax) {
+    f = sum > 0.0f ? f / sum : 0.0f;          // the sum is at least 1
+  }
+  return f * s * unit;
+}
+
 // ---- the choice in float32 --------------------------------------------------------
 // A lane's experts are VPL consecutive ones.  WHOLE: a lane's are all of one
 // group, and a group is a power of two of lanes.
@@ -503,27 +547,31 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
 
   // weights of the chosen
   const bool mine = lane < p.k;
+  const float x = mine ? clean(row[my_e]) : -INFINITY;
   float s = 0.0f;
+  bool far;
   if (p.softmax) {
-    const float x = mine ? clean(row[my_e]) : -INFINITY;
     if (p.renorm) {                           // the whole softmax's sum cancels
       top = value_of(__reduce_max_sync(kFull, key_of(x)));
       if (top == -INFINITY) top = 0.0f;
     }
-    // x - top exactly, as its rounding and what that lost
-    const float d = x - top, back = d - x, lost = (x - (d - back)) + (-top - back);
-    s = mine && d > -200.0f ? expf(d) * (1.0f + lost) : 0.0f;
+    const Shifted d = shifted(x, top);
+    far = d.v < kFar && d.v > -kFarthest;
+    s = mine ? expf(d.v) * (1.0f + d.lost) : 0.0f;
     if (!p.renorm) s = sum > 0.0f ? s / sum : 0.0f;
-  } else if (mine) {
-    s = 1.0f / (1.0f + expf(-clean(row[my_e])));
+  } else {
+    far = x < kFar && x >= kNoSigmoid;
+    if (mine) s = 1.0f / (1.0f + expf(-x));
   }
   if (p.renorm) {
     const float all = warp_sum(s);
     s = all > 0.0f ? s / all : 0.0f;
   }
+  s *= p.factor;
+  if (__any_sync(kFull, far)) s = far_weight(p, x, top, sum);
   if (mine) {
     p.idx[int64_t(t) * p.k + lane] = my_e;
-    p.w[int64_t(t) * p.k + lane] = s * p.factor;
+    p.w[int64_t(t) * p.k + lane] = s;
   }
 }
 

@@ -92,3 +92,27 @@ def test_route_of_zeros_agrees_with_the_plain_router(B):
     logits[:20] -= (torch.arange(96, device="cuda") % 7 > 1).float()
     for score_fn, renorm in itertools.product(["sigmoid", "softmax"], [True, False]):
         assert torch.equal(B.moe_route_topk(logits, 8, score_fn, renorm)[0], B.moe_route_grouped(logits, 8, score_fn, renorm)[0])
+
+
+@pytest.mark.parametrize("score_fn,renormalize", list(itertools.product(["sigmoid", "softmax"], [True, False])))
+@pytest.mark.parametrize("scale", [2.5, -1.0, 9.9e29, 1e-20])
+def test_route_weights_of_logits_far_to_the_left(B, score_fn, renormalize, scale):
+    """Scores below float32's numbers: their ratios are the weights, and a large factor brings them back."""
+    g = torch.Generator().manual_seed(4)
+    logits = -90.0 - 60.0 * torch.rand(12, 64, generator=g)
+    logits[0] = -100.0 - torch.arange(64)
+    logits[1, :2] = torch.tensor([-90.0, -90.1])
+    logits[2] *= 4.0                               # down to -600
+    logits[3, 5] = -5.0
+    logits[4, 9] = 3.0
+    logits[5, ::2] = -float("inf")
+    logits[6] = -800.0 - torch.arange(64)          # below e^-709 a sigmoid counts as 0
+    logits[7] = torch.finfo(torch.float32).min
+    logits[7, 3] = -700.0
+    logits[8] = -16.0 - torch.rand(64, generator=g)
+    logits[9] = -80.0 - 16.0 * torch.rand(64, generator=g)
+    logits[10] = torch.finfo(torch.float32).min
+    logits[11] = 40.0 - 4.0 * torch.arange(64)
+    for bias in (None, 0.1 * torch.randn(64, generator=g)):
+        check_route(B, logits, bias, 4, score_fn=score_fn, renormalize=renormalize, scale=scale)
+        check_route(B, logits, bias, 30, score_fn=score_fn, renormalize=renormalize, scale=scale, n_group=8, topk_group=5)

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
       float b[VPL];
       load<VPL>(b, p.bias, e0, p.E, p.wide);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] = fmaxf(c[i] + b[i], -INFINITY);      // NaN: -inf
+      for (int i = 0; i < VPL; ++i) c[i] += clean(b[i]);                        // never +inf or NaN
     }
   }
   uint32_t key[VPL];
@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
 
   bool alike = false, sure = true, open = true;              // open (WHOLE): the lane's group is kept
   if (p.groups > 1) {
-    float value, size;                        // of group g, in lane g (not WHOLE) or the group's lanes; |c| of its parts
+    // of group g, in lane g (not WHOLE) or the group's lanes; |c| of its parts.  Sums of two as halves: biases of the
+    // type's lowest and largest value do not leave float32's range.
+    float value, size;
     const int lanes = WHOLE ? per / VPL : 1;
     if (WHOLE) {
       float a = c[0], b = -INFINITY;
@@ -343,8 +345,8 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
         b = fmaxf(fminf(a, oa), fmaxf(b, ob));
         a = fmaxf(a, oa);
       }
-      value = p.best == 2 ? a + b : a;
-      size = p.best == 2 ? fabsf(a) + fabsf(b) : fabsf(a);
+      value = p.best == 2 ? 0.5f * a + 0.5f * b : a;
+      size = p.best == 2 ? 0.5f * fabsf(a) + 0.5f * fabsf(b) : fabsf(a);
     } else {
       float* sh = s_group[warp];
 #pragma unroll
@@ -356,8 +358,8 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
         b = fmaxf(b, fminf(a, x));
         a = fmaxf(a, x);
       }
-      value = p.best == 2 ? a + b : a;
-      size = p.best == 2 ? fabsf(a) + fabsf(b) : fabsf(a);
+      value = p.best == 2 ? 0.5f * a + 0.5f * b : a;
+      size = p.best == 2 ? 0.5f * fabsf(a) + 0.5f * fabsf(b) : fabsf(a);
     }
     // lane g: group g's value and rank
     const float mine = __shfl_sync(kFull, value, (lane * lanes) & 31);
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
       const float high = value_of(__reduce_max_sync(kFull, lane < p.groups && !is_kept ? key_of(mine) : 0u));
       size = __shfl_sync(kFull, size, (lane * lanes) & 31);
       size = __uint_as_float(__reduce_max_sync(kFull, lane < p.groups ? __float_as_uint(size) : 0u));
-      const float span = 2.0f * (p.best * error + 0x1p-23f * size);       // the parts' rounding and the sum's
+      const float span = 2.0f * (error + 0x1p-22f * size);                // the parts' rounding and the sum's
       if (!(low - high > span) && !(alike = all_alike(p, row, lane))) {
         // Exact values of those that the order of float32 values leaves open, for the places
         // that the others do not take: lanes 2 j and 2 j + 1 take the j-th one's two experts.

@@ -116,3 +116,66 @@ def test_route_weights_of_logits_far_to_the_left(B, score_fn, renormalize, scale
     for bias in (None, 0.1 * torch.randn(64, generator=g)):
         check_route(B, logits, bias, 4, score_fn=score_fn, renormalize=renormalize, scale=scale)
         check_route(B, logits, bias, 30, score_fn=score_fn, renormalize=renormalize, scale=scale, n_group=8, topk_group=5)
+
+
+INF, MIN, MAX = float("inf"), torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+
+
+def bias_of(kind, E, n_group, g):
+    """Biases of which some are the type's ends; the others random."""
+    b = (0.1 * torch.randn(E, generator=g)).view(n_group, -1)
+    per = b.shape[1]
+    if kind == "one infinite, the rest masked":          # the sum of two is -inf: the last group
+        b[0, 0], b[0, 1:] = INF, -INF
+    elif kind == "one infinite":
+        b[n_group - 1, 0] = INF
+    elif kind == "infinite in several":
+        b[0, 0] = INF
+        b[1, :2] = INF
+        b[n_group - 1, per - 1] = MAX
+    elif kind == "all infinite":
+        b[:] = INF
+    elif kind == "all the largest":
+        b[:] = MAX
+    elif kind == "a group of the lowest":
+        b[1] = MIN
+    elif kind == "a group masked":
+        b[0] = -INF
+    elif kind == "lowest and masked":
+        b[0], b[1] = -INF, MIN
+        b[2:, 1:] = MIN
+    elif kind == "all but one masked":
+        b[:, 1:] = -INF
+    elif kind == "one expert left":
+        b[:] = -INF
+        b[n_group - 1, 1] = 0.0
+    elif kind == "-1e9":
+        b[1] = -1e9
+        b[2, 1:] = -1e9
+    elif kind == "nan":
+        b[0] = float("nan")
+        b[2, 0] = INF
+    return b.reshape(E)
+
+
+@pytest.mark.parametrize("kind", [
+    "one infinite, the rest masked", "one infinite", "infinite in several", "all infinite", "all the largest",
+    "a group of the lowest", "a group masked", "lowest and masked", "all but one masked", "one expert left", "-1e9", "nan"])
+@pytest.mark.parametrize("E,k,n_group,topk_group", [(8, 2, 4, 1), (32, 4, 4, 2), (64, 8, 8, 3), (64, 8, 32, 20), (40, 6, 4, 3),
+                                                    (256, 8, 8, 4), (512, 8, 4, 1)])
+def test_route_of_biases_at_the_ends_of_the_type(B, E, k, n_group, topk_group, kind):
+    """+inf is the largest float32, NaN is -inf, and sums are those of float64: (largest + largest) is above (largest + 1),
+    (lowest + lowest) above -inf."""
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randn(20, E, generator=g)
+    bias = bias_of(kind, E, n_group, g)
+    for score_fn, best, groups in itertools.product(["sigmoid", "softmax"], [2, 1], [n_group, 1]):
+        keep = topk_group if groups > 1 else 1
+        idx, w = B.moe_route_grouped(logits.cuda(), k, score_fn, select_bias=bias.cuda(), n_group=groups, topk_group=keep,
+                                     group_best=best)
+        for t in range(20):
+            ri, rw = R.route(logits[t], bias, k, score_fn, True, groups, keep, best, 1.0)
+            assert idx[t].tolist() == ri, (score_fn, best, groups, t)
+            ref = torch.tensor(rw, dtype=torch.float64)
+            assert ((w[t].double().cpu() - ref).abs() <= 1e-6 * ref).all()
+    B.sync_status()

@@ -18,10 +18,11 @@
 // of integer keys that order like the floats; the lowest lane with the maximum
 // has the lowest index.
 //
-// Bound by instructions (issue slots 74 % busy, DRAM 10 %): 16384 tokens of 256
-// experts take 20 us in 8 groups of which 4 are kept, 15 us without groups, one
-// token 3.1 us.  Choosing all groups again in float64 where two were close took
-// 31 us for the 16384.
+// Bound by the instructions that it spends on a token (issue slots 74 % busy, DRAM
+// 10 %): 16384 tokens of 256 experts take 21 us in 8 groups of which 4 are kept, 16.6
+// us without groups, 24 us with one group masked by its biases, one token 3.3 us.
+// Choosing all groups again in float64 where two were close took 31 us for the
+// 16384, and one bound for all groups, the widest, 299 us beside a masked one.
 #include <cfloat>
 #include <climits>
 #include <cstdint>
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
       float b[VPL];
       load<VPL>(b, p.bias, e0, p.E, p.wide);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] += clean(b[i]);                        // never +inf or NaN
+      for (int i = 0; i < VPL; ++i) c[i] = fminf(fmaxf(c[i] + b[i], -INFINITY), FLT_MAX);   // as of a clean bias
     }
   }
   uint32_t key[VPL];
@@ -327,11 +328,17 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
 #pragma unroll
   for (int i = 1; i < VPL; ++i) local = max(local, key[i]);
 
+  // Whether two keys in descending order (0: none) are those of experts in that order.  -inf is exact (a masked expert).
+  auto clear = [&](uint32_t before, uint32_t after) {
+    const float x = value_of(before), y = value_of(after);
+    return after == 0u || y == -INFINITY || x - y > 2.0f * error + 0x1p-22f * fmaxf(fabsf(x), fabsf(y));
+  };
+
   bool alike = false, sure = true, open = true;              // open (WHOLE): the lane's group is kept
   if (p.groups > 1) {
-    // of group g, in lane g (not WHOLE) or the group's lanes; |c| of its parts.  Sums of two as halves: biases of the
-    // type's lowest and largest value do not leave float32's range.
-    float value, size;
+    // of group g, in lane g (not WHOLE) or the group's lanes; and what it is off by: its parts' errors, their
+    // rounding, its own and that of its bounds.  Sums of two as halves: biases of the type's lowest and largest value do not leave float32's range.
+    float value, off;
     const int lanes = WHOLE ? per / VPL : 1;
     if (WHOLE) {
       float a = c[0], b = -INFINITY;
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
         a = fmaxf(a, oa);
       }
       value = p.best == 2 ? 0.5f * a + 0.5f * b : a;
-      size = p.best == 2 ? 0.5f * fabsf(a) + 0.5f * fabsf(b) : fabsf(a);
+      off = error + 0x1.8p-23f * (p.best == 2 ? 0.5f * fabsf(a) + 0.5f * fabsf(b) : fabsf(a));
     } else {
       float* sh = s_group[warp];
 #pragma unroll
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
         a = fmaxf(a, x);
       }
       value = p.best == 2 ? 0.5f * a + 0.5f * b : a;
-      size = p.best == 2 ? 0.5f * fabsf(a) + 0.5f * fabsf(b) : fabsf(a);
+      off = error + 0x1.8p-23f * (p.best == 2 ? 0.5f * fabsf(a) + 0.5f * fabsf(b) : fabsf(a));
     }
     // lane g: group g's value and rank
     const float mine = __shfl_sync(kFull, value, (lane * lanes) & 31);
@@ -370,15 +377,16 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
     }
     bool is_kept = lane < p.groups && rank < p.keep;
     if (!plain && p.keep < p.groups) {
-      const float low = value_of(__reduce_min_sync(kFull, is_kept ? key_of(mine) : kFull));
-      const float high = value_of(__reduce_max_sync(kFull, lane < p.groups && !is_kept ? key_of(mine) : 0u));
-      size = __shfl_sync(kFull, size, (lane * lanes) & 31);
-      size = __uint_as_float(__reduce_max_sync(kFull, lane < p.groups ? __float_as_uint(size) : 0u));
-      const float span = 2.0f * (error + 0x1p-22f * size);                // the parts' rounding and the sum's
-      if (!(low - high > span) && !(alike = all_alike(p, row, lane))) {
+      // -inf is exact (a masked expert), and a tie of two goes by their indexes, as the ranks do
+      off = __shfl_sync(kFull, off, (lane * lanes) & 31);
+      const bool masked = mine == -INFINITY;
+      const float least = masked ? mine : mine - off, most = masked ? mine : mine + off;
+      const float low = value_of(__reduce_min_sync(kFull, is_kept ? key_of(least) : kFull));
+      const float high = value_of(__reduce_max_sync(kFull, lane < p.groups && !is_kept ? key_of(most) : 0u));
+      if (low <= high && high > -INFINITY && !(alike = all_alike(p, row, lane))) {
         // Exact values of those that the order of float32 values leaves open, for the places
         // that the others do not take: lanes 2 j and 2 j + 1 take the j-th one's two experts.
-        const uint32_t near = __ballot_sync(kFull, lane < p.groups && (is_kept ? mine <= high + span : mine >= low - span));
+        const uint32_t near = __ballot_sync(kFull, lane < p.groups && (is_kept ? least <= high : !masked && most >= low));
         const int places = __popc(__ballot_sync(kFull, is_kept) & near), count = __popc(near);
         sure = count <= 16;
         int e = 0;
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
               if (n < p.best && lane == 2 * j + n) e = expert;
             }
             // and whether float32 tells which experts they are
-            sure = sure && (m == 0u || value_of(last) - value_of(m) > span);
+            sure = sure && clear(last, m);
           }
         }
         if (sure) {
@@ -485,23 +493,17 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
     my_e = s_expert[warp][lane];
     const uint32_t here = s_sorted[warp][lane], next = s_sorted[warp][lane + 1];
     last = value_of(__shfl_sync(kFull, here, p.k - 1));
-    if (!plain)
-      sure = sure && __all_sync(kFull, lane >= p.k || next == 0u || value_of(here) - value_of(next) >
-                                                                           2.0f * error + 0x1p-22f * fmaxf(fabsf(value_of(here)), fabsf(value_of(next))));
+    if (!plain) sure = sure && __all_sync(kFull, lane >= p.k || clear(here, next));
   } else {
     // many equal or hardly any lanes: k rounds of the warp's maximum
     uint32_t left[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) left[i] = open ? key[i] : 0u;
-    last = INFINITY;
-    auto margin = [&](uint32_t m) {           // to the one before
-      const float now = value_of(m);
-      sure = sure && (m == 0u || last - now > 2.0f * error + 0x1p-22f * fmaxf(fabsf(last), fabsf(now)) || last == INFINITY);
-    };
+    uint32_t before = 0u;
     for (int j = 0; j < p.k; ++j) {
       const uint32_t m = __reduce_max_sync(kFull, local);
-      if (!plain) margin(m);
-      last = value_of(m);
+      if (!plain && j > 0) sure = sure && clear(before, m);
+      before = m;
       const int from = __ffs(__ballot_sync(kFull, local == m)) - 1;
       int e = 0;
       if (lane == from) {
@@ -519,7 +521,8 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 5 : 1) route_grouped_k
       e = __shfl_sync(kFull, e, from);
       if (lane == j) my_e = e;
     }
-    if (!plain) margin(__reduce_max_sync(kFull, local));
+    last = value_of(before);
+    if (!plain) sure = sure && clear(before, __reduce_max_sync(kFull, local));
   }
   if (!sure) {
     // the exact k best are within 2 d of the k-th here

@@ -179,3 +179,17 @@ def test_route_of_biases_at_the_ends_of_the_type(B, E, k, n_group, topk_group, k
             ref = torch.tensor(rw, dtype=torch.float64)
             assert ((w[t].double().cpu() - ref).abs() <= 1e-6 * ref).all()
     B.sync_status()
+
+
+@pytest.mark.parametrize("mask", [-INF, MIN, -1e9, -1000.0])
+@pytest.mark.parametrize("spread", [1.0, 2.0 ** -13, 2.0 ** -20])
+def test_route_of_close_scores_beside_masked_groups(B, spread, mask):
+    """Groups that are close to one another and groups, or most of a group's experts, that are far below all."""
+    g = torch.Generator().manual_seed(7)
+    logits = 0.5 + spread * torch.randn(200, 64, generator=g)
+    logits[::4] = 0.5 + spread * torch.randint(0, 4, (50, 64), generator=g).float()
+    bias = spread * torch.randint(-3, 4, (64,), generator=g).float()
+    bias[8:16] = mask
+    bias[17:24] = mask
+    for score_fn, keep, best in itertools.product(["sigmoid", "softmax"], [2, 6], [1, 2]):
+        check_route(B, logits, bias, 8, score_fn=score_fn, n_group=8, topk_group=keep, group_best=best)

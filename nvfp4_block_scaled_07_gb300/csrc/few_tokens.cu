@@ -14,7 +14,8 @@
 // lies in 2^-10 .. 2688, so the product is exact.  E8M0 scales do not fit that
 // range: of the 256 values of a row that a step takes, the largest scale is
 // the reference 2^X, codes are multiplied by 2^(scale - X + 13), and the sum
-// by 2^(X - 13); what is smaller than 2^-27 of that reference counts as zero.
+// by 2^(X - 13).  Scales below 2^-27 of that reference, which hardly ever are, take
+// another pass over the step with the largest of them as its reference.
 // Activations become float16 too, in blocks of 256 values of a token that are
 // multiplied by the power of two which brings the largest into 2^14 .. 2^15:
 // exact for every bf16 or fp16 value above 2^-28 of its block's largest, and
@@ -68,6 +69,8 @@ struct FewParams {
   void* out;
   Plan* plan;
 };
+
+constexpr int kReach = 27;  // float16 takes scales down to 2^-27 of the largest
 
 // 32 bytes of each of a lane's four rows, and their scale words.
 struct Rows {
@@ -140,6 +143,57 @@ __device__ __forceinline__ void load_rows(Rows& r, const FewParams& p, const Lan
       for (int j = 0; j < 8; ++j) r.w[i][j] = 0;
     }
   }
+}
+
+// The products of a step's weights with the tokens' activations, in two tiles: `from` is this lane's part of them, m tokens'
+// pieces apart.  MX: scale(i, half) is a block's scale less its row's reference, as a power of two.
+template <bool MX, bool TWO, typename Scale>
+__device__ __forceinline__ void multiply(float (&acc)[2][4], const Rows& r, const Scale& scale, const uint8_t* from, int m,
+                                         int second, bool has) {
+  uint32_t sc[4];                       // the rows' scales of this word as float16 pairs
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (!MX && (j & 1) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t two = ue4m3x2_to_half(j < 4 ? r.s[i] : r.s[i] >> 16);
+        sc[i] = __byte_perm(two, two, (j & 2) ? 0x3232 : 0x1010);
+      }
+    }
+    if (MX && (j & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)       // exponent fields of 2^(scale - reference + 13), or 0
+        sc[i] = uint32_t(max(scale(i, j >> 2) + kReach + 1, 0)) * 0x04000400u;
+    }
+    uint32_t a[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      codes_to_half(r.w[i][j], a[i]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) a[i][q] = hmul2(a[i][q], sc[i]);
+    }
+#pragma unroll
+    for (int part = 0; part < (TWO ? 2 : 1); ++part) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (has) x = *reinterpret_cast<const uint4*>(from + part * second + j * m * 64);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mma(acc[i], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
+        mma(acc[i], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
+      }
+    }
+  }
+}
+
+// The largest of the four lanes that hold a row.
+__device__ __forceinline__ int row_max(int v) {
+  v = max(v, __shfl_xor_sync(kFull, v, 1));
+  return max(v, __shfl_xor_sync(kFull, v, 2));
+}
+
+// Whether a lane's block (half of its 32 bytes of a row) has codes other than 0.
+__device__ __forceinline__ bool has_codes(const uint32_t (&w)[8], int half) {
+  return ((w[4 * half] | w[4 * half + 1] | w[4 * half + 2] | w[4 * half + 3]) & 0x77777777u) != 0;
 }
 
 template <bool MX, int SRC, int MODE>
@@ -250,6 +304,32 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
   float total[2][4] = {};
   const int g = lane >> 2;
 
+  // A step's products into the totals, tokens of this expert only.
+  auto add = [&](const float (&acc)[2][4], const int (&ref)[4]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int t = 2 * l.tg + c;
+      if ((tokens >> t) & 1) {
+        const int slot = __popc(tokens & ((1u << t) - 1));
+        const float f = factor[(MODE == kDown ? base + slot : slot) * steps + step];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = acc[i >> 1][(i & 1) * 2 + c];
+          if (MX) {
+            if (ref[i] < 0) continue;          // nothing is left of this row
+            // 2^(ref - 127 - 13) as two factors of float32's normal range
+            const int x = ref[i] - 140;
+            v = ref[i] == 255 ? __int_as_float(0x7FFFFFFF) : v * exp2i(x >> 1);
+            total[i >> 1][(i & 1) * 2 + c] += v * f * exp2i(x - (x >> 1));
+          } else {
+            total[i >> 1][(i & 1) * 2 + c] += v * f;
+          }
+        }
+      }
+    }
+  };
+
+  bool again = false;                   // MX: scales were out of reach
   for (int u = warp; u < units; u += kWarps) {
     // the next step's weights on their way
     int nstep = step + kWarps, next = seg;
@@ -264,75 +344,69 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const FewParams p) {
     const uint8_t* from = smem + ((MODE == kDown ? base : 0) * steps + step * m) * kUnitBytes +
                           __popc(tokens & ((1u << g) - 1)) * 64 + l.tg * 16;
 
-    uint32_t ref[4];                    // MX: a row's largest scale of this step
+    int ref[4];                         // MX: a row's largest scale of this step
     if (MX) {
+      bool far = false;                 // and whether others are out of its reach
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t top = max(cur.s[i] & 255u, cur.s[i] >> 8);
-        top = max(top, __shfl_xor_sync(kFull, top, 1));
-        ref[i] = max(top, __shfl_xor_sync(kFull, top, 2));
+        const int x = cur.s[i] & 255u, y = cur.s[i] >> 8;
+        ref[i] = row_max(max(x, y));
+        far |= min(x, y) < ref[i] - kReach;
+      }
+      if (__any_sync(kFull, far)) {
+        far = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          far |= (int(cur.s[i] & 255u) < ref[i] - kReach && has_codes(cur.w[i], 0)) ||
+                 (int(cur.s[i] >> 8) < ref[i] - kReach && has_codes(cur.w[i], 1));
+        again |= __any_sync(kFull, far);
       }
     }
     float acc[2][4] = {};
-    uint32_t sc[4];                     // the rows' scales of this word as float16 pairs
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!MX && (j & 1) == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t two = ue4m3x2_to_half(j < 4 ? cur.s[i] : cur.s[i] >> 16);
-          sc[i] = __byte_perm(two, two, (j & 2) ? 0x3232 : 0x1010);
-        }
-      }
-      if (MX && (j & 3) == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int x = int(j < 4 ? cur.s[i] & 255u : cur.s[i] >> 8) - int(ref[i]) + 28;
-          sc[i] = uint32_t(max(x, 0)) * 0x04000400u;   // exponent fields of 2^(scale - reference + 13), or 0
-        }
-      }
-      uint32_t a[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        codes_to_half(cur.w[i][j], a[i]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) a[i][q] = hmul2(a[i][q], sc[i]);
-      }
-#pragma unroll
-      for (int part = 0; part < (kTwo ? 2 : 1); ++part) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (has) x = *reinterpret_cast<const uint4*>(from + part * second + j * m * 64);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mma(acc[i], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], x.x, x.y);
-          mma(acc[i], a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3], x.z, x.w);
-        }
-      }
-    }
-    // into the totals, tokens of this expert only
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int t = 2 * l.tg + c;
-      if ((tokens >> t) & 1) {
-        const int slot = __popc(tokens & ((1u << t) - 1));
-        const float f = factor[(MODE == kDown ? base + slot : slot) * steps + step];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = acc[i >> 1][(i & 1) * 2 + c];
-          if (MX) {
-            // 2^(ref - 127 - 13) as two factors of float32's normal range
-            const int x = int(ref[i]) - 140;
-            v = ref[i] == 255 ? __int_as_float(0x7FFFFFFF) : v * exp2i(x >> 1);
-            total[i >> 1][(i & 1) * 2 + c] += v * f * exp2i(x - (x >> 1));
-          } else {
-            total[i >> 1][(i & 1) * 2 + c] += v * f;
-          }
-        }
-      }
-    }
+    multiply<MX, kTwo>(acc, cur, [&](int i, int half) { return int(half ? cur.s[i] >> 8 : cur.s[i] & 255u) - ref[i]; }, from, m,
+                       second, has);
+    add(acc, ref);
     cur = nxt;
     step = nstep;
     seg = next;
+  }
+
+  // MX: the blocks whose scales were out of reach, pass by pass, each with the largest scale that is left as a reference.
+  if (MX && again) {
+    constexpr int kDone = -512;         // below every scale and its reach
+    step = warp, seg = 0;
+    for (int u = warp; u < units; u += kWarps, step += kWarps) {
+      while (step >= steps) step -= steps, ++seg;
+      load_rows<MX>(cur, p, l, MODE == kDown ? s_expert[seg] : e, step);
+      if (MODE == kDown) tokens = s_tokens[seg], base = s_base[seg];
+      const int m = __popc(tokens);
+      const bool has = (tokens >> g) & 1;
+      const uint8_t* from = smem + ((MODE == kDown ? base : 0) * steps + step * m) * kUnitBytes +
+                            __popc(tokens & ((1u << g) - 1)) * 64 + l.tg * 16;
+      int s[4][2], ref[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[i][0] = has_codes(cur.w[i], 0) ? int(cur.s[i] & 255u) : kDone;
+        s[i][1] = has_codes(cur.w[i], 1) ? int(cur.s[i] >> 8) : kDone;
+        ref[i] = row_max(max(cur.s[i] & 255u, cur.s[i] >> 8));
+      }
+#pragma unroll 1
+      for (int pass = 0; pass < 8; ++pass) {   // a row has eight blocks in a step, of which a pass ends one or more
+        bool left = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (s[i][h] >= ref[i] - kReach) s[i][h] = kDone;
+          ref[i] = row_max(max(s[i][0], s[i][1]));
+          left |= ref[i] != kDone;
+        }
+        if (!__any_sync(kFull, left)) break;
+        float acc[2][4] = {};
+        multiply<MX, kTwo>(acc, cur, [&](int i, int half) { return s[i][half] - ref[i]; }, from, m, second, has);
+        add(acc, ref);
+      }
+    }
   }
 
   // Joins the warps along the columns: [warp][tile][row 0..15][8 tokens].

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from . import few_reference as R
-from .test_gpu_few import check_route, experts, normal, on_gpu, routing
+from .test_gpu_few import check_route, experts, matvec, normal, on_gpu, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -64,6 +64,63 @@ def test_experts_of_many_rows_of_few_tokens(B, T, k, fmt):
     gu, d = R.Matrices(40, 256, 128, fmt, seed=T), R.Matrices(40, 128, 128, fmt, seed=T + 1)
     x, (idx, w) = normal(T, 128, seed=k), routing(T, 40, k, seed=k)
     out = experts(B, fmt, x.cuda(), idx.cuda(), w.cuda(), on_gpu(B, gu, True), on_gpu(B, d, True))
+    ref, tol = R.experts(x, idx, w, gu, d)
+    R.check(out, ref, tol)
+
+
+# ---- MXFP4 scales far apart -----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("T,N,K", [(1, 128, 512), (5, 256, 1280), (8, 128, 384), (9, 128, 512), (20, 256, 640)])
+@pytest.mark.parametrize("far", [28, 60, 120])
+def test_mxfp4_scales_far_apart_in_a_row(B, T, N, K, far):
+    """Blocks with large scales meet activations of 0: what is left comes from blocks 2^-28 and less of them, and counts."""
+    m = R.Matrices(1, N, K, "mxfp4", seed=far)
+    x = normal(T, K, seed=2).view(T, -1, 32).clone()
+    large = torch.arange(K // 32) % 3 == 1
+    m.scales[:, :, large] = 127 + far // 2
+    m.scales[:, :, ~large] = 127 + far // 2 - far
+    m.scales[:, ::5, ~large] -= 3
+    x[:, large] = 0
+    x = x.view(T, K)
+    y = matvec(B, "mxfp4", x.cuda(), on_gpu(B, m, True))
+    keep = m.values(0) * (~large).repeat_interleave(32)
+    ref, tol = R.product(x.double(), keep)
+    R.check(y, ref, tol + R.half_step(x.dtype) * (ref.abs() + tol) + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("T", [1, 4, 8])
+def test_mxfp4_scales_of_every_size_in_a_row(B, T):
+    """Scales from 2^-100 to 2^100 side by side, the activations of each block small where its scale is large."""
+    K = 768
+    m = R.Matrices(1, 128, K, "mxfp4", seed=3)
+    e = torch.tensor([(i * 37) % 201 - 100 for i in range(K // 32)])
+    m.scales[:] = (127 + e).to(torch.uint8)
+    for i in range(K // 32):                      # one block at a time: the others meet zeros
+        x = torch.zeros(T, K // 32, 32)
+        x[:, i] = normal(T, 32, seed=i).float() * 2.0 ** (-float(e[i]))
+        x = x.view(T, K).to(torch.bfloat16)
+        y = matvec(B, "mxfp4", x.cuda(), on_gpu(B, m, False))
+        keep = torch.zeros_like(m.values(0))
+        keep[:, 32 * i:32 * i + 32] = m.values(0)[:, 32 * i:32 * i + 32]
+        ref, tol = R.product(x.double(), keep)
+        R.check(y, ref, tol + R.half_step(x.dtype) * (ref.abs() + tol), f"block {i}")
+
+
+@pytest.mark.parametrize("T", [1, 4, 8])
+def test_mxfp4_experts_with_scales_far_apart(B, T):
+    """In both products: x is 0 where the gate's and up's scales are large, h where the down matrix's are."""
+    E, k, H, I, far = 3, 2, 512, 384, 60
+    gu, d = R.Matrices(E, 2 * I, H, "mxfp4", seed=1), R.Matrices(E, H, I, "mxfp4", seed=2)
+    x, (idx, w) = normal(T, H, seed=4), routing(T, E, k, seed=T)
+    large = torch.arange(H // 32) % 3 == 1
+    gu.scales[:, :, large] += far
+    x.view(T, -1, 32)[:, large] = 0
+    large = torch.arange(I // 32) % 4 == 2
+    d.scales[:, :, large] += far
+    gu.packed[:, I:][:, large.repeat_interleave(32)] = 0
+    out = experts(B, "mxfp4", x.cuda(), idx.cuda(), w.cuda(), on_gpu(B, gu, True), on_gpu(B, d, True))
+    # the reference on matrices without the blocks that meet zeros: its bounds are those of the others
+    gu.scales[:, :, torch.arange(H // 32) % 3 == 1] -= far
+    d.scales[:, :, large] -= far
     ref, tol = R.experts(x, idx, w, gu, d)
     R.check(out, ref, tol)
 

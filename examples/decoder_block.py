@@ -73,7 +73,6 @@ class Stepper:
             self.graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(self.graph, stream=side):
                 self.y = self._step()
-        self.buffers = dict(vars(block.experts))     # the graph's, which the layer replaces at another batch size
         torch.cuda.current_stream().wait_stream(side)
         for t, was in zip((self.lens, tables, free_count), state):
             t.copy_(was)

@@ -863,7 +863,10 @@ class MoELayer:
     allocated for one batch size T (at construction when T is given, else at
     the first call, and again when T changes); otherwise forward() allocates
     nothing, and the tensor it returns is overwritten by the next call
-    unless the caller passes `out`.  With fused_prepare (the default):
+    unless the caller passes `out`.  Buffers that a CUDA graph has captured
+    (capture(), or a forward() or one of its steps inside a capture of the
+    caller's) stay allocated when T changes: the first with the graph, the
+    others with the layer.  With fused_prepare (the default):
     moe_prepare (route + quantise + permute; moe_prepare_mxfp4 for
     fmt="mxfp4"), the gate/up GEMM with SwiGLU and requantisation, the down
     GEMM and finalize -- otherwise the six separate calls.
@@ -931,10 +934,25 @@ class MoELayer:
             self.w_d_packed = tile_expert_weights(self.w_d_packed)
         self.h_scale = torch.full((1,), h_scale, dtype=torch.float32, device=self.device)
         self.T = None
+        self._captured, self._kept = False, []     # whether a graph holds the buffers' addresses; earlier ones that one holds
         if T is not None:
             self._alloc(T)
 
+    # what _alloc makes for a batch size
+    _BUFFERS = ("topk_idx", "topk_w", "r_ws", "out", "few_ws", "x_gscale", "xq", "xs", "q_ws", "perm", "p_ws", "prep_ws",
+                "hq", "hs", "y", "acc")
+
+    def _buffers(self):
+        return {name: getattr(self, name, None) for name in self._BUFFERS}
+
+    def _note_capture(self):
+        if torch.cuda.is_current_stream_capturing():
+            self._captured = True
+
     def _alloc(self, T):
+        if self._captured:
+            self._kept.append(self._buffers())
+            self._captured = False
         dev, E, k, H, I = self.device, self.E, self.k, self.H, self.I
         self.T = T
         self.topk_idx = _empty((T, k), torch.int32, dev)
@@ -961,6 +979,7 @@ class MoELayer:
 
     # ---- the steps of forward() (bench.py times them one by one) ----
     def _has_steps(self):
+        self._note_capture()
         if self.few:
             raise ValueError(f"a batch of {self.T} tokens (few_tokens {self.few_tokens}) has no separate steps")
 
@@ -1054,6 +1073,7 @@ class MoELayer:
     __call__ = forward
 
     def _forward_few(self, x, logits, out=None):
+        self._note_capture()
         out = self.out if out is None else out
         self._route(logits)
         if self.fmt == "mxfp4":
@@ -1067,7 +1087,10 @@ class MoELayer:
         graph and returns it; graph.replay() then runs the whole layer (every
         kernel launch of prepare, both GEMM plans and finalize) with no host
         work per step, reading x and logits where they are and writing
-        self.out.  Copy each step's inputs into x and logits before replaying.
+        graph.out (self.out until the batch size changes).  Copy each step's
+        inputs into x and logits before replaying.  The graph keeps x, logits,
+        the layer and the buffers of this batch size alive, so other batches may
+        run between replays.
         The launch plans for x's batch size are chosen first (autotune, which
         synchronises); nothing in forward() synchronises or allocates, so the
         capture holds exactly the eager launches."""
@@ -1078,6 +1101,7 @@ class MoELayer:
             self.autotune(x, logits)
         side = torch.cuda.Stream(device=self.device) if stream is None else stream
         side.wait_stream(torch.cuda.current_stream(self.device))
+        captured = self._captured
         with torch.cuda.stream(side):
             self.forward(x, logits)      # one eager step on the capture stream first
             side.synchronize()
@@ -1085,6 +1109,8 @@ class MoELayer:
             with torch.cuda.graph(graph, stream=side):
                 self.forward(x, logits)
         torch.cuda.current_stream(self.device).wait_stream(side)
+        graph.out, graph.holds = self.out, (self, x, logits, self._buffers())
+        self._captured = captured         # this graph holds the buffers by itself
         return graph
 
     # ---- tile autotuner ----

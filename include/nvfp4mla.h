@@ -71,9 +71,10 @@ extern "C" {
  * end; these and tokens past row T raise NVFP4MOE_ERR_DEVICE_DATA.
  * past_lens, new_lens, seq_lens, granted device int32 [B]; block_tables device
  * int32 [B, max_pages], rows table_stride apart; free_pages device int32
- * [num_free]; positions device int32 [T], slots device int64 [T]; outputs must
- * not overlap anything else.  Limits: B, T, max_pages, num_free >= 0, page_size
- * a power of two >= 16. */
+ * [num_free]; positions device int32 [T], slots device int64 [T].  In place:
+ * seq_lens may be past_lens, granted new_lens and free_count_out free_count;
+ * outputs and tables that share memory otherwise are refused.  Limits: B, T,
+ * max_pages, num_free >= 0, page_size a power of two >= 16. */
 int mla_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size,
              int32_t* block_tables, int64_t table_stride, int max_pages,
              const int32_t* free_pages, int num_free, const int32_t* free_count, int T,

@@ -901,6 +901,21 @@ int mla_append(const void* latent, int64_t latent_stride, const void* k_rope, in
   return cuda_status(launch_mla_append(a, stream), "mla_append launch");
 }
 
+// Whether two arrays share memory.
+static bool share(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a_bytes > 0 && b_bytes > 0 && x < y + uint64_t(b_bytes) && y < x + uint64_t(a_bytes);
+}
+
+// Whether an array shares memory with one of n rows that lie `step` >= `row` bytes apart.
+static bool share_rows(const void* a, int64_t a_bytes, const void* rows, int64_t n, int64_t row, int64_t step) {
+  if (n <= 0 || row <= 0 || a_bytes <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(rows);
+  if (x + uint64_t(a_bytes) <= y) return false;
+  const uint64_t first = x < y + uint64_t(row) ? 0 : (x - y - uint64_t(row)) / uint64_t(step) + 1;   // that ends after a's begin
+  return first < uint64_t(n) && y + first * uint64_t(step) < x + uint64_t(a_bytes);
+}
+
 int mla_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_tables,
              int64_t table_stride, int max_pages, const int32_t* free_pages, int num_free, const int32_t* free_count, int T,
              int32_t* positions, int64_t* slots, int32_t* cu_seqlens, int32_t* seq_lens, int32_t* granted,
@@ -921,6 +936,34 @@ int mla_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_
   for (const void* w : words)
     NVFP4MOE_REQUIRE((reinterpret_cast<uintptr_t>(w) & 3) == 0, NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
   NVFP4MOE_REQUIRE((reinterpret_cast<uintptr_t>(slots) & 7) == 0, NVFP4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  struct Array {
+    const char* name;
+    const void* at;
+    int64_t bytes;
+  };
+  const Array outs[] = {{"positions", positions, int64_t(T) * 4},     {"slots", slots, int64_t(T) * 8},
+                        {"cu_seqlens", cu_seqlens, (int64_t(B) + 1) * 4}, {"seq_lens", seq_lens, int64_t(B) * 4},
+                        {"granted", granted, int64_t(B) * 4},         {"free_count_out", free_count_out, 4}};
+  const Array ins[] = {{"past_lens", past_lens, int64_t(B) * 4},
+                       {"new_lens", new_lens, int64_t(B) * 4},
+                       {"free_pages", free_pages, int64_t(num_free) * 4},
+                       {"free_count", free_count, 4}};
+  for (int i = 0; i < 6; ++i) {
+    const Array& o = outs[i];
+    for (const Array& in : ins)
+      NVFP4MOE_REQUIRE(!share(o.at, o.bytes, in.at, in.bytes) ||
+                           (o.at == in.at && ((o.at == seq_lens && in.at == past_lens) || (o.at == granted && in.at == new_lens) ||
+                                              (o.at == free_count_out && in.at == free_count))),
+                       NVFP4MOE_ERR_INVALID_ARG, "%s overlaps %s", o.name, in.name);
+    for (int j = 0; j < i; ++j)
+      NVFP4MOE_REQUIRE(!share(o.at, o.bytes, outs[j].at, outs[j].bytes), NVFP4MOE_ERR_INVALID_ARG, "%s overlaps %s", o.name,
+                       outs[j].name);
+    NVFP4MOE_REQUIRE(!share_rows(o.at, o.bytes, block_tables, B, int64_t(max_pages) * 4, table_stride * 4),
+                     NVFP4MOE_ERR_INVALID_ARG, "%s overlaps block_tables", o.name);
+  }
+  for (const Array& in : ins)
+    NVFP4MOE_REQUIRE(!share_rows(in.at, in.bytes, block_tables, B, int64_t(max_pages) * 4, table_stride * 4),
+                     NVFP4MOE_ERR_INVALID_ARG, "%s overlaps block_tables", in.name);
   DeviceInfo d;
   if (int st = current_device(&d)) return st;
   MlaPlanArgs a;

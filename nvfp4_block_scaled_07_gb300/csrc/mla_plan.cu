@@ -244,8 +244,9 @@ __global__ void __launch_bounds__(256) plan_tokens_kernel(const MlaPlanArgs p) {
     }
     position[j] = 0, id[j] = -1;
     if (b < p.B) {
-      position[j] = int64_t(max(p.past[b], 0)) + t[j] - p.cu_seqlens[b];
-      if (p.granted[b] > 0) id[j] = p.tables[b * p.table_stride + (position[j] >> p.shift)];
+      const int granted = p.granted[b];       // seq_lens - granted: the tokens before; past_lens may be seq_lens itself
+      position[j] = int64_t(p.seq_lens[b]) - granted + t[j] - p.cu_seqlens[b];
+      if (granted > 0) id[j] = p.tables[b * p.table_stride + (position[j] >> p.shift)];
     }
   }
 #pragma unroll

@@ -132,7 +132,9 @@ def mla_plan(past_lens, new_lens, block_tables, free_pages, free_count, page_siz
     free_pages int32 [n] with free_count int32 [1] of them free, popped from the
     end; tokens: rows of the step's buffers (those past the last token get slot
     -1).  A request whose pages are not there is refused: granted 0, slots -1.
-    Returns a TokenPlan (`out`, if given)."""
+    Returns a TokenPlan (`out`, if given).  out.seq_lens may be past_lens,
+    out.granted new_lens and out.free_count free_count; outputs that share
+    memory otherwise, with one another, the inputs or the tables, are refused."""
     dev = past_lens.get_device()
     _on_cuda(dev, "past_lens")
     B = past_lens.shape[0]

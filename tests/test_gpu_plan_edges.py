@@ -1,0 +1,86 @@
+"""mla_plan in place: lengths, grants and the count of free pages updated where they are."""
+import pytest
+import torch
+
+from . import few_reference as R
+from .test_gpu_plan import I32, M, case  # noqa: F401  (M is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,most,page", [(1, 1, 16), (5, 40, 16), (700, 3, 16), (40, 900, 64), (300, 30, 64), (2000, 70, 128)])
+@pytest.mark.parametrize("share", [0.6, 1.5])
+def test_plan_in_place(M, B, most, page, share):  # noqa: F811
+    """seq_lens into past_lens, granted into new_lens, the count into itself: with one kernel and with two."""
+    g = torch.Generator().manual_seed(B)
+    past = torch.randint(0, 500, (B,), generator=g).tolist()
+    new = torch.randint(1, most + 1, (B,), generator=g).tolist()
+    if B > 3:
+        past[2] = -5
+        new[3] = 0
+    need = sum(-(-(max(p, 0) + n) // page) - -(-max(p, 0) // page) for p, n in zip(past, new))
+    c = case([max(p, 0) for p in past], new, page, free=int(share * need) + 1, seed=B, T=sum(new) + 3) | dict(past=past)
+    lens, fresh = torch.tensor(past, **I32), torch.tensor(new, **I32)
+    tables, free, count = torch.tensor(c["tables"], **I32), torch.tensor(c["free"], **I32), torch.tensor([len(c["free"])], **I32)
+    out = M.alloc_token_plan(B, c["T"], "cuda", count)
+    out.seq_lens, out.granted = lens, fresh
+    M.mla_plan(lens, fresh, tables, free, count, page, c["T"], out=out)
+    if B > 3:
+        with pytest.raises(M.Nvfp4MoeError) as e:
+            M.sync_status()
+        assert e.value.status == 7
+    M.sync_status()
+    want_tables = [list(r) for r in c["tables"]]
+    want = R.plan(past, new, want_tables, c["free"], len(c["free"]), page, c["T"])
+    for name, value in want.items():
+        assert getattr(out, name).tolist() == value, name
+    assert tables.tolist() == want_tables
+
+
+def test_plan_refuses_outputs_that_overlap(M):  # noqa: F811
+    B, T = 4, 16
+    buf = torch.zeros(64, **I32)
+    tables, free, count = torch.full((B, 4), -1, **I32), torch.arange(8, **I32), torch.tensor([8], **I32)
+    lens, new = buf[:4], torch.ones(4, **I32)
+    for name, part in (("seq_lens", buf[1:5]), ("granted", buf[3:7]), ("cu_seqlens", buf[2:7]), ("positions", buf[:16]),
+                       ("free_count", buf[:1]), ("free_count", free[:1]), ("granted", tables[1])):
+        out = M.alloc_token_plan(B, T, "cuda")
+        setattr(out, name, part)
+        with pytest.raises(M.Nvfp4MoeError) as e:
+            M.mla_plan(lens, new, tables, free, count, 16, T, out=out)
+        assert e.value.status == 1 and "overlaps" in str(e.value)
+    assert (buf == 0).all() and (tables == -1).all() and count.item() == 8
+    M.sync_status()
+
+
+def test_steps_of_several_tokens_in_a_graph_in_place(M):  # noqa: F811
+    """A replayed step whose lengths are its own input: 200 requests of seven tokens, two kernels."""
+    page, B, n = 16, 200, 7
+    g = torch.Generator().manual_seed(2)
+    lens0 = torch.randint(0, 40, (B,), generator=g).tolist()
+    c = case(lens0, [60] * B, page, free=600, seed=1)
+    lens, new = torch.tensor(lens0, **I32), torch.full((B,), n, **I32)
+    tables, free, count = torch.tensor(c["tables"], **I32), torch.tensor(c["free"], **I32), torch.tensor([600], **I32)
+    T = B * n + 300
+    out = M.alloc_token_plan(B, T, "cuda", count)
+    out.seq_lens = lens
+    start = [t.clone() for t in (lens, tables, count)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        M.mla_plan(lens, new, tables, free, count, page, T, out=out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            M.mla_plan(lens, new, tables, free, count, page, T, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    for t, s in zip((lens, tables, count), start):
+        t.copy_(s)
+    now, want, left = lens0, [list(r) for r in c["tables"]], 600
+    for _ in range(6):
+        graph.replay()
+        ref = R.plan(now, [n] * B, want, c["free"], left, page, T)
+        assert out.slots.tolist() == ref["slots"] and out.positions.tolist() == ref["positions"]
+        assert tables.tolist() == want and count.tolist() == ref["free_count"]
+        now, left = ref["seq_lens"], ref["free_count"][0]
+        assert lens.tolist() == now
+    M.sync_status()

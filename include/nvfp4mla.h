@@ -53,7 +53,8 @@ extern "C" {
  * gets them as entries ceil(past / page_size) .. of its row of block_tables.
  * A request is refused as a whole (no page, no slot) when the pages that it
  * and the requests before it miss are more than free_count, its tokens more
- * than max_pages hold, or its last token past row T; the first leaves the
+ * than max_pages hold (or past + n more than 2^31 - 1), or its last token past
+ * row T; the first leaves the
  * later requests that miss no page as they are, the second and third miss
  * nothing.
  *   granted[b]     n, or 0 of a refused request

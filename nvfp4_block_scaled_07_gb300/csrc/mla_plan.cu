@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const MlaPlanArgs p, 
       fresh = fresh < 0 ? 0 : fresh;
     }
     const int64_t held = (past + page - 1) >> p.shift, after = (past + fresh + page - 1) >> p.shift;
-    const bool short_table = after > p.max_pages;
+    const bool short_table = after > p.max_pages || past + fresh > INT_MAX;    // a length has 31 bits
     int64_t need = short_table ? 0 : after - held;
     int64_t piece_tokens, piece_pages, upto, asked;
     bool rows = true;                         // the request's tokens have rows

@@ -1,4 +1,4 @@
-"""mla_plan in place: lengths, grants and the count of free pages updated where they are."""
+"""mla_plan in place (lengths, grants and the count of free pages updated where they are), and at the ends of its ranges."""
 import pytest
 import torch
 
@@ -84,3 +84,30 @@ def test_steps_of_several_tokens_in_a_graph_in_place(M):  # noqa: F811
         now, left = ref["seq_lens"], ref["free_count"][0]
         assert lens.tolist() == now
     M.sync_status()
+
+
+@pytest.mark.parametrize("new", [1, 2, 3, 12, 3000])
+def test_plan_of_the_longest_requests(M, new):  # noqa: F811
+    """Lengths up to 2^31 - 1, in large pages; a request that would pass that is refused, the others go on."""
+    page, top = 1 << 20, 2 ** 31 - 1
+    past = [top - 2, 5, top - new, top, top - 1]
+    tables = torch.full((5, 2049), -1, **I32)
+    tables[:, :2048] = torch.arange(2048, **I32)
+    tables[1] = -1
+    tables[1, 0] = 7
+    want_tables = tables.tolist()
+    free, T = list(range(3000, 3010)), 5 * new + 2
+    p = M.mla_plan(torch.tensor(past, **I32), torch.full((5,), new, **I32), tables, torch.tensor(free, **I32),
+                   torch.tensor([10], **I32), page, T)
+    M.sync_status()
+    granted = [new if q + new <= top else 0 for q in past]
+    assert p.granted.tolist() == granted and p.granted.tolist()[1:4] == [new, new, 0]
+    assert p.seq_lens.tolist() == [q + n for q, n in zip(past, granted)]
+    assert p.cu_seqlens.tolist() == [i * new for i in range(6)] and p.free_count.item() == 10
+    slots, positions = p.slots.tolist(), p.positions.tolist()
+    for b, q in enumerate(past):
+        for i in range(0, new, max(1, new // 5)):
+            t, at = b * new + i, q + i
+            assert positions[t] == min(at, top)
+            assert slots[t] == ((7 if b == 1 else at // page) * page + at % page if granted[b] else -1)
+    assert slots[-2:] == [-1, -1] and tables.tolist() == want_tables

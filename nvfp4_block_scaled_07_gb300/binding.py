@@ -896,6 +896,12 @@ class MoELayer:
         self.grouped = n_group != 1 or select_bias is not None or routed_scale != 1.0
         if self.grouped and (bias is not None or (k_primary is not None and k_primary < k)):
             raise ValueError("groups, select_bias and routed_scale exclude bias and k_primary")
+        if not 1 <= topk_group <= n_group or group_best not in (1, 2):
+            raise ValueError(f"topk_group {topk_group} outside [1, n_group = {n_group}] or group_best {group_best} not 1 or 2")
+        if n_group > 1 and (w_gu.shape[0] % n_group or group_best * n_group > w_gu.shape[0] or
+                            k * n_group > topk_group * w_gu.shape[0]):
+            raise ValueError(f"{n_group} groups of {w_gu.shape[0]} experts, of which {topk_group} are kept, by their {group_best} "
+                             f"best, for {k} a token")
         if not 0 <= few_tokens <= FEW_MAX_TOKENS:
             raise ValueError(f"few_tokens {few_tokens} outside [0, {FEW_MAX_TOKENS}]")
         self.select_bias, self.n_group, self.topk_group, self.group_best = select_bias, n_group, topk_group, group_best

@@ -77,3 +77,19 @@ def test_captured_steps_outlive_other_batches(layer):
     step(moe, 3)
     gc.collect()
     assert all(r() is not None for r in held.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(topk_group=2), dict(topk_group=0), dict(group_best=3), dict(group_best=0), dict(n_group=4, topk_group=5),
+    dict(n_group=3), dict(n_group=8), dict(n_group=16, group_best=1), dict(n_group=8, topk_group=1, group_best=1),
+    dict(n_group=4, topk_group=0)])
+def test_groups_that_do_not_fit_are_refused(layer, kw):
+    """At construction: without groups too, where they would be passed over in silence."""
+    with pytest.raises(ValueError, match="group"):
+        layer(**kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(group_best=1), dict(n_group=4), dict(n_group=8, topk_group=2, group_best=1),
+                                dict(n_group=2, topk_group=2), dict(n_group=1, topk_group=1, routed_scale=2.0)])
+def test_groups_that_fit(layer, kw):
+    assert layer(**kw).few_tokens == 8

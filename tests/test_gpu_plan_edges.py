@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from . import few_reference as R
-from .test_gpu_plan import I32, M, case  # noqa: F401  (M is a fixture)
+from .test_gpu_plan import I32, M, case, check  # noqa: F401  (M is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,42 @@ def test_plan_of_the_longest_requests(M, new):  # noqa: F811
             assert positions[t] == min(at, top)
             assert slots[t] == ((7 if b == 1 else at // page) * page + at % page if granted[b] else -1)
     assert slots[-2:] == [-1, -1] and tables.tolist() == want_tables
+
+
+BORDER = 1 << 20          # rows and free pages up to which tokens and pages share one scan
+
+
+def many(c, num_free, count):
+    """The case with a free list of num_free pages, of which the first `count` are free."""
+    own = c["free"][:count]
+    return c | dict(free=own + list(range(10 ** 7, 10 ** 7 + num_free - len(own)))), len(own)
+
+
+@pytest.mark.parametrize("num_free,T", [(BORDER - 1, 40), (BORDER, 40), (BORDER + 1, 40), (9, BORDER), (9, BORDER + 1), (9, BORDER + 3000),
+                                        (BORDER + 1, BORDER + 1)])
+@pytest.mark.parametrize("kind", ["few", "many tokens", "many requests", "refused"])
+def test_plan_around_the_border_of_one_scan(M, num_free, T, kind):  # noqa: F811
+    """Few valid requests among many free pages or padded rows, on both sides of the border."""
+    if kind == "few":
+        c, bad = case([14, 0, 31, 16], [3, 1, 0, 8], 16, free=9), False
+    elif kind == "many tokens":               # a request of more tokens than its thread writes by itself
+        c, bad = case([14, 0, 31], [20, 2, 17], 16, free=9), False
+    elif kind == "many requests":             # several pieces
+        new = [1] * 30 + [0] * 2000 + [1] * 9
+        c, bad = case([15 + i % 3 for i in range(len(new))], new, 16, free=9), False
+    else:                                     # tokens past the rows
+        c, bad = case([14, 0, 31, 5], [3, T, 2, 1], 16, free=9), True
+        for row in c["tables"]:
+            del row[4:]
+    c, count = many(c | dict(T=T), num_free, 9)
+    check(M, c, count=count, bad=bad)
+
+
+@pytest.mark.parametrize("free", [0, 3, 19, 20, 21])
+def test_plan_of_a_request_that_misses_more_than_all_pages(M, free):  # noqa: F811
+    """Those after it that miss none go on; the others miss what it asked for too."""
+    for tail in ([1, 2], [1] * 40):
+        past = [0, 20, 16] + [17] * len(tail)
+        p = check(M, case(past, [320, 5, 1] + tail, 16, free=free))
+        assert p.granted.tolist()[0] == (320 if free >= 20 else 0) and p.granted.tolist()[1] == 5
+        assert p.granted.tolist()[2] == (1 if free >= 21 else 0) and p.granted.tolist()[3:] == tail

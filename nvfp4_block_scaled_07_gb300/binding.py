@@ -880,8 +880,8 @@ class MoELayer:
     with the given tile_n.
 
     n_group, topk_group, group_best, select_bias and routed_scale route with
-    moe_route_grouped (the six separate calls then, not the fused prepare);
-    they exclude `bias` and k_primary.  Batches of up to few_tokens tokens (at
+    moe_route_grouped (the six separate calls then, not the fused prepare: up
+    to 2 % of a layer of 64 experts of [6144, 2048] in a graph); they exclude `bias` and k_primary.  Batches of up to few_tokens tokens (at
     most FEW_MAX_TOKENS; 0: none) run as route and moe_experts_*: the same
     weights with 16-bit activations, so closer to the unquantised layer than
     the larger batches' results, and without the steps below."""

@@ -26,9 +26,10 @@
 // leaves its sums in the workspace, and the one that is last adds them in the
 // order of the ranges: a repeated call gives the same bits.
 //
-// Bound by the weights' bytes up to 16 tokens, of which 132 MB take 25.6 us (one
-// token) to 27.8 us (16) with about 6 us of start and joins, 5.2 TB/s; at 32
-// tokens, 35.8 us, by one accumulator and three stages of terms.  The
+// 132 MB of weights take 25.5 us (one token) to 27.4 us (16), 5.2 to 4.8 TB/s with
+// the launch that makes the terms.  19.5 us are the bytes; the rest, in which memory
+// idles, are the starts of two launches and the last joins.  32 tokens take 35.8 us,
+// bound by one accumulator and three stages of terms.  The
 // same stream on mma.sync, with the codes widened to float16 in registers, was
 // bound by those instructions: 31 us at 8 tokens, 79 us at 32, and 1390 us for 23
 // tokens through a layer that takes 451 us here.
@@ -728,8 +729,8 @@ cudaError_t launch_stream(const FewMatrix& w, int E, StreamParams p, int num_sms
   p.gscale = MODE == kDown ? nullptr : w.gscale;
   p.N = w.N, p.K = w.K, p.tiled = w.tiled;
   p.wait_us = wait_limit_us();
-  // Up to 16 tokens two accumulators and eight stages: 16 tokens x [32768, 7168] 27.8 us, with WIDE 28.4; one
-  // token through 8 experts of [6144, 2048] 42.3, with WIDE 44.9.
+  // Up to 16 tokens two accumulators and eight stages: with WIDE 16 tokens x [32768, 7168] take 2 % longer, one
+  // token through 8 experts of [6144, 2048] 6 %.
   if (p.T <= 16)
     return w.mx ? launch_one<true, MODE, false>(w, p, num_sms, st) : launch_one<false, MODE, false>(w, p, num_sms, st);
   return w.mx ? launch_one<true, MODE, true>(w, p, num_sms, st) : launch_one<false, MODE, true>(w, p, num_sms, st);

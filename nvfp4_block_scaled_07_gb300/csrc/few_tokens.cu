@@ -22,9 +22,9 @@
 // smaller ones are off by at most 2^-39 of it.  The gated products h (float32)
 // become two such numbers, the second what the rounding to the first leaves:
 // 22 bits, off by 2^-22 of themselves, as four float32 roundings.  (One number,
-// 11 bits, was lost in differences of nearly equal products and moved one bf16
-// result in 30; it took 7.4 us instead of 7.7 for the three tokens.)  Sums are
-// float32.
+// 11 bits, took 7.4 us instead of 7.7 for the three tokens, but differences of
+// nearly equal products were lost in it, and the bf16 results were 8e-4 off in
+// norm where they now are those of float32.)  Sums are float32.
 //
 // A warp takes 32 rows of a matrix as two 16-row tiles (of gate and of up in
 // the gated product) and steps of 256 of its columns, a lane 32 bytes of four

@@ -1,10 +1,16 @@
 // Host-side kernel launch with programmatic dependent launch (PDL).
 //
-// Every kernel of the library starts with griddepcontrol.wait before it
-// touches global memory, and signals griddepcontrol.launch_dependents soon
-// after, so a kernel launched here behind another kernel may be scheduled
-// while its predecessor drains; its reads and writes still happen after the
-// predecessor has completed.  NVFP4MOE_PDL=0 in the environment launches
+// A kernel of the library starts with griddepcontrol.wait before it touches
+// global memory, and signals griddepcontrol.launch_dependents only after, so a
+// kernel launched here behind another kernel may be scheduled while its
+// predecessor drains; its reads and writes still happen after the predecessor
+// has completed.  Because the signal comes after the wait, a kernel that runs
+// early finds everything before its predecessor complete.  stream_kernel
+// (few_stream.cu), always launched behind a kernel of the same call, rests on
+// that: its producer warps read the call's weights, ids and plan, which that
+// predecessor does not write (of the gated product: the ids, not the plan),
+// before the wait.  A kernel that signals before its own wait must not be
+// followed by one that does so.  NVFP4MOE_PDL=0 in the environment launches
 // without the attribute (plain stream order), for comparisons.
 #pragma once
 

@@ -10,7 +10,7 @@
 // One block scans the requests (tokens, then pages) in pieces of its threads,
 // and writes the new table entries and a few tokens.  More tokens are written by a second kernel over all SMs, which reads the
 // tables.  Bound by latency: a decode step is one launch and two scans.  One
-// request of one token takes 2.6 us, 700 of three 4.9 us, 37 of 7000 8.6 us.
+// request of one token takes 2.5 us, 700 of three 4.8 us, 37 of 7000 8.6 us.
 #include <climits>
 #include <cstdint>
 
@@ -28,7 +28,7 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kMaxThreads = 1024;
 // The one block writes up to kOneBlock tokens, and up to kFew a request on average, which the scanning threads write as
 // they go.  Measured (us with one kernel, with two): 8 requests of 1024 tokens together 6.4, 6.3, of 8192 9.8, 6.4, of
-// 65536 41, 6.8; 300 requests of 4096 9.8, 8.7; 700 requests of three each 4.4, 11.1; 10000 of one 24, 59.
+// 65536 41, 6.8; 300 requests of 4096 9.8, 8.7; 700 requests of three each 4.8, 11.1; 10000 of one 24, 59.
 constexpr int kOneBlock = 1024;
 constexpr int kFew = 8;           // new tokens of a request: at most two pages
 constexpr int kSmall = 1 << 20;   // up to so many rows and free pages, a piece's two sums fit one 64-bit scan

@@ -75,11 +75,12 @@ int moe_route_grouped(const float* logits, const float* select_bias, int T, int 
  *
  * How exact the operands are on the tensor core goes by the size of the call:
  *   small (T <= 8, and K <= 6144, T K <= 2^14, T K^2 N <= 2^37; for experts H <=
- *   6144, T H <= 2^14, T k 2 I H <= 2^24, (T k I)^2 2 H <= 2^36): float16 with a
- *   power of two for 256 consecutive activations of a token: exact down to 2^-28
- *   of their largest, below off by at most 2^-39 of it.  Infinities and NaN go
- *   through the sums (with MXFP4 an infinity may come out as NaN where scales of
- *   256 consecutive weights of a row are more than 2^27 apart).
+ *   6144, T H <= 2^14, T k 2 I H <= 2^24, (T k I)^2 2 H <= 2^36, T k ceil(I /
+ *   256) <= 127): float16 with a power of two for 256 consecutive activations of
+ *   a token: exact down to 2^-28 of their largest, below off by at most 2^-39 of
+ *   it.  Infinities and NaN go through the sums (with MXFP4 an infinity may come
+ *   out as NaN where scales of 256 consecutive weights of a row are more than
+ *   2^27 apart).
  *   else: activations are sums of eight 4-bit terms with a scale for 16 (MXFP4:
  *   32) of them: off by at most 2^-18 of their largest, with NVFP4 also by 2^-34
  *   of the row's (of 2^-80 if that is larger).  An infinity or NaN makes all of
